@@ -277,8 +277,8 @@ def _prepare_accept(case, seed):
           "length": torch.empty(B, dtype=torch.int32, device="cuda"),
           "out": torch.empty((B, case["chain"]), dtype=torch.int32, device="cuda"), "host": (parent, table)}
     if own:
-        st["model"], st["kv"], st["tree"] = _model(B, N, case["Hkv"], case["Hkv"], case["hd"], 0, ctx, case["layers"],
-                                                   pool)
+        st["model"], st["kv"], st["tree"] = _model(B, N, 2 * case["Hkv"], case["Hkv"], case["hd"], 0, ctx,
+                                                   case["layers"], pool)
         st["tree"].plan(st["kv"], np.arange(0, B * N + 1, N), parent, np.full(B, ctx, np.int32), table)
     return st
 
