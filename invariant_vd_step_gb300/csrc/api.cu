@@ -25,6 +25,7 @@
 
 #include "vd_device.cuh"
 #include "vd_internal.h"
+#include "vd_model.h"
 
 namespace vd {
 
@@ -133,191 +134,11 @@ int make_map_kv(CUtensorMap* map, const void* base, uint64_t rows, int hd, int b
 
 using namespace vd;
 
-namespace {
+const char* const vd::kKernelNames[] = {"embed",     "rmsnorm",  "gemm_qkv",     "rope_kv",   "attention",
+                                        "attn_merge", "gemm_o",  "gemm_gate_up", "gemm_down", "final_norm",
+                                        "gemm_lm_head", "sample"};
 
-constexpr int kSplitKeys = 512;  // S_kv, fixed for every model
-
-struct ProfRec {
-  int cls;
-  int kernels;  // kernel launches between the two events
-  cudaEvent_t a, b;
-};
-const char* const kKernelNames[] = {"embed",     "rmsnorm",  "gemm_qkv",     "rope_kv",   "attention",
-                                    "attn_merge", "gemm_o",  "gemm_gate_up", "gemm_down", "final_norm",
-                                    "gemm_lm_head", "sample"};
-enum KernelClass {
-  K_EMBED, K_RMSNORM, K_GEMM_QKV, K_ROPE, K_ATTN, K_MERGE, K_GEMM_O, K_GEMM_GU, K_GEMM_DOWN, K_FINAL_NORM,
-  K_GEMM_LM, K_SAMPLE, K_COUNT
-};
-
-// Activation buffer with TMA maps for row counts 1, 2, 4, ... (capped at
-// the capacity), each in every token tile width: a GEMM over T rows uses the
-// smallest row count covering T, so rows past T are either never fetched or
-// (within the bucket) computed and discarded -- a GEMM column depends on its
-// own row only.
-struct ActBuf {
-  __nv_bfloat16* ptr = nullptr;
-  int cols = 0;
-  std::vector<int> rows;
-  std::vector<std::array<CUtensorMap, kNumBn>> maps;
-  size_t bucket(int T) const {
-    for (size_t i = 0; i < rows.size(); ++i)
-      if (rows[i] >= T) return i;
-    return rows.size() - 1;
-  }
-  ActMaps view(int T) const {
-    ActMaps v;
-    v.maps = maps[bucket(T)].data();
-    v.rows = rows[bucket(T)];
-    return v;
-  }
-};
-
-// Host-side layout of the uploaded step descriptor (int32 offsets).
-struct Desc {
-  int T = 0, B = 0, R = 0, stride = 0;
-  int tokens, positions, slot_page, cu_q, cached, page_table, logit_rows, dec_seq, dec_start, pre_seq, pre_start;
-  // (merge_tok: offset of the token list the merge kernel folds)
-  int n_dec = 0, n_pre = 0, items_dec = 0, items_pre = 0;
-  bool fold = false;  // decode class in fold mode
-  bool pre_tc = false;  // prefill class on the tcgen05 kernel (128 rows per CTA), else mma.sync (64)
-  int merge_tok = 0, n_merge = 0;
-  int grid_dec = 0, grid_pre = 0;  // attention CTAs launched (>= items; extra CTAs exit)
-  int total = 0;
-  const int* feed = nullptr;  // device tokens that entries -(1 + i) of `tokens` refer to
-};
-
-// What a captured step graph depends on beyond the model: every kernel
-// argument and grid size of a step is a function of these fields.
-struct GraphKey {
-  unsigned long long pool_id = 0;
-  const void* logits = nullptr;
-  const void* tokens = nullptr;  // fused token choice (vd_step_sample) or null
-  const void* feed = nullptr;    // device-side token feedback or null
-  int T = 0, B = 0, R = 0, stride = 0, n_dec = 0, n_pre = 0, grid_dec = 0, grid_pre = 0, fold = 0, n_merge = 0;
-  int pre_tc = 0;
-  int fast = 0;
-  unsigned plan_epoch = 0;  // GEMM plan override in force
-  bool operator==(const GraphKey& o) const {
-    return pool_id == o.pool_id && logits == o.logits && tokens == o.tokens && feed == o.feed && T == o.T && B == o.B && R == o.R && stride == o.stride &&
-           n_dec == o.n_dec && n_pre == o.n_pre && grid_dec == o.grid_dec && grid_pre == o.grid_pre &&
-           fold == o.fold && pre_tc == o.pre_tc && n_merge == o.n_merge && fast == o.fast &&
-           plan_epoch == o.plan_epoch;
-  }
-};
-struct GraphEntry {
-  GraphKey key;
-  cudaGraphExec_t exec = nullptr;
-  long long used = 0;
-};
-
-}  // namespace
-
-struct vd_model {
-  vd_model_config cfg{};
-  int device = 0;
-  const __nv_bfloat16* embed = nullptr;
-  const __nv_bfloat16* final_norm = nullptr;
-  const __nv_bfloat16* lm_head = nullptr;
-  std::vector<vd_layer_weights> layers;
-  // fixed kernel choices
-  int split = kSplitKeys;
-  int key_tile = 64;
-  int max_splits = 0;
-  int G = 1;
-  // TMA maps
-  std::vector<WeightMaps> m_qkv, m_o, m_gu, m_down;
-  WeightMaps m_lm{};
-  ActBuf a, o, z, ar;
-  // workspace
-  __nv_bfloat16 *x = nullptr, *qkv = nullptr, *q = nullptr;
-  __nv_bfloat16* hsub = nullptr;  // sandwich norms: a sub-layer's output before its norm
-  float embed_scale = 0.f;        // 0: none, else bf16(sqrt(d)) as float
-  int fold_mode = 0;              // 0: default (split mode), 1: fold the decode class whenever legal, 2: never
-  int prefill_kernel = 0;         // 0: tcgen05 attention for the prefill class where hd allows, 1: mma.sync
-  // fast (non-invariant) path: split-K for GEMMs with too few weight tiles
-  int fast = 0;
-  int n_sm = 0;
-  float* splitk_part = nullptr;
-  size_t splitk_cap = 0;          // floats
-  std::vector<int> scratch_dec;   // host scratch of build_desc
-  float gain_offset = 0.f;        // RMSNorm gains are w + gain_offset
-  float *part_o = nullptr, *part_ml = nullptr;
-  float *cos_g = nullptr, *sin_g = nullptr, *cos_l = nullptr, *sin_l = nullptr;
-  int* status = nullptr;
-  int* d_desc = nullptr;
-  int* h_desc[2] = {nullptr, nullptr};
-  cudaEvent_t desc_ev[2] = {nullptr, nullptr};
-  int desc_slot = 0;
-  size_t desc_cap = 0;
-  vd_sampler* d_samp = nullptr;
-  float* samp_part_v = nullptr;  // per-chunk winners of the sampler's first pass
-  int* samp_part_i = nullptr;
-  float* fused_part_v = nullptr;  // per-32-row-group winners of the fused LM-head epilogue
-  int* fused_part_i = nullptr;
-  vd_sampler* h_samp = nullptr;
-  cudaEvent_t samp_ev = nullptr;
-  std::vector<void*> dev_allocs;
-  // profiling
-  bool profiling = false;
-  std::vector<ProfRec> recs;
-  std::vector<cudaEvent_t> ev_pool;
-  double prof_ms[K_COUNT] = {};
-  int prof_n[K_COUNT] = {};
-  int prof_k[K_COUNT] = {};
-  // graph replay of steps
-  int graph_max = 0;
-  cudaStream_t cap_stream = nullptr;
-  std::vector<GraphEntry> graphs;
-  long long graph_clock = 0, graph_captures = 0, graph_replays = 0, graph_eager = 0;
-};
-
-struct vd_kv_pool {
-  vd_model* m = nullptr;
-  unsigned long long id = 0;  // never reused, unlike the host address
-  int num_pages = 0;
-  void* data = nullptr;
-  bool owned = false;
-  long long rows = 0;  // 16-slot rows of hd elements
-  CUtensorMap map{};     // boxes for the mma.sync attention kernels
-  CUtensorMap map_tc{};  // boxes for the tcgen05 attention kernel
-};
-
-namespace {
-
-// ---------------------------------------------------------------- profiling
-cudaEvent_t take_event(vd_model* m) {
-  if (!m->ev_pool.empty()) {
-    cudaEvent_t e = m->ev_pool.back();
-    m->ev_pool.pop_back();
-    return e;
-  }
-  cudaEvent_t e = nullptr;
-  cudaEventCreate(&e);
-  return e;
-}
-struct Prof {
-  vd_model* m;
-  int cls;
-  cudaStream_t s;
-  cudaEvent_t a = nullptr;
-  int kernels = 1;
-  Prof(vd_model* m_, int cls_, cudaStream_t s_) : m(m_), cls(cls_), s(s_) {
-    if (m->profiling) {
-      a = take_event(m);
-      cudaEventRecord(a, s);
-    }
-  }
-  ~Prof() {
-    if (m->profiling) {
-      cudaEvent_t b = take_event(m);
-      cudaEventRecord(b, s);
-      m->recs.push_back({cls, kernels, a, b});
-    }
-  }
-};
-
-int dev_alloc(vd_model* m, void** p, size_t bytes) {
+int vd::dev_alloc(vd_model* m, void** p, size_t bytes) {
   if (bytes == 0) bytes = 256;
   cudaError_t e = cudaMalloc(p, bytes);
   if (e != cudaSuccess) return fail(VD_ERR_CUDA, std::string("cudaMalloc: ") + cudaGetErrorString(e));
@@ -325,6 +146,8 @@ int dev_alloc(vd_model* m, void** p, size_t bytes) {
   cudaMemset(*p, 0, bytes);
   return VD_OK;
 }
+
+namespace {
 
 int make_act(vd_model* m, ActBuf& buf, int cap_rows, int cols) {
   int rc = dev_alloc(m, reinterpret_cast<void**>(&buf.ptr), static_cast<size_t>(cap_rows) * cols * 2);
@@ -361,11 +184,13 @@ int rope_table(vd_model* m, float theta, int hd, float** cs, float** sn) {
   return VD_OK;
 }
 
-bool layer_is_local(const vd_model_config& c, int i) {
+}  // namespace
+
+bool vd::layer_is_local(const vd_model_config& c, int i) {
   return c.sliding_window > 0 && c.local_global_period > 0 && ((i + 1) % c.local_global_period) != 0;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+namespace {
 
 // Items of one attention work class for request with q_len, kv_len.
 int attn_items(int qlen, int kv_len, int G, int Hkv, int rows_per_cta) {
@@ -543,6 +368,7 @@ int upload_desc(vd_model* m, vd_kv_pool* pool, const vd_batch* b, bool need_toke
   int* h = m->h_desc[slot];
   int rc = build_desc(m, pool, b, need_tokens, d, h, graph_shape, feed_index);
   if (rc || d.T == 0) return rc;
+  d.base = m->d_desc;
   VD_CUDA_TRY(cudaMemcpyAsync(m->d_desc, h, static_cast<size_t>(d.total) * 4, cudaMemcpyHostToDevice, s));
   VD_CUDA_TRY(cudaEventRecord(m->desc_ev[slot], s));
   return VD_OK;
@@ -550,6 +376,7 @@ int upload_desc(vd_model* m, vd_kv_pool* pool, const vd_batch* b, bool need_toke
 
 int run_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv_bfloat16* q,
                   __nv_bfloat16* out, cudaStream_t s) {
+  if (d.tree) return run_tree_attention(m, pool, layer, d, q, out, s);
   const vd_model_config& c = m->cfg;
   const int hd = c.head_dim;
   const int window = layer_is_local(c, layer) ? c.sliding_window : 0;
@@ -557,9 +384,9 @@ int run_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const
   a.q = q;
   a.part_o = m->part_o;
   a.part_ml = m->part_ml;
-  a.cu_q = m->d_desc + d.cu_q;
-  a.cached_len = m->d_desc + d.cached;
-  a.page_table = m->d_desc + d.page_table;
+  a.cu_q = d.base + d.cu_q;
+  a.cached_len = d.base + d.cached;
+  a.page_table = d.base + d.page_table;
   a.pt_stride = d.stride;
   a.Hq = c.n_heads;
   a.Hkv = c.n_kv_heads;
@@ -573,8 +400,8 @@ int run_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const
   int rc;
   if (d.n_dec) {
     Prof p(m, K_ATTN, s);
-    a.cls_seq = m->d_desc + d.dec_seq;
-    a.cls_start = m->d_desc + d.dec_start;
+    a.cls_seq = d.base + d.dec_seq;
+    a.cls_start = d.base + d.dec_start;
     a.n_cls = d.n_dec;
     a.fold = d.fold;
     a.out = out;
@@ -583,8 +410,8 @@ int run_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const
   }
   if (d.n_pre) {
     Prof p(m, K_ATTN, s);
-    a.cls_seq = m->d_desc + d.pre_seq;
-    a.cls_start = m->d_desc + d.pre_start;
+    a.cls_seq = d.base + d.pre_seq;
+    a.cls_start = d.base + d.pre_start;
     a.n_cls = d.n_pre;
     if ((rc = d.pre_tc ? launch_attention_tc(pool->map_tc, a, hd, d.grid_pre, s)
                         : launch_attention(pool->map, a, hd, true, d.grid_pre, s)))
@@ -595,8 +422,8 @@ int run_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const
   g.part_o = m->part_o;
   g.part_ml = m->part_ml;
   g.out = out;
-  g.positions = m->d_desc + d.positions;
-  g.tokens = d.fold ? m->d_desc + d.merge_tok : nullptr;
+  g.positions = d.base + d.positions;
+  g.tokens = d.fold ? d.base + d.merge_tok : nullptr;
   g.T = d.n_merge;
   g.Hq = c.n_heads;
   g.window = window;
@@ -606,7 +433,9 @@ int run_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const
   return launch_merge(g, hd, s);
 }
 
-int run_rope(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv_bfloat16* qkv,
+}  // namespace
+
+int vd::run_rope(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv_bfloat16* qkv,
              __nv_bfloat16* q_out, cudaStream_t s) {
   const vd_model_config& c = m->cfg;
   const bool local = layer_is_local(c, layer);
@@ -614,8 +443,10 @@ int run_rope(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv
   r.qkv = qkv;
   r.q_out = q_out;
   r.pool = static_cast<__nv_bfloat16*>(pool->data);
-  r.positions = m->d_desc + d.positions;
-  r.slot_page = m->d_desc + d.slot_page;
+  r.positions = d.base + d.positions;
+  r.slot_page = d.base + d.slot_page;
+  r.slots = d.tree ? d.base + d.slots : nullptr;
+  r.shape = local ? m->rope_l : m->rope_g;
   r.cos_t = local ? m->cos_l : m->cos_g;
   r.sin_t = local ? m->sin_l : m->sin_g;
   r.q_norm = c.qk_norm ? static_cast<const __nv_bfloat16*>(m->layers[layer].q_norm) : nullptr;
@@ -631,6 +462,8 @@ int run_rope(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv
   return launch_rope_kv(r, s);
 }
 
+namespace {
+
 // vd_op_attention with the split partials in caller-independent static
 // scratch (part_o / part_ml, row stride `splits`) instead of the workspace.
 int run_attention_static(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv_bfloat16* q,
@@ -642,9 +475,9 @@ int run_attention_static(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d
   a.q = q;
   a.part_o = part_o;
   a.part_ml = part_ml;
-  a.cu_q = m->d_desc + d.cu_q;
-  a.cached_len = m->d_desc + d.cached;
-  a.page_table = m->d_desc + d.page_table;
+  a.cu_q = d.base + d.cu_q;
+  a.cached_len = d.base + d.cached;
+  a.page_table = d.base + d.page_table;
   a.pt_stride = d.stride;
   a.Hq = c.n_heads;
   a.Hkv = c.n_kv_heads;
@@ -657,8 +490,8 @@ int run_attention_static(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d
   a.status = m->status;
   int rc;
   if (d.n_dec) {
-    a.cls_seq = m->d_desc + d.dec_seq;
-    a.cls_start = m->d_desc + d.dec_start;
+    a.cls_seq = d.base + d.dec_seq;
+    a.cls_start = d.base + d.dec_start;
     a.n_cls = d.n_dec;
     a.fold = d.fold;
     a.out = out;
@@ -666,8 +499,8 @@ int run_attention_static(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d
     a.fold = 0;
   }
   if (d.n_pre) {
-    a.cls_seq = m->d_desc + d.pre_seq;
-    a.cls_start = m->d_desc + d.pre_start;
+    a.cls_seq = d.base + d.pre_seq;
+    a.cls_start = d.base + d.pre_start;
     a.n_cls = d.n_pre;
     if ((rc = d.pre_tc ? launch_attention_tc(pool->map_tc, a, hd, d.items_pre, s)
                         : launch_attention(pool->map, a, hd, true, d.items_pre, s)))
@@ -678,8 +511,8 @@ int run_attention_static(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d
   g.part_o = part_o;
   g.part_ml = part_ml;
   g.out = out;
-  g.positions = m->d_desc + d.positions;
-  g.tokens = d.fold ? m->d_desc + d.merge_tok : nullptr;
+  g.positions = d.base + d.positions;
+  g.tokens = d.fold ? d.base + d.merge_tok : nullptr;
   g.T = d.n_merge;
   g.Hq = c.n_heads;
   g.window = window;
@@ -702,7 +535,11 @@ int* op_status() {
   return words[dev];
 }
 
-int check_model(const vd_model* m) { return m ? VD_OK : fail(VD_ERR_INVALID_ARG, "null model"); }
+}  // namespace
+
+int vd::check_model(const vd_model* m) { return m ? VD_OK : fail(VD_ERR_INVALID_ARG, "null model"); }
+
+namespace {
 
 // Fast path only: tokens per step up to which narrow GEMMs split K.
 constexpr int kFastMaxTokens = 256;
@@ -744,8 +581,10 @@ int gemm_step(vd_model* m, const WeightMaps& w, const ActBuf& xb, int T, int ldo
   return launch_splitk_reduce(m->splitk_part, ks, T, np, epi, out, residual, s);
 }
 
+}  // namespace
+
 // The kernel sequence of one step (descriptor already uploaded).
-int enqueue_step(vd_model* m, vd_kv_pool* pool, const Desc& d, float* logits_out, int* tokens_out, cudaStream_t s) {
+int vd::enqueue_step(vd_model* m, vd_kv_pool* pool, const Desc& d, float* logits_out, int* tokens_out, cudaStream_t s) {
   int rc;
   const vd_model_config& c = m->cfg;
   const int T = d.T, dm = c.d_model, hd = c.head_dim, F = c.ffn_dim;
@@ -754,7 +593,7 @@ int enqueue_step(vd_model* m, vd_kv_pool* pool, const Desc& d, float* logits_out
   const bool sandwich = c.sandwich_norm != 0;
   {
     Prof p(m, K_EMBED, s);
-    if ((rc = launch_embed(m->embed, m->d_desc + d.tokens, d.feed, c.vocab, m->status, m->embed_scale, m->x, T, dm,
+    if ((rc = launch_embed(m->embed, d.base + d.tokens, d.feed, c.vocab, m->status, m->embed_scale, m->x, T, dm,
                            s)))
       return rc;
   }
@@ -817,7 +656,7 @@ int enqueue_step(vd_model* m, vd_kv_pool* pool, const Desc& d, float* logits_out
   if (d.R > 0) {
     {
       Prof p(m, K_FINAL_NORM, s);
-      if ((rc = launch_rmsnorm(m->x, m->d_desc + d.logit_rows, m->final_norm, m->ar.ptr, d.R, dm, c.rms_eps, off, s)))
+      if ((rc = launch_rmsnorm(m->x, d.base + d.logit_rows, m->final_norm, m->ar.ptr, d.R, dm, c.rms_eps, off, s)))
         return rc;
     }
     {
@@ -845,6 +684,8 @@ int enqueue_step(vd_model* m, vd_kv_pool* pool, const Desc& d, float* logits_out
   }
   return VD_OK;
 }
+
+namespace {
 
 // Replays the graph captured for d's key.  A key seen for the first time
 // runs eagerly and is remembered; the second time it is captured, so one-off
@@ -914,14 +755,13 @@ int replay_step(vd_model* m, vd_kv_pool* pool, const Desc& d, float* logits_out,
   return VD_OK;
 }
 
-void drop_graphs(vd_model* m) {
+}  // namespace
+
+void vd::drop_graphs(vd_model* m) {
   for (GraphEntry& e : m->graphs)
     if (e.exec) cudaGraphExecDestroy(e.exec);
   m->graphs.clear();
 }
-
-
-}  // namespace
 
 // ====================================================================== API
 extern "C" {

@@ -96,7 +96,9 @@ struct TcAttnCfg {
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
-template <int HD>
+// TREE: rows are the nodes of a token tree and fold only the cached tiles
+// they share (as in attention.cu).
+template <int HD, bool TREE>
 __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, AttnArgs a) {
   using C = TcAttnCfg<HD>;
@@ -135,7 +137,8 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
   const int b = a.cls_seq[lo_i];
   int local = item - a.cls_start[lo_i];
   const int q0 = a.cu_q[b], qlen = a.cu_q[b + 1] - q0, cached = a.cached_len[b];
-  const int kv_len = cached + qlen;
+  const int shared = cached / C::BNK * C::BNK;  // TREE: keys of the tiles that every node folds alike
+  const int kv_len = TREE ? shared : cached + qlen;
   const int G = a.Hq / a.Hkv;
   const int nsplit = (kv_len - 1) / a.split + 1;
   const int sidx = local % nsplit;
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
   const int rows = qlen * G;
   const int r0 = rb * C::ROWS;
   const int r_end = min(rows, r0 + C::ROWS);
-  const int p_min = cached + r0 / G, p_max = cached + (r_end - 1) / G;
+  const int p_min = TREE ? cached : cached + r0 / G, p_max = TREE ? shared - 1 : cached + (r_end - 1) / G;
   const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
   const int key_lo = max(sidx * a.split, lo_min);
   const int key_hi = min((sidx + 1) * a.split - 1, p_max);
@@ -296,8 +299,8 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
       valid[r] = row < rows;
       tok[r] = row / G;
       hq[r] = kvh * G + row % G;
-      pos[r] = valid[r] ? cached + tok[r] : -1;
-      lo[r] = valid[r] ? (a.window > 0 ? max(0, pos[r] - a.window + 1) : 0) : 1;
+      pos[r] = valid[r] ? (TREE ? shared - 1 : cached + tok[r]) : -1;
+      lo[r] = valid[r] ? (a.window > 0 ? max(0, (TREE ? a.tree_pos[q0 + tok[r]] : pos[r]) - a.window + 1) : 0) : 1;
     }
     {  // O = +0, as the mma.sync kernel's accumulators start
       float z[16];
@@ -466,15 +469,15 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
   }
 }
 
-template <int HD>
+template <int HD, bool TREE>
 int launch_attn_tc_t(const CUtensorMap& kvmap, const AttnArgs& a, int n_items, cudaStream_t s) {
   using C = TcAttnCfg<HD>;
   static bool configured = false;
   if (!configured) {
-    VD_CUDA_TRY(cudaFuncSetAttribute(attn_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    VD_CUDA_TRY(cudaFuncSetAttribute(attn_tc_kernel<HD, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
     configured = true;
   }
-  VD_CUDA_TRY(launch_k(attn_tc_kernel<HD>, dim3(n_items), dim3(C::THREADS), C::SMEM, s, kvmap, a));
+  VD_CUDA_TRY(launch_k(attn_tc_kernel<HD, TREE>, dim3(n_items), dim3(C::THREADS), C::SMEM, s, kvmap, a));
   return VD_OK;
 }
 
@@ -487,9 +490,9 @@ int launch_attention_tc(const CUtensorMap& kvmap_tc, const AttnArgs& a, int hd, 
   if (a.fold) return fail(VD_ERR_INVALID_ARG, "split folding is for decode-class CTAs");
   if (a.split > TcAttnCfg<128>::PIDS * 16)  // a CTA stages the ids of every page its split streams
     return fail(VD_ERR_INVALID_ARG, "KV split larger than the staged page ids");
-  if (hd == 64) return launch_attn_tc_t<64>(kvmap_tc, a, n_items, s);
-  if (hd == 128) return launch_attn_tc_t<128>(kvmap_tc, a, n_items, s);
-  if (hd == 256) return launch_attn_tc_t<256>(kvmap_tc, a, n_items, s);
+  if (hd == 64) return a.tree_pos ? launch_attn_tc_t<64, true>(kvmap_tc, a, n_items, s) : launch_attn_tc_t<64, false>(kvmap_tc, a, n_items, s);
+  if (hd == 128) return a.tree_pos ? launch_attn_tc_t<128, true>(kvmap_tc, a, n_items, s) : launch_attn_tc_t<128, false>(kvmap_tc, a, n_items, s);
+  if (hd == 256) return a.tree_pos ? launch_attn_tc_t<256, true>(kvmap_tc, a, n_items, s) : launch_attn_tc_t<256, false>(kvmap_tc, a, n_items, s);
   return fail(VD_ERR_UNSUPPORTED, "the tcgen05 attention kernel takes head_dim 64, 128 or 256");
 }
 

@@ -236,7 +236,13 @@ __global__ void postnorm_residual_kernel(const __nv_bfloat16* __restrict__ h, __
 // One warp per (token, head).  Lane l owns the rotate-half pairs
 // (i, i + hd/2) for i = l, l+32, ...  q heads -> q_out, k heads -> pool K
 // slot, v heads -> pool V slot of the token's (page, position % 16).
+// GEN: the other pair layouts and a rotated part of the head (RopeShape), and
+// slots given per token (the nodes of a token tree, whose slots do not follow
+// their positions).  Pairs past the rotated part are pairs of neighbours that
+// pass through.  With the default shape every value goes through the same
+// operations in the same order as without GEN.
 constexpr int kRopeWarps = 8;
+template <bool GEN>
 __global__ void __launch_bounds__(kRopeWarps * 32) rope_kv_kernel(RopeArgs a) {
   const int t = blockIdx.x;
   const int head = blockIdx.y * kRopeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -249,8 +255,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kv_kernel(RopeArgs a) {
   const bool live = head < nh;
   const int p = live ? a.positions[t] : 0;
   const size_t page = live ? static_cast<size_t>(a.slot_page[t]) : 0;
-  const int slot = p & 15;
+  const int slot = GEN && a.slots ? (live ? a.slots[t] : 0) : p & 15;
   const int np = (half + 31) / 32;
+  const int hrot = GEN && a.shape.rot ? a.shape.rot >> 1 : half;  // rotated pairs
+  auto e1 = [&](int i) { return !GEN || (i < hrot && !a.shape.interleaved) ? i : 2 * i; };
+  auto e2 = [&](int i) { return !GEN || (i < hrot && !a.shape.interleaved) ? i + hrot : 2 * i + 1; };
   float cs[4] = {0.f, 0.f, 0.f, 0.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
   if (live && head < a.Hq + a.Hkv) {
 #pragma unroll
@@ -277,8 +286,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kv_kernel(RopeArgs a) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int i = lane + 32 * k;
-    x1[k] = (k < np && i < half) ? __bfloat162float(src[i]) : 0.f;
-    x2[k] = (k < np && i < half) ? __bfloat162float(src[i + half]) : 0.f;
+    x1[k] = (k < np && i < half) ? __bfloat162float(src[e1(i)]) : 0.f;
+    x2[k] = (k < np && i < half) ? __bfloat162float(src[e2(i)]) : 0.f;
   }
   const __nv_bfloat16* nw = is_q ? a.q_norm : a.k_norm;
   if (nw) {  // per-head RMSNorm (QK-norm), rounded to bf16 before RoPE
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kv_kernel(RopeArgs a) {
     for (int k = 0; k < 4; ++k) {
       const int i = lane + 32 * k;
       if (k < np && i < half) {
-        float g1 = __bfloat162float(nw[i]), g2 = __bfloat162float(nw[i + half]);
+        float g1 = __bfloat162float(nw[e1(i)]), g2 = __bfloat162float(nw[e2(i)]);
         if (a.gain_offset != 0.f) {
           g1 = __fadd_rn(g1, a.gain_offset);
           g2 = __fadd_rn(g2, a.gain_offset);
@@ -316,8 +325,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kv_kernel(RopeArgs a) {
     const int i = lane + 32 * k;
     if (k < np && i < half) {
       const float c = cs[k], s = sn[k];
-      dst[i] = __float2bfloat16_rn(__fsub_rn(__fmul_rn(x1[k], c), __fmul_rn(x2[k], s)));
-      dst[i + half] = __float2bfloat16_rn(__fadd_rn(__fmul_rn(x2[k], c), __fmul_rn(x1[k], s)));
+      if (GEN && i >= hrot) {  // past the rotated part
+        dst[e1(i)] = __float2bfloat16_rn(x1[k]);
+        dst[e2(i)] = __float2bfloat16_rn(x2[k]);
+        continue;
+      }
+      dst[e1(i)] = __float2bfloat16_rn(__fsub_rn(__fmul_rn(x1[k], c), __fmul_rn(x2[k], s)));
+      dst[e2(i)] = __float2bfloat16_rn(__fadd_rn(__fmul_rn(x2[k], c), __fmul_rn(x1[k], s)));
     }
   }
 }
@@ -375,7 +389,8 @@ int launch_rope_kv(const RopeArgs& a, cudaStream_t s) {
   if (a.T <= 0) return VD_OK;
   const int nh = a.Hq + 2 * a.Hkv;
   dim3 grid(a.T, (nh + kRopeWarps - 1) / kRopeWarps);
-  VD_CUDA_TRY(launch_k(rope_kv_kernel, grid, dim3(kRopeWarps * 32), 0, s, a));
+  const bool gen = a.slots || a.shape.rot || a.shape.interleaved;
+  VD_CUDA_TRY(launch_k(gen ? rope_kv_kernel<true> : rope_kv_kernel<false>, grid, dim3(kRopeWarps * 32), 0, s, a));
   return VD_OK;
 }
 

@@ -12,6 +12,7 @@
 #include "vd.h"
 #include "vd_ops.h"
 #include "vd_engine.h"
+#include "vd_tree.h"
 
 namespace vd {
 
@@ -160,6 +161,7 @@ struct AttnArgs {
                            // writing out directly (no partials); 0 = one CTA per split
   __nv_bfloat16* out;      // [T][Hq][hd] (fold mode)
   int* status;
+  const int* tree_pos;     // token trees: [T] position of each node (the row order holds no positions), else null
 };
 struct MergeArgs {
   const float* part_o;
@@ -174,6 +176,46 @@ int attn_key_tile(int hd);
 int launch_attention(const CUtensorMap& kvmap, const AttnArgs& a, int hd, bool prefill_class, int n_items,
                      cudaStream_t s);
 int launch_merge(const MergeArgs& a, int hd, cudaStream_t s);
+// Token trees (a.tree_pos set): the cached tiles that every node of a request
+// shares, as split partials; launch_attention_tc takes them too.
+int launch_attention_tree(const CUtensorMap& kvmap, const AttnArgs& a, int hd, bool prefill_class, int n_items,
+                          cudaStream_t s);
+// The tiles that differ from node to node: takes up the partial of the split
+// that holds key `cached_len`, folds the node's remaining cached keys and its
+// path, and writes the split partials back.
+struct TreeTailArgs {
+  const __nv_bfloat16* q;     // [T][Hq][hd]
+  const __nv_bfloat16* pool;  // the layer's first page
+  float* part_o;              // [T][Hq][max_splits][hd]
+  float* part_ml;             // [T][Hq][max_splits][2]
+  const int* node_seq;        // [T] request of each node
+  const int* cu_q;            // [B + 1]
+  const int* cached_len;      // [B]
+  const int* page_table;      // [B][pt_stride]
+  const int* positions;       // [T] cached_len + depth
+  const int* path_off;        // [T] the node's path in `path`: node ids of depth 0, 1, ..., its own
+  const int* path;
+  int T, Hq, Hkv, pt_stride, window, split, max_splits;
+  float scale_log2;
+  int* status;
+};
+int launch_tree_tail(const TreeTailArgs& a, int hd, cudaStream_t s);
+struct TreeAcceptArgs {
+  const int* tokens;          // [T] token of each node
+  const int* choices;         // [T] token chosen after each node
+  const int* parent;          // [T] parent within the request, -1 for its root
+  const int* cu_q;            // [B + 1]
+  const int* cached_len;      // [B]
+  const int* page_table;      // [B][pt_stride]
+  __nv_bfloat16* pool;
+  int* accepted_len;          // [B]
+  int* out_tokens;            // [B][out_stride]
+  long long layer_elems;      // pool elements of a layer
+  int B, layers, Hkv, hd, pt_stride, out_stride;
+  int* status;
+};
+constexpr int kTreeMaxNodes = 1024;  // nodes of one request's tree
+int launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t s);
 // Prefill-class attention on tcgen05 (128 rows per CTA), same per-row
 // arithmetic as launch_attention's kernels; kvmap_tc has one-page boxes of
 // 64 head dims.
@@ -196,12 +238,20 @@ int launch_rmsnorm(const void* x, const int* row_idx, const void* w, void* y, in
 // then, if w_pre is not null, y = rms(x; w_pre).  Gains are w + gain_offset.
 int launch_postnorm_residual(const void* h, void* x, const void* w_post, const void* w_pre, void* y, int rows, int d,
                              float eps, float gain_offset, cudaStream_t s);
+// Which elements of a head form the rotated pairs: the first `rot` dims (0:
+// the whole head), pair i = (i, i + rot/2) or, interleaved, (2i, 2i + 1).
+struct RopeShape {
+  int rot = 0;
+  int interleaved = 0;
+};
 struct RopeArgs {
   const __nv_bfloat16* qkv;   // [T][(Hq+2Hkv) hd]
   __nv_bfloat16* q_out;       // [T][Hq][hd]
   __nv_bfloat16* pool;        // pool base
   const int* positions;       // [T]
   const int* slot_page;       // [T] physical page of the token's slot
+  const int* slots;           // [T] slot inside that page, or null: position % 16
+  RopeShape shape;
   const float* cos_t;         // [max_ctx][hd/2]
   const float* sin_t;
   const __nv_bfloat16* q_norm;  // nullable

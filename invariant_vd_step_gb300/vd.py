@@ -84,6 +84,12 @@ class EngineStats(ctypes.Structure):
                 ("steps", "prefix_hit_pages", "registered", "evicted", "preempted", "hash_candidates_rejected")]
 
 
+class TreeBatch(ctypes.Structure):
+    _fields_ = [("num_nodes", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("page_table_stride", ctypes.c_int32),
+                ("pad_", ctypes.c_int32), ("cu_nodes", _I32P), ("parent", _I32P), ("cached_len", _I32P),
+                ("page_table", _I32P), ("token_ids", _I32P)]
+
+
 class PlanOut(ctypes.Structure):
     _fields_ = [("batch", Batch), ("rids", ctypes.POINTER(ctypes.c_int64)),
                 ("samplers", ctypes.POINTER(Sampler))]
@@ -129,6 +135,13 @@ _SIGS = {
     "vd_op_tma_stream": (ctypes.c_int, [_VP, ctypes.c_int64, ctypes.c_int64, _VP, ctypes.c_int64, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP]),
     "vd_op_mma_issue_probe": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP, _VP]),
+    "vd_tree_create": (ctypes.c_int, [_VP, ctypes.c_int32, ctypes.POINTER(_VP)]),
+    "vd_destroy_tree": (None, [_VP]),
+    "vd_tree_plan": (ctypes.c_int, [_VP, _VP, ctypes.POINTER(TreeBatch), _VP]),
+    "vd_op_tree_attention": (ctypes.c_int, [_VP, _VP, ctypes.c_int32, _VP, _VP, _VP]),
+    "vd_op_tree_rope_kv": (ctypes.c_int, [_VP, _VP, ctypes.c_int32, _VP, _VP, _VP]),
+    "vd_step_tree": (ctypes.c_int, [_VP, _VP, _VP, _VP]),
+    "vd_tree_accept": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP]),
     "vd_engine_create": (ctypes.c_int, [ctypes.POINTER(EngineConfig), ctypes.POINTER(_VP)]),
     "vd_engine_destroy": (None, [_VP]),
     "vd_engine_add_request": (ctypes.c_int, [_VP, _I32P, ctypes.c_int32, ctypes.c_int32, ctypes.c_uint64,
@@ -421,6 +434,90 @@ class KVPool:
             raise RuntimeError("view() needs a pool created over caller memory")
         return self.memory.view(torch.bfloat16)[: s.n_layers * self.num_pages * 2 * s.n_kv_heads * 16 * s.head_dim] \
             .view(s.n_layers, self.num_pages, 2, s.n_kv_heads, 16, s.head_dim)
+
+
+def _need(ok, message: str):
+    """Argument checks that only the binding can make (it sees tensors, the library pointers)."""
+    if not ok:
+        raise VDError(VD_ERR_INVALID_ARG, message)
+
+
+def _check_out(t, shape, dtype, name: str):
+    _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
+          f"{name}: a contiguous {dtype} CUDA tensor of shape {tuple(shape)} is needed, got {t.dtype} "
+          f"{tuple(t.shape)} on {t.device}")
+
+
+class Tree:
+    """A vd_tree: attention, steps and acceptance of drafted token trees (include/vd_tree.h).
+
+    `plan` takes the trees of one step as arrays: cu_nodes [B + 1], parent [T] (-1 for each request's node 0, else
+    an earlier node's number within the request), cached_len [B], page_table [B][stride] and optionally token_ids
+    [T].  The other calls run on the plan in force."""
+
+    def __init__(self, model: Model, max_nodes: int):
+        self.model = model
+        self.num_nodes = self.num_seqs = 0
+        h = ctypes.c_void_p()
+        check(lib().vd_tree_create(model.h, int(max_nodes), ctypes.byref(h)))
+        self.h = h
+
+    def close(self):
+        if getattr(self, "h", None):
+            if getattr(self.model, "h", None):  # a closed model has taken its device state with it
+                lib().vd_destroy_tree(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def plan(self, pool: KVPool, cu_nodes, parent, cached_len, page_table, token_ids=None, stream=None):
+        cu, p_cu = _i32(cu_nodes)
+        par, p_par = _i32(np.asarray(parent).reshape(-1))
+        c, p_c = _i32(cached_len)
+        pt = np.ascontiguousarray(page_table, dtype=np.int32)
+        pt = pt.reshape(len(c), -1) if len(c) else pt.reshape(0, 0)
+        tok, p_tok = _i32(np.asarray(token_ids).reshape(-1)) if token_ids is not None else (None, None)
+        _need(len(cu) == len(c) + 1 and len(par) == cu[-1] and (tok is None or len(tok) == cu[-1]),
+              "cu_nodes [B + 1], cached_len [B], parent and token_ids [cu_nodes[B]]")
+        b = TreeBatch(len(par), len(c), pt.shape[1], 0, p_cu, p_par, p_c, pt.ctypes.data_as(_I32P), p_tok)
+        check(lib().vd_tree_plan(self.h, pool.h, ctypes.byref(b), _stream(stream)))
+        self.num_nodes, self.num_seqs = len(par), len(c)
+
+    def attention(self, pool: KVPool, layer: int, q: torch.Tensor, out: torch.Tensor, stream=None):
+        """vd_op_tree_attention: q, out bf16 [T][Hq][hd]."""
+        s = self.model.spec
+        for t, name in ((q, "q"), (out, "out")):
+            _check_out(t, (self.num_nodes, s.n_heads, s.head_dim), torch.bfloat16, name)
+        check(lib().vd_op_tree_attention(self.h, pool.h, layer, _ptr(q), _ptr(out), _stream(stream)))
+
+    def rope_kv(self, pool: KVPool, layer: int, qkv: torch.Tensor, q_out: torch.Tensor, stream=None):
+        """vd_op_tree_rope_kv: qkv bf16 [T][(Hq + 2 Hkv) hd], q_out bf16 [T][Hq][hd]."""
+        s = self.model.spec
+        _check_out(qkv, (self.num_nodes, s.qkv_dim), torch.bfloat16, "qkv")
+        _check_out(q_out, (self.num_nodes, s.n_heads, s.head_dim), torch.bfloat16, "q_out")
+        check(lib().vd_op_tree_rope_kv(self.h, pool.h, layer, _ptr(qkv), _ptr(q_out), _stream(stream)))
+
+    def step(self, pool: KVPool, logits: torch.Tensor, stream=None):
+        """vd_step_tree: logits float32 [T][V] of every planned node."""
+        _check_out(logits, (self.num_nodes, self.model.spec.vocab), torch.float32, "logits")
+        check(lib().vd_step_tree(self.h, pool.h, _ptr(logits), _stream(stream)))
+
+    def accept(self, pool: KVPool, node_tokens, choices: torch.Tensor, accepted_len: torch.Tensor,
+               out_tokens: torch.Tensor, stream=None):
+        """vd_tree_accept: node_tokens int32 [T] or None (the plan's token_ids), choices int32 [T],
+        accepted_len int32 [B], out_tokens int32 [B][longest path or more]."""
+        _check_out(choices, (self.num_nodes,), torch.int32, "choices")
+        if node_tokens is not None:
+            _check_out(node_tokens, (self.num_nodes,), torch.int32, "node_tokens")
+        _check_out(accepted_len, (self.num_seqs,), torch.int32, "accepted_len")
+        _need(out_tokens.dim() == 2, "out_tokens: [B][stride]")
+        _check_out(out_tokens, (self.num_seqs, out_tokens.shape[1]), torch.int32, "out_tokens")
+        check(lib().vd_tree_accept(self.h, pool.h, _ptr(node_tokens), _ptr(choices), _ptr(accepted_len),
+                                   _ptr(out_tokens), out_tokens.shape[1], _stream(stream)))
 
 
 def gemm(A, W, C, epilogue=EPI_BF16, residual=None, stream=None):
