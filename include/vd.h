@@ -144,6 +144,47 @@ typedef struct vd_sampler {
   float pad_;
 } vd_sampler;
 
+/* Rotary positions.  Pair i of a head's first rot_dim dims turns by angle
+ * p * f_i at position p; f_i = theta^(-2i / rot_dim), scaled:
+ *   LINEAR  f_i / factor (position interpolation);
+ *   BANDS   with n_i = original_max_position * f_i / 2 pi turns within the
+ *           original context: f_i where n_i >= high_freq_factor, f_i / factor
+ *           where n_i <= low_freq_factor, in between a blend linear in n_i
+ *           (the published Llama-3.1 rule);
+ *   YARN    a blend linear in i between the pairs that turn beta_fast and
+ *           beta_slow times within the original context, f_i before and
+ *           f_i / factor after them.
+ * The rotated vector is scaled by attn_factor (0: 0.1 ln(factor) + 1 for YARN
+ * with factor > 1, else 1).  HALF pairs dims (i, i + rot_dim / 2), INTERLEAVED
+ * (2i, 2i + 1); the dims from rot_dim on are left as they are. */
+enum { VD_ROPE_HALF = 0, VD_ROPE_INTERLEAVED = 1 };
+enum { VD_ROPE_SCALE_NONE = 0, VD_ROPE_SCALE_LINEAR = 1, VD_ROPE_SCALE_BANDS = 2, VD_ROPE_SCALE_YARN = 3 };
+typedef struct vd_rope vd_rope;
+typedef struct vd_rope_config {
+  int32_t head_dim;          /* even                                            */
+  int32_t rot_dim;           /* even, at most head_dim and 512; 0: head_dim     */
+  int32_t layout;            /* VD_ROPE_HALF or VD_ROPE_INTERLEAVED             */
+  int32_t scaling;           /* VD_ROPE_SCALE_*                                 */
+  double theta;              /* above 1                                         */
+  double factor;
+  double low_freq_factor, high_freq_factor; /* BANDS                            */
+  double beta_fast, beta_slow;              /* YARN                             */
+  double original_max_position;             /* BANDS, YARN                      */
+  double attn_factor;
+} vd_rope_config;
+/* A rope is host memory only: it serves every device, stream and position,
+ * and calls may share it.  Errors: VD_ERR_INVALID_ARG, VD_ERR_UNSUPPORTED,
+ * VD_ERR_CAPACITY. */
+int vd_rope_create(const vd_rope_config* cfg, vd_rope** out);
+void vd_destroy_rope(vd_rope* r);
+/* From here on the model rotates with these ropes: `global` on its global
+ * layers, `local` (null: the same) on its local ones, in place of the ones
+ * vd_create_model made from rope_theta.  The ropes are copied.  Keys already
+ * in a pool keep the rotation they were written with.  Synchronises the
+ * device and drops captured step graphs.
+ * Errors: VD_ERR_INVALID_ARG (another head_dim or device), VD_ERR_CUDA. */
+int vd_set_rope(vd_model* m, const vd_rope* global, const vd_rope* local);
+
 typedef struct vd_kernel_stat {
   char name[32];
   int32_t launches;   /* timed regions (event pairs) of this class     */

@@ -137,6 +137,19 @@ int vd_op_attention_static(vd_model* m, vd_kv_pool* p, int32_t layer, const vd_b
 int vd_op_rope_kv(vd_model* m, vd_kv_pool* p, int32_t layer, const vd_batch* b, const void* qkv, void* q_out,
                   void* stream);
 
+/* Rotates the heads of T tokens by their positions (dev int32 [T], any value;
+ * a negative one turns backwards): y[t][h] = rotation of x[t][h], or with
+ * inverse = 1 the vector that rotates to x[t][h] (it also divides by
+ * attn_factor).  x, y: dev, dtype VD_DTYPE_*, the head_dim elements of a row
+ * contiguous, token and head strides in elements (any for x; the rows of y
+ * must not overlap).  y may be x itself with the same strides, else they must
+ * not overlap.  Products and sums in float32, one rounding to the dtype; the
+ * angle is exact to 2^-33 of a turn at every position. */
+enum { VD_DTYPE_BF16 = 0, VD_DTYPE_F16 = 1, VD_DTYPE_F32 = 2 };
+int vd_op_rotary(const vd_rope* r, const void* x, void* y, int32_t T, int32_t H, int64_t x_stride_t, int64_t x_stride_h,
+                 int64_t y_stride_t, int64_t y_stride_h, int32_t dtype, const int32_t* positions, int32_t inverse,
+                 void* stream);
+
 /* The sampler's Philox4x32-10 stream: out[i] = word used for vocabulary index
  * i at (seed, step); dev uint32 [n]. */
 int vd_op_philox(uint64_t seed, uint64_t step, int32_t n, uint32_t* out, void* stream);

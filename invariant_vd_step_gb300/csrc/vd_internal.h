@@ -238,6 +238,7 @@ int launch_rmsnorm(const void* x, const int* row_idx, const void* w, void* y, in
 // then, if w_pre is not null, y = rms(x; w_pre).  Gains are w + gain_offset.
 int launch_postnorm_residual(const void* h, void* x, const void* w_post, const void* w_pre, void* y, int rows, int d,
                              float eps, float gain_offset, cudaStream_t s);
+constexpr int kRopeMaxPairs = 256;  // rotated pairs of a vd_rope
 // Which elements of a head form the rotated pairs: the first `rot` dims (0:
 // the whole head), pair i = (i, i + rot/2) or, interleaved, (2i, 2i + 1).
 struct RopeShape {

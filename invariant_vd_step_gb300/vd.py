@@ -84,6 +84,13 @@ class EngineStats(ctypes.Structure):
                 ("steps", "prefix_hit_pages", "registered", "evicted", "preempted", "hash_candidates_rejected")]
 
 
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32)] + \
+               [(n, ctypes.c_double) for n in ("theta", "factor", "low_freq_factor", "high_freq_factor", "beta_fast",
+                                               "beta_slow", "original_max_position", "attn_factor")]
+
+
 class TreeBatch(ctypes.Structure):
     _fields_ = [("num_nodes", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("page_table_stride", ctypes.c_int32),
                 ("pad_", ctypes.c_int32), ("cu_nodes", _I32P), ("parent", _I32P), ("cached_len", _I32P),
@@ -135,6 +142,11 @@ _SIGS = {
     "vd_op_tma_stream": (ctypes.c_int, [_VP, ctypes.c_int64, ctypes.c_int64, _VP, ctypes.c_int64, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP]),
     "vd_op_mma_issue_probe": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP, _VP]),
+    "vd_rope_create": (ctypes.c_int, [ctypes.POINTER(RopeConfig), ctypes.POINTER(_VP)]),
+    "vd_destroy_rope": (None, [_VP]),
+    "vd_set_rope": (ctypes.c_int, [_VP, _VP, _VP]),
+    "vd_op_rotary": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                                    ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _VP, ctypes.c_int32, _VP]),
     "vd_tree_create": (ctypes.c_int, [_VP, ctypes.c_int32, ctypes.POINTER(_VP)]),
     "vd_destroy_tree": (None, [_VP]),
     "vd_tree_plan": (ctypes.c_int, [_VP, _VP, ctypes.POINTER(TreeBatch), _VP]),
@@ -375,6 +387,10 @@ class Model:
         """0: batch-invariant steps (default); 1: fast split-K steps (not invariant; verify them)."""
         check(lib().vd_set_reduction_mode(self.h, int(mode)))
 
+    def set_rope(self, rope: "Rope", local: "Rope | None" = None):
+        """vd_set_rope: the ropes of the global layers and of the local ones (default: the same)."""
+        check(lib().vd_set_rope(self.h, rope.h, local.h if local is not None else None))
+
     def set_attention_fold(self, mode: int):
         """Decode attention mapping: 0 default (one CTA per split), 1 fold all splits in one CTA, 2 split."""
         check(lib().vd_set_attention_fold(self.h, int(mode)))
@@ -446,6 +462,60 @@ def _check_out(t, shape, dtype, name: str):
     _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
           f"{name}: a contiguous {dtype} CUDA tensor of shape {tuple(shape)} is needed, got {t.dtype} "
           f"{tuple(t.shape)} on {t.device}")
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+class Rope:
+    """A vd_rope: rotary positions with a pair layout, a rotated part of the head and a frequency scaling.
+
+    ``scaling``: None or a dict with "type" ("none", "linear", "bands", "yarn") and that type's parameters, named as
+    in vd_rope_config (factor, low_freq_factor, high_freq_factor, beta_fast, beta_slow, original_max_position,
+    attn_factor; YaRN's betas default to 32 and 1)."""
+
+    def __init__(self, head_dim: int, rot_dim: int = 0, layout: str = "half", theta: float = 1e4, scaling=None):
+        sc = dict(scaling or {})
+        kind = sc.pop("type", "none")
+        _need(layout in _LAYOUTS, f"layout {layout!r}: one of {sorted(_LAYOUTS)}")
+        _need(kind in _SCALINGS, f"scaling {kind!r}: one of {sorted(_SCALINGS)}")
+        if kind == "yarn":
+            sc = {"beta_fast": 32.0, "beta_slow": 1.0, **sc}
+        fields = {n for n, _ in RopeConfig._fields_[5:]}
+        _need(set(sc) <= fields, f"unknown scaling parameters {sorted(set(sc) - fields)}")
+        cfg = RopeConfig(head_dim, rot_dim, _LAYOUTS[layout], _SCALINGS[kind], theta, **{k: float(v) for k, v in sc.items()})
+        h = ctypes.c_void_p()
+        check(lib().vd_rope_create(ctypes.byref(cfg), ctypes.byref(h)))
+        self.h, self.head_dim = h, head_dim
+
+    def __del__(self):
+        try:
+            if getattr(self, "h", None):
+                lib().vd_destroy_rope(self.h)
+                self.h = None
+        except Exception:
+            pass
+
+    def apply(self, x: torch.Tensor, positions: torch.Tensor, out: torch.Tensor | None = None, inverse: bool = False,
+              stream=None) -> torch.Tensor:
+        """vd_op_rotary: x [T][H][head_dim] (bf16, fp16 or fp32, any token and head strides), positions int32 [T];
+        out like x (a new contiguous tensor by default; x itself to rotate in place)."""
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _need(x.dim() == 3 and x.shape == out.shape and x.shape[2] == self.head_dim,
+              f"x and out: [T][H][{self.head_dim}], got {tuple(x.shape)} and {tuple(out.shape)}")
+        _need(x.dtype in _DTYPES and out.dtype == x.dtype, f"x and out of one type, bf16, fp16 or fp32, got {x.dtype} "
+              f"and {out.dtype}")
+        _need(x.is_cuda and out.device == x.device and positions.device == x.device, "x, out and positions on one GPU")
+        _need(positions.dtype == torch.int32 and positions.shape == x.shape[:1] and positions.is_contiguous(),
+              "positions: contiguous int32 [T]")
+        T, H, _ = x.shape
+        _need(x.stride(2) == 1 and out.stride(2) == 1 or T * H == 0, "the elements of a row must be contiguous")
+        check(lib().vd_op_rotary(self.h, _ptr(x), _ptr(out), T, H, x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+                                 _DTYPES[x.dtype], _ptr(positions), int(inverse), _stream(stream)))
+        return out
 
 
 class Tree:
