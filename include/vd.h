@@ -144,6 +144,19 @@ typedef struct vd_sampler {
   float pad_;
 } vd_sampler;
 
+/* Filters of a row's token choice, in this order: the top_k most likely tokens
+ * (0: off); of these, from the most likely on, the tokens before which the
+ * probability mass is below top_p (1: off; the first token always stays); of
+ * these, the tokens at least min_p times as likely as the most likely one
+ * (0: off).  Probabilities are softmax(l / temperature), for top_p over the
+ * top_k tokens; equally likely tokens are ordered by index. */
+typedef struct vd_filter {
+  int32_t top_k;   /* >= 0       */
+  float top_p;     /* in [0, 1]  */
+  float min_p;     /* in [0, 1]  */
+  float pad_;
+} vd_filter;
+
 /* Rotary positions.  Pair i of a head's first rot_dim dims turns by angle
  * p * f_i at position p; f_i = theta^(-2i / rot_dim), scaled:
  *   LINEAR  f_i / factor (position interpolation);
@@ -299,6 +312,18 @@ int vd_graph_stats(const vd_model* m, int64_t* out4);
  * rows.  Errors: VD_ERR_INVALID_ARG (null or misaligned pointers, R < 0). */
 int vd_sample(vd_model* m, const float* logits, int32_t R, const vd_sampler* per_row,
               int32_t* tokens_out, void* stream);
+
+/* vd_sample with filters: the same choice, argmax(l_i / T - log(-log(u_i)))
+ * with the row's random numbers, over the tokens that the row's filters keep
+ * (filters: host [R]; null: none), so that a row without filters gets
+ * vd_sample's token.  logprobs_out (dev float32 [R], nullable): the
+ * log-probability of the chosen token under the distribution it was drawn
+ * from, softmax(l / T) over the kept tokens; 0 for a greedy row, whose filters
+ * do not matter.  Tokens of logit -inf or NaN are never kept; a row without
+ * any other gets vd_sample's token, at log-probability 0.  Errors as vd_sample, and
+ * VD_ERR_INVALID_ARG for filters out of range. */
+int vd_sample_filtered(vd_model* m, const float* logits, int32_t R, const vd_sampler* per_row,
+                       const vd_filter* filters, int32_t* tokens_out, float* logprobs_out, void* stream);
 
 /* One engine step with the token choice fused into the LM-head GEMM
  * [B §二 Definition 2.1: per-request sampler_0; Theorem 4.1 for the logits].

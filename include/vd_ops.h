@@ -137,6 +137,20 @@ int vd_op_attention_static(vd_model* m, vd_kv_pool* p, int32_t layer, const vd_b
 int vd_op_rope_kv(vd_model* m, vd_kv_pool* p, int32_t layer, const vd_batch* b, const void* qkv, void* q_out,
                   void* stream);
 
+/* vd_sample_filtered for logits of any vocabulary size and row stride, without
+ * a model: logits dev float32 [R] rows of V, row_stride elements apart
+ * (at least V); rows whose stride is a multiple of 4 on a 16-byte aligned base
+ * load 16 bytes at a time.  workspace: dev, vd_sample_workspace_bytes(R, V)
+ * bytes, 16-byte aligned, in use until the call's work is done (calls that may
+ * run at the same time, captured graphs included, need one each).  The host
+ * arrays are read during the call; captured into a graph, the call replays
+ * with the values it was captured with.  V in [1, 2^21].
+ * Errors: VD_ERR_INVALID_ARG, VD_ERR_UNSUPPORTED, VD_ERR_CAPACITY, VD_ERR_CUDA. */
+size_t vd_sample_workspace_bytes(int32_t R, int32_t V);
+int vd_op_sample(const float* logits, int32_t R, int32_t V, int64_t row_stride, const vd_sampler* per_row,
+                 const vd_filter* filters, int32_t* tokens_out, float* logprobs_out, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
 /* Rotates the heads of T tokens by their positions (dev int32 [T], any value;
  * a negative one turns backwards): y[t][h] = rotation of x[t][h], or with
  * inverse = 1 the vector that rotates to x[t][h] (it also divides by

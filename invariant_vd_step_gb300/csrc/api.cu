@@ -1090,6 +1090,53 @@ int vd_sample(vd_model* m, const float* logits, int32_t R, const vd_sampler* per
   return launch_sample(logits, R, m->cfg.vocab, m->d_samp, m->samp_part_v, m->samp_part_i, tokens_out, s);
 }
 
+namespace {
+int check_filters(const vd_filter* f, int R) {
+  for (int i = 0; f && i < R; ++i)
+    if (f[i].top_k < 0 || !(f[i].top_p >= 0.f && f[i].top_p <= 1.f) || !(f[i].min_p >= 0.f && f[i].min_p <= 1.f))
+      return fail(VD_ERR_INVALID_ARG, "filters: top_k >= 0, top_p and min_p in [0, 1]");
+  return VD_OK;
+}
+}  // namespace
+
+int vd_sample_filtered(vd_model* m, const float* logits, int32_t R, const vd_sampler* per_row,
+                       const vd_filter* filters, int32_t* tokens_out, float* logprobs_out, void* stream) {
+  if (check_model(m)) return VD_ERR_INVALID_ARG;
+  if (R < 0 || R > m->cfg.max_logit_rows) return fail(VD_ERR_CAPACITY, "R exceeds max_logit_rows");
+  if (R == 0) return VD_OK;
+  if (!logits || !per_row || !tokens_out) return fail(VD_ERR_INVALID_ARG, "null argument");
+  if (reinterpret_cast<uintptr_t>(logits) & 15) return fail(VD_ERR_INVALID_ARG, "logits must be 16-byte aligned");
+  if (const int rc = check_filters(filters, R)) return rc;
+  if (m->cfg.vocab > (1 << 21)) return fail(VD_ERR_UNSUPPORTED, "filters take vocabularies of at most 2^21 tokens");
+  if (!m->filter_ws)
+    if (const int rc = dev_alloc(m, &m->filter_ws, sample_filter_workspace(m->cfg.max_logit_rows, m->cfg.vocab))) return rc;
+  SampleFilterArgs a{logits, R, m->cfg.vocab, m->cfg.vocab, per_row, filters, tokens_out, logprobs_out, m->filter_ws};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Prof p(m, K_SAMPLE, s);
+  p.kernels = 2 * ((R + 511) / 512);
+  return launch_sample_filter(a, s);
+}
+
+size_t vd_sample_workspace_bytes(int32_t R, int32_t V) { return R < 1 || V < 1 ? 0 : sample_filter_workspace(R, V); }
+
+int vd_op_sample(const float* logits, int32_t R, int32_t V, int64_t row_stride, const vd_sampler* per_row,
+                 const vd_filter* filters, int32_t* tokens_out, float* logprobs_out, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+  if (R < 0 || V < 1) return fail(VD_ERR_INVALID_ARG, "R >= 0 and V >= 1");
+  if (V > (1 << 21)) return fail(VD_ERR_UNSUPPORTED, "filters take vocabularies of at most 2^21 tokens");
+  if (R == 0) return VD_OK;
+  if (R > 1 && row_stride < V) return fail(VD_ERR_INVALID_ARG, "row_stride below V");
+  if (!logits || !per_row || !tokens_out || !workspace) return fail(VD_ERR_INVALID_ARG, "null argument");
+  if ((reinterpret_cast<uintptr_t>(logits) & 3) || (reinterpret_cast<uintptr_t>(tokens_out) & 3) ||
+      (reinterpret_cast<uintptr_t>(logprobs_out) & 3) || !aligned16(workspace))
+    return fail(VD_ERR_INVALID_ARG, "pointers must be aligned (workspace: 16 bytes)");
+  if (workspace_bytes < sample_filter_workspace(R, V))
+    return fail(VD_ERR_CAPACITY, "workspace smaller than vd_sample_workspace_bytes()");
+  if (const int rc = check_filters(filters, R)) return rc;
+  SampleFilterArgs a{logits, R, V, R > 1 ? row_stride : 0, per_row, filters, tokens_out, logprobs_out, workspace};
+  return launch_sample_filter(a, static_cast<cudaStream_t>(stream));
+}
+
 int vd_copy_kv(vd_model* m, vd_kv_pool* pool, int32_t layer, const int32_t* page_table, int32_t n_tokens,
                void* out_k, void* out_v, void* stream) {
   if (check_model(m) || !pool || pool->m != m) return fail(VD_ERR_INVALID_ARG, "null or foreign model/pool");

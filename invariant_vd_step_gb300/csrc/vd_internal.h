@@ -271,6 +271,19 @@ int launch_sample(const float* logits, int R, int V, const vd_sampler* dev_param
                   int* out, cudaStream_t s);
 // Second pass alone: per row, the best of nchunk (score, index) partials.
 int launch_sample_final(const float* part_v, const int* part_i, int R, int nchunk, int* out, cudaStream_t s);
+// Filtered token choice; workspace: sample_filter_workspace(R, V) bytes, 16-byte aligned.
+struct SampleFilterArgs {
+  const float* logits;        // [R][ld]
+  int R, V;
+  long long ld;
+  const vd_sampler* samplers; // host [R]
+  const vd_filter* filters;   // host [R] or null (no filters)
+  int* tokens;                // [R]
+  float* logprobs;            // [R] or null
+  void* workspace;
+};
+size_t sample_filter_workspace(int R, int V);
+int launch_sample_filter(const SampleFilterArgs& a, cudaStream_t s);
 int launch_philox(uint64_t seed, uint64_t step, int n, uint32_t* out, cudaStream_t s);
 int launch_wait_probe(int* status, uint64_t limit_ns, int* out, cudaStream_t s);
 // Streams a [rows][K] bf16 weight matrix through shared memory with a GEMM

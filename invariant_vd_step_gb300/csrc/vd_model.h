@@ -136,6 +136,7 @@ struct vd_model {
   float* fused_part_v = nullptr;  // per-32-row-group winners of the fused LM-head epilogue
   int* fused_part_i = nullptr;
   vd_sampler* h_samp = nullptr;
+  void* filter_ws = nullptr;     // workspace of the filtered token choice (allocated on first use)
   cudaEvent_t samp_ev = nullptr;
   std::vector<void*> dev_allocs;
   // profiling

@@ -84,6 +84,11 @@ class EngineStats(ctypes.Structure):
                 ("steps", "prefix_hit_pages", "registered", "evicted", "preempted", "hash_candidates_rejected")]
 
 
+# The same layouts as numpy records, for callers that keep their rows' states as arrays.
+SAMPLER = np.dtype([("seed", "u8"), ("step", "u8"), ("temperature", "f4"), ("pad_", "f4")])
+FILTER = np.dtype([("top_k", "i4"), ("top_p", "f4"), ("min_p", "f4"), ("pad_", "f4")])
+
+
 class RopeConfig(ctypes.Structure):
     _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
                 ("scaling", ctypes.c_int32)] + \
@@ -142,6 +147,10 @@ _SIGS = {
     "vd_op_tma_stream": (ctypes.c_int, [_VP, ctypes.c_int64, ctypes.c_int64, _VP, ctypes.c_int64, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP]),
     "vd_op_mma_issue_probe": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP, _VP]),
+    "vd_sample_filtered": (ctypes.c_int, [_VP, _VP, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP]),
+    "vd_sample_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "vd_op_sample": (ctypes.c_int, [_VP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, _VP, _VP, _VP, _VP, _VP,
+                                    ctypes.c_size_t, _VP]),
     "vd_rope_create": (ctypes.c_int, [ctypes.POINTER(RopeConfig), ctypes.POINTER(_VP)]),
     "vd_destroy_rope": (None, [_VP]),
     "vd_set_rope": (ctypes.c_int, [_VP, _VP, _VP]),
@@ -227,6 +236,35 @@ def config_of(spec, max_tokens: int, max_seqs: int, max_logit_rows: int, max_con
         max_seqs=max_seqs, max_logit_rows=max_logit_rows, max_context=max_context,
         embed_scale=int(getattr(spec, "embed_scale", False)), norm_offset=int(getattr(spec, "norm_offset", False)),
         sandwich_norm=int(getattr(spec, "sandwich_norm", False)))
+
+
+def _need(ok, message: str):
+    """Argument checks that only the binding can make (it sees tensors, the library pointers)."""
+    if not ok:
+        raise VDError(VD_ERR_INVALID_ARG, message)
+
+
+def _rows(rows, dtype):
+    """Per-row states as one array of records: an array of that dtype as it is, else from tuples without the padding."""
+    if rows is None or (isinstance(rows, np.ndarray) and rows.dtype == dtype and rows.flags.c_contiguous):
+        return rows
+    return np.array([(*r, 0) for r in rows], dtype=dtype)
+
+
+def _rows_ptr(rows):
+    return None if rows is None else rows.ctypes.data
+
+
+def _check_choice(logits, V, samplers, filters, tokens_out, logprobs_out):
+    R = len(samplers)
+    if not (logits.is_cuda and logits.dtype == torch.float32 and logits.dim() == 2 and tuple(logits.shape) == (R, V)
+            and (V == 0 or logits.stride(1) == 1)):
+        raise VDError(VD_ERR_INVALID_ARG, f"logits: float32 CUDA rows [{R}][{V}], one sampler each")
+    if filters is not None and len(filters) != R:
+        raise VDError(VD_ERR_INVALID_ARG, "one filter per row")
+    for t, dtype in ((tokens_out, torch.int32), (logprobs_out, torch.float32)):
+        if t is not None and not (t.device == logits.device and t.dtype == dtype and t.shape == (R,) and t.is_contiguous()):
+            raise VDError(VD_ERR_INVALID_ARG, f"one contiguous {dtype} output per row, on the logits' GPU")
 
 
 class StepBatch:
@@ -334,6 +372,15 @@ class Model:
         for i, (seed, step, temp) in enumerate(samplers):
             arr[i] = Sampler(seed, step, temp, 0.0)
         check(lib().vd_sample(self.h, _ptr(logits), R, arr, _ptr(tokens_out), _stream(stream)))
+
+    def sample_filtered(self, logits: torch.Tensor, samplers, filters, tokens_out: torch.Tensor, logprobs_out=None,
+                        stream=None):
+        """vd_sample_filtered: `sample` among the tokens that each row's (top_k, top_p, min_p) keeps."""
+        s, f = _rows(samplers, SAMPLER), _rows(filters, FILTER)
+        _check_choice(logits, self.spec.vocab, s, f, tokens_out, logprobs_out)
+        _need(logits.is_contiguous(), "logits must be contiguous")
+        check(lib().vd_sample_filtered(self.h, _ptr(logits), len(s), _rows_ptr(s), _rows_ptr(f), _ptr(tokens_out),
+                                       _ptr(logprobs_out), _stream(stream)))
 
     def step_sample(self, pool: "KVPool", batch: StepBatch, samplers, logits, tokens_out: torch.Tensor,
                     stream=None):
@@ -452,16 +499,32 @@ class KVPool:
             .view(s.n_layers, self.num_pages, 2, s.n_kv_heads, 16, s.head_dim)
 
 
-def _need(ok, message: str):
-    """Argument checks that only the binding can make (it sees tensors, the library pointers)."""
-    if not ok:
-        raise VDError(VD_ERR_INVALID_ARG, message)
-
-
 def _check_out(t, shape, dtype, name: str):
     _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
           f"{name}: a contiguous {dtype} CUDA tensor of shape {tuple(shape)} is needed, got {t.dtype} "
           f"{tuple(t.shape)} on {t.device}")
+
+
+def sample_workspace(R: int, V: int, device="cuda") -> torch.Tensor:
+    """Workspace of `sample` for up to R rows of V logits."""
+    return torch.empty(int(lib().vd_sample_workspace_bytes(R, V)), dtype=torch.uint8, device=device)
+
+
+def sample(logits: torch.Tensor, samplers, filters, tokens_out: torch.Tensor, logprobs_out=None, workspace=None,
+           stream=None):
+    """vd_op_sample: the token choice with filters for logits [R][V] of any row stride.  samplers: (seed, step,
+    temperature) per row; filters: (top_k, top_p, min_p) per row or None; workspace: from `sample_workspace`, kept by
+    the caller (default: a new one, which torch's allocator may hand out again only to work on the current stream)."""
+    s, f = _rows(samplers, SAMPLER), _rows(filters, FILTER)
+    _check_choice(logits, logits.shape[-1], s, f, tokens_out, logprobs_out)
+    R, V = logits.shape
+    if workspace is None:
+        workspace = sample_workspace(R, V, logits.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    check(lib().vd_op_sample(_ptr(logits), R, V, logits.stride(0), _rows_ptr(s), _rows_ptr(f), _ptr(tokens_out),
+                             _ptr(logprobs_out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                             _stream(stream)))
 
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
