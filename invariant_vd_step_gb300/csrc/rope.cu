@@ -103,35 +103,55 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T, E>& r) {
     *p = r.v[0];
 }
 
-// Block (x: a head's chunks, y: heads in parallel, z: tokens).  A chunk is two
-// packs: half layout, elements i.. of the first half and of the second;
-// interleaved, 2E neighbours.  The block first computes its tokens' cosines
-// and sines once for all heads, then each thread keeps those of its chunk in
-// registers and runs over the heads, kUnroll at a time.  Bound by memory.
+// Block (x: a head's chunks, y: heads, z: tokens).  A chunk is two packs: half
+// layout, elements i.. of the first half and of the second; interleaved, 2E
+// neighbours.  A thread's first kUnroll heads are loaded before anything else,
+// so that the position's round trip, the cosines and sines (once per token for
+// all heads) and the barrier pass while the data is on its way.
 constexpr int kUnroll = 4;
 template <typename T, int E, bool INTER>
 __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RopeTurns turns, RotaryArgs a) {
   extern __shared__ float cs_s[];  // [tokens][2][pairs]: cosines, then sines
   const int pairs = a.rot >> 1, chunks = pairs / E;
+  const int total = chunks + (a.rest ? (a.hd - a.rot) / (2 * E) : 0);
   const int tid = threadIdx.x + blockDim.x * (threadIdx.y + blockDim.y * threadIdx.z);
   const int threads = blockDim.x * blockDim.y * blockDim.z;
   const long long t0 = static_cast<long long>(blockIdx.x) * blockDim.z;
   const int nt = static_cast<int>(min(static_cast<long long>(blockDim.z), a.T - t0));
-  pdl_wait();
-  pdl_trigger();
-  for (int k = tid; k < nt * pairs; k += threads) {
-    const int tt = k / pairs, i = k % pairs;
-    const float2 c = turn_cs(turns.turn[i], a.pos[t0 + tt], a.mag);
-    cs_s[(2 * tt) * pairs + i] = c.x;
-    cs_s[(2 * tt + 1) * pairs + i] = a.inverse ? -c.y : c.y;
-  }
-  __syncthreads();
   const int tt = threadIdx.z;
-  if (tt >= nt) return;
   const T* x = static_cast<const T*>(a.x) + (t0 + tt) * a.xs_t;
   T* y = static_cast<T*>(a.y) + (t0 + tt) * a.ys_t;
-  const int total = chunks + (a.rest ? (a.hd - a.rot) / (2 * E) : 0);
-  for (int ch = threadIdx.x; ch < total; ch += blockDim.x) {
+  int ch = threadIdx.x, h0 = threadIdx.y;
+  Pack<T, E> p0[kUnroll], p1[kUnroll];
+  auto offsets = [&](int& o0, int& o1) {  // the chunk's two packs
+    const bool split = ch < chunks && !INTER;
+    o0 = split ? ch * E : ch * 2 * E;
+    o1 = split ? o0 + pairs : o0 + E;
+  };
+  auto load = [&] {
+    int o0, o1;
+    offsets(o0, o1);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + u * blockDim.y;
+      if (h >= a.H) continue;
+      p0[u] = load_pack<T, E>(x + h * a.xs_h + o0);
+      p1[u] = load_pack<T, E>(x + h * a.xs_h + o1);
+    }
+  };
+  pdl_wait();
+  pdl_trigger();
+  if (tt < nt && ch < total) load();
+  for (int k = tid; k < nt * pairs; k += threads) {
+    const int tk = k / pairs, i = k % pairs;
+    const float2 c = turn_cs(turns.turn[i], a.pos[t0 + tk], a.mag);
+    cs_s[(2 * tk) * pairs + i] = c.x;
+    cs_s[(2 * tk + 1) * pairs + i] = a.inverse ? -c.y : c.y;
+  }
+  __syncthreads();
+  if (tt >= nt) return;
+  bool loaded = true;
+  for (; ch < total; ch += blockDim.x) {
     const bool rot = ch < chunks;
     float c[E], s[E];
     if (rot) {
@@ -141,17 +161,11 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rop
         s[k] = cs_s[(2 * tt + 1) * pairs + ch * E + k];
       }
     }
-    const int o0 = !rot || INTER ? ch * 2 * E : ch * E;       // the chunk's two packs
-    const int o1 = !rot || INTER ? o0 + E : o0 + pairs;
-    for (int h0 = threadIdx.y; h0 < a.H; h0 += blockDim.y * kUnroll) {
-      Pack<T, E> p0[kUnroll], p1[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = h0 + u * blockDim.y;
-        if (h >= a.H) continue;
-        p0[u] = load_pack<T, E>(x + h * a.xs_h + o0);
-        p1[u] = load_pack<T, E>(x + h * a.xs_h + o1);
-      }
+    int o0, o1;
+    offsets(o0, o1);
+    for (h0 = threadIdx.y; h0 < a.H; h0 += blockDim.y * kUnroll) {
+      if (!loaded) load();
+      loaded = false;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int h = h0 + u * blockDim.y;
@@ -190,10 +204,10 @@ template <typename T, int E>
 int launch_rotary(const vd_rope* r, const RotaryArgs& a, cudaStream_t s) {
   const int pairs = a.rot / 2;
   const int total = pairs / E + (a.rest ? (a.hd - a.rot) / (2 * E) : 0);
-  // 256 threads: the chunks of a head, then heads, then tokens
+  // up to 256 threads: the chunks of a head, every kUnroll-th head, then tokens
   dim3 block(std::min(total, 128), 1, 1);
-  block.y = std::max(1, std::min<int>(a.H, 256 / block.x));
-  block.z = std::max(1, std::min<int>({a.T, 4, static_cast<int>(256 / (block.x * block.y))}));
+  block.y = std::max(1, std::min<int>((a.H + kUnroll - 1) / kUnroll, 256 / block.x));
+  block.z = std::max(1, std::min<int>({a.T, 8, static_cast<int>(256 / (block.x * block.y))}));
   const unsigned blocks = (static_cast<unsigned>(a.T) + block.z - 1) / block.z;
   const size_t smem = static_cast<size_t>(block.z) * a.rot * sizeof(float);
   auto k = r->cfg.layout == VD_ROPE_INTERLEAVED ? rotary_kernel<T, E, true> : rotary_kernel<T, E, false>;

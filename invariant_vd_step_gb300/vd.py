@@ -217,6 +217,20 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# torch.cuda.current_stream() builds a Python object per call (2.9 us); this gives the handle alone (0.1 us).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, device: int) -> int:
+    """Handle of `stream`, or of the current stream of `device`, the tensors' device, which has to be the current one."""
+    if device != torch.cuda.current_device():
+        raise VDError(VD_ERR_INVALID_ARG, f"the tensors are on cuda:{device}, the current device is "
+                                          f"cuda:{torch.cuda.current_device()}")
+    if stream is not None:
+        return stream.cuda_stream
+    return _current_raw_stream(device) if _current_raw_stream else torch.cuda.current_stream().cuda_stream
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -257,8 +271,8 @@ def _rows_ptr(rows):
 
 def _check_choice(logits, V, samplers, filters, tokens_out, logprobs_out):
     R = len(samplers)
-    if not (logits.is_cuda and logits.dtype == torch.float32 and logits.dim() == 2 and tuple(logits.shape) == (R, V)
-            and (V == 0 or logits.stride(1) == 1)):
+    if not (logits.is_cuda and logits.dtype == torch.float32 and logits.shape == (R, V)
+            and (V <= 1 or logits.stride(1) == 1)):
         raise VDError(VD_ERR_INVALID_ARG, f"logits: float32 CUDA rows [{R}][{V}], one sampler each")
     if filters is not None and len(filters) != R:
         raise VDError(VD_ERR_INVALID_ARG, "one filter per row")
@@ -379,8 +393,9 @@ class Model:
         s, f = _rows(samplers, SAMPLER), _rows(filters, FILTER)
         _check_choice(logits, self.spec.vocab, s, f, tokens_out, logprobs_out)
         _need(logits.is_contiguous(), "logits must be contiguous")
-        check(lib().vd_sample_filtered(self.h, _ptr(logits), len(s), _rows_ptr(s), _rows_ptr(f), _ptr(tokens_out),
-                                       _ptr(logprobs_out), _stream(stream)))
+        check(lib().vd_sample_filtered(self.h, logits.data_ptr(), len(s), _rows_ptr(s), _rows_ptr(f),
+                                       tokens_out.data_ptr(), None if logprobs_out is None else logprobs_out.data_ptr(),
+                                       _raw_stream(stream, logits.get_device())))
 
     def step_sample(self, pool: "KVPool", batch: StepBatch, samplers, logits, tokens_out: torch.Tensor,
                     stream=None):
@@ -500,9 +515,9 @@ class KVPool:
 
 
 def _check_out(t, shape, dtype, name: str):
-    _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-          f"{name}: a contiguous {dtype} CUDA tensor of shape {tuple(shape)} is needed, got {t.dtype} "
-          f"{tuple(t.shape)} on {t.device}")
+    if not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        raise VDError(VD_ERR_INVALID_ARG, f"{name}: a contiguous {dtype} CUDA tensor of shape {shape} is needed, got "
+                                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def sample_workspace(R: int, V: int, device="cuda") -> torch.Tensor:
@@ -522,9 +537,13 @@ def sample(logits: torch.Tensor, samplers, filters, tokens_out: torch.Tensor, lo
         workspace = sample_workspace(R, V, logits.device)
         if stream is not None:
             workspace.record_stream(stream)
-    check(lib().vd_op_sample(_ptr(logits), R, V, logits.stride(0), _rows_ptr(s), _rows_ptr(f), _ptr(tokens_out),
-                             _ptr(logprobs_out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                             _stream(stream)))
+    if workspace.get_device() != logits.get_device() or not workspace.is_contiguous():
+        raise VDError(VD_ERR_INVALID_ARG, "workspace: contiguous, on the logits' GPU")
+    rc = lib().vd_op_sample(logits.data_ptr(), R, V, logits.stride(0), _rows_ptr(s), _rows_ptr(f),
+                            tokens_out.data_ptr(), None if logprobs_out is None else logprobs_out.data_ptr(),
+                            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, logits.get_device()))
+    if rc:
+        check(rc)
 
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -567,17 +586,24 @@ class Rope:
         out like x (a new contiguous tensor by default; x itself to rotate in place)."""
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _need(x.dim() == 3 and x.shape == out.shape and x.shape[2] == self.head_dim,
-              f"x and out: [T][H][{self.head_dim}], got {tuple(x.shape)} and {tuple(out.shape)}")
-        _need(x.dtype in _DTYPES and out.dtype == x.dtype, f"x and out of one type, bf16, fp16 or fp32, got {x.dtype} "
-              f"and {out.dtype}")
-        _need(x.is_cuda and out.device == x.device and positions.device == x.device, "x, out and positions on one GPU")
-        _need(positions.dtype == torch.int32 and positions.shape == x.shape[:1] and positions.is_contiguous(),
-              "positions: contiguous int32 [T]")
-        T, H, _ = x.shape
-        _need(x.stride(2) == 1 and out.stride(2) == 1 or T * H == 0, "the elements of a row must be contiguous")
-        check(lib().vd_op_rotary(self.h, _ptr(x), _ptr(out), T, H, x.stride(0), x.stride(1), out.stride(0), out.stride(1),
-                                 _DTYPES[x.dtype], _ptr(positions), int(inverse), _stream(stream)))
+        shape, dtype, device = x.shape, _DTYPES.get(x.dtype), x.get_device()
+        if len(shape) != 3 or out.shape != shape or shape[2] != self.head_dim:
+            raise VDError(VD_ERR_INVALID_ARG, f"x and out: [T][H][{self.head_dim}], got {tuple(shape)} and "
+                                              f"{tuple(out.shape)}")
+        if dtype is None or out.dtype != x.dtype:
+            raise VDError(VD_ERR_INVALID_ARG, f"x and out of one type, bf16, fp16 or fp32, got {x.dtype} and {out.dtype}")
+        T, H, _ = shape
+        if device < 0 or out.get_device() != device or positions.get_device() != device:
+            raise VDError(VD_ERR_INVALID_ARG, "x, out and positions on one GPU")
+        if positions.dtype != torch.int32 or positions.shape != (T,) or not positions.is_contiguous():
+            raise VDError(VD_ERR_INVALID_ARG, "positions: contiguous int32 [T]")
+        (xt, xh, xe), (yt, yh, ye) = x.stride(), out.stride()
+        if (xe != 1 or ye != 1) and T * H > 0:
+            raise VDError(VD_ERR_INVALID_ARG, "the elements of a row must be contiguous")
+        rc = lib().vd_op_rotary(self.h, x.data_ptr(), out.data_ptr(), T, H, xt, xh, yt, yh, dtype, positions.data_ptr(),
+                                1 if inverse else 0, _raw_stream(stream, device))
+        if rc:
+            check(rc)
         return out
 
 
@@ -622,22 +648,26 @@ class Tree:
 
     def attention(self, pool: KVPool, layer: int, q: torch.Tensor, out: torch.Tensor, stream=None):
         """vd_op_tree_attention: q, out bf16 [T][Hq][hd]."""
-        s = self.model.spec
-        for t, name in ((q, "q"), (out, "out")):
-            _check_out(t, (self.num_nodes, s.n_heads, s.head_dim), torch.bfloat16, name)
-        check(lib().vd_op_tree_attention(self.h, pool.h, layer, _ptr(q), _ptr(out), _stream(stream)))
+        shape = (self.num_nodes, self.model.spec.n_heads, self.model.spec.head_dim)
+        _check_out(q, shape, torch.bfloat16, "q")
+        _check_out(out, shape, torch.bfloat16, "out")
+        rc = lib().vd_op_tree_attention(self.h, pool.h, layer, q.data_ptr(), out.data_ptr(),
+                                        _raw_stream(stream, out.get_device()))
+        if rc:
+            check(rc)
 
     def rope_kv(self, pool: KVPool, layer: int, qkv: torch.Tensor, q_out: torch.Tensor, stream=None):
         """vd_op_tree_rope_kv: qkv bf16 [T][(Hq + 2 Hkv) hd], q_out bf16 [T][Hq][hd]."""
         s = self.model.spec
         _check_out(qkv, (self.num_nodes, s.qkv_dim), torch.bfloat16, "qkv")
         _check_out(q_out, (self.num_nodes, s.n_heads, s.head_dim), torch.bfloat16, "q_out")
-        check(lib().vd_op_tree_rope_kv(self.h, pool.h, layer, _ptr(qkv), _ptr(q_out), _stream(stream)))
+        check(lib().vd_op_tree_rope_kv(self.h, pool.h, layer, qkv.data_ptr(), q_out.data_ptr(),
+                                       _raw_stream(stream, q_out.get_device())))
 
     def step(self, pool: KVPool, logits: torch.Tensor, stream=None):
         """vd_step_tree: logits float32 [T][V] of every planned node."""
         _check_out(logits, (self.num_nodes, self.model.spec.vocab), torch.float32, "logits")
-        check(lib().vd_step_tree(self.h, pool.h, _ptr(logits), _stream(stream)))
+        check(lib().vd_step_tree(self.h, pool.h, logits.data_ptr(), _raw_stream(stream, logits.get_device())))
 
     def accept(self, pool: KVPool, node_tokens, choices: torch.Tensor, accepted_len: torch.Tensor,
                out_tokens: torch.Tensor, stream=None):
@@ -647,10 +677,13 @@ class Tree:
         if node_tokens is not None:
             _check_out(node_tokens, (self.num_nodes,), torch.int32, "node_tokens")
         _check_out(accepted_len, (self.num_seqs,), torch.int32, "accepted_len")
-        _need(out_tokens.dim() == 2, "out_tokens: [B][stride]")
-        _check_out(out_tokens, (self.num_seqs, out_tokens.shape[1]), torch.int32, "out_tokens")
-        check(lib().vd_tree_accept(self.h, pool.h, _ptr(node_tokens), _ptr(choices), _ptr(accepted_len),
-                                   _ptr(out_tokens), out_tokens.shape[1], _stream(stream)))
+        stride = out_tokens.shape[-1]
+        _check_out(out_tokens, (self.num_seqs, stride), torch.int32, "out_tokens")
+        rc = lib().vd_tree_accept(self.h, pool.h, None if node_tokens is None else node_tokens.data_ptr(),
+                                  choices.data_ptr(), accepted_len.data_ptr(), out_tokens.data_ptr(), stride,
+                                  _raw_stream(stream, choices.get_device()))
+        if rc:
+            check(rc)
 
 
 def gemm(A, W, C, epilogue=EPI_BF16, residual=None, stream=None):
