@@ -7,21 +7,34 @@
 // sampler.cu over the kept tokens, with the same random numbers and the same
 // scores, so that a row without filters gets exactly vd_sample's token.
 //
-// Almost every row is decided by a few dozen of its V logits.  Pass 1 reads
-// the logits once, at memory speed: a warp takes a segment of 1024, finds its
-// maximum, its sum of exponentials and a threshold that at least `keep` of
-// its logits reach (the keep-th largest of the 32 lanes' maxima), and writes
-// the logits from that threshold on to a short list.  Every logit at or above
-// the largest threshold of a row's segments is then in a list.  Pass 2, one
-// cluster per row, sorts as many listed candidates as it needs and walks down
-// them.  Where the cut lies below the lists (flat distributions, huge top_k,
-// logits sorted by value along the vocabulary), the cluster re-reads the row:
-// a histogram over 2048 bins of value finds the bin of the cut, bins of the
-// (value, index) order refine it until it holds at most kList tokens, and one
-// more pass scores everything above the bin and collects it.
+// Almost every row is decided by a few dozen of its V logits.
 //
-// Sums that decide something do not depend on timing: candidate masses are
-// summed in sorted order, histogram masses as 64-bit integers.
+//   scan     reads the logits once, at memory speed.  A warp takes a segment
+//            of 1024, finds its maximum, its sum of exponentials and a
+//            threshold that a few of its logits reach (the smallest maximum of
+//            a few groups of lanes), and writes the logits from that threshold
+//            on to a short list: every logit at or above the largest threshold
+//            of a row's segments is then in a list.
+//   select   one CTA per row sorts as many listed candidates as it needs and
+//            walks down them.
+//
+// A row whose cut lies below the lists (flat distributions, logits sorted
+// along the vocabulary) is "wide".  Two more kernels, whose CTAs take (wide
+// row, chunk of 8192) items, read it again:
+//
+//   count    a histogram of 4096 bins of value, tokens and their mean place in
+//            the bin; the last CTA of a row estimates each bin's mass from
+//            them and picks the window of bins that holds the cut;
+//   collect  scores every token above the window and sums their mass, and
+//            lists the tokens inside it; the last CTA of a row sorts those,
+//            checks that the cut is among them and chooses.
+//
+// What that cannot settle (a window of more than kList tokens, top-p within a
+// top_k beyond the lists) one CTA settles by exact histograms over the
+// (value, index) order, refined until the cut's bin fits the list.
+//
+// Sums that decide something do not depend on timing: candidates are summed
+// in sorted order, chunks in their order, histogram masses as integers.
 #include <limits.h>
 #include <math.h>
 
@@ -37,8 +50,12 @@ constexpr int kSeg = 1024;        // logits of a segment (one warp: 8 x 4 per la
 constexpr int kSegCap = 64;       // list entries per segment
 constexpr int kScanThreads = 256;
 constexpr int kSelThreads = 256;
-constexpr int kBins = 2048;
-constexpr int kList = 2048;       // candidates that pass 2 sorts
+constexpr int kBins = 2048;       // exact histogram: counts and masses, by (value, index) order
+constexpr int kCountBins = 4096;  // a wide row's histogram, by value
+constexpr float kBinNats = 24.f;  // its range below the largest logit, in units of T
+constexpr int kList = 2048;       // candidates that a CTA sorts
+constexpr int kChunk = 8192;      // tokens of a wide row's work item
+constexpr int kScanRows = 120;    // rows of a scan launch: their parameters fit 4 KB
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMassScale = 68719476736.f;  // 2^36: fixed-point unit of histogram masses (V <= 2^21: sums below 2^57)
 
@@ -59,7 +76,7 @@ __device__ __forceinline__ int row_mode(const RowParam& p) {
 }
 
 // What pass 1 leaves of a segment.
-struct __align__(32) SegOut {
+struct __align__(16) SegOut {
   float max, sum;   // largest logit; sum of exp((l - max) / T)
   uint32_t thr;     // every logit whose key is at least this is in the list
   int count;        // list entries
@@ -93,28 +110,37 @@ __device__ __forceinline__ float weight(float l, float m, float c) {
 // The best Gumbel score of a stream of tokens, without the two logarithms
 // for tokens that cannot win: G = -log(-log u) <= -log(1 - u), so a token
 // beats `best` only if 1 - u <= exp(x - best).  The test errs on the side of
-// scoring (1e-3 and 2^-21 of the magnitudes cover its own rounding and that of
-// the score), so the winner is the one that scoring every token finds.
+// scoring: its margin (1e-3 and 2^-20 of the magnitudes) covers the rounding
+// of the test, of l / T and of the score, so the winner is the one that
+// scoring every token finds.  It costs six instructions a token; 1 - u is
+// read off the random word as the float 1 + 2^-23 (~word >> 9).
 struct Race {
   float best = -INFINITY;
   int best_i = INT_MAX;
-  float lim = -INFINITY;  // best less its margin
-  __device__ __forceinline__ void set_lim() {
-    lim = __fsub_rn(best, __fadd_rn(__fmul_rn(fabsf(best), 4.76837158203125e-7f), 1e-3f));
+  float k0 = INFINITY;  // -log2(e) (best - margin)
+  __device__ __forceinline__ void set_bound() {
+    const float margin = __fmaf_rn(fabsf(best), 9.5367431640625e-7f, 1.1e-3f);
+    k0 = __fmul_rn(__fsub_rn(margin, best), kLog2e);
   }
   __device__ __forceinline__ void take(float v, int i) {
     if (better(v, i, best, best_i)) {
       best = v;
       best_i = i;
-      set_lim();
+      set_bound();
     }
   }
-  // inv_t = 1 / T
-  __device__ __forceinline__ void token(float l, int i, uint32_t word, float t, float inv_t) {
-    const float x = __fmul_rn(l, inv_t);
-    const float rest = __fmul_rn(__fadd_rn(static_cast<float>(0xFFFFFFu - (word >> 8)), 0.5f), 5.9604644775390625e-8f);
-    const float a = ex2(__fmul_rn(__fsub_rn(__fadd_rn(x, __fmul_rn(fabsf(x), 4.76837158203125e-7f)), lim), kLog2e));
-    if (!(rest > a)) take(gumbel_score(l, word, t), i);
+  // The same with the exponential at hand: w = exp((l - top) / T), ratio from
+  // `ratio_to(top, c)` for the current bound.
+  __device__ __forceinline__ float ratio_to(float top, float c) const { return ex2(__fmaf_rn(top, c, k0)); }
+  __device__ __forceinline__ bool may_win(float w, float ratio, uint32_t word) const {
+    const float rest = __uint_as_float((~word >> 9) | 0x3F800000u);
+    return !(rest > __fadd_rn(__fmul_rn(w, ratio), 1.0000002384185791015625f));
+  }
+  // c = log2(e) / T
+  __device__ __forceinline__ void token(float l, int i, uint32_t word, float t, float c) {
+    const float a = ex2(__fmaf_rn(l, c, k0));
+    const float rest = __uint_as_float((~word >> 9) | 0x3F800000u);
+    if (!(rest > __fadd_rn(a, 1.0000002384185791015625f))) take(gumbel_score(l, word, t), i);
   }
   // over the warp; every lane ends with the winner
   __device__ __forceinline__ void warp_reduce() {
@@ -127,7 +153,7 @@ struct Race {
         best_i = oi;
       }
     }
-    set_lim();
+    set_bound();
   }
 };
 
@@ -147,17 +173,79 @@ __device__ __forceinline__ float4 load4(const float* row, int i0, int V) {
   return v;
 }
 
-// ---------------------------------------------------------------- pass 1
+// What one row's wide kernels share.
+struct __align__(16) WideState {
+  double z;              // the row's whole mass, relative to `top`
+  uint64_t clo, chi;     // the window: a range of comp, inclusive
+  float top;             // largest logit
+  float least;           // smallest value that min-p keeps
+  uint32_t above_n;      // tokens above the window
+  uint32_t in_n;         // tokens inside it; more than kList: no usable window
+  uint32_t arrived[2];   // CTAs done, per kernel
+  int n;                 // tokens listed
+  int pad_;
+};
+struct __align__(16) ChunkOut {
+  double mass;           // of the chunk's tokens above the window (and at least `least`)
+  float best;
+  int best_i;
+};
+
+// The workspace of R rows.
+struct Space {
+  RowParam* params;      // [R]
+  SegOut* segs;          // [R][nseg]
+  uint64_t* lists;       // [R][nseg][kSegCap]
+  WideState* wide;       // [R]
+  ChunkOut* chunks;      // [R][nchunk]
+  uint64_t* window;      // [R][kList]
+  uint32_t* count;       // [R][kCountBins] tokens
+  uint32_t* place;       // [R][kCountBins] sums of their places in the bin, in 32nds
+  int* wide_rows;        // [R]
+  int* n_wide;
+};
+inline __host__ size_t space_of(Space* sp, void* base, int R, int nseg, int nchunk) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += (bytes + 127) / 128 * 128;
+    return static_cast<char*>(base) + o;
+  };
+  const size_t r = R;
+  sp->n_wide = reinterpret_cast<int*>(take(sizeof(int)));
+  sp->wide_rows = reinterpret_cast<int*>(take(r * sizeof(int)));
+  sp->params = reinterpret_cast<RowParam*>(take(r * sizeof(RowParam)));
+  sp->wide = reinterpret_cast<WideState*>(take(r * sizeof(WideState)));
+  sp->segs = reinterpret_cast<SegOut*>(take(r * nseg * sizeof(SegOut)));
+  sp->lists = reinterpret_cast<uint64_t*>(take(r * nseg * kSegCap * sizeof(uint64_t)));
+  sp->chunks = reinterpret_cast<ChunkOut*>(take(r * nchunk * sizeof(ChunkOut)));
+  sp->window = reinterpret_cast<uint64_t*>(take(r * kList * sizeof(uint64_t)));
+  sp->count = reinterpret_cast<uint32_t*>(take(r * kCountBins * sizeof(uint32_t)));
+  sp->place = reinterpret_cast<uint32_t*>(take(r * kCountBins * sizeof(uint32_t)));
+  return off;
+}
+
+// ---------------------------------------------------------------- scan
+// first: the call's first scan launch.  The others depend on no earlier kernel
+// but through it, so they wait for their predecessor at their end: they run
+// next to it, and whatever waits for the last one waits for all.
 template <int N, bool VEC>
-__global__ void __launch_bounds__(kScanThreads)
+__global__ void __launch_bounds__(kScanThreads, 4)
     filter_scan_kernel(const __grid_constant__ RowParams<N> params, const float* __restrict__ logits, int V,
-                       long long ld, int nseg, int keep, SegOut* __restrict__ segs, uint64_t* __restrict__ lists) {
-  pdl_wait();
+                       long long ld, int nseg, int groups, bool first, Space sp, int r0) {
+  if (first) pdl_wait();
   pdl_trigger();
   const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seg = blockIdx.x * (kScanThreads / 32) + warp;
-  if (seg >= nseg) return;
-  const float* row = logits + r * ld;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    sp.params[r0 + r] = params.r[r];
+    if (first && r == 0) *sp.n_wide = 0;
+  }
+  if (seg >= nseg) {
+    if (!first) pdl_wait();
+    return;
+  }
+  const float* row = logits + (r0 + r) * ld;
   const int i0 = seg * kSeg + lane * 4;
   float v[8][4];
 #pragma unroll
@@ -201,39 +289,37 @@ __global__ void __launch_bounds__(kScanThreads)
     for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
     out.sum = sum;
     if (mode == ROW_FREE) {
-      const float inv_t = __fdiv_rn(1.f, p.temp);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const int i = i0 + q * 128;
         const uint4 w = philox_block(p.seed, p.step, static_cast<uint32_t>(i) / 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (i + e < V) race.token(v[q][e], i + e, word_of(w, e), p.temp, inv_t);
+          if (i + e < V) race.token(v[q][e], i + e, word_of(w, e), p.temp, c);
         if (q == 0) race.warp_reduce();  // a bound for the rest of the segment
       }
       race.warp_reduce();
     } else {
-      // lane maxima in descending order (bitonic, over the warp)
-      float s = lm;
-#pragma unroll
-      for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j > 0; j >>= 1) {
-          const float o = __shfl_xor_sync(0xffffffffu, s, j);
-          const bool up = ((lane & k) == 0) == ((lane & j) == 0);  // this lane keeps the larger
-          s = up ? fmaxf(s, o) : fminf(s, o);
-        }
-      // the lowest threshold whose list fits: the keep-th lane maximum, else a higher one, else none
+      // The smallest of the maxima of `groups` groups of lanes: at least
+      // `groups` logits reach it (about groups (ln(groups) + 0.58) of logits
+      // in no order).  Where the list would be too long (one segment in 500),
+      // half the groups, down to the maximum alone; if even that repeats too
+      // often, nothing is listed.
       out.thr = key_of(m) + 1;
-      uint64_t* list = lists + (static_cast<size_t>(r) * nseg + seg) * kSegCap;
-      for (int rank = keep - 1; rank >= 0; rank = rank > 3 ? 3 : rank > 0 ? 0 : -1) {
-        const uint32_t t = max(key_of(__shfl_sync(0xffffffffu, s, rank)), kKeyLowest);  // -inf is never listed
+      uint64_t* list = sp.lists + (static_cast<size_t>(r0 + r) * nseg + seg) * kSegCap;
+#pragma unroll 1
+      for (int g = groups; g > 0; g >>= 1) {
+        float low = lm;
+        for (int o = 1; o < 32 / g; o <<= 1) low = fmaxf(low, __shfl_xor_sync(0xffffffffu, low, o));
+        for (int o = 32 / g; o < 32; o <<= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+        const uint32_t t = max(key_of(low), kKeyLowest);  // -inf is never listed
         const float tv = value_of(t);
-        int n = 0;
+        uint32_t mine = 0;  // bit 4 q + e: v[q][e] is listed
 #pragma unroll
         for (int q = 0; q < 8; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) n += v[q][e] >= tv;
+          for (int e = 0; e < 4; ++e) mine |= v[q][e] >= tv ? 1u << (4 * q + e) : 0u;
+        const int n = __popc(mine);
         int before = n;  // inclusive prefix sum over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -243,11 +329,11 @@ __global__ void __launch_bounds__(kScanThreads)
         const int total = __shfl_sync(0xffffffffu, before, 31);
         if (total > kSegCap) continue;
         before -= n;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (v[q][e] >= tv) list[before++] = comp_of(v[q][e], i0 + q * 128 + e);
+        while (mine) {  // the few that are listed, read again from the cache (their registers have no run-time index)
+          const int k = __ffs(mine) - 1, i = i0 + (k >> 2) * 128 + (k & 3);
+          mine &= mine - 1;
+          list[before++] = comp_of(row[i], i);
+        }
         out.thr = t;
         out.count = total;
         break;
@@ -257,78 +343,32 @@ __global__ void __launch_bounds__(kScanThreads)
   out.best = race.best;
   out.best_i = race.best_i;
   if (out.thr == 0) out.thr = kKeyLowest;  // nothing to list
-  if (lane == 0) segs[static_cast<size_t>(r) * nseg + seg] = out;
+  if (lane == 0) sp.segs[static_cast<size_t>(r0 + r) * nseg + seg] = out;
+  if (!first) pdl_wait();
 }
 
-// ---------------------------------------------------------------- pass 2
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address, in the cluster's shared window, of CTA `rank`'s copy of p.
-__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ uint32_t peer_ld32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint64_t peer_ld64(uint32_t a) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void peer_st32(uint32_t a, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ void peer_st64(uint32_t a, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t peer_add32(uint32_t a, uint32_t v) {
-  uint32_t o;
-  asm volatile("atom.add.shared::cluster.u32 %0, [%1], %2;" : "=r"(o) : "r"(a), "r"(v) : "memory");
-  return o;
-}
-
-// Shared memory of a CTA.  The histogram and the sorted list are never in use
-// at the same time.
+// ---------------------------------------------------------------- shared by the deciding kernels
 struct SelShared {
   union {
     struct {
       uint32_t cnt[kBins], lo[kBins], hi[kBins];  // tokens; masses as 64-bit integers in two words
     } h;
+    uint32_t count[kCountBins];
     struct {
       uint64_t comp[kList];
       double pre[kList];  // masses up to and including each
     } l;
   };
   double redd[kSelThreads / 32];
+  uint64_t redu[kSelThreads / 32];
   float redf[kSelThreads / 32];
   int redi[kSelThreads / 32];
-  uint64_t redu[kSelThreads / 32];
-  int go;                    // the row has to be re-read
-  float top;                 // its largest logit
   int n;                     // list entries
+  int flag;
   uint64_t clo, chi;         // tokens of the undecided bin (comp range, inclusive)
   uint64_t above_mass;       // of the tokens above it
-  uint32_t above_cnt, in_cnt;
-  uint64_t last_comp;        // the top_k-th token, where top-p cuts within top-k
   uint64_t total_mass;
-  float r_best[16];          // per rank: the best of the tokens above the bin
-  int r_best_i[16];
-  uint64_t r_mass[16];
+  uint32_t above_n, in_n;
 };
 
 template <typename T, typename Op>
@@ -343,35 +383,123 @@ __device__ __forceinline__ T block_reduce(T v, T* red, Op op) {
   for (int w = 1; w < kSelThreads / 32; ++w) v = op(v, red[w]);
   return v;
 }
+__device__ __forceinline__ int block_sum(SelShared& sh, int v) {
+  return block_reduce(v, sh.redi, [](int a, int b) { return a + b; });
+}
+__device__ __forceinline__ int block_max(SelShared& sh, int v) {
+  return block_reduce(v, sh.redi, [](int a, int b) { return max(a, b); });
+}
+__device__ __forceinline__ double block_sum(SelShared& sh, double v) {
+  return block_reduce(v, sh.redd, [](double a, double b) { return a + b; });
+}
+// The best of the block, on every thread.
+__device__ __forceinline__ void block_best(SelShared& sh, Race& race) {
+  race.warp_reduce();
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    sh.redf[threadIdx.x >> 5] = race.best;
+    sh.redi[threadIdx.x >> 5] = race.best_i;
+  }
+  __syncthreads();
+  for (int w = 0; w < kSelThreads / 32; ++w)
+    if (better(sh.redf[w], sh.redi[w], race.best, race.best_i)) {
+      race.best = sh.redf[w];
+      race.best_i = sh.redi[w];
+    }
+}
 
-// Sorts comp[0, n) in descending order (n <= kList, the values all different).
+// Bitonic sort, descending, of N = E * kSelThreads values, E consecutive ones
+// per thread: distances below E inside the thread, below 32 E by shuffles,
+// the rest through shared memory.
+template <int E>
+__device__ __forceinline__ void bitonic_desc(uint64_t (&v)[E], uint64_t* buf) {
+  constexpr int N = E * kSelThreads;
+  const int i0 = threadIdx.x * E;
+#pragma unroll
+  for (int k = 2; k <= N; k <<= 1) {
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      if (j >= 32 * E) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) buf[i0 + e] = v[e];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int i = i0 + e;
+          const uint64_t o = buf[i ^ j];
+          const bool larger = ((i & k) == 0) == ((i & j) == 0);
+          v[e] = (o > v[e]) == larger ? o : v[e];
+        }
+      } else if (j >= E) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int i = i0 + e;
+          const uint64_t o = __shfl_xor_sync(0xffffffffu, v[e], j / E);
+          const bool larger = ((i & k) == 0) == ((i & j) == 0);
+          v[e] = (o > v[e]) == larger ? o : v[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((e & j) == 0) {
+            const bool down = ((i0 + e) & k) == 0;
+            const uint64_t x = v[e], y = v[e ^ j];
+            const bool swap = (y > x) == down;
+            v[e] = swap ? y : x;
+            v[e ^ j] = swap ? x : y;
+          }
+      }
+    }
+  }
+}
+template <int E>
+__device__ void sort_n(uint64_t* comp, int n) {
+  uint64_t v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = threadIdx.x * E + e < n ? comp[threadIdx.x * E + e] : 0;
+  bitonic_desc<E>(v, comp);
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; ++e) comp[threadIdx.x * E + e] = v[e];
+  __syncthreads();
+}
+// Sorts comp[0, n) in descending order (n <= kList, the values all different
+// and above 0); the entries up to the next size are zeroed.
 __device__ void sort_desc(uint64_t* comp, int n) {
-  if (n <= kSelThreads) {  // by rank: each thread counts the values above its own
+  static_assert(kList == 8 * kSelThreads, "sizes below");
+  if (n <= 32) {  // one warp, by shuffles
+    if (threadIdx.x < 32) {
+      uint64_t x = static_cast<int>(threadIdx.x) < n ? comp[threadIdx.x] : 0;
+#pragma unroll
+      for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1) {
+          const uint64_t o = __shfl_xor_sync(0xffffffffu, x, j);
+          const bool larger = ((threadIdx.x & k) == 0) == ((threadIdx.x & j) == 0);
+          x = (o > x) == larger ? o : x;
+        }
+      comp[threadIdx.x] = x;
+    }
+    __syncthreads();
+  } else if (n <= kSelThreads / 2) {  // by rank: each thread counts the values above its own
     const int i = threadIdx.x;
     const uint64_t mine = i < n ? comp[i] : 0;
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) rank += comp[j] > mine;
     __syncthreads();
     if (i < n) comp[rank] = mine;
     __syncthreads();
-    return;
+  } else if (n <= kSelThreads) {
+    sort_n<1>(comp, n);
+  } else if (n <= 2 * kSelThreads) {
+    sort_n<2>(comp, n);
+  } else if (n <= 4 * kSelThreads) {
+    sort_n<4>(comp, n);
+  } else {
+    sort_n<8>(comp, n);
   }
-  int p = 2 * kSelThreads;
-  while (p < n) p <<= 1;
-  for (int i = n + threadIdx.x; i < p; i += kSelThreads) comp[i] = 0;
-  __syncthreads();
-  for (int k = 2; k <= p; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int t = threadIdx.x; t < p / 2; t += kSelThreads) {
-        const int a = 2 * t - (t & (j - 1)), b = a + j;
-        const uint64_t x = comp[a], y = comp[b];
-        if ((x < y) == ((a & k) == 0)) {
-          comp[a] = y;
-          comp[b] = x;
-        }
-      }
-      __syncthreads();
-    }
 }
 
 // pre[j] = base + weights of comp[0 .. j], summed in that order.
@@ -402,11 +530,30 @@ __device__ void prefix_mass(SelShared& sh, int n, float top, float t, double bas
 __device__ __forceinline__ bool min_p_keeps(float l, float top, float t, float log_min_p) {
   return l == top || __fdiv_rn(__fsub_rn(l, top), t) >= log_min_p;
 }
+// The smallest value that min-p keeps, by bisection over the keys.
+__device__ float min_p_least(const RowParam& p, float top) {
+  if (!(p.log_min_p > -INFINITY)) return value_of(kKeyLowest);
+  uint32_t lo = kKeyLowest, hi = key_of(top);
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (min_p_keeps(value_of(mid), top, p.temp, p.log_min_p)) hi = mid;
+    else lo = mid + 1;
+  }
+  return value_of(lo);
+}
+
+struct Out {
+  const float* logits;
+  long long ld;
+  int V, nseg, nchunk;
+  int* tokens;
+  float* logprobs;  // or null
+};
 
 // The choice among the first `kept` of the sorted list and `race` (the best
-// of tokens outside it); mass: that of every kept token.
-__device__ void choose(SelShared& sh, const RowParam& p, int kept, Race race, double mass, float top, const float* row,
-                       int* token_out, float* logprob_out) {
+// of tokens outside it); mass: that of every kept token, relative to `top`.
+__device__ void choose(SelShared& sh, const Out& o, int r, const RowParam& p, int kept, Race race, double mass,
+                       float top, bool point) {
   for (int j = threadIdx.x; j < kept; j += kSelThreads) {
     const uint64_t cp = sh.l.comp[j];
     const int i = index_of(cp);
@@ -417,579 +564,714 @@ __device__ void choose(SelShared& sh, const RowParam& p, int kept, Race race, do
       race.best_i = i;
     }
   }
-  race.warp_reduce();
-  const int warp = threadIdx.x >> 5;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    sh.redf[warp] = race.best;
-    sh.redi[warp] = race.best_i;
-  }
-  __syncthreads();
+  block_best(sh, race);
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kSelThreads / 32; ++w)
-      if (better(sh.redf[w], sh.redi[w], race.best, race.best_i)) {
-        race.best = sh.redf[w];
-        race.best_i = sh.redi[w];
-      }
     const int tok = race.best_i == INT_MAX ? 0 : race.best_i;
-    *token_out = tok;
-    if (logprob_out) {
-      const float l = row[tok];
+    o.tokens[r] = tok;
+    if (o.logprobs) {
+      const float l = o.logits[r * o.ld + tok];
       const float d = l == top ? 0.f : __fdiv_rn(__fsub_rn(l, top), p.temp);
-      *logprob_out = __fsub_rn(d, log1pf(static_cast<float>(mass - 1.0)));
+      o.logprobs[r] = point ? 0.f : __fsub_rn(d, log1pf(static_cast<float>(mass - 1.0)));
     }
   }
 }
 
-struct SelectArgs {
-  const float* logits;
-  long long ld;
-  int V, nseg;
-  const SegOut* segs;
-  const uint64_t* lists;
-  int* tokens;
-  float* logprobs;  // or null
-};
-
-// The cluster's re-read of a row: f(four logits, their index / 4) over this
-// CTA's part.
-template <bool VEC, typename F>
-__device__ __forceinline__ void for_slice(const float* row, int V, uint32_t rank, uint32_t size, F f) {
-  const int quads = (V + 3) / 4, per = (quads + size - 1) / size;
-  const int q0 = rank * per, q1 = min(quads, q0 + per);
-  for (int q = q0 + threadIdx.x; q < q1; q += 4 * kSelThreads) {
-    float4 x[4];
+// Quads [q0, q1) of a row: f(four logits, their index / 4), every lane of a
+// warp taking part in each call (NaN past the end); end() after every kQuads.
+constexpr int kQuads = 4;
+template <bool VEC, typename F, typename E>
+__device__ __forceinline__ void for_quads(const float* row, int V, int q0, int q1, F f, E end) {
+  for (int qb = q0; qb < q1; qb += kQuads * kSelThreads) {
+    float4 x[kQuads];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (q + u * kSelThreads < q1) x[u] = load4<VEC>(row, (q + u * kSelThreads) * 4, V);
+    for (int u = 0; u < kQuads; ++u) {
+      const int q = qb + u * kSelThreads + threadIdx.x;
+      x[u] = q < q1 ? load4<VEC>(row, q * 4, V) : make_float4(NAN, NAN, NAN, NAN);
+    }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (q + u * kSelThreads < q1) f(x[u], q + u * kSelThreads);
+    for (int u = 0; u < kQuads; ++u) f(x[u], qb + u * kSelThreads + static_cast<int>(threadIdx.x));
+    end();
   }
 }
 
-// Bin of a token: by value below `top` at first (the last bin takes
-// everything further down), then by its place in [clo, chi].
-struct Binner {
-  bool first;
-  float top, scale;    // first: bins per unit of (top - l)
-  uint64_t clo, chi;
-  int shift;
-  __device__ __forceinline__ int operator()(float l, uint64_t comp) const {
-    if (first) {
-      const float d = l == top ? 0.f : __fmul_rn(__fsub_rn(top, l), scale);
-      return d < static_cast<float>(kBins - 1) ? static_cast<int>(d) : kBins - 1;
+// Tokens of quads [q0, q1): those of [clo, chi] go to `list` (its first kList
+// places, counted in *n), and over those above chi of value at least `least`
+// the mass is summed and, with SCORE, the race run.  mass: this thread's.
+template <bool VEC, bool SCORE>
+__device__ __forceinline__ void collect_quads(const float* row, int V, int q0, int q1, const RowParam& p, float top,
+                                              float least, uint64_t clo, uint64_t chi, uint64_t* list, int* n,
+                                              Race& race, float& mass) {
+  const float c = __fdiv_rn(kLog2e, p.temp);
+  const float v_lo = value_of(static_cast<uint32_t>(clo >> 32)), v_hi = value_of(static_cast<uint32_t>(chi >> 32));
+  float ratio = race.ratio_to(top, c);
+  mass = 0.f;
+  int turn = 0;
+  for_quads<VEC>(row, V, q0, q1, [&](const float4& x, int q) {
+    const float v[4] = {x.x, x.y, x.z, x.w};
+    float w[4];
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      bool above = v[e] > v_hi;
+      if (!above && v[e] >= v_lo) {  // of the window's values, or just above chi within one value
+        const uint64_t cp = comp_of(v[e], q * 4 + e);
+        above = cp > chi;
+        if (!above && cp >= clo) {
+          const int at = atomicAdd(n, 1);
+          if (at < kList) list[at] = cp;
+        }
+      }
+      above = above && v[e] >= least;
+      w[e] = above ? (v[e] == top ? 1.f : ex2(__fmul_rn(__fsub_rn(v[e], top), c))) : -1.f;
+      any |= above;
+      mass = __fadd_rn(mass, fmaxf(w[e], 0.f));
     }
-    return static_cast<int>((chi - comp) >> shift);
-  }
-};
+    if (SCORE && any) {
+      const uint4 ws = philox_block(p.seed, p.step, static_cast<uint32_t>(q));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (w[e] >= 0.f && race.may_win(w[e], ratio, word_of(ws, e))) {
+          race.take(gumbel_score(v[e], word_of(ws, e), p.temp), q * 4 + e);
+          ratio = race.ratio_to(top, c);
+        }
+    }
+  }, [&] {
+    if (SCORE && (turn & (turn + 1)) == 0) {  // a bound that the warp shares, after 1, 2, 4, ... turns
+      race.warp_reduce();
+      ratio = race.ratio_to(top, c);
+    }
+    ++turn;
+  });
+}
 
-// One histogram over the tokens of [clo, chi] (and, on the first pass, the
-// universe comp >= ulo), merged over the cluster; then the bin where the
-// criterion cuts.  by_count: the bin of the target-th token, else the bin in
-// which the mass before a token reaches `share` of the total.  Narrows
-// sh.clo / chi and adds to above_mass / above_cnt on every rank.
+// ---------------------------------------------------------------- the exact path
+// One histogram over the tokens of [clo, chi] at or above ulo, and the bin
+// where the criterion cuts: by_count, that of the top_k-th token; else the one
+// in which the mass before a token reaches top_p of the total.  The first pass
+// bins by value below `top`, the later ones by the place in [clo, chi].
+// Narrows sh.clo / chi, adds to above_mass / above_n, sets in_n.
 template <bool VEC>
-__device__ void histogram_cut(SelShared& sh, const float* row, int V, const RowParam& p, bool first, uint64_t ulo,
-                              bool by_count, int target, float share) {
-  const uint32_t rank = cluster_rank(), size = cluster_size();
-  const float c = __fdiv_rn(kLog2e, p.temp), top = sh.top;
-  Binner bin;
-  bin.first = first;
-  bin.top = top;
-  bin.scale = __fdiv_rn(static_cast<float>(kBins) / 24.f, p.temp);  // 24 nats over the bins
-  bin.clo = sh.clo;
-  bin.chi = sh.chi;
-  bin.shift = max(0, 64 - __clzll(static_cast<long long>(sh.chi - sh.clo)) - 11);
-  const uint64_t clo = max(sh.clo, ulo), chi = sh.chi;
+__device__ void histogram_cut(SelShared& sh, const float* row, int V, const RowParam& p, float top, bool first,
+                              uint64_t ulo, bool by_count) {
+  const float c = __fdiv_rn(kLog2e, p.temp), scale = __fdiv_rn(static_cast<float>(kBins) / kBinNats, p.temp);
+  const uint64_t lo0 = sh.clo, hi0 = sh.chi, clo = max(lo0, ulo);
+  const int shift = max(0, 64 - __clzll(static_cast<long long>(hi0 - lo0)) - 11);
+  auto by_value = [&](float l) {
+    const float d = l == top ? 0.f : __fmul_rn(__fsub_rn(top, l), scale);
+    return d < static_cast<float>(kBins - 1) ? static_cast<int>(d) : kBins - 1;
+  };
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.h.cnt[i] = sh.h.lo[i] = sh.h.hi[i] = 0;
   __syncthreads();
-  for_slice<VEC>(row, V, rank, size, [&](const float4& x, int q) {
+  for_quads<VEC>(row, V, 0, (V + 3) / 4, [&](const float4& x, int q) {
     const float v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint64_t cp = comp_of(v[e], q * 4 + e);
-      if (cp < clo || cp > chi) continue;
-      const int b = bin(v[e], cp);
+      if (cp < clo || cp > hi0) continue;
+      const int b = first ? by_value(v[e]) : static_cast<int>((hi0 - cp) >> shift);
       atomicAdd(&sh.h.cnt[b], 1u);
       const uint64_t w = static_cast<uint64_t>(__fmul_rn(weight(v[e], top, c), kMassScale));
-      const uint32_t wl = static_cast<uint32_t>(w);
       if (w) {
-        const uint32_t old = atomicAdd(&sh.h.lo[b], wl);
+        const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&sh.h.lo[b], wl);
         const uint32_t up = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
         if (up) atomicAdd(&sh.h.hi[b], up);
       }
     }
-  });
+  }, [] {});
   __syncthreads();
-  cluster_sync();
-  // rank r sums bins r * per ... over all ranks into its own copy, for rank 0 to read
-  const int per = kBins / size;
-  for (int i = threadIdx.x; i < per; i += kSelThreads) {
-    const int b = rank * per + i;
-    uint32_t n = 0;
-    uint64_t m = 0;
-    for (uint32_t k = 0; k < size; ++k) {
-      n += peer_ld32(peer(&sh.h.cnt[b], k));
-      m += peer_ld32(peer(&sh.h.lo[b], k)) + (static_cast<uint64_t>(peer_ld32(peer(&sh.h.hi[b], k))) << 32);
-    }
-    // bin b of another rank's copy is read by this rank alone: overwrite rank 0's
-    peer_st32(peer(&sh.h.cnt[b], 0), n);
-    peer_st32(peer(&sh.h.lo[b], 0), static_cast<uint32_t>(m));
-    peer_st32(peer(&sh.h.hi[b], 0), static_cast<uint32_t>(m >> 32));
+  constexpr int PT = kBins / kSelThreads;
+  const int b0 = threadIdx.x * PT, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto mass_of = [&](int b) { return sh.h.lo[b] + (static_cast<uint64_t>(sh.h.hi[b]) << 32); };
+  uint32_t n = 0;
+  uint64_t m = 0;
+  for (int k = 0; k < PT; ++k) {
+    n += sh.h.cnt[b0 + k];
+    m += mass_of(b0 + k);
   }
-  cluster_sync();
-  if (rank == 0) {
-    // every thread: eight bins; prefix over the threads; the thread that holds the cut says so
-    constexpr int PT = kBins / kSelThreads;
-    const int b0 = threadIdx.x * PT;
-    uint32_t n = 0;
-    uint64_t m = 0;
-    for (int k = 0; k < PT; ++k) {
-      n += sh.h.cnt[b0 + k];
-      m += sh.h.lo[b0 + k] + (static_cast<uint64_t>(sh.h.hi[b0 + k]) << 32);
-    }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t sn = n;
-    uint64_t sm = m;
+  uint32_t sn = n;
+  uint64_t sm = m;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t xn = __shfl_up_sync(0xffffffffu, sn, o);
-      const uint64_t xm = __shfl_up_sync(0xffffffffu, sm, o);
-      if (lane >= o) {
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t xn = __shfl_up_sync(0xffffffffu, sn, o);
+    const uint64_t xm = __shfl_up_sync(0xffffffffu, sm, o);
+    if (lane >= o) {
+      sn += xn;
+      sm += xm;
+    }
+  }
+  if (lane == 31) {
+    sh.redi[warp] = static_cast<int>(sn);
+    sh.redu[warp] = sm;
+  }
+  __syncthreads();
+  uint32_t an = sh.above_n + sn - n;
+  uint64_t am = sh.above_mass + sm - m, total = sh.above_mass;
+  for (int w = 0; w < kSelThreads / 32; ++w) {
+    if (w < warp) {
+      an += sh.redi[w];
+      am += sh.redu[w];
+    }
+    total += sh.redu[w];
+  }
+  if (!first) total = sh.total_mass;  // the whole universe's, from the first pass
+  const double want = static_cast<double>(p.top_p) * static_cast<double>(total);
+  __syncthreads();
+  // the last non-empty bin before which the criterion still holds
+  int cut = -1;
+  uint32_t cut_n = 0, cut_in = 0;
+  uint64_t cut_m = 0;
+  for (int k = 0; k < PT; ++k) {
+    const uint32_t bn = sh.h.cnt[b0 + k];
+    if (bn && (by_count ? an < static_cast<uint32_t>(p.top_k) : an == 0 || static_cast<double>(am) < want)) {
+      cut = b0 + k;
+      cut_n = an;
+      cut_m = am;
+      cut_in = bn;
+    }
+    an += bn;
+    am += mass_of(b0 + k);
+  }
+  const int last = block_max(sh, cut);
+  if (threadIdx.x == 0) {
+    sh.total_mass = total;
+    if (last < 0) sh.in_n = 0;  // an empty universe
+  }
+  if (cut == last && cut >= 0) {
+    sh.above_n = cut_n;
+    sh.above_mass = cut_m;
+    sh.in_n = cut_in;
+    if (first) {  // the bin's smallest and largest key, by bisection (the bin number falls as the key grows)
+      uint32_t a = kKeyLowest, b = key_of(top);
+      while (a < b) {
+        const uint32_t mid = a + (b - a) / 2;
+        if (by_value(value_of(mid)) <= cut) b = mid;
+        else a = mid + 1;
+      }
+      sh.clo = max(static_cast<uint64_t>(a) << 32, ulo);
+      b = key_of(top);
+      while (a < b) {
+        const uint32_t mid = a + (b - a + 1) / 2;
+        if (by_value(value_of(mid)) >= cut) a = mid;
+        else b = mid - 1;
+      }
+      sh.chi = (static_cast<uint64_t>(a) << 32) | 0xFFFFFFFFu;
+    } else {
+      const uint64_t hi = hi0 - (static_cast<uint64_t>(cut) << shift), span = (1ull << shift) - 1;
+      sh.chi = hi;
+      sh.clo = max(max(lo0, hi > span ? hi - span : 0), ulo);
+    }
+  }
+  __syncthreads();
+}
+
+// A row by exact histograms, one CTA.
+template <bool VEC>
+__device__ __noinline__ void exact_row(SelShared& sh, const Out& o, int r, const RowParam& p, float top) {
+  const float* row = o.logits + r * o.ld;
+  const int V = o.V, quads = (V + 3) / 4;
+  const bool has_k = p.top_k > 0, has_p = p.top_p < 1.f;
+  const float least = min_p_least(p, top);
+  uint64_t ulo = static_cast<uint64_t>(kKeyLowest) << 32;  // the universe: comp >= ulo
+  auto narrow = [&](bool by_count) {  // each pass leaves at most 1 / 2048 of the range: six at most
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      sh.clo = ulo;
+      sh.chi = ~0ull;
+      sh.above_mass = 0;
+      sh.above_n = 0;
+      sh.in_n = 0;
+    }
+    __syncthreads();
+    bool first = true;
+    do {
+      histogram_cut<VEC>(sh, row, V, p, top, first, ulo, by_count);
+      first = false;
+    } while (sh.in_n > kList);
+  };
+  Race race;
+  auto collect = [&](float from, bool score) {  // the window's tokens, sorted and summed, and the mass above
+    __syncthreads();
+    if (threadIdx.x == 0) sh.n = 0;
+    __syncthreads();
+    float m;
+    if (score) collect_quads<VEC, true>(row, V, 0, quads, p, top, from, sh.clo, sh.chi, sh.l.comp, &sh.n, race, m);
+    else collect_quads<VEC, false>(row, V, 0, quads, p, top, from, sh.clo, sh.chi, sh.l.comp, &sh.n, race, m);
+    const double above = block_sum(sh, static_cast<double>(m));
+    const int n = min(sh.n, kList);
+    sort_desc(sh.l.comp, n);
+    prefix_mass(sh, n, top, p.temp, above);
+    return above;
+  };
+  double z = 0;
+  if (has_k) {
+    narrow(true);
+    if (has_p) {  // the top_k-th token and the mass down to it, then top-p within them
+      const double above = collect(value_of(kKeyLowest), false);
+      const int n = min(sh.n, kList), last = min(n, static_cast<int>(p.top_k - sh.above_n)) - 1;
+      if (last >= 0) {
+        ulo = sh.l.comp[last];
+        z = sh.l.pre[last];
+      } else {
+        z = above;
+      }
+    }
+  }
+  if (has_p) {
+    narrow(false);
+    if (!has_k) z = static_cast<double>(sh.total_mass) / kMassScale;
+  } else if (!has_k) {  // min-p alone: every token is "above", nothing undecided
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      sh.clo = ulo;
+      sh.chi = ulo - 1;
+      sh.above_n = 0;
+    }
+    __syncthreads();
+  }
+  const double base = collect(least, true), want = static_cast<double>(p.top_p) * z;
+  const int n = min(sh.n, kList);
+  int kept = 0;
+  for (int j = threadIdx.x; j < n; j += kSelThreads) {
+    const bool in_k = has_p || !has_k || sh.above_n + j < static_cast<uint32_t>(p.top_k);
+    const bool in_p = !has_p || sh.above_n + j == 0 || (j == 0 ? base : sh.l.pre[j - 1]) < want;
+    kept += in_k && in_p && value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32)) >= least;
+  }
+  kept = block_sum(sh, kept);
+  choose(sh, o, r, p, kept, race, kept > 0 ? sh.l.pre[kept - 1] : base, top, false);
+}
+
+// ---------------------------------------------------------------- select
+// wide_next: the count and collect kernels follow, and take rows that the
+// lists do not decide.
+template <bool VEC>
+__global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space sp, bool wide_next) {
+  __shared__ SelShared sh;
+  extern __shared__ float seg_max[];                     // [nseg]
+  int* seg_n = reinterpret_cast<int*>(seg_max + o.nseg);  // [nseg]
+  pdl_wait();
+  pdl_trigger();
+  const int r = blockIdx.x, lane = threadIdx.x & 31;
+  const RowParam p = sp.params[r];
+  const int mode = row_mode(p);
+  const SegOut* segs = sp.segs + static_cast<size_t>(r) * o.nseg;
+  float top = -INFINITY;
+  uint32_t floor = kKeyLowest;  // every logit from here on is listed
+  Race race;
+  for (int i = threadIdx.x; i < o.nseg; i += kSelThreads) {
+    const SegOut s = segs[i];
+    seg_max[i] = s.max;
+    seg_n[i] = s.count;
+    top = fmaxf(top, s.max);
+    floor = max(floor, s.thr);
+    if (better(s.best, s.best_i, race.best, race.best_i)) {
+      race.best = s.best;
+      race.best_i = s.best_i;
+    }
+  }
+  top = block_reduce(top, sh.redf, [](float x, float y) { return fmaxf(x, y); });
+  double z = 0;
+  if (mode != ROW_GREEDY) {
+    const float c = __fdiv_rn(kLog2e, p.temp);
+    for (int i = threadIdx.x; i < o.nseg; i += kSelThreads)
+      z += static_cast<double>(segs[i].sum) * static_cast<double>(weight(seg_max[i], top, c));
+    z = block_sum(sh, z);
+  }
+  if (mode != ROW_FILTER || top == -INFINITY) {  // (without any finite logit the filters do not matter)
+    choose(sh, o, r, p, 0, race, z, top, mode != ROW_FREE || top == -INFINITY);
+    return;
+  }
+  floor = static_cast<uint32_t>(block_reduce(floor, reinterpret_cast<uint32_t*>(sh.redi),
+                                             [](uint32_t x, uint32_t y) { return max(x, y); }));
+  const bool all = floor <= kKeyLowest;  // the lists hold every finite logit
+  // First as many candidates as there are large segment maxima (at least the
+  // first `want` tokens are among those at or above the want-th largest), then,
+  // if that does not decide the row, every listed one.
+  for (int level = 0; level < 2; ++level) {
+    uint32_t from = floor;
+    if (level == 0) {
+      const int want = min(p.top_k > 0 ? min(p.top_k, 64) : 48, o.nseg);
+      uint32_t mine = 0;  // the want-th largest segment maximum's key
+      for (int i = threadIdx.x; i < o.nseg; i += kSelThreads) {
+        int above = 0;
+        const float m = seg_max[i];
+#pragma unroll 8
+        for (int j = 0; j < o.nseg; ++j) above += seg_max[j] > m || (seg_max[j] == m && j < i);
+        if (above == want - 1) mine = key_of(m);
+      }
+      from = max(block_reduce(mine, reinterpret_cast<uint32_t*>(sh.redi),
+                              [](uint32_t x, uint32_t y) { return max(x, y); }),
+                 floor);
+      if (from == floor) continue;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh.n = 0;
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < o.nseg; i += kSelThreads / 32) {
+      if (key_of(seg_max[i]) < from) continue;
+      const uint64_t* list = sp.lists + (static_cast<size_t>(r) * o.nseg + i) * kSegCap;
+      for (int k = lane; k < seg_n[i]; k += 32) {
+        const uint64_t cp = list[k];
+        if (static_cast<uint32_t>(cp >> 32) >= from) {
+          const int at = atomicAdd(&sh.n, 1);
+          if (at < kList) sh.l.comp[at] = cp;
+        }
+      }
+    }
+    __syncthreads();
+    const int n = sh.n;
+    if (n > kList || n == 0) continue;  // too many candidates, or none listed (ties)
+    const bool complete = all && from == floor;
+    sort_desc(sh.l.comp, n);
+    prefix_mass(sh, n, top, p.temp, 0.0);
+    const int lim = p.top_k > 0 ? min(p.top_k, n) : n;
+    const bool k_known = complete || p.top_k <= n;  // with top_k on: the list holds all of its tokens
+    const bool has_p = p.top_p < 1.f;
+    if (p.top_k > 0 && has_p && !k_known) continue;
+    const double share = static_cast<double>(p.top_p) * (p.top_k > 0 ? sh.l.pre[lim - 1] : z);
+    int kept = 0;
+    for (int j = threadIdx.x; j < lim; j += kSelThreads) {
+      const float l = value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32));
+      kept += (!has_p || j == 0 || sh.l.pre[j - 1] < share) && min_p_keeps(l, top, p.temp, p.log_min_p);
+    }
+    kept = block_sum(sh, kept);
+    const bool decided = complete || kept < n || (p.top_k > 0 && p.top_k <= n) || (has_p && sh.l.pre[lim - 1] >= share);
+    if (!decided) continue;
+    choose(sh, o, r, p, kept, Race(), kept > 0 ? sh.l.pre[kept - 1] : 1.0, top, false);
+    return;
+  }
+  if (!wide_next || (p.top_k > 0 && p.top_p < 1.f)) {
+    exact_row<VEC>(sh, o, r, p, top);
+    return;
+  }
+  for (int i = threadIdx.x; i < kCountBins; i += kSelThreads) {
+    sp.count[static_cast<size_t>(r) * kCountBins + i] = 0;
+    sp.place[static_cast<size_t>(r) * kCountBins + i] = 0;
+  }
+  if (threadIdx.x == 0) {
+    WideState w{};
+    w.z = z;
+    w.top = top;
+    w.least = min_p_least(p, top);
+    w.clo = static_cast<uint64_t>(kKeyLowest) << 32;  // min-p alone: an empty window below every token
+    w.chi = w.clo - 1;
+    sp.wide[r] = w;
+    sp.wide_rows[atomicAdd(sp.n_wide, 1)] = r;  // in any order: rows do not depend on one another
+  }
+}
+
+// ---------------------------------------------------------------- wide rows
+// Whether this CTA is the last of a row's `total` to arrive; what the others
+// wrote before arriving is then visible to it.
+__device__ __forceinline__ bool last_arrival(uint32_t* arrived, int total, int* flag) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) *flag = atomicAdd(arrived, 1u) == static_cast<uint32_t>(total) - 1;
+  __syncthreads();
+  const bool last = *flag != 0;
+  if (last) __threadfence();
+  return last;
+}
+
+// A token's place in its row's value bins: bin << 5 | 32nd of the bin.
+__device__ __forceinline__ int value_place(float l, float top, float scale32) {
+  const float d = l == top ? 0.f : __fmul_rn(__fsub_rn(top, l), scale32);
+  constexpr int kLast = (kCountBins - 1) * 32;
+  return d < static_cast<float>(kLast) ? static_cast<int>(d) : kLast;
+}
+
+// The estimate of a bin's mass from its tokens' mean place is off by the
+// rounding of the places (half a 32nd of a bin's 0.6 %, at most 9e-5 of the
+// bin's mass and less for values in no order) and by the spread inside a bin
+// (2e-6): the window takes kSlack of the whole mass to either side, and
+// `collect` checks the sums themselves.
+constexpr double kSlack = 1e-4;
+
+template <bool VEC>
+__global__ void __launch_bounds__(kSelThreads) filter_count_kernel(Out o, Space sp) {
+  __shared__ SelShared sh;
+  pdl_wait();
+  pdl_trigger();
+  const int items = *reinterpret_cast<volatile int*>(sp.n_wide) * o.nchunk;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int r = sp.wide_rows[item / o.nchunk], chunk = item % o.nchunk;
+    const RowParam p = sp.params[r];
+    const bool by_count = p.top_k > 0;
+    if (!by_count && p.top_p >= 1.f) continue;  // min-p alone needs no window
+    WideState& st = sp.wide[r];
+    const float top = st.top, scale32 = __fdiv_rn(32.f * kCountBins / kBinNats, p.temp);
+    const float low = value_of(kKeyLowest);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kCountBins; i += kSelThreads) sh.count[i] = 0;
+    __syncthreads();
+    // tokens in the upper 14 bits, the sum of their 32nds in the lower 18: no
+    // bin of a chunk's 8192 tokens carries over (8192 * 31 < 2^18, and 8192 < 2^14)
+    static_assert(kChunk * 31 < (1 << 18) && kChunk < (1 << 14), "packed counters");
+    const int quads = (o.V + 3) / 4, q0 = chunk * (kChunk / 4);
+    for_quads<VEC>(o.logits + r * o.ld, o.V, q0, min(quads, q0 + kChunk / 4), [&](const float4& x, int) {
+      const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (v[e] >= low) {
+          const int at = value_place(v[e], top, scale32);
+          atomicAdd(&sh.count[at >> 5], (1u << 18) + (at & 31));
+        }
+    }, [] {});
+    __syncthreads();
+    uint32_t* count = sp.count + static_cast<size_t>(r) * kCountBins;
+    uint32_t* place = sp.place + static_cast<size_t>(r) * kCountBins;
+    for (int i = threadIdx.x; i < kCountBins; i += kSelThreads)
+      if (const uint32_t h = sh.count[i]) {
+        atomicAdd(&count[i], h >> 18);
+        if (h & 0x3FFFF) atomicAdd(&place[i], h & 0x3FFFF);
+      }
+    if (!last_arrival(&st.arrived[0], o.nchunk, &sh.flag)) continue;
+    // ---- the window
+    constexpr int PT = kCountBins / kSelThreads;
+    const int b0 = threadIdx.x * PT;
+    const float step = kBinNats / kCountBins;  // nats of a bin
+    uint32_t bn[PT];
+    float bm[PT];
+    uint32_t n = 0;
+    double m = 0;
+#pragma unroll
+    for (int k = 0; k < PT; ++k) {
+      bn[k] = __ldcg(&count[b0 + k]);
+      const float mean = __fdiv_rn(static_cast<float>(__ldcg(&place[b0 + k])), 32.f * fmaxf(static_cast<float>(bn[k]), 1.f));
+      bm[k] = __fmul_rn(static_cast<float>(bn[k]),
+                        ex2(__fmul_rn(-step * kLog2e, __fadd_rn(static_cast<float>(b0 + k), __fadd_rn(mean, 1.f / 64)))));
+      n += bn[k];
+      m += bm[k];
+    }
+    uint32_t sn = n;
+    double sm = m;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const uint32_t xn = __shfl_up_sync(0xffffffffu, sn, s);
+      const double xm = __shfl_up_sync(0xffffffffu, sm, s);
+      if (lane >= s) {
         sn += xn;
         sm += xm;
       }
     }
     if (lane == 31) {
       sh.redi[warp] = static_cast<int>(sn);
-      sh.redu[warp] = sm;
+      sh.redd[warp] = sm;
     }
     __syncthreads();
-    uint32_t an = sh.above_cnt + sn - n;
-    uint64_t am = sh.above_mass + sm - m, total = sh.above_mass;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < warp) {
-        an += sh.redi[w];
-        am += sh.redu[w];
-      }
-      total += sh.redu[w];
+    uint32_t an = sn - n;
+    double am = sm - m;
+    for (int w = 0; w < warp; ++w) {
+      an += sh.redi[w];
+      am += sh.redd[w];
     }
-    if (!first) total = sh.total_mass;  // the whole universe's, from the first pass
-    const double want = static_cast<double>(share) * static_cast<double>(total);
-    __syncthreads();
-    if (threadIdx.x == 0) sh.total_mass = total;
-    // the last non-empty bin before which the criterion still holds
-    int cut = -1;
-    uint32_t cut_n = 0, cut_in = 0;
-    uint64_t cut_m = 0;
+    const double want = static_cast<double>(p.top_p) * st.z, slack = kSlack * st.z;
+    int lo = kCountBins, hi = -1;  // the window's first and last bin
+    uint32_t lo_n = 0, hi_n = 0;   // tokens above the first, tokens up to the last
+#pragma unroll
     for (int k = 0; k < PT; ++k) {
-      const uint32_t bn = sh.h.cnt[b0 + k];
-      if (bn) {
-        const bool holds = by_count ? an < static_cast<uint32_t>(target)
-                                    : an == 0 || static_cast<double>(am) < want;
+      if (bn[k]) {
+        const bool enters = by_count ? an + bn[k] >= static_cast<uint32_t>(p.top_k) : am + bm[k] > want - slack;
+        const bool holds = by_count ? an < static_cast<uint32_t>(p.top_k) : an == 0 || am < want + slack;
+        if (enters && lo == kCountBins) {
+          lo = b0 + k;
+          lo_n = an;
+        }
         if (holds) {
-          cut = b0 + k;
-          cut_n = an;
-          cut_m = am;
-          cut_in = bn;
+          hi = b0 + k;
+          hi_n = an + bn[k];
         }
       }
-      an += bn;
-      am += sh.h.lo[b0 + k] + (static_cast<uint64_t>(sh.h.hi[b0 + k]) << 32);
+      an += bn[k];
+      am += bm[k];
     }
-    const int last = block_reduce(cut, sh.redi, [](int a, int b) { return max(a, b); });
-    if (last < 0 && threadIdx.x == 0) sh.in_cnt = 0;  // an empty universe
-    if (cut == last && cut >= 0) {
-      sh.above_cnt = cut_n;
-      sh.above_mass = cut_m;
-      sh.in_cnt = cut_in;
-      // its tokens: a range of comp
-      if (first) {
-        // smallest and largest key of the bin, by bisection (the bin number falls with the key)
-        auto at = [&](uint32_t key) { return bin(value_of(key), 0); };
-        uint32_t a = kKeyLowest, b = key_of(top);  // at(b) <= cut
-        while (a < b) {                               // smallest key with at(key) <= cut
+    __syncthreads();
+    const int last = block_max(sh, hi);
+    const int first = min(-block_max(sh, -lo), last);
+    if (threadIdx.x == 0) sh.above_n = sh.in_n = 0xFFFFFFFFu;
+    __syncthreads();
+    if (last >= 0 && lo == first) sh.above_n = lo_n;
+    if (last >= 0 && hi == last) sh.in_n = hi_n;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const bool found = sh.above_n <= sh.in_n && sh.in_n != 0xFFFFFFFFu;
+      st.above_n = sh.above_n;
+      st.in_n = found ? sh.in_n - sh.above_n : 0xFFFFFFFFu;
+      if (found) {  // the keys of bins first .. last, by bisection (the bin number falls as the key grows)
+        auto at = [&](uint32_t key) { return value_place(value_of(key), top, scale32) >> 5; };
+        uint32_t a = kKeyLowest, b = key_of(top);
+        while (a < b) {  // smallest key whose bin is at most `last`
           const uint32_t mid = a + (b - a) / 2;
-          if (at(mid) <= cut) b = mid;
+          if (at(mid) <= last) b = mid;
           else a = mid + 1;
         }
-        const uint32_t kmin = a;
-        a = kmin;
+        st.clo = static_cast<uint64_t>(a) << 32;
         b = key_of(top);
-        while (a < b) {  // largest key with at(key) >= cut
+        while (a < b) {  // largest key whose bin is at least `first`
           const uint32_t mid = a + (b - a + 1) / 2;
-          if (at(mid) >= cut) a = mid;
+          if (at(mid) >= first) a = mid;
           else b = mid - 1;
         }
-        sh.clo = max(static_cast<uint64_t>(kmin) << 32, ulo);
-        sh.chi = (static_cast<uint64_t>(a) << 32) | 0xFFFFFFFFu;
-      } else {
-        const uint64_t hi = bin.chi - (static_cast<uint64_t>(cut) << bin.shift);
-        const uint64_t span = (1ull << bin.shift) - 1;
-        sh.chi = hi;
-        sh.clo = max(max(bin.clo, hi > span ? hi - span : 0), ulo);
+        st.chi = (static_cast<uint64_t>(a) << 32) | 0xFFFFFFFFu;
       }
     }
-    __syncthreads();
   }
-  cluster_sync();
-  if (rank != 0 && threadIdx.x == 0) {
-    sh.clo = peer_ld64(peer(&sh.clo, 0));
-    sh.chi = peer_ld64(peer(&sh.chi, 0));
-    sh.above_mass = peer_ld64(peer(&sh.above_mass, 0));
-    sh.above_cnt = peer_ld32(peer(&sh.above_cnt, 0));
-    sh.in_cnt = peer_ld32(peer(&sh.in_cnt, 0));
-  }
-  __syncthreads();
-  cluster_sync();  // rank 0 goes on to change them
 }
 
-// The tokens of [clo, chi] into rank 0's list and, with SCORE, the race over
-// the tokens above chi that min-p keeps, with their mass.
-template <bool VEC, bool SCORE>
-__device__ void collect(SelShared& sh, const float* row, int V, const RowParam& p, Race& race, uint64_t& mass) {
-  const uint32_t rank = cluster_rank(), size = cluster_size();
-  const float c = __fdiv_rn(kLog2e, p.temp), inv_t = __fdiv_rn(1.f, p.temp), top = sh.top;
-  const uint64_t clo = sh.clo, chi = sh.chi;
-  if (rank == 0 && threadIdx.x == 0) sh.n = 0;
-  cluster_sync();
-  const uint32_t n_at = peer(&sh.n, 0), list_at = peer(sh.l.comp, 0);
-  mass = 0;
-  for_slice<VEC>(row, V, rank, size, [&](const float4& x, int q) {
-    const float v[4] = {x.x, x.y, x.z, x.w};
-    bool up[4], any = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint64_t cp = comp_of(v[e], q * 4 + e);
-      up[e] = false;
-      if (cp < clo) continue;
-      if (cp <= chi) {
-        const uint32_t at = peer_add32(n_at, 1u);
-        if (at < kList) peer_st64(list_at + 8 * at, cp);
-      } else if (SCORE && min_p_keeps(v[e], top, p.temp, p.log_min_p)) {
-        up[e] = any = true;
-        mass += static_cast<uint64_t>(__fmul_rn(weight(v[e], top, c), kMassScale));
-      }
-    }
-    if (SCORE && any) {
-      const uint4 w = philox_block(p.seed, p.step, static_cast<uint32_t>(q));
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (up[e]) race.token(v[e], q * 4 + e, word_of(w, e), p.temp, inv_t);
-    }
-  });
-  cluster_sync();
-}
-
-// A row whose cut lies below the lists: the whole cluster re-reads it.
 template <bool VEC>
-__device__ void wide_row(SelShared& sh, const SelectArgs& a, const RowParam& p, int r) {
-  const uint32_t rank = cluster_rank(), size = cluster_size();
-  const float* row = a.logits + r * a.ld;
-  const int V = a.V;
-  uint64_t ulo = static_cast<uint64_t>(kKeyLowest) << 32;  // the universe: comp >= ulo
-  Race race;
-  uint64_t mass = 0;
-  auto restart = [&] {
-    if (threadIdx.x == 0) {
-      sh.clo = ulo;
-      sh.chi = ~0ull;
-      sh.above_mass = 0;
-      sh.above_cnt = 0;
-      sh.in_cnt = 0;
-    }
-    __syncthreads();
-  };
-  auto narrow = [&](bool by_count, float share) {
-    restart();
-    bool first = true;
-    do {
-      histogram_cut<VEC>(sh, row, V, p, first, ulo, by_count, p.top_k, share);
-      first = false;
-    } while (sh.in_cnt > kList);
-  };
-  const bool has_p = p.top_p < 1.f;
-  double z = 0;  // mass that top-p is a share of, where top-k cut first
-  if (p.top_k > 0) {
-    narrow(true, 0.f);
-    if (has_p) {  // top-k exactly, then top-p within it
-      collect<VEC, false>(sh, row, V, p, race, mass);
-      if (rank == 0) {
-        sort_desc(sh.l.comp, sh.n);
-        if (threadIdx.x == 0) {
-          const int last = min(sh.n, static_cast<int>(p.top_k - sh.above_cnt)) - 1;
-          sh.last_comp = sh.l.comp[max(last, 0)];
-        }
-        __syncthreads();
-      }
-      cluster_sync();
-      ulo = peer_ld64(peer(&sh.last_comp, 0));
-      cluster_sync();
-    }
-  }
-  if (has_p) {
-    narrow(false, p.top_p);
-    z = static_cast<double>(sh.total_mass);  // rank 0's
-  } else if (p.top_k == 0) {  // min-p alone: every token is "above", nothing undecided
-    if (threadIdx.x == 0) {
-      sh.clo = ulo;
-      sh.chi = ulo - 1;
-      sh.above_cnt = 0;
-      sh.above_mass = 0;
-    }
-    __syncthreads();
-  }
-  const uint64_t above = sh.above_mass;  // of the tokens above the undecided bin
-  const uint32_t above_n = sh.above_cnt;
-  collect<VEC, true>(sh, row, V, p, race, mass);
-  mass = block_reduce(mass, sh.redu, [](uint64_t x, uint64_t y) { return x + y; });
-  race.warp_reduce();
-  if ((threadIdx.x & 31) == 0) {
-    sh.redf[threadIdx.x >> 5] = race.best;
-    sh.redi[threadIdx.x >> 5] = race.best_i;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kSelThreads / 32; ++w) race.take(sh.redf[w], sh.redi[w]);
-    peer_st32(peer(&sh.r_best[rank], 0), __float_as_uint(race.best));
-    peer_st32(peer(&sh.r_best_i[rank], 0), static_cast<uint32_t>(race.best_i));
-    peer_st64(peer(&sh.r_mass[rank], 0), mass);
-  }
-  cluster_sync();  // the last access to another CTA's memory
-  if (rank != 0) return;
-  Race best;
-  uint64_t kept_mass = 0;
-  for (uint32_t k = 0; k < size; ++k) {
-    if (better(sh.r_best[k], sh.r_best_i[k], best.best, best.best_i)) {
-      best.best = sh.r_best[k];
-      best.best_i = sh.r_best_i[k];
-    }
-    kept_mass += sh.r_mass[k];
-  }
-  const int n = sh.n;
-  const double unit = 1.0 / kMassScale, base = static_cast<double>(above) * unit;
-  const double want = static_cast<double>(p.top_p) * (z * unit);
-  sort_desc(sh.l.comp, n);
-  prefix_mass(sh, n, sh.top, p.temp, base);
-  int kept = 0;
-  for (int j = threadIdx.x; j < n; j += kSelThreads) {
-    const float l = value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32));
-    const bool in_k = has_p || p.top_k == 0 || above_n + j < static_cast<uint32_t>(p.top_k);
-    const bool in_p = !has_p || above_n + j == 0 || (j == 0 ? base : sh.l.pre[j - 1]) < want;
-    kept += in_k && in_p && min_p_keeps(l, sh.top, p.temp, p.log_min_p);
-  }
-  kept = block_reduce(kept, sh.redi, [](int x, int y) { return x + y; });
-  const double total = static_cast<double>(kept_mass) * unit + (kept > 0 ? sh.l.pre[kept - 1] - base : 0.0);
-  choose(sh, p, kept, best, total, sh.top, row, a.tokens + r, a.logprobs ? a.logprobs + r : nullptr);
-}
-
-template <int N, bool VEC>
-__global__ void __launch_bounds__(kSelThreads)
-    filter_select_kernel(const __grid_constant__ RowParams<N> params, SelectArgs a) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  SelShared& sh = *reinterpret_cast<SelShared*>(smem_raw);
-  float* seg_max = reinterpret_cast<float*>(smem_raw + sizeof(SelShared));  // [nseg]
-  int* seg_n = reinterpret_cast<int*>(seg_max + a.nseg);                     // [nseg]
-  const uint32_t rank = cluster_rank(), size = cluster_size();
-  const int r = blockIdx.x / size;
-  const RowParam p = params.r[r];
-  const int mode = row_mode(p);
+__global__ void __launch_bounds__(kSelThreads, 4) filter_collect_kernel(Out o, Space sp) {
+  __shared__ SelShared sh;
   pdl_wait();
   pdl_trigger();
-  if (mode != ROW_FILTER && rank != 0) return;
-  const float* row = a.logits + r * a.ld;
-  bool wide = false;
-  if (rank == 0) {
-    const SegOut* segs = a.segs + static_cast<size_t>(r) * a.nseg;
-    float top = -INFINITY;
-    uint32_t thr = kKeyLowest;
+  const int items = *reinterpret_cast<volatile int*>(sp.n_wide) * o.nchunk;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int r = sp.wide_rows[item / o.nchunk], chunk = item % o.nchunk;
+    const RowParam p = sp.params[r];
+    WideState& st = sp.wide[r];
+    const bool has_k = p.top_k > 0, has_p = p.top_p < 1.f;
+    const float top = st.top, least = st.least;
+    if ((has_k || has_p) && st.in_n > kList) {  // no window
+      if (chunk == 0) exact_row<VEC>(sh, o, r, p, top);
+      continue;
+    }
     Race race;
-    for (int i = threadIdx.x; i < a.nseg; i += kSelThreads) {
-      const SegOut s = segs[i];
-      seg_max[i] = s.max;
-      seg_n[i] = s.count;
-      top = fmaxf(top, s.max);
-      thr = max(thr, s.thr);
-      if (better(s.best, s.best_i, race.best, race.best_i)) {
-        race.best = s.best;
-        race.best_i = s.best_i;
+    float mass;
+    uint64_t* window = sp.window + static_cast<size_t>(r) * kList;
+    const int quads = (o.V + 3) / 4, q0 = chunk * (kChunk / 4);
+    collect_quads<VEC, true>(o.logits + r * o.ld, o.V, q0, min(quads, q0 + kChunk / 4), p, top, least, st.clo, st.chi,
+                             window, &st.n, race, mass);
+    const double sum = block_sum(sh, static_cast<double>(mass));
+    block_best(sh, race);
+    ChunkOut* chunks = sp.chunks + static_cast<size_t>(r) * o.nchunk;
+    if (threadIdx.x == 0) chunks[chunk] = ChunkOut{sum, race.best, race.best_i};
+    if (!last_arrival(&st.arrived[1], o.nchunk, &sh.flag)) continue;
+    // ---- the choice
+    double base = 0;  // in the chunks' order
+    Race best;
+    for (int k = 0; k < o.nchunk; ++k) {
+      const ChunkOut* co = chunks + k;
+      base += __ldcg(&co->mass);
+      const float b = __ldcg(&co->best);
+      const int bi = __ldcg(&co->best_i);
+      if (better(b, bi, best.best, best.best_i)) {
+        best.best = b;
+        best.best_i = bi;
       }
     }
-    top = block_reduce(top, sh.redf, [](float x, float y) { return fmaxf(x, y); });
-    double z = 0;
-    if (mode != ROW_GREEDY) {
-      const float c = __fdiv_rn(kLog2e, p.temp);
-      for (int i = threadIdx.x; i < a.nseg; i += kSelThreads)
-        z += static_cast<double>(segs[i].sum) * static_cast<double>(weight(seg_max[i], top, c));
-      z = block_reduce(z, sh.redd, [](double x, double y) { return x + y; });
-    }
-    if (mode != ROW_FILTER || top == -INFINITY) {
-      choose(sh, p, 0, race, mode == ROW_GREEDY ? 1.0 : z, top, row, a.tokens + r, nullptr);
-      if (threadIdx.x == 0 && a.logprobs) {
-        const int tok = a.tokens[r];
-        const float l = row[tok], d = l == top ? 0.f : __fdiv_rn(__fsub_rn(l, top), p.temp);
-        a.logprobs[r] = mode != ROW_FREE || top == -INFINITY ? 0.f : __fsub_rn(d, log1pf(static_cast<float>(z - 1.0)));
-      }
-      if (mode != ROW_FILTER) return;
-    }
-    thr = block_reduce(thr, reinterpret_cast<uint32_t*>(sh.redi), [](uint32_t x, uint32_t y) { return max(x, y); });
-    const uint32_t floor = thr;  // every logit from here on is listed
-    const bool all = floor <= kKeyLowest;  // the lists hold every finite logit
-    // First as many candidates as there are large segment maxima (at least the
-    // first `want` tokens are among those at or above the want-th largest), then,
-    // if that does not decide the row, every listed one.
-    wide = top > -INFINITY;  // without any finite logit the choice has been made
-    for (int level = 0; level < 2 && wide; ++level) {
-      uint32_t from = floor;
-      if (level == 0) {
-        const int want = min(p.top_k > 0 ? min(p.top_k, 64) : 48, a.nseg);
-        uint32_t mine = 0;  // the want-th largest segment maximum's key
-        for (int i = threadIdx.x; i < a.nseg; i += kSelThreads) {
-          int above = 0;
-          const float m = seg_max[i];
-          for (int j = 0; j < a.nseg; ++j) above += seg_max[j] > m || (seg_max[j] == m && j < i);
-          if (above == want - 1) mine = key_of(m);
-        }
-        from = max(block_reduce(mine, reinterpret_cast<uint32_t*>(sh.redi),
-                                [](uint32_t x, uint32_t y) { return max(x, y); }),
-                   floor);
-        if (from == floor) continue;
-      }
-      if (threadIdx.x == 0) sh.n = 0;
-      __syncthreads();
-      const int lane = threadIdx.x & 31;
-      for (int i = threadIdx.x >> 5; i < a.nseg; i += kSelThreads / 32) {
-        if (key_of(seg_max[i]) < from) continue;
-        const uint64_t* list = a.lists + (static_cast<size_t>(r) * a.nseg + i) * kSegCap;
-        for (int k = lane; k < seg_n[i]; k += 32) {
-          const uint64_t cp = list[k];
-          if (static_cast<uint32_t>(cp >> 32) >= from) {
-            const int at = atomicAdd(&sh.n, 1);
-            if (at < kList) sh.l.comp[at] = cp;
-          }
-        }
-      }
-      __syncthreads();
-      const int n = sh.n;
-      if (n > kList || n == 0) continue;  // too many candidates, or none listed (ties)
-      const bool complete = all && from == floor;
-      sort_desc(sh.l.comp, n);
-      prefix_mass(sh, n, top, p.temp, 0.0);
-      const int lim = p.top_k > 0 ? min(p.top_k, n) : n;
-      const bool k_known = complete || p.top_k <= n;  // with top_k on: the list holds all of its tokens
-      const bool has_p = p.top_p < 1.f;
-      if (p.top_k > 0 && has_p && !k_known) continue;
-      const double share = static_cast<double>(p.top_p) * (p.top_k > 0 ? sh.l.pre[lim - 1] : z);
-      int kept = 0;
-      for (int j = threadIdx.x; j < lim; j += kSelThreads) {
-        const float l = value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32));
-        kept += (!has_p || j == 0 || sh.l.pre[j - 1] < share) && min_p_keeps(l, top, p.temp, p.log_min_p);
-      }
-      kept = block_reduce(kept, sh.redi, [](int x, int y) { return x + y; });
-      const bool decided = complete || kept < n || (p.top_k > 0 && p.top_k <= n) ||
-                           (has_p && sh.l.pre[lim - 1] >= share);
-      if (!decided) continue;
-      wide = false;
-      choose(sh, p, kept, Race(), kept > 0 ? sh.l.pre[kept - 1] : 1.0, top, row, a.tokens + r,
-             a.logprobs ? a.logprobs + r : nullptr);
-    }
-    if (threadIdx.x == 0) {
-      sh.go = wide;
-      sh.top = top;
-    }
-  }
-  cluster_sync();
-  if (rank != 0) {
-    wide = peer_ld32(peer(&sh.go, 0)) != 0;
-    const float top = __uint_as_float(peer_ld32(peer(&sh.top, 0)));
+    const int n = min(__ldcg(&st.n), kList);
+    for (int j = threadIdx.x; j < n; j += kSelThreads) sh.l.comp[j] = __ldcg(&window[j]);
     __syncthreads();
-    if (threadIdx.x == 0) sh.top = top;
+    sort_desc(sh.l.comp, n);
+    prefix_mass(sh, n, top, p.temp, base);
+    const double want = static_cast<double>(p.top_p) * st.z;
+    // Does the window hold the cut?  (Where min-p starts above it, min-p cuts and not top-p.)
+    const bool min_cuts = least > value_of(static_cast<uint32_t>(st.chi >> 32));
+    if (has_p && !min_cuts && !((st.above_n == 0 || base < want) && n > 0 && sh.l.pre[n - 1] >= want)) {
+      exact_row<VEC>(sh, o, r, p, top);
+      continue;
+    }
+    int kept = 0;
+    for (int j = threadIdx.x; j < n; j += kSelThreads) {
+      const bool in_k = !has_k || st.above_n + j < static_cast<uint32_t>(p.top_k);
+      const bool in_p = !has_p || st.above_n + j == 0 || (j == 0 ? base : sh.l.pre[j - 1]) < want;
+      kept += in_k && in_p && value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32)) >= least;
+    }
+    kept = block_sum(sh, kept);
+    choose(sh, o, r, p, kept, best, kept > 0 ? sh.l.pre[kept - 1] : base, top, false);
   }
-  cluster_sync();
-  if (wide) wide_row<VEC>(sh, a, p, r);
 }
 
-template <int N>
-int launch_filter_n(const SampleFilterArgs& a, int r0, int rows, cudaStream_t s) {
-  RowParams<N> params;
-  for (int i = 0; i < rows; ++i) {
-    const vd_sampler& sp = a.samplers[r0 + i];
-    RowParam& p = params.r[i];
-    p.seed = sp.seed;
-    p.step = sp.step;
-    p.temp = sp.temperature;
-    p.top_p = 1.f;
-    p.log_min_p = -INFINITY;
-    p.top_k = 0;
-    if (a.filters) {
-      const vd_filter& f = a.filters[r0 + i];
-      p.top_k = f.top_k > 0 && f.top_k < a.V ? f.top_k : 0;
-      p.top_p = f.top_p;
-      p.log_min_p = f.min_p > 0.f ? static_cast<float>(log(static_cast<double>(f.min_p))) : -INFINITY;
-    }
+// ---------------------------------------------------------------- host
+int sm_count_filter() {
+  static int n = 0;
+  if (!n) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
   }
-  for (int i = rows; i < N; ++i) params.r[i] = RowParam{};
-  const int nseg = (a.V + kSeg - 1) / kSeg;
-  // a list's length in all: about 1500 candidates a row reach the largest threshold
-  const int keep = nseg <= 128 ? 16 : nseg <= 256 ? 8 : nseg <= 512 ? 4 : 2;
-  SegOut* segs = static_cast<SegOut*>(a.workspace) + static_cast<size_t>(r0) * nseg;
-  uint64_t* lists = reinterpret_cast<uint64_t*>(static_cast<SegOut*>(a.workspace) + static_cast<size_t>(a.R) * nseg) +
-                    static_cast<size_t>(r0) * nseg * kSegCap;
-  const float* logits = a.logits + r0 * a.ld;
-  const bool vec = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.ld % 4 == 0;
+  return n;
+}
+
+void row_param(const SampleFilterArgs& a, int r, RowParam* p) {
+  const vd_sampler& s = a.samplers[r];
+  p->seed = s.seed;
+  p->step = s.step;
+  p->temp = s.temperature;
+  p->top_p = 1.f;
+  p->log_min_p = -INFINITY;
+  p->top_k = 0;
+  if (a.filters) {
+    const vd_filter& f = a.filters[r];
+    p->top_k = f.top_k > 0 && f.top_k < a.V ? f.top_k : 0;
+    p->top_p = f.top_p;
+    p->log_min_p = f.min_p > 0.f ? static_cast<float>(log(static_cast<double>(f.min_p))) : -INFINITY;
+  }
+}
+
+// Rows whose top_k is at most this are decided by their lists unless the
+// logits are adversarial (the lists hold about 1000 tokens of logits in no
+// order): a call of such rows alone does without the wide kernels.
+constexpr int kNarrowK = 256;
+
+template <int N>
+int launch_scan(const SampleFilterArgs& a, const Space& sp, int nseg, int r0, int rows, bool vec, bool* wide,
+                cudaStream_t s) {
+  RowParams<N> params;
+  for (int i = 0; i < N; ++i) {
+    if (i < rows) row_param(a, r0 + i, &params.r[i]);
+    else params.r[i] = RowParam{};
+    const RowParam& p = params.r[i];
+    *wide |= p.temp > 0.f && !(p.top_k > 0 && p.top_k <= kNarrowK) &&
+             (p.top_k > 0 || p.top_p < 1.f || p.log_min_p > -INFINITY);
+  }
+  // 8 groups list about 22 logits of a segment, 4 about 8, 2 about 3: a row's lists hold 1000 to 3000 in all, and
+  // those from its largest threshold on fit a CTA's list
+  const int groups = nseg <= 128 ? 8 : nseg <= 384 ? 4 : 2;
   VD_CUDA_TRY(launch_k(vec ? filter_scan_kernel<N, true> : filter_scan_kernel<N, false>,
                        dim3((nseg + kScanThreads / 32 - 1) / (kScanThreads / 32), rows), dim3(kScanThreads), 0, s, params,
-                       logits, a.V, a.ld, nseg, keep, segs, lists));
-  SelectArgs sel{};
-  sel.logits = logits;
-  sel.ld = a.ld;
-  sel.V = a.V;
-  sel.nseg = nseg;
-  sel.segs = segs;
-  sel.lists = lists;
-  sel.tokens = a.tokens + r0;
-  sel.logprobs = a.logprobs ? a.logprobs + r0 : nullptr;
-  const int cluster = rows <= 64 ? 8 : 4;
-  const size_t smem = sizeof(SelShared) + static_cast<size_t>(nseg) * 8;
-  auto k = vec ? filter_select_kernel<N, true> : filter_select_kernel<N, false>;
-  if (smem > 48 * 1024)
-    VD_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(rows * cluster);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  VD_CUDA_TRY(cudaLaunchKernelEx(&cfg, k, params, sel));
+                       a.logits, a.V, a.ld, nseg, groups, r0 == 0, sp, r0));
   return VD_OK;
 }
+
+template <bool VEC>
+int launch_decide(const Out& o, const Space& sp, int R, bool wide, cudaStream_t s) {
+  const size_t smem = static_cast<size_t>(o.nseg) * 8;
+  if (smem + sizeof(SelShared) > 48 * 1024)
+    VD_CUDA_TRY(cudaFuncSetAttribute(filter_select_kernel<VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem)));
+  VD_CUDA_TRY(launch_k(filter_select_kernel<VEC>, dim3(R), dim3(kSelThreads), smem, s, o, sp, wide));
+  if (!wide) return VD_OK;
+  const int grid = static_cast<int>(std::min<long long>(static_cast<long long>(R) * o.nchunk, 4LL * sm_count_filter()));
+  VD_CUDA_TRY(launch_k(filter_count_kernel<VEC>, dim3(grid), dim3(kSelThreads), 0, s, o, sp));
+  VD_CUDA_TRY(launch_k(filter_collect_kernel<VEC>, dim3(grid), dim3(kSelThreads), 0, s, o, sp));
+  return VD_OK;
+}
+
+int segments(int V) { return (V + kSeg - 1) / kSeg; }
+int chunks_of(int V) { return (V + kChunk - 1) / kChunk; }
 
 }  // namespace
 
 size_t sample_filter_workspace(int R, int V) {
-  const size_t nseg = (static_cast<size_t>(V) + kSeg - 1) / kSeg;
-  return static_cast<size_t>(R) * nseg * (sizeof(SegOut) + kSegCap * sizeof(uint64_t));
+  Space sp;
+  return space_of(&sp, nullptr, R, segments(V), chunks_of(V));
 }
 
 int launch_sample_filter(const SampleFilterArgs& a, cudaStream_t s) {
-  // the rows' parameters travel in the kernel parameters (40 bytes each)
-  for (int r0 = 0; r0 < a.R; r0 += 512) {
-    const int rows = std::min(512, a.R - r0);
-    const int rc = rows <= 16 ? launch_filter_n<16>(a, r0, rows, s)
-                   : rows <= 128 ? launch_filter_n<128>(a, r0, rows, s)
-                                 : launch_filter_n<512>(a, r0, rows, s);
+  Out o{a.logits, a.ld, a.V, segments(a.V), chunks_of(a.V), a.tokens, a.logprobs};
+  Space sp;
+  space_of(&sp, a.workspace, a.R, o.nseg, o.nchunk);
+  const bool vec = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.ld % 4 == 0;
+  bool wide = false;
+  int rc = VD_OK;
+  for (int r0 = 0; r0 < a.R; r0 += kScanRows) {
+    const int rows = std::min(kScanRows, a.R - r0);
+    rc = rows <= 16 ? launch_scan<16>(a, sp, o.nseg, r0, rows, vec, &wide, s)
+                    : launch_scan<kScanRows>(a, sp, o.nseg, r0, rows, vec, &wide, s);
     if (rc) return rc;
   }
-  return VD_OK;
+  return vec ? launch_decide<true>(o, sp, a.R, wide, s) : launch_decide<false>(o, sp, a.R, wide, s);
 }
 
 }  // namespace vd

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(TreeTailArgs
   uint8_t* sv = sk + C::TILE_BYTES;
   auto group_sync = [&] {
     if constexpr (DS == 1) __syncwarp();
-    else bar_sync_named(1 + group, DS * 32);
+    else asm volatile("barrier.sync %0, %1;" ::"r"(1 + group), "r"(DS * 32) : "memory");  // not .aligned: per thread
   };
   // the tree's description was written before the step's first kernel
   const int item = blockIdx.x * GROUPS + group;

@@ -108,6 +108,26 @@ def test_choice_vs_float64_large_vocabularies(V, kind):
     assert check(x, samplers, filters, tok, lp) <= 1
 
 
+def test_many_wide_rows_back_to_back():
+    """Several calls on one workspace with nothing waited for between them: rows that need the wide kernels, the exact
+    histograms and only the lists, side by side."""
+    ready()
+    V, R = 40000, 40
+    rng = np.random.default_rng(3)
+    kinds = ["flat", "normal", "ties", "sorted", "equal", "masked", "nan", "peak"]
+    x = np.concatenate([rows_of(kinds[r % 8], 1, V, r) for r in range(R)])
+    f = [FILTERS[int(i)] for i in rng.integers(0, len(FILTERS), R)]
+    lg, ws = torch.from_numpy(x).cuda(), vd.sample_workspace(R, V)
+    outs = []
+    for call in range(6):
+        s = [(r, call, TEMPS[(r + call) % len(TEMPS)]) for r in range(R)]
+        tok, lp = torch.empty(R, dtype=torch.int32, device="cuda"), torch.empty(R, device="cuda")
+        vd.sample(lg, s, f, tok, lp, ws)
+        outs.append((s, tok, lp))
+    torch.cuda.synchronize()
+    assert sum(check(x, s, f, tok.cpu().numpy(), lp.cpu().numpy()) for s, tok, lp in outs) <= 2
+
+
 def test_rows_without_filters_get_the_samplers_token():
     ready()
     V = 2048
