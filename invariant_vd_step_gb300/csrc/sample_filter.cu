@@ -33,8 +33,8 @@
 // top_k beyond the lists) one CTA settles by exact histograms over the
 // (value, index) order, refined until the cut's bin fits the list.
 //
-// Sums that decide something do not depend on timing: candidates are summed
-// in sorted order, chunks in their order, histogram masses as integers.
+// Sums that decide something do not depend on timing: masses are summed as
+// integers.
 #include <limits.h>
 #include <math.h>
 
@@ -49,15 +49,16 @@ namespace {
 constexpr int kSeg = 1024;        // logits of a segment (one warp: 8 x 4 per lane)
 constexpr int kSegCap = 64;       // list entries per segment
 constexpr int kScanThreads = 256;
+constexpr int kScanCtas = 2;      // resident per SM
 constexpr int kSelThreads = 256;
 constexpr int kBins = 2048;       // exact histogram: counts and masses, by (value, index) order
 constexpr int kCountBins = 4096;  // a wide row's histogram, by value
 constexpr float kBinNats = 24.f;  // its range below the largest logit, in units of T
 constexpr int kList = 2048;       // candidates that a CTA sorts
-constexpr int kChunk = 8192;      // tokens of a wide row's work item
+constexpr int kChunk = 8192;      // unit of a wide row's work items
 constexpr int kScanRows = 120;    // rows of a scan launch: their parameters fit 4 KB
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMassScale = 68719476736.f;  // 2^36: fixed-point unit of histogram masses (V <= 2^21: sums below 2^57)
+constexpr float kMassScale = 68719476736.f;  // 2^36
 
 enum RowMode { ROW_GREEDY = 0, ROW_FREE = 1, ROW_FILTER = 2 };
 
@@ -75,7 +76,13 @@ __device__ __forceinline__ int row_mode(const RowParam& p) {
   return p.top_k > 0 || p.top_p < 1.f || p.log_min_p > -INFINITY ? ROW_FILTER : ROW_FREE;
 }
 
-// What pass 1 leaves of a segment.
+// Whether a row's whole mass is asked for: top-p over every token, or the
+// log-probability of an unfiltered choice.
+__device__ __forceinline__ bool needs_mass(const RowParam& p) {
+  return p.temp > 0.f && p.top_k == 0 && (p.top_p < 1.f || !(p.log_min_p > -INFINITY));
+}
+
+// What the scan leaves of a segment.
 struct __align__(16) SegOut {
   float max, sum;   // largest logit; sum of exp((l - max) / T)
   uint32_t thr;     // every logit whose key is at least this is in the list
@@ -105,6 +112,18 @@ __device__ __forceinline__ int index_of(uint64_t comp) { return static_cast<int>
 __device__ __forceinline__ float weight(float l, float m, float c) {
   const float w = ex2(__fmul_rn(__fsub_rn(l, m), c));
   return l == m ? 1.f : w == w ? w : 0.f;
+}
+
+// One copy of the score's two logarithms and division per kernel: the streams
+// below call it for few tokens, from many unrolled places.
+__device__ __noinline__ float score_of(float l, uint32_t word, float t) { return gumbel_score(l, word, t); }
+
+// Masses are 64-bit integers in units of 2^-36 of the largest token's: sums
+// are exact in any order (V <= 2^21 tokens of mass at most 1: below 2^57), and
+// the GPU's few double-precision units stay out of it.
+__device__ __forceinline__ uint64_t fixed(float w) { return static_cast<uint64_t>(__fmul_rn(w, kMassScale)); }
+__device__ __forceinline__ uint64_t share_of(float top_p, uint64_t mass) {
+  return static_cast<uint64_t>(static_cast<double>(top_p) * static_cast<double>(mass));
 }
 
 // The best Gumbel score of a stream of tokens, without the two logarithms
@@ -140,7 +159,7 @@ struct Race {
   __device__ __forceinline__ void token(float l, int i, uint32_t word, float t, float c) {
     const float a = ex2(__fmaf_rn(l, c, k0));
     const float rest = __uint_as_float((~word >> 9) | 0x3F800000u);
-    if (!(rest > __fadd_rn(a, 1.0000002384185791015625f))) take(gumbel_score(l, word, t), i);
+    if (!(rest > __fadd_rn(a, 1.0000002384185791015625f))) take(score_of(l, word, t), i);
   }
   // over the warp; every lane ends with the winner
   __device__ __forceinline__ void warp_reduce() {
@@ -157,6 +176,26 @@ struct Race {
   }
 };
 
+// philox_block with each 32 x 32 product as one wide multiply and the key
+// schedule shared by a thread's blocks (the same words).
+struct Philox {
+  uint32_t k0, k1, c1, c2;
+  __device__ __forceinline__ explicit Philox(const RowParam& p)
+      : k0(static_cast<uint32_t>(p.seed)), k1(static_cast<uint32_t>(p.seed >> 32)), c1(static_cast<uint32_t>(p.step)),
+        c2(static_cast<uint32_t>(p.step >> 32)) {}
+  __device__ __forceinline__ uint4 block(uint32_t blk) const {
+    uint32_t x = blk, y = c1, z = c2, w = 0x5644u;
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+      const uint64_t a = static_cast<uint64_t>(0xD2511F53u) * x, b = static_cast<uint64_t>(0xCD9E8D57u) * z;
+      x = static_cast<uint32_t>(b >> 32) ^ y ^ (k0 + r * 0x9E3779B9u);
+      y = static_cast<uint32_t>(b);
+      z = static_cast<uint32_t>(a >> 32) ^ w ^ (k1 + r * 0xBB67AE85u);
+      w = static_cast<uint32_t>(a);
+    }
+    return make_uint4(x, y, z, w);
+  }
+};
 __device__ __forceinline__ uint32_t word_of(const uint4& w, int e) {
   return e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w;
 }
@@ -175,7 +214,7 @@ __device__ __forceinline__ float4 load4(const float* row, int i0, int V) {
 
 // What one row's wide kernels share.
 struct __align__(16) WideState {
-  double z;              // the row's whole mass, relative to `top`
+  uint64_t z;            // the row's whole mass
   uint64_t clo, chi;     // the window: a range of comp, inclusive
   float top;             // largest logit
   float least;           // smallest value that min-p keeps
@@ -183,10 +222,10 @@ struct __align__(16) WideState {
   uint32_t in_n;         // tokens inside it; more than kList: no usable window
   uint32_t arrived[2];   // CTAs done, per kernel
   int n;                 // tokens listed
-  int pad_;
+  float bound;           // a score that some kept token has: only tokens that reach it matter
 };
 struct __align__(16) ChunkOut {
-  double mass;           // of the chunk's tokens above the window (and at least `least`)
+  uint64_t mass;           // of an item's tokens above the window (and at least `least`)
   float best;
   int best_i;
 };
@@ -202,7 +241,7 @@ struct Space {
   uint32_t* count;       // [R][kCountBins] tokens
   uint32_t* place;       // [R][kCountBins] sums of their places in the bin, in 32nds
   int* wide_rows;        // [R]
-  int* n_wide;
+  int* n_wide;           // wide rows; then the next item of `count` and of `collect`
 };
 inline __host__ size_t space_of(Space* sp, void* base, int R, int nseg, int nchunk) {
   size_t off = 0;
@@ -212,7 +251,7 @@ inline __host__ size_t space_of(Space* sp, void* base, int R, int nseg, int nchu
     return static_cast<char*>(base) + o;
   };
   const size_t r = R;
-  sp->n_wide = reinterpret_cast<int*>(take(sizeof(int)));
+  sp->n_wide = reinterpret_cast<int*>(take(3 * sizeof(int)));
   sp->wide_rows = reinterpret_cast<int*>(take(r * sizeof(int)));
   sp->params = reinterpret_cast<RowParam*>(take(r * sizeof(RowParam)));
   sp->wide = reinterpret_cast<WideState*>(take(r * sizeof(WideState)));
@@ -226,77 +265,81 @@ inline __host__ size_t space_of(Space* sp, void* base, int R, int nseg, int nchu
 }
 
 // ---------------------------------------------------------------- scan
-// first: the call's first scan launch.  The others depend on no earlier kernel
-// but through it, so they wait for their predecessor at their end: they run
-// next to it, and whatever waits for the last one waits for all.
+// A warp walks over (row, segment) items and loads the next segment while it
+// works on one.  first: the call's first scan launch.  The others depend on no
+// earlier kernel but through it, so they wait for their predecessor at their
+// end: they run next to it, and whatever waits for the last one waits for all.
+template <bool VEC>
+__device__ __forceinline__ void load_seg(float4 (&x)[8], const float* row, int i0, int V) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) x[q] = load4<VEC>(row, i0 + q * 128, V);
+}
+
 template <int N, bool VEC>
-__global__ void __launch_bounds__(kScanThreads, 4)
+__global__ void __launch_bounds__(kScanThreads, kScanCtas)
     filter_scan_kernel(const __grid_constant__ RowParams<N> params, const float* __restrict__ logits, int V,
-                       long long ld, int nseg, int groups, bool first, Space sp, int r0) {
+                       long long ld, int nseg, int groups, bool first, Space sp, int r0, int rows) {
   if (first) pdl_wait();
   pdl_trigger();
-  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int seg = blockIdx.x * (kScanThreads / 32) + warp;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    sp.params[r0 + r] = params.r[r];
-    if (first && r == 0) *sp.n_wide = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) {
+    for (int r = threadIdx.x; r < rows; r += kScanThreads) sp.params[r0 + r] = params.r[r];
+    if (first && threadIdx.x < 3) sp.n_wide[threadIdx.x] = 0;
   }
-  if (seg >= nseg) {
-    if (!first) pdl_wait();
-    return;
-  }
-  const float* row = logits + (r0 + r) * ld;
-  const int i0 = seg * kSeg + lane * 4;
-  float v[8][4];
+  const int items = rows * nseg, step = gridDim.x * (kScanThreads / 32);
+  int item = blockIdx.x * (kScanThreads / 32) + warp;
+  int r = item / nseg, seg = item % nseg;
+  float4 next[8];
+  if (item < items) load_seg<VEC>(next, logits + (r0 + r) * ld, seg * kSeg + lane * 4, V);
+  while (item < items) {
+    float v[8][4];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float4 x = load4<VEC>(row, i0 + q * 128, V);
-    v[q][0] = x.x;
-    v[q][1] = x.y;
-    v[q][2] = x.z;
-    v[q][3] = x.w;
-  }
-  const RowParam p = params.r[r];
-  const int mode = row_mode(p);
-  float lm = -INFINITY;
+    for (int q = 0; q < 8; ++q) {
+      v[q][0] = next[q].x;
+      v[q][1] = next[q].y;
+      v[q][2] = next[q].z;
+      v[q][3] = next[q].w;
+    }
+    const RowParam p = params.r[r];
+    const int row_i = r0 + r, this_seg = seg, i0 = seg * kSeg + lane * 4;
+    const float* row = logits + row_i * ld;
+    item += step;
+    r = item / nseg;
+    seg = item % nseg;
+    if (item < items) load_seg<VEC>(next, logits + (r0 + r) * ld, seg * kSeg + lane * 4, V);
+
+    const int mode = row_mode(p);
+    float lm = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
+    for (int q = 0; q < 8; ++q) lm = fmaxf(lm, fmaxf(fmaxf(v[q][0], v[q][1]), fmaxf(v[q][2], v[q][3])));
+    float m = lm;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) lm = fmaxf(lm, v[q][e]);
-  float m = lm;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  SegOut out{};
-  out.max = m;
-  Race race;
-  if (mode == ROW_GREEDY || m == -INFINITY) {
-    // the lowest index among the maxima; a row of NaN and -inf has its lowest -inf
-#pragma unroll
-    for (int q = 7; q >= 0; --q)
-#pragma unroll
-      for (int e = 3; e >= 0; --e)
-        if (v[q][e] == m) race.best_i = i0 + q * 128 + e;
-    race.best = race.best_i == INT_MAX ? -INFINITY : m;
-    race.warp_reduce();
-  } else {
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    SegOut out{};
+    out.max = m;
+    out.thr = kKeyLowest;
+    Race race;
     const float c = __fdiv_rn(kLog2e, p.temp);
-    float sum = 0.f;
+    if (mode == ROW_GREEDY || m == -INFINITY) {
+      // the lowest index among the maxima; a row of NaN and -inf has its lowest -inf
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
+      for (int q = 7; q >= 0; --q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum = __fadd_rn(sum, weight(v[q][e], m, c));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-    out.sum = sum;
-    if (mode == ROW_FREE) {
+        for (int e = 3; e >= 0; --e)
+          if (v[q][e] == m) race.best_i = i0 + q * 128 + e;
+      race.best = race.best_i == INT_MAX ? -INFINITY : m;
+      race.warp_reduce();
+    } else if (mode == ROW_FREE) {
+      const Philox ph(p);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const int i = i0 + q * 128;
-        const uint4 w = philox_block(p.seed, p.step, static_cast<uint32_t>(i) / 4);
+        const uint4 w = ph.block(static_cast<uint32_t>(i) / 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) {
           if (i + e < V) race.token(v[q][e], i + e, word_of(w, e), p.temp, c);
-        if (q == 0) race.warp_reduce();  // a bound for the rest of the segment
+          if (q == 0) race.warp_reduce();  // a bound for the rest of the segment
+        }
       }
       race.warp_reduce();
     } else {
@@ -306,7 +349,7 @@ __global__ void __launch_bounds__(kScanThreads, 4)
       // half the groups, down to the maximum alone; if even that repeats too
       // often, nothing is listed.
       out.thr = key_of(m) + 1;
-      uint64_t* list = sp.lists + (static_cast<size_t>(r0 + r) * nseg + seg) * kSegCap;
+      uint64_t* list = sp.lists + (static_cast<size_t>(row_i) * nseg + this_seg) * kSegCap;
 #pragma unroll 1
       for (int g = groups; g > 0; g >>= 1) {
         float low = lm;
@@ -339,11 +382,28 @@ __global__ void __launch_bounds__(kScanThreads, 4)
         break;
       }
     }
+    if (needs_mass(p)) {
+      float sum = 0.f;
+      if (fabsf(m) < INFINITY) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sum = __fadd_rn(sum, fmaxf(ex2(__fmul_rn(__fsub_rn(v[q][e], m), c)), 0.f));  // (the maximum drops NaN)
+      } else {  // infinite logits share the mass
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum = __fadd_rn(sum, v[q][e] == m ? 1.f : 0.f);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+      out.sum = sum;
+    }
+    out.best = race.best;
+    out.best_i = race.best_i;
+    if (lane == 0) sp.segs[static_cast<size_t>(row_i) * nseg + this_seg] = out;
   }
-  out.best = race.best;
-  out.best_i = race.best_i;
-  if (out.thr == 0) out.thr = kKeyLowest;  // nothing to list
-  if (lane == 0) sp.segs[static_cast<size_t>(r0 + r) * nseg + seg] = out;
   if (!first) pdl_wait();
 }
 
@@ -356,10 +416,9 @@ struct SelShared {
     uint32_t count[kCountBins];
     struct {
       uint64_t comp[kList];
-      double pre[kList];  // masses up to and including each
+      uint64_t pre[kList];  // masses up to and including each
     } l;
   };
-  double redd[kSelThreads / 32];
   uint64_t redu[kSelThreads / 32];
   float redf[kSelThreads / 32];
   int redi[kSelThreads / 32];
@@ -389,8 +448,8 @@ __device__ __forceinline__ int block_sum(SelShared& sh, int v) {
 __device__ __forceinline__ int block_max(SelShared& sh, int v) {
   return block_reduce(v, sh.redi, [](int a, int b) { return max(a, b); });
 }
-__device__ __forceinline__ double block_sum(SelShared& sh, double v) {
-  return block_reduce(v, sh.redd, [](double a, double b) { return a + b; });
+__device__ __forceinline__ uint64_t block_sum(SelShared& sh, uint64_t v) {
+  return block_reduce(v, sh.redu, [](uint64_t a, uint64_t b) { return a + b; });
 }
 // The best of the block, on every thread.
 __device__ __forceinline__ void block_best(SelShared& sh, Race& race) {
@@ -502,44 +561,65 @@ __device__ void sort_desc(uint64_t* comp, int n) {
   }
 }
 
-// pre[j] = base + weights of comp[0 .. j], summed in that order.
-__device__ void prefix_mass(SelShared& sh, int n, float top, float t, double base) {
-  const int per = (n + kSelThreads - 1) / kSelThreads, j0 = threadIdx.x * per;
-  double sum = 0;
-  for (int j = j0; j < min(n, j0 + per); ++j) {
-    const float l = value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32));
-    sum += l == top ? 1.0 : static_cast<double>(expf(__fdiv_rn(__fsub_rn(l, top), t)));
+__device__ __forceinline__ float weight_of(uint64_t comp, float top, float t) {
+  const float l = value_of(static_cast<uint32_t>(comp >> 32));
+  return l == top ? 1.f : expf(__fdiv_rn(__fsub_rn(l, top), t));
+}
+// pre[j] = base + the masses of comp[0 .. j].
+__device__ void prefix_mass(SelShared& sh, int n, float top, float t, uint64_t base) {
+  const int per = (n + kSelThreads - 1) / kSelThreads, j0 = threadIdx.x * per, j1 = min(n, j0 + per);
+  uint64_t sum = 0;
+  for (int j = j0; j < j1; ++j) {
+    sum += fixed(weight_of(sh.l.comp[j], top, t));
     sh.l.pre[j] = sum;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double s = sum;
+  uint64_t s = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double x = __shfl_up_sync(0xffffffffu, s, o);
+    const uint64_t x = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += x;
   }
   __syncthreads();
-  if (lane == 31) sh.redd[warp] = s;
+  if (lane == 31) sh.redu[warp] = s;
   __syncthreads();
-  double off = base + (s - sum);
-  for (int w = 0; w < warp; ++w) off += sh.redd[w];
-  for (int j = j0; j < min(n, j0 + per); ++j) sh.l.pre[j] += off;
+  uint64_t off = base + s - sum;
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w)
+    if (w < warp) off += sh.redu[w];
+  for (int j = j0; j < j1; ++j) sh.l.pre[j] += off;
   __syncthreads();
 }
 
 __device__ __forceinline__ bool min_p_keeps(float l, float top, float t, float log_min_p) {
   return l == top || __fdiv_rn(__fsub_rn(l, top), t) >= log_min_p;
 }
-// The smallest value that min-p keeps, by bisection over the keys.
+// The smallest key in [lo, hi] for which `holds`, which is true from some key
+// on and at hi; a whole warp searches, 32 keys a round.
+template <typename F>
+__device__ __forceinline__ uint32_t first_key(uint32_t lo, uint32_t hi, F holds) {
+  const uint32_t lane = threadIdx.x & 31;
+  while (lo < hi) {
+    const uint32_t step = (hi - lo) / 32 + 1;
+    const uint64_t k = static_cast<uint64_t>(lo) + static_cast<uint64_t>(lane) * step;
+    const uint32_t yes = __ballot_sync(0xffffffffu, k >= hi || holds(static_cast<uint32_t>(k)));
+    const uint32_t f = __ffs(yes) - 1;  // lane 31's key is at or past hi unless a lane before it holds
+    if (yes == 0) {
+      lo = lo + 31 * step + 1;
+    } else {
+      const uint64_t at = static_cast<uint64_t>(lo) + static_cast<uint64_t>(f) * step;
+      if (f > 0) lo = lo + (f - 1) * step + 1;
+      hi = at < hi ? static_cast<uint32_t>(at) : hi;
+      if (f == 0) break;
+    }
+  }
+  return hi;
+}
+// The smallest value that min-p keeps (a whole warp).
 __device__ float min_p_least(const RowParam& p, float top) {
   if (!(p.log_min_p > -INFINITY)) return value_of(kKeyLowest);
-  uint32_t lo = kKeyLowest, hi = key_of(top);
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (min_p_keeps(value_of(mid), top, p.temp, p.log_min_p)) hi = mid;
-    else lo = mid + 1;
-  }
-  return value_of(lo);
+  return value_of(first_key(kKeyLowest, key_of(top),
+                            [&](uint32_t k) { return min_p_keeps(value_of(k), top, p.temp, p.log_min_p); }));
 }
 
 struct Out {
@@ -552,13 +632,14 @@ struct Out {
 
 // The choice among the first `kept` of the sorted list and `race` (the best
 // of tokens outside it); mass: that of every kept token, relative to `top`.
-__device__ void choose(SelShared& sh, const Out& o, int r, const RowParam& p, int kept, Race race, double mass,
+__device__ void choose(SelShared& sh, const Out& o, int r, const RowParam& p, int kept, Race race, uint64_t mass,
                        float top, bool point) {
+  const Philox ph(p);
   for (int j = threadIdx.x; j < kept; j += kSelThreads) {
     const uint64_t cp = sh.l.comp[j];
     const int i = index_of(cp);
-    const uint4 w = philox_block(p.seed, p.step, static_cast<uint32_t>(i) / 4);
-    const float v = gumbel_score(value_of(static_cast<uint32_t>(cp >> 32)), word_of(w, i & 3), p.temp);
+    const uint4 w = ph.block(static_cast<uint32_t>(i) / 4);
+    const float v = score_of(value_of(static_cast<uint32_t>(cp >> 32)), word_of(w, i & 3), p.temp);
     if (better(v, i, race.best, race.best_i)) {
       race.best = v;
       race.best_i = i;
@@ -571,14 +652,16 @@ __device__ void choose(SelShared& sh, const Out& o, int r, const RowParam& p, in
     if (o.logprobs) {
       const float l = o.logits[r * o.ld + tok];
       const float d = l == top ? 0.f : __fdiv_rn(__fsub_rn(l, top), p.temp);
-      o.logprobs[r] = point ? 0.f : __fsub_rn(d, log1pf(static_cast<float>(mass - 1.0)));
+      // the largest token's mass is 1: log1p of the rest
+      const float rest = __fmul_rn(static_cast<float>(mass - static_cast<uint64_t>(kMassScale)), 1.f / kMassScale);
+      o.logprobs[r] = point ? 0.f : __fsub_rn(d, log1pf(rest));
     }
   }
 }
 
 // Quads [q0, q1) of a row: f(four logits, their index / 4), every lane of a
 // warp taking part in each call (NaN past the end); end() after every kQuads.
-constexpr int kQuads = 4;
+constexpr int kQuads = 2;
 template <bool VEC, typename F, typename E>
 __device__ __forceinline__ void for_quads(const float* row, int V, int q0, int q1, F f, E end) {
   for (int qb = q0; qb < q1; qb += kQuads * kSelThreads) {
@@ -600,11 +683,13 @@ __device__ __forceinline__ void for_quads(const float* row, int V, int q0, int q
 template <bool VEC, bool SCORE>
 __device__ __forceinline__ void collect_quads(const float* row, int V, int q0, int q1, const RowParam& p, float top,
                                               float least, uint64_t clo, uint64_t chi, uint64_t* list, int* n,
-                                              Race& race, float& mass) {
+                                              Race& race, uint64_t& mass) {
+  const Philox ph(p);
   const float c = __fdiv_rn(kLog2e, p.temp);
   const float v_lo = value_of(static_cast<uint32_t>(clo >> 32)), v_hi = value_of(static_cast<uint32_t>(chi >> 32));
   float ratio = race.ratio_to(top, c);
-  mass = 0.f;
+  mass = 0;
+  float part = 0.f;  // of kQuads quads: eight terms
   int turn = 0;
   for_quads<VEC>(row, V, q0, q1, [&](const float4& x, int q) {
     const float v[4] = {x.x, x.y, x.z, x.w};
@@ -624,18 +709,20 @@ __device__ __forceinline__ void collect_quads(const float* row, int V, int q0, i
       above = above && v[e] >= least;
       w[e] = above ? (v[e] == top ? 1.f : ex2(__fmul_rn(__fsub_rn(v[e], top), c))) : -1.f;
       any |= above;
-      mass = __fadd_rn(mass, fmaxf(w[e], 0.f));
+      part = __fadd_rn(part, fmaxf(w[e], 0.f));
     }
     if (SCORE && any) {
-      const uint4 ws = philox_block(p.seed, p.step, static_cast<uint32_t>(q));
+      const uint4 ws = ph.block(static_cast<uint32_t>(q));
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (w[e] >= 0.f && race.may_win(w[e], ratio, word_of(ws, e))) {
-          race.take(gumbel_score(v[e], word_of(ws, e), p.temp), q * 4 + e);
+          race.take(score_of(v[e], word_of(ws, e), p.temp), q * 4 + e);
           ratio = race.ratio_to(top, c);
         }
     }
   }, [&] {
+    mass += fixed(part);
+    part = 0.f;
     if (SCORE && (turn & (turn + 1)) == 0) {  // a bound that the warp shares, after 1, 2, 4, ... turns
       race.warp_reduce();
       ratio = race.ratio_to(top, c);
@@ -645,6 +732,23 @@ __device__ __forceinline__ void collect_quads(const float* row, int V, int q0, i
 }
 
 // ---------------------------------------------------------------- the exact path
+// The comp range of the tokens in value bins first .. last (the bin number
+// falls as the key grows), at or above ulo: warps 0 and 1 find its ends.
+template <typename F>
+__device__ __forceinline__ void value_range(int first, int last, float top, F bin, uint64_t ulo, uint64_t* clo,
+                                            uint64_t* chi) {
+  const int warp = threadIdx.x >> 5;
+  const uint32_t hi = key_of(top);
+  if (warp == 0) {
+    const uint32_t k = first_key(kKeyLowest, hi, [&](uint32_t key) { return bin(value_of(key)) <= last; });
+    if ((threadIdx.x & 31) == 0) *clo = max(static_cast<uint64_t>(k) << 32, ulo);
+  } else if (warp == 1) {
+    // the first key past the bins, less one; none past them: up to `top`
+    const uint32_t k = first_key(kKeyLowest, hi + 1, [&](uint32_t key) { return bin(value_of(key)) < first; });
+    if ((threadIdx.x & 31) == 0) *chi = (static_cast<uint64_t>(k - 1) << 32) | 0xFFFFFFFFu;
+  }
+}
+
 // One histogram over the tokens of [clo, chi] at or above ulo, and the bin
 // where the criterion cuts: by_count, that of the top_k-th token; else the one
 // in which the mass before a token reaches top_p of the total.  The first pass
@@ -671,7 +775,7 @@ __device__ void histogram_cut(SelShared& sh, const float* row, int V, const RowP
       if (cp < clo || cp > hi0) continue;
       const int b = first ? by_value(v[e]) : static_cast<int>((hi0 - cp) >> shift);
       atomicAdd(&sh.h.cnt[b], 1u);
-      const uint64_t w = static_cast<uint64_t>(__fmul_rn(weight(v[e], top, c), kMassScale));
+      const uint64_t w = fixed(weight(v[e], top, c));
       if (w) {
         const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&sh.h.lo[b], wl);
         const uint32_t up = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
@@ -715,7 +819,7 @@ __device__ void histogram_cut(SelShared& sh, const float* row, int V, const RowP
     total += sh.redu[w];
   }
   if (!first) total = sh.total_mass;  // the whole universe's, from the first pass
-  const double want = static_cast<double>(p.top_p) * static_cast<double>(total);
+  const uint64_t want = share_of(p.top_p, total);
   __syncthreads();
   // the last non-empty bin before which the criterion still holds
   int cut = -1;
@@ -723,7 +827,7 @@ __device__ void histogram_cut(SelShared& sh, const float* row, int V, const RowP
   uint64_t cut_m = 0;
   for (int k = 0; k < PT; ++k) {
     const uint32_t bn = sh.h.cnt[b0 + k];
-    if (bn && (by_count ? an < static_cast<uint32_t>(p.top_k) : an == 0 || static_cast<double>(am) < want)) {
+    if (bn && (by_count ? an < static_cast<uint32_t>(p.top_k) : an == 0 || am < want)) {
       cut = b0 + k;
       cut_n = an;
       cut_m = am;
@@ -741,27 +845,16 @@ __device__ void histogram_cut(SelShared& sh, const float* row, int V, const RowP
     sh.above_n = cut_n;
     sh.above_mass = cut_m;
     sh.in_n = cut_in;
-    if (first) {  // the bin's smallest and largest key, by bisection (the bin number falls as the key grows)
-      uint32_t a = kKeyLowest, b = key_of(top);
-      while (a < b) {
-        const uint32_t mid = a + (b - a) / 2;
-        if (by_value(value_of(mid)) <= cut) b = mid;
-        else a = mid + 1;
-      }
-      sh.clo = max(static_cast<uint64_t>(a) << 32, ulo);
-      b = key_of(top);
-      while (a < b) {
-        const uint32_t mid = a + (b - a + 1) / 2;
-        if (by_value(value_of(mid)) >= cut) a = mid;
-        else b = mid - 1;
-      }
-      sh.chi = (static_cast<uint64_t>(a) << 32) | 0xFFFFFFFFu;
+    if (first) {
+      sh.flag = cut;  // its range of keys below
     } else {
       const uint64_t hi = hi0 - (static_cast<uint64_t>(cut) << shift), span = (1ull << shift) - 1;
       sh.chi = hi;
       sh.clo = max(max(lo0, hi > span ? hi - span : 0), ulo);
     }
   }
+  __syncthreads();
+  if (first && last >= 0) value_range(sh.flag, sh.flag, top, by_value, ulo, &sh.clo, &sh.chi);
   __syncthreads();
 }
 
@@ -794,20 +887,20 @@ __device__ __noinline__ void exact_row(SelShared& sh, const Out& o, int r, const
     __syncthreads();
     if (threadIdx.x == 0) sh.n = 0;
     __syncthreads();
-    float m;
+    uint64_t m;
     if (score) collect_quads<VEC, true>(row, V, 0, quads, p, top, from, sh.clo, sh.chi, sh.l.comp, &sh.n, race, m);
     else collect_quads<VEC, false>(row, V, 0, quads, p, top, from, sh.clo, sh.chi, sh.l.comp, &sh.n, race, m);
-    const double above = block_sum(sh, static_cast<double>(m));
+    const uint64_t above = block_sum(sh, m);
     const int n = min(sh.n, kList);
     sort_desc(sh.l.comp, n);
     prefix_mass(sh, n, top, p.temp, above);
     return above;
   };
-  double z = 0;
+  uint64_t z = 0;
   if (has_k) {
     narrow(true);
     if (has_p) {  // the top_k-th token and the mass down to it, then top-p within them
-      const double above = collect(value_of(kKeyLowest), false);
+      const uint64_t above = collect(value_of(kKeyLowest), false);
       const int n = min(sh.n, kList), last = min(n, static_cast<int>(p.top_k - sh.above_n)) - 1;
       if (last >= 0) {
         ulo = sh.l.comp[last];
@@ -819,7 +912,7 @@ __device__ __noinline__ void exact_row(SelShared& sh, const Out& o, int r, const
   }
   if (has_p) {
     narrow(false);
-    if (!has_k) z = static_cast<double>(sh.total_mass) / kMassScale;
+    if (!has_k) z = sh.total_mass;
   } else if (!has_k) {  // min-p alone: every token is "above", nothing undecided
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -829,7 +922,7 @@ __device__ __noinline__ void exact_row(SelShared& sh, const Out& o, int r, const
     }
     __syncthreads();
   }
-  const double base = collect(least, true), want = static_cast<double>(p.top_p) * z;
+  const uint64_t base = collect(least, true), want = share_of(p.top_p, z);
   const int n = min(sh.n, kList);
   int kept = 0;
   for (int j = threadIdx.x; j < n; j += kSelThreads) {
@@ -848,7 +941,8 @@ template <bool VEC>
 __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space sp, bool wide_next) {
   __shared__ SelShared sh;
   extern __shared__ float seg_max[];                     // [nseg]
-  int* seg_n = reinterpret_cast<int*>(seg_max + o.nseg);  // [nseg]
+  int* seg_n = reinterpret_cast<int*>(seg_max + o.nseg);  // [nseg] list entries
+  int* seg_off = seg_n + o.nseg;                          // [nseg] where a list starts among those taken
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x, lane = threadIdx.x & 31;
@@ -869,21 +963,35 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
       race.best_i = s.best_i;
     }
   }
-  top = block_reduce(top, sh.redf, [](float x, float y) { return fmaxf(x, y); });
-  double z = 0;
-  if (mode != ROW_GREEDY) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    floor = max(floor, __shfl_xor_sync(0xffffffffu, floor, s));
+  }
+  if (lane == 0) {
+    sh.redf[threadIdx.x >> 5] = top;
+    sh.redi[threadIdx.x >> 5] = static_cast<int>(floor);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) {
+    top = fmaxf(top, sh.redf[w]);
+    floor = max(floor, static_cast<uint32_t>(sh.redi[w]));
+  }
+  uint64_t z = 0;
+  if (needs_mass(p)) {
     const float c = __fdiv_rn(kLog2e, p.temp);
     for (int i = threadIdx.x; i < o.nseg; i += kSelThreads)
-      z += static_cast<double>(segs[i].sum) * static_cast<double>(weight(seg_max[i], top, c));
+      z += fixed(__fmul_rn(segs[i].sum, weight(seg_max[i], top, c)));
     z = block_sum(sh, z);
   }
   if (mode != ROW_FILTER || top == -INFINITY) {  // (without any finite logit the filters do not matter)
+    __syncthreads();
     choose(sh, o, r, p, 0, race, z, top, mode != ROW_FREE || top == -INFINITY);
     return;
   }
-  floor = static_cast<uint32_t>(block_reduce(floor, reinterpret_cast<uint32_t*>(sh.redi),
-                                             [](uint32_t x, uint32_t y) { return max(x, y); }));
   const bool all = floor <= kKeyLowest;  // the lists hold every finite logit
+  Race listed;  // the best of the listed tokens, where they are all kept
   // First as many candidates as there are large segment maxima (at least the
   // first `want` tokens are among those at or above the want-th largest), then,
   // if that does not decide the row, every listed one.
@@ -907,28 +1015,63 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     __syncthreads();
     if (threadIdx.x == 0) sh.n = 0;
     __syncthreads();
-    for (int i = threadIdx.x >> 5; i < o.nseg; i += kSelThreads / 32) {
-      if (key_of(seg_max[i]) < from) continue;
-      const uint64_t* list = sp.lists + (static_cast<size_t>(r) * o.nseg + i) * kSegCap;
-      for (int k = lane; k < seg_n[i]; k += 32) {
-        const uint64_t cp = list[k];
-        if (static_cast<uint32_t>(cp >> 32) >= from) {
-          const int at = atomicAdd(&sh.n, 1);
-          if (at < kList) sh.l.comp[at] = cp;
+    // the qualifying segments' lists end to end: entry e is in the last segment that starts at or before it
+    const int per = (o.nseg + kSelThreads - 1) / kSelThreads, s0 = threadIdx.x * per, s1 = min(o.nseg, s0 + per);
+    int mine = 0;
+    for (int i = s0; i < s1; ++i) mine += key_of(seg_max[i]) >= from ? seg_n[i] : 0;
+    int start = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, start, s);
+      if (lane >= s) start += x;
+    }
+    if (lane == 31) sh.redi[threadIdx.x >> 5] = start;
+    __syncthreads();
+    start -= mine;
+    int entries = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      if (w < static_cast<int>(threadIdx.x >> 5)) start += sh.redi[w];
+      entries += sh.redi[w];
+    }
+    for (int i = s0; i < s1; ++i) {
+      seg_off[i] = start;
+      start += key_of(seg_max[i]) >= from ? seg_n[i] : 0;
+    }
+    __syncthreads();
+    constexpr int kAhead = 4;
+    for (int e0 = threadIdx.x; e0 < entries; e0 += kAhead * kSelThreads) {
+      uint64_t cp[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int e = e0 + u * kSelThreads;
+        if (e >= entries) continue;
+        int a = 0, b = o.nseg - 1;
+        while (a < b) {
+          const int mid = (a + b + 1) >> 1;
+          if (seg_off[mid] <= e) a = mid;
+          else b = mid - 1;
         }
+        cp[u] = sp.lists[(static_cast<size_t>(r) * o.nseg + a) * kSegCap + (e - seg_off[a])];
       }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (e0 + u * kSelThreads < entries && static_cast<uint32_t>(cp[u] >> 32) >= from) {
+          const int at = atomicAdd(&sh.n, 1);
+          if (at < kList) sh.l.comp[at] = cp[u];
+        }
     }
     __syncthreads();
     const int n = sh.n;
     if (n > kList || n == 0) continue;  // too many candidates, or none listed (ties)
     const bool complete = all && from == floor;
     sort_desc(sh.l.comp, n);
-    prefix_mass(sh, n, top, p.temp, 0.0);
+    prefix_mass(sh, n, top, p.temp, 0);
     const int lim = p.top_k > 0 ? min(p.top_k, n) : n;
     const bool k_known = complete || p.top_k <= n;  // with top_k on: the list holds all of its tokens
     const bool has_p = p.top_p < 1.f;
     if (p.top_k > 0 && has_p && !k_known) continue;
-    const double share = static_cast<double>(p.top_p) * (p.top_k > 0 ? sh.l.pre[lim - 1] : z);
+    const uint64_t share = has_p ? share_of(p.top_p, p.top_k > 0 ? sh.l.pre[lim - 1] : z) : 0;
     int kept = 0;
     for (int j = threadIdx.x; j < lim; j += kSelThreads) {
       const float l = value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32));
@@ -936,8 +1079,20 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     }
     kept = block_sum(sh, kept);
     const bool decided = complete || kept < n || (p.top_k > 0 && p.top_k <= n) || (has_p && sh.l.pre[lim - 1] >= share);
-    if (!decided) continue;
-    choose(sh, o, r, p, kept, Race(), kept > 0 ? sh.l.pre[kept - 1] : 1.0, top, false);
+    if (!decided) {
+      if (level == 1 && wide_next && !(p.top_k > 0 && has_p)) {  // every listed token is kept
+        const Philox ph(p);
+        for (int j = threadIdx.x; j < n; j += kSelThreads) {
+          const uint64_t cp = sh.l.comp[j];
+          const int i = index_of(cp);
+          listed.take(score_of(value_of(static_cast<uint32_t>(cp >> 32)),
+                                   word_of(ph.block(static_cast<uint32_t>(i) / 4), i & 3), p.temp), i);
+        }
+        block_best(sh, listed);
+      }
+      continue;
+    }
+    choose(sh, o, r, p, kept, Race(), kept > 0 ? sh.l.pre[kept - 1] : 0, top, false);
     return;
   }
   if (!wide_next || (p.top_k > 0 && p.top_p < 1.f)) {
@@ -948,11 +1103,13 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     sp.count[static_cast<size_t>(r) * kCountBins + i] = 0;
     sp.place[static_cast<size_t>(r) * kCountBins + i] = 0;
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 32) {
     WideState w{};
     w.z = z;
     w.top = top;
     w.least = min_p_least(p, top);
+    if (lane != 0) return;
+    w.bound = listed.best;
     w.clo = static_cast<uint64_t>(kKeyLowest) << 32;  // min-p alone: an empty window below every token
     w.chi = w.clo - 1;
     sp.wide[r] = w;
@@ -973,6 +1130,20 @@ __device__ __forceinline__ bool last_arrival(uint32_t* arrived, int total, int* 
   return last;
 }
 
+// The CTA's next work item, in the order the CTAs ask.
+__device__ __forceinline__ int next_item(int* counter, int* slot) {
+  __syncthreads();
+  if (threadIdx.x == 0) *slot = atomicAdd(counter, 1);
+  __syncthreads();
+  return *slot;
+}
+
+// Units of kChunk tokens per work item: one while there are few items, up to
+// four where the CTAs have several items each anyway (fewer merges and ends).
+__device__ __forceinline__ int item_units(int n_wide, int nchunk) {
+  return min(4, max(1, static_cast<int>(static_cast<long long>(n_wide) * nchunk / (2 * gridDim.x))));
+}
+
 // A token's place in its row's value bins: bin << 5 | 32nd of the bin.
 __device__ __forceinline__ int value_place(float l, float top, float scale32) {
   const float d = l == top ? 0.f : __fmul_rn(__fsub_rn(top, l), scale32);
@@ -983,73 +1154,88 @@ __device__ __forceinline__ int value_place(float l, float top, float scale32) {
 // The estimate of a bin's mass from its tokens' mean place is off by the
 // rounding of the places (half a 32nd of a bin's 0.6 %, at most 9e-5 of the
 // bin's mass and less for values in no order) and by the spread inside a bin
-// (2e-6): the window takes kSlack of the whole mass to either side, and
+// (2e-6): the window takes 1 / kSlack of the whole mass to either side, and
 // `collect` checks the sums themselves.
-constexpr double kSlack = 1e-4;
+constexpr int kSlack = 10000;
 
 template <bool VEC>
-__global__ void __launch_bounds__(kSelThreads) filter_count_kernel(Out o, Space sp) {
+__global__ void __launch_bounds__(kSelThreads, 3) filter_count_kernel(Out o, Space sp) {
   __shared__ SelShared sh;
   pdl_wait();
   pdl_trigger();
-  const int items = *reinterpret_cast<volatile int*>(sp.n_wide) * o.nchunk;
+  const int n_wide = *reinterpret_cast<volatile int*>(sp.n_wide), units = item_units(n_wide, o.nchunk);
+  const int parts = (o.nchunk + units - 1) / units, items = n_wide * parts;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int r = sp.wide_rows[item / o.nchunk], chunk = item % o.nchunk;
+  for (int item; (item = next_item(sp.n_wide + 1, &sh.n)) < items;) {
+    const int r = sp.wide_rows[item / parts], part = item % parts;
     const RowParam p = sp.params[r];
     const bool by_count = p.top_k > 0;
     if (!by_count && p.top_p >= 1.f) continue;  // min-p alone needs no window
     WideState& st = sp.wide[r];
     const float top = st.top, scale32 = __fdiv_rn(32.f * kCountBins / kBinNats, p.temp);
     const float low = value_of(kKeyLowest);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kCountBins; i += kSelThreads) sh.count[i] = 0;
-    __syncthreads();
-    // tokens in the upper 14 bits, the sum of their 32nds in the lower 18: no
-    // bin of a chunk's 8192 tokens carries over (8192 * 31 < 2^18, and 8192 < 2^14)
-    static_assert(kChunk * 31 < (1 << 18) && kChunk < (1 << 14), "packed counters");
-    const int quads = (o.V + 3) / 4, q0 = chunk * (kChunk / 4);
-    for_quads<VEC>(o.logits + r * o.ld, o.V, q0, min(quads, q0 + kChunk / 4), [&](const float4& x, int) {
-      const float v[4] = {x.x, x.y, x.z, x.w};
+    constexpr int PT = kCountBins / kSelThreads;
+    uint32_t bn[PT], bp[PT];  // tokens and places of bins threadIdx.x + k * kSelThreads
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (v[e] >= low) {
-          const int at = value_place(v[e], top, scale32);
-          atomicAdd(&sh.count[at >> 5], (1u << 18) + (at & 31));
-        }
-    }, [] {});
+    for (int k = 0; k < PT; ++k) bn[k] = bp[k] = 0;
     __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PT; ++k) sh.count[threadIdx.x + k * kSelThreads] = 0;
+    const int quads = (o.V + 3) / 4;
+    for (int unit = part * units; unit < min(o.nchunk, (part + 1) * units); ++unit) {
+      __syncthreads();
+      // tokens in the upper 14 bits, the sum of their 32nds in the lower 18: no
+      // bin of a unit's 8192 tokens carries over (8192 * 31 < 2^18, and 8192 < 2^14)
+      static_assert(kChunk * 31 < (1 << 18) && kChunk < (1 << 14), "packed counters");
+      const int q0 = unit * (kChunk / 4);
+      for_quads<VEC>(o.logits + r * o.ld, o.V, q0, min(quads, q0 + kChunk / 4), [&](const float4& x, int) {
+        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (v[e] >= low) {
+            const int at = value_place(v[e], top, scale32);
+            atomicAdd(&sh.count[at >> 5], (1u << 18) + (at & 31));
+          }
+      }, [] {});
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < PT; ++k) {
+        const uint32_t h = sh.count[threadIdx.x + k * kSelThreads];
+        sh.count[threadIdx.x + k * kSelThreads] = 0;
+        bn[k] += h >> 18;
+        bp[k] += h & 0x3FFFF;
+      }
+    }
     uint32_t* count = sp.count + static_cast<size_t>(r) * kCountBins;
     uint32_t* place = sp.place + static_cast<size_t>(r) * kCountBins;
-    for (int i = threadIdx.x; i < kCountBins; i += kSelThreads)
-      if (const uint32_t h = sh.count[i]) {
-        atomicAdd(&count[i], h >> 18);
-        if (h & 0x3FFFF) atomicAdd(&place[i], h & 0x3FFFF);
+#pragma unroll
+    for (int k = 0; k < PT; ++k)
+      if (bn[k]) {
+        atomicAdd(&count[threadIdx.x + k * kSelThreads], bn[k]);
+        if (bp[k]) atomicAdd(&place[threadIdx.x + k * kSelThreads], bp[k]);
       }
-    if (!last_arrival(&st.arrived[0], o.nchunk, &sh.flag)) continue;
+    if (!last_arrival(&st.arrived[0], parts, &sh.flag)) continue;
     // ---- the window
-    constexpr int PT = kCountBins / kSelThreads;
     const int b0 = threadIdx.x * PT;
     const float step = kBinNats / kCountBins;  // nats of a bin
-    uint32_t bn[PT];
-    float bm[PT];
+    uint64_t bm[PT];
     uint32_t n = 0;
-    double m = 0;
+    uint64_t m = 0;
 #pragma unroll
     for (int k = 0; k < PT; ++k) {
       bn[k] = __ldcg(&count[b0 + k]);
       const float mean = __fdiv_rn(static_cast<float>(__ldcg(&place[b0 + k])), 32.f * fmaxf(static_cast<float>(bn[k]), 1.f));
-      bm[k] = __fmul_rn(static_cast<float>(bn[k]),
-                        ex2(__fmul_rn(-step * kLog2e, __fadd_rn(static_cast<float>(b0 + k), __fadd_rn(mean, 1.f / 64)))));
+      bm[k] = fixed(__fmul_rn(static_cast<float>(bn[k]), ex2(__fmul_rn(-step * kLog2e, __fadd_rn(static_cast<float>(b0 + k),
+                                                                                    __fadd_rn(mean, 1.f / 64))))));
       n += bn[k];
       m += bm[k];
     }
     uint32_t sn = n;
-    double sm = m;
+    uint64_t sm = m;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
       const uint32_t xn = __shfl_up_sync(0xffffffffu, sn, s);
-      const double xm = __shfl_up_sync(0xffffffffu, sm, s);
+      const uint64_t xm = __shfl_up_sync(0xffffffffu, sm, s);
       if (lane >= s) {
         sn += xn;
         sm += xm;
@@ -1057,22 +1243,22 @@ __global__ void __launch_bounds__(kSelThreads) filter_count_kernel(Out o, Space 
     }
     if (lane == 31) {
       sh.redi[warp] = static_cast<int>(sn);
-      sh.redd[warp] = sm;
+      sh.redu[warp] = sm;
     }
     __syncthreads();
     uint32_t an = sn - n;
-    double am = sm - m;
+    uint64_t am = sm - m;
     for (int w = 0; w < warp; ++w) {
       an += sh.redi[w];
-      am += sh.redd[w];
+      am += sh.redu[w];
     }
-    const double want = static_cast<double>(p.top_p) * st.z, slack = kSlack * st.z;
+    const uint64_t z = st.z, want = share_of(p.top_p, z), slack = z / kSlack;
     int lo = kCountBins, hi = -1;  // the window's first and last bin
     uint32_t lo_n = 0, hi_n = 0;   // tokens above the first, tokens up to the last
 #pragma unroll
     for (int k = 0; k < PT; ++k) {
       if (bn[k]) {
-        const bool enters = by_count ? an + bn[k] >= static_cast<uint32_t>(p.top_k) : am + bm[k] > want - slack;
+        const bool enters = by_count ? an + bn[k] >= static_cast<uint32_t>(p.top_k) : am + bm[k] + slack > want;
         const bool holds = by_count ? an < static_cast<uint32_t>(p.top_k) : an == 0 || am < want + slack;
         if (enters && lo == kCountBins) {
           lo = b0 + k;
@@ -1094,28 +1280,13 @@ __global__ void __launch_bounds__(kSelThreads) filter_count_kernel(Out o, Space 
     if (last >= 0 && lo == first) sh.above_n = lo_n;
     if (last >= 0 && hi == last) sh.in_n = hi_n;
     __syncthreads();
+    const bool found = sh.above_n <= sh.in_n && sh.in_n != 0xFFFFFFFFu;
     if (threadIdx.x == 0) {
-      const bool found = sh.above_n <= sh.in_n && sh.in_n != 0xFFFFFFFFu;
       st.above_n = sh.above_n;
       st.in_n = found ? sh.in_n - sh.above_n : 0xFFFFFFFFu;
-      if (found) {  // the keys of bins first .. last, by bisection (the bin number falls as the key grows)
-        auto at = [&](uint32_t key) { return value_place(value_of(key), top, scale32) >> 5; };
-        uint32_t a = kKeyLowest, b = key_of(top);
-        while (a < b) {  // smallest key whose bin is at most `last`
-          const uint32_t mid = a + (b - a) / 2;
-          if (at(mid) <= last) b = mid;
-          else a = mid + 1;
-        }
-        st.clo = static_cast<uint64_t>(a) << 32;
-        b = key_of(top);
-        while (a < b) {  // largest key whose bin is at least `first`
-          const uint32_t mid = a + (b - a + 1) / 2;
-          if (at(mid) >= first) a = mid;
-          else b = mid - 1;
-        }
-        st.chi = (static_cast<uint64_t>(a) << 32) | 0xFFFFFFFFu;
-      }
     }
+    if (found)
+      value_range(first, last, top, [&](float l) { return value_place(l, top, scale32) >> 5; }, 0, &st.clo, &st.chi);
   }
 }
 
@@ -1124,34 +1295,37 @@ __global__ void __launch_bounds__(kSelThreads, 4) filter_collect_kernel(Out o, S
   __shared__ SelShared sh;
   pdl_wait();
   pdl_trigger();
-  const int items = *reinterpret_cast<volatile int*>(sp.n_wide) * o.nchunk;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int r = sp.wide_rows[item / o.nchunk], chunk = item % o.nchunk;
+  const int n_wide = *reinterpret_cast<volatile int*>(sp.n_wide), units = item_units(n_wide, o.nchunk);
+  const int parts = (o.nchunk + units - 1) / units, items = n_wide * parts;
+  for (int item; (item = next_item(sp.n_wide + 2, &sh.n)) < items;) {
+    const int r = sp.wide_rows[item / parts], part = item % parts;
     const RowParam p = sp.params[r];
     WideState& st = sp.wide[r];
     const bool has_k = p.top_k > 0, has_p = p.top_p < 1.f;
     const float top = st.top, least = st.least;
     if ((has_k || has_p) && st.in_n > kList) {  // no window
-      if (chunk == 0) exact_row<VEC>(sh, o, r, p, top);
+      if (part == 0) exact_row<VEC>(sh, o, r, p, top);
       continue;
     }
     Race race;
-    float mass;
+    race.best = st.bound;  // with no token: any that reaches it takes over
+    race.set_bound();
+    uint64_t mass;
     uint64_t* window = sp.window + static_cast<size_t>(r) * kList;
-    const int quads = (o.V + 3) / 4, q0 = chunk * (kChunk / 4);
-    collect_quads<VEC, true>(o.logits + r * o.ld, o.V, q0, min(quads, q0 + kChunk / 4), p, top, least, st.clo, st.chi,
-                             window, &st.n, race, mass);
-    const double sum = block_sum(sh, static_cast<double>(mass));
+    const int quads = (o.V + 3) / 4, q0 = part * units * (kChunk / 4);
+    collect_quads<VEC, true>(o.logits + r * o.ld, o.V, q0, min(quads, q0 + units * (kChunk / 4)), p, top, least, st.clo,
+                             st.chi, window, &st.n, race, mass);
+    const uint64_t sum = block_sum(sh, mass);
     block_best(sh, race);
     ChunkOut* chunks = sp.chunks + static_cast<size_t>(r) * o.nchunk;
-    if (threadIdx.x == 0) chunks[chunk] = ChunkOut{sum, race.best, race.best_i};
-    if (!last_arrival(&st.arrived[1], o.nchunk, &sh.flag)) continue;
+    if (threadIdx.x == 0) chunks[part] = ChunkOut{sum, race.best, race.best_i};
+    if (!last_arrival(&st.arrived[1], parts, &sh.flag)) continue;
     // ---- the choice
-    double base = 0;  // in the chunks' order
+    uint64_t base = 0;
     Race best;
-    for (int k = 0; k < o.nchunk; ++k) {
+    for (int k = threadIdx.x; k < parts; k += kSelThreads) {
       const ChunkOut* co = chunks + k;
-      base += __ldcg(&co->mass);
+      base += __ldcg(reinterpret_cast<const unsigned long long*>(&co->mass));
       const float b = __ldcg(&co->best);
       const int bi = __ldcg(&co->best_i);
       if (better(b, bi, best.best, best.best_i)) {
@@ -1159,12 +1333,13 @@ __global__ void __launch_bounds__(kSelThreads, 4) filter_collect_kernel(Out o, S
         best.best_i = bi;
       }
     }
+    base = block_sum(sh, base);
     const int n = min(__ldcg(&st.n), kList);
-    for (int j = threadIdx.x; j < n; j += kSelThreads) sh.l.comp[j] = __ldcg(&window[j]);
+    for (int j = threadIdx.x; j < n; j += kSelThreads) sh.l.comp[j] = __ldcg(reinterpret_cast<const unsigned long long*>(window) + j);
     __syncthreads();
     sort_desc(sh.l.comp, n);
     prefix_mass(sh, n, top, p.temp, base);
-    const double want = static_cast<double>(p.top_p) * st.z;
+    const uint64_t want = share_of(p.top_p, st.z);
     // Does the window hold the cut?  (Where min-p starts above it, min-p cuts and not top-p.)
     const bool min_cuts = least > value_of(static_cast<uint32_t>(st.chi >> 32));
     if (has_p && !min_cuts && !((st.above_n == 0 || base < want) && n > 0 && sh.l.pre[n - 1] >= want)) {
@@ -1229,20 +1404,21 @@ int launch_scan(const SampleFilterArgs& a, const Space& sp, int nseg, int r0, in
   // those from its largest threshold on fit a CTA's list
   const int groups = nseg <= 128 ? 8 : nseg <= 384 ? 4 : 2;
   VD_CUDA_TRY(launch_k(vec ? filter_scan_kernel<N, true> : filter_scan_kernel<N, false>,
-                       dim3((nseg + kScanThreads / 32 - 1) / (kScanThreads / 32), rows), dim3(kScanThreads), 0, s, params,
-                       a.logits, a.V, a.ld, nseg, groups, r0 == 0, sp, r0));
+                       dim3(std::min((rows * nseg + kScanThreads / 32 - 1) / (kScanThreads / 32),
+                                     kScanCtas * sm_count_filter())),
+                       dim3(kScanThreads), 0, s, params, a.logits, a.V, a.ld, nseg, groups, r0 == 0, sp, r0, rows));
   return VD_OK;
 }
 
 template <bool VEC>
 int launch_decide(const Out& o, const Space& sp, int R, bool wide, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(o.nseg) * 8;
+  const size_t smem = static_cast<size_t>(o.nseg) * 12;
   if (smem + sizeof(SelShared) > 48 * 1024)
     VD_CUDA_TRY(cudaFuncSetAttribute(filter_select_kernel<VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(smem)));
   VD_CUDA_TRY(launch_k(filter_select_kernel<VEC>, dim3(R), dim3(kSelThreads), smem, s, o, sp, wide));
   if (!wide) return VD_OK;
-  const int grid = static_cast<int>(std::min<long long>(static_cast<long long>(R) * o.nchunk, 4LL * sm_count_filter()));
+  const int grid = static_cast<int>(std::min<long long>(static_cast<long long>(R) * o.nchunk, 3LL * sm_count_filter()));
   VD_CUDA_TRY(launch_k(filter_count_kernel<VEC>, dim3(grid), dim3(kSelThreads), 0, s, o, sp));
   VD_CUDA_TRY(launch_k(filter_collect_kernel<VEC>, dim3(grid), dim3(kSelThreads), 0, s, o, sp));
   return VD_OK;
@@ -1265,8 +1441,9 @@ int launch_sample_filter(const SampleFilterArgs& a, cudaStream_t s) {
   const bool vec = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.ld % 4 == 0;
   bool wide = false;
   int rc = VD_OK;
-  for (int r0 = 0; r0 < a.R; r0 += kScanRows) {
-    const int rows = std::min(kScanRows, a.R - r0);
+  const int launches = (a.R + kScanRows - 1) / kScanRows, each = (a.R + launches - 1) / launches;
+  for (int r0 = 0; r0 < a.R; r0 += each) {
+    const int rows = std::min(each, a.R - r0);
     rc = rows <= 16 ? launch_scan<16>(a, sp, o.nseg, r0, rows, vec, &wide, s)
                     : launch_scan<kScanRows>(a, sp, o.nseg, r0, rows, vec, &wide, s);
     if (rc) return rc;
