@@ -34,10 +34,9 @@ struct vd_tree {
 
 namespace {
 
-// Requests of at most this many rows (nodes x query heads per KV head) run
-// their shared tiles on one mma.sync CTA of 64 rows per split; more rows take
-// the tcgen05 kernel's 128-row CTAs (the same bits).
-constexpr int kTreeMmaRows = 64;
+// Rows (nodes x query heads per KV head) of a CTA of each class, the same
+// bits in every one.
+constexpr int kClsRows[4] = {16, 32, 64, 128};
 
 int check_call(const vd_tree* t, const vd_kv_pool* pool, cudaStream_t s) {
   if (!t || !pool) return fail(VD_ERR_INVALID_ARG, "null tree or pool");
@@ -101,19 +100,17 @@ int vd::run_tree_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc&
   a.tree_pos = d.base + d.positions;
   int rc;
   Prof p(m, K_ATTN, s);
-  p.kernels = (d.items_dec > 0) + (d.items_pre > 0) + (d.items_tc > 0) + 2;
-  a.cls_seq = d.base + d.dec_seq;
-  a.cls_start = d.base + d.dec_start;
-  a.n_cls = d.n_dec;
-  if ((rc = launch_attention_tree(pool->map, a, hd, false, d.items_dec, s))) return rc;
-  a.cls_seq = d.base + d.pre_seq;
-  a.cls_start = d.base + d.pre_start;
-  a.n_cls = d.n_pre;
-  if ((rc = launch_attention_tree(pool->map, a, hd, true, d.items_pre, s))) return rc;
-  a.cls_seq = d.base + d.tc_seq;
-  a.cls_start = d.base + d.tc_start;
-  a.n_cls = d.n_tc;
-  if ((rc = launch_attention_tc(pool->map_tc, a, hd, d.items_tc, s))) return rc;
+  p.kernels = 2;
+  for (int k = 0; k < 4; ++k) {
+    if (d.cls[k].items == 0) continue;
+    ++p.kernels;
+    a.cls_seq = d.base + d.cls[k].seq;
+    a.cls_start = d.base + d.cls[k].start;
+    a.n_cls = d.cls[k].n;
+    if ((rc = k == 3 ? launch_attention_tc(pool->map_tc, a, hd, d.cls[k].items, s)
+                     : launch_attention_tree(pool->map, a, hd, kClsRows[k], d.cls[k].items, s)))
+      return rc;
+  }
   TreeTailArgs t{};
   t.q = q;
   t.pool = static_cast<const __nv_bfloat16*>(pool->data) +
@@ -266,12 +263,10 @@ int vd_tree_plan(vd_tree* t, vd_kv_pool* pool, const vd_tree_batch* b, void* str
   d.parent = take(T);
   d.cu_q = take(B + 1);
   d.cached = take(B);
-  d.dec_seq = take(B);
-  d.dec_start = take(B + 1);
-  d.pre_seq = take(B);
-  d.pre_start = take(B + 1);
-  d.tc_seq = take(B);
-  d.tc_start = take(B + 1);
+  for (auto& k : d.cls) {
+    k.seq = take(B);
+    k.start = take(B + 1);
+  }
   d.path = take(paths);
   d.page_table = take(static_cast<size_t>(B) * stride);
   if (off > (1u << 30)) return fail(VD_ERR_CAPACITY, "plan too large");
@@ -297,6 +292,12 @@ int vd_tree_plan(vd_tree* t, vd_kv_pool* pool, const vd_tree_batch* b, void* str
     const int r = nodes * m->G, nsplit = shared > 0 ? (shared - 1) / m->split + 1 : 0;
     return (r + rows_per_cta - 1) / rows_per_cta * c.n_kv_heads * nsplit;
   };
+  // A launch of at most one 16-row CTA per SM is bound by its CTAs' latency, not
+  // by what they read: blocks of 16 rows (their K/V tiles shared by four warps)
+  // then beat fewer CTAs of more rows.
+  long long small_items = 0;
+  for (int i = 0; i < B; ++i)
+    small_items += items(b->cu_nodes[i + 1] - b->cu_nodes[i], b->cached_len[i] / m->key_tile * m->key_tile, 16);
   for (int i = 0; i < B; ++i) {
     const int n0 = b->cu_nodes[i], n = b->cu_nodes[i + 1] - n0, cached = b->cached_len[i];
     for (int j = 0; j < stride; ++j)
@@ -323,18 +324,15 @@ int vd_tree_plan(vd_tree* t, vd_kv_pool* pool, const vd_tree_batch* b, void* str
     h[d.cached + i] = cached;
     // the request's class, by its rows
     const int shared = cached / m->key_tile * m->key_tile, r = n * m->G;
-    const bool tc = r > kTreeMmaRows && m->prefill_kernel == 0 && attn_tc_supported(c.head_dim);
-    int& cnt = r <= 16 ? d.n_dec : tc ? d.n_tc : d.n_pre;
-    int& at = r <= 16 ? d.items_dec : tc ? d.items_tc : d.items_pre;
-    h[(r <= 16 ? d.dec_seq : tc ? d.tc_seq : d.pre_seq) + cnt] = i;
-    h[(r <= 16 ? d.dec_start : tc ? d.tc_start : d.pre_start) + cnt] = at;
-    at += items(n, shared, r <= 16 ? 16 : tc ? 128 : 64);
-    ++cnt;
+    const bool tc = m->prefill_kernel == 0 && attn_tc_supported(c.head_dim);
+    const int k = r <= 16 || small_items <= m->n_sm ? 0 : tc ? 3 : r <= 32 ? 1 : 2;
+    h[d.cls[k].seq + d.cls[k].n] = i;
+    h[d.cls[k].start + d.cls[k].n] = d.cls[k].items;
+    d.cls[k].items += items(n, shared, kClsRows[k]);
+    ++d.cls[k].n;
   }
   h[d.cu_q + B] = T;
-  h[d.dec_start + d.n_dec] = d.items_dec;
-  h[d.pre_start + d.n_pre] = d.items_pre;
-  h[d.tc_start + d.n_tc] = d.items_tc;
+  for (const auto& k : d.cls) h[k.start + k.n] = k.items;
   d.base = t->dev;
   d.part_o = t->part;
   d.part_ml = t->part + rows * c.head_dim;

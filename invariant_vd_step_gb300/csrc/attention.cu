@@ -876,18 +876,19 @@ int launch_attention(const CUtensorMap& kvmap, const AttnArgs& a, int hd, bool p
   return fail(VD_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
 }
 
-int launch_attention_tree(const CUtensorMap& kvmap, const AttnArgs& a, int hd, bool prefill_class, int n_items,
+int launch_attention_tree(const CUtensorMap& kvmap, const AttnArgs& a, int hd, int cta_rows, int n_items,
                           cudaStream_t s) {
   if (n_items <= 0) return VD_OK;
   if (a.fold) return fail(VD_ERR_INVALID_ARG, "tree attention does not fold splits");
   if (a.split > AttnCfg<64>::PIDS * 16) return fail(VD_ERR_INVALID_ARG, "KV split larger than the staged page ids");
-  const bool wide = !prefill_class && n_items <= sm_count_attn();
+  const bool wide = cta_rows == 16 && n_items <= sm_count_attn();
   const bool sf = wide && a.split <= kSfTiles * AttnCfg<64>::BNK;
 #define VD_ATTN_TREE_LAUNCH(HD_)                                                                         \
   if (hd == HD_)                                                                                         \
-    return prefill_class ? launch_attn_t<HD_, 4, 1, false, false, true>(kvmap, a, n_items, s)            \
-           : wide        ? launch_attn_wide<HD_, true>(kvmap, a, n_items, sf, s)                         \
-                         : launch_attn_t<HD_, 2, 2, false, false, true>(kvmap, a, n_items, s);
+    return cta_rows == 64   ? launch_attn_t<HD_, 4, 1, false, false, true>(kvmap, a, n_items, s)         \
+           : cta_rows == 32 ? launch_attn_t<HD_, 2, 1, false, false, true>(kvmap, a, n_items, s)         \
+           : wide           ? launch_attn_wide<HD_, true>(kvmap, a, n_items, sf, s)                      \
+                            : launch_attn_t<HD_, 2, 2, false, false, true>(kvmap, a, n_items, s);
   VD_ATTN_TREE_LAUNCH(64)
   VD_ATTN_TREE_LAUNCH(128)
   VD_ATTN_TREE_LAUNCH(256)

@@ -26,7 +26,7 @@
 // kernel; the attention tests check that bitwise.
 //
 // Roles (320 threads; 576 at hd 256): warp 0 allocates TMEM, reads the
-// split's page ids and one lane issues the K/V page copies (3-D TMA boxes of
+// split's page ids and issues the K/V page copies, one per lane (3-D TMA boxes of
 // one page and 64 head dims, so that the K or V of a stage, two tiles, is [hd
 // block][64 keys][64] with the 128-byte swizzle, the canonical operand
 // layout); warp 1, one lane, issues the MMAs; the softmax warps (8, or 16 at
@@ -158,6 +158,11 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
   const int nstage = (ntiles + 1) >> 1;  // K/V stages: tiles 2 g and 2 g + 1 (the latter may be past the end)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Softmax warps that hold a row.  TREE: the others take no part once Q is
+  // loaded (a tree's rows often fill a fraction of the 128, and idle warps'
+  // softmax would slow the others down); their lanes' P is whatever tensor
+  // memory holds, and their O is never read.
+  const int active = TREE ? min(8, (r_end - r0 + 15) / 16) * (C::NSW / 8) * 32 : C::NS;
   // The physical ids of the split's pages (-1 past its tiles or the
   // context), read by one warp in one round trip, so that no copy waits for a
   // page-table load.
@@ -174,8 +179,8 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
       mbar_init(&kv_empty[s], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, C::NS);
-    mbar_init(p_full, C::NS);
+    mbar_init(s_free, active);
+    mbar_init(p_full, active);
     mbar_init(pv_done, 1);
     mbar_init(q_full, C::NS);
     mbar_init(mma_done, 1);
@@ -193,29 +198,27 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
 
   int issued = 0;  // producer: stages whose copies were issued
   if (warp == 0) {
-    if (lane == 0) {
-      for (int g = 0; g < nstage && !*abort_flag; ++g) {
-        const int s = g % C::STAGES;
-        if (g >= C::STAGES && !mbar_wait(&kv_empty[s], ((g / C::STAGES) - 1) & 1, abort_flag, a.status)) break;
-        uint8_t* sk = skv + s * 2 * C::KV_BYTES;
-        uint8_t* sv = sk + C::KV_BYTES;
-        mbar_arrive_expect_tx(&kv_full[s], 2 * C::KV_BYTES);
-#pragma unroll
-        for (int pg = 0; pg < C::SK / 16; ++pg) {
-          const int phys = pid_s[g * (C::SK / 16) + pg];
-          int rk = a.pool_rows, rvw = a.pool_rows;  // outside the pool (past the tiles or the context): zero fill
-          if (phys >= 0) {
-            rk = a.layer_row0 + ((phys * 2) * a.Hkv + kvh) * 16;
-            rvw = rk + a.Hkv * 16;
-          }
-#pragma unroll
-          for (int c = 0; c < C::KB; ++c) {
-            tma_load_3d(sk + c * C::HB + pg * 2048, &kvmap, &kv_full[s], 0, c, rk);
-            tma_load_3d(sv + c * C::HB + pg * 2048, &kvmap, &kv_full[s], 0, c, rvw);
-          }
-        }
-        issued = g + 1;
+    // One box per lane, all of a stage's boxes in one instruction: a single
+    // thread needs about 290 cycles for each, which made the copies' issue the
+    // longest step of a tile (16 boxes every two tiles at hd 128).
+    constexpr int kBoxes = 2 * (C::SK / 16) * C::KB;
+    static_assert(kBoxes <= 32, "one lane per box");
+    const int box_v = lane & 1, box_c = (lane >> 1) % C::KB, box_pg = (lane >> 1) / C::KB;  // K or V, hd block, page
+    for (int g = 0; g < nstage; ++g) {
+      const int s = g % C::STAGES;
+      const bool go = !*abort_flag &&
+                      (g < C::STAGES || mbar_wait(&kv_empty[s], ((g / C::STAGES) - 1) & 1, abort_flag, a.status));
+      if (!__all_sync(0xffffffffu, go)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], 2 * C::KV_BYTES);
+      __syncwarp();
+      if (lane < kBoxes) {
+        const int phys = pid_s[g * (C::SK / 16) + box_pg];
+        // outside the pool (past the tiles or the context): zero fill
+        const int row = phys >= 0 ? a.layer_row0 + ((phys * 2 + box_v) * a.Hkv + kvh) * 16 : a.pool_rows;
+        tma_load_3d(skv + s * 2 * C::KV_BYTES + box_v * C::KV_BYTES + box_c * C::HB + box_pg * 2048, &kvmap, &kv_full[s],
+                    0, box_c, row);
       }
+      issued = g + 1;
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -317,7 +320,8 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status));
     };
     bool ok = true;
-    for (int t = 0; t < ntiles; ++t) {
+    const bool takes_part = !TREE || r0 + lrow0 < r_end;
+    for (int t = 0; takes_part && t < ntiles; ++t) {
       if (!(t & 1)) {  // a new stage's scores
         if (!warp_wait(s_full, (t >> 1) & 1)) {
           ok = false;
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
       tc_fence_before();
       mbar_arrive(p_full);
     }
-    if (ok && warp_wait(pv_done, (ntiles - 1) & 1)) {
+    if (takes_part && ok && warp_wait(pv_done, (ntiles - 1) & 1)) {
       tc_fence_after();
       // ---- split partial of every row that saw a key here
       float* po[2] = {nullptr, nullptr};  // this thread's columns of each stored row

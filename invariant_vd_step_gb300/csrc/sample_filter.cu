@@ -49,7 +49,7 @@ namespace {
 constexpr int kSeg = 1024;        // logits of a segment (one warp: 8 x 4 per lane)
 constexpr int kSegCap = 64;       // list entries per segment
 constexpr int kScanThreads = 256;
-constexpr int kScanCtas = 2;      // resident per SM
+constexpr int kScanCtas = 4;      // resident per SM
 constexpr int kSelThreads = 256;
 constexpr int kBins = 2048;       // exact histogram: counts and masses, by (value, index) order
 constexpr int kCountBins = 4096;  // a wide row's histogram, by value
@@ -265,16 +265,10 @@ inline __host__ size_t space_of(Space* sp, void* base, int R, int nseg, int nchu
 }
 
 // ---------------------------------------------------------------- scan
-// A warp walks over (row, segment) items and loads the next segment while it
-// works on one.  first: the call's first scan launch.  The others depend on no
-// earlier kernel but through it, so they wait for their predecessor at their
-// end: they run next to it, and whatever waits for the last one waits for all.
-template <bool VEC>
-__device__ __forceinline__ void load_seg(float4 (&x)[8], const float* row, int i0, int V) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) x[q] = load4<VEC>(row, i0 + q * 128, V);
-}
-
+// A warp walks over (row, segment) items.  first: the call's first scan launch.
+// The others depend on no earlier kernel but through it, so they wait for
+// their predecessor at their end: they run next to it, and whatever waits for
+// the last one waits for all.
 template <int N, bool VEC>
 __global__ void __launch_bounds__(kScanThreads, kScanCtas)
     filter_scan_kernel(const __grid_constant__ RowParams<N> params, const float* __restrict__ logits, int V,
@@ -286,28 +280,20 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
     for (int r = threadIdx.x; r < rows; r += kScanThreads) sp.params[r0 + r] = params.r[r];
     if (first && threadIdx.x < 3) sp.n_wide[threadIdx.x] = 0;
   }
-  const int items = rows * nseg, step = gridDim.x * (kScanThreads / 32);
-  int item = blockIdx.x * (kScanThreads / 32) + warp;
-  int r = item / nseg, seg = item % nseg;
-  float4 next[8];
-  if (item < items) load_seg<VEC>(next, logits + (r0 + r) * ld, seg * kSeg + lane * 4, V);
-  while (item < items) {
+  const int items = rows * nseg;
+  for (int item = blockIdx.x * (kScanThreads / 32) + warp; item < items; item += gridDim.x * (kScanThreads / 32)) {
+    const int r = item / nseg, seg = item % nseg, row_i = r0 + r, i0 = seg * kSeg + lane * 4;
+    const float* row = logits + row_i * ld;
     float v[8][4];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      v[q][0] = next[q].x;
-      v[q][1] = next[q].y;
-      v[q][2] = next[q].z;
-      v[q][3] = next[q].w;
+      const float4 x = load4<VEC>(row, i0 + q * 128, V);
+      v[q][0] = x.x;
+      v[q][1] = x.y;
+      v[q][2] = x.z;
+      v[q][3] = x.w;
     }
-    const RowParam p = params.r[r];
-    const int row_i = r0 + r, this_seg = seg, i0 = seg * kSeg + lane * 4;
-    const float* row = logits + row_i * ld;
-    item += step;
-    r = item / nseg;
-    seg = item % nseg;
-    if (item < items) load_seg<VEC>(next, logits + (r0 + r) * ld, seg * kSeg + lane * 4, V);
-
+    const RowParam& p = params.r[r];
     const int mode = row_mode(p);
     float lm = -INFINITY;
 #pragma unroll
@@ -330,16 +316,22 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
       race.best = race.best_i == INT_MAX ? -INFINITY : m;
       race.warp_reduce();
     } else if (mode == ROW_FREE) {
+      // each lane's largest logit first: the best of those 32 leaves few others to score
       const Philox ph(p);
+      int at = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) at = v[q][e] == lm ? q * 128 + e : at;
+      if (lm > -INFINITY) race.take(score_of(lm, word_of(ph.block(static_cast<uint32_t>(i0 + at) / 4), at & 3), p.temp), i0 + at);
+      race.warp_reduce();
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const int i = i0 + q * 128;
         const uint4 w = ph.block(static_cast<uint32_t>(i) / 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4; ++e)
           if (i + e < V) race.token(v[q][e], i + e, word_of(w, e), p.temp, c);
-          if (q == 0) race.warp_reduce();  // a bound for the rest of the segment
-        }
       }
       race.warp_reduce();
     } else {
@@ -349,7 +341,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
       // half the groups, down to the maximum alone; if even that repeats too
       // often, nothing is listed.
       out.thr = key_of(m) + 1;
-      uint64_t* list = sp.lists + (static_cast<size_t>(row_i) * nseg + this_seg) * kSegCap;
+      uint64_t* list = sp.lists + (static_cast<size_t>(row_i) * nseg + seg) * kSegCap;
 #pragma unroll 1
       for (int g = groups; g > 0; g >>= 1) {
         float low = lm;
@@ -402,7 +394,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
     }
     out.best = race.best;
     out.best_i = race.best_i;
-    if (lane == 0) sp.segs[static_cast<size_t>(row_i) * nseg + this_seg] = out;
+    if (lane == 0) sp.segs[static_cast<size_t>(row_i) * nseg + seg] = out;
   }
   if (!first) pdl_wait();
 }
@@ -998,7 +990,7 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
   for (int level = 0; level < 2; ++level) {
     uint32_t from = floor;
     if (level == 0) {
-      const int want = min(p.top_k > 0 ? min(p.top_k, 64) : 48, o.nseg);
+      const int want = min(p.top_k > 0 ? p.top_k : 48, o.nseg);
       uint32_t mine = 0;  // the want-th largest segment maximum's key
       for (int i = threadIdx.x; i < o.nseg; i += kSelThreads) {
         int above = 0;

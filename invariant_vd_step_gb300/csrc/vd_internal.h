@@ -178,7 +178,8 @@ int launch_attention(const CUtensorMap& kvmap, const AttnArgs& a, int hd, bool p
 int launch_merge(const MergeArgs& a, int hd, cudaStream_t s);
 // Token trees (a.tree_pos set): the cached tiles that every node of a request
 // shares, as split partials; launch_attention_tc takes them too.
-int launch_attention_tree(const CUtensorMap& kvmap, const AttnArgs& a, int hd, bool prefill_class, int n_items,
+// cta_rows: 16, 32 or 64.
+int launch_attention_tree(const CUtensorMap& kvmap, const AttnArgs& a, int hd, int cta_rows, int n_items,
                           cudaStream_t s);
 // The tiles that differ from node to node: takes up the partial of the split
 // that holds key `cached_len`, folds the node's remaining cached keys and its

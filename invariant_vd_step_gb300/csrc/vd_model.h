@@ -61,7 +61,10 @@ struct Desc {
   // Token trees (vd_tree): the offsets of the tree's own arrays, and its split partials
   bool tree = false;
   int slots = 0, path = 0, path_off = 0, node_seq = 0, parent = 0;
-  int tc_seq = 0, tc_start = 0, n_tc = 0, items_tc = 0;  // requests whose shared tiles run on tcgen05
+  // requests by the CTAs that run their shared tiles: 16, 32 or 64 rows on mma.sync, 128 on tcgen05
+  struct {
+    int seq = 0, start = 0, n = 0, items = 0;
+  } cls[4];
   float *part_o = nullptr, *part_ml = nullptr;
   int part_splits = 0;  // splits per row of the partials
 };
