@@ -133,6 +133,11 @@ int vd::run_tree_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc&
   t.max_splits = a.max_splits;
   t.scale_log2 = a.scale_log2;
   t.status = m->status;
+  t.blk_seq = d.base + d.blk_seq;
+  t.blk_first = d.base + d.blk_first;
+  t.n_blk = d.n_blk;
+  t.npg = d.npg;
+  t.tail_rows = d.tail_rows;
   if ((rc = launch_tree_tail(t, hd, s))) return rc;
   MergeArgs g{};
   g.part_o = d.part_o;
@@ -267,6 +272,13 @@ int vd_tree_plan(vd_tree* t, vd_kv_pool* pool, const vd_tree_batch* b, void* str
     k.seq = take(B);
     k.start = take(B + 1);
   }
+  for (int i = 0; i < B; ++i)
+    d.tail_rows = std::max(d.tail_rows, b->cached_len[i] % m->key_tile + b->cu_nodes[i + 1] - b->cu_nodes[i]);
+  int per_blk = 1;
+  d.npg = tree_nodes_per_warp(c.head_dim, T, c.n_kv_heads, m->G, d.tail_rows, m->n_sm, &per_blk);
+  for (int i = 0; i < B; ++i) d.n_blk += (b->cu_nodes[i + 1] - b->cu_nodes[i] + per_blk - 1) / per_blk;
+  d.blk_seq = take(d.n_blk);
+  d.blk_first = take(d.n_blk);
   d.path = take(paths);
   d.page_table = take(static_cast<size_t>(B) * stride);
   if (off > (1u << 30)) return fail(VD_ERR_CAPACITY, "plan too large");
@@ -287,7 +299,7 @@ int vd_tree_plan(vd_tree* t, vd_kv_pool* pool, const vd_tree_batch* b, void* str
   t->planned = false;  // until the new plan is on its way
   if ((rc = grow(&t->dev, &t->dev_cap, off)) || (rc = grow(&t->part, &t->part_cap, rows * (c.head_dim + 2)))) return rc;
   int* h = t->host[slot];
-  int npath = 0;
+  int npath = 0, nblk = 0;
   auto items = [&](int nodes, int shared, int rows_per_cta) {
     const int r = nodes * m->G, nsplit = shared > 0 ? (shared - 1) / m->split + 1 : 0;
     return (r + rows_per_cta - 1) / rows_per_cta * c.n_kv_heads * nsplit;
@@ -322,6 +334,10 @@ int vd_tree_plan(vd_tree* t, vd_kv_pool* pool, const vd_tree_batch* b, void* str
     }
     h[d.cu_q + i] = n0;
     h[d.cached + i] = cached;
+    for (int k = 0; k < n; k += per_blk, ++nblk) {
+      h[d.blk_seq + nblk] = i;
+      h[d.blk_first + nblk] = k;
+    }
     // the request's class, by its rows
     const int shared = cached / m->key_tile * m->key_tile, r = n * m->G;
     const bool tc = m->prefill_kernel == 0 && attn_tc_supported(c.head_dim);

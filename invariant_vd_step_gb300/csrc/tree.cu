@@ -27,6 +27,16 @@ namespace {
 // layout of a TMA-staged tile.
 constexpr int kTailWarps = 4;
 
+// Whether a bounded wait of this step has given up; one read for the whole
+// CTA keeps its exit uniform.
+__device__ __forceinline__ bool skip_step(int* status) {
+  __shared__ int skip;
+  if (threadIdx.x == 0) skip = status ? *reinterpret_cast<volatile int*>(status) : 0;
+  __syncthreads();
+  return skip != 0;
+}
+
+
 template <int HD, int DS>
 __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(TreeTailArgs a) {
   using C = AttnCfg<HD>;
@@ -37,6 +47,7 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(TreeTailArgs
   const int group = warp / DS, part = warp % DS, gl = part * 32 + lane;
   uint8_t* sk = smem + group * 2 * C::TILE_BYTES;
   uint8_t* sv = sk + C::TILE_BYTES;
+  if (skip_step(a.status)) return;
   auto group_sync = [&] {
     if constexpr (DS == 1) __syncwarp();
     else asm volatile("barrier.sync %0, %1;" ::"r"(1 + group), "r"(DS * 32) : "memory");  // not .aligned: per thread
@@ -51,7 +62,6 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(TreeTailArgs
   const int shared = c / C::BNK * C::BNK;
   pdl_wait();
   pdl_trigger();
-  if (a.status && *reinterpret_cast<volatile int*>(a.status)) return;  // the same for the whole group
 
   const int G = a.Hq / a.Hkv, gq = lane >> 2, t4 = lane & 3, dim0 = part * ND;
   const bool lower8 = G <= 8;
@@ -150,6 +160,224 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(TreeTailArgs
   store(p / a.split);
 }
 
+// The same with the rows staged once per CTA, for trees whose tail fits shared
+// memory.  A CTA owns a block of nodes of one (request, KV head) and copies the
+// cached keys past the shared tiles and every node's K and V into rows of its
+// own (16-byte chunks swizzled within 128 bytes).  A warp (DS of them, each with
+// its part of the head dimension) folds up to 16 / G nodes at once, their query
+// heads as the 16 rows of an mma tile: scores and P V are one chain of
+// instructions per node, on K and V rows gathered by ldmatrix address from the
+// node's path, with the other nodes' rows ignored in the scores and zero in P
+// (they add nothing to O); softmax, rescale and state are shared.  16-key
+// halves of a tile in which a node sees no key are left out: zeros again.
+// Bound by the instruction issue of the chains: at 16384 nodes x heads of 4
+// rows, one node per warp took 1886 warp instructions a node.
+template <int HD>
+struct Staged {
+  static constexpr int ROW = HD * 2;  // bytes of a K or V row
+  static constexpr size_t bytes(int tail_rows) { return 128 + static_cast<size_t>(tail_rows) * 2 * ROW; }
+  __device__ static __forceinline__ uint32_t off(int row, int chunk) {
+    return row * ROW + ((chunk & ~7) << 4) + (((chunk & 7) ^ (row & 7)) << 4);
+  }
+};
+constexpr size_t kStagedBytes = 100 * 1024;  // two CTAs share an SM
+
+template <int HD, int DS>
+__global__ void __launch_bounds__(kTailWarps * 32, 2) tree_tail_staged_kernel(TreeTailArgs a) {
+  using S = Staged<HD>;
+  constexpr int BNK = 32, CH = HD / 8, ND = HD / DS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int row_s[kTailWarps][16][BNK];  // a tile's staged rows, of each node of a warp
+  if (skip_step(a.status)) return;
+  uint8_t* smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int dim0 = (warp % DS) * ND, gq = lane >> 2, t4 = lane & 3;
+  const int mi = lane >> 3, r8 = lane & 7;
+  // ---- item -> (request, block of nodes), KV head; the description was written before the step's first kernel
+  const int item = blockIdx.x, kvh = blockIdx.y;
+  const int b = a.blk_seq[item], n0 = a.cu_q[b], nodes = a.cu_q[b + 1] - n0, c = a.cached_len[b];
+  const int G = a.Hq / a.Hkv;
+  const int first = a.blk_first[item] + (warp / DS) * a.npg;  // this warp's first node
+  const int count = max(0, min(a.npg, nodes - first));
+  const int* table = a.page_table + static_cast<size_t>(b) * a.pt_stride;
+  const int shared = c / BNK * BNK, rows = c - shared + nodes;  // staged row i: slot shared + i
+  const uint32_t sk = smem_u32(smem), sv = sk + rows * S::ROW;
+  int node[2], pos[2], lo[2];
+  bool valid[2];
+  size_t out_row[2];  // of the row in q, and times max_splits in the partials
+  int p_max = -1, lo_min = INT_MAX;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int i = gq + 8 * r;
+    node[r] = i / G;
+    valid[r] = node[r] < count;
+    const int t = n0 + first + (valid[r] ? node[r] : 0);
+    const int p = valid[r] ? a.positions[t] : -1;
+    pos[r] = p;
+    lo[r] = valid[r] ? (a.window > 0 ? max(0, p - a.window + 1) : 0) : 1;
+    out_row[r] = static_cast<size_t>(t) * a.Hq + kvh * G + i % G;
+    p_max = max(p_max, p);
+    if (valid[r]) lo_min = min(lo_min, lo[r]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    p_max = max(p_max, __shfl_xor_sync(0xffffffffu, p_max, o));
+    lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
+  }
+  // lane n of the warp knows node n
+  const int my_t = n0 + first + min(lane, max(count - 1, 0));
+  const int my_p = lane < count ? a.positions[my_t] : -1, my_path = lane < count ? a.path_off[my_t] : 0;
+  pdl_wait();
+  pdl_trigger();
+  for (int i = threadIdx.x; i < rows * CH; i += kTailWarps * 32) {
+    const int r = i / CH, ch = i % CH, slot = shared + r;
+    const size_t row = (static_cast<size_t>(table[slot >> 4]) * 2 * a.Hkv + kvh) * 16 + (slot & 15);
+    const __nv_bfloat16* src = a.pool + row * HD + ch * 8;
+    cp_async16(smem + S::off(r, ch), src);
+    cp_async16(smem + rows * S::ROW + S::off(r, ch), src + static_cast<size_t>(a.Hkv) * 16 * HD);
+  }
+  uint32_t qf[HD / 16][4];
+  RowState<ND> st;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const __nv_bfloat16* qr = a.q + out_row[r] * HD;
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+      qf[kk][r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + t4 * 2) : 0u;
+      qf[kk][2 + r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8 + t4 * 2) : 0u;
+    }
+    // the state of the split that the shared tiles began
+    const bool begun = valid[r] && max(lo[r], shared / a.split * a.split) < shared;
+    const size_t at = out_row[r] * a.max_splits + shared / a.split;
+    st.m[r] = begun ? a.part_ml[at * 2] : -INFINITY;
+    st.l[r] = begun ? a.part_ml[at * 2 + 1] : 0.f;
+    const float* po = a.part_o + at * HD + dim0;
+#pragma unroll
+    for (int n = 0; n < ND / 8; ++n) {
+      const float2 v = begun ? *reinterpret_cast<const float2*>(po + n * 8 + t4 * 2) : make_float2(0.f, 0.f);
+      st.o[n][2 * r] = v.x;
+      st.o[n][2 * r + 1] = v.y;
+    }
+  }
+  cp_async_wait_all();
+  __syncthreads();  // the rows have landed, and every warp of a node has its state before one stores another
+  if (count == 0) return;
+  auto store = [&](int r, int split) {
+    const size_t at = out_row[r] * a.max_splits + split;
+    if (t4 == 0 && dim0 == 0) {
+      a.part_ml[at * 2] = st.m[r];
+      a.part_ml[at * 2 + 1] = st.l[r];
+    }
+    float* po = a.part_o + at * HD + dim0;
+#pragma unroll
+    for (int n = 0; n < ND / 8; ++n)
+      *reinterpret_cast<float2*>(po + n * 8 + t4 * 2) = make_float2(st.o[n][2 * r], st.o[n][2 * r + 1]);
+  };
+  int key0 = max(shared, lo_min / BNK * BNK);
+  for (; key0 <= p_max; key0 += BNK) {
+    if (key0 != shared && key0 % a.split == 0) {  // the previous split is complete
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (valid[r] && max(lo[r], key0 - a.split) <= min(pos[r], key0 - 1)) store(r, key0 / a.split - 1);
+        st.m[r] = -INFINITY;
+        st.l[r] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < ND / 8; ++n) st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
+    }
+    // ---- scores: each node's on its own keys
+    float s[BNK / 8][4];
+#pragma unroll
+    for (int j = 0; j < BNK / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+    // the row of each node's key at key0 + lane: a cached slot's, or that of the path's node at that position
+    const int key = key0 + lane;
+    __syncwarp();
+#pragma unroll 4
+    for (int n = 0; n < count; ++n) {
+      const int p = __shfl_sync(0xffffffffu, my_p, n), path = __shfl_sync(0xffffffffu, my_path, n);
+      row_s[warp][n][lane] = key < c ? key - shared : c - shared + (key <= p ? a.path[path + key - c] : first + n);
+    }
+    __syncwarp();
+    for (int n = 0; n < count; ++n) {
+      const int p = __shfl_sync(0xffffffffu, my_p, n);
+      if (p < key0) continue;
+      const bool both = p >= key0 + 16;
+#pragma unroll
+      for (int jp = 0; jp < BNK / 16; ++jp) {
+        if (jp == 1 && !both) continue;
+        const int kr = row_s[warp][n][jp * 16 + (mi >> 1) * 8 + r8];
+        float x[2][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[0][e] = x[1][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          uint32_t f[4];
+          ldmatrix_x4(f, sk + S::off(kr, kk * 2 + (mi & 1)));
+          mma_bf16_16816(x[0], qf[kk], f);
+          mma_bf16_16816(x[1], qf[kk], f + 2);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[2 * jp + j][e] = node[e >> 1] == n ? x[j][e] : s[2 * jp + j][e];
+      }
+    }
+    // ---- softmax of the tile, all rows
+    float mx[2], mnew[2], alpha[2], rs[2];
+    bool rv[2];
+    uint32_t pa[BNK / 16][4], pl[BNK / 16][4];
+    tile_mask_max<BNK, false>(s, mx, key0, pos, lo, a.scale_log2, lane);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) tile_running_max(st.m[r], mx[r], mnew[r], alpha[r], rv[r]);
+    tile_probs<BNK, false>(s, mnew, pa, pl, rs);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      tile_update_l(st.l[r], alpha[r], rs[r], rv[r]);
+      st.m[r] = mnew[r];
+    }
+    tile_rescale<ND, false>(st.o, alpha);
+    // ---- P V: each node's rows of P on its own values
+    for (int n = 0; n < count; ++n) {
+      const int p = __shfl_sync(0xffffffffu, my_p, n);
+      if (p < key0) continue;
+      const bool both = p >= key0 + 16;
+#pragma unroll
+      for (int ks = 0; ks < BNK / 16; ++ks) {
+        if (ks == 1 && !both) continue;
+        const int vr = row_s[warp][n][ks * 16 + (mi & 1) * 8 + r8];
+        uint32_t ph[4], pw[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ph[e] = node[e & 1] == n ? pa[ks][e] : 0u;
+          pw[e] = node[e & 1] == n ? pl[ks][e] : 0u;
+        }
+#pragma unroll
+        for (int np = 0; np < ND / 16; ++np) {
+          uint32_t f[4];
+          ldmatrix_x4_trans(f, sv + S::off(vr, dim0 / 8 + np * 2 + (mi >> 1)));
+          mma_bf16_16816(st.o[2 * np], ph, f);
+          mma_bf16_16816(st.o[2 * np], pw, f);
+          mma_bf16_16816(st.o[2 * np + 1], ph, f + 2);
+          mma_bf16_16816(st.o[2 * np + 1], pw, f + 2);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r)  // rows whose last split is the one just folded (the others' are stored)
+    if (valid[r] && pos[r] / a.split == (key0 - BNK) / a.split) store(r, pos[r] / a.split);
+}
+
+template <int HD>
+int launch_tail_staged(const TreeTailArgs& a, cudaStream_t s) {
+  constexpr int DS = HD == 256 ? 2 : 1;
+  const size_t smem = Staged<HD>::bytes(a.tail_rows);
+  VD_CUDA_TRY(cudaFuncSetAttribute(tree_tail_staged_kernel<HD, DS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(smem)));
+  VD_CUDA_TRY(launch_k(tree_tail_staged_kernel<HD, DS>, dim3(a.n_blk, a.Hkv), dim3(kTailWarps * 32), smem, s, a));
+  return VD_OK;
+}
+
 template <int HD, int DS>
 int launch_tail_t(const TreeTailArgs& a, cudaStream_t s) {
   using C = AttnCfg<HD>;
@@ -173,6 +401,7 @@ constexpr int kAcceptBatch = 8;  // nodes read before their copies are written
 
 __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(TreeAcceptArgs a) {
   extern __shared__ int next[];  // [nodes] the child the path goes on to, then the path itself
+  if (skip_step(a.status)) return;
   const int b = blockIdx.x, layer = blockIdx.y;
   const int n0 = a.cu_q[b], n = a.cu_q[b + 1] - n0, c = a.cached_len[b];
   int* path = next + n;
@@ -181,7 +410,6 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(TreeAcceptA
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  if (a.status && *reinterpret_cast<volatile int*>(a.status)) return;
   for (int i = threadIdx.x; i < n; i += kAcceptThreads) {
     const int p = a.parent[n0 + i];
     if (p >= 0 && a.tokens[n0 + i] == a.choices[n0 + p]) atomicMin(&next[p], i);
@@ -221,8 +449,27 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(TreeAcceptA
 
 }  // namespace
 
+// Nodes that a warp folds at once: one while the launch has warps to spare (a
+// node's chains are then the latency), up to 16 / G.  0: the tail does not fit.
+int tree_nodes_per_warp(int hd, int nodes, int Hkv, int G, int tail_rows, int n_sm, int* blk_nodes) {
+  const size_t bytes = hd == 64 ? Staged<64>::bytes(tail_rows)
+                       : hd == 128 ? Staged<128>::bytes(tail_rows) : Staged<256>::bytes(tail_rows);
+  *blk_nodes = 1;
+  if (bytes > kStagedBytes) return 0;
+  const int groups = kTailWarps / (hd == 256 ? 2 : 1);
+  const long long each = (static_cast<long long>(nodes) * Hkv - 1) / (2LL * n_sm * groups) + 1;
+  const int npg = static_cast<int>(each < 16 / G ? each : 16 / G);
+  *blk_nodes = groups * npg;
+  return npg;
+}
+
 int launch_tree_tail(const TreeTailArgs& a, int hd, cudaStream_t s) {
   if (a.T <= 0) return VD_OK;
+  if (a.npg > 0) {
+    if (hd == 64) return launch_tail_staged<64>(a, s);
+    if (hd == 128) return launch_tail_staged<128>(a, s);
+    if (hd == 256) return launch_tail_staged<256>(a, s);
+  }
   if (hd == 64) return launch_tail_t<64, 1>(a, s);
   if (hd == 128) return launch_tail_t<128, 1>(a, s);
   if (hd == 256) return launch_tail_t<256, 2>(a, s);

@@ -199,7 +199,13 @@ struct TreeTailArgs {
   int T, Hq, Hkv, pt_stride, window, split, max_splits;
   float scale_log2;
   int* status;
+  const int* blk_seq;         // [n_blk] blocks of nodes: request, first node
+  const int* blk_first;
+  int n_blk;
+  int npg;                    // nodes that a warp folds at once; 0: one node per warp, rows gathered from the pool
+  int tail_rows;              // most (cached keys past the shared tiles + nodes) of a request
 };
+int tree_nodes_per_warp(int hd, int nodes, int Hkv, int G, int tail_rows, int n_sm, int* blk_nodes);
 int launch_tree_tail(const TreeTailArgs& a, int hd, cudaStream_t s);
 struct TreeAcceptArgs {
   const int* tokens;          // [T] token of each node

@@ -61,6 +61,7 @@ struct Desc {
   // Token trees (vd_tree): the offsets of the tree's own arrays, and its split partials
   bool tree = false;
   int slots = 0, path = 0, path_off = 0, node_seq = 0, parent = 0;
+  int blk_seq = 0, blk_first = 0, n_blk = 0, npg = 0, tail_rows = 0;  // blocks of nodes of the tail kernel
   // requests by the CTAs that run their shared tiles: 16, 32 or 64 rows on mma.sync, 128 on tcgen05
   struct {
     int seq = 0, start = 0, n = 0, items = 0;
