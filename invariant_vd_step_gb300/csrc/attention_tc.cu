@@ -118,8 +118,12 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* pid_s = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(kv_full) + 256);  // [PIDS]
 
-  pdl_wait();
-  pdl_trigger();
+  // TREE: up to its wait, which comes with the page ids, the CTA reads only the
+  // status word and the step's description (as attention.cu's decode CTAs).
+  if (!TREE) {
+    pdl_wait();
+    pdl_trigger();
+  }
   {
     __shared__ int skip;  // one read for the whole CTA keeps the exit uniform
     if (threadIdx.x == 0) skip = a.status ? *reinterpret_cast<volatile int*>(a.status) : 0;
@@ -130,6 +134,14 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
   const int item = blockIdx.x;
   if (item >= a.cls_start[a.n_cls]) return;
   int lo_i = 0, hi_i = a.n_cls - 1;
+  if (TREE) {  // last j with cls_start[j] <= item: 32 of them per memory round trip
+    while (lo_i < hi_i) {
+      const int step = (hi_i - lo_i) / 32 + 1, j = lo_i + (static_cast<int>(threadIdx.x) & 31) * step;
+      const unsigned at = __ballot_sync(0xffffffffu, j <= hi_i && a.cls_start[j] <= item);  // lane 0 always
+      lo_i += (31 - __clz(at)) * step;
+      hi_i = min(hi_i, lo_i + step - 1);
+    }
+  }
   while (lo_i < hi_i) {
     const int mid = (lo_i + hi_i + 1) >> 1;
     if (a.cls_start[mid] <= item) lo_i = mid; else hi_i = mid - 1;
@@ -162,7 +174,14 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
   // loaded (a tree's rows often fill a fraction of the 128, and idle warps'
   // softmax would slow the others down); their lanes' P is whatever tensor
   // memory holds, and their O is never read.
-  const int active = TREE ? min(8, (r_end - r0 + 15) / 16) * (C::NSW / 8) * 32 : C::NS;
+  // A CTA of at most 64 rows spreads them: 16 to each of the four 32-lane
+  // quarters of tensor memory, so that all of a quarter's softmax warps hold the
+  // same 16 rows and share O's columns (the rescale before every P V, the
+  // longest step of a tile, gets that much shorter).
+  const bool spread = TREE && r_end - r0 <= 64;
+  const int active = !TREE    ? C::NS
+                     : spread ? (r_end - r0 + 15) / 16 * (C::NSW / 4) * 32
+                              : min(8, (r_end - r0 + 15) / 16) * (C::NSW / 8) * 32;
   // The physical ids of the split's pages (-1 past its tiles or the
   // context), read by one warp in one round trip, so that no copy waits for a
   // page-table load.
@@ -173,6 +192,10 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
       pid_s[j] = (j < ntiles * (C::BNK / 16) && lp * 16 < kv_len)
                      ? a.page_table[static_cast<size_t>(b) * a.pt_stride + lp] : -1;
     }
+  if (TREE) {
+    pdl_wait();
+    pdl_trigger();
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&kv_full[s], 1);
@@ -279,8 +302,8 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
 #pragma unroll
       for (int i = 0; i < C::ROWS * CH / C::NS; ++i) {
         const int idx = st + i * C::NS, qr = idx / CH, c16 = idx % CH;
-        const int row = r0 + qr;
-        const bool valid = row < rows;
+        const int row = r0 + (spread ? (qr >> 5) * 16 + (qr & 15) : qr);
+        const bool valid = row < rows && !(spread && (qr & 16));
         const int tok = row / G, hq = kvh * G + row % G;
         const uint4* qs = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD);
         const uint4 v = valid ? qs[c16] : make_uint4(0u, 0u, 0u, 0u);
@@ -289,10 +312,14 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     }
-    const int lrow0 = 32 * (warp & 3) + 16 * (((warp - 2) >> 2) & 1);  // first CTA row of this warp
-    const int ocol = C::O_COL + 128 * ((warp - 2) >> 3);             // first O column of this warp
-    const bool writes_p = warp - 2 < 8;                              // one warp of a pair writes P and m, l
-    const uint32_t frag = tmem + (static_cast<uint32_t>(lrow0) << 16);
+    constexpr int OWS = HD / (C::NSW / 4);  // O columns per softmax warp of a spread CTA
+    const int quarter = 32 * (warp & 3), k4 = (warp - 2) >> 2;
+    const int lane0 = quarter + (spread ? 0 : 16 * (k4 & 1));          // first TMEM lane of this warp's rows
+    const int lrow0 = spread ? 16 * (warp & 3) : lane0;                // first CTA row of this warp
+    const int ocol = C::O_COL + (spread ? OWS * k4 : 128 * (k4 >> 1));  // first O column of this warp
+    const int ochunks = (spread ? OWS : C::OW) / 32;                    // 32-column blocks of O it owns
+    const bool writes_p = spread ? k4 == 0 : k4 < 2;                    // one of the warps that share rows writes P and m, l
+    const uint32_t frag = tmem + (static_cast<uint32_t>(lane0) << 16);
     const int gq = lane >> 2, t4 = lane & 3;
     int pos[2], lo[2], tok[2], hq[2];
     bool valid[2];
@@ -310,7 +337,8 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
 #pragma unroll
       for (int i = 0; i < 16; ++i) z[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < C::OW / 32; ++c) tmem_st16x4(frag + ocol + 32 * c, z);
+      for (int c = 0; c < C::OW / 32; ++c)
+        if (!TREE || c < ochunks) tmem_st16x4(frag + ocol + 32 * c, z);
       tmem_wait_st();
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -420,6 +448,7 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
         if (!__all_sync(0xffffffffu, alpha[0] == 1.0f && alpha[1] == 1.0f)) {
 #pragma unroll
           for (int c = 0; c < C::OW / 32; ++c) {
+            if (TREE && c >= ochunks) break;
             float o[16];
             tmem_ld16x4(frag + ocol + 32 * c, o);
 #pragma unroll
@@ -448,6 +477,7 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
       }
 #pragma unroll
       for (int c = 0; c < C::OW / 32; ++c) {
+        if (TREE && c >= ochunks) break;
         float o[16];
         tmem_ld16x4(frag + ocol + 32 * c, o);
 #pragma unroll
