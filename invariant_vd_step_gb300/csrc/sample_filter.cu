@@ -55,8 +55,10 @@ constexpr int kBins = 2048;       // exact histogram: counts and masses, by (val
 constexpr int kCountBins = 4096;  // a wide row's histogram, by value
 constexpr float kBinNats = 24.f;  // its range below the largest logit, in units of T
 constexpr int kList = 2048;       // candidates that a CTA sorts
+constexpr int kListBins = 1024;   // an unsorted list's bins of value
+constexpr int kCutList = 512;     // candidates of the cut's bin
 constexpr int kChunk = 8192;      // unit of a wide row's work items
-constexpr int kScanRows = 120;    // rows of a scan launch: their parameters fit 4 KB
+constexpr int kScanRows = 512;    // rows of a scan launch (their parameters travel with it: 32 bytes each)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMassScale = 68719476736.f;  // 2^36
 
@@ -408,7 +410,13 @@ struct SelShared {
     uint32_t count[kCountBins];
     struct {
       uint64_t comp[kList];
-      uint64_t pre[kList];  // masses up to and including each
+      union {
+        uint64_t pre[kList];  // masses up to and including each
+        struct {              // or, for an unsorted list: bins of value, and the cut's bin
+          uint32_t cnt[kListBins], lo[kListBins], hi[kListBins];
+          uint64_t cut[kCutList];
+        } b;
+      };
     } l;
   };
   uint64_t redu[kSelThreads / 32];
@@ -927,6 +935,123 @@ __device__ __noinline__ void exact_row(SelShared& sh, const Out& o, int r, const
 }
 
 // ---------------------------------------------------------------- select
+// The race over the list's tokens of comp >= cut and value >= least.
+__device__ void score_list(const SelShared& sh, const RowParam& p, int n, uint64_t cut, float least, Race& race) {
+  const Philox ph(p);
+  for (int j = threadIdx.x; j < n; j += kSelThreads) {
+    const uint64_t cp = sh.l.comp[j];
+    const float l = value_of(static_cast<uint32_t>(cp >> 32));
+    if (cp < cut || l < least) continue;
+    const int i = index_of(cp);
+    race.take(score_of(l, word_of(ph.block(static_cast<uint32_t>(i) / 4), i & 3), p.temp), i);
+  }
+}
+
+// A row without top-k by its unsorted list of n tokens, every one at or above
+// `bottom`: true if that decides it.  top-p's cut is found in 1024 bins of
+// value (their masses as integers); only the cut's bin is sorted.  An undecided
+// row leaves the best score of the listed tokens, all of them kept, in `best`.
+__device__ __noinline__ bool cut_unsorted(SelShared& sh, const Out& o, int r, const RowParam& p, int n, float top,
+                                          float bottom, uint64_t z, bool complete, bool wide_next, Race& best) {
+  const bool has_p = p.top_p < 1.f;
+  const float least = min_p_least(p, top);
+  uint64_t mass = 0;
+  int below = 0;  // listed tokens that min-p drops
+  for (int j = threadIdx.x; j < n; j += kSelThreads) {
+    mass += fixed(weight_of(sh.l.comp[j], top, p.temp));
+    below += value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32)) < least;
+  }
+  mass = block_sum(sh, mass);
+  below = block_sum(sh, below);
+  const uint64_t want = has_p ? share_of(p.top_p, z) : 0;
+  if (!complete && below == 0 && (!has_p || mass < want)) {
+    if (wide_next) {
+      score_list(sh, p, n, 0, least, best);
+      block_best(sh, best);
+    }
+    return false;
+  }
+  uint64_t cut = 0;  // the lowest kept comp
+  if (has_p && mass >= want) {
+    auto& b = sh.l.b;
+    const float scale = __fdiv_rn(static_cast<float>(kListBins - 1), __fsub_rn(top, bottom));
+    auto bin = [&](uint64_t cp) {
+      const float l = value_of(static_cast<uint32_t>(cp >> 32));
+      const float d = l == top ? 0.f : __fmul_rn(__fsub_rn(top, l), scale);
+      return d < static_cast<float>(kListBins - 1) ? static_cast<int>(d) : kListBins - 1;
+    };
+    for (int i = threadIdx.x; i < kListBins; i += kSelThreads) b.cnt[i] = b.lo[i] = b.hi[i] = 0;
+    if (threadIdx.x == 0) sh.in_n = 0;
+    __syncthreads();
+    for (int j = threadIdx.x; j < n; j += kSelThreads) {
+      const uint64_t w = fixed(weight_of(sh.l.comp[j], top, p.temp));
+      const int i = bin(sh.l.comp[j]);
+      const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&b.lo[i], wl);
+      const uint32_t up = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
+      if (up) atomicAdd(&b.hi[i], up);
+      atomicAdd(&b.cnt[i], 1u);
+    }
+    __syncthreads();
+    constexpr int PT = kListBins / kSelThreads;
+    const int b0 = threadIdx.x * PT, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t m = 0;
+#pragma unroll
+    for (int k = 0; k < PT; ++k) m += b.lo[b0 + k] + (static_cast<uint64_t>(b.hi[b0 + k]) << 32);
+    uint64_t am = m;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const uint64_t x = __shfl_up_sync(0xffffffffu, am, s);
+      if (lane >= s) am += x;
+    }
+    if (lane == 31) sh.redu[warp] = am;
+    __syncthreads();
+    am -= m;
+    for (int w = 0; w < warp; ++w) am += sh.redu[w];
+    int last = -1;  // the last bin before which the mass is below the share (bin 0 holds the largest token)
+    uint64_t last_m = 0;
+#pragma unroll
+    for (int k = 0; k < PT; ++k) {
+      if (b.cnt[b0 + k] && (b0 + k == 0 || am < want)) {
+        last = b0 + k;
+        last_m = am;
+      }
+      am += b.lo[b0 + k] + (static_cast<uint64_t>(b.hi[b0 + k]) << 32);
+    }
+    const int cut_bin = block_max(sh, last);
+    if (last == cut_bin) sh.above_mass = last_m;
+    __syncthreads();
+    uint64_t before = sh.above_mass;
+    for (int j = threadIdx.x; j < n; j += kSelThreads)
+      if (bin(sh.l.comp[j]) == cut_bin) {
+        const uint32_t at = atomicAdd(&sh.in_n, 1u);
+        if (at < kCutList) b.cut[at] = sh.l.comp[j];
+      }
+    __syncthreads();
+    const int in = static_cast<int>(sh.in_n);
+    if (in > kCutList) return false;  // ties: the wide kernels or the exact histograms
+    // a token of the bin is kept if the masses before it (those of larger comp) stay below the share
+    uint64_t lowest = ~0ull;
+    for (int j = threadIdx.x; j < in; j += kSelThreads) {
+      const uint64_t mine = b.cut[j];
+      uint64_t ahead = before;
+      for (int k = 0; k < in; ++k)
+        if (b.cut[k] > mine) ahead += fixed(weight_of(b.cut[k], top, p.temp));
+      if ((ahead < want || ahead == 0) && mine < lowest) lowest = mine;
+    }
+    cut = block_reduce(lowest, sh.redu, [](uint64_t x, uint64_t y) { return x < y ? x : y; });
+  }
+  uint64_t kept = 0;
+  Race race;
+  for (int j = threadIdx.x; j < n; j += kSelThreads) {
+    const uint64_t cp = sh.l.comp[j];
+    if (cp >= cut && value_of(static_cast<uint32_t>(cp >> 32)) >= least) kept += fixed(weight_of(cp, top, p.temp));
+  }
+  kept = block_sum(sh, kept);
+  score_list(sh, p, n, cut, least, race);
+  choose(sh, o, r, p, 0, race, kept, top, false);
+  return true;
+}
+
 // wide_next: the count and collect kernels follow, and take rows that the
 // lists do not decide.
 template <bool VEC>
@@ -1057,6 +1182,11 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     const int n = sh.n;
     if (n > kList || n == 0) continue;  // too many candidates, or none listed (ties)
     const bool complete = all && from == floor;
+    if (level == 1 && p.top_k == 0) {  // top-p and min-p alone need no order but at the cut
+      const bool done = cut_unsorted(sh, o, r, p, n, top, value_of(floor), z, complete, wide_next, listed);
+      if (done) return;
+      continue;
+    }
     sort_desc(sh.l.comp, n);
     prefix_mass(sh, n, top, p.temp, 0);
     const int lim = p.top_k > 0 ? min(p.top_k, n) : n;
@@ -1072,14 +1202,8 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     kept = block_sum(sh, kept);
     const bool decided = complete || kept < n || (p.top_k > 0 && p.top_k <= n) || (has_p && sh.l.pre[lim - 1] >= share);
     if (!decided) {
-      if (level == 1 && wide_next && !(p.top_k > 0 && has_p)) {  // every listed token is kept
-        const Philox ph(p);
-        for (int j = threadIdx.x; j < n; j += kSelThreads) {
-          const uint64_t cp = sh.l.comp[j];
-          const int i = index_of(cp);
-          listed.take(score_of(value_of(static_cast<uint32_t>(cp >> 32)),
-                                   word_of(ph.block(static_cast<uint32_t>(i) / 4), i & 3), p.temp), i);
-        }
+      if (level == 1 && wide_next && !has_p) {  // every listed token is kept
+        score_list(sh, p, n, 0, -INFINITY, listed);
         block_best(sh, listed);
       }
       continue;
@@ -1437,7 +1561,8 @@ int launch_sample_filter(const SampleFilterArgs& a, cudaStream_t s) {
   for (int r0 = 0; r0 < a.R; r0 += each) {
     const int rows = std::min(each, a.R - r0);
     rc = rows <= 16 ? launch_scan<16>(a, sp, o.nseg, r0, rows, vec, &wide, s)
-                    : launch_scan<kScanRows>(a, sp, o.nseg, r0, rows, vec, &wide, s);
+         : rows <= 120 ? launch_scan<120>(a, sp, o.nseg, r0, rows, vec, &wide, s)
+                       : launch_scan<kScanRows>(a, sp, o.nseg, r0, rows, vec, &wide, s);
     if (rc) return rc;
   }
   return vec ? launch_decide<true>(o, sp, a.R, wide, s) : launch_decide<false>(o, sp, a.R, wide, s);
