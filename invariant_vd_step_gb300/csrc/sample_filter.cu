@@ -20,7 +20,7 @@
 //
 // A row whose cut lies below the lists (flat distributions, logits sorted
 // along the vocabulary) is "wide".  Two more kernels, whose CTAs take (wide
-// row, chunk of 8192) items, read it again:
+// row, part of it) items, read it again:
 //
 //   count    a histogram of 4096 bins of value, tokens and their mean place in
 //            the bin; the last CTA of a row estimates each bin's mass from
@@ -53,11 +53,12 @@ constexpr int kScanCtas = 4;      // resident per SM
 constexpr int kSelThreads = 256;
 constexpr int kBins = 2048;       // exact histogram: counts and masses, by (value, index) order
 constexpr int kCountBins = 4096;  // a wide row's histogram, by value
-constexpr float kBinNats = 24.f;  // its range below the largest logit, in units of T
+constexpr float kBinNats = 24.f;  // its range below the largest logit at most, in units of T
 constexpr int kList = 2048;       // candidates that a CTA sorts
 constexpr int kListBins = 1024;   // an unsorted list's bins of value
 constexpr int kCutList = 512;     // candidates of the cut's bin
-constexpr int kChunk = 8192;      // unit of a wide row's work items
+constexpr int kChunk = 4096;      // a wide row's work item has this many tokens or more
+constexpr int kCountTurn = 8192;  // tokens that the packed counters of `count` hold
 constexpr int kScanRows = 512;    // rows of a scan launch (their parameters travel with it: 32 bytes each)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMassScale = 68719476736.f;  // 2^36
@@ -225,6 +226,7 @@ struct __align__(16) WideState {
   uint32_t arrived[2];   // CTAs done, per kernel
   int n;                 // tokens listed
   float bound;           // a score that some kept token has: only tokens that reach it matter
+  float range;           // of the bins of `count`, down from `top`
 };
 struct __align__(16) ChunkOut {
   uint64_t mass;           // of an item's tokens above the window (and at least `least`)
@@ -240,8 +242,7 @@ struct Space {
   WideState* wide;       // [R]
   ChunkOut* chunks;      // [R][nchunk]
   uint64_t* window;      // [R][kList]
-  uint32_t* count;       // [R][kCountBins] tokens
-  uint32_t* place;       // [R][kCountBins] sums of their places in the bin, in 32nds
+  unsigned long long* count;  // [R][kCountBins] tokens << 32 | the sum of their places in the bin, in 32nds
   int* wide_rows;        // [R]
   int* n_wide;           // wide rows; then the next item of `count` and of `collect`
 };
@@ -261,8 +262,7 @@ inline __host__ size_t space_of(Space* sp, void* base, int R, int nseg, int nchu
   sp->lists = reinterpret_cast<uint64_t*>(take(r * nseg * kSegCap * sizeof(uint64_t)));
   sp->chunks = reinterpret_cast<ChunkOut*>(take(r * nchunk * sizeof(ChunkOut)));
   sp->window = reinterpret_cast<uint64_t*>(take(r * kList * sizeof(uint64_t)));
-  sp->count = reinterpret_cast<uint32_t*>(take(r * kCountBins * sizeof(uint32_t)));
-  sp->place = reinterpret_cast<uint32_t*>(take(r * kCountBins * sizeof(uint32_t)));
+  sp->count = reinterpret_cast<unsigned long long*>(take(r * kCountBins * sizeof(unsigned long long)));
   return off;
 }
 
@@ -423,6 +423,7 @@ struct SelShared {
   float redf[kSelThreads / 32];
   int redi[kSelThreads / 32];
   int n;                     // list entries
+  int listed;                // and those of one item of a wide row
   int flag;
   uint64_t clo, chi;         // tokens of the undecided bin (comp range, inclusive)
   uint64_t above_mass;       // of the tokens above it
@@ -664,15 +665,22 @@ __device__ void choose(SelShared& sh, const Out& o, int r, const RowParam& p, in
 constexpr int kQuads = 2;
 template <bool VEC, typename F, typename E>
 __device__ __forceinline__ void for_quads(const float* row, int V, int q0, int q1, F f, E end) {
-  for (int qb = q0; qb < q1; qb += kQuads * kSelThreads) {
-    float4 x[kQuads];
+  float4 x[kQuads];
+  auto load = [&](int qb) {
 #pragma unroll
     for (int u = 0; u < kQuads; ++u) {
       const int q = qb + u * kSelThreads + threadIdx.x;
       x[u] = q < q1 ? load4<VEC>(row, q * 4, V) : make_float4(NAN, NAN, NAN, NAN);
     }
+  };
+  load(q0);
+  for (int qb = q0; qb < q1; qb += kQuads * kSelThreads) {
+    float4 y[kQuads];
 #pragma unroll
-    for (int u = 0; u < kQuads; ++u) f(x[u], qb + u * kSelThreads + static_cast<int>(threadIdx.x));
+    for (int u = 0; u < kQuads; ++u) y[u] = x[u];
+    load(qb + kQuads * kSelThreads);  // the next turn's, in flight during this one
+#pragma unroll
+    for (int u = 0; u < kQuads; ++u) f(y[u], qb + u * kSelThreads + static_cast<int>(threadIdx.x));
     end();
   }
 }
@@ -689,36 +697,43 @@ __device__ __forceinline__ void collect_quads(const float* row, int V, int q0, i
   const float v_lo = value_of(static_cast<uint32_t>(clo >> 32)), v_hi = value_of(static_cast<uint32_t>(chi >> 32));
   float ratio = race.ratio_to(top, c);
   mass = 0;
-  float part = 0.f;  // of kQuads quads: eight terms
+  const float start = fmaxf(v_hi, least);  // no token below it counts
+  float part = 0.f;                        // of kQuads quads: eight terms
   int turn = 0;
   for_quads<VEC>(row, V, q0, q1, [&](const float4& x, int q) {
     const float v[4] = {x.x, x.y, x.z, x.w};
-    float w[4];
-    bool any = false;
+    uint32_t over = 0;  // bit e: above the window by its place, within the value of chi
+    if ((v[0] <= v_hi && v[0] >= v_lo) || (v[1] <= v_hi && v[1] >= v_lo) || (v[2] <= v_hi && v[2] >= v_lo) ||
+        (v[3] <= v_hi && v[3] >= v_lo)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      bool above = v[e] > v_hi;
-      if (!above && v[e] >= v_lo) {  // of the window's values, or just above chi within one value
+      for (int e = 0; e < 4; ++e) {
         const uint64_t cp = comp_of(v[e], q * 4 + e);
-        above = cp > chi;
-        if (!above && cp >= clo) {
+        if (v[e] <= v_hi && cp > chi) over |= 1u << e;
+        if (cp <= chi && cp >= clo) {
           const int at = atomicAdd(n, 1);
           if (at < kList) list[at] = cp;
         }
       }
-      above = above && v[e] >= least;
-      w[e] = above ? (v[e] == top ? 1.f : ex2(__fmul_rn(__fsub_rn(v[e], top), c))) : -1.f;
-      any |= above;
-      part = __fadd_rn(part, fmaxf(w[e], 0.f));
     }
-    if (SCORE && any) {
-      const uint4 ws = ph.block(static_cast<uint32_t>(q));
+    float w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (w[e] >= 0.f && race.may_win(w[e], ratio, word_of(ws, e))) {
-          race.take(score_of(v[e], word_of(ws, e), p.temp), q * 4 + e);
-          ratio = race.ratio_to(top, c);
-        }
+    for (int e = 0; e < 4; ++e) {
+      const bool above = (v[e] > v_hi || (over >> e & 1)) && v[e] >= least;
+      w[e] = above ? (v[e] == top ? 1.f : ex2(__fmul_rn(__fsub_rn(v[e], top), c))) : 0.f;
+      part = __fadd_rn(part, w[e]);
+    }
+    // (a weight of zero takes no part unless the bound is so low that any token may win)
+    if (SCORE && fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= start) {
+      const uint4 ws = ph.block(static_cast<uint32_t>(q));
+      if (race.may_win(w[0], ratio, ws.x) || race.may_win(w[1], ratio, ws.y) || race.may_win(w[2], ratio, ws.z) ||
+          race.may_win(w[3], ratio, ws.w)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((v[e] > v_hi || (over >> e & 1)) && v[e] >= least && race.may_win(w[e], ratio, word_of(ws, e))) {
+            race.take(score_of(v[e], word_of(ws, e), p.temp), q * 4 + e);
+            ratio = race.ratio_to(top, c);
+          }
+      }
     }
   }, [&] {
     mass += fixed(part);
@@ -957,10 +972,16 @@ __device__ __noinline__ bool cut_unsorted(SelShared& sh, const Out& o, int r, co
   const float least = min_p_least(p, top);
   uint64_t mass = 0;
   int below = 0;  // listed tokens that min-p drops
+  float low = top;
   for (int j = threadIdx.x; j < n; j += kSelThreads) {
     mass += fixed(weight_of(sh.l.comp[j], top, p.temp));
-    below += value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32)) < least;
+    const float l = value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32));
+    below += l < least;
+    low = fminf(low, l);
   }
+  if (complete)  // (`bottom` is then no logit's, but the lowest finite value)
+    bottom = value_of(block_reduce(key_of(low), reinterpret_cast<uint32_t*>(sh.redi),
+                                   [](uint32_t x, uint32_t y) { return min(x, y); }));
   mass = block_sum(sh, mass);
   below = block_sum(sh, below);
   const uint64_t want = has_p ? share_of(p.top_p, z) : 0;
@@ -1215,12 +1236,26 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     exact_row<VEC>(sh, o, r, p, top);
     return;
   }
-  for (int i = threadIdx.x; i < kCountBins; i += kSelThreads) {
-    sp.count[static_cast<size_t>(r) * kCountBins + i] = 0;
-    sp.place[static_cast<size_t>(r) * kCountBins + i] = 0;
+  for (int i = threadIdx.x; i < kCountBins; i += kSelThreads) sp.count[static_cast<size_t>(r) * kCountBins + i] = 0;
+  // The bins of `count` reach from the largest logit down to the lowest of 4096
+  // spread over the row (lower ones share the last bin), kBinNats T at most: a
+  // bin of a flat row then holds few enough tokens to list.
+  float low = top;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float4 x = load4<VEC>(o.logits + r * o.ld, (u * kSelThreads + static_cast<int>(threadIdx.x)) *
+                                                         ((o.V + 3) / 4) / (4 * kSelThreads) * 4, o.V);
+    const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v[e] >= value_of(kKeyLowest)) low = fminf(low, v[e]);
   }
+  low = value_of(block_reduce(key_of(low), reinterpret_cast<uint32_t*>(sh.redi),
+                              [](uint32_t x, uint32_t y) { return min(x, y); }));
   if (threadIdx.x < 32) {
     WideState w{};
+    const float most = __fmul_rn(kBinNats, p.temp), range = __fsub_rn(top, low);
+    w.range = range > 0.f ? fminf(range, most) : most;
     w.z = z;
     w.top = top;
     w.least = min_p_least(p, top);
@@ -1254,11 +1289,20 @@ __device__ __forceinline__ int next_item(int* counter, int* slot) {
   return *slot;
 }
 
-// Units of kChunk tokens per work item: one while there are few items, up to
-// four where the CTAs have several items each anyway (fewer merges and ends).
-__device__ __forceinline__ int item_units(int n_wide, int nchunk) {
-  return min(4, max(1, static_cast<int>(static_cast<long long>(n_wide) * nchunk / (2 * gridDim.x))));
-}
+// A wide row's parts, one work item each: as many as the grid has CTAs for, in
+// the fewest whole rounds that leave a row 8 (so that no more than one CTA in
+// nine idles in the last), and none below kChunk tokens.
+struct Parts {
+  int n, quads;  // parts of a row; quads of a part
+  __device__ __forceinline__ Parts(int n_wide, int V) {
+    const int all = (V + 3) / 4, grid = static_cast<int>(gridDim.x);
+    int most = 1;  // (no wide row: no items)
+    if (n_wide > 0) most = max(1, (8 * n_wide + grid - 1) / grid * grid / n_wide);
+    n = min(most, (V + kChunk - 1) / kChunk);
+    quads = ((all + n - 1) / n + 7) / 8 * 8;
+    n = (all + quads - 1) / quads;
+  }
+};
 
 // A token's place in its row's value bins: bin << 5 | 32nd of the bin.
 __device__ __forceinline__ int value_place(float l, float top, float scale32) {
@@ -1279,8 +1323,9 @@ __global__ void __launch_bounds__(kSelThreads, 3) filter_count_kernel(Out o, Spa
   __shared__ SelShared sh;
   pdl_wait();
   pdl_trigger();
-  const int n_wide = *reinterpret_cast<volatile int*>(sp.n_wide), units = item_units(n_wide, o.nchunk);
-  const int parts = (o.nchunk + units - 1) / units, items = n_wide * parts;
+  const int n_wide = *reinterpret_cast<volatile int*>(sp.n_wide);
+  const Parts ps(n_wide, o.V);
+  const int parts = ps.n, items = n_wide * parts;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int item; (item = next_item(sp.n_wide + 1, &sh.n)) < items;) {
     const int r = sp.wide_rows[item / parts], part = item % parts;
@@ -1288,7 +1333,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) filter_count_kernel(Out o, Spa
     const bool by_count = p.top_k > 0;
     if (!by_count && p.top_p >= 1.f) continue;  // min-p alone needs no window
     WideState& st = sp.wide[r];
-    const float top = st.top, scale32 = __fdiv_rn(32.f * kCountBins / kBinNats, p.temp);
+    const float top = st.top, scale32 = __fdiv_rn(32.f * kCountBins, st.range);
     const float low = value_of(kKeyLowest);
     constexpr int PT = kCountBins / kSelThreads;
     uint32_t bn[PT], bp[PT];  // tokens and places of bins threadIdx.x + k * kSelThreads
@@ -1297,14 +1342,13 @@ __global__ void __launch_bounds__(kSelThreads, 3) filter_count_kernel(Out o, Spa
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < PT; ++k) sh.count[threadIdx.x + k * kSelThreads] = 0;
-    const int quads = (o.V + 3) / 4;
-    for (int unit = part * units; unit < min(o.nchunk, (part + 1) * units); ++unit) {
+    const int end = min((o.V + 3) / 4, (part + 1) * ps.quads);
+    for (int q0 = part * ps.quads; q0 < end; q0 += kCountTurn / 4) {
       __syncthreads();
       // tokens in the upper 14 bits, the sum of their 32nds in the lower 18: no
-      // bin of a unit's 8192 tokens carries over (8192 * 31 < 2^18, and 8192 < 2^14)
-      static_assert(kChunk * 31 < (1 << 18) && kChunk < (1 << 14), "packed counters");
-      const int q0 = unit * (kChunk / 4);
-      for_quads<VEC>(o.logits + r * o.ld, o.V, q0, min(quads, q0 + kChunk / 4), [&](const float4& x, int) {
+      // bin of 8192 tokens carries over (8192 * 31 < 2^18, and 8192 < 2^14)
+      static_assert(kCountTurn * 31 < (1 << 18) && kCountTurn < (1 << 14), "packed counters");
+      for_quads<VEC>(o.logits + r * o.ld, o.V, q0, min(end, q0 + kCountTurn / 4), [&](const float4& x, int) {
         const float v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -1322,25 +1366,22 @@ __global__ void __launch_bounds__(kSelThreads, 3) filter_count_kernel(Out o, Spa
         bp[k] += h & 0x3FFFF;
       }
     }
-    uint32_t* count = sp.count + static_cast<size_t>(r) * kCountBins;
-    uint32_t* place = sp.place + static_cast<size_t>(r) * kCountBins;
+    unsigned long long* count = sp.count + static_cast<size_t>(r) * kCountBins;
 #pragma unroll
-    for (int k = 0; k < PT; ++k)
-      if (bn[k]) {
-        atomicAdd(&count[threadIdx.x + k * kSelThreads], bn[k]);
-        if (bp[k]) atomicAdd(&place[threadIdx.x + k * kSelThreads], bp[k]);
-      }
+    for (int k = 0; k < PT; ++k)  // (V <= 2^21: the places' sum stays below 2^26)
+      if (bn[k]) atomicAdd(&count[threadIdx.x + k * kSelThreads], static_cast<unsigned long long>(bn[k]) << 32 | bp[k]);
     if (!last_arrival(&st.arrived[0], parts, &sh.flag)) continue;
     // ---- the window
     const int b0 = threadIdx.x * PT;
-    const float step = kBinNats / kCountBins;  // nats of a bin
+    const float step = __fdiv_rn(st.range, __fmul_rn(p.temp, static_cast<float>(kCountBins)));  // nats of a bin
     uint64_t bm[PT];
     uint32_t n = 0;
     uint64_t m = 0;
 #pragma unroll
     for (int k = 0; k < PT; ++k) {
-      bn[k] = __ldcg(&count[b0 + k]);
-      const float mean = __fdiv_rn(static_cast<float>(__ldcg(&place[b0 + k])), 32.f * fmaxf(static_cast<float>(bn[k]), 1.f));
+      const unsigned long long both = __ldcg(&count[b0 + k]);
+      bn[k] = static_cast<uint32_t>(both >> 32);
+      const float mean = __fdiv_rn(static_cast<float>(static_cast<uint32_t>(both)), 32.f * fmaxf(static_cast<float>(bn[k]), 1.f));
       bm[k] = fixed(__fmul_rn(static_cast<float>(bn[k]), ex2(__fmul_rn(-step * kLog2e, __fadd_rn(static_cast<float>(b0 + k),
                                                                                     __fadd_rn(mean, 1.f / 64))))));
       n += bn[k];
@@ -1411,8 +1452,9 @@ __global__ void __launch_bounds__(kSelThreads, 4) filter_collect_kernel(Out o, S
   __shared__ SelShared sh;
   pdl_wait();
   pdl_trigger();
-  const int n_wide = *reinterpret_cast<volatile int*>(sp.n_wide), units = item_units(n_wide, o.nchunk);
-  const int parts = (o.nchunk + units - 1) / units, items = n_wide * parts;
+  const int n_wide = *reinterpret_cast<volatile int*>(sp.n_wide);
+  const Parts ps(n_wide, o.V);
+  const int parts = ps.n, items = n_wide * parts;
   for (int item; (item = next_item(sp.n_wide + 2, &sh.n)) < items;) {
     const int r = sp.wide_rows[item / parts], part = item % parts;
     const RowParam p = sp.params[r];
@@ -1428,9 +1470,19 @@ __global__ void __launch_bounds__(kSelThreads, 4) filter_collect_kernel(Out o, S
     race.set_bound();
     uint64_t mass;
     uint64_t* window = sp.window + static_cast<size_t>(r) * kList;
-    const int quads = (o.V + 3) / 4, q0 = part * units * (kChunk / 4);
-    collect_quads<VEC, true>(o.logits + r * o.ld, o.V, q0, min(quads, q0 + units * (kChunk / 4)), p, top, least, st.clo,
-                             st.chi, window, &st.n, race, mass);
+    const int q0 = part * ps.quads;
+    if (threadIdx.x == 0) sh.listed = 0;
+    __syncthreads();
+    collect_quads<VEC, true>(o.logits + r * o.ld, o.V, q0, min((o.V + 3) / 4, q0 + ps.quads), p, top, least, st.clo,
+                             st.chi, sh.l.comp, &sh.listed, race, mass);
+    __syncthreads();
+    if (const int mine = min(sh.listed, kList); mine > 0) {  // to the row's list, in one piece
+      __syncthreads();
+      if (threadIdx.x == 0) sh.listed = atomicAdd(&st.n, mine);
+      __syncthreads();
+      const int at = sh.listed;
+      for (int j = threadIdx.x; j < mine && at + j < kList; j += kSelThreads) window[at + j] = sh.l.comp[j];
+    }
     const uint64_t sum = block_sum(sh, mass);
     block_best(sh, race);
     ChunkOut* chunks = sp.chunks + static_cast<size_t>(r) * o.nchunk;
@@ -1534,9 +1586,11 @@ int launch_decide(const Out& o, const Space& sp, int R, bool wide, cudaStream_t 
                                      static_cast<int>(smem)));
   VD_CUDA_TRY(launch_k(filter_select_kernel<VEC>, dim3(R), dim3(kSelThreads), smem, s, o, sp, wide));
   if (!wide) return VD_OK;
-  const int grid = static_cast<int>(std::min<long long>(static_cast<long long>(R) * o.nchunk, 3LL * sm_count_filter()));
-  VD_CUDA_TRY(launch_k(filter_count_kernel<VEC>, dim3(grid), dim3(kSelThreads), 0, s, o, sp));
-  VD_CUDA_TRY(launch_k(filter_collect_kernel<VEC>, dim3(grid), dim3(kSelThreads), 0, s, o, sp));
+  const long long most = static_cast<long long>(R) * o.nchunk, n_sm = sm_count_filter();
+  VD_CUDA_TRY(launch_k(filter_count_kernel<VEC>, dim3(static_cast<unsigned>(std::min(most, 3 * n_sm))), dim3(kSelThreads),
+                       0, s, o, sp));
+  VD_CUDA_TRY(launch_k(filter_collect_kernel<VEC>, dim3(static_cast<unsigned>(std::min(most, 4 * n_sm))),
+                       dim3(kSelThreads), 0, s, o, sp));
   return VD_OK;
 }
 
