@@ -1108,13 +1108,17 @@ int vd_sample_filtered(vd_model* m, const float* logits, int32_t R, const vd_sam
   if (reinterpret_cast<uintptr_t>(logits) & 15) return fail(VD_ERR_INVALID_ARG, "logits must be 16-byte aligned");
   if (const int rc = check_filters(filters, R)) return rc;
   if (m->cfg.vocab > (1 << 21)) return fail(VD_ERR_UNSUPPORTED, "filters take vocabularies of at most 2^21 tokens");
-  if (!m->filter_ws)
+  if (!m->filter_ws) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    VD_CUDA_TRY(cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cap));
+    if (cap != cudaStreamCaptureStatusNone)
+      return fail(VD_ERR_UNSUPPORTED, "a model's first filtered choice allocates its workspace: make one before a capture");
     if (const int rc = dev_alloc(m, &m->filter_ws, sample_filter_workspace(m->cfg.max_logit_rows, m->cfg.vocab))) return rc;
+  }
   SampleFilterArgs a{logits, R, m->cfg.vocab, m->cfg.vocab, per_row, filters, tokens_out, logprobs_out, m->filter_ws};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Prof p(m, K_SAMPLE, s);
-  p.kernels = 2 * ((R + 511) / 512);
-  return launch_sample_filter(a, s);
+  return launch_sample_filter(a, s, &p.kernels);
 }
 
 size_t vd_sample_workspace_bytes(int32_t R, int32_t V) { return R < 1 || V < 1 ? 0 : sample_filter_workspace(R, V); }

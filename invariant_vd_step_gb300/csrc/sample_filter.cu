@@ -1304,11 +1304,12 @@ struct Parts {
   }
 };
 
-// A token's place in its row's value bins: bin << 5 | 32nd of the bin.
-__device__ __forceinline__ int value_place(float l, float top, float scale32) {
-  const float d = l == top ? 0.f : __fmul_rn(__fsub_rn(top, l), scale32);
-  constexpr int kLast = (kCountBins - 1) * 32;
-  return d < static_cast<float>(kLast) ? static_cast<int>(d) : kLast;
+// A token's place in its row's value bins: bin << 5 | 32nd of the bin, to the
+// nearest (adding 2^23 rounds to a whole number in the low bits, where a
+// conversion would take the slow unit).
+__device__ __forceinline__ uint32_t value_place(float l, float top, float scale32) {
+  const float d = fminf(__fmul_rn(__fsub_rn(top, l), scale32), static_cast<float>((kCountBins - 1) * 32));
+  return __float_as_uint(__fadd_rn(l == top ? 0.f : d, 8388608.f)) & 0x7FFFFFu;
 }
 
 // The estimate of a bin's mass from its tokens' mean place is off by the
@@ -1353,8 +1354,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) filter_count_kernel(Out o, Spa
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (v[e] >= low) {
-            const int at = value_place(v[e], top, scale32);
-            atomicAdd(&sh.count[at >> 5], (1u << 18) + (at & 31));
+            const uint32_t at = value_place(v[e], top, scale32);
+            atomicAdd(&sh.count[at >> 5], (at & 31) | (1u << 18));
           }
       }, [] {});
       __syncthreads();
@@ -1383,7 +1384,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) filter_count_kernel(Out o, Spa
       bn[k] = static_cast<uint32_t>(both >> 32);
       const float mean = __fdiv_rn(static_cast<float>(static_cast<uint32_t>(both)), 32.f * fmaxf(static_cast<float>(bn[k]), 1.f));
       bm[k] = fixed(__fmul_rn(static_cast<float>(bn[k]), ex2(__fmul_rn(-step * kLog2e, __fadd_rn(static_cast<float>(b0 + k),
-                                                                                    __fadd_rn(mean, 1.f / 64))))));
+                                                                                    mean)))));
       n += bn[k];
       m += bm[k];
     }
@@ -1443,7 +1444,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) filter_count_kernel(Out o, Spa
       st.in_n = found ? sh.in_n - sh.above_n : 0xFFFFFFFFu;
     }
     if (found)
-      value_range(first, last, top, [&](float l) { return value_place(l, top, scale32) >> 5; }, 0, &st.clo, &st.chi);
+      value_range(first, last, top, [&](float l) { return static_cast<int>(value_place(l, top, scale32) >> 5); }, 0, &st.clo, &st.chi);
   }
 }
 
@@ -1604,7 +1605,7 @@ size_t sample_filter_workspace(int R, int V) {
   return space_of(&sp, nullptr, R, segments(V), chunks_of(V));
 }
 
-int launch_sample_filter(const SampleFilterArgs& a, cudaStream_t s) {
+int launch_sample_filter(const SampleFilterArgs& a, cudaStream_t s, int* launched) {
   Out o{a.logits, a.ld, a.V, segments(a.V), chunks_of(a.V), a.tokens, a.logprobs};
   Space sp;
   space_of(&sp, a.workspace, a.R, o.nseg, o.nchunk);
@@ -1619,6 +1620,7 @@ int launch_sample_filter(const SampleFilterArgs& a, cudaStream_t s) {
                        : launch_scan<kScanRows>(a, sp, o.nseg, r0, rows, vec, &wide, s);
     if (rc) return rc;
   }
+  if (launched) *launched = launches + (wide ? 3 : 1);
   return vec ? launch_decide<true>(o, sp, a.R, wide, s) : launch_decide<false>(o, sp, a.R, wide, s);
 }
 

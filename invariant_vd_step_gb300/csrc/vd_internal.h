@@ -290,7 +290,7 @@ struct SampleFilterArgs {
   void* workspace;
 };
 size_t sample_filter_workspace(int R, int V);
-int launch_sample_filter(const SampleFilterArgs& a, cudaStream_t s);
+int launch_sample_filter(const SampleFilterArgs& a, cudaStream_t s, int* launches = nullptr);  // launches: how many kernels
 int launch_philox(uint64_t seed, uint64_t step, int n, uint32_t* out, cudaStream_t s);
 int launch_wait_probe(int* status, uint64_t limit_ns, int* out, cudaStream_t s);
 // Streams a [rows][K] bf16 weight matrix through shared memory with a GEMM

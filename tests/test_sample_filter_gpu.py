@@ -163,6 +163,34 @@ def test_infinite_and_missing_logits_under_filters():
         assert lp[0] == lp[1] == lp[5] == 0 and lp[2] == lp[4] == 0 and abs(lp[3] - np.log(0.5)) < 1e-6
 
 
+@pytest.mark.parametrize("levels,count", [(0, 300), (1, 40), (1, 700), (3, 700), (5, 2500)])
+def test_cuts_among_the_few_likely_tokens(levels, count):
+    """Likely tokens far above the bulk, so that top-p and min-p cut among them: of any value (levels 0), or of a few
+    values each shared by many tokens, up to more than a list's bin takes."""
+    ready()
+    V, filters = 128256, [(0, 0.3, 0.0), (0, 0.9, 0.0), (0, 0.97, 0.05), (0, 1.0, 0.2), (0, 0.6, 0.5), (0, 0.999, 0.0)]
+    rng = np.random.default_rng(count)
+    x = rows_of("normal", len(filters), V, count)
+    for row in x:
+        top = rng.random(count) * 8 if levels == 0 else rng.integers(0, levels, count) * 1.5
+        row[rng.permutation(V)[:count]] = 20 + top
+    s = [(r, count, [0.7, 1.0, 1.4][r % 3]) for r in range(len(filters))]
+    assert check(x, s, filters, *run(x, s, filters)) <= 1
+
+
+@pytest.mark.parametrize("V,std,R", [(262144, 0.2, 20), (262144, 0.01, 3), (40001, 6.0, 90), (131072, 1.0, 700)])
+def test_wide_rows_of_any_spread(V, std, R):
+    ready()
+    some = np.random.default_rng(V).standard_normal((min(R, 10), V)).astype(np.float32) * np.float32(std)
+    x = np.tile(some, (-(-R // len(some)), 1))[:R]
+    filters = [[(0, 0.95, 0.0), (0, 0.99, 1e-7), (0, 1.0, 1e-6), (V // 3, 1.0, 0.0), (0, 0.9, 0.0)][r % 5] for r in range(R)]
+    s = [(7, r % 10, [1.0, 1.6][r % 2]) for r in range(R)]
+    tok, lp = run(x, s, filters)
+    assert check(x[:10], s[:10], filters[:10], tok[:10], lp[:10]) <= 1
+    for r in range(10, R):  # the same ten rows again
+        assert tok[r] == tok[r % 10] and lp[r] == lp[r % 10]
+
+
 def test_row_alone_equals_row_in_a_batch_and_many_rows():
     ready()
     V, R = 3001, 1100  # more rows than one launch takes
@@ -216,6 +244,34 @@ def test_capture_replays_on_new_logits():
     vd.sample(x, s, f, t2, l2)
     torch.cuda.synchronize()
     assert torch.equal(tok, t2) and torch.equal(lp, l2)
+
+
+def test_a_models_first_filtered_choice_is_refused_in_a_capture():
+    ready()
+    V = 4096
+    spec = synth.TINY.with_(vocab=V)
+    model = vd.Model(spec, {k: v.cuda() for k, v in synth.make_weights(spec).items()}, max_tokens=16, max_seqs=4,
+                     max_logit_rows=4, max_context=64)
+    x, s, f = torch.randn((2, V), device="cuda"), [(1, 2, 1.0), (3, 4, 0.8)], [(0, 0.9, 0.0), (5, 1.0, 0.0)]
+    tok, want = torch.full((2,), -1, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    vd.sample(x, s, f, want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+        mark = x + 1  # (a graph is not empty)
+        with pytest.raises(vd.VDError):
+            model.sample_filtered(x, s, f, tok)
+    model.sample_filtered(x, s, f, tok)
+    assert torch.equal(tok, want)
+    tok.fill_(-1)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        model.sample_filtered(x, s, f, tok)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(tok, want) and mark.shape == x.shape
+    model.close()
 
 
 def test_refusals():
