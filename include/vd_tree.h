@@ -55,7 +55,8 @@ typedef struct vd_tree_batch {
 } vd_tree_batch;
 
 /* max_nodes: most nodes of one plan (at most the model's max_tokens; at most
- * 1024 per request).  Destroy a tree before its model.
+ * 1024 per request).  Once its model is destroyed, vd_destroy_tree is the only
+ * call that a tree takes.
  * Errors: VD_ERR_INVALID_ARG, VD_ERR_CAPACITY, VD_ERR_CUDA. */
 int vd_tree_create(vd_model* m, int32_t max_nodes, vd_tree** out);
 void vd_destroy_tree(vd_tree* t);
@@ -95,7 +96,8 @@ int vd_step_tree(vd_tree* t, vd_kv_pool* pool, float* logits_out, void* stream);
  * -1; out_stride at least the longest path of the plan.  The K/V of the path's
  * node at depth d is moved to slot cached_len + d, in every layer, so that
  * cached_len + accepted_len slots of the request then hold its history;
- * other slots are left as they are.
+ * other slots are left as they are.  A plan is accepted once: the move
+ * overwrites slots of nodes off the path, and of nodes that have moved.
  * Errors: VD_ERR_INVALID_ARG, VD_ERR_CAPACITY, VD_ERR_CUDA. */
 int vd_tree_accept(vd_tree* t, vd_kv_pool* pool, const int32_t* node_tokens, const int32_t* choices,
                    int32_t* accepted_len, int32_t* out_tokens, int32_t out_stride, void* stream);

@@ -1106,7 +1106,12 @@ int vd_sample_filtered(vd_model* m, const float* logits, int32_t R, const vd_sam
   if (R == 0) return VD_OK;
   if (!logits || !per_row || !tokens_out) return fail(VD_ERR_INVALID_ARG, "null argument");
   if (reinterpret_cast<uintptr_t>(logits) & 15) return fail(VD_ERR_INVALID_ARG, "logits must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(tokens_out) | reinterpret_cast<uintptr_t>(logprobs_out)) & 3)
+    return fail(VD_ERR_INVALID_ARG, "tokens_out and logprobs_out must be 4-byte aligned");
   if (const int rc = check_filters(filters, R)) return rc;
+  int dev = -1;
+  VD_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev != m->device) return fail(VD_ERR_INVALID_ARG, "the model lives on another device than the current one");
   if (m->cfg.vocab > (1 << 21)) return fail(VD_ERR_UNSUPPORTED, "filters take vocabularies of at most 2^21 tokens");
   if (!m->filter_ws) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;

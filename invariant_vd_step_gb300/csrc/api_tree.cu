@@ -15,6 +15,7 @@ using namespace vd;
 
 struct vd_tree {
   vd_model* m = nullptr;
+  int device = 0;  // the model's
   int max_nodes = 0;
   // the plan in force
   Desc d;
@@ -159,8 +160,12 @@ int vd_tree_create(vd_model* m, int32_t max_nodes, vd_tree** out) {
   *out = nullptr;
   if (max_nodes < 1) return fail(VD_ERR_INVALID_ARG, "max_nodes must be >= 1");
   if (max_nodes > m->cfg.max_tokens) return fail(VD_ERR_CAPACITY, "max_nodes exceeds the model's max_tokens");
+  int dev = -1;
+  VD_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev != m->device) return fail(VD_ERR_INVALID_ARG, "the model lives on another device than the current one");
   vd_tree* t = new vd_tree();
   t->m = m;
+  t->device = dev;
   t->max_nodes = max_nodes;
   for (cudaEvent_t& e : t->uploaded)
     if (cudaEventCreateWithFlags(&e, cudaEventDisableTiming) != cudaSuccess) {
@@ -173,6 +178,9 @@ int vd_tree_create(vd_model* m, int32_t max_nodes, vd_tree** out) {
 
 void vd_destroy_tree(vd_tree* t) {
   if (!t) return;
+  int dev = t->device;  // the caller's current device, put back below
+  cudaGetDevice(&dev);
+  if (dev != t->device) cudaSetDevice(t->device);
   cudaDeviceSynchronize();
   for (int k = 0; k < 2; ++k) {
     if (t->host[k]) cudaFreeHost(t->host[k]);
@@ -180,6 +188,7 @@ void vd_destroy_tree(vd_tree* t) {
   }
   if (t->dev) cudaFree(t->dev);
   if (t->part) cudaFree(t->part);
+  if (dev != t->device) cudaSetDevice(dev);
   delete t;
 }
 
@@ -402,6 +411,9 @@ int vd_tree_accept(vd_tree* t, vd_kv_pool* pool, const int32_t* node_tokens, con
   if (t->d.T == 0) return VD_OK;
   if (!node_tokens && !t->has_tokens) return fail(VD_ERR_INVALID_ARG, "neither node_tokens nor token_ids in the plan");
   if (!choices || !accepted_len || !out_tokens) return fail(VD_ERR_INVALID_ARG, "null argument");
+  if ((reinterpret_cast<uintptr_t>(node_tokens) | reinterpret_cast<uintptr_t>(choices) |
+       reinterpret_cast<uintptr_t>(accepted_len) | reinterpret_cast<uintptr_t>(out_tokens)) & 3)
+    return fail(VD_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
   if (out_stride < t->longest_path) return fail(VD_ERR_CAPACITY, "out_stride is shorter than the longest path of the plan");
   const vd_model_config& c = t->m->cfg;
   const Desc& d = t->d;

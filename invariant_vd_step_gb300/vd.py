@@ -7,6 +7,7 @@ fallback: if libvd.so is missing or fails to load, every call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -229,6 +230,12 @@ def _raw_stream(stream, device: int) -> int:
     if stream is not None:
         return stream.cuda_stream
     return _current_raw_stream(device) if _current_raw_stream else torch.cuda.current_stream().cuda_stream
+
+
+def _allocating(stream):
+    """Context in which torch allocates for work on `stream` (None: the current one): memory that torch takes back from
+    one stream may still be in use there."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 def _ptr(t):
@@ -529,14 +536,13 @@ def sample(logits: torch.Tensor, samplers, filters, tokens_out: torch.Tensor, lo
            stream=None):
     """vd_op_sample: the token choice with filters for logits [R][V] of any row stride.  samplers: (seed, step,
     temperature) per row; filters: (top_k, top_p, min_p) per row or None; workspace: from `sample_workspace`, kept by
-    the caller (default: a new one, which torch's allocator may hand out again only to work on the current stream)."""
+    the caller (default: a new one per call, allocated for `stream`)."""
     s, f = _rows(samplers, SAMPLER), _rows(filters, FILTER)
     _check_choice(logits, logits.shape[-1], s, f, tokens_out, logprobs_out)
     R, V = logits.shape
     if workspace is None:
-        workspace = sample_workspace(R, V, logits.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        with _allocating(stream):
+            workspace = sample_workspace(R, V, logits.device)
     if workspace.get_device() != logits.get_device() or not workspace.is_contiguous():
         raise VDError(VD_ERR_INVALID_ARG, "workspace: contiguous, on the logits' GPU")
     rc = lib().vd_op_sample(logits.data_ptr(), R, V, logits.stride(0), _rows_ptr(s), _rows_ptr(f),
@@ -585,7 +591,8 @@ class Rope:
         """vd_op_rotary: x [T][H][head_dim] (bf16, fp16 or fp32, any token and head strides), positions int32 [T];
         out like x (a new contiguous tensor by default; x itself to rotate in place)."""
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            with _allocating(stream):
+                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         shape, dtype, device = x.shape, _DTYPES.get(x.dtype), x.get_device()
         if len(shape) != 3 or out.shape != shape or shape[2] != self.head_dim:
             raise VDError(VD_ERR_INVALID_ARG, f"x and out: [T][H][{self.head_dim}], got {tuple(shape)} and "
@@ -623,9 +630,14 @@ class Tree:
 
     def close(self):
         if getattr(self, "h", None):
-            if getattr(self.model, "h", None):  # a closed model has taken its device state with it
-                lib().vd_destroy_tree(self.h)
+            lib().vd_destroy_tree(self.h)
             self.h = None
+
+    def _live(self):
+        """The handle, as long as the tree and its model are open."""
+        if not self.h or not self.model.h:
+            raise VDError(VD_ERR_INVALID_ARG, "the tree or its model is closed")
+        return self.h
 
     def __del__(self):
         try:
@@ -643,7 +655,7 @@ class Tree:
         _need(len(cu) == len(c) + 1 and len(par) == cu[-1] and (tok is None or len(tok) == cu[-1]),
               "cu_nodes [B + 1], cached_len [B], parent and token_ids [cu_nodes[B]]")
         b = TreeBatch(len(par), len(c), pt.shape[1], 0, p_cu, p_par, p_c, pt.ctypes.data_as(_I32P), p_tok)
-        check(lib().vd_tree_plan(self.h, pool.h, ctypes.byref(b), _stream(stream)))
+        check(lib().vd_tree_plan(self._live(), pool.h, ctypes.byref(b), _stream(stream)))
         self.num_nodes, self.num_seqs = len(par), len(c)
 
     def attention(self, pool: KVPool, layer: int, q: torch.Tensor, out: torch.Tensor, stream=None):
@@ -651,7 +663,7 @@ class Tree:
         shape = (self.num_nodes, self.model.spec.n_heads, self.model.spec.head_dim)
         _check_out(q, shape, torch.bfloat16, "q")
         _check_out(out, shape, torch.bfloat16, "out")
-        rc = lib().vd_op_tree_attention(self.h, pool.h, layer, q.data_ptr(), out.data_ptr(),
+        rc = lib().vd_op_tree_attention(self._live(), pool.h, layer, q.data_ptr(), out.data_ptr(),
                                         _raw_stream(stream, out.get_device()))
         if rc:
             check(rc)
@@ -661,13 +673,13 @@ class Tree:
         s = self.model.spec
         _check_out(qkv, (self.num_nodes, s.qkv_dim), torch.bfloat16, "qkv")
         _check_out(q_out, (self.num_nodes, s.n_heads, s.head_dim), torch.bfloat16, "q_out")
-        check(lib().vd_op_tree_rope_kv(self.h, pool.h, layer, qkv.data_ptr(), q_out.data_ptr(),
+        check(lib().vd_op_tree_rope_kv(self._live(), pool.h, layer, qkv.data_ptr(), q_out.data_ptr(),
                                        _raw_stream(stream, q_out.get_device())))
 
     def step(self, pool: KVPool, logits: torch.Tensor, stream=None):
         """vd_step_tree: logits float32 [T][V] of every planned node."""
         _check_out(logits, (self.num_nodes, self.model.spec.vocab), torch.float32, "logits")
-        check(lib().vd_step_tree(self.h, pool.h, logits.data_ptr(), _raw_stream(stream, logits.get_device())))
+        check(lib().vd_step_tree(self._live(), pool.h, logits.data_ptr(), _raw_stream(stream, logits.get_device())))
 
     def accept(self, pool: KVPool, node_tokens, choices: torch.Tensor, accepted_len: torch.Tensor,
                out_tokens: torch.Tensor, stream=None):
@@ -677,9 +689,9 @@ class Tree:
         if node_tokens is not None:
             _check_out(node_tokens, (self.num_nodes,), torch.int32, "node_tokens")
         _check_out(accepted_len, (self.num_seqs,), torch.int32, "accepted_len")
-        stride = out_tokens.shape[-1]
+        stride = out_tokens.shape[-1] if out_tokens.dim() else 0
         _check_out(out_tokens, (self.num_seqs, stride), torch.int32, "out_tokens")
-        rc = lib().vd_tree_accept(self.h, pool.h, None if node_tokens is None else node_tokens.data_ptr(),
+        rc = lib().vd_tree_accept(self._live(), pool.h, None if node_tokens is None else node_tokens.data_ptr(),
                                   choices.data_ptr(), accepted_len.data_ptr(), out_tokens.data_ptr(), stride,
                                   _raw_stream(stream, choices.get_device()))
         if rc:

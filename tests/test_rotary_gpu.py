@@ -193,3 +193,24 @@ def test_default_rope_keeps_the_models_results_near_and_graphs_follow_a_new_rope
     want = run(scaled)
     assert not torch.equal(want, same)
     assert torch.equal(run(None, graphs=2, again=scaled), want)  # captured graphs do not outlive the rope
+
+
+def test_outputs_and_workspaces_made_by_a_call_belong_to_its_stream():
+    """Memory that torch still has in use on the current stream is not handed to a call on another one."""
+    ready()
+    side, x = torch.cuda.Stream(), torch.randn((64, 8, 64), device="cuda", dtype=torch.bfloat16)
+    pos, rope = torch.arange(64, dtype=torch.int32, device="cuda"), vd.Rope(64)
+    want = rope.apply(x, pos)
+    logits = torch.randn((4, 5000), device="cuda")
+    s, f = [(1, k, 1.0) for k in range(4)], [(0, 0.9, 0.0)] * 4
+    tok, tok_side = (torch.empty(4, dtype=torch.int32, device="cuda") for _ in range(2))
+    vd.sample(logits, s, f, tok)
+    torch.cuda.synchronize()
+    held = torch.empty_like(x)
+    freed = held.data_ptr()
+    del held  # the current stream's allocator would hand this block out next
+    got = rope.apply(x, pos, stream=side)
+    assert got.data_ptr() != freed
+    vd.sample(logits, s, f, tok_side, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(tok_side, tok)

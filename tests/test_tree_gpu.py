@@ -17,7 +17,7 @@ def check_rows(sc, window=0, layer=0):
     np.testing.assert_array_equal(bits(got), bits(ref))
     want, vmax = sc.oracle(window)
     # weights enter P V as two bf16 terms (relative 2^-16 of a weight, whose sum is 1) over fp32 sums, then one
-    # rounding to bf16 (2^-8 relative would be half a step's bound of 2^-9 doubled for the sum's own error)
+    # rounding to bf16 (half a step: 2^-8 relative)
     tol = 2.0 ** -14 * vmax + 2.0 ** -8 * np.abs(want)
     err = np.abs(f64(got) - want)
     assert np.all(err <= tol), f"max excess {(err - tol).max():.3g}"
@@ -299,3 +299,34 @@ def test_refusals_leave_plan_and_memory_alone():
     empty.plan(sc.pool, [0], [], [], np.zeros((0, 0), np.int32))
     empty.attention(sc.pool, 0, sc.q[:0], sc.q[:0])
     assert sc.model.device_status() == 0
+
+
+def test_side_stream_alignment_and_closing():
+    ready()
+    sc = TreeScenario(tree_spec(8, 2, 64), [(40, make_tree("random", 12, 3)), (600, make_tree("chain", 5))], seed=4)
+    want = sc.attention()
+    out, side = torch.full_like(sc.q, float("nan")), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sc.tree.plan(sc.pool, *sc.descriptor(), token_ids=np.arange(17), stream=side)
+    sc.tree.attention(sc.pool, 0, sc.q, out, stream=side)
+    side.synchronize()
+    np.testing.assert_array_equal(bits(out), bits(want))
+    # acceptance takes 4-byte aligned arrays only
+    L, i32 = vd.lib(), torch.zeros(256, dtype=torch.int32, device="cuda")
+    before, at = sc.pool.memory.clone(), i32.data_ptr()
+    for shift in ((1, 0, 0), (0, 2, 0), (0, 0, 3)):
+        args = [at + 256 * k + s for k, s in enumerate(shift)]
+        assert L.vd_tree_accept(sc.tree.h, sc.pool.h, None, *args, 16, None) == vd.VD_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert torch.equal(sc.pool.memory, before) and not i32.any()
+    # a model may be closed before its tree, which then only closes
+    other = vd.Tree(sc.model, max_nodes=4)
+    sc.tree.close()
+    with pytest.raises(vd.VDError):
+        sc.tree.attention(sc.pool, 0, sc.q, out)
+    sc.pool.close()
+    sc.model.close()
+    with pytest.raises(vd.VDError):
+        other.plan(sc.pool, *sc.descriptor())
+    other.close()
+    other.close()
