@@ -59,7 +59,7 @@ constexpr int kListBins = 1024;   // an unsorted list's bins of value
 constexpr int kCutList = 512;     // candidates of the cut's bin
 constexpr int kChunk = 4096;      // a wide row's work item has this many tokens or more
 constexpr int kCountTurn = 8192;  // tokens that the packed counters of `count` hold
-constexpr int kScanRows = 512;    // rows of a scan launch (their parameters travel with it: 32 bytes each)
+constexpr int kScanRows = 512;    // rows of a scan launch (their parameters travel with it: 34 bytes each)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMassScale = 68719476736.f;  // 2^36
 
@@ -73,15 +73,16 @@ struct RowParam {
 template <int N>
 struct RowParams {
   RowParam r[N];
+  short row[N];  // the row of each, after the launch's first
 };
-__device__ __forceinline__ int row_mode(const RowParam& p) {
+__host__ __device__ __forceinline__ int row_mode(const RowParam& p) {
   if (!(p.temp > 0.f)) return ROW_GREEDY;
   return p.top_k > 0 || p.top_p < 1.f || p.log_min_p > -INFINITY ? ROW_FILTER : ROW_FREE;
 }
 
 // Whether a row's whole mass is asked for: top-p over every token, or the
 // log-probability of an unfiltered choice.
-__device__ __forceinline__ bool needs_mass(const RowParam& p) {
+__host__ __device__ __forceinline__ bool needs_mass(const RowParam& p) {
   return p.temp > 0.f && p.top_k == 0 && (p.top_p < 1.f || !(p.log_min_p > -INFINITY));
 }
 
@@ -279,12 +280,12 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0) {
-    for (int r = threadIdx.x; r < rows; r += kScanThreads) sp.params[r0 + r] = params.r[r];
+    for (int r = threadIdx.x; r < rows; r += kScanThreads) sp.params[r0 + params.row[r]] = params.r[r];
     if (first && threadIdx.x < 3) sp.n_wide[threadIdx.x] = 0;
   }
   const int items = rows * nseg;
   for (int item = blockIdx.x * (kScanThreads / 32) + warp; item < items; item += gridDim.x * (kScanThreads / 32)) {
-    const int r = item / nseg, seg = item % nseg, row_i = r0 + r, i0 = seg * kSeg + lane * 4;
+    const int r = item / nseg, seg = item % nseg, row_i = r0 + params.row[r], i0 = seg * kSeg + lane * 4;
     const float* row = logits + row_i * ld;
     float v[8][4];
 #pragma unroll
@@ -1561,13 +1562,30 @@ constexpr int kNarrowK = 256;
 template <int N>
 int launch_scan(const SampleFilterArgs& a, const Space& sp, int nseg, int r0, int rows, bool vec, bool* wide,
                 cudaStream_t s) {
+  // Unfiltered rows (four times a filtered row's work) first, then those whose
+  // mass is asked for: every warp's turns then cost about the same.
   RowParams<N> params;
-  for (int i = 0; i < N; ++i) {
-    if (i < rows) row_param(a, r0 + i, &params.r[i]);
-    else params.r[i] = RowParam{};
-    const RowParam& p = params.r[i];
+  RowParam given[N];
+  int at[3] = {0, 0, 0};
+  auto kind = [](const RowParam& p) { return row_mode(p) == ROW_FREE ? 0 : needs_mass(p) ? 1 : 2; };
+  for (int i = 0; i < rows; ++i) {
+    row_param(a, r0 + i, &given[i]);
+    const RowParam& p = given[i];
     *wide |= p.temp > 0.f && !(p.top_k > 0 && p.top_k <= kNarrowK) &&
              (p.top_k > 0 || p.top_p < 1.f || p.log_min_p > -INFINITY);
+    ++at[kind(p)];
+  }
+  at[2] = at[0] + at[1];
+  at[1] = at[0];
+  at[0] = 0;
+  for (int i = 0; i < rows; ++i) {
+    const int k = at[kind(given[i])]++;
+    params.r[k] = given[i];
+    params.row[k] = static_cast<short>(i);
+  }
+  for (int i = rows; i < N; ++i) {
+    params.r[i] = RowParam{};
+    params.row[i] = 0;
   }
   // 8 groups list about 22 logits of a segment, 4 about 8, 2 about 3: a row's lists hold 1000 to 3000 in all, and
   // those from its largest threshold on fit a CTA's list
