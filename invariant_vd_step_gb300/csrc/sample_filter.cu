@@ -15,8 +15,9 @@
 //            a few groups of lanes), and writes the logits from that threshold
 //            on to a short list: every logit at or above the largest threshold
 //            of a row's segments is then in a list.
-//   select   one CTA per row sorts as many listed candidates as it needs and
-//            walks down them.
+//   select   one CTA per row takes as many listed candidates as it needs and
+//            finds the cut among them: up to 128 sorted, more by bins of value
+//            (only the cut's bin needs an order).
 //
 // A row whose cut lies below the lists (flat distributions, logits sorted
 // along the vocabulary) is "wide".  Two more kernels, whose CTAs take (wide
@@ -35,6 +36,11 @@
 //
 // Sums that decide something do not depend on timing: masses are summed as
 // integers.
+//
+// Measured: one row of 128256, top-k 50 and top-p 0.9, 14 us (host 13); 256
+// rows of mixed settings 101 us, 61 rows of 262144 with nuclei of tens of
+// thousands of tokens 144 us.  The floor is one read of the logits, 19.4 us and
+// 9.5 us; each kernel's comment says what it spends.
 #include <limits.h>
 #include <math.h>
 
@@ -268,7 +274,10 @@ inline __host__ size_t space_of(Space* sp, void* base, int R, int nseg, int nchu
 }
 
 // ---------------------------------------------------------------- scan
-// A warp walks over (row, segment) items.  first: the call's first scan launch.
+// A warp walks over (row, segment) items.  Bound by instruction issue next to
+// memory: 131 MB in 36 us (3.6 TB/s), 640 warp instructions per segment, issue 56
+// % active; copies through shared memory one item ahead measured 35 us, L2
+// prefetches of the next item nothing.  first: the call's first scan launch.
 // The others depend on no earlier kernel but through it, so they wait for
 // their predecessor at their end: they run next to it, and whatever waits for
 // the last one waits for all.
@@ -527,8 +536,8 @@ __device__ void sort_n(uint64_t* comp, int n) {
 }
 // Sorts comp[0, n) in descending order (n <= kList, the values all different
 // and above 0); the entries up to the next size are zeroed.
-__device__ void sort_desc(uint64_t* comp, int n) {
-  static_assert(kList == 8 * kSelThreads, "sizes below");
+constexpr int kFew = kSelThreads / 2;
+__device__ void sort_few(uint64_t* comp, int n) {
   if (n <= 32) {  // one warp, by shuffles
     if (threadIdx.x < 32) {
       uint64_t x = static_cast<int>(threadIdx.x) < n ? comp[threadIdx.x] : 0;
@@ -543,7 +552,7 @@ __device__ void sort_desc(uint64_t* comp, int n) {
       comp[threadIdx.x] = x;
     }
     __syncthreads();
-  } else if (n <= kSelThreads / 2) {  // by rank: each thread counts the values above its own
+  } else {  // by rank: each thread counts the values above its own
     const int i = threadIdx.x;
     const uint64_t mine = i < n ? comp[i] : 0;
     int rank = 0;
@@ -552,6 +561,12 @@ __device__ void sort_desc(uint64_t* comp, int n) {
     __syncthreads();
     if (i < n) comp[rank] = mine;
     __syncthreads();
+  }
+}
+__device__ void sort_desc(uint64_t* comp, int n) {
+  static_assert(kList == 8 * kSelThreads, "sizes below");
+  if (n <= kFew) {
+    sort_few(comp, n);
   } else if (n <= kSelThreads) {
     sort_n<1>(comp, n);
   } else if (n <= 2 * kSelThreads) {
@@ -963,19 +978,97 @@ __device__ void score_list(const SelShared& sh, const RowParam& p, int n, uint64
   }
 }
 
-// A row without top-k by its unsorted list of n tokens, every one at or above
-// `bottom`: true if that decides it.  top-p's cut is found in 1024 bins of
-// value (their masses as integers); only the cut's bin is sorted.  An undecided
-// row leaves the best score of the listed tokens, all of them kept, in `best`.
+// The lowest comp among the list's tokens from `from` on before which weigh()'s
+// sum is still below `want` (the first token's always): bins of value, their
+// weights as integers, then the cut's bin token by token.  False: that bin is
+// too large (ties).  bottom: no listed token's value is below it.
+template <typename W>
+__device__ __forceinline__ bool list_cut(SelShared& sh, int n, float top, float bottom, uint64_t from, uint64_t want,
+                                         W weigh, uint64_t* cut) {
+  auto& b = sh.l.b;
+  const float scale = __fdiv_rn(static_cast<float>(kListBins - 1), __fsub_rn(top, bottom));
+  auto bin = [&](uint64_t cp) {
+    const float l = value_of(static_cast<uint32_t>(cp >> 32));
+    const float d = l == top ? 0.f : __fmul_rn(__fsub_rn(top, l), scale);
+    return d < static_cast<float>(kListBins - 1) ? static_cast<int>(d) : kListBins - 1;
+  };
+  __syncthreads();
+  for (int i = threadIdx.x; i < kListBins; i += kSelThreads) b.cnt[i] = b.lo[i] = b.hi[i] = 0;
+  if (threadIdx.x == 0) sh.in_n = 0;
+  __syncthreads();
+  for (int j = threadIdx.x; j < n; j += kSelThreads) {
+    if (sh.l.comp[j] < from) continue;
+    const uint64_t w = weigh(sh.l.comp[j]);
+    const int i = bin(sh.l.comp[j]);
+    const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&b.lo[i], wl);
+    const uint32_t up = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
+    if (up) atomicAdd(&b.hi[i], up);
+    atomicAdd(&b.cnt[i], 1u);
+  }
+  __syncthreads();
+  constexpr int PT = kListBins / kSelThreads;
+  const int b0 = threadIdx.x * PT, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t m = 0;
+#pragma unroll
+  for (int k = 0; k < PT; ++k) m += b.lo[b0 + k] + (static_cast<uint64_t>(b.hi[b0 + k]) << 32);
+  uint64_t am = m;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, am, s);
+    if (lane >= s) am += x;
+  }
+  if (lane == 31) sh.redu[warp] = am;
+  __syncthreads();
+  am -= m;
+  for (int w = 0; w < warp; ++w) am += sh.redu[w];
+  int last = -1;  // the last bin before which the sum is below `want` (the first bin with a token at least)
+  uint64_t last_m = 0;
+#pragma unroll
+  for (int k = 0; k < PT; ++k) {
+    if (b.cnt[b0 + k] && (am == 0 || am < want)) {
+      last = b0 + k;
+      last_m = am;
+    }
+    am += b.lo[b0 + k] + (static_cast<uint64_t>(b.hi[b0 + k]) << 32);
+  }
+  const int cut_bin = block_max(sh, last);
+  if (last == cut_bin) sh.above_mass = last_m;
+  __syncthreads();
+  const uint64_t before = sh.above_mass;
+  for (int j = threadIdx.x; j < n; j += kSelThreads)
+    if (sh.l.comp[j] >= from && bin(sh.l.comp[j]) == cut_bin) {
+      const uint32_t at = atomicAdd(&sh.in_n, 1u);
+      if (at < kCutList) b.cut[at] = sh.l.comp[j];
+    }
+  __syncthreads();
+  const int in = static_cast<int>(sh.in_n);
+  if (in > kCutList) return false;
+  // a token of the bin is kept if the sum before it (over those of larger comp) stays below `want`
+  uint64_t lowest = ~0ull;
+  for (int j = threadIdx.x; j < in; j += kSelThreads) {
+    const uint64_t mine = b.cut[j];
+    uint64_t ahead = before;
+    for (int k = 0; k < in; ++k)
+      if (b.cut[k] > mine) ahead += weigh(b.cut[k]);
+    if ((ahead < want || ahead == 0) && mine < lowest) lowest = mine;
+  }
+  *cut = block_reduce(lowest, sh.redu, [](uint64_t x, uint64_t y) { return x < y ? x : y; });
+  return true;
+}
+
+// A row by its unsorted list of n tokens, which are all tokens at or above
+// `bottom` (complete: all there are): true if that decides it.  An undecided row
+// of which every listed token is kept leaves the best of their scores in `best`
+// (bound: asked for).
 __device__ __noinline__ bool cut_unsorted(SelShared& sh, const Out& o, int r, const RowParam& p, int n, float top,
-                                          float bottom, uint64_t z, bool complete, bool wide_next, Race& best) {
-  const bool has_p = p.top_p < 1.f;
+                                          float bottom, uint64_t z, bool complete, bool bound, Race& best) {
+  const bool has_p = p.top_p < 1.f, has_k = p.top_k > 0, k_listed = has_k && p.top_k <= n;
+  if (has_k && has_p && !k_listed && !complete) return false;  // top-p's share is of the top-k's mass
   const float least = min_p_least(p, top);
-  uint64_t mass = 0;
+  auto mass_of = [&](uint64_t cp) { return fixed(weight_of(cp, top, p.temp)); };
   int below = 0;  // listed tokens that min-p drops
   float low = top;
   for (int j = threadIdx.x; j < n; j += kSelThreads) {
-    mass += fixed(weight_of(sh.l.comp[j], top, p.temp));
     const float l = value_of(static_cast<uint32_t>(sh.l.comp[j] >> 32));
     below += l < least;
     low = fminf(low, l);
@@ -983,90 +1076,33 @@ __device__ __noinline__ bool cut_unsorted(SelShared& sh, const Out& o, int r, co
   if (complete)  // (`bottom` is then no logit's, but the lowest finite value)
     bottom = value_of(block_reduce(key_of(low), reinterpret_cast<uint32_t*>(sh.redi),
                                    [](uint32_t x, uint32_t y) { return min(x, y); }));
-  mass = block_sum(sh, mass);
   below = block_sum(sh, below);
-  const uint64_t want = has_p ? share_of(p.top_p, z) : 0;
-  if (!complete && below == 0 && (!has_p || mass < want)) {
-    if (wide_next) {
+  uint64_t cut = 0;  // the lowest kept comp
+  if (k_listed && !list_cut(sh, n, top, bottom, 0, p.top_k, [](uint64_t) { return 1ull; }, &cut)) return false;
+  bool decided = complete || below > 0 || k_listed;
+  if (has_p) {
+    uint64_t mass = 0;
+    for (int j = threadIdx.x; j < n; j += kSelThreads)
+      if (sh.l.comp[j] >= cut) mass += mass_of(sh.l.comp[j]);
+    mass = block_sum(sh, mass);
+    const uint64_t want = share_of(p.top_p, has_k ? mass : z);
+    if (mass >= want) {
+      decided = true;
+      if (!list_cut(sh, n, top, bottom, cut, want, mass_of, &cut)) return false;
+    }
+  }
+  if (!decided) {
+    if (bound) {
       score_list(sh, p, n, 0, least, best);
       block_best(sh, best);
     }
     return false;
   }
-  uint64_t cut = 0;  // the lowest kept comp
-  if (has_p && mass >= want) {
-    auto& b = sh.l.b;
-    const float scale = __fdiv_rn(static_cast<float>(kListBins - 1), __fsub_rn(top, bottom));
-    auto bin = [&](uint64_t cp) {
-      const float l = value_of(static_cast<uint32_t>(cp >> 32));
-      const float d = l == top ? 0.f : __fmul_rn(__fsub_rn(top, l), scale);
-      return d < static_cast<float>(kListBins - 1) ? static_cast<int>(d) : kListBins - 1;
-    };
-    for (int i = threadIdx.x; i < kListBins; i += kSelThreads) b.cnt[i] = b.lo[i] = b.hi[i] = 0;
-    if (threadIdx.x == 0) sh.in_n = 0;
-    __syncthreads();
-    for (int j = threadIdx.x; j < n; j += kSelThreads) {
-      const uint64_t w = fixed(weight_of(sh.l.comp[j], top, p.temp));
-      const int i = bin(sh.l.comp[j]);
-      const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&b.lo[i], wl);
-      const uint32_t up = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
-      if (up) atomicAdd(&b.hi[i], up);
-      atomicAdd(&b.cnt[i], 1u);
-    }
-    __syncthreads();
-    constexpr int PT = kListBins / kSelThreads;
-    const int b0 = threadIdx.x * PT, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t m = 0;
-#pragma unroll
-    for (int k = 0; k < PT; ++k) m += b.lo[b0 + k] + (static_cast<uint64_t>(b.hi[b0 + k]) << 32);
-    uint64_t am = m;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const uint64_t x = __shfl_up_sync(0xffffffffu, am, s);
-      if (lane >= s) am += x;
-    }
-    if (lane == 31) sh.redu[warp] = am;
-    __syncthreads();
-    am -= m;
-    for (int w = 0; w < warp; ++w) am += sh.redu[w];
-    int last = -1;  // the last bin before which the mass is below the share (bin 0 holds the largest token)
-    uint64_t last_m = 0;
-#pragma unroll
-    for (int k = 0; k < PT; ++k) {
-      if (b.cnt[b0 + k] && (b0 + k == 0 || am < want)) {
-        last = b0 + k;
-        last_m = am;
-      }
-      am += b.lo[b0 + k] + (static_cast<uint64_t>(b.hi[b0 + k]) << 32);
-    }
-    const int cut_bin = block_max(sh, last);
-    if (last == cut_bin) sh.above_mass = last_m;
-    __syncthreads();
-    uint64_t before = sh.above_mass;
-    for (int j = threadIdx.x; j < n; j += kSelThreads)
-      if (bin(sh.l.comp[j]) == cut_bin) {
-        const uint32_t at = atomicAdd(&sh.in_n, 1u);
-        if (at < kCutList) b.cut[at] = sh.l.comp[j];
-      }
-    __syncthreads();
-    const int in = static_cast<int>(sh.in_n);
-    if (in > kCutList) return false;  // ties: the wide kernels or the exact histograms
-    // a token of the bin is kept if the masses before it (those of larger comp) stay below the share
-    uint64_t lowest = ~0ull;
-    for (int j = threadIdx.x; j < in; j += kSelThreads) {
-      const uint64_t mine = b.cut[j];
-      uint64_t ahead = before;
-      for (int k = 0; k < in; ++k)
-        if (b.cut[k] > mine) ahead += fixed(weight_of(b.cut[k], top, p.temp));
-      if ((ahead < want || ahead == 0) && mine < lowest) lowest = mine;
-    }
-    cut = block_reduce(lowest, sh.redu, [](uint64_t x, uint64_t y) { return x < y ? x : y; });
-  }
   uint64_t kept = 0;
   Race race;
   for (int j = threadIdx.x; j < n; j += kSelThreads) {
     const uint64_t cp = sh.l.comp[j];
-    if (cp >= cut && value_of(static_cast<uint32_t>(cp >> 32)) >= least) kept += fixed(weight_of(cp, top, p.temp));
+    if (cp >= cut && value_of(static_cast<uint32_t>(cp >> 32)) >= least) kept += mass_of(cp);
   }
   kept = block_sum(sh, kept);
   score_list(sh, p, n, cut, least, race);
@@ -1075,7 +1111,9 @@ __device__ __noinline__ bool cut_unsorted(SelShared& sh, const Out& o, int r, co
 }
 
 // wide_next: the count and collect kernels follow, and take rows that the
-// lists do not decide.
+// lists do not decide.  Bound by a row's chain of small steps (segment maxima,
+// gather, cut, race): 12 us for one row, 26 us for 256 of mixed settings, two to
+// an SM; sorting every list took 17 and 29 us.
 template <bool VEC>
 __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space sp, bool wide_next) {
   __shared__ SelShared sh;
@@ -1204,12 +1242,11 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     const int n = sh.n;
     if (n > kList || n == 0) continue;  // too many candidates, or none listed (ties)
     const bool complete = all && from == floor;
-    if (level == 1 && p.top_k == 0) {  // top-p and min-p alone need no order but at the cut
-      const bool done = cut_unsorted(sh, o, r, p, n, top, value_of(floor), z, complete, wide_next, listed);
-      if (done) return;
+    if (n > kFew) {  // no order is needed but at the cut
+      if (cut_unsorted(sh, o, r, p, n, top, value_of(from), z, complete, level == 1 && wide_next, listed)) return;
       continue;
     }
-    sort_desc(sh.l.comp, n);
+    sort_few(sh.l.comp, n);
     prefix_mass(sh, n, top, p.temp, 0);
     const int lim = p.top_k > 0 ? min(p.top_k, n) : n;
     const bool k_known = complete || p.top_k <= n;  // with top_k on: the list holds all of its tokens
@@ -1224,7 +1261,7 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     kept = block_sum(sh, kept);
     const bool decided = complete || kept < n || (p.top_k > 0 && p.top_k <= n) || (has_p && sh.l.pre[lim - 1] >= share);
     if (!decided) {
-      if (level == 1 && wide_next && !has_p) {  // every listed token is kept
+      if (level == 1 && wide_next) {  // every listed token is kept
         score_list(sh, p, n, 0, -INFINITY, listed);
         block_best(sh, listed);
       }
@@ -1270,6 +1307,10 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
 }
 
 // ---------------------------------------------------------------- wide rows
+// 61 rows of 262144 (64 MB, in L2 after the scan): count 44 us, bound by its
+// shared-memory atomics; collect 63 to 70 us, bound by issue (Philox and the
+// race's bound, 70 warp instructions per 32 tokens).  A few wide rows among 256
+// take 20 us each, the chain of one part and of the row's last CTA.
 // Whether this CTA is the last of a row's `total` to arrive; what the others
 // wrote before arriving is then visible to it.
 __device__ __forceinline__ bool last_arrival(uint32_t* arrived, int total, int* flag) {

@@ -24,7 +24,8 @@ namespace {
 // A group of DS warps folds the tail tiles of one (node, KV head): the
 // group's query heads are the first G of the 16 rows of the mma tile, and its
 // keys are gathered from the slots of its path, 16 bytes per copy, into the
-// layout of a TMA-staged tile.
+// layout of a TMA-staged tile.  For trees whose tail does not fit shared memory
+// (below); bound by the latency of its gathers.
 constexpr int kTailWarps = 4;
 
 // Whether a bounded wait of this step has given up; one read for the whole
@@ -170,8 +171,10 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(TreeTailArgs
 // node's path, with the other nodes' rows ignored in the scores and zero in P
 // (they add nothing to O); softmax, rescale and state are shared.  16-key
 // halves of a tile in which a node sees no key are left out: zeros again.
-// Bound by the instruction issue of the chains: at 16384 nodes x heads of 4
-// rows, one node per warp took 1886 warp instructions a node.
+// Bound by its chains' latency at two CTAs of four warps per SM (208 registers:
+// Q, the state and the scores of 16 rows; three CTAs spill and measured the
+// same): at 32 trees x 64 nodes x 8 KV heads, 4 rows each, 51 us, a quarter of
+// the mma.sync rate, 11 M warp instructions.  One node per warp took 85 us.
 template <int HD>
 struct Staged {
   static constexpr int ROW = HD * 2;  // bytes of a K or V row
@@ -395,7 +398,10 @@ int launch_tail_t(const TreeTailArgs& a, cudaStream_t s) {
 // the K/V of the path's node at depth d from slot c + node to slot c + d.  A
 // thread moves the same 16-byte column of every node, in ascending depth: a
 // node's number is at least its depth, so no slot is overwritten before it
-// has been read.
+// has been read.  Bound by one chain of dependent reads (parents and tokens, the
+// path's pages, K/V), whatever the batch: 5.7 us for 32 trees of 32 nodes in 32
+// layers of 8 heads x 128 (33 MB moved if half of 8-node chains are accepted),
+// the same for one tree of 8.
 constexpr int kAcceptThreads = 256;
 constexpr int kAcceptBatch = 8;  // nodes read before their copies are written
 
@@ -450,7 +456,9 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(TreeAcceptA
 }  // namespace
 
 // Nodes that a warp folds at once: one while the launch has warps to spare (a
-// node's chains are then the latency), up to 16 / G.  0: the tail does not fit.
+// node's chains are then the latency: 7 us for 8 nodes), up to 16 / G where it
+// has not (32 x 64 nodes: 51 us, against 85 us of one per warp).  0: the tail
+// does not fit.
 int tree_nodes_per_warp(int hd, int nodes, int Hkv, int G, int tail_rows, int n_sm, int* blk_nodes) {
   const size_t bytes = hd == 64 ? Staged<64>::bytes(tail_rows)
                        : hd == 128 ? Staged<128>::bytes(tail_rows) : Staged<256>::bytes(tail_rows);
