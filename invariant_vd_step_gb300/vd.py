@@ -272,20 +272,33 @@ def _rows(rows, dtype):
     return np.array([(*r, 0) for r in rows], dtype=dtype)
 
 
+_NOTHING = ctypes.c_byte * 0
+
+
 def _rows_ptr(rows):
-    return None if rows is None else rows.ctypes.data
+    """The records' address, as an argument that also keeps them alive."""
+    if rows is None:
+        return None
+    try:
+        return _NOTHING.from_buffer(rows)  # half the time of rows.ctypes.data
+    except TypeError:  # read-only records
+        return rows.ctypes.data
 
 
 def _check_choice(logits, V, samplers, filters, tokens_out, logprobs_out):
-    R = len(samplers)
-    if not (logits.is_cuda and logits.dtype == torch.float32 and logits.shape == (R, V)
-            and (V <= 1 or logits.stride(1) == 1)):
+    """Checks of a token choice's tensors; the row stride and the device."""
+    R, device, stride = len(samplers), logits.get_device(), logits.stride()
+    if device < 0 or logits.dtype != torch.float32 or logits.shape != (R, V) or (V > 1 and stride[1] != 1):
         raise VDError(VD_ERR_INVALID_ARG, f"logits: float32 CUDA rows [{R}][{V}], one sampler each")
     if filters is not None and len(filters) != R:
         raise VDError(VD_ERR_INVALID_ARG, "one filter per row")
-    for t, dtype in ((tokens_out, torch.int32), (logprobs_out, torch.float32)):
-        if t is not None and not (t.device == logits.device and t.dtype == dtype and t.shape == (R,) and t.is_contiguous()):
-            raise VDError(VD_ERR_INVALID_ARG, f"one contiguous {dtype} output per row, on the logits' GPU")
+    if (tokens_out.get_device() != device or tokens_out.dtype != torch.int32 or tokens_out.shape != (R,)
+            or not tokens_out.is_contiguous()):
+        raise VDError(VD_ERR_INVALID_ARG, "tokens_out: one contiguous int32 per row, on the logits' GPU")
+    if logprobs_out is not None and (logprobs_out.get_device() != device or logprobs_out.dtype != torch.float32
+                                     or logprobs_out.shape != (R,) or not logprobs_out.is_contiguous()):
+        raise VDError(VD_ERR_INVALID_ARG, "logprobs_out: one contiguous float32 per row, on the logits' GPU")
+    return stride[0], device
 
 
 class StepBatch:
@@ -538,16 +551,16 @@ def sample(logits: torch.Tensor, samplers, filters, tokens_out: torch.Tensor, lo
     temperature) per row; filters: (top_k, top_p, min_p) per row or None; workspace: from `sample_workspace`, kept by
     the caller (default: a new one per call, allocated for `stream`)."""
     s, f = _rows(samplers, SAMPLER), _rows(filters, FILTER)
-    _check_choice(logits, logits.shape[-1], s, f, tokens_out, logprobs_out)
-    R, V = logits.shape
+    R, V = len(s), logits.shape[-1]
+    row_stride, device = _check_choice(logits, V, s, f, tokens_out, logprobs_out)
     if workspace is None:
         with _allocating(stream):
             workspace = sample_workspace(R, V, logits.device)
-    if workspace.get_device() != logits.get_device() or not workspace.is_contiguous():
+    if workspace.get_device() != device or not workspace.is_contiguous():
         raise VDError(VD_ERR_INVALID_ARG, "workspace: contiguous, on the logits' GPU")
-    rc = lib().vd_op_sample(logits.data_ptr(), R, V, logits.stride(0), _rows_ptr(s), _rows_ptr(f),
-                            tokens_out.data_ptr(), None if logprobs_out is None else logprobs_out.data_ptr(),
-                            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, logits.get_device()))
+    rc = lib().vd_op_sample(logits.data_ptr(), R, V, row_stride, _rows_ptr(s), _rows_ptr(f), tokens_out.data_ptr(),
+                            None if logprobs_out is None else logprobs_out.data_ptr(), workspace.data_ptr(),
+                            workspace.nbytes, _raw_stream(stream, device))
     if rc:
         check(rc)
 
