@@ -320,7 +320,9 @@ int vd_sample(vd_model* m, const float* logits, int32_t R, const vd_sampler* per
  * log-probability of the chosen token under the distribution it was drawn
  * from, softmax(l / T) over the kept tokens; 0 for a greedy row, whose filters
  * do not matter.  Tokens of logit -inf or NaN are never kept; a row without
- * any other gets vd_sample's token, at log-probability 0.  A model's calls share
+ * any other gets vd_sample's token, at log-probability 0.  Token and
+ * log-probability depend on the row, its state and its filter only, bit for
+ * bit, never on R or the other rows.  A model's calls share
  * a workspace, which the first one allocates: they are ordered by the caller.
  * Errors as vd_sample, VD_ERR_INVALID_ARG for filters out of range, and
  * VD_ERR_UNSUPPORTED above 2^21 tokens, or for a first call on a stream that

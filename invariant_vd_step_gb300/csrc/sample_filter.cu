@@ -34,12 +34,12 @@
 // top_k beyond the lists) one CTA settles by exact histograms over the
 // (value, index) order, refined until the cut's bin fits the list.
 //
-// Sums that decide something do not depend on timing: masses are summed as
-// integers.
+// Masses are integers, one per token whichever kernel adds it: nothing depends
+// on timing, on the CTAs that share a row or on the other rows of the call.
 //
-// Measured: one row of 128256, top-k 50 and top-p 0.9, 14 us (host 13); 256
-// rows of mixed settings 101 us, 61 rows of 262144 with nuclei of tens of
-// thousands of tokens 144 us.  The floor is one read of the logits, 19.4 us and
+// Measured: one row of 128256, top-k 50 and top-p 0.9, 13 us (host 11); 256
+// rows of mixed settings 83 to 115 us by seed, 61 rows of 262144 with nuclei of
+// tens of thousands of tokens 145 us.  The floor is one read of the logits, 19.4 us and
 // 9.5 us; each kernel's comment says what it spends.
 #include <limits.h>
 #include <math.h>
@@ -132,6 +132,25 @@ __device__ __noinline__ float score_of(float l, uint32_t word, float t) { return
 // are exact in any order (V <= 2^21 tokens of mass at most 1: below 2^57), and
 // the GPU's few double-precision units stay out of it.
 __device__ __forceinline__ uint64_t fixed(float w) { return static_cast<uint64_t>(__fmul_rn(w, kMassScale)); }
+// Sums of fixed(w), w in [0, 1], without its conversions: adding 32 rounded down
+// leaves floor(2^18 w) in the low bits of the float, adding 2^-13 to what is
+// left over (exact) leaves the next 18 bits.  The sums of the bits are taken
+// modulo 2^32 and the constants' bits off again: exact for 2^13 tokens.  So a
+// token's mass is the same whichever kernel, part and thread adds it.
+struct MassSum {
+  uint32_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add4(const float (&w)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float t = __fadd_rd(w[e], 32.f), r = __fsub_rn(w[e], __fsub_rn(t, 32.f));
+      hi += __float_as_uint(t);
+      lo += __float_as_uint(__fadd_rd(r, 1.220703125e-4f));
+    }
+    hi -= 4u * 0x42000000u;
+    lo -= 4u * 0x39000000u;
+  }
+  __device__ __forceinline__ uint64_t value() const { return (static_cast<uint64_t>(hi) << 18) + lo; }
+};
 __device__ __forceinline__ uint64_t share_of(float top_p, uint64_t mass) {
   return static_cast<uint64_t>(static_cast<double>(top_p) * static_cast<double>(mass));
 }
@@ -712,9 +731,8 @@ __device__ __forceinline__ void collect_quads(const float* row, int V, int q0, i
   const float c = __fdiv_rn(kLog2e, p.temp);
   const float v_lo = value_of(static_cast<uint32_t>(clo >> 32)), v_hi = value_of(static_cast<uint32_t>(chi >> 32));
   float ratio = race.ratio_to(top, c);
-  mass = 0;
   const float start = fmaxf(v_hi, least);  // no token below it counts
-  float part = 0.f;                        // of kQuads quads: eight terms
+  MassSum part;                            // (V <= 2^21: at most 2^13 tokens a thread)
   int turn = 0;
   for_quads<VEC>(row, V, q0, q1, [&](const float4& x, int q) {
     const float v[4] = {x.x, x.y, x.z, x.w};
@@ -736,8 +754,8 @@ __device__ __forceinline__ void collect_quads(const float* row, int V, int q0, i
     for (int e = 0; e < 4; ++e) {
       const bool above = (v[e] > v_hi || (over >> e & 1)) && v[e] >= least;
       w[e] = above ? (v[e] == top ? 1.f : ex2(__fmul_rn(__fsub_rn(v[e], top), c))) : 0.f;
-      part = __fadd_rn(part, w[e]);
     }
+    part.add4(w);
     // (a weight of zero takes no part unless the bound is so low that any token may win)
     if (SCORE && fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= start) {
       const uint4 ws = ph.block(static_cast<uint32_t>(q));
@@ -752,14 +770,13 @@ __device__ __forceinline__ void collect_quads(const float* row, int V, int q0, i
       }
     }
   }, [&] {
-    mass += fixed(part);
-    part = 0.f;
     if (SCORE && (turn & (turn + 1)) == 0) {  // a bound that the warp shares, after 1, 2, 4, ... turns
       race.warp_reduce();
       ratio = race.ratio_to(top, c);
     }
     ++turn;
   });
+  mass = part.value();
 }
 
 // ---------------------------------------------------------------- the exact path

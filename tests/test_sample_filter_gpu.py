@@ -207,6 +207,28 @@ def test_row_alone_equals_row_in_a_batch_and_many_rows():
     np.testing.assert_array_equal(run(x, s, filters, logprobs=False)[0], tok)
 
 
+@pytest.mark.parametrize("V", [40001, 131072, 262144])
+def test_rows_do_not_depend_on_the_rest_of_the_call(V):
+    """A row's token and log-probability, bit for bit, alone and in calls of other rows, which change how many CTAs
+    share a row and which kernels a call has."""
+    ready()
+    kinds = ["normal", "flat", "ties", "equal", "sorted", "normal"]
+    x = np.concatenate([rows_of(k, 1, V, i) for i, k in enumerate(kinds)])
+    filters = [(0, 0.95, 0.0), (0, 0.9, 0.0), (0, 0.97, 0.0), (50, 1.0, 0.0), (200, 1.0, 1e-4), (V // 5, 1.0, 0.0),
+               (0, 1.0, 1e-6), (100, 0.99, 0.0)]
+    # every row under every filter: row k of the call is kind k % 6 under filter k // 6
+    n = len(kinds) * len(filters)
+    xs, fs = x[np.arange(n) % 6], [filters[k // 6] for k in range(n)]
+    s = [(5 + k, k, [1.0, 1.7][k % 2]) for k in range(n)]
+    tok, lp = run(xs, s, fs)
+    for group in (1, 5):
+        for k0 in range(0, n, group):
+            rows = range(k0, min(n, k0 + group))
+            t1, l1 = run(xs[k0:k0 + group], [s[k] for k in rows], [fs[k] for k in rows])
+            for k in rows:
+                assert t1[k - k0] == tok[k] and l1[k - k0] == lp[k], (group, kinds[k % 6], fs[k])
+
+
 def test_frequencies_follow_the_filtered_distribution():
     ready()
     V, R = 64, 512
