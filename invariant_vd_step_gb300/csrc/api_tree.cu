@@ -139,6 +139,8 @@ int vd::run_tree_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc&
   t.n_blk = d.n_blk;
   t.npg = d.npg;
   t.tail_rows = d.tail_rows;
+  // (with a window a CTA of the attention kernel may see no key and leave before its wait)
+  t.early = a.window == 0 && d.cls[0].items + d.cls[1].items + d.cls[2].items + d.cls[3].items > 0;
   if ((rc = launch_tree_tail(t, hd, s))) return rc;
   MergeArgs g{};
   g.part_o = d.part_o;

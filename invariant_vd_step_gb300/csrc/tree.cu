@@ -230,8 +230,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2) tree_tail_staged_kernel(Tr
   // lane n of the warp knows node n
   const int my_t = n0 + first + min(lane, max(count - 1, 0));
   const int my_p = lane < count ? a.positions[my_t] : -1, my_path = lane < count ? a.path_off[my_t] : 0;
-  pdl_wait();
-  pdl_trigger();
+  if (!a.early) pdl_wait();
   for (int i = threadIdx.x; i < rows * CH; i += kTailWarps * 32) {
     const int r = i / CH, ch = i % CH, slot = shared + r;
     const size_t row = (static_cast<size_t>(table[slot >> 4]) * 2 * a.Hkv + kvh) * 16 + (slot & 15);
@@ -249,6 +248,11 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2) tree_tail_staged_kernel(Tr
       qf[kk][r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + t4 * 2) : 0u;
       qf[kk][2 + r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8 + t4 * 2) : 0u;
     }
+  }
+  if (a.early) pdl_wait();
+  pdl_trigger();
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
     // the state of the split that the shared tiles began
     const bool begun = valid[r] && max(lo[r], shared / a.split * a.split) < shared;
     const size_t at = out_row[r] * a.max_splits + shared / a.split;

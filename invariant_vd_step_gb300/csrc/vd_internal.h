@@ -204,6 +204,8 @@ struct TreeTailArgs {
   int n_blk;
   int npg;                    // nodes that a warp folds at once; 0: one node per warp, rows gathered from the pool
   int tail_rows;              // most (cached keys past the shared tiles + nodes) of a request
+  int early;                  // 1: the kernel before this one is an attention kernel of the same step all of whose
+                              // CTAs wait before they trigger, so that q and the nodes' K/V are there before the wait
 };
 int tree_nodes_per_warp(int hd, int nodes, int Hkv, int G, int tail_rows, int n_sm, int* blk_nodes);
 int launch_tree_tail(const TreeTailArgs& a, int hd, cudaStream_t s);
