@@ -1186,10 +1186,13 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
   }
   const bool all = floor <= kKeyLowest;  // the lists hold every finite logit
   Race listed;  // the best of the listed tokens, where they are all kept
-  // First as many candidates as there are large segment maxima (at least the
-  // first `want` tokens are among those at or above the want-th largest), then,
-  // if that does not decide the row, every listed one.
-  for (int level = 0; level < 2; ++level) {
+  // Level 0: as many candidates as there are large segment maxima (at least the
+  // first `want` tokens are among those at or above the want-th largest).  Level
+  // 1: every listed one.  Rows with a top-k take the few first; the others all
+  // (61 wide rows 22 -> 16 us), and the few only where those are too many.
+  for (int turn = 0; turn < 2; ++turn) {
+    const int level = p.top_k > 0 ? turn : 1 - turn;
+    const bool last = turn == 1 || p.top_k == 0;  // what is undecided then goes on to the wide kernels
     uint32_t from = floor;
     if (level == 0) {
       const int want = min(p.top_k > 0 ? p.top_k : 48, o.nseg);
@@ -1260,7 +1263,8 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     if (n > kList || n == 0) continue;  // too many candidates, or none listed (ties)
     const bool complete = all && from == floor;
     if (n > kFew) {  // no order is needed but at the cut
-      if (cut_unsorted(sh, o, r, p, n, top, value_of(from), z, complete, level == 1 && wide_next, listed)) return;
+      if (cut_unsorted(sh, o, r, p, n, top, value_of(from), z, complete, last && wide_next, listed)) return;
+      if (p.top_k == 0) break;
       continue;
     }
     sort_few(sh.l.comp, n);
@@ -1278,10 +1282,11 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
     kept = block_sum(sh, kept);
     const bool decided = complete || kept < n || (p.top_k > 0 && p.top_k <= n) || (has_p && sh.l.pre[lim - 1] >= share);
     if (!decided) {
-      if (level == 1 && wide_next) {  // every listed token is kept
+      if (last && wide_next) {  // every listed token is kept
         score_list(sh, p, n, 0, -INFINITY, listed);
         block_best(sh, listed);
       }
+      if (p.top_k == 0) break;
       continue;
     }
     choose(sh, o, r, p, kept, Race(), kept > 0 ? sh.l.pre[kept - 1] : 0, top, false);
