@@ -352,7 +352,9 @@ __device__ __forceinline__ uint4 philox_block(uint64_t seed, uint64_t step, uint
                        static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32));
 }
 // Gumbel-max score of logit v: v / T + G with G = -log(-log(u)),
-// u = ((word >> 8) + 0.5) * 2^-24 (exact in fp32, never 0 or 1).
+// u = ((word >> 8) + 0.5) * 2^-24 as fp32 holds it: exact below 1/2; from 1/2 on
+// the half rounds to even, and a word of 24 leading ones (one in 2^24) gives
+// u = 1, an infinite score that wins whatever the logit.
 __device__ __forceinline__ float gumbel_score(float v, uint32_t word, float temperature) {
   const float u = __fmul_rn(__fadd_rn(static_cast<float>(word >> 8), 0.5f), 5.9604644775390625e-8f);
   const float g = -logf(-logf(u));

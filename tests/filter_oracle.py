@@ -20,14 +20,15 @@ def words(index, seed, step):
 
 def row_choice(logits, sampler, filt, slack):
     """(token, logprob, may): the choice, its log-probability, and a dict of the tokens that a computation within
-    `slack` (relative in masses, absolute in scores) may choose, with the log-probability each then has."""
+    `slack` (relative in masses, absolute in scores) may choose, each with the log-probabilities that it may then have
+    (a token whose mass before it is within `slack` of the cut may be kept or not)."""
     seed, step, t = sampler
     k, top_p, min_p = filt
     x = np.asarray(logits, dtype=np.float64)
     real = np.flatnonzero(~np.isnan(x))
     if t <= 0 or len(real) == 0 or x[real].max() == -np.inf:
         tok = int(real[np.argmax(x[real])]) if len(real) else 0
-        return tok, 0.0, {tok: 0.0}
+        return tok, 0.0, {tok: [0.0]}
     filtered = (0 < k < len(x)) or top_p < 1 or min_p > 0
     cand = real[x[real] > -np.inf] if filtered else real
     cand = cand[np.lexsort((cand, -x[cand]))]
@@ -46,14 +47,19 @@ def row_choice(logits, sampler, filt, slack):
         if min_p > 0:
             keep &= (d >= np.log(np.float64(np.float32(min_p))) - shift) | (d == 0)
         kept = cand[keep]
-        u = ((words(kept, seed, step) >> np.uint64(8)).astype(np.float64) + 0.5) / 2.0 ** 24
-        s = x[kept] / np.float64(np.float32(t)) - np.log(-np.log(u))
+        # the sampler's uniforms as its float32 holds them: from 1/2 on the half rounds to even, and a word of 24 ones
+        # in front gives 1, whose score is infinite
+        u = np.float64((words(kept, seed, step) >> np.uint64(8)).astype(np.float32) + np.float32(0.5)) / 2.0 ** 24
+        with np.errstate(divide="ignore", invalid="ignore"):
+            s = x[kept] / np.float64(np.float32(t)) - np.log(-np.log(u))
+        s[np.isnan(s)] = -np.inf  # a logit of -inf under an infinite draw: no score beats another
         z = np.log(w[keep].sum())
         near = s >= s.max() - slack * max(1.0, abs(s.max())) if np.isfinite(s.max()) else s == s.max()
         first = int(np.flatnonzero(s == s.max())[0])
         return int(kept[first]), d[keep][first] - z, {int(kept[i]): d[keep][i] - z for i in np.flatnonzero(near)}
-    tok, lp, may = choice(0.0)
-    for shift in (-slack, slack):
+    tok, lp, _ = choice(0.0)
+    may = {}
+    for shift in (0.0, -slack, slack):
         for token, l in choice(shift)[2].items():
-            may.setdefault(token, l)
+            may.setdefault(token, []).append(l)
     return tok, lp, may
