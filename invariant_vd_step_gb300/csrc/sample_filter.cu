@@ -1129,7 +1129,7 @@ __device__ __noinline__ bool cut_unsorted(SelShared& sh, const Out& o, int r, co
 
 // wide_next: the count and collect kernels follow, and take rows that the
 // lists do not decide.  Bound by a row's chain of small steps (segment maxima,
-// gather, cut, race): 12 us for one row, 26 us for 256 of mixed settings, two to
+// gather, cut, race): 12 us for one row, 23 us for 256 of mixed settings, two to
 // an SM; sorting every list took 17 and 29 us.
 template <bool VEC>
 __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space sp, bool wide_next) {
