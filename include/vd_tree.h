@@ -89,11 +89,12 @@ int vd_step_tree(vd_tree* t, vd_kv_pool* pool, float* logits_out, void* stream);
 /* Acceptance.  choices: dev int32 [T], the token chosen after each node;
  * node_tokens: dev int32 [T] or null (the plan's token_ids).  A request's path
  * starts at its root and goes on to the lowest-numbered child whose token is
- * the one chosen after the path's last node, while there is one.
+ * the one chosen after the path's last node, while there is one and the path
+ * has fewer than out_stride nodes.
  * accepted_len: dev int32 [B], the nodes of the path (at least 1).
  * out_tokens: dev int32 [B][out_stride], row b the tokens chosen along the
  * path (accepted_len of them: the accepted drafts and one new token), then
- * -1; out_stride at least the longest path of the plan.  The K/V of the path's
+ * -1; out_stride at least 1 (a whole row holds the longest path of the plan).  The K/V of the path's
  * node at depth d is moved to slot cached_len + d, in every layer, so that
  * cached_len + accepted_len slots of the request then hold its history;
  * other slots are left as they are.  A plan is accepted once: the move

@@ -21,7 +21,6 @@ struct vd_tree {
   Desc d;
   unsigned long long pool_id = 0;
   bool planned = false, has_tokens = false;
-  int longest_path = 0;
   // device copy of the plan and split partials; both grow with the plans
   int* dev = nullptr;
   size_t dev_cap = 0;  // ints
@@ -209,13 +208,12 @@ int vd_tree_plan(vd_tree* t, vd_kv_pool* pool, const vd_tree_batch* b, void* str
     t->planned = true;
     t->has_tokens = true;
     t->pool_id = pool->id;
-    t->longest_path = 0;
     return VD_OK;
   }
   if (B == 0 || !b->cu_nodes || !b->parent || !b->cached_len || !b->page_table)
     return fail(VD_ERR_INVALID_ARG, "missing descriptor array");
   if (b->cu_nodes[0] != 0 || b->cu_nodes[B] != T) return fail(VD_ERR_INVALID_ARG, "cu_nodes must run from 0 to num_nodes");
-  int stride = 0, splits = 1, longest = 0;
+  int stride = 0, splits = 1;
   size_t paths = 0;
   std::vector<int> depth(T);
   for (int i = 0; i < B; ++i) {
@@ -235,7 +233,6 @@ int vd_tree_plan(vd_tree* t, vd_kv_pool* pool, const vd_tree_batch* b, void* str
         return fail(VD_ERR_INVALID_ARG, "parent: -1 for a request's first node, else an earlier node of the request");
       depth[k] = k == n0 ? 0 : depth[n0 + p] + 1;
       paths += depth[k] + 1;
-      longest = std::max(longest, depth[k] + 1);
       splits = std::max(splits, (cached + depth[k]) / m->split + 1);
       if (b->token_ids && (b->token_ids[k] < 0 || b->token_ids[k] >= c.vocab))
         return fail(VD_ERR_OUT_OF_RANGE, "token id out of range");
@@ -371,7 +368,6 @@ int vd_tree_plan(vd_tree* t, vd_kv_pool* pool, const vd_tree_batch* b, void* str
   t->d = d;
   t->pool_id = pool->id;
   t->has_tokens = b->token_ids != nullptr;
-  t->longest_path = longest;
   t->planned = true;
   return VD_OK;
 }
@@ -414,11 +410,11 @@ int vd_tree_accept(vd_tree* t, vd_kv_pool* pool, const int32_t* node_tokens, con
   if (const int rc = check_planned(t, pool, s)) return rc;
   if (t->d.T == 0) return VD_OK;
   if (!node_tokens && !t->has_tokens) return fail(VD_ERR_INVALID_ARG, "neither node_tokens nor token_ids in the plan");
+  if (out_stride < 1) return fail(VD_ERR_CAPACITY, "out_stride must hold a path of at least one node");
   if (!choices || !accepted_len || !out_tokens) return fail(VD_ERR_INVALID_ARG, "null argument");
   if ((reinterpret_cast<uintptr_t>(node_tokens) | reinterpret_cast<uintptr_t>(choices) |
        reinterpret_cast<uintptr_t>(accepted_len) | reinterpret_cast<uintptr_t>(out_tokens)) & 3)
     return fail(VD_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
-  if (out_stride < t->longest_path) return fail(VD_ERR_CAPACITY, "out_stride is shorter than the longest path of the plan");
   const vd_model_config& c = t->m->cfg;
   const Desc& d = t->d;
   TreeAcceptArgs a{};

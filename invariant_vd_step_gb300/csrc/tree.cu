@@ -398,6 +398,7 @@ int launch_tail_t(const TreeTailArgs& a, cudaStream_t s) {
 
 // Acceptance.  CTA (request, layer): from the root, the path goes on to the
 // lowest-numbered child that holds the token chosen after its last node.
+// A path longer than out_stride ends there.
 // Every layer's CTA finds the path for itself (no second launch), then moves
 // the K/V of the path's node at depth d from slot c + node to slot c + d.  A
 // thread moves the same 16-byte column of every node, in ascending depth: a
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(TreeAcceptA
   __syncthreads();
   if (threadIdx.x == 0) {
     int len = 0;
-    for (int i = 0; i != INT_MAX; i = next[i]) path[len++] = i;
+    for (int i = 0; i != INT_MAX && len < a.out_stride; i = next[i]) path[len++] = i;
     length = len;
   }
   __syncthreads();

@@ -697,7 +697,7 @@ class Tree:
     def accept(self, pool: KVPool, node_tokens, choices: torch.Tensor, accepted_len: torch.Tensor,
                out_tokens: torch.Tensor, stream=None):
         """vd_tree_accept: node_tokens int32 [T] or None (the plan's token_ids), choices int32 [T],
-        accepted_len int32 [B], out_tokens int32 [B][longest path or more]."""
+        accepted_len int32 [B], out_tokens int32 [B][the most nodes of a path to accept]."""
         _check_out(choices, (self.num_nodes,), torch.int32, "choices")
         if node_tokens is not None:
             _check_out(node_tokens, (self.num_nodes,), torch.int32, "node_tokens")

@@ -177,8 +177,9 @@ def test_tree_step_sampling_and_acceptance_equal_plain_decoding(name):
     assert model.device_status() == 0
 
 
+@pytest.mark.parametrize("most", [None, 1, 2, 5])
 @pytest.mark.parametrize("layers,Hkv,hd,n", [(1, 1, 64, 1), (3, 2, 64, 40), (2, 8, 128, 33), (2, 2, 256, 1024)])
-def test_accept_moves_the_path_and_nothing_else(layers, Hkv, hd, n):
+def test_accept_moves_the_path_and_nothing_else(layers, Hkv, hd, n, most):
     ready()
     spec = tree_spec(2 * Hkv, Hkv, hd, layers=layers)
     W = {k: v.cuda() for k, v in synth.make_weights(spec, seed=1).items()}
@@ -203,14 +204,14 @@ def test_accept_moves_the_path_and_nothing_else(layers, Hkv, hd, n):
     tree = vd.Tree(model, max_nodes=2 * n)
     tree.plan(pool, [0, n, 2 * n], np.concatenate(parents), cached, pt)
     got_n = torch.full((2,), -5, dtype=torch.int32, device="cuda")
-    stride = n + 3
+    stride = most or n + 3  # a path longer than that ends there
     got = torch.full((2, stride), -5, dtype=torch.int32, device="cuda")
     tree.accept(pool, torch.from_numpy(tok).cuda(), torch.from_numpy(choice).cuda(), got_n, got)
     torch.cuda.synchronize()
     want = before.clone()
     for r in range(2):
         path = [0]
-        while True:
+        while len(path) < stride:
             kids = [i for i in np.flatnonzero(parents[r] == path[-1]) if tok[r * n + i] == choice[r * n + path[-1]]]
             if not kids:
                 break
@@ -275,12 +276,12 @@ def test_refusals_leave_plan_and_memory_alone():
         sc.tree.attention(sc.pool, 0, sc.q.float(), torch.empty_like(sc.q))
     with pytest.raises(vd.VDError):
         sc.tree.step(sc.pool, torch.empty((8, spec.vocab), device="cuda"))  # no token_ids in the plan
-    n, out = torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty((2, 1), dtype=torch.int32, device="cuda")
+    n, out = torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty((2, 0), dtype=torch.int32, device="cuda")
     ch = torch.zeros(8, dtype=torch.int32, device="cuda")
     with pytest.raises(vd.VDError):
         sc.tree.accept(sc.pool, None, ch, n, out)           # no tokens
     with pytest.raises(vd.VDError) as e:
-        sc.tree.accept(sc.pool, ch, ch, n, out)             # out_tokens narrower than the longest path
+        sc.tree.accept(sc.pool, ch, ch, n, out)             # out_tokens without room for the root's choice
     assert e.value.code == 4
     s = torch.cuda.Stream()
     g = torch.cuda.CUDAGraph()
