@@ -110,7 +110,12 @@ __global__ void __launch_bounds__((NW + PROD) * 32)
   const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
   const int key_lo = FOLD ? lo_min : max(sidx * a.split, lo_min);
   const int key_hi = FOLD ? p_max : min((sidx + 1) * a.split - 1, p_max);
-  if (key_lo > key_hi) return;  // no visible key of these rows in this split
+  if (key_lo > key_hi) {  // no visible key of these rows in this split
+    // A window may leave a whole launch of a tree's shared tiles without a key;
+    // the next kernel's wait covers this grid only, so it still waits.
+    if (TREE) pdl_wait();
+    return;
+  }
   const int tile_lo = key_lo / C::BNK;
   const int ntiles = key_hi / C::BNK - tile_lo + 1;
   // Decode-shaped split CTAs (few CTAs per SM, so each copy's issue latency
@@ -585,7 +590,10 @@ __global__ void __launch_bounds__((kSfWarps + 1) * 32, 1)
   const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
   const int key_lo = max(sidx * a.split, lo_min);
   const int key_hi = min((sidx + 1) * a.split - 1, p_max);
-  if (key_lo > key_hi) return;
+  if (key_lo > key_hi) {  // (as in attn_kernel)
+    if (TREE) pdl_wait();
+    return;
+  }
   const int tile_lo = key_lo / C::BNK;
   const int ntiles = key_hi / C::BNK - tile_lo + 1;  // <= kSfTiles (checked at launch)
 

@@ -167,7 +167,10 @@ __global__ void __launch_bounds__(TcAttnCfg<HD>::THREADS, HD == 256 ? 1 : 2)
   const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
   const int key_lo = max(sidx * a.split, lo_min);
   const int key_hi = min((sidx + 1) * a.split - 1, p_max);
-  if (key_lo > key_hi) return;  // no visible key of these rows in this split
+  if (key_lo > key_hi) {  // no visible key of these rows in this split
+    if (TREE) pdl_wait();  // the wait below is not reached (as in attention.cu)
+    return;
+  }
   const int tile_lo = key_lo / C::BNK;
   const int ntiles = key_hi / C::BNK - tile_lo + 1;
   const int nstage = (ntiles + 1) >> 1;  // K/V stages: tiles 2 g and 2 g + 1 (the latter may be past the end)

@@ -32,7 +32,9 @@ __device__ __forceinline__ uint64_t globaltimer() {
 // pdl_wait returns once the grids this one depends on have completed and
 // their writes are visible (a no-op for a launch without the programmatic
 // attribute); every kernel calls it before touching memory that an earlier
-// kernel of the stream writes or reads.  pdl_trigger lets the next kernel of
+// kernel of the stream writes or reads, and some thread of every grid before it
+// ends, whatever work it finds: the next kernel's wait covers that grid alone.
+// pdl_trigger lets the next kernel of
 // the stream be scheduled (it still waits for this grid in its own pdl_wait).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
