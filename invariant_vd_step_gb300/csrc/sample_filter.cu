@@ -118,7 +118,8 @@ __device__ __forceinline__ uint64_t comp_of(float l, int i) {
 __device__ __forceinline__ int index_of(uint64_t comp) { return static_cast<int>(~static_cast<uint32_t>(comp)); }
 
 // exp((l - m) / T) for l <= m, c = log2(e) / T; 1 at m itself (also for m
-// infinite), 0 for NaN.
+// infinite), 0 for NaN.  Every token's mass is made of this (collect_quads has
+// it inline), with the one value of c that __fdiv_rn(kLog2e, T) gives.
 __device__ __forceinline__ float weight(float l, float m, float c) {
   const float w = ex2(__fmul_rn(__fsub_rn(l, m), c));
   return l == m ? 1.f : w == w ? w : 0.f;
@@ -597,16 +598,19 @@ __device__ void sort_desc(uint64_t* comp, int n) {
   }
 }
 
-__device__ __forceinline__ float weight_of(uint64_t comp, float top, float t) {
-  const float l = value_of(static_cast<uint32_t>(comp >> 32));
-  return l == top ? 1.f : expf(__fdiv_rn(__fsub_rn(l, top), t));
+// A listed token's mass, by the same operations as in the kernels that stream
+// the row: which of a row's tokens are listed depends on the kernels that a
+// call has, and may not show in the sums.
+__device__ __forceinline__ uint64_t mass_at(uint64_t comp, float top, float c) {
+  return fixed(weight(value_of(static_cast<uint32_t>(comp >> 32)), top, c));
 }
 // pre[j] = base + the masses of comp[0 .. j].
 __device__ void prefix_mass(SelShared& sh, int n, float top, float t, uint64_t base) {
   const int per = (n + kSelThreads - 1) / kSelThreads, j0 = threadIdx.x * per, j1 = min(n, j0 + per);
+  const float c = __fdiv_rn(kLog2e, t);
   uint64_t sum = 0;
   for (int j = j0; j < j1; ++j) {
-    sum += fixed(weight_of(sh.l.comp[j], top, t));
+    sum += mass_at(sh.l.comp[j], top, c);
     sh.l.pre[j] = sum;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1082,7 +1086,8 @@ __device__ __noinline__ bool cut_unsorted(SelShared& sh, const Out& o, int r, co
   const bool has_p = p.top_p < 1.f, has_k = p.top_k > 0, k_listed = has_k && p.top_k <= n;
   if (has_k && has_p && !k_listed && !complete) return false;  // top-p's share is of the top-k's mass
   const float least = min_p_least(p, top);
-  auto mass_of = [&](uint64_t cp) { return fixed(weight_of(cp, top, p.temp)); };
+  const float c = __fdiv_rn(kLog2e, p.temp);
+  auto mass_of = [&](uint64_t cp) { return mass_at(cp, top, c); };
   int below = 0;  // listed tokens that min-p drops
   float low = top;
   for (int j = threadIdx.x; j < n; j += kSelThreads) {
