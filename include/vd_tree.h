@@ -9,8 +9,10 @@
  * and the nodes from the root to itself.  Its row is bit for bit the row that
  * decoding that path token by token computes: the logits of vd_step_tree
  * equal those of vd_step on the history followed by the path, whatever the
- * rest of the tree and of the batch [B §二 Theorem 4.1].  Trees are an
- * addition of this library; the pages verify single continuations [L, §4].
+ * rest of the tree and of the batch [B §二 Theorem 4.1], be it infinite or NaN
+ * (cached K/V have to be finite where a window hides them from some of the
+ * nodes only, as in a prefill chunk).  Trees are an addition of this library;
+ * the pages verify single continuations [L, §4].
  *
  * Use, per step: vd_tree_plan() with the nodes of every request, then
  * vd_step_tree() (or the single ops per layer), a token choice for every node

@@ -170,106 +170,127 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(TreeTailArgs
 // instructions per node, on K and V rows gathered by ldmatrix address from the
 // node's path, with the other nodes' rows ignored in the scores and zero in P
 // (they add nothing to O); softmax, rescale and state are shared.  16-key
-// halves of a tile in which a node sees no key are left out: zeros again.
-// Bound by its chains' latency at two CTAs of four warps per SM (208 registers:
+// halves of a tile in which a node sees no key are left out: zeros again.  A zero
+// of P times an infinity or NaN of V is no zero, so a node's masked keys take a
+// staged row of zeros, and a CTA that finds such a value among its V rows (each
+// thread in what it copied) folds its nodes one after the other, each on the
+// state it started from.
+// Bound by its chains' latency at two CTAs of four warps per SM (210 registers:
 // Q, the state and the scores of 16 rows; three CTAs spill and measured the
 // same): at 32 trees x 64 nodes x 8 KV heads, 4 rows each, 51 us, a quarter of
-// the mma.sync rate, 11 M warp instructions.  One node per warp took 85 us.
+// the mma.sync rate, 11 M warp instructions.  One node per warp took 85 us.  The
+// look for values that are not finite takes 0.1 % of the operator there.
 template <int HD>
 struct Staged {
   static constexpr int ROW = HD * 2;  // bytes of a K or V row
-  static constexpr size_t bytes(int tail_rows) { return 128 + static_cast<size_t>(tail_rows) * 2 * ROW; }
+  // K rows, V rows, and a V row of zeros
+  static constexpr size_t bytes(int tail_rows) { return 128 + (static_cast<size_t>(tail_rows) * 2 + 1) * ROW; }
   __device__ static __forceinline__ uint32_t off(int row, int chunk) {
     return row * ROW + ((chunk & ~7) << 4) + (((chunk & 7) ^ (row & 7)) << 4);
   }
 };
 constexpr size_t kStagedBytes = 100 * 1024;  // two CTAs share an SM
 
+// Whether one of the two bf16 is an infinity or NaN (exponent all ones: adding
+// its lowest bit carries into the sign's place).
+__device__ __forceinline__ uint32_t not_finite(uint32_t two) {
+  return ((two & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+
+// A warp's part of a staged tail: the nodes [first, first + count) of one request
+// and KV head, dims [dim0, dim0 + ND).
 template <int HD, int DS>
-__global__ void __launch_bounds__(kTailWarps * 32, 2) tree_tail_staged_kernel(TreeTailArgs a) {
+struct TailFold {
   using S = Staged<HD>;
-  constexpr int BNK = 32, CH = HD / 8, ND = HD / DS;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ int row_s[kTailWarps][16][BNK];  // a tile's staged rows, of each node of a warp
-  if (skip_step(a.status)) return;
-  uint8_t* smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int dim0 = (warp % DS) * ND, gq = lane >> 2, t4 = lane & 3;
-  const int mi = lane >> 3, r8 = lane & 7;
-  // ---- item -> (request, block of nodes), KV head; the description was written before the step's first kernel
-  const int item = blockIdx.x, kvh = blockIdx.y;
-  const int b = a.blk_seq[item], n0 = a.cu_q[b], nodes = a.cu_q[b + 1] - n0, c = a.cached_len[b];
-  const int G = a.Hq / a.Hkv;
-  const int first = a.blk_first[item] + (warp / DS) * a.npg;  // this warp's first node
-  const int count = max(0, min(a.npg, nodes - first));
-  const int* table = a.page_table + static_cast<size_t>(b) * a.pt_stride;
-  const int shared = c / BNK * BNK, rows = c - shared + nodes;  // staged row i: slot shared + i
-  const uint32_t sk = smem_u32(smem), sv = sk + rows * S::ROW;
+  static constexpr int BNK = 32, ND = HD / DS;
+  int kvh, nodes, c, first, count, shared, rows, dim0;
+  const int* table;
+  uint32_t sk, sv;
   int node[2], pos[2], lo[2];
   bool valid[2];
   size_t out_row[2];  // of the row in q, and times max_splits in the partials
-  int p_max = -1, lo_min = INT_MAX;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int i = gq + 8 * r;
-    node[r] = i / G;
-    valid[r] = node[r] < count;
-    const int t = n0 + first + (valid[r] ? node[r] : 0);
-    const int p = valid[r] ? a.positions[t] : -1;
-    pos[r] = p;
-    lo[r] = valid[r] ? (a.window > 0 ? max(0, p - a.window + 1) : 0) : 1;
-    out_row[r] = static_cast<size_t>(t) * a.Hq + kvh * G + i % G;
-    p_max = max(p_max, p);
-    if (valid[r]) lo_min = min(lo_min, lo[r]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    p_max = max(p_max, __shfl_xor_sync(0xffffffffu, p_max, o));
-    lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
-  }
-  // lane n of the warp knows node n
-  const int my_t = n0 + first + min(lane, max(count - 1, 0));
-  const int my_p = lane < count ? a.positions[my_t] : -1, my_path = lane < count ? a.path_off[my_t] : 0;
-  if (!a.early) pdl_wait();
-  for (int i = threadIdx.x; i < rows * CH; i += kTailWarps * 32) {
-    const int r = i / CH, ch = i % CH, slot = shared + r;
-    const size_t row = (static_cast<size_t>(table[slot >> 4]) * 2 * a.Hkv + kvh) * 16 + (slot & 15);
-    const __nv_bfloat16* src = a.pool + row * HD + ch * 8;
-    cp_async16(smem + S::off(r, ch), src);
-    cp_async16(smem + rows * S::ROW + S::off(r, ch), src + static_cast<size_t>(a.Hkv) * 16 * HD);
-  }
+  int p_max, lo_min;
+  int my_p, my_path;  // lane n of the warp knows node n
   uint32_t qf[HD / 16][4];
   RowState<ND> st;
+
+  // The description was written before the step's first kernel.
+  __device__ __forceinline__ void init(const TreeTailArgs& a, uint32_t smem) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = blockIdx.x;
+    const int b = a.blk_seq[item], n0 = a.cu_q[b], G = a.Hq / a.Hkv;
+    kvh = blockIdx.y;
+    nodes = a.cu_q[b + 1] - n0;
+    c = a.cached_len[b];
+    first = a.blk_first[item] + (warp / DS) * a.npg;
+    count = max(0, min(a.npg, nodes - first));
+    table = a.page_table + static_cast<size_t>(b) * a.pt_stride;
+    shared = c / BNK * BNK;
+    rows = c - shared + nodes;  // staged row i: slot shared + i
+    dim0 = (warp % DS) * ND;
+    sk = smem;
+    sv = sk + rows * S::ROW;
+    p_max = -1;
+    lo_min = INT_MAX;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const __nv_bfloat16* qr = a.q + out_row[r] * HD;
+    for (int r = 0; r < 2; ++r) {
+      const int i = (lane >> 2) + 8 * r;
+      node[r] = i / G;
+      valid[r] = node[r] < count;
+      const int t = n0 + first + (valid[r] ? node[r] : 0);
+      const int p = valid[r] ? a.positions[t] : -1;
+      pos[r] = p;
+      lo[r] = valid[r] ? (a.window > 0 ? max(0, p - a.window + 1) : 0) : 1;
+      out_row[r] = static_cast<size_t>(t) * a.Hq + kvh * G + i % G;
+      p_max = max(p_max, p);
+      if (valid[r]) lo_min = min(lo_min, lo[r]);
+    }
 #pragma unroll
-    for (int kk = 0; kk < HD / 16; ++kk) {
-      qf[kk][r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + t4 * 2) : 0u;
-      qf[kk][2 + r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8 + t4 * 2) : 0u;
+    for (int o = 16; o > 0; o >>= 1) {
+      p_max = max(p_max, __shfl_xor_sync(0xffffffffu, p_max, o));
+      lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
+    }
+    const int my_t = n0 + first + min(lane, max(count - 1, 0));
+    my_p = lane < count ? a.positions[my_t] : -1;
+    my_path = lane < count ? a.path_off[my_t] : 0;
+  }
+  __device__ __forceinline__ void load_q(const TreeTailArgs& a) {
+    const int t4 = threadIdx.x & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const __nv_bfloat16* qr = a.q + out_row[r] * HD;
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        qf[kk][r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + t4 * 2) : 0u;
+        qf[kk][2 + r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8 + t4 * 2) : 0u;
+      }
     }
   }
-  if (a.early) pdl_wait();
-  pdl_trigger();
+  // The state of the split that the shared tiles began: m and l (of every warp of a
+  // node; ML) and the O of this warp's columns (which no other warp writes).  One
+  // condition for all of a row's loads (asked beside each of them, a tree of 8 nodes
+  // took 18.5 us, and 17.1 so).
+  template <bool ML>
+  __device__ __forceinline__ void load_state(const TreeTailArgs& a) {
+    const int t4 = threadIdx.x & 3;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    // the state of the split that the shared tiles began
-    const bool begun = valid[r] && max(lo[r], shared / a.split * a.split) < shared;
-    const size_t at = out_row[r] * a.max_splits + shared / a.split;
-    st.m[r] = begun ? a.part_ml[at * 2] : -INFINITY;
-    st.l[r] = begun ? a.part_ml[at * 2 + 1] : 0.f;
-    const float* po = a.part_o + at * HD + dim0;
+    for (int r = 0; r < 2; ++r) {
+      const bool begun = valid[r] && max(lo[r], shared / a.split * a.split) < shared;
+      const size_t at = out_row[r] * a.max_splits + shared / a.split;
+      if constexpr (ML) {
+        st.m[r] = begun ? a.part_ml[at * 2] : -INFINITY;
+        st.l[r] = begun ? a.part_ml[at * 2 + 1] : 0.f;
+      }
+      const float* po = a.part_o + at * HD + dim0;
 #pragma unroll
-    for (int n = 0; n < ND / 8; ++n) {
-      const float2 v = begun ? *reinterpret_cast<const float2*>(po + n * 8 + t4 * 2) : make_float2(0.f, 0.f);
-      st.o[n][2 * r] = v.x;
-      st.o[n][2 * r + 1] = v.y;
+      for (int n = 0; n < ND / 8; ++n) {
+        const float2 v = begun ? *reinterpret_cast<const float2*>(po + n * 8 + t4 * 2) : make_float2(0.f, 0.f);
+        st.o[n][2 * r] = v.x;
+        st.o[n][2 * r + 1] = v.y;
+      }
     }
   }
-  cp_async_wait_all();
-  __syncthreads();  // the rows have landed, and every warp of a node has its state before one stores another
-  if (count == 0) return;
-  auto store = [&](int r, int split) {
+  __device__ __forceinline__ void store(const TreeTailArgs& a, int r, int split) {
+    const int t4 = threadIdx.x & 3;
     const size_t at = out_row[r] * a.max_splits + split;
     if (t4 == 0 && dim0 == 0) {
       a.part_ml[at * 2] = st.m[r];
@@ -279,109 +300,187 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2) tree_tail_staged_kernel(Tr
 #pragma unroll
     for (int n = 0; n < ND / 8; ++n)
       *reinterpret_cast<float2*>(po + n * 8 + t4 * 2) = make_float2(st.o[n][2 * r], st.o[n][2 * r + 1]);
-  };
-  int key0 = max(shared, lo_min / BNK * BNK);
-  for (; key0 <= p_max; key0 += BNK) {
-    if (key0 != shared && key0 % a.split == 0) {  // the previous split is complete
+  }
+
+  // Folds the tail of the warp's nodes, or APART that of node `only`, and stores
+  // its splits.  row_s: a tile's staged rows, of each node.
+  template <bool APART>
+  __device__ __forceinline__ void fold(const TreeTailArgs& a, int (*row_s)[BNK], int only) {
+    const int lane = threadIdx.x & 31, mi = lane >> 3, r8 = lane & 7;
+    const int na = APART ? only : 0, nb = APART ? only + 1 : count;
+    auto mine = [&](int r) { return APART ? valid[r] && node[r] == only : valid[r]; };
+    int key0 = max(shared, lo_min / BNK * BNK);
+    for (; key0 <= p_max; key0 += BNK) {
+      if (key0 != shared && key0 % a.split == 0) {  // the previous split is complete
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (mine(r) && max(lo[r], key0 - a.split) <= min(pos[r], key0 - 1)) store(a, r, key0 / a.split - 1);
+          st.m[r] = -INFINITY;
+          st.l[r] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < ND / 8; ++n) st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
+      }
+      // tiles that are none of node n's: past its position, or (where it matters) below its window
+      auto skips = [&](int p) { return p < key0 || (APART && a.window > 0 && p - a.window + 1 >= key0 + BNK); };
+      // ---- scores: each node's on its own keys
+      float s[BNK / 8][4];
+#pragma unroll
+      for (int j = 0; j < BNK / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      // the row of each node's key at key0 + lane: a cached slot's, that of the path's node at that position, or past
+      // the node's own the row of zeros (as a K row, whatever lies there: masked)
+      const int key = key0 + lane;
+      __syncwarp();
+#pragma unroll 4
+      for (int n = na; n < nb; ++n) {
+        const int p = __shfl_sync(0xffffffffu, my_p, n), path = __shfl_sync(0xffffffffu, my_path, n);
+        row_s[n][lane] = key < c ? key - shared : c - shared + (key <= p ? a.path[path + key - c] : nodes);
+      }
+      __syncwarp();
+      for (int n = na; n < nb; ++n) {
+        const int p = __shfl_sync(0xffffffffu, my_p, n);
+        if (skips(p)) continue;
+        const bool both = p >= key0 + 16;
+#pragma unroll
+        for (int jp = 0; jp < BNK / 16; ++jp) {
+          if (jp == 1 && !both) continue;
+          const int kr = row_s[n][jp * 16 + (mi >> 1) * 8 + r8];
+          float x[2][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[0][e] = x[1][e] = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            uint32_t f[4];
+            ldmatrix_x4(f, sk + S::off(kr, kk * 2 + (mi & 1)));
+            mma_bf16_16816(x[0], qf[kk], f);
+            mma_bf16_16816(x[1], qf[kk], f + 2);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[2 * jp + j][e] = node[e >> 1] == n ? x[j][e] : s[2 * jp + j][e];
+        }
+      }
+      // ---- softmax of the tile, all rows
+      float mx[2], mnew[2], alpha[2], rs[2];
+      bool rv[2];
+      uint32_t pa[BNK / 16][4], pl[BNK / 16][4];
+      tile_mask_max<BNK, false>(s, mx, key0, pos, lo, a.scale_log2, lane);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) tile_running_max(st.m[r], mx[r], mnew[r], alpha[r], rv[r]);
+      tile_probs<BNK, false>(s, mnew, pa, pl, rs);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        if (valid[r] && max(lo[r], key0 - a.split) <= min(pos[r], key0 - 1)) store(r, key0 / a.split - 1);
-        st.m[r] = -INFINITY;
-        st.l[r] = 0.f;
+        tile_update_l(st.l[r], alpha[r], rs[r], rv[r]);
+        st.m[r] = mnew[r];
       }
+      tile_rescale<ND, false>(st.o, alpha);
+      // ---- P V: each node's rows of P on its own values
+      for (int n = na; n < nb; ++n) {
+        const int p = __shfl_sync(0xffffffffu, my_p, n);
+        if (skips(p)) continue;
+        const bool both = p >= key0 + 16;
 #pragma unroll
-      for (int n = 0; n < ND / 8; ++n) st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
-    }
-    // ---- scores: each node's on its own keys
-    float s[BNK / 8][4];
+        for (int ks = 0; ks < BNK / 16; ++ks) {
+          if (ks == 1 && !both) continue;
+          const int vr = row_s[n][ks * 16 + (mi & 1) * 8 + r8];
+          uint32_t ph[4], pw[4];
 #pragma unroll
-    for (int j = 0; j < BNK / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-    // the row of each node's key at key0 + lane: a cached slot's, or that of the path's node at that position
-    const int key = key0 + lane;
-    __syncwarp();
-#pragma unroll 4
-    for (int n = 0; n < count; ++n) {
-      const int p = __shfl_sync(0xffffffffu, my_p, n), path = __shfl_sync(0xffffffffu, my_path, n);
-      row_s[warp][n][lane] = key < c ? key - shared : c - shared + (key <= p ? a.path[path + key - c] : first + n);
-    }
-    __syncwarp();
-    for (int n = 0; n < count; ++n) {
-      const int p = __shfl_sync(0xffffffffu, my_p, n);
-      if (p < key0) continue;
-      const bool both = p >= key0 + 16;
+          for (int e = 0; e < 4; ++e) {
+            ph[e] = node[e & 1] == n ? pa[ks][e] : 0u;
+            pw[e] = node[e & 1] == n ? pl[ks][e] : 0u;
+          }
 #pragma unroll
-      for (int jp = 0; jp < BNK / 16; ++jp) {
-        if (jp == 1 && !both) continue;
-        const int kr = row_s[warp][n][jp * 16 + (mi >> 1) * 8 + r8];
-        float x[2][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[0][e] = x[1][e] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          uint32_t f[4];
-          ldmatrix_x4(f, sk + S::off(kr, kk * 2 + (mi & 1)));
-          mma_bf16_16816(x[0], qf[kk], f);
-          mma_bf16_16816(x[1], qf[kk], f + 2);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[2 * jp + j][e] = node[e >> 1] == n ? x[j][e] : s[2 * jp + j][e];
-      }
-    }
-    // ---- softmax of the tile, all rows
-    float mx[2], mnew[2], alpha[2], rs[2];
-    bool rv[2];
-    uint32_t pa[BNK / 16][4], pl[BNK / 16][4];
-    tile_mask_max<BNK, false>(s, mx, key0, pos, lo, a.scale_log2, lane);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) tile_running_max(st.m[r], mx[r], mnew[r], alpha[r], rv[r]);
-    tile_probs<BNK, false>(s, mnew, pa, pl, rs);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      tile_update_l(st.l[r], alpha[r], rs[r], rv[r]);
-      st.m[r] = mnew[r];
-    }
-    tile_rescale<ND, false>(st.o, alpha);
-    // ---- P V: each node's rows of P on its own values
-    for (int n = 0; n < count; ++n) {
-      const int p = __shfl_sync(0xffffffffu, my_p, n);
-      if (p < key0) continue;
-      const bool both = p >= key0 + 16;
-#pragma unroll
-      for (int ks = 0; ks < BNK / 16; ++ks) {
-        if (ks == 1 && !both) continue;
-        const int vr = row_s[warp][n][ks * 16 + (mi & 1) * 8 + r8];
-        uint32_t ph[4], pw[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ph[e] = node[e & 1] == n ? pa[ks][e] : 0u;
-          pw[e] = node[e & 1] == n ? pl[ks][e] : 0u;
-        }
-#pragma unroll
-        for (int np = 0; np < ND / 16; ++np) {
-          uint32_t f[4];
-          ldmatrix_x4_trans(f, sv + S::off(vr, dim0 / 8 + np * 2 + (mi >> 1)));
-          mma_bf16_16816(st.o[2 * np], ph, f);
-          mma_bf16_16816(st.o[2 * np], pw, f);
-          mma_bf16_16816(st.o[2 * np + 1], ph, f + 2);
-          mma_bf16_16816(st.o[2 * np + 1], pw, f + 2);
+          for (int np = 0; np < ND / 16; ++np) {
+            uint32_t f[4];
+            ldmatrix_x4_trans(f, sv + S::off(vr, dim0 / 8 + np * 2 + (mi >> 1)));
+            mma_bf16_16816(st.o[2 * np], ph, f);
+            mma_bf16_16816(st.o[2 * np], pw, f);
+            mma_bf16_16816(st.o[2 * np + 1], ph, f + 2);
+            mma_bf16_16816(st.o[2 * np + 1], pw, f + 2);
+          }
         }
       }
     }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)  // rows whose last split is the one just folded (the others' are stored)
+      if (mine(r) && pos[r] / a.split == (key0 - BNK) / a.split) store(a, r, pos[r] / a.split);
   }
-#pragma unroll
-  for (int r = 0; r < 2; ++r)  // rows whose last split is the one just folded (the others' are stored)
-    if (valid[r] && pos[r] / a.split == (key0 - BNK) / a.split) store(r, pos[r] / a.split);
+};
+
+// The nodes one after the other, each on the state it starts from (ml: m and l,
+// read before any warp of the node stored one).  Out of line: its copy of the fold
+// costs the usual one no registers.
+template <int HD, int DS>
+__device__ __noinline__ void fold_apart(const TreeTailArgs& a, uint32_t smem, int (*row_s)[32], float4 ml) {
+  TailFold<HD, DS> f;
+  f.init(a, smem);
+  f.load_q(a);
+#pragma unroll 1
+  for (int n = 0; n < f.count; ++n) {
+    f.st.m[0] = ml.x;
+    f.st.m[1] = ml.y;
+    f.st.l[0] = ml.z;
+    f.st.l[1] = ml.w;
+    f.template load_state<false>(a);
+    f.template fold<true>(a, row_s, n);
+  }
+}
+
+// MANY: a warp folds more than one node, and looks for values that are not finite
+// (with one node to a warp there is nobody to keep them from, and the look cost a
+// tree of 8 nodes 0.5 of its 17.1 us).
+template <int HD, int DS, bool MANY>
+__global__ void __launch_bounds__(kTailWarps * 32, 2) tree_tail_staged_kernel(const __grid_constant__ TreeTailArgs a) {
+  using S = Staged<HD>;
+  constexpr int BNK = 32, CH = HD / 8;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int row_s[kTailWarps][16][BNK];
+  if (skip_step(a.status)) return;
+  uint8_t* smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
+  TailFold<HD, DS> f;
+  f.init(a, smem_u32(smem));
+  uint8_t* vrows = smem + f.rows * S::ROW;
+  if (!a.early) pdl_wait();
+  for (int i = threadIdx.x; i < f.rows * CH; i += kTailWarps * 32) {
+    const int r = i / CH, ch = i % CH, slot = f.shared + r;
+    const size_t row = (static_cast<size_t>(f.table[slot >> 4]) * 2 * a.Hkv + f.kvh) * 16 + (slot & 15);
+    const __nv_bfloat16* src = a.pool + row * HD + ch * 8;
+    cp_async16(smem + S::off(r, ch), src);
+    cp_async16(vrows + S::off(r, ch), src + static_cast<size_t>(a.Hkv) * 16 * HD);
+  }
+  if (threadIdx.x < CH)
+    *reinterpret_cast<uint4*>(vrows + S::off(f.rows, threadIdx.x)) = make_uint4(0u, 0u, 0u, 0u);
+  f.load_q(a);
+  if (a.early) pdl_wait();
+  pdl_trigger();
+  f.template load_state<true>(a);
+  cp_async_wait_all();
+  int(*rows_of)[BNK] = row_s[threadIdx.x >> 5];
+  // the rows have landed, and every warp of a node has its m and l before one stores another
+  if constexpr (MANY) {
+    uint32_t sick = 0;
+    for (int i = threadIdx.x; i < f.rows * CH; i += kTailWarps * 32) {
+      const uint4 v = *reinterpret_cast<const uint4*>(vrows + S::off(i / CH, i % CH));
+      sick |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
+    }
+    if (__syncthreads_or(sick != 0)) {
+      fold_apart<HD, DS>(a, smem_u32(smem), rows_of, make_float4(f.st.m[0], f.st.m[1], f.st.l[0], f.st.l[1]));
+      return;
+    }
+  } else {
+    __syncthreads();
+  }
+  if (f.count > 0) f.template fold<false>(a, rows_of, 0);
 }
 
 template <int HD>
 int launch_tail_staged(const TreeTailArgs& a, cudaStream_t s) {
   constexpr int DS = HD == 256 ? 2 : 1;
   const size_t smem = Staged<HD>::bytes(a.tail_rows);
-  VD_CUDA_TRY(cudaFuncSetAttribute(tree_tail_staged_kernel<HD, DS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(smem)));
-  VD_CUDA_TRY(launch_k(tree_tail_staged_kernel<HD, DS>, dim3(a.n_blk, a.Hkv), dim3(kTailWarps * 32), smem, s, a));
+  auto k = a.npg > 1 ? tree_tail_staged_kernel<HD, DS, true> : tree_tail_staged_kernel<HD, DS, false>;
+  VD_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  VD_CUDA_TRY(launch_k(k, dim3(a.n_blk, a.Hkv), dim3(kTailWarps * 32), smem, s, a));
   return VD_OK;
 }
 
