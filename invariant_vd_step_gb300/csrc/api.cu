@@ -1112,7 +1112,7 @@ int vd_sample_filtered(vd_model* m, const float* logits, int32_t R, const vd_sam
   int dev = -1;
   VD_CUDA_TRY(cudaGetDevice(&dev));
   if (dev != m->device) return fail(VD_ERR_INVALID_ARG, "the model lives on another device than the current one");
-  if (m->cfg.vocab > (1 << 21)) return fail(VD_ERR_UNSUPPORTED, "filters take vocabularies of at most 2^21 tokens");
+  if (m->cfg.vocab > kFilterMaxVocab) return fail(VD_ERR_UNSUPPORTED, "filters take vocabularies of at most 2^21 tokens");
   if (!m->filter_ws) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     VD_CUDA_TRY(cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cap));
@@ -1132,7 +1132,7 @@ int vd_op_sample(const float* logits, int32_t R, int32_t V, int64_t row_stride, 
                  const vd_filter* filters, int32_t* tokens_out, float* logprobs_out, void* workspace,
                  size_t workspace_bytes, void* stream) {
   if (R < 0 || V < 1) return fail(VD_ERR_INVALID_ARG, "R >= 0 and V >= 1");
-  if (V > (1 << 21)) return fail(VD_ERR_UNSUPPORTED, "filters take vocabularies of at most 2^21 tokens");
+  if (V > kFilterMaxVocab) return fail(VD_ERR_UNSUPPORTED, "filters take vocabularies of at most 2^21 tokens");
   if (R == 0) return VD_OK;
   if (R > 1 && row_stride < V) return fail(VD_ERR_INVALID_ARG, "row_stride below V");
   if (!logits || !per_row || !tokens_out || !workspace) return fail(VD_ERR_INVALID_ARG, "null argument");

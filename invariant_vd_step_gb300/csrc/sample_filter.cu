@@ -1668,9 +1668,9 @@ int launch_scan(const SampleFilterArgs& a, const Space& sp, int nseg, int r0, in
 template <bool VEC>
 int launch_decide(const Out& o, const Space& sp, int R, bool wide, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(o.nseg) * 12;
-  if (smem + sizeof(SelShared) > 48 * 1024)
+  if (smem + sizeof(SelShared) > 48 * 1024)  // the most that any launch takes: another thread's may come in between
     VD_CUDA_TRY(cudaFuncSetAttribute(filter_select_kernel<VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem)));
+                                     (kFilterMaxVocab + kSeg - 1) / kSeg * 12));
   VD_CUDA_TRY(launch_k(filter_select_kernel<VEC>, dim3(R), dim3(kSelThreads), smem, s, o, sp, wide));
   if (!wide) return VD_OK;
   const long long most = static_cast<long long>(R) * o.nchunk, n_sm = sm_count_filter();

@@ -479,7 +479,8 @@ int launch_tail_staged(const TreeTailArgs& a, cudaStream_t s) {
   constexpr int DS = HD == 256 ? 2 : 1;
   const size_t smem = Staged<HD>::bytes(a.tail_rows);
   auto k = a.npg > 1 ? tree_tail_staged_kernel<HD, DS, true> : tree_tail_staged_kernel<HD, DS, false>;
-  VD_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  // the most that any launch takes: another thread's may come between this and the launch
+  VD_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kStagedBytes)));
   VD_CUDA_TRY(launch_k(k, dim3(a.n_blk, a.Hkv), dim3(kTailWarps * 32), smem, s, a));
   return VD_OK;
 }

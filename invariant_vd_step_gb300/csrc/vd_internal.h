@@ -280,6 +280,7 @@ int launch_sample(const float* logits, int R, int V, const vd_sampler* dev_param
                   int* out, cudaStream_t s);
 // Second pass alone: per row, the best of nchunk (score, index) partials.
 int launch_sample_final(const float* part_v, const int* part_i, int R, int nchunk, int* out, cudaStream_t s);
+constexpr int kFilterMaxVocab = 1 << 21;  // tokens of a row of the filtered token choice
 // Filtered token choice; workspace: sample_filter_workspace(R, V) bytes, 16-byte aligned.
 struct SampleFilterArgs {
   const float* logits;        // [R][ld]
