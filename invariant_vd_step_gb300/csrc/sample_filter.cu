@@ -41,6 +41,7 @@
 // rows of mixed settings 83 to 99 us by seed, 61 rows of 262144 with nuclei of
 // tens of thousands of tokens 139 us.  The floor is one read of the logits, 19.4 us and
 // 9.5 us; each kernel's comment says what it spends.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -119,7 +120,9 @@ __device__ __forceinline__ int index_of(uint64_t comp) { return static_cast<int>
 
 // exp((l - m) / T) for l <= m, c = log2(e) / T; 1 at m itself (also for m
 // infinite), 0 for NaN.  Every token's mass is made of this (collect_quads has
-// it inline), with the one value of c that __fdiv_rn(kLog2e, T) gives.
+// it inline) and of mass_rate(T), c kept finite: a difference of zero times an
+// infinite c, as of T below float32's normal range, is no zero.
+__device__ __forceinline__ float mass_rate(float t) { return fminf(__fdiv_rn(kLog2e, t), FLT_MAX); }
 __device__ __forceinline__ float weight(float l, float m, float c) {
   const float w = ex2(__fmul_rn(__fsub_rn(l, m), c));
   return l == m ? 1.f : w == w ? w : 0.f;
@@ -407,13 +410,14 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
       }
     }
     if (needs_mass(p)) {
+      const float rate = fminf(c, FLT_MAX);  // mass_rate
       float sum = 0.f;
       if (fabsf(m) < INFINITY) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            sum = __fadd_rn(sum, fmaxf(ex2(__fmul_rn(__fsub_rn(v[q][e], m), c)), 0.f));  // (the maximum drops NaN)
+            sum = __fadd_rn(sum, fmaxf(ex2(__fmul_rn(__fsub_rn(v[q][e], m), rate)), 0.f));  // (the maximum drops NaN)
       } else {  // infinite logits share the mass
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -607,7 +611,7 @@ __device__ __forceinline__ uint64_t mass_at(uint64_t comp, float top, float c) {
 // pre[j] = base + the masses of comp[0 .. j].
 __device__ void prefix_mass(SelShared& sh, int n, float top, float t, uint64_t base) {
   const int per = (n + kSelThreads - 1) / kSelThreads, j0 = threadIdx.x * per, j1 = min(n, j0 + per);
-  const float c = __fdiv_rn(kLog2e, t);
+  const float c = mass_rate(t);
   uint64_t sum = 0;
   for (int j = j0; j < j1; ++j) {
     sum += mass_at(sh.l.comp[j], top, c);
@@ -732,7 +736,7 @@ __device__ __forceinline__ void collect_quads(const float* row, int V, int q0, i
                                               float least, uint64_t clo, uint64_t chi, uint64_t* list, int* n,
                                               Race& race, uint64_t& mass) {
   const Philox ph(p);
-  const float c = __fdiv_rn(kLog2e, p.temp);
+  const float c = __fdiv_rn(kLog2e, p.temp), rate = fminf(c, FLT_MAX);  // mass_rate
   const float v_lo = value_of(static_cast<uint32_t>(clo >> 32)), v_hi = value_of(static_cast<uint32_t>(chi >> 32));
   float ratio = race.ratio_to(top, c);
   const float start = fmaxf(v_hi, least);  // no token below it counts
@@ -757,7 +761,7 @@ __device__ __forceinline__ void collect_quads(const float* row, int V, int q0, i
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const bool above = (v[e] > v_hi || (over >> e & 1)) && v[e] >= least;
-      w[e] = above ? (v[e] == top ? 1.f : ex2(__fmul_rn(__fsub_rn(v[e], top), c))) : 0.f;
+      w[e] = above ? (v[e] == top ? 1.f : ex2(__fmul_rn(__fsub_rn(v[e], top), rate))) : 0.f;
     }
     part.add4(w);
     // (a weight of zero takes no part unless the bound is so low that any token may win)
@@ -809,7 +813,7 @@ __device__ __forceinline__ void value_range(int first, int last, float top, F bi
 template <bool VEC>
 __device__ void histogram_cut(SelShared& sh, const float* row, int V, const RowParam& p, float top, bool first,
                               uint64_t ulo, bool by_count) {
-  const float c = __fdiv_rn(kLog2e, p.temp), scale = __fdiv_rn(static_cast<float>(kBins) / kBinNats, p.temp);
+  const float c = mass_rate(p.temp), scale = __fdiv_rn(static_cast<float>(kBins) / kBinNats, p.temp);
   const uint64_t lo0 = sh.clo, hi0 = sh.chi, clo = max(lo0, ulo);
   const int shift = max(0, 64 - __clzll(static_cast<long long>(hi0 - lo0)) - 11);
   auto by_value = [&](float l) {
@@ -1086,7 +1090,7 @@ __device__ __noinline__ bool cut_unsorted(SelShared& sh, const Out& o, int r, co
   const bool has_p = p.top_p < 1.f, has_k = p.top_k > 0, k_listed = has_k && p.top_k <= n;
   if (has_k && has_p && !k_listed && !complete) return false;  // top-p's share is of the top-k's mass
   const float least = min_p_least(p, top);
-  const float c = __fdiv_rn(kLog2e, p.temp);
+  const float c = mass_rate(p.temp);
   auto mass_of = [&](uint64_t cp) { return mass_at(cp, top, c); };
   int below = 0;  // listed tokens that min-p drops
   float low = top;
@@ -1179,7 +1183,7 @@ __global__ void __launch_bounds__(kSelThreads) filter_select_kernel(Out o, Space
   }
   uint64_t z = 0;
   if (needs_mass(p)) {
-    const float c = __fdiv_rn(kLog2e, p.temp);
+    const float c = mass_rate(p.temp);
     for (int i = threadIdx.x; i < o.nseg; i += kSelThreads)
       z += fixed(__fmul_rn(segs[i].sum, weight(seg_max[i], top, c)));
     z = block_sum(sh, z);

@@ -55,3 +55,21 @@ def test_narrow_rows_do_not_depend_on_wide_rows(kind, V):
         one = [choose(lg[1 + r:2 + r], s[r:r + 1], f[r:r + 1]) for r in range(0, R, 97)]
         np.testing.assert_array_equal([int(t[0]) for t, _ in one], alone[0][::97])
         np.testing.assert_array_equal([int(l[0]) for _, l in one], alone[1][::97])
+
+
+@pytest.mark.parametrize("V", [1000, 40001])
+def test_temperatures_whose_reciprocal_overflows(V):
+    """At T = 1e-40, below float32's normal range, all mass is the largest logits': log-probability 0 for one of them,
+    -log n for n that tie, and top-p keeps as many of those as it asks for."""
+    ready()
+    T = 1e-40
+    rng = np.random.default_rng(V)
+    x = -1.0 - rng.random((3, V)).astype(np.float32)
+    x[0, 77], x[1, [3, 500, 999]], x[2, [5, 6]] = 2.0, 2.0, 2.0
+    lg = torch.from_numpy(np.repeat(x, 4, axis=0)).cuda()
+    filters = [(0, 1.0, 0.0), (0, 0.9, 0.0), (0, 1.0, 0.5), (0, 0.4, 0.0)] * 3
+    tok, lp = choose(lg, [(1, k, T) for k in range(12)], filters)
+    assert tok.tolist() == [77] * 4 + [3] * 4 + [5] * 4  # every score is infinite: the lowest index
+    want = np.array([0.0] * 4 + [-np.log(3)] * 3 + [-np.log(2)] + [-np.log(2)] * 3 + [0.0])
+    # log1p's error (2 ulp) and the rounding of a mass near 2 or 3 in float32: 2^-22 of values below 2
+    assert np.all(np.abs(lp.view(np.float32) - want) <= 2.0 ** -21), lp.view(np.float32)
