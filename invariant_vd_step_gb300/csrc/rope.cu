@@ -231,6 +231,23 @@ int launch_rotary_t(const vd_rope* r, const RotaryArgs& a, cudaStream_t s) {
 
 bool bad(double v) { return !(v > 0) || isinf(v); }
 
+// Whether two of the rows [t * st + h * sh, + hd), t < T and h < H, share an
+// element: |dt * st + dh * sh| < hd for some differences, not both zero.
+bool rows_overlap(int T, int H, long long st, long long sh, int hd) {
+  using wide = __int128;
+  const wide at = st < 0 ? -wide(st) : wide(st), ah = sh < 0 ? -wide(sh) : wide(sh);
+  if ((T > 1 && at < hd) || (H > 1 && ah < hd)) return true;
+  if (T == 1 || H == 1) return false;
+  // rows of the smaller stride, again after every larger one: nested, or interleaved and looked at one by one
+  const wide small = at < ah ? at : ah, large = at < ah ? ah : at;
+  const wide n_small = at < ah ? T : H, n_large = at < ah ? H : T, span = (n_small - 1) * small;
+  for (wide d = 1; d < n_large && d * large < span + hd; ++d) {
+    const wide below = d * large / small, rest = d * large % small;
+    if ((below < n_small && rest < hd) || (below + 1 < n_small && small - rest < hd)) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -311,9 +328,7 @@ int vd_op_rotary(const vd_rope* r, const void* x, void* y, int32_t T, int32_t H,
     return fail(VD_ERR_INVALID_ARG, "pointer not aligned to its type");
   const int hd = r->cfg.head_dim;
   // the rows y[t][h] must not overlap one another, nor x's (but for the same rows in place)
-  const long long st = y_stride_t < 0 ? -y_stride_t : y_stride_t, sh = y_stride_h < 0 ? -y_stride_h : y_stride_h;
-  const long long small = std::min(H > 1 ? sh : INT64_MAX, T > 1 ? st : INT64_MAX);
-  if (small < hd || (T > 1 && H > 1 && std::max(st, sh) / (st < sh ? T : H) < std::min(st, sh)))
+  if (rows_overlap(T, H, y_stride_t, y_stride_h, hd))
     return fail(VD_ERR_INVALID_ARG, "rows of y overlap");
   const bool in_place = x == y;
   if (in_place && ((T > 1 && x_stride_t != y_stride_t) || (H > 1 && x_stride_h != y_stride_h)))
