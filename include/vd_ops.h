@@ -158,7 +158,9 @@ int vd_op_sample(const float* logits, int32_t R, int32_t V, int64_t row_stride, 
  * contiguous, token and head strides in elements (any for x; the rows of y
  * must not overlap).  y may be x itself with the same strides, else they must
  * not overlap.  Products and sums in float32, one rounding to the dtype; the
- * angle is exact to 2^-33 of a turn at every position. */
+ * angle is reduced modulo a turn to 2^-32 of it at every position (frequencies
+ * above 1, which scaling factors below 1 give, times as much), then rounded to
+ * float32, by at most 2^-28 of a turn. */
 enum { VD_DTYPE_BF16 = 0, VD_DTYPE_F16 = 1, VD_DTYPE_F32 = 2 };
 int vd_op_rotary(const vd_rope* r, const void* x, void* y, int32_t T, int32_t H, int64_t x_stride_t, int64_t x_stride_h,
                  int64_t y_stride_t, int64_t y_stride_h, int32_t dtype, const int32_t* positions, int32_t inverse,

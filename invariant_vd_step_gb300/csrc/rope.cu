@@ -3,12 +3,16 @@
 // Pair i of a head turns by angle p * f_i at position p, f_i = theta^(-2i/rot)
 // after scaling.  An angle is only needed modulo a full turn, so f_i / 2 pi
 // is held as a 64-bit fraction of a turn, tau_i = floor(2^64 f_i / 2 pi), and
-// p * tau_i in wrapping 64-bit integers *is* the reduced angle: its error is
-// at most |p| 2^-64 turns (2^-33 at the largest int32 position), where a float32
-// product p * f_i would lose every bit of a far position's angle.  The two
-// top bits (after rounding to the nearest quarter) are the quadrant, the rest
-// a float32 in [-1/4, 1/4] half-turns for sincospif.  No table is read: a
-// handle works for every position, on every device and stream.
+// p * tau_i in wrapping 64-bit integers *is* the reduced angle, where a float32
+// product p * f_i would lose every bit of a far position's angle.  Its error is
+// |p| times that of tau_i: 2^-64 turns for the floor, and as much again for f_i,
+// which is made in long double (64 bits or more) and at most 1 unless a scaling
+// factor below 1 makes it larger: 2^-32 turns at the largest int32 position (a
+// frequency held as a double would be off by 2^-25 there).  The two top bits
+// (after rounding to the nearest quarter) are the quadrant, the rest is rounded
+// to a float32 in [-1/4, 1/4] half-turns, by 2^-28 turns at most, for sincospif.
+// No table is read: a handle works for every position, on every device and
+// stream.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -289,22 +293,24 @@ int vd_rope_create(const vd_rope_config* cfg, vd_rope** out) {
   r->rot = rot;
   r->mag = static_cast<float>(mag);
   r->inv_mag = static_cast<float>(1.0 / mag);
+  // in extended precision: a position of 2^31 multiplies what a double leaves off
+  using real = long double;
+  const real full = 6.283185307179586476925286766559005768L;
   for (int i = 0; i < rot / 2; ++i) {
-    double f = pow(c.theta, -2.0 * i / rot);
+    real f = powl(c.theta, -2.0L * i / rot);
     if (c.scaling == VD_ROPE_SCALE_LINEAR) f /= c.factor;
     if (c.scaling == VD_ROPE_SCALE_BANDS) {
-      const double turns = c.original_max_position * f / two_pi;
-      const double keep = (turns - c.low_freq_factor) / (c.high_freq_factor - c.low_freq_factor);
-      const double k = std::min(std::max(keep, 0.0), 1.0);
-      f = k * f + (1.0 - k) * f / c.factor;
+      const real turns = c.original_max_position * f / full;
+      const real keep = (turns - c.low_freq_factor) / (static_cast<real>(c.high_freq_factor) - c.low_freq_factor);
+      const real k = std::min(std::max(keep, 0.0L), 1.0L);
+      f = k * f + (1 - k) * f / c.factor;
     }
     if (c.scaling == VD_ROPE_SCALE_YARN) {
-      const double ramp = std::min(std::max((i - ylo) / (yhi > ylo ? yhi - ylo : 0.001), 0.0), 1.0);
-      f = (1.0 - ramp) * f + ramp * f / c.factor;
+      const real ramp = std::min(std::max((i - ylo) / (yhi > ylo ? yhi - ylo : static_cast<real>(0.001)), 0.0L), 1.0L);
+      f = (1 - ramp) * f + ramp * f / c.factor;
     }
     // turns per position in units of 2^-64; whole turns (factors below 1) drop out
-    const long double turns = static_cast<long double>(f) / 6.283185307179586476925286766559L;
-    const long double frac = turns - floorl(turns);
+    const real turns = f / full, frac = turns - floorl(turns);
     r->turns.turn[i] = static_cast<unsigned long long>(ldexpl(frac, 64));
   }
   *out = r;
