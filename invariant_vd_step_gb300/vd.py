@@ -534,10 +534,13 @@ class KVPool:
             .view(s.n_layers, self.num_pages, 2, s.n_kv_heads, 16, s.head_dim)
 
 
-def _check_out(t, shape, dtype, name: str):
+def _check_out(t, shape, dtype, name: str, device=None):
+    """device: the GPU that the call's other tensors are on."""
     if not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
         raise VDError(VD_ERR_INVALID_ARG, f"{name}: a contiguous {dtype} CUDA tensor of shape {shape} is needed, got "
                                           f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if device is not None and t.get_device() != device:
+        raise VDError(VD_ERR_INVALID_ARG, f"{name} is on {t.device}, the call's other tensors on cuda:{device}")
 
 
 def sample_workspace(R: int, V: int, device="cuda") -> torch.Tensor:
@@ -674,8 +677,8 @@ class Tree:
     def attention(self, pool: KVPool, layer: int, q: torch.Tensor, out: torch.Tensor, stream=None):
         """vd_op_tree_attention: q, out bf16 [T][Hq][hd]."""
         shape = (self.num_nodes, self.model.spec.n_heads, self.model.spec.head_dim)
-        _check_out(q, shape, torch.bfloat16, "q")
         _check_out(out, shape, torch.bfloat16, "out")
+        _check_out(q, shape, torch.bfloat16, "q", out.get_device())
         rc = lib().vd_op_tree_attention(self._live(), pool.h, layer, q.data_ptr(), out.data_ptr(),
                                         _raw_stream(stream, out.get_device()))
         if rc:
@@ -684,8 +687,8 @@ class Tree:
     def rope_kv(self, pool: KVPool, layer: int, qkv: torch.Tensor, q_out: torch.Tensor, stream=None):
         """vd_op_tree_rope_kv: qkv bf16 [T][(Hq + 2 Hkv) hd], q_out bf16 [T][Hq][hd]."""
         s = self.model.spec
-        _check_out(qkv, (self.num_nodes, s.qkv_dim), torch.bfloat16, "qkv")
         _check_out(q_out, (self.num_nodes, s.n_heads, s.head_dim), torch.bfloat16, "q_out")
+        _check_out(qkv, (self.num_nodes, s.qkv_dim), torch.bfloat16, "qkv", q_out.get_device())
         check(lib().vd_op_tree_rope_kv(self._live(), pool.h, layer, qkv.data_ptr(), q_out.data_ptr(),
                                        _raw_stream(stream, q_out.get_device())))
 
@@ -699,14 +702,15 @@ class Tree:
         """vd_tree_accept: node_tokens int32 [T] or None (the plan's token_ids), choices int32 [T],
         accepted_len int32 [B], out_tokens int32 [B][the most nodes of a path to accept]."""
         _check_out(choices, (self.num_nodes,), torch.int32, "choices")
+        device = choices.get_device()
         if node_tokens is not None:
-            _check_out(node_tokens, (self.num_nodes,), torch.int32, "node_tokens")
-        _check_out(accepted_len, (self.num_seqs,), torch.int32, "accepted_len")
+            _check_out(node_tokens, (self.num_nodes,), torch.int32, "node_tokens", device)
+        _check_out(accepted_len, (self.num_seqs,), torch.int32, "accepted_len", device)
         stride = out_tokens.shape[-1] if out_tokens.dim() else 0
-        _check_out(out_tokens, (self.num_seqs, stride), torch.int32, "out_tokens")
+        _check_out(out_tokens, (self.num_seqs, stride), torch.int32, "out_tokens", device)
         rc = lib().vd_tree_accept(self._live(), pool.h, None if node_tokens is None else node_tokens.data_ptr(),
                                   choices.data_ptr(), accepted_len.data_ptr(), out_tokens.data_ptr(), stride,
-                                  _raw_stream(stream, choices.get_device()))
+                                  _raw_stream(stream, device))
         if rc:
             check(rc)
 
