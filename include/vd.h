@@ -168,8 +168,9 @@ typedef struct vd_filter {
  *           beta_slow times within the original context, f_i before and
  *           f_i / factor after them.
  * The rotated vector is scaled by attn_factor (0: 0.1 ln(factor) + 1 for YARN
- * with factor > 1, else 1).  HALF pairs dims (i, i + rot_dim / 2), INTERLEAVED
- * (2i, 2i + 1); the dims from rot_dim on are left as they are. */
+ * with factor > 1, else 1), which float32 has to hold, and its inverse too.
+ * HALF pairs dims (i, i + rot_dim / 2), INTERLEAVED (2i, 2i + 1); the dims from
+ * rot_dim on are left as they are. */
 enum { VD_ROPE_HALF = 0, VD_ROPE_INTERLEAVED = 1 };
 enum { VD_ROPE_SCALE_NONE = 0, VD_ROPE_SCALE_LINEAR = 1, VD_ROPE_SCALE_BANDS = 2, VD_ROPE_SCALE_YARN = 3 };
 typedef struct vd_rope vd_rope;

@@ -287,6 +287,8 @@ int vd_rope_create(const vd_rope_config* cfg, vd_rope** out) {
     yhi = std::min(ceil(dim_of(c.beta_slow)), rot - 1.0);
     if (c.attn_factor == 0 && c.factor > 1) mag = 0.1 * log(c.factor) + 1.0;
   }
+  if (!isnormal(static_cast<float>(mag)) || !isnormal(static_cast<float>(1.0 / mag)))
+    return fail(VD_ERR_INVALID_ARG, "attn_factor and its inverse must be float32 numbers");
   vd_rope* r = new (std::nothrow) vd_rope();
   if (!r) return fail(VD_ERR_CAPACITY, "out of host memory");
   r->cfg = c;

@@ -1,4 +1,7 @@
-"""Rows of the rotary op's output that overlap are refused, on the host, whatever the strides."""
+"""Refusals of the rotary op on the host: rows of the output that overlap, whatever the strides, and magnitudes that
+float32 does not hold."""
+
+import pytest
 
 from invariant_vd_step_gb300 import build, vd
 
@@ -26,3 +29,17 @@ def test_overlapping_rows_are_refused():
     least, most = -2 ** 63, 2 ** 63 - 1  # strides whose products need more than 64 bits
     for T, H, st, sh in ((3, 2, most // 2, most), (2, 2, least, least), (2, 3, most, most // 2 - 2), (2, 2, 0, least)):
         assert L.vd_op_rotary(r.h, 64, 1 << 20, T, H, 6, 6, st, sh, 0, 64, 0, None) == vd.VD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("attn_factor,taken", [(0.0, True), (1.25, True), (1e-30, True), (1e30, True), (1e-46, False),
+                                               (1e-40, False), (1e39, False), (3e38, False), (1e300, False), (1e-300, False)])
+def test_magnitudes_that_float32_holds(attn_factor, taken):
+    """The op multiplies by the magnitude, or by its inverse, in float32: neither may be zero, infinite or subnormal."""
+    build.build()
+    scaling = {"type": "linear", "factor": 2.0, "attn_factor": attn_factor}
+    if taken:
+        vd.Rope(64, scaling=scaling)
+        return
+    with pytest.raises(vd.VDError) as e:
+        vd.Rope(64, scaling=scaling)
+    assert e.value.code == vd.VD_ERR_INVALID_ARG
