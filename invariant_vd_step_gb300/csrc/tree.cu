@@ -129,10 +129,11 @@ __global__ void __launch_bounds__(kTailWarps * 32) tree_tail_kernel(TreeTailArgs
       if (max(lo, key0 - a.split) < key0) store(key0 / a.split - 1);
       clear();
     }
-    // the pool row of key key0 + lane: a cached slot, or the slot of the path's node at that position
+    // the pool row of key key0 + lane: a cached slot, or the slot of the path's node at that position (those below the
+    // window too: the decoded path's products take them, with the weight 0)
     const int key = key0 + lane;
     long long row = -1;
-    if (key >= lo && key <= p) {
+    if (key <= p) {
       const int slot = key < c ? key : c + a.path[node0 + key - c];
       row = (static_cast<long long>(table[slot >> 4]) * 2 * a.Hkv + kvh) * 16 + (slot & 15);
     }

@@ -49,3 +49,20 @@ def test_siblings_of_nodes_that_are_not_finite(Hq, Hkv, hd, B, n, window):
     assert len(keep) > B and torch.isfinite(got[keep].float()).all() and not torch.isfinite(got.float()).all()
     np.testing.assert_array_equal(bits(got[keep]), bits(finite[keep]))
     assert sc.model.device_status() == 0
+
+
+@pytest.mark.parametrize("window", [0, 9, 40])
+@pytest.mark.parametrize("Hq,Hkv,hd,n", [(8, 2, 128, 210), (4, 2, 256, 110)])
+def test_long_tails_with_nodes_that_are_not_finite(Hq, Hkv, hd, n, window):
+    """Trees whose tails shared memory does not hold; also ancestors that a window hides within its lowest tile, whose
+    weight is zero and whose values enter the decoded path's products all the same."""
+    ready()
+    trees = [(45, make_tree("chain", n)), (31, make_tree("comb", n)), (500, make_tree("random", 12, 1))]
+    sc = TreeScenario(tree_spec(Hq, Hkv, hd, window), trees, seed=hd + window)
+    for r, node, value in [(0, 60, float("inf")), (0, 101, float("nan")), (1, 80, float("-inf")), (1, 31, float("inf")),
+                           (2, 4, float("nan"))]:
+        poison(sc, r, node, value, slice(2, 9))
+    got, ref = sc.attention(), sc.decoded()
+    np.testing.assert_array_equal(bits(got), bits(ref))
+    assert torch.isfinite(got.float()).any() and not torch.isfinite(got.float()).all()
+    assert sc.model.device_status() == 0
