@@ -535,11 +535,12 @@ class KVPool:
 
 
 def _check_out(t, shape, dtype, name: str, device=None):
-    """device: the GPU that the call's other tensors are on."""
-    if not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+    """device: the GPU that the call's other tensors are on (any)."""
+    at = t.get_device()  # -1: not on a GPU
+    if at < 0 or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise VDError(VD_ERR_INVALID_ARG, f"{name}: a contiguous {dtype} CUDA tensor of shape {shape} is needed, got "
                                           f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    if device is not None and t.get_device() != device:
+    if device is not None and at != device:
         raise VDError(VD_ERR_INVALID_ARG, f"{name} is on {t.device}, the call's other tensors on cuda:{device}")
 
 
