@@ -308,9 +308,12 @@ int vd_graph_stats(const vd_model* m, int64_t* out4);
  * take finite logits].  Temperature 0: greedy argmax, lowest index on ties.
  * Temperature T > 0: Gumbel-max argmax_i(l_i / T - log(-log(u_i))) with u_i
  * from Philox4x32-10 (Salmon et al., SC'11) keyed by the row's (seed, step)
- * (host array per_row[R]; the generator is this library's choice).  The
- * result depends on the row and its state only, never on R or the other
- * rows.  Errors: VD_ERR_INVALID_ARG (null or misaligned pointers, R < 0). */
+ * (host array per_row[R]; the generator is this library's choice), the upper
+ * 24 bits of a word plus a half, times 2^-24, in float32: from 1/2 on the half
+ * rounds to even, and 24 ones (one word in 2^24) give u_i = 1, an infinite
+ * score that wins whatever the logit.  The result depends on the row and its
+ * state only, never on R or the other rows.
+ * Errors: VD_ERR_INVALID_ARG (null or misaligned pointers, R < 0). */
 int vd_sample(vd_model* m, const float* logits, int32_t R, const vd_sampler* per_row,
               int32_t* tokens_out, void* stream);
 
@@ -318,9 +321,10 @@ int vd_sample(vd_model* m, const float* logits, int32_t R, const vd_sampler* per
  * with the row's random numbers, over the tokens that the row's filters keep
  * (filters: host [R]; null: none), so that a row without filters gets
  * vd_sample's token.  logprobs_out (dev float32 [R], nullable): the
- * log-probability of the chosen token under the distribution it was drawn
- * from, softmax(l / T) over the kept tokens; 0 for a greedy row, whose filters
- * do not matter.  Tokens of logit -inf or NaN are never kept; a row without
+ * log-probability of the chosen token under softmax(l / T) over the kept
+ * tokens, from which it was drawn (but for draws that vd_sample's u_i = 1
+ * decides: 2^-24 per kept token); 0 for a greedy row, whose filters do not
+ * matter.  Tokens of logit -inf or NaN are never kept; a row without
  * any other gets vd_sample's token, at log-probability 0.  Token and
  * log-probability depend on the row, its state and its filter only, bit for
  * bit, never on R or the other rows.  A model's calls share

@@ -38,8 +38,8 @@
 // on timing, on the CTAs that share a row or on the other rows of the call.
 //
 // Measured: one row of 128256, top-k 50 and top-p 0.9, 13 us (host 11); 256
-// rows of mixed settings 83 to 99 us by seed, 61 rows of 262144 with nuclei of
-// tens of thousands of tokens 139 us.  The floor is one read of the logits, 19.4 us and
+// rows of mixed settings 83 to 101 us by seed, 61 rows of 262144 with nuclei of
+// tens of thousands of tokens 134 to 146 us.  The floor is one read of the logits, 19.4 us and
 // 9.5 us; each kernel's comment says what it spends.
 #include <float.h>
 #include <limits.h>

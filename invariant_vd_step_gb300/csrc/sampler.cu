@@ -6,7 +6,7 @@
 // 3" (SC'11), implemented here from that definition.  For vocabulary index
 // i at sampler state (seed, step): key = (seed lo, seed hi), counter =
 // (i / 4, step lo, step hi, 0x5644), word i % 4 of the block, and
-// u = ((word >> 8) + 0.5) * 2^-24 (exact in fp32, never 0 or 1).  The
+// u = ((word >> 8) + 0.5) * 2^-24 as fp32 holds it (gumbel_score).  The
 // sampler state is the per-request "sampler_0" of 深入解析 Vosti §二
 // Definition 2.1.
 //

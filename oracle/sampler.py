@@ -13,8 +13,10 @@ of the output token and advances once per emitted token.  That state is the
 Stream layout (shared contract with the CUDA sampler, stated, not shared
 code): for vocabulary index i, key = (seed & 0xffffffff, seed >> 32),
 counter = (i // 4, step & 0xffffffff, step >> 32, 0x5644), and the uniform
-is word i % 4 of the block, mapped to u = ((word >> 8) + 0.5) / 2**24, a
-24-bit uniform that float32 holds exactly and that is never 0 or 1.
+is word i % 4 of the block, mapped to u = ((word >> 8) + 0.5) / 2**24.  Here
+u is that number, never 0 or 1; the CUDA sampler has it in float32, exact
+below 1/2 and with the half rounded to even from there on: a word of 24
+leading ones (one in 2**24) gives 1 there, and an infinite score.
 
 Pinned by tests/test_oracle_sampler.py: Philox known-answer vectors from
 the Random123 distribution, a chi-square uniformity check, argmax against
