@@ -377,6 +377,10 @@ int upload_desc(vd_model* m, vd_kv_pool* pool, const vd_batch* b, bool need_toke
 int run_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv_bfloat16* q,
                   __nv_bfloat16* out, cudaStream_t s) {
   if (d.tree) return run_tree_attention(m, pool, layer, d, q, out, s);
+  if (d.kv8) {  // the pages that the step completes, then attention over the 8-bit cache
+    if (const int rc = run_kv8_seal(m, pool, layer, d, s)) return rc;
+    return run_kv8_attention(m, pool, layer, d, q, out, s);
+  }
   const vd_model_config& c = m->cfg;
   const int hd = c.head_dim;
   const int window = layer_is_local(c, layer) ? c.sliding_window : 0;

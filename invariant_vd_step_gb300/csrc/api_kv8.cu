@@ -1,0 +1,592 @@
+// C ABI of the 8-bit KV cache (vd_kv8): the cache, plans of steps over it, the
+// ops of a layer and the whole step, and page copies.
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+#include <new>
+#include <string>
+#include <unordered_set>
+#include <vector>
+
+#include "vd_internal.h"
+#include "vd_model.h"
+
+using namespace vd;
+
+struct vd_kv8 {
+  vd_model* m = nullptr;
+  unsigned long long id = 0;  // never reused, unlike the host address
+  int device = 0, format = 0, num_pages = 0;
+  void* data = nullptr;
+  bool owned = false;
+  uint8_t* codes(int layer) const { return static_cast<uint8_t*>(data) + layer * codes_layer(); }
+  float4* scales(int layer) const {
+    return reinterpret_cast<float4*>(static_cast<uint8_t*>(data) + m->cfg.n_layers * codes_layer()) +
+           layer * scales_layer();
+  }
+  long long codes_layer() const { return static_cast<long long>(num_pages) * m->cfg.n_kv_heads * 32 * m->cfg.head_dim; }
+  long long scales_layer() const { return static_cast<long long>(num_pages) * m->cfg.n_kv_heads; }
+};
+
+struct vd_kv8_plan {
+  vd_model* m = nullptr;
+  int device = 0, max_tokens = 0;
+  // the plan in force
+  Desc d;
+  unsigned long long pool_id = 0, cache_id = 0;
+  bool planned = false, has_tokens = false;
+  // device copy of the plan and split partials; both grow with the plans
+  int* dev = nullptr;
+  size_t dev_cap = 0;  // ints
+  float* part = nullptr;
+  size_t part_cap = 0;  // floats
+  int* host[2] = {nullptr, nullptr};  // pinned staging
+  size_t host_cap[2] = {0, 0};
+  cudaEvent_t uploaded[2] = {nullptr, nullptr};
+  int slot = 0;
+};
+
+namespace {
+
+int check_device(const vd_model* m) {
+  int dev = -1;
+  VD_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev != m->device) return fail(VD_ERR_INVALID_ARG, "the model lives on another device than the current one");
+  return VD_OK;
+}
+
+int check_pair(const vd_kv8* c, const vd_kv_pool* pool) {
+  if (!c || !pool) return fail(VD_ERR_INVALID_ARG, "null cache or pool");
+  if (pool->m != c->m) return fail(VD_ERR_INVALID_ARG, "the pool belongs to another model than the cache");
+  return check_device(c->m);
+}
+
+int check_call(const vd_kv8_plan* p, const vd_kv8* c, const vd_kv_pool* pool, cudaStream_t s) {
+  if (!p || !c || !pool) return fail(VD_ERR_INVALID_ARG, "null plan, cache or pool");
+  if (c->m != p->m || pool->m != p->m) return fail(VD_ERR_INVALID_ARG, "the cache or pool belongs to another model");
+  if (const int rc = check_device(p->m)) return rc;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  VD_CUDA_TRY(cudaStreamIsCapturing(s, &cap));
+  if (cap != cudaStreamCaptureStatusNone)
+    return fail(VD_ERR_UNSUPPORTED, "calls on a plan cannot be captured: it changes from step to step");
+  return VD_OK;
+}
+
+int check_planned(const vd_kv8_plan* p, const vd_kv8* c, const vd_kv_pool* pool, cudaStream_t s) {
+  if (const int rc = check_call(p, c, pool, s)) return rc;
+  if (!p->planned) return fail(VD_ERR_INVALID_ARG, "nothing has been planned");
+  if (p->pool_id != pool->id || p->cache_id != c->id)
+    return fail(VD_ERR_INVALID_ARG, "the step was planned for another cache or pool");
+  return VD_OK;
+}
+
+int check_layer(const vd_model* m, int layer) {
+  return layer < 0 || layer >= m->cfg.n_layers ? fail(VD_ERR_OUT_OF_RANGE, "layer out of range") : VD_OK;
+}
+
+// Page ids of a copy-like call.  `across`: src and dst are pages of one space.
+int check_pages(int n, const int* src, const int* dst, int src_pages, int dst_pages, bool across) {
+  if (n < 0) return fail(VD_ERR_INVALID_ARG, "negative number of pages");
+  if (n > 0 && (!src || !dst)) return fail(VD_ERR_INVALID_ARG, "null page list");
+  std::vector<unsigned char> seen(n > 0 ? dst_pages : 0, 0);
+  for (int i = 0; i < n; ++i) {
+    if (src[i] < 0 || src[i] >= src_pages || dst[i] < 0 || dst[i] >= dst_pages)
+      return fail(VD_ERR_OUT_OF_RANGE, "page id out of range");
+    if (seen[dst[i]]) return fail(VD_ERR_INVALID_ARG, "a page is written twice");
+    seen[dst[i]] = 1;
+  }
+  if (across)
+    for (int i = 0; i < n; ++i)
+      if (seen[src[i]]) return fail(VD_ERR_INVALID_ARG, "a page is both a source and a destination");
+  return VD_OK;
+}
+
+template <typename F>
+int for_pairs(int n, const int* src, const int* dst, F launch) {
+  for (int i = 0; i < n; i += kPagePairs) {
+    PagePairs p;
+    p.dev = nullptr;
+    p.n = std::min(kPagePairs, n - i);
+    for (int k = 0; k < p.n; ++k) p.at[k] = make_int2(src[i + k], dst[i + k]);
+    if (const int rc = launch(p)) return rc;
+  }
+  return VD_OK;
+}
+
+SealArgs seal_args(const vd_kv8* c, const vd_kv_pool* pool, int layer) {  // layer -1: all
+  const vd_model_config& f = c->m->cfg;
+  SealArgs a{};
+  a.pool_layer = static_cast<long long>(pool->num_pages) * 2 * f.n_kv_heads * 16 * f.head_dim;
+  a.codes_layer = c->codes_layer();
+  a.scales_layer = c->scales_layer();
+  const int l0 = std::max(layer, 0);
+  a.pool = static_cast<__nv_bfloat16*>(pool->data) + l0 * a.pool_layer;
+  a.codes = c->codes(l0);
+  a.scales = c->scales(l0);
+  a.layers = layer < 0 ? f.n_layers : 1;
+  a.Hkv = f.n_kv_heads;
+  a.hd = f.head_dim;
+  a.format = c->format;
+  return a;
+}
+
+int seal_call(vd_kv8* c, vd_kv_pool* pool, int layer, int n, const int* src, const int* dst, bool unseal, void* stream) {
+  if (const int rc = check_pair(c, pool)) return rc;
+  if (layer < -1 || layer >= c->m->cfg.n_layers) return fail(VD_ERR_OUT_OF_RANGE, "layer out of range");
+  const int np = pool->num_pages, nc = c->num_pages;
+  if (const int rc = check_pages(n, src, dst, unseal ? nc : np, unseal ? np : nc, false)) return rc;
+  const SealArgs a = seal_args(c, pool, layer);
+  return for_pairs(n, src, dst, [&](const PagePairs& p) {
+    return launch_kv8_seal(a, p, unseal, static_cast<cudaStream_t>(stream));
+  });
+}
+
+// Grows a device buffer to at least n elements (the old one is freed once the
+// device is done with it).
+template <typename T>
+int grow(T** p, size_t* cap, size_t n) {
+  if (n <= *cap) return VD_OK;
+  const size_t want = std::max(n, *cap + *cap / 2);
+  if (*p) cudaFree(*p);
+  *p = nullptr;
+  *cap = 0;
+  VD_CUDA_TRY(cudaMalloc(reinterpret_cast<void**>(p), want * sizeof(T)));
+  *cap = want;
+  return VD_OK;
+}
+
+// A call's host containers may fail to allocate; no exception leaves the C ABI.
+template <typename F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return fail(VD_ERR_CAPACITY, "out of host memory");
+  }
+}
+
+int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batch* b, cudaStream_t s) {
+  vd_model* m = t->m;
+  const vd_model_config& c = m->cfg;
+  if (!b) return fail(VD_ERR_INVALID_ARG, "null batch");
+  const int T = b->num_tokens, B = b->num_seqs, R = b->num_logit_rows;
+  if (T < 0 || B < 0 || R < 0) return fail(VD_ERR_INVALID_ARG, "negative size");
+  if (T > t->max_tokens || B > c.max_seqs || R > c.max_logit_rows)
+    return fail(VD_ERR_CAPACITY, "plan exceeds max_tokens, max_seqs or max_logit_rows");
+  if (T == 0 && B == 0) {
+    if (R > 0) return fail(VD_ERR_OUT_OF_RANGE, "logit row out of range");
+    t->d = Desc{};
+    t->planned = true;
+    t->has_tokens = true;
+    t->pool_id = pool->id;
+    t->cache_id = cache->id;
+    return VD_OK;
+  }
+  if (B == 0 || !b->cu_q || !b->cached_len || !b->open_table) return fail(VD_ERR_INVALID_ARG, "missing descriptor array");
+  if (R > 0 && !b->logit_rows) return fail(VD_ERR_INVALID_ARG, "missing logit_rows");
+  if (b->cu_q[0] != 0 || b->cu_q[B] != T) return fail(VD_ERR_INVALID_ARG, "cu_q must run from 0 to num_tokens");
+  // lengths, table widths, page ids
+  int stride = 0, open_stride = 0, splits = 1, n_seal = 0, most_q = 1, most_dec = 0;
+  for (int i = 0; i < B; ++i) {
+    const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i];
+    if (ql < 1 || b->cu_q[i + 1] > T) return fail(VD_ERR_INVALID_ARG, "every request needs q_len >= 1");
+    if (cached < 0) return fail(VD_ERR_INVALID_ARG, "negative cached_len");
+    const long long kv = static_cast<long long>(cached) + ql;
+    if (kv > c.max_context) return fail(VD_ERR_CAPACITY, "request exceeds max_context");
+    const int full = static_cast<int>(kv / 16), first = cached / 16, open = static_cast<int>((kv + 15) / 16) - first;
+    if (full > 0 && !b->page_table) return fail(VD_ERR_INVALID_ARG, "missing page_table");
+    if (full > b->page_table_stride || open > b->open_stride)
+      return fail(VD_ERR_OUT_OF_RANGE, "page table narrower than the request");
+    stride = std::max(stride, full);
+    open_stride = std::max(open_stride, open);
+    splits = std::max(splits, static_cast<int>((kv - 1) / kAttn8Split) + 1);
+    n_seal += full - first;
+    if (ql * m->G <= 16) {
+      most_q = std::max(most_q, ql);
+      most_dec = std::max(most_dec, ql * m->G);
+    }
+  }
+  for (int k = 0; b->token_ids && k < T; ++k)
+    if (b->token_ids[k] < 0 || b->token_ids[k] >= c.vocab) return fail(VD_ERR_OUT_OF_RANGE, "token id out of range");
+  for (int j = 0; j < R; ++j)
+    if (b->logit_rows[j] < 0 || b->logit_rows[j] >= T) return fail(VD_ERR_OUT_OF_RANGE, "logit row out of range");
+  std::vector<unsigned char> sealed(cache->num_pages, 0);  // pages that the step seals
+  std::unordered_set<long long> written;
+  written.reserve(static_cast<size_t>(T) * 2);
+  for (int i = 0; i < B; ++i) {
+    const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i], first = cached / 16;
+    const int* ot = b->open_table + static_cast<size_t>(i) * b->open_stride;
+    for (int j = 0; j < (cached + ql + 15) / 16 - first; ++j)
+      if (ot[j] < 0 || ot[j] >= pool->num_pages) return fail(VD_ERR_OUT_OF_RANGE, "page id of the open table out of range");
+    for (int k = 0; k < ql; ++k) {
+      const int pos = cached + k;
+      if (!written.insert(static_cast<long long>(ot[pos / 16 - first]) * 16 + (pos & 15)).second)
+        return fail(VD_ERR_INVALID_ARG, "two new tokens of the step write the same KV slot");
+    }
+    for (int j = first; j < (cached + ql) / 16; ++j) {
+      const int pg = b->page_table[static_cast<size_t>(i) * b->page_table_stride + j];
+      if (pg < 0 || pg >= cache->num_pages) return fail(VD_ERR_OUT_OF_RANGE, "page id out of range");
+      if (sealed[pg]) return fail(VD_ERR_INVALID_ARG, "a page of the cache is sealed twice");
+      sealed[pg] = 1;
+    }
+  }
+  for (int i = 0; i < B; ++i) {
+    const int* pt = b->page_table + static_cast<size_t>(i) * b->page_table_stride;
+    for (int j = 0; j < b->cached_len[i] / 16; ++j) {
+      if (pt[j] < 0 || pt[j] >= cache->num_pages) return fail(VD_ERR_OUT_OF_RANGE, "page id out of range");
+      if (sealed[pt[j]]) return fail(VD_ERR_INVALID_ARG, "the step seals a page that a row sees as an earlier one");
+    }
+  }
+
+  // the image
+  Desc d;
+  d.T = T;
+  d.B = B;
+  d.R = R;
+  d.stride = stride;
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t o = off;
+    off += n;
+    return static_cast<int>(o);
+  };
+  d.seal = take(2 * static_cast<size_t>(n_seal));  // int2: first, for its alignment
+  d.n_seal = n_seal;
+  d.tokens = take(T);
+  d.positions = take(T);
+  d.slot_page = take(T);
+  d.logit_rows = take(R);
+  d.cu_q = take(B + 1);
+  d.cached = take(B);
+  d.dec_seq = take(B);
+  d.dec_start = take(B + 1);
+  d.pre_seq = take(B);
+  d.pre_start = take(B + 1);
+  d.open_stride = open_stride;
+  d.open_table = take(static_cast<size_t>(B) * open_stride);
+  d.page_table = take(static_cast<size_t>(B) * stride);
+  if (off > (1u << 30)) return fail(VD_ERR_CAPACITY, "plan too large");
+  d.total = static_cast<int>(off);
+  d.part_splits = splits;
+  d.own_slots = most_q > 1 ? 2 : 1;
+  d.lower8 = most_dec <= 8;
+  long long items[2] = {0, 0};
+  auto items_of = [&](int i, int rows_per_cta) {
+    const int ql = b->cu_q[i + 1] - b->cu_q[i], kv = b->cached_len[i] + ql;
+    return static_cast<long long>((ql * m->G + rows_per_cta - 1) / rows_per_cta) * c.n_kv_heads * ((kv - 1) / kAttn8Split + 1);
+  };
+  for (int i = 0; i < B; ++i) items[(b->cu_q[i + 1] - b->cu_q[i]) * m->G > 16] += items_of(i, 16);
+  if (items[0] > 0x7fffffffLL || items[1] > 0x7fffffffLL) return fail(VD_ERR_CAPACITY, "plan too large");
+
+  const int slot = t->slot;
+  VD_CUDA_TRY(cudaEventSynchronize(t->uploaded[slot]));  // this staging buffer's previous copy is done
+  if (t->host_cap[slot] < off) {
+    if (t->host[slot]) cudaFreeHost(t->host[slot]);
+    t->host[slot] = nullptr;
+    t->host_cap[slot] = 0;
+    VD_CUDA_TRY(cudaMallocHost(reinterpret_cast<void**>(&t->host[slot]), off * 2 * sizeof(int)));
+    t->host_cap[slot] = off * 2;
+  }
+  const size_t rows = static_cast<size_t>(T) * c.n_heads * splits;
+  int rc;
+  if (off > t->dev_cap || rows * (c.head_dim + 2) > t->part_cap) t->planned = false;  // the old plan's buffers go
+  if ((rc = grow(&t->dev, &t->dev_cap, off)) || (rc = grow(&t->part, &t->part_cap, rows * (c.head_dim + 2)))) return rc;
+  int* h = t->host[slot];
+  int ns = 0;
+  for (int i = 0; i < B; ++i) {
+    const int q0 = b->cu_q[i], ql = b->cu_q[i + 1] - q0, cached = b->cached_len[i], first = cached / 16;
+    const int full = (cached + ql) / 16, open = (cached + ql + 15) / 16 - first;
+    for (int j = 0; j < stride; ++j)
+      h[d.page_table + static_cast<size_t>(i) * stride + j] =
+          j < full ? b->page_table[static_cast<size_t>(i) * b->page_table_stride + j] : 0;
+    for (int j = 0; j < open_stride; ++j)
+      h[d.open_table + static_cast<size_t>(i) * open_stride + j] =
+          j < open ? b->open_table[static_cast<size_t>(i) * b->open_stride + j] : 0;
+    for (int j = first; j < full; ++j, ++ns) {
+      h[d.seal + 2 * ns] = h[d.open_table + static_cast<size_t>(i) * open_stride + j - first];
+      h[d.seal + 2 * ns + 1] = h[d.page_table + static_cast<size_t>(i) * stride + j];
+    }
+    for (int k = 0; k < ql; ++k) {
+      h[d.tokens + q0 + k] = b->token_ids ? b->token_ids[q0 + k] : 0;
+      h[d.positions + q0 + k] = cached + k;
+      h[d.slot_page + q0 + k] = h[d.open_table + static_cast<size_t>(i) * open_stride + (cached + k) / 16 - first];
+    }
+    h[d.cu_q + i] = q0;
+    h[d.cached + i] = cached;
+    if (ql * m->G <= 16) {
+      h[d.dec_seq + d.n_dec] = i;
+      h[d.dec_start + d.n_dec++] = d.items_dec;
+      d.items_dec += static_cast<int>(items_of(i, 16));
+    } else {
+      h[d.pre_seq + d.n_pre] = i;
+      h[d.pre_start + d.n_pre++] = d.items_pre;
+      d.items_pre += static_cast<int>(items_of(i, 16));
+    }
+  }
+  h[d.cu_q + B] = T;
+  h[d.dec_start + d.n_dec] = d.items_dec;
+  h[d.pre_start + d.n_pre] = d.items_pre;
+  for (int j = 0; j < R; ++j) h[d.logit_rows + j] = b->logit_rows[j];
+  d.base = t->dev;
+  d.part_o = t->part;
+  d.part_ml = t->part + rows * c.head_dim;
+  d.kv8 = cache;
+  t->planned = false;  // until the new plan is on its way
+  VD_CUDA_TRY(cudaMemcpyAsync(t->dev, h, off * sizeof(int), cudaMemcpyHostToDevice, s));
+  VD_CUDA_TRY(cudaEventRecord(t->uploaded[slot], s));
+  t->slot ^= 1;
+  t->d = d;
+  t->pool_id = pool->id;
+  t->cache_id = cache->id;
+  t->has_tokens = b->token_ids != nullptr;
+  t->planned = true;
+  return VD_OK;
+}
+
+}  // namespace
+
+int vd::run_kv8_seal(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, cudaStream_t s) {
+  if (d.n_seal == 0) return VD_OK;
+  Prof p(m, K_ROPE, s);
+  PagePairs pairs;
+  pairs.dev = reinterpret_cast<const int2*>(d.base + d.seal);
+  pairs.n = d.n_seal;
+  return launch_kv8_seal(seal_args(d.kv8, pool, layer), pairs, false, s);
+}
+
+int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv_bfloat16* q,
+                          __nv_bfloat16* out, cudaStream_t s) {
+  const vd_model_config& c = m->cfg;
+  Attn8Args a{};
+  a.q = q;
+  a.part_o = d.part_o;
+  a.part_ml = d.part_ml;
+  a.cu_q = d.base + d.cu_q;
+  a.cached_len = d.base + d.cached;
+  a.page_table = d.base + d.page_table;
+  a.open_table = d.base + d.open_table;
+  a.codes = d.kv8->codes(layer);
+  a.scales = d.kv8->scales(layer);
+  a.pt_stride = d.stride;
+  a.open_stride = d.open_stride;
+  a.Hq = c.n_heads;
+  a.Hkv = c.n_kv_heads;
+  a.layer_row0 = static_cast<int>(static_cast<long long>(layer) * pool->num_pages * 2 * c.n_kv_heads * 16);
+  a.window = layer_is_local(c, layer) ? c.sliding_window : 0;
+  a.max_splits = d.part_splits;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(c.head_dim)));
+  a.status = m->status;
+  int rc;
+  if (d.n_dec) {
+    Prof p(m, K_ATTN, s);
+    a.cls_seq = d.base + d.dec_seq;
+    a.cls_start = d.base + d.dec_start;
+    a.n_cls = d.n_dec;
+    a.own_slots = d.own_slots;
+    if ((rc = launch_attention8(pool->map, a, c.head_dim, d.kv8->format, d.lower8, d.items_dec, s))) return rc;
+  }
+  if (d.n_pre) {
+    Prof p(m, K_ATTN, s);
+    a.cls_seq = d.base + d.pre_seq;
+    a.cls_start = d.base + d.pre_start;
+    a.n_cls = d.n_pre;
+    a.own_slots = 2;
+    if ((rc = launch_attention8(pool->map, a, c.head_dim, d.kv8->format, false, d.items_pre, s))) return rc;
+  }
+  MergeArgs g{};
+  g.part_o = d.part_o;
+  g.part_ml = d.part_ml;
+  g.out = out;
+  g.positions = d.base + d.positions;
+  g.T = d.T;
+  g.Hq = c.n_heads;
+  g.window = a.window;
+  g.split = kAttn8Split;
+  g.max_splits = d.part_splits;
+  Prof p(m, K_MERGE, s);
+  return launch_merge(g, c.head_dim, s);
+}
+
+extern "C" {
+
+size_t vd_kv8_bytes(const vd_model* m, int32_t num_pages) {
+  if (!m || num_pages < 0) return 0;
+  return static_cast<size_t>(m->cfg.n_layers) * num_pages * m->cfg.n_kv_heads * (32 * m->cfg.head_dim + 16);
+}
+
+int vd_kv8_create(vd_model* m, int32_t format, int32_t num_pages, void* dev_mem, size_t bytes, vd_kv8** out) {
+  if (!out) return fail(VD_ERR_INVALID_ARG, "null argument");
+  *out = nullptr;
+  if (check_model(m)) return VD_ERR_INVALID_ARG;
+  if (format != VD_KV8_INT8 && format != VD_KV8_E4M3) return fail(VD_ERR_INVALID_ARG, "format: VD_KV8_INT8 or VD_KV8_E4M3");
+  if (num_pages < 1) return fail(VD_ERR_INVALID_ARG, "num_pages must be >= 1");
+  if (const int rc = check_device(m)) return rc;
+  const size_t need = vd_kv8_bytes(m, num_pages);
+  if (dev_mem && bytes < need) return fail(VD_ERR_CAPACITY, "dev_mem smaller than vd_kv8_bytes()");
+  if (reinterpret_cast<uintptr_t>(dev_mem) & 255) return fail(VD_ERR_INVALID_ARG, "dev_mem must be 256-byte aligned");
+  vd_kv8* c = new (std::nothrow) vd_kv8();
+  if (!c) return fail(VD_ERR_CAPACITY, "out of host memory");
+  static std::atomic<unsigned long long> next_id{1};
+  c->m = m;
+  c->id = next_id++;
+  c->device = m->device;
+  c->format = format;
+  c->num_pages = num_pages;
+  c->data = dev_mem;
+  if (!dev_mem) {
+    if (cudaMalloc(&c->data, need) != cudaSuccess) {
+      delete c;
+      return fail(VD_ERR_CUDA, "cudaMalloc(8-bit cache) failed");
+    }
+    c->owned = true;
+  }
+  if (cudaMemset(c->data, 0, need) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    vd_destroy_kv8(c);
+    return fail(VD_ERR_CUDA, "cudaMemset(8-bit cache) failed");
+  }
+  *out = c;
+  return VD_OK;
+}
+
+void vd_destroy_kv8(vd_kv8* c) {
+  if (!c) return;
+  if (c->owned && c->data) {
+    int dev = c->device;
+    cudaGetDevice(&dev);
+    if (dev != c->device) cudaSetDevice(c->device);
+    cudaDeviceSynchronize();
+    cudaFree(c->data);
+    if (dev != c->device) cudaSetDevice(dev);
+  }
+  delete c;
+}
+
+void* vd_kv8_data(vd_kv8* c) { return c ? c->data : nullptr; }
+
+int vd_kv8_seal(vd_kv8* c, vd_kv_pool* pool, int32_t layer, int32_t n, const int32_t* src, const int32_t* dst,
+                void* stream) {
+  return guarded([&] { return seal_call(c, pool, layer, n, src, dst, false, stream); });
+}
+int vd_kv8_unseal(vd_kv8* c, vd_kv_pool* pool, int32_t layer, int32_t n, const int32_t* src, const int32_t* dst,
+                  void* stream) {
+  return guarded([&] { return seal_call(c, pool, layer, n, src, dst, true, stream); });
+}
+
+int vd_kv8_plan_create(vd_model* m, int32_t max_tokens, vd_kv8_plan** out) {
+  if (!out) return fail(VD_ERR_INVALID_ARG, "null argument");
+  *out = nullptr;
+  if (check_model(m)) return VD_ERR_INVALID_ARG;
+  if (max_tokens < 1) return fail(VD_ERR_INVALID_ARG, "max_tokens must be >= 1");
+  if (max_tokens > m->cfg.max_tokens) return fail(VD_ERR_CAPACITY, "max_tokens exceeds the model's");
+  if (const int rc = check_device(m)) return rc;
+  vd_kv8_plan* t = new (std::nothrow) vd_kv8_plan();
+  if (!t) return fail(VD_ERR_CAPACITY, "out of host memory");
+  t->m = m;
+  t->device = m->device;
+  t->max_tokens = max_tokens;
+  for (cudaEvent_t& e : t->uploaded)
+    if (cudaEventCreateWithFlags(&e, cudaEventDisableTiming) != cudaSuccess) {
+      vd_destroy_kv8_plan(t);
+      return fail(VD_ERR_CUDA, "cudaEventCreate failed");
+    }
+  *out = t;
+  return VD_OK;
+}
+
+void vd_destroy_kv8_plan(vd_kv8_plan* t) {
+  if (!t) return;
+  int dev = t->device;  // the caller's current device, put back below
+  cudaGetDevice(&dev);
+  if (dev != t->device) cudaSetDevice(t->device);
+  cudaDeviceSynchronize();
+  for (int k = 0; k < 2; ++k) {
+    if (t->host[k]) cudaFreeHost(t->host[k]);
+    if (t->uploaded[k]) cudaEventDestroy(t->uploaded[k]);
+  }
+  if (t->dev) cudaFree(t->dev);
+  if (t->part) cudaFree(t->part);
+  if (dev != t->device) cudaSetDevice(dev);
+  delete t;
+}
+
+int vd_kv8_plan_make(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, const vd_kv8_batch* b, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (const int rc = check_call(p, c, pool, s)) return rc;
+  return guarded([&] { return make_plan(p, c, pool, b, s); });
+}
+
+int vd_op_kv8_rope_kv(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, int32_t layer, const void* qkv, void* q_out,
+                      void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int rc;
+  if ((rc = check_planned(p, c, pool, s)) || (rc = check_layer(p->m, layer))) return rc;
+  if (p->d.T == 0) return VD_OK;
+  if (!qkv || !q_out) return fail(VD_ERR_INVALID_ARG, "null argument");
+  if (!aligned16(qkv) || !aligned16(q_out)) return fail(VD_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  return run_rope(p->m, pool, layer, p->d, static_cast<const __nv_bfloat16*>(qkv), static_cast<__nv_bfloat16*>(q_out), s);
+}
+
+int vd_op_kv8_seal(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, int32_t layer, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int rc;
+  if ((rc = check_planned(p, c, pool, s)) || (rc = check_layer(p->m, layer))) return rc;
+  return p->d.T == 0 ? VD_OK : run_kv8_seal(p->m, pool, layer, p->d, s);
+}
+
+int vd_op_kv8_attention(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, int32_t layer, const void* q, void* out,
+                        void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int rc;
+  if ((rc = check_planned(p, c, pool, s)) || (rc = check_layer(p->m, layer))) return rc;
+  if (p->d.T == 0) return VD_OK;
+  if (!q || !out) return fail(VD_ERR_INVALID_ARG, "null argument");
+  if (!aligned16(q) || !aligned16(out)) return fail(VD_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  return run_kv8_attention(p->m, pool, layer, p->d, static_cast<const __nv_bfloat16*>(q),
+                           static_cast<__nv_bfloat16*>(out), s);
+}
+
+int vd_step_kv8(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, float* logits_out, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (const int rc = check_planned(p, c, pool, s)) return rc;
+  if (!p->has_tokens) return fail(VD_ERR_INVALID_ARG, "the plan has no token_ids");
+  if (p->d.T == 0) return VD_OK;
+  if (p->d.R > 0 && (!logits_out || !aligned16(logits_out)))
+    return fail(VD_ERR_INVALID_ARG, "logits_out null or not 16-byte aligned");
+  return enqueue_step(p->m, pool, p->d, logits_out, nullptr, s);
+}
+
+int vd_kv_copy_pages(vd_kv_pool* pool, int32_t n, const int32_t* src, const int32_t* dst, void* stream) {
+  if (!pool) return fail(VD_ERR_INVALID_ARG, "null pool");
+  return guarded([&]() -> int {
+    int rc;
+    if ((rc = check_device(pool->m)) || (rc = check_pages(n, src, dst, pool->num_pages, pool->num_pages, true))) return rc;
+    const vd_model_config& f = pool->m->cfg;
+    CopyArgs a{};
+    a.data = static_cast<uint8_t*>(pool->data);
+    a.bytes = 2LL * f.n_kv_heads * 16 * f.head_dim * 2;
+    a.layer = a.bytes * pool->num_pages;
+    a.layers = f.n_layers;
+    return for_pairs(n, src, dst, [&](const PagePairs& p) { return launch_copy_pages(a, p, static_cast<cudaStream_t>(stream)); });
+  });
+}
+
+int vd_kv8_copy_pages(vd_kv8* c, int32_t n, const int32_t* src, const int32_t* dst, void* stream) {
+  if (!c) return fail(VD_ERR_INVALID_ARG, "null cache");
+  return guarded([&]() -> int {
+    int rc;
+    if ((rc = check_device(c->m)) || (rc = check_pages(n, src, dst, c->num_pages, c->num_pages, true))) return rc;
+    const vd_model_config& f = c->m->cfg;
+    CopyArgs a{};
+    a.data = c->codes(0);
+    a.bytes = 32LL * f.n_kv_heads * f.head_dim;
+    a.layer = c->codes_layer();
+    a.extra = c->scales(0);
+    a.extra_layer = c->scales_layer();
+    a.n_extra = f.n_kv_heads;
+    a.layers = f.n_layers;
+    return for_pairs(n, src, dst, [&](const PagePairs& p) { return launch_copy_pages(a, p, static_cast<cudaStream_t>(stream)); });
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,525 @@
+// Attention over the 8-bit KV cache: mma.sync kernel.
+//
+// Rows and splits are those of attention.cu: for request b and KV head g the
+// (token, query head of the group) pairs, token-major, in blocks of 16, and
+// splits of 512 keys.  A split is four chunks of 128 keys (eight pages), one per
+// warp.  What a row sees of a page i: its 8-bit version if i < own = floor(p /
+// 16), its bf16 version if i = own, nothing beyond.
+//
+// Per chunk and row, with codes c, K scale k, V scale v of each page and
+// everything else float32 unless stated:
+//   t_j = (q c_j) k scale + log2 v       (the product in fp16, exact operands)
+//   m   = max_j t_j,   p_j = 2^(t_j - m)
+//   l   = sum_j p_j / v,   O = sum_j fp16(p_j) c_j
+// so O / l is the softmax's mean of the values: the V scale rides in the
+// exponent and the codes enter the product as they are.  fp16(p) is off by 2^-12
+// of p or 2^-25 (the largest p of a chunk is 1), where bf16 would be off by 2^-9.
+// The row's own page takes part with a scale per token, a power of two that
+// makes its bf16 values exact in fp16 (kv8.cuh).  No state is rescaled within a
+// chunk: its 128 scores are all there before the maximum is taken.
+//
+// Order: the pages of a chunk ascending, the own page last; partial sums of l
+// over keys {2t, 2t+1, 8+2t, 9+2t} of each page in thread t of four, then (s_0 +
+// s_1) + (s_2 + s_3); the chunks of a split folded left to right with the merge
+// kernel's arithmetic, then the splits by the merge kernel.  A masked key has the
+// weight 0 and adds +0 to every sum.  None of it depends on the batch, the block
+// a row is in or the other rows.
+#include <math.h>
+
+#include "attn_tile.cuh"
+#include "kv8.cuh"
+#include "vd_internal.h"
+
+namespace vd {
+namespace {
+
+constexpr int kSplit8 = 512;   // keys of a split
+constexpr int kChunk8 = 128;   // keys of a chunk
+constexpr int kChunkPages = kChunk8 / 16;
+
+template <int HD, int SL>
+struct Attn8Cfg {
+  static constexpr int PART = Kv8Cfg<HD>::PART;
+  static constexpr int OWN = 2 * 32 * HD;  // K and V of one bf16 page
+  static constexpr int RING = SL * PART;   // per warp
+  static_assert(RING >= 16 * HD * 4, "the chunk's O fits the warp's ring");
+  static constexpr int smem(int own_slots) { return 1024 + own_slots * OWN + 4 * RING + (4 * SL + 2) * 8 + 16; }
+};
+
+// LOWER8: the block holds at most 8 rows (their lanes' second rows hold none).
+template <int HD, int FMT, int SL, bool LOWER8>
+__global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUtensorMap kvmap, Attn8Args a) {
+  using C = Attn8Cfg<HD, SL>;
+  constexpr int NR = LOWER8 ? 1 : 2;  // rows per lane
+  constexpr int KK = HD / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gq = lane >> 2, t4 = lane & 3;
+  uint8_t* own_s = smem;
+  uint8_t* ring0 = smem + a.own_slots * C::OWN;
+  uint8_t* ring = ring0 + warp * C::RING;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring0 + 4 * C::RING);
+  uint64_t* bar = bars + warp * SL;
+  uint64_t* own_bar = bars + 4 * SL;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(own_bar + 2);
+  __shared__ float fold_m[4][16], fold_l[4][16];
+
+  // Up to the wait for the previous kernel the CTA reads only the status word and
+  // the plan (uploaded before the step's first kernel).
+  {
+    __shared__ int skip;
+    if (threadIdx.x == 0) skip = a.status ? *reinterpret_cast<volatile int*>(a.status) : 0;
+    __syncthreads();
+    if (skip) return;
+  }
+  const int item = blockIdx.x;
+  int lo_i = 0, hi_i = a.n_cls - 1;
+  while (lo_i < hi_i) {  // last j with cls_start[j] <= item: 32 of them per memory round trip
+    const int step = (hi_i - lo_i) / 32 + 1, j = lo_i + lane * step;
+    const unsigned at = __ballot_sync(0xffffffffu, j <= hi_i && a.cls_start[j] <= item);  // lane 0 always
+    lo_i += (31 - __clz(at)) * step;
+    hi_i = min(hi_i, lo_i + step - 1);
+  }
+  const int b = a.cls_seq[lo_i];
+  int local = item - a.cls_start[lo_i];
+  const int q0 = a.cu_q[b], qlen = a.cu_q[b + 1] - q0, cached = a.cached_len[b];
+  const int kv_len = cached + qlen;
+  const int G = a.Hq / a.Hkv;
+  const int nsplit = (kv_len - 1) / kSplit8 + 1;
+  const int sidx = local % nsplit;
+  local /= nsplit;
+  const int kvh = local % a.Hkv;
+  const int rows = qlen * G;
+  const int r0 = (local / a.Hkv) * 16;
+  const int r_end = min(rows, r0 + 16);
+  const int p_min = cached + r0 / G, p_max = cached + (r_end - 1) / G;
+  const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
+  if (max(sidx * kSplit8, lo_min) > min(sidx * kSplit8 + kSplit8 - 1, p_max)) {  // no visible key of these rows
+    pdl_wait();  // the next kernel's wait covers this grid only, and this may be all of it
+    return;
+  }
+  // this warp's chunk: pages [a8, a8 + n8) in 8 bits, [ao, ao + no) in bf16
+  const int pg0 = (sidx * kSplit8 + warp * kChunk8) >> 4;
+  const int own_lo = p_min >> 4, own_hi = p_max >> 4;
+  const int a8 = max(pg0, lo_min >> 4), n8 = max(0, min(pg0 + kChunkPages, own_hi) - a8);
+  const int ao = max(pg0, own_lo), no = max(0, min(pg0 + kChunkPages - 1, own_hi) - ao + 1);
+  int pid = 0, opid = 0;
+  if (lane < n8) pid = a.page_table[static_cast<size_t>(b) * a.pt_stride + a8 + lane];
+  if (lane < no) opid = a.open_table[static_cast<size_t>(b) * a.open_stride + ao + lane - (cached >> 4)];
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 4 * SL + 2; ++k) mbar_init(&bars[k], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  // Copies of this warp: its K pages, then its V pages, copy j into slot j % SL,
+  // issued by the lane that holds the page's id.
+  const uint8_t* page = a.codes + (static_cast<size_t>(pid) * a.Hkv + kvh) * (2 * C::PART);
+  auto issue = [&](int j, bool v) {
+    uint64_t* f = &bar[j % SL];
+    mbar_arrive_expect_tx(f, C::PART);
+    bulk_load(ring + (j % SL) * C::PART, page + (v ? C::PART : 0), C::PART, f);
+  };
+  if (lane < n8 && lane < SL) issue(lane, false);
+  if (lane < n8 && n8 + lane < SL) issue(n8 + lane, true);
+  int issued = min(SL, 2 * n8);
+  if (lane < no) {
+    const int o = ao + lane - own_lo, row = a.layer_row0 + ((opid * 2) * a.Hkv + kvh) * 16;
+    mbar_arrive_expect_tx(&own_bar[o], C::OWN);
+    tma_load_3d(own_s + o * C::OWN, &kvmap, &own_bar[o], 0, 0, row);
+    tma_load_3d(own_s + o * C::OWN + C::OWN / 2, &kvmap, &own_bar[o], 0, 0, row + a.Hkv * 16);
+  }
+  float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (lane < n8) sc = a.scales[static_cast<size_t>(pid) * a.Hkv + kvh];
+
+  // ---- this lane's rows g (and g + 8), their queries as fp16 fragments
+  int pos[NR], lo[NR], own[NR], tok[NR], hq[NR];
+  bool valid[NR];
+  uint32_t qf[KK][4];
+  float rowfac[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int row = r0 + gq + 8 * r;
+    valid[r] = row < rows;
+    tok[r] = row / G;
+    hq[r] = kvh * G + row % G;
+    pos[r] = valid[r] ? cached + tok[r] : -1;
+    own[r] = pos[r] >> 4;  // -1 for a row that is none
+    lo[r] = valid[r] ? (a.window > 0 ? max(0, pos[r] - a.window + 1) : 0) : 1;
+    const __nv_bfloat16* qr = a.q + (static_cast<size_t>(q0 + tok[r]) * a.Hq + hq[r]) * HD + t4 * 2;
+    uint32_t mx = 0u;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      qf[kk][r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16) : 0u;
+      qf[kk][2 + r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8) : 0u;
+      mx = __vmaxu2(mx, __vmaxu2(qf[kk][r] & 0x7fff7fffu, qf[kk][2 + r] & 0x7fff7fffu));
+    }
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const int e = kv8_exp(kv8_max_halves(mx));
+    const float up = kv8_up(e);
+    rowfac[r] = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      qf[kk][r] = kv8_to_f16(qf[kk][r], up);
+      qf[kk][2 + r] = kv8_to_f16(qf[kk][2 + r], up);
+    }
+  }
+  if (LOWER8)
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) qf[kk][1] = qf[kk][3] = 0u;
+
+  bool ok = true;
+  auto wait = [&](uint64_t* f, uint32_t parity) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(f, parity, abort_flag, a.status));
+    return ok;
+  };
+  int used = 0;  // copies waited for
+  // The slot of copy j is free: copy j + SL goes there.
+  auto refill = [&](int j) {
+    __syncwarp();
+    const int k = j + SL;
+    if (k < 2 * n8) {
+      if (lane == (k < n8 ? k : k - n8)) issue(k, k >= n8);
+      issued = k + 1;
+    }
+  };
+
+  // ---- scores of the 8-bit pages
+  float s[kChunkPages][2][2 * NR];  // [page][key block][row, key pair]
+  float mx[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
+  // pages whose every key every row of the block sees (rows that are none aside)
+  const int full_lo = a.window > 0 ? (max(0, p_max - a.window + 1) + 15) >> 4 : 0;
+#pragma unroll
+  for (int i = 0; i < kChunkPages; ++i) {
+    if (i < n8 && wait(&bar[i % SL], (i / SL) & 1)) {
+      used = i + 1;
+      const uint4* kp = reinterpret_cast<const uint4*>(ring + (i % SL) * C::PART) + lane;
+      float acc[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+      for (int u = 0; u < Kv8Cfg<HD>::UNITS; ++u) {
+        const uint4 w = kp[u * 32];
+        uint32_t b0, b1;
+        kv8_expand<FMT>(w.x, b0, b1);
+        mma_f16_16816(acc[0], qf[2 * u], b0, b1);
+        kv8_expand<FMT>(w.y, b0, b1);
+        mma_f16_16816(acc[1], qf[2 * u], b0, b1);
+        kv8_expand<FMT>(w.z, b0, b1);
+        mma_f16_16816(acc[0], qf[2 * u + 1], b0, b1);
+        kv8_expand<FMT>(w.w, b0, b1);
+        mma_f16_16816(acc[1], qf[2 * u + 1], b0, b1);
+      }
+      refill(i);
+      const float ks = __shfl_sync(0xffffffffu, sc.x, i), lv = __shfl_sync(0xffffffffu, sc.z, i);
+      const int pgi = a8 + i;
+      const bool full = pgi < own_lo && pgi >= full_lo;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float c = __fmul_rn(ks, rowfac[r]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = __fmaf_rn(acc[j][2 * r + e], c, lv);
+            if (!full) {
+              const int key = pgi * 16 + j * 8 + t4 * 2 + e;
+              if (!(key >= lo[r] && pgi < own[r])) v = -INFINITY;
+            }
+            s[i][j][2 * r + e] = v;
+            mx[r] = fmaxf(mx[r], v);
+          }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2 * NR; ++e) s[i][j][e] = -INFINITY;
+    }
+  }
+  // ---- scores of the own pages
+  float so[2][2][2 * NR];
+#pragma unroll
+  for (int o = 0; o < 2; ++o)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 2 * NR; ++e) so[o][j][e] = -INFINITY;
+  int ve[2][2][2];  // [own page][key block][key of the pair]: the V token's exponent
+  if (no > 0) {
+    const int mi = lane >> 3, r8 = lane & 7;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      if (o >= no) break;
+      const int oi = ao + o - own_lo;
+      if (!wait(&own_bar[oi], 0)) break;
+      const uint32_t kb = smem_u32(own_s + oi * C::OWN), vb = kb + C::OWN / 2;
+      // largest magnitudes: of K tokens 8 j + g, then of V tokens 8 j + 2 t + {0, 1}
+      uint32_t km[2] = {0u, 0u}, vm[2] = {0u, 0u};
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        uint32_t w[4];
+        ldmatrix_x4(w, kb + kv_off<HD>((mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
+        km[0] = __vmaxu2(km[0], __vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu));
+        km[1] = __vmaxu2(km[1], __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+        ldmatrix_x4_trans(w, vb + kv_off<HD>((mi & 1) * 8 + r8, kk * 2 + (mi >> 1)));
+        vm[0] = __vmaxu2(vm[0], __vmaxu2(w[0] & 0x7fff7fffu, w[2] & 0x7fff7fffu));
+        vm[1] = __vmaxu2(vm[1], __vmaxu2(w[1] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+      }
+      int ke[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        km[j] = __vmaxu2(km[j], __shfl_xor_sync(0xffffffffu, km[j], 1));
+        km[j] = __vmaxu2(km[j], __shfl_xor_sync(0xffffffffu, km[j], 2));
+        ke[j] = kv8_exp(kv8_max_halves(km[j]));
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) vm[j] = __vmaxu2(vm[j], __shfl_xor_sync(0xffffffffu, vm[j], x));
+        ve[o][j][0] = kv8_exp(vm[j] & 0xffffu);
+        ve[o][j][1] = kv8_exp(vm[j] >> 16);
+      }
+      const float kup[2] = {kv8_up(ke[0]), kv8_up(ke[1])};
+      float acc[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        uint32_t w[4];
+        ldmatrix_x4(w, kb + kv_off<HD>((mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
+        mma_f16_16816(acc[0], qf[kk], kv8_to_f16(w[0], kup[0]), kv8_to_f16(w[1], kup[0]));
+        mma_f16_16816(acc[1], qf[kk], kv8_to_f16(w[2], kup[1]), kv8_to_f16(w[3], kup[1]));
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int kx = __shfl_sync(0xffffffffu, ke[j], (2 * t4 + e) * 4), vx = ve[o][j][e];
+          const float kd = kx == 255 ? kv8_nan() : kv8_down(kx);
+          const float lv = vx == 255 ? kv8_nan() : kv8_log2_down(vx);
+          const int key = (ao + o) * 16 + j * 8 + t4 * 2 + e;
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const bool vis = key >= lo[r] && key <= pos[r] && ao + o == own[r];
+            const float v = vis ? __fmaf_rn(acc[j][2 * r + e], __fmul_rn(kd, rowfac[r]), lv) : -INFINITY;
+            so[o][j][2 * r + e] = v;
+            mx[r] = fmaxf(mx[r], v);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+  }
+
+  // ---- weights, their sums and P V
+  float l[NR], o_acc[HD / 8][4];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) l[r] = 0.f;
+#pragma unroll
+  for (int n = 0; n < HD / 8; ++n) o_acc[n][0] = o_acc[n][1] = o_acc[n][2] = o_acc[n][3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kChunkPages; ++i) {
+    const int cp = n8 + i;  // the copy of page i's V
+    if (i < n8 && wait(&bar[cp % SL], (cp / SL) & 1)) {
+      used = cp + 1;
+      const float iv = __shfl_sync(0xffffffffu, sc.y, i);
+      const bool full = a8 + i < own_lo && a8 + i >= full_lo;
+      uint32_t pa[4];
+      if (LOWER8) pa[1] = pa[3] = 0u;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float p[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          p[x] = ex2(__fsub_rn(s[i][x >> 1][2 * r + (x & 1)], mx[r]));
+          if (!full) {
+            const int key = (a8 + i) * 16 + (x >> 1) * 8 + t4 * 2 + (x & 1);
+            if (!(key >= lo[r] && a8 + i < own[r])) p[x] = 0.f;
+          }
+        }
+        float ps = __fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3]));
+        ps = __fmaf_rn(ps, iv, l[r]);
+        // (a page that the row does not see stays out, whatever its scale)
+        l[r] = full || (a8 + i < own[r] && (a8 + i) * 16 + 15 >= lo[r]) ? ps : l[r];
+        pa[r] = pack_f16x2(p[0], p[1]);
+        pa[2 + r] = pack_f16x2(p[2], p[3]);
+      }
+      const uint4* vp = reinterpret_cast<const uint4*>(ring + (cp % SL) * C::PART) + lane;
+#pragma unroll
+      for (int u = 0; u < Kv8Cfg<HD>::UNITS; ++u) {
+        const uint4 w = vp[u * 32];
+        uint32_t b0, b1;
+        kv8_expand<FMT>(w.x, b0, b1);
+        mma_f16_16816(o_acc[4 * u], pa, b0, b1);
+        kv8_expand<FMT>(w.y, b0, b1);
+        mma_f16_16816(o_acc[4 * u + 1], pa, b0, b1);
+        kv8_expand<FMT>(w.z, b0, b1);
+        mma_f16_16816(o_acc[4 * u + 2], pa, b0, b1);
+        kv8_expand<FMT>(w.w, b0, b1);
+        mma_f16_16816(o_acc[4 * u + 3], pa, b0, b1);
+      }
+      refill(cp);
+    }
+  }
+  if (no > 0 && ok) {
+    const int mi = lane >> 3, r8 = lane & 7;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      if (o >= no) break;
+      const uint32_t vb = smem_u32(own_s + (ao + o - own_lo) * C::OWN + C::OWN / 2);
+      float up[4];   // of keys 2t, 2t + 1, 2t + 8, 2t + 9 (0: a token that is not finite, whose weight is NaN or 0)
+      bool fin[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        up[x] = kv8_up(ve[o][x >> 1][x & 1]);
+        fin[x] = ve[o][x >> 1][x & 1] != 255;
+      }
+      uint32_t pa[4];
+      if (LOWER8) pa[1] = pa[3] = 0u;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float p[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int key = (ao + o) * 16 + (x >> 1) * 8 + t4 * 2 + (x & 1);
+          const bool vis = key >= lo[r] && key <= pos[r] && ao + o == own[r];
+          p[x] = vis ? ex2(__fsub_rn(so[o][x >> 1][2 * r + (x & 1)], mx[r])) : 0.f;
+          l[r] = vis ? __fmaf_rn(p[x], up[x], l[r]) : l[r];
+        }
+        pa[r] = pack_f16x2(p[0], p[1]);
+        pa[2 + r] = pack_f16x2(p[2], p[3]);
+      }
+#pragma unroll
+      for (int np = 0; np < HD / 16; ++np) {
+        uint32_t w[4];
+        ldmatrix_x4_trans(w, vb + kv_off<HD>((mi & 1) * 8 + r8, np * 2 + (mi >> 1)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x0 = w[2 * h], x1 = w[2 * h + 1];
+          const uint32_t b0 = pack_f16x2(fin[0] ? __fmul_rn(bf16_lo(x0), up[0]) : 0.f, fin[1] ? __fmul_rn(bf16_hi(x0), up[1]) : 0.f);
+          const uint32_t b1 = pack_f16x2(fin[2] ? __fmul_rn(bf16_lo(x1), up[2]) : 0.f, fin[3] ? __fmul_rn(bf16_hi(x1), up[3]) : 0.f);
+          mma_f16_16816(o_acc[2 * np + h], pa, b0, b1);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 1));
+    l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 2));
+  }
+  if (!ok) {  // gave up: every copy lands before the warp leaves
+    for (int j = used; j < issued; ++j) drain_wait(&bar[j % SL], (j / SL) & 1);
+    for (int o = 0; o < no; ++o) drain_wait(&own_bar[ao + o - own_lo], 0);
+  }
+
+  // ---- the chunks of the split, left to right.  Each warp's O goes to its own
+  // ring, all of whose copies have been used.
+  __syncwarp();
+  float* fo = reinterpret_cast<float*>(ring);  // [row][HD]
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    if (t4 == 0) {
+      fold_m[warp][gq + 8 * r] = mx[r];
+      fold_l[warp][gq + 8 * r] = l[r];
+    }
+#pragma unroll
+    for (int n = 0; n < HD / 8; ++n)
+      *reinterpret_cast<float2*>(fo + (gq + 8 * r) * HD + n * 8 + t4 * 2) =
+          make_float2(o_acc[n][2 * r], o_acc[n][2 * r + 1]);
+  }
+  __syncthreads();
+  if (*abort_flag) return;
+  constexpr int TPR = 128 / (8 * NR), PER = HD / TPR;  // threads and dims per row
+  const int frow = threadIdx.x / TPR, fd = threadIdx.x % TPR;
+  const int row = r0 + frow;
+  if (row >= rows) return;
+  const int p = cached + row / G, flo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+  float M = 0.f, L = 0.f, O[PER];
+  bool any = false;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int k0 = sidx * kSplit8 + w * kChunk8;
+    if (max(flo, k0) > min(p, k0 + kChunk8 - 1)) continue;  // the row sees no key of the chunk
+    const float m = fold_m[w][frow], lw = fold_l[w][frow];
+    const float* src = reinterpret_cast<const float*>(ring0 + w * C::RING) + frow * HD;
+    if (!any) {
+      M = m;
+      L = lw;
+#pragma unroll
+      for (int i = 0; i < PER / 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(src + (i * TPR + fd) * 4);
+        O[4 * i] = v.x;
+        O[4 * i + 1] = v.y;
+        O[4 * i + 2] = v.z;
+        O[4 * i + 3] = v.w;
+      }
+      any = true;
+    } else {
+      const float mn = fmaxf(M, m), ca = ex2(__fsub_rn(M, mn)), cb = ex2(__fsub_rn(m, mn));
+      L = __fadd_rn(__fmul_rn(L, ca), __fmul_rn(lw, cb));
+#pragma unroll
+      for (int i = 0; i < PER / 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(src + (i * TPR + fd) * 4);
+        O[4 * i] = __fadd_rn(__fmul_rn(O[4 * i], ca), __fmul_rn(v.x, cb));
+        O[4 * i + 1] = __fadd_rn(__fmul_rn(O[4 * i + 1], ca), __fmul_rn(v.y, cb));
+        O[4 * i + 2] = __fadd_rn(__fmul_rn(O[4 * i + 2], ca), __fmul_rn(v.z, cb));
+        O[4 * i + 3] = __fadd_rn(__fmul_rn(O[4 * i + 3], ca), __fmul_rn(v.w, cb));
+      }
+      M = mn;
+    }
+  }
+  if (!any) return;
+  const size_t base = (static_cast<size_t>(q0 + row / G) * a.Hq + kvh * G + row % G) * a.max_splits + sidx;
+  if (fd == 0) {
+    a.part_ml[base * 2] = M;
+    a.part_ml[base * 2 + 1] = L;
+  }
+#pragma unroll
+  for (int i = 0; i < PER / 4; ++i)
+    *reinterpret_cast<float4*>(a.part_o + base * HD + (i * TPR + fd) * 4) =
+        make_float4(O[4 * i], O[4 * i + 1], O[4 * i + 2], O[4 * i + 3]);
+}
+
+template <int HD, int FMT, bool LOWER8>
+int launch_attn8_t(const CUtensorMap& kvmap, const Attn8Args& a, int n_items, cudaStream_t s) {
+  constexpr int SL = 6;
+  using C = Attn8Cfg<HD, SL>;
+  static_assert(C::smem(2) + 1024 <= 227 * 1024, "shared memory");
+  VD_CUDA_TRY(cudaFuncSetAttribute(attn8_kernel<HD, FMT, SL, LOWER8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   C::smem(2)));
+  VD_CUDA_TRY(launch_k(attn8_kernel<HD, FMT, SL, LOWER8>, dim3(n_items), dim3(128), C::smem(a.own_slots), s, kvmap, a));
+  return VD_OK;
+}
+
+}  // namespace
+
+static_assert(kAttn8Split == kSplit8, "split of the plan's items");
+
+int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int format, bool lower8, int n_items,
+                      cudaStream_t s) {
+  if (n_items <= 0) return VD_OK;
+#define VD_ATTN8(HD_)                                                                                             \
+  if (hd == HD_) {                                                                                                \
+    if (format == VD_KV8_INT8)                                                                                    \
+      return lower8 ? launch_attn8_t<HD_, kKv8Int8, true>(kvmap, a, n_items, s)                                   \
+                    : launch_attn8_t<HD_, kKv8Int8, false>(kvmap, a, n_items, s);                                 \
+    return lower8 ? launch_attn8_t<HD_, kKv8E4m3, true>(kvmap, a, n_items, s)                                     \
+                  : launch_attn8_t<HD_, kKv8E4m3, false>(kvmap, a, n_items, s);                                   \
+  }
+  VD_ATTN8(64)
+  VD_ATTN8(128)
+  VD_ATTN8(256)
+#undef VD_ATTN8
+  return fail(VD_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+}
+
+}  // namespace vd

@@ -13,6 +13,7 @@
 #include "vd_ops.h"
 #include "vd_engine.h"
 #include "vd_tree.h"
+#include "vd_kv8.h"
 
 namespace vd {
 
@@ -230,6 +231,57 @@ int launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t s);
 // 64 head dims.
 bool attn_tc_supported(int hd);
 int launch_attention_tc(const CUtensorMap& kvmap_tc, const AttnArgs& a, int hd, int n_items, cudaStream_t s);
+// Attention over the 8-bit cache (attn8.cu): split partials, folded by launch_merge.
+constexpr int kAttn8Split = 512;  // keys of a split
+struct Attn8Args {
+  const __nv_bfloat16* q;   // [T][Hq][hd]
+  float* part_o;            // [T][Hq][max_splits][hd]
+  float* part_ml;           // [T][Hq][max_splits][2]
+  const int* cu_q;          // [B + 1]
+  const int* cached_len;    // [B]
+  const int* page_table;    // [B][pt_stride] pages of the cache
+  const int* open_table;    // [B][open_stride] pages of the bf16 pool, from logical page cached_len / 16 on
+  const int* cls_seq;       // seqs of this launch class
+  const int* cls_start;     // [n_cls + 1] item prefix sums
+  const uint8_t* codes;     // the layer's first page
+  const float4* scales;
+  int n_cls;
+  int pt_stride, open_stride;
+  int Hq, Hkv;
+  int layer_row0;           // first row of this layer in the bf16 pool
+  int window;               // 0: global
+  int max_splits;
+  int own_slots;            // bf16 pages that a block of 16 rows can hold: 1, or 2 if some request has several tokens
+  float scale_log2;         // log2(e) / sqrt(hd)
+  int* status;
+};
+// lower8: every block of the launch has at most 8 rows.
+int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int format, bool lower8, int n_items,
+                      cudaStream_t s);
+// Sealing and its reverse, page copies (kv8.cu).  Pairs of page ids: `dev` on the
+// device (a plan's), or else in the launch's own arguments.
+constexpr int kPagePairs = 448;
+struct PagePairs {
+  const int2* dev;  // [n] (source, destination) or null
+  int n;
+  int2 at[kPagePairs];
+};
+struct SealArgs {
+  __nv_bfloat16* pool;      // first layer
+  uint8_t* codes;
+  float4* scales;
+  long long pool_layer, codes_layer, scales_layer;  // elements, bytes, float4 of a layer
+  int layers, Hkv, hd, format;
+};
+int launch_kv8_seal(const SealArgs& a, const PagePairs& pairs, bool unseal, cudaStream_t s);
+struct CopyArgs {
+  uint8_t* data;            // pages of `bytes` bytes, `layer` bytes from layer to layer
+  long long bytes, layer;
+  float4* extra;            // and their scales (n_extra per page), or null
+  long long extra_layer;
+  int n_extra, layers;
+};
+int launch_copy_pages(const CopyArgs& a, const PagePairs& pairs, cudaStream_t s);
 // Fixed-size device scratch of vd_op_attention_static (bytes) and its
 // device address on the current device (looked up once per device).
 constexpr size_t kAttnStaticScratchBytes = static_cast<size_t>(16) << 20;

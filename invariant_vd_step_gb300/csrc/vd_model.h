@@ -68,6 +68,12 @@ struct Desc {
   } cls[4];
   float *part_o = nullptr, *part_ml = nullptr;
   int part_splits = 0;  // splits per row of the partials
+  // Steps over the 8-bit cache (vd_kv8_plan); part_* as above
+  const vd_kv8* kv8 = nullptr;
+  int seal = 0, n_seal = 0;              // offset of the (bf16 page, cache page) pairs that the step seals
+  int open_table = 0, open_stride = 0;   // pages of the bf16 pool, per request
+  int own_slots = 1;                     // bf16 pages that a decode-class block can hold
+  bool lower8 = false;                   // every decode-class block has at most 8 rows
 };
 
 // What a captured step graph depends on beyond the model: every kernel
@@ -183,6 +189,10 @@ int run_rope(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv
 // Attention and RoPE + K/V write of a token tree (api_tree.cu).
 int run_tree_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv_bfloat16* q,
                        __nv_bfloat16* out, cudaStream_t s);
+// The 8-bit cache (api_kv8.cu): sealing of the pages that the step completes, and attention.
+int run_kv8_seal(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, cudaStream_t s);
+int run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& d, const __nv_bfloat16* q,
+                      __nv_bfloat16* out, cudaStream_t s);
 
 // ---------------------------------------------------------------- profiling
 inline cudaEvent_t take_event(vd_model* m) {

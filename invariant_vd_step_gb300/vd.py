@@ -103,6 +103,13 @@ class TreeBatch(ctypes.Structure):
                 ("page_table", _I32P), ("token_ids", _I32P)]
 
 
+class KV8Batch(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("num_logit_rows", ctypes.c_int32),
+                ("page_table_stride", ctypes.c_int32), ("open_stride", ctypes.c_int32), ("pad_", ctypes.c_int32),
+                ("cu_q", _I32P), ("cached_len", _I32P), ("page_table", _I32P), ("open_table", _I32P),
+                ("token_ids", _I32P), ("logit_rows", _I32P)]
+
+
 class PlanOut(ctypes.Structure):
     _fields_ = [("batch", Batch), ("rids", ctypes.POINTER(ctypes.c_int64)),
                 ("samplers", ctypes.POINTER(Sampler))]
@@ -164,6 +171,30 @@ _SIGS = {
     "vd_op_tree_rope_kv": (ctypes.c_int, [_VP, _VP, ctypes.c_int32, _VP, _VP, _VP]),
     "vd_step_tree": (ctypes.c_int, [_VP, _VP, _VP, _VP]),
     "vd_tree_accept": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP]),
+    "vd_kv8_bytes": (ctypes.c_size_t, [_VP, ctypes.c_int32]),
+    "vd_kv8_create": (ctypes.c_int, [_VP, ctypes.c_int32, ctypes.c_int32, _VP, ctypes.c_size_t, ctypes.POINTER(_VP)]),
+    "vd_destroy_kv8": (None, [_VP]),
+    "vd_kv8_data": (_VP, [_VP]),
+    "vd_kv8_seal": (ctypes.c_int, [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP]),
+    "vd_kv8_unseal": (ctypes.c_int, [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP]),
+    "vd_kv8_plan_create": (ctypes.c_int, [_VP, ctypes.c_int32, ctypes.POINTER(_VP)]),
+    "vd_destroy_kv8_plan": (None, [_VP]),
+    "vd_kv8_plan_make": (ctypes.c_int, [_VP, _VP, _VP, ctypes.POINTER(KV8Batch), _VP]),
+    "vd_op_kv8_rope_kv": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int32, _VP, _VP, _VP]),
+    "vd_op_kv8_seal": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int32, _VP]),
+    "vd_op_kv8_attention": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int32, _VP, _VP, _VP]),
+    "vd_step_kv8": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP]),
+    "vd_kv_copy_pages": (ctypes.c_int, [_VP, ctypes.c_int32, _VP, _VP, _VP]),
+    "vd_kv8_copy_pages": (ctypes.c_int, [_VP, ctypes.c_int32, _VP, _VP, _VP]),
+    "vd_pages_create": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(_VP)]),
+    "vd_destroy_pages": (None, [_VP]),
+    "vd_pages_free": (ctypes.c_int32, [_VP]),
+    "vd_pages_refs": (ctypes.c_int32, [_VP, ctypes.c_int32]),
+    "vd_pages_alloc": (ctypes.c_int, [_VP, ctypes.c_int32, _VP]),
+    "vd_pages_retain": (ctypes.c_int, [_VP, ctypes.c_int32, _VP]),
+    "vd_pages_release": (ctypes.c_int, [_VP, ctypes.c_int32, _VP]),
+    "vd_pages_fork": (ctypes.c_int, [_VP, ctypes.c_int32, ctypes.c_int32, _VP, ctypes.c_int32, _VP, _VP, _VP]),
+    "vd_pages_compact": (ctypes.c_int, [_VP, ctypes.c_int32, _VP, _VP, _I32P, ctypes.c_int32, _VP]),
     "vd_engine_create": (ctypes.c_int, [ctypes.POINTER(EngineConfig), ctypes.POINTER(_VP)]),
     "vd_engine_destroy": (None, [_VP]),
     "vd_engine_add_request": (ctypes.c_int, [_VP, _I32P, ctypes.c_int32, ctypes.c_int32, ctypes.c_uint64,
@@ -397,6 +428,9 @@ class Model:
     def pool_bytes(self, num_pages: int) -> int:
         return int(lib().vd_kv_pool_bytes(self.h, num_pages))
 
+    def kv8_bytes(self, num_pages: int) -> int:
+        return int(lib().vd_kv8_bytes(self.h, num_pages))
+
     def step(self, pool: "KVPool", batch: StepBatch, logits: torch.Tensor, stream=None):
         check(lib().vd_step(self.h, pool.h, ctypes.byref(batch.c), _ptr(logits), _stream(stream)))
 
@@ -532,6 +566,43 @@ class KVPool:
             raise RuntimeError("view() needs a pool created over caller memory")
         return self.memory.view(torch.bfloat16)[: s.n_layers * self.num_pages * 2 * s.n_kv_heads * 16 * s.head_dim] \
             .view(s.n_layers, self.num_pages, 2, s.n_kv_heads, 16, s.head_dim)
+
+    def copy_pages(self, src, dst, stream=None):
+        """vd_kv_copy_pages: pages src[i] to pages dst[i], in every layer."""
+        n, src, dst = _page_lists(src, dst)
+        check(lib().vd_kv_copy_pages(_live(self), n, src.ctypes.data, dst.ctypes.data, _model_stream(self.model, stream)))
+
+
+def _ids(a):
+    """Page ids as a contiguous int32 array; ids that int32 does not hold are refused."""
+    a = np.asarray(a)
+    if a.dtype != np.int32 or a.ndim != 1 or not a.flags.c_contiguous:
+        _need(a.size == 0 or (a.dtype.kind in "iu" and -2 ** 31 <= int(a.min()) and int(a.max()) < 2 ** 31),
+              "page ids: integers that fit in 32 bits")
+        a = np.ascontiguousarray(a.reshape(-1), dtype=np.int32)
+    return a
+
+
+def _page_lists(src, dst):
+    src, dst = _ids(src), _ids(dst)
+    _need(len(src) == len(dst), "as many destinations as sources")
+    return len(src), src, dst
+
+
+def _live(*objects):
+    """The first one's handle, as long as all of them and their models are open."""
+    for x in objects:
+        if not x.h or not x.model.h:
+            raise VDError(VD_ERR_INVALID_ARG, f"a {type(x).__name__} or its model is closed")
+    return objects[0].h
+
+
+def _model_stream(model, stream) -> int:
+    """Handle of `stream`, or of the current stream; the library checks the device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _current_raw_stream(torch.cuda.current_device()) if _current_raw_stream else \
+        torch.cuda.current_stream().cuda_stream
 
 
 def _check_out(t, shape, dtype, name: str, device=None):
@@ -714,6 +785,205 @@ class Tree:
                                   _raw_stream(stream, device))
         if rc:
             check(rc)
+
+
+_FORMATS = {"int8": 0, "e4m3": 1}
+
+
+class KV8Cache:
+    """A vd_kv8: complete pages in 8 bits, "int8" or "e4m3", with a scale for each page, K or V, and KV head
+    (include/vd_kv8.h)."""
+
+    def __init__(self, model: Model, num_pages: int, format: str = "int8", memory: torch.Tensor | None = None):
+        _need(format in _FORMATS, f"format {format!r}: one of {sorted(_FORMATS)}")
+        self.model, self.num_pages, self.format = model, num_pages, format
+        self.memory = memory  # keep alive when caller-owned
+        if memory is not None:
+            _need(memory.get_device() >= 0 and memory.is_contiguous(), "memory: contiguous, on the model's GPU")
+        h = ctypes.c_void_p()
+        check(lib().vd_kv8_create(model.h, _FORMATS[format], num_pages, None if memory is None else memory.data_ptr(),
+                                  0 if memory is None else memory.nbytes, ctypes.byref(h)))
+        self.h = h
+
+    def close(self):
+        if getattr(self, "h", None):
+            lib().vd_destroy_kv8(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _split(self):
+        if self.memory is None:
+            raise RuntimeError("codes() and scales() need a cache created over caller memory")
+        s, flat = self.model.spec, self.memory.view(torch.uint8).reshape(-1)
+        blocks = s.n_layers * self.num_pages * s.n_kv_heads
+        return s, flat[:blocks * 32 * s.head_dim], flat[blocks * 32 * s.head_dim:blocks * (32 * s.head_dim + 16)]
+
+    def codes(self) -> torch.Tensor:
+        """The codes as bytes [layers][pages][Hkv][32 hd], in the order of vd_kv8.h (requires caller memory)."""
+        s, codes, _ = self._split()
+        return codes.view(s.n_layers, self.num_pages, s.n_kv_heads, 32 * s.head_dim)
+
+    def scales(self) -> torch.Tensor:
+        """The scales as float32 [layers][pages][Hkv][4] (requires caller memory)."""
+        s, _, scales = self._split()
+        return scales.view(torch.float32).view(s.n_layers, self.num_pages, s.n_kv_heads, 4)
+
+    def seal(self, pool: KVPool, src, dst, layer: int = -1, stream=None):
+        """vd_kv8_seal: pages src[i] of the bf16 pool into pages dst[i], in one layer or in all (-1)."""
+        n, src, dst = _page_lists(src, dst)
+        check(lib().vd_kv8_seal(_live(self, pool), pool.h, layer, n, src.ctypes.data, dst.ctypes.data,
+                                _model_stream(self.model, stream)))
+
+    def unseal(self, pool: KVPool, src, dst, layer: int = -1, stream=None):
+        """vd_kv8_unseal: the values of pages src[i], rounded to bf16, into pages dst[i] of the bf16 pool."""
+        n, src, dst = _page_lists(src, dst)
+        check(lib().vd_kv8_unseal(_live(self, pool), pool.h, layer, n, src.ctypes.data, dst.ctypes.data,
+                                  _model_stream(self.model, stream)))
+
+    def copy_pages(self, src, dst, stream=None):
+        """vd_kv8_copy_pages: pages src[i] to pages dst[i], in every layer."""
+        n, src, dst = _page_lists(src, dst)
+        check(lib().vd_kv8_copy_pages(_live(self), n, src.ctypes.data, dst.ctypes.data,
+                                      _model_stream(self.model, stream)))
+
+
+class KV8Plan:
+    """A vd_kv8_plan: steps over an 8-bit cache (include/vd_kv8.h).
+
+    `plan` takes the requests of one step as arrays: cu_q [B + 1], cached_len [B], page_table [B][stride] of the
+    cache (logical pages that are complete after the step), open_table [B][stride] of the bf16 pool (logical pages
+    from cached_len // 16 on), and for `step` token_ids [T] and logit_rows.  The other calls run on the plan in
+    force."""
+
+    def __init__(self, model: Model, max_tokens: int):
+        self.model = model
+        self.num_tokens = self.num_logit_rows = 0
+        h = ctypes.c_void_p()
+        check(lib().vd_kv8_plan_create(model.h, int(max_tokens), ctypes.byref(h)))
+        self.h = h
+
+    def close(self):
+        if getattr(self, "h", None):
+            lib().vd_destroy_kv8_plan(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def plan(self, cache: KV8Cache, pool: KVPool, cu_q, cached_len, page_table, open_table, token_ids=None,
+             logit_rows=(), stream=None):
+        cu, p_cu = _i32(cu_q)
+        c, p_c = _i32(cached_len)
+        tables = []
+        for t in (page_table, open_table):
+            t = np.ascontiguousarray(t, dtype=np.int32)
+            tables.append(t.reshape(len(c), -1) if t.size else t.reshape(len(c), 0))
+        tok, p_tok = _i32(np.asarray(token_ids).reshape(-1)) if token_ids is not None else (None, None)
+        rows, p_rows = _i32(np.asarray(logit_rows).reshape(-1))
+        _need(cu.ndim == 1 and c.ndim == 1 and len(cu) == len(c) + 1 and (tok is None or len(tok) == cu[-1]),
+              "cu_q [B + 1], cached_len [B], token_ids [cu_q[B]]")
+        b = KV8Batch(int(cu[-1]), len(c), len(rows), tables[0].shape[1], tables[1].shape[1], 0, p_cu, p_c,
+                     tables[0].ctypes.data_as(_I32P), tables[1].ctypes.data_as(_I32P), p_tok, p_rows)
+        check(lib().vd_kv8_plan_make(_live(self, cache, pool), cache.h, pool.h, ctypes.byref(b),
+                                     _model_stream(self.model, stream)))
+        self.num_tokens, self.num_logit_rows = int(cu[-1]), len(rows)
+
+    def rope_kv(self, cache: KV8Cache, pool: KVPool, layer: int, qkv: torch.Tensor, q_out: torch.Tensor, stream=None):
+        """vd_op_kv8_rope_kv: qkv bf16 [T][(Hq + 2 Hkv) hd], q_out bf16 [T][Hq][hd]."""
+        s = self.model.spec
+        _check_out(q_out, (self.num_tokens, s.n_heads, s.head_dim), torch.bfloat16, "q_out")
+        _check_out(qkv, (self.num_tokens, s.qkv_dim), torch.bfloat16, "qkv", q_out.get_device())
+        check(lib().vd_op_kv8_rope_kv(_live(self, cache, pool), cache.h, pool.h, layer, qkv.data_ptr(), q_out.data_ptr(),
+                                      _raw_stream(stream, q_out.get_device())))
+
+    def seal(self, cache: KV8Cache, pool: KVPool, layer: int, stream=None):
+        """vd_op_kv8_seal: the pages that the planned step completes, in one layer."""
+        check(lib().vd_op_kv8_seal(_live(self, cache, pool), cache.h, pool.h, layer, _model_stream(self.model, stream)))
+
+    def attention(self, cache: KV8Cache, pool: KVPool, layer: int, q: torch.Tensor, out: torch.Tensor, stream=None):
+        """vd_op_kv8_attention: q, out bf16 [T][Hq][hd]."""
+        shape = (self.num_tokens, self.model.spec.n_heads, self.model.spec.head_dim)
+        _check_out(out, shape, torch.bfloat16, "out")
+        _check_out(q, shape, torch.bfloat16, "q", out.get_device())
+        rc = lib().vd_op_kv8_attention(_live(self, cache, pool), cache.h, pool.h, layer, q.data_ptr(), out.data_ptr(),
+                                       _raw_stream(stream, out.get_device()))
+        if rc:
+            check(rc)
+
+    def step(self, cache: KV8Cache, pool: KVPool, logits: torch.Tensor | None = None, stream=None):
+        """vd_step_kv8: logits float32 [R][V] of the plan's logit_rows (None if it has none)."""
+        if logits is not None:
+            _check_out(logits, (self.num_logit_rows, self.model.spec.vocab), torch.float32, "logits")
+        check(lib().vd_step_kv8(_live(self, cache, pool), cache.h, pool.h, None if logits is None else logits.data_ptr(),
+                                _model_stream(self.model, stream) if logits is None
+                                else _raw_stream(stream, logits.get_device())))
+
+
+class Pages:
+    """A vd_pages: reference counts of the pages of a pool or cache (host memory only)."""
+
+    def __init__(self, num_pages: int):
+        h = ctypes.c_void_p()
+        check(lib().vd_pages_create(int(num_pages), ctypes.byref(h)))
+        self.h, self.num_pages = h, int(num_pages)
+
+    def __del__(self):
+        try:
+            if getattr(self, "h", None):
+                lib().vd_destroy_pages(self.h)
+                self.h = None
+        except Exception:
+            pass
+
+    @property
+    def free(self) -> int:
+        return int(lib().vd_pages_free(self.h))
+
+    def refs(self, page: int) -> int:
+        return int(lib().vd_pages_refs(self.h, int(page)))
+
+    def alloc(self, n: int) -> np.ndarray:
+        """The n lowest free pages, one reference each."""
+        out = np.empty(max(int(n), 0), np.int32)
+        check(lib().vd_pages_alloc(self.h, int(n), out.ctypes.data))
+        return out
+
+    def retain(self, pages):
+        ids = _ids(pages)
+        check(lib().vd_pages_retain(self.h, len(ids), ids.ctypes.data))
+
+    def release(self, pages):
+        ids = _ids(pages)
+        check(lib().vd_pages_release(self.h, len(ids), ids.ctypes.data))
+
+    def fork(self, table, n_shared: int, children: int = 1):
+        """vd_pages_fork: (tables [children][n], src, dst) of `children` requests that share the first n_shared pages of
+        `table`; the copies src -> dst are the caller's to make (`copy_pages`)."""
+        t = _ids(table)
+        _need(0 <= n_shared <= len(t) and children >= 0, "0 <= n_shared <= pages, children >= 0")
+        n = (len(t) - n_shared) * children
+        out, src, dst = np.empty((children, len(t)), np.int32), np.empty(n, np.int32), np.empty(n, np.int32)
+        check(lib().vd_pages_fork(self.h, len(t), int(n_shared), t.ctypes.data, int(children), out.ctypes.data,
+                                  src.ctypes.data, dst.ctypes.data))
+        return out, src, dst
+
+    def compact(self, tables: np.ndarray, max_moves: int | None = None):
+        """vd_pages_compact: (src, dst) of the moves; `tables` (int32, contiguous) is rewritten in place."""
+        _need(isinstance(tables, np.ndarray) and tables.dtype == np.int32 and tables.flags.c_contiguous
+              and tables.flags.writeable, "tables: a contiguous, writeable int32 array")
+        most = self.num_pages if max_moves is None else int(max_moves)
+        src, dst, n = np.empty(max(most, 0), np.int32), np.empty(max(most, 0), np.int32), ctypes.c_int32()
+        check(lib().vd_pages_compact(self.h, most, src.ctypes.data, dst.ctypes.data, ctypes.byref(n), tables.size,
+                                     tables.ctypes.data))
+        return src[:n.value].copy(), dst[:n.value].copy()
 
 
 def gemm(A, W, C, epilogue=EPI_BF16, residual=None, stream=None):
