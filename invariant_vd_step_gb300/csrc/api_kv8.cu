@@ -187,7 +187,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   if (R > 0 && !b->logit_rows) return fail(VD_ERR_INVALID_ARG, "missing logit_rows");
   if (b->cu_q[0] != 0 || b->cu_q[B] != T) return fail(VD_ERR_INVALID_ARG, "cu_q must run from 0 to num_tokens");
   // lengths, table widths, page ids
-  int stride = 0, open_stride = 0, splits = 1, n_seal = 0, most_q = 1, most_dec = 0;
+  int stride = 0, open_stride = 0, splits = 1, n_seal = 0, most_q = 1, most_dec = 0, n_dec = 0;
   for (int i = 0; i < B; ++i) {
     const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i];
     if (ql < 1 || b->cu_q[i + 1] > T) return fail(VD_ERR_INVALID_ARG, "every request needs q_len >= 1");
@@ -205,6 +205,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     if (ql * m->G <= 16) {
       most_q = std::max(most_q, ql);
       most_dec = std::max(most_dec, ql * m->G);
+      ++n_dec;
     }
   }
   for (int k = 0; b->token_ids && k < T; ++k)
@@ -251,17 +252,14 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     off += n;
     return static_cast<int>(o);
   };
-  d.seal = take(2 * static_cast<size_t>(n_seal));  // int2: first, for its alignment
+  d.cls_desc = take(4 * static_cast<size_t>(B));   // int4, then int2: first, for their alignment
+  d.seal = take(2 * static_cast<size_t>(n_seal));
   d.n_seal = n_seal;
   d.tokens = take(T);
   d.positions = take(T);
   d.slot_page = take(T);
   d.logit_rows = take(R);
-  d.cu_q = take(B + 1);
-  d.cached = take(B);
-  d.dec_seq = take(B);
   d.dec_start = take(B + 1);
-  d.pre_seq = take(B);
   d.pre_start = take(B + 1);
   d.open_stride = open_stride;
   d.open_table = take(static_cast<size_t>(B) * open_stride);
@@ -312,19 +310,20 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       h[d.positions + q0 + k] = cached + k;
       h[d.slot_page + q0 + k] = h[d.open_table + static_cast<size_t>(i) * open_stride + (cached + k) / 16 - first];
     }
-    h[d.cu_q + i] = q0;
-    h[d.cached + i] = cached;
-    if (ql * m->G <= 16) {
-      h[d.dec_seq + d.n_dec] = i;
+    const bool dec = ql * m->G <= 16;  // the decode class's descriptions, then the other one's
+    int* at = h + d.cls_desc + 4 * static_cast<size_t>(dec ? d.n_dec : n_dec + d.n_pre);
+    at[0] = i;
+    at[1] = q0;
+    at[2] = ql;
+    at[3] = cached;
+    if (dec) {
       h[d.dec_start + d.n_dec++] = d.items_dec;
       d.items_dec += static_cast<int>(items_of(i, 16));
     } else {
-      h[d.pre_seq + d.n_pre] = i;
       h[d.pre_start + d.n_pre++] = d.items_pre;
       d.items_pre += static_cast<int>(items_of(i, 16));
     }
   }
-  h[d.cu_q + B] = T;
   h[d.dec_start + d.n_dec] = d.items_dec;
   h[d.pre_start + d.n_pre] = d.items_pre;
   for (int j = 0; j < R; ++j) h[d.logit_rows + j] = b->logit_rows[j];
@@ -362,8 +361,6 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
   a.q = q;
   a.part_o = d.part_o;
   a.part_ml = d.part_ml;
-  a.cu_q = d.base + d.cu_q;
-  a.cached_len = d.base + d.cached;
   a.page_table = d.base + d.page_table;
   a.open_table = d.base + d.open_table;
   a.codes = d.kv8->codes(layer);
@@ -380,7 +377,7 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
   int rc;
   if (d.n_dec) {
     Prof p(m, K_ATTN, s);
-    a.cls_seq = d.base + d.dec_seq;
+    a.cls_desc = reinterpret_cast<const int4*>(d.base + d.cls_desc);
     a.cls_start = d.base + d.dec_start;
     a.n_cls = d.n_dec;
     a.own_slots = d.own_slots;
@@ -388,7 +385,7 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
   }
   if (d.n_pre) {
     Prof p(m, K_ATTN, s);
-    a.cls_seq = d.base + d.pre_seq;
+    a.cls_desc = reinterpret_cast<const int4*>(d.base + d.cls_desc) + d.n_dec;
     a.cls_start = d.base + d.pre_start;
     a.n_cls = d.n_pre;
     a.own_slots = 2;

@@ -37,21 +37,24 @@ constexpr int kSplit8 = 512;   // keys of a split
 constexpr int kChunk8 = 128;   // keys of a chunk
 constexpr int kChunkPages = kChunk8 / 16;
 
-template <int HD, int SL>
+// LOWER8: the block holds at most 8 rows (a lane's second row is none).
+template <int HD, bool LOWER8>
 struct Attn8Cfg {
   static constexpr int PART = Kv8Cfg<HD>::PART;
-  static constexpr int OWN = 2 * 32 * HD;  // K and V of one bf16 page
-  static constexpr int RING = SL * PART;   // per warp
-  static_assert(RING >= 16 * HD * 4, "the chunk's O fits the warp's ring");
-  static constexpr int smem(int own_slots) { return 1024 + own_slots * OWN + 4 * RING + (4 * SL + 2) * 8 + 16; }
+  static constexpr int SL = LOWER8 ? 3 : 4;         // copies in flight per warp
+  static constexpr int NR = LOWER8 ? 1 : 2;         // rows per lane
+  static constexpr int OWN = 2 * 32 * HD;           // K and V of one bf16 page
+  static constexpr int RING = SL * PART;            // per warp
+  static constexpr int SC = (kChunkPages + 2) * 32 * NR * 16;  // scores per warp: [page][lane][key block][row, key pair]
+  static_assert(RING >= 8 * NR * HD * 4, "the chunk's O fits the warp's ring");
+  static constexpr int smem(int own_slots) { return 1024 + own_slots * OWN + 4 * (RING + SC) + (4 * SL + 2) * 8 + 16; }
 };
 
-// LOWER8: the block holds at most 8 rows (their lanes' second rows hold none).
-template <int HD, int FMT, int SL, bool LOWER8>
-__global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUtensorMap kvmap, Attn8Args a) {
-  using C = Attn8Cfg<HD, SL>;
-  constexpr int NR = LOWER8 ? 1 : 2;  // rows per lane
-  constexpr int KK = HD / 16;
+template <int HD, int FMT, bool LOWER8>
+__global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
+    attn8_kernel(const __grid_constant__ CUtensorMap kvmap, Attn8Args a) {
+  using C = Attn8Cfg<HD, LOWER8>;
+  constexpr int NR = C::NR, SL = C::SL, KK = HD / 16, UNITS = Kv8Cfg<HD>::UNITS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -59,19 +62,21 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
   uint8_t* own_s = smem;
   uint8_t* ring0 = smem + a.own_slots * C::OWN;
   uint8_t* ring = ring0 + warp * C::RING;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring0 + 4 * C::RING);
+  float4* score = reinterpret_cast<float4*>(ring0 + 4 * C::RING + warp * C::SC) + lane * NR;  // page i at score[i * 32 * NR]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring0 + 4 * (C::RING + C::SC));
   uint64_t* bar = bars + warp * SL;
   uint64_t* own_bar = bars + 4 * SL;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(own_bar + 2);
-  __shared__ float fold_m[4][16], fold_l[4][16];
+  __shared__ float fold_m[4][8 * NR], fold_l[4][8 * NR];
 
   // Up to the wait for the previous kernel the CTA reads only the status word and
   // the plan (uploaded before the step's first kernel).
-  {
-    __shared__ int skip;
-    if (threadIdx.x == 0) skip = a.status ? *reinterpret_cast<volatile int*>(a.status) : 0;
-    __syncthreads();
-    if (skip) return;
+  __shared__ int skip;
+  if (threadIdx.x == 0) {
+    skip = a.status ? *reinterpret_cast<volatile int*>(a.status) : 0;
+    for (int k = 0; k < 4 * SL + 2; ++k) mbar_init(&bars[k], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
   }
   const int item = blockIdx.x;
   int lo_i = 0, hi_i = a.n_cls - 1;
@@ -81,9 +86,9 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
     lo_i += (31 - __clz(at)) * step;
     hi_i = min(hi_i, lo_i + step - 1);
   }
-  const int b = a.cls_seq[lo_i];
+  const int4 desc = a.cls_desc[lo_i];  // request, first token, tokens, cached tokens
+  const int b = desc.x, q0 = desc.y, qlen = desc.z, cached = desc.w;
   int local = item - a.cls_start[lo_i];
-  const int q0 = a.cu_q[b], qlen = a.cu_q[b + 1] - q0, cached = a.cached_len[b];
   const int kv_len = cached + qlen;
   const int G = a.Hq / a.Hkv;
   const int nsplit = (kv_len - 1) / kSplit8 + 1;
@@ -95,10 +100,6 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
   const int r_end = min(rows, r0 + 16);
   const int p_min = cached + r0 / G, p_max = cached + (r_end - 1) / G;
   const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
-  if (max(sidx * kSplit8, lo_min) > min(sidx * kSplit8 + kSplit8 - 1, p_max)) {  // no visible key of these rows
-    pdl_wait();  // the next kernel's wait covers this grid only, and this may be all of it
-    return;
-  }
   // this warp's chunk: pages [a8, a8 + n8) in 8 bits, [ao, ao + no) in bf16
   const int pg0 = (sidx * kSplit8 + warp * kChunk8) >> 4;
   const int own_lo = p_min >> 4, own_hi = p_max >> 4;
@@ -107,14 +108,11 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
   int pid = 0, opid = 0;
   if (lane < n8) pid = a.page_table[static_cast<size_t>(b) * a.pt_stride + a8 + lane];
   if (lane < no) opid = a.open_table[static_cast<size_t>(b) * a.open_stride + ao + lane - (cached >> 4)];
-  if (threadIdx.x == 0) {
-    for (int k = 0; k < 4 * SL + 2; ++k) mbar_init(&bars[k], 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+  if (skip) return;
+  if (max(sidx * kSplit8, lo_min) > min(sidx * kSplit8 + kSplit8 - 1, p_max)) return;  // no visible key of these rows
 
   // Copies of this warp: its K pages, then its V pages, copy j into slot j % SL,
   // issued by the lane that holds the page's id.
@@ -137,27 +135,27 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
   if (lane < n8) sc = a.scales[static_cast<size_t>(pid) * a.Hkv + kvh];
 
   // ---- this lane's rows g (and g + 8), their queries as fp16 fragments
-  int pos[NR], lo[NR], own[NR], tok[NR], hq[NR];
-  bool valid[NR];
+  int pos[NR], lo[NR], own[NR];
   uint32_t qf[KK][4];
   float rowfac[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     const int row = r0 + gq + 8 * r;
-    valid[r] = row < rows;
-    tok[r] = row / G;
-    hq[r] = kvh * G + row % G;
-    pos[r] = valid[r] ? cached + tok[r] : -1;
+    const bool valid = row < rows;
+    const int tok = row / G, hq = kvh * G + row % G;
+    pos[r] = valid ? cached + tok : -1;
     own[r] = pos[r] >> 4;  // -1 for a row that is none
-    lo[r] = valid[r] ? (a.window > 0 ? max(0, pos[r] - a.window + 1) : 0) : 1;
-    const __nv_bfloat16* qr = a.q + (static_cast<size_t>(q0 + tok[r]) * a.Hq + hq[r]) * HD + t4 * 2;
+    lo[r] = valid ? (a.window > 0 ? max(0, pos[r] - a.window + 1) : 0) : 1;
+    const __nv_bfloat16* qr = a.q + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD + t4 * 2;
     uint32_t mx = 0u;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
-      qf[kk][r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16) : 0u;
-      qf[kk][2 + r] = valid[r] ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8) : 0u;
-      mx = __vmaxu2(mx, __vmaxu2(qf[kk][r] & 0x7fff7fffu, qf[kk][2 + r] & 0x7fff7fffu));
+      qf[kk][r] = valid ? *reinterpret_cast<const uint32_t*>(qr + kk * 16) : 0u;
+      qf[kk][2 + r] = valid ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8) : 0u;
     }
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk)
+      mx = __vmaxu2(mx, __vmaxu2(qf[kk][r] & 0x7fff7fffu, qf[kk][2 + r] & 0x7fff7fffu));
     mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const int e = kv8_exp(kv8_max_halves(mx));
@@ -181,137 +179,149 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
   int used = 0;  // copies waited for
   // The slot of copy j is free: copy j + SL goes there.
   auto refill = [&](int j) {
-    __syncwarp();
     const int k = j + SL;
     if (k < 2 * n8) {
       if (lane == (k < n8 ? k : k - n8)) issue(k, k >= n8);
       issued = k + 1;
     }
   };
+  // Pages whose every key every row of the block sees (rows that are none aside)
+  // take no masking: [full_lo, own_lo).
+  const int full_lo = a.window > 0 ? (max(0, p_max - a.window + 1) + 15) >> 4 : 0;
+  auto full = [&](int pg) { return pg >= full_lo && pg < own_lo; };
 
-  // ---- scores of the 8-bit pages
-  float s[kChunkPages][2][2 * NR];  // [page][key block][row, key pair]
+  // ---- scores of the 8-bit pages, two at a time (four chains of products); the
+  // odd last one is taken twice
   float mx[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
-  // pages whose every key every row of the block sees (rows that are none aside)
-  const int full_lo = a.window > 0 ? (max(0, p_max - a.window + 1) + 15) >> 4 : 0;
+#pragma unroll 1
+  for (int i = 0; i < n8; i += 2) {
+    const int i1 = min(i + 1, n8 - 1);
+    if (!wait(&bar[i % SL], (i / SL) & 1) || !wait(&bar[i1 % SL], (i1 / SL) & 1)) break;
+    used = i1 + 1;
+    const uint4* kp0 = reinterpret_cast<const uint4*>(ring + (i % SL) * C::PART) + lane;
+    const uint4* kp1 = reinterpret_cast<const uint4*>(ring + (i1 % SL) * C::PART) + lane;
+    float acc[2][2][4];
 #pragma unroll
-  for (int i = 0; i < kChunkPages; ++i) {
-    if (i < n8 && wait(&bar[i % SL], (i / SL) & 1)) {
-      used = i + 1;
-      const uint4* kp = reinterpret_cast<const uint4*>(ring + (i % SL) * C::PART) + lane;
-      float acc[2][4];
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+      for (int j = 0; j < 2; ++j) acc[x][j][0] = acc[x][j][1] = acc[x][j][2] = acc[x][j][3] = 0.f;
 #pragma unroll
-      for (int u = 0; u < Kv8Cfg<HD>::UNITS; ++u) {
-        const uint4 w = kp[u * 32];
-        uint32_t b0, b1;
-        kv8_expand<FMT>(w.x, b0, b1);
-        mma_f16_16816(acc[0], qf[2 * u], b0, b1);
-        kv8_expand<FMT>(w.y, b0, b1);
-        mma_f16_16816(acc[1], qf[2 * u], b0, b1);
-        kv8_expand<FMT>(w.z, b0, b1);
-        mma_f16_16816(acc[0], qf[2 * u + 1], b0, b1);
-        kv8_expand<FMT>(w.w, b0, b1);
-        mma_f16_16816(acc[1], qf[2 * u + 1], b0, b1);
-      }
-      refill(i);
-      const float ks = __shfl_sync(0xffffffffu, sc.x, i), lv = __shfl_sync(0xffffffffu, sc.z, i);
-      const int pgi = a8 + i;
-      const bool full = pgi < own_lo && pgi >= full_lo;
+    for (int u = 0; u < UNITS; ++u) {
+      const uint4 w0 = kp0[u * 32], w1 = kp1[u * 32];
+      uint32_t b0, b1;
+      kv8_expand<FMT>(w0.x, b0, b1);
+      mma_f16_16816(acc[0][0], qf[2 * u], b0, b1);
+      kv8_expand<FMT>(w0.y, b0, b1);
+      mma_f16_16816(acc[0][1], qf[2 * u], b0, b1);
+      kv8_expand<FMT>(w1.x, b0, b1);
+      mma_f16_16816(acc[1][0], qf[2 * u], b0, b1);
+      kv8_expand<FMT>(w1.y, b0, b1);
+      mma_f16_16816(acc[1][1], qf[2 * u], b0, b1);
+      kv8_expand<FMT>(w0.z, b0, b1);
+      mma_f16_16816(acc[0][0], qf[2 * u + 1], b0, b1);
+      kv8_expand<FMT>(w0.w, b0, b1);
+      mma_f16_16816(acc[0][1], qf[2 * u + 1], b0, b1);
+      kv8_expand<FMT>(w1.z, b0, b1);
+      mma_f16_16816(acc[1][0], qf[2 * u + 1], b0, b1);
+      kv8_expand<FMT>(w1.w, b0, b1);
+      mma_f16_16816(acc[1][1], qf[2 * u + 1], b0, b1);
+    }
+    __syncwarp();
+    refill(i);
+    if (i1 > i) refill(i1);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int ii = x ? i1 : i, pgi = a8 + ii;
+      const float ks = __shfl_sync(0xffffffffu, sc.x, ii), lv = __shfl_sync(0xffffffffu, sc.z, ii);
+      float v[NR][4];  // [row][key block, key of the pair]
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const float c = __fmul_rn(ks, rowfac[r]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int e = 0; e < 4; ++e) v[r][e] = __fmaf_rn(acc[x][e >> 1][2 * r + (e & 1)], c, lv);
+      }
+      if (!full(pgi)) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = __fmaf_rn(acc[j][2 * r + e], c, lv);
-            if (!full) {
-              const int key = pgi * 16 + j * 8 + t4 * 2 + e;
-              if (!(key >= lo[r] && pgi < own[r])) v = -INFINITY;
-            }
-            s[i][j][2 * r + e] = v;
-            mx[r] = fmaxf(mx[r], v);
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = pgi * 16 + (e >> 1) * 8 + t4 * 2 + (e & 1);
+            if (!(key >= lo[r] && pgi < own[r])) v[r][e] = -INFINITY;
           }
       }
-    } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2 * NR; ++e) s[i][j][e] = -INFINITY;
+      for (int r = 0; r < NR; ++r) {
+        mx[r] = fmaxf(mx[r], fmaxf(fmaxf(v[r][0], v[r][1]), fmaxf(v[r][2], v[r][3])));
+        score[ii * 32 * NR + r] = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+      }
     }
   }
   // ---- scores of the own pages
-  float so[2][2][2 * NR];
-#pragma unroll
-  for (int o = 0; o < 2; ++o)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 2 * NR; ++e) so[o][j][e] = -INFINITY;
-  int ve[2][2][2];  // [own page][key block][key of the pair]: the V token's exponent
-  if (no > 0) {
-    const int mi = lane >> 3, r8 = lane & 7;
-#pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      if (o >= no) break;
-      const int oi = ao + o - own_lo;
-      if (!wait(&own_bar[oi], 0)) break;
-      const uint32_t kb = smem_u32(own_s + oi * C::OWN), vb = kb + C::OWN / 2;
-      // largest magnitudes: of K tokens 8 j + g, then of V tokens 8 j + 2 t + {0, 1}
-      uint32_t km[2] = {0u, 0u}, vm[2] = {0u, 0u};
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        uint32_t w[4];
-        ldmatrix_x4(w, kb + kv_off<HD>((mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
-        km[0] = __vmaxu2(km[0], __vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu));
-        km[1] = __vmaxu2(km[1], __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-        ldmatrix_x4_trans(w, vb + kv_off<HD>((mi & 1) * 8 + r8, kk * 2 + (mi >> 1)));
-        vm[0] = __vmaxu2(vm[0], __vmaxu2(w[0] & 0x7fff7fffu, w[2] & 0x7fff7fffu));
-        vm[1] = __vmaxu2(vm[1], __vmaxu2(w[1] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-      }
-      int ke[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        km[j] = __vmaxu2(km[j], __shfl_xor_sync(0xffffffffu, km[j], 1));
-        km[j] = __vmaxu2(km[j], __shfl_xor_sync(0xffffffffu, km[j], 2));
-        ke[j] = kv8_exp(kv8_max_halves(km[j]));
-#pragma unroll
-        for (int x = 4; x < 32; x *= 2) vm[j] = __vmaxu2(vm[j], __shfl_xor_sync(0xffffffffu, vm[j], x));
-        ve[o][j][0] = kv8_exp(vm[j] & 0xffffu);
-        ve[o][j][1] = kv8_exp(vm[j] >> 16);
-      }
-      const float kup[2] = {kv8_up(ke[0]), kv8_up(ke[1])};
-      float acc[2][4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        uint32_t w[4];
-        ldmatrix_x4(w, kb + kv_off<HD>((mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
-        mma_f16_16816(acc[0], qf[kk], kv8_to_f16(w[0], kup[0]), kv8_to_f16(w[1], kup[0]));
-        mma_f16_16816(acc[1], qf[kk], kv8_to_f16(w[2], kup[1]), kv8_to_f16(w[3], kup[1]));
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int kx = __shfl_sync(0xffffffffu, ke[j], (2 * t4 + e) * 4), vx = ve[o][j][e];
-          const float kd = kx == 255 ? kv8_nan() : kv8_down(kx);
-          const float lv = vx == 255 ? kv8_nan() : kv8_log2_down(vx);
-          const int key = (ao + o) * 16 + j * 8 + t4 * 2 + e;
-#pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const bool vis = key >= lo[r] && key <= pos[r] && ao + o == own[r];
-            const float v = vis ? __fmaf_rn(acc[j][2 * r + e], __fmul_rn(kd, rowfac[r]), lv) : -INFINITY;
-            so[o][j][2 * r + e] = v;
-            mx[r] = fmaxf(mx[r], v);
-          }
-        }
+  int ve[2][4];  // [own page][key]: the exponents of V tokens 2t, 2t + 1, 2t + 8, 2t + 9
+  const int mi = lane >> 3, r8 = lane & 7;
+#pragma unroll 1
+  for (int o = 0; o < no; ++o) {
+    const int oi = ao + o - own_lo;
+    if (!wait(&own_bar[oi], 0)) break;
+    const uint32_t kb = smem_u32(own_s + oi * C::OWN), vb = kb + C::OWN / 2;
+    // largest magnitudes: of K tokens 8 j + g, then of V tokens 8 j + 2 t + {0, 1}
+    uint32_t km[2] = {0u, 0u}, vm[2] = {0u, 0u};
+#pragma unroll 4
+    for (int kk = 0; kk < KK; ++kk) {
+      uint32_t w[4];
+      ldmatrix_x4(w, kb + kv_off<HD>((mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
+      km[0] = __vmaxu2(km[0], __vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu));
+      km[1] = __vmaxu2(km[1], __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+      ldmatrix_x4_trans(w, vb + kv_off<HD>((mi & 1) * 8 + r8, kk * 2 + (mi >> 1)));
+      vm[0] = __vmaxu2(vm[0], __vmaxu2(w[0] & 0x7fff7fffu, w[2] & 0x7fff7fffu));
+      vm[1] = __vmaxu2(vm[1], __vmaxu2(w[1] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
     }
+    int ke[2], vx[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      km[j] = __vmaxu2(km[j], __shfl_xor_sync(0xffffffffu, km[j], 1));
+      km[j] = __vmaxu2(km[j], __shfl_xor_sync(0xffffffffu, km[j], 2));
+      ke[j] = kv8_exp(kv8_max_halves(km[j]));
+#pragma unroll
+      for (int x = 4; x < 32; x *= 2) vm[j] = __vmaxu2(vm[j], __shfl_xor_sync(0xffffffffu, vm[j], x));
+      vx[2 * j] = kv8_exp(vm[j] & 0xffffu);
+      vx[2 * j + 1] = kv8_exp(vm[j] >> 16);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (o == 0) ve[0][x] = vx[x];
+      else ve[1][x] = vx[x];
+    }
+    const float kup[2] = {kv8_up(ke[0]), kv8_up(ke[1])};
+    float acc[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      uint32_t w[4];
+      ldmatrix_x4(w, kb + kv_off<HD>((mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
+      mma_f16_16816(acc[0], qf[kk], kv8_to_f16(w[0], kup[0]), kv8_to_f16(w[1], kup[0]));
+      mma_f16_16816(acc[1], qf[kk], kv8_to_f16(w[2], kup[1]), kv8_to_f16(w[3], kup[1]));
+    }
+    float v[NR][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int kx = __shfl_sync(0xffffffffu, ke[e >> 1], (2 * t4 + (e & 1)) * 4);
+      const float kd = kx == 255 ? kv8_nan() : kv8_down(kx);
+      const float lv = vx[e] == 255 ? kv8_nan() : kv8_log2_down(vx[e]);
+      const int key = (ao + o) * 16 + (e >> 1) * 8 + t4 * 2 + (e & 1);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const bool vis = key >= lo[r] && key <= pos[r] && ao + o == own[r];
+        v[r][e] = vis ? __fmaf_rn(acc[e >> 1][2 * r + (e & 1)], __fmul_rn(kd, rowfac[r]), lv) : -INFINITY;
+        mx[r] = fmaxf(mx[r], v[r][e]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+      score[(kChunkPages + o) * 32 * NR + r] = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
   }
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
@@ -319,84 +329,79 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
     mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
   }
 
-  // ---- weights, their sums and P V
+  // ---- weights, their sums and P V.  A masked score is -inf and its weight 0; a
+  // row that sees no key of the chunk (m = -inf) may get NaN here, in its own O
+  // and l only, which the fold below leaves out.
   float l[NR], o_acc[HD / 8][4];
 #pragma unroll
   for (int r = 0; r < NR; ++r) l[r] = 0.f;
 #pragma unroll
   for (int n = 0; n < HD / 8; ++n) o_acc[n][0] = o_acc[n][1] = o_acc[n][2] = o_acc[n][3] = 0.f;
+  auto weights = [&](int i, float (&p)[NR][4], uint32_t (&pa)[4]) {
+    if (LOWER8) pa[1] = pa[3] = 0u;
 #pragma unroll
-  for (int i = 0; i < kChunkPages; ++i) {
-    const int cp = n8 + i;  // the copy of page i's V
-    if (i < n8 && wait(&bar[cp % SL], (cp / SL) & 1)) {
-      used = cp + 1;
-      const float iv = __shfl_sync(0xffffffffu, sc.y, i);
-      const bool full = a8 + i < own_lo && a8 + i >= full_lo;
-      uint32_t pa[4];
-      if (LOWER8) pa[1] = pa[3] = 0u;
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float p[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          p[x] = ex2(__fsub_rn(s[i][x >> 1][2 * r + (x & 1)], mx[r]));
-          if (!full) {
-            const int key = (a8 + i) * 16 + (x >> 1) * 8 + t4 * 2 + (x & 1);
-            if (!(key >= lo[r] && a8 + i < own[r])) p[x] = 0.f;
-          }
-        }
-        float ps = __fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3]));
-        ps = __fmaf_rn(ps, iv, l[r]);
-        // (a page that the row does not see stays out, whatever its scale)
-        l[r] = full || (a8 + i < own[r] && (a8 + i) * 16 + 15 >= lo[r]) ? ps : l[r];
-        pa[r] = pack_f16x2(p[0], p[1]);
-        pa[2 + r] = pack_f16x2(p[2], p[3]);
-      }
-      const uint4* vp = reinterpret_cast<const uint4*>(ring + (cp % SL) * C::PART) + lane;
-#pragma unroll
-      for (int u = 0; u < Kv8Cfg<HD>::UNITS; ++u) {
-        const uint4 w = vp[u * 32];
-        uint32_t b0, b1;
-        kv8_expand<FMT>(w.x, b0, b1);
-        mma_f16_16816(o_acc[4 * u], pa, b0, b1);
-        kv8_expand<FMT>(w.y, b0, b1);
-        mma_f16_16816(o_acc[4 * u + 1], pa, b0, b1);
-        kv8_expand<FMT>(w.z, b0, b1);
-        mma_f16_16816(o_acc[4 * u + 2], pa, b0, b1);
-        kv8_expand<FMT>(w.w, b0, b1);
-        mma_f16_16816(o_acc[4 * u + 3], pa, b0, b1);
-      }
-      refill(cp);
+    for (int r = 0; r < NR; ++r) {
+      const float4 v = score[i * 32 * NR + r];
+      p[r][0] = ex2(__fsub_rn(v.x, mx[r]));
+      p[r][1] = ex2(__fsub_rn(v.y, mx[r]));
+      p[r][2] = ex2(__fsub_rn(v.z, mx[r]));
+      p[r][3] = ex2(__fsub_rn(v.w, mx[r]));
+      pa[r] = pack_f16x2(p[r][0], p[r][1]);
+      pa[2 + r] = pack_f16x2(p[r][2], p[r][3]);
     }
-  }
-  if (no > 0 && ok) {
-    const int mi = lane >> 3, r8 = lane & 7;
+  };
+#pragma unroll 1
+  for (int i = 0; i < n8; ++i) {
+    const int cp = n8 + i;  // the copy of page i's V
+    float p[NR][4];
+    uint32_t pa[4];
+    weights(i, p, pa);
+    const float iv = __shfl_sync(0xffffffffu, sc.y, i);
 #pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      if (o >= no) break;
+    for (int r = 0; r < NR; ++r) {
+      const float ps = __fadd_rn(__fadd_rn(p[r][0], p[r][1]), __fadd_rn(p[r][2], p[r][3]));
+      const float ln = __fmaf_rn(ps, iv, l[r]);
+      // (a page that the row does not see stays out, whatever its scale)
+      if (full(a8 + i) || (a8 + i < own[r] && (a8 + i) * 16 + 15 >= lo[r])) l[r] = ln;
+    }
+    if (!wait(&bar[cp % SL], (cp / SL) & 1)) break;
+    used = cp + 1;
+    const uint4* vp = reinterpret_cast<const uint4*>(ring + (cp % SL) * C::PART) + lane;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      const uint4 w = vp[u * 32];
+      uint32_t b0, b1;
+      kv8_expand<FMT>(w.x, b0, b1);
+      mma_f16_16816(o_acc[4 * u], pa, b0, b1);
+      kv8_expand<FMT>(w.y, b0, b1);
+      mma_f16_16816(o_acc[4 * u + 1], pa, b0, b1);
+      kv8_expand<FMT>(w.z, b0, b1);
+      mma_f16_16816(o_acc[4 * u + 2], pa, b0, b1);
+      kv8_expand<FMT>(w.w, b0, b1);
+      mma_f16_16816(o_acc[4 * u + 3], pa, b0, b1);
+    }
+    __syncwarp();
+    refill(cp);
+  }
+  if (ok) {
+#pragma unroll 1
+    for (int o = 0; o < no; ++o) {
       const uint32_t vb = smem_u32(own_s + (ao + o - own_lo) * C::OWN + C::OWN / 2);
-      float up[4];   // of keys 2t, 2t + 1, 2t + 8, 2t + 9 (0: a token that is not finite, whose weight is NaN or 0)
-      bool fin[4];
+      float up[4];    // of keys 2t, 2t + 1, 2t + 8, 2t + 9
+      uint32_t keep[2] = {0u, 0u};  // fp16 pairs: a token that is not finite counts as 0 here (its weight is NaN, or 0)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        up[x] = kv8_up(ve[o][x >> 1][x & 1]);
-        fin[x] = ve[o][x >> 1][x & 1] != 255;
+        const int e = o == 0 ? ve[0][x] : ve[1][x];
+        up[x] = kv8_up(e);
+        if (e != 255) keep[x >> 1] |= 0xffffu << (16 * (x & 1));
       }
+      float p[NR][4];
       uint32_t pa[4];
-      if (LOWER8) pa[1] = pa[3] = 0u;
+      weights(kChunkPages + o, p, pa);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float p[4];
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = (ao + o) * 16 + (x >> 1) * 8 + t4 * 2 + (x & 1);
-          const bool vis = key >= lo[r] && key <= pos[r] && ao + o == own[r];
-          p[x] = vis ? ex2(__fsub_rn(so[o][x >> 1][2 * r + (x & 1)], mx[r])) : 0.f;
-          l[r] = vis ? __fmaf_rn(p[x], up[x], l[r]) : l[r];
-        }
-        pa[r] = pack_f16x2(p[0], p[1]);
-        pa[2 + r] = pack_f16x2(p[2], p[3]);
-      }
+        for (int x = 0; x < 4; ++x) l[r] = __fmaf_rn(p[r][x], up[x], l[r]);
 #pragma unroll
       for (int np = 0; np < HD / 16; ++np) {
         uint32_t w[4];
@@ -404,8 +409,8 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t x0 = w[2 * h], x1 = w[2 * h + 1];
-          const uint32_t b0 = pack_f16x2(fin[0] ? __fmul_rn(bf16_lo(x0), up[0]) : 0.f, fin[1] ? __fmul_rn(bf16_hi(x0), up[1]) : 0.f);
-          const uint32_t b1 = pack_f16x2(fin[2] ? __fmul_rn(bf16_lo(x1), up[2]) : 0.f, fin[3] ? __fmul_rn(bf16_hi(x1), up[3]) : 0.f);
+          const uint32_t b0 = pack_f16x2(__fmul_rn(bf16_lo(x0), up[0]), __fmul_rn(bf16_hi(x0), up[1])) & keep[0];
+          const uint32_t b1 = pack_f16x2(__fmul_rn(bf16_lo(x1), up[2]), __fmul_rn(bf16_hi(x1), up[3])) & keep[1];
           mma_f16_16816(o_acc[2 * np + h], pa, b0, b1);
         }
       }
@@ -422,7 +427,8 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
   }
 
   // ---- the chunks of the split, left to right.  Each warp's O goes to its own
-  // ring, all of whose copies have been used.
+  // ring, all of whose copies have been used; 8-float groups of a row are XORed
+  // with the row, so that the stores of a warp meet no bank twice.
   __syncwarp();
   float* fo = reinterpret_cast<float*>(ring);  // [row][HD]
 #pragma unroll
@@ -433,7 +439,7 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
     }
 #pragma unroll
     for (int n = 0; n < HD / 8; ++n)
-      *reinterpret_cast<float2*>(fo + (gq + 8 * r) * HD + n * 8 + t4 * 2) =
+      *reinterpret_cast<float2*>(fo + (gq + 8 * r) * HD + ((n ^ gq) * 8) + t4 * 2) =
           make_float2(o_acc[n][2 * r], o_acc[n][2 * r + 1]);
   }
   __syncthreads();
@@ -451,29 +457,26 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
     if (max(flo, k0) > min(p, k0 + kChunk8 - 1)) continue;  // the row sees no key of the chunk
     const float m = fold_m[w][frow], lw = fold_l[w][frow];
     const float* src = reinterpret_cast<const float*>(ring0 + w * C::RING) + frow * HD;
+    float x[PER];
+#pragma unroll
+    for (int i = 0; i < PER / 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(src + (((i * TPR + fd) * 4) ^ ((frow & 7) * 8)));
+      x[4 * i] = v.x;
+      x[4 * i + 1] = v.y;
+      x[4 * i + 2] = v.z;
+      x[4 * i + 3] = v.w;
+    }
     if (!any) {
       M = m;
       L = lw;
 #pragma unroll
-      for (int i = 0; i < PER / 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(src + (i * TPR + fd) * 4);
-        O[4 * i] = v.x;
-        O[4 * i + 1] = v.y;
-        O[4 * i + 2] = v.z;
-        O[4 * i + 3] = v.w;
-      }
+      for (int i = 0; i < PER; ++i) O[i] = x[i];
       any = true;
     } else {
       const float mn = fmaxf(M, m), ca = ex2(__fsub_rn(M, mn)), cb = ex2(__fsub_rn(m, mn));
       L = __fadd_rn(__fmul_rn(L, ca), __fmul_rn(lw, cb));
 #pragma unroll
-      for (int i = 0; i < PER / 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(src + (i * TPR + fd) * 4);
-        O[4 * i] = __fadd_rn(__fmul_rn(O[4 * i], ca), __fmul_rn(v.x, cb));
-        O[4 * i + 1] = __fadd_rn(__fmul_rn(O[4 * i + 1], ca), __fmul_rn(v.y, cb));
-        O[4 * i + 2] = __fadd_rn(__fmul_rn(O[4 * i + 2], ca), __fmul_rn(v.z, cb));
-        O[4 * i + 3] = __fadd_rn(__fmul_rn(O[4 * i + 3], ca), __fmul_rn(v.w, cb));
-      }
+      for (int i = 0; i < PER; ++i) O[i] = __fadd_rn(__fmul_rn(O[i], ca), __fmul_rn(x[i], cb));
       M = mn;
     }
   }
@@ -491,12 +494,10 @@ __global__ void __launch_bounds__(128) attn8_kernel(const __grid_constant__ CUte
 
 template <int HD, int FMT, bool LOWER8>
 int launch_attn8_t(const CUtensorMap& kvmap, const Attn8Args& a, int n_items, cudaStream_t s) {
-  constexpr int SL = 6;
-  using C = Attn8Cfg<HD, SL>;
+  using C = Attn8Cfg<HD, LOWER8>;
   static_assert(C::smem(2) + 1024 <= 227 * 1024, "shared memory");
-  VD_CUDA_TRY(cudaFuncSetAttribute(attn8_kernel<HD, FMT, SL, LOWER8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   C::smem(2)));
-  VD_CUDA_TRY(launch_k(attn8_kernel<HD, FMT, SL, LOWER8>, dim3(n_items), dim3(128), C::smem(a.own_slots), s, kvmap, a));
+  VD_CUDA_TRY(cudaFuncSetAttribute(attn8_kernel<HD, FMT, LOWER8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2)));
+  VD_CUDA_TRY(launch_k(attn8_kernel<HD, FMT, LOWER8>, dim3(n_items), dim3(128), C::smem(a.own_slots), s, kvmap, a));
   return VD_OK;
 }
 

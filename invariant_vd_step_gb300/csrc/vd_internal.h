@@ -237,11 +237,9 @@ struct Attn8Args {
   const __nv_bfloat16* q;   // [T][Hq][hd]
   float* part_o;            // [T][Hq][max_splits][hd]
   float* part_ml;           // [T][Hq][max_splits][2]
-  const int* cu_q;          // [B + 1]
-  const int* cached_len;    // [B]
   const int* page_table;    // [B][pt_stride] pages of the cache
   const int* open_table;    // [B][open_stride] pages of the bf16 pool, from logical page cached_len / 16 on
-  const int* cls_seq;       // seqs of this launch class
+  const int4* cls_desc;     // [n_cls] requests of this launch class: number, first token, tokens, cached tokens
   const int* cls_start;     // [n_cls + 1] item prefix sums
   const uint8_t* codes;     // the layer's first page
   const float4* scales;
