@@ -49,6 +49,9 @@ struct vd_kv8_plan {
 
 namespace {
 
+// Runs of splits per SM that the tcgen05 blocks are cut into, if they have as many.
+constexpr int kRunsPerSM = 4;
+
 int check_device(const vd_model* m) {
   int dev = -1;
   VD_CUDA_TRY(cudaGetDevice(&dev));
@@ -187,7 +190,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   if (R > 0 && !b->logit_rows) return fail(VD_ERR_INVALID_ARG, "missing logit_rows");
   if (b->cu_q[0] != 0 || b->cu_q[B] != T) return fail(VD_ERR_INVALID_ARG, "cu_q must run from 0 to num_tokens");
   // lengths, table widths, page ids
-  int stride = 0, open_stride = 0, splits = 1, n_seal = 0, most_q = 1, most_dec = 0, n_dec = 0;
+  int stride = 0, open_stride = 0, splits = 1, n_seal = 0, most_q = 1, most_dec = 0;
   for (int i = 0; i < B; ++i) {
     const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i];
     if (ql < 1 || b->cu_q[i + 1] > T) return fail(VD_ERR_INVALID_ARG, "every request needs q_len >= 1");
@@ -205,7 +208,6 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     if (ql * m->G <= 16) {
       most_q = std::max(most_q, ql);
       most_dec = std::max(most_dec, ql * m->G);
-      ++n_dec;
     }
   }
   for (int k = 0; b->token_ids && k < T; ++k)
@@ -252,15 +254,45 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     off += n;
     return static_cast<int>(o);
   };
-  d.cls_desc = take(4 * static_cast<size_t>(B));   // int4, then int2: first, for their alignment
+  // Attention blocks: 16 rows and a split for decode-shaped requests, 256 rows and
+  // a run of splits on tcgen05 for the others (16 rows and a split where that kernel
+  // does not go); for global layers and, without the splits that the window hides,
+  // for local ones.
+  std::vector<int> blocks[4];
+  const bool windowed = c.sliding_window > 0 && c.local_global_period > 0;
+  d.pre_tc = m->prefill_kernel == 0 && c.head_dim <= 128;
+  for (int local = 0; local <= (windowed ? 1 : 0); ++local)
+    for (int pre = 0; pre < 2; ++pre) {
+      const int step = pre && d.pre_tc ? 256 : 16;
+      std::vector<int>& to = blocks[2 * local + pre];
+      long long units = 0;
+      for (int pass = 0; pass < 2; ++pass) {  // the (row block, split) pairs are counted, then dealt out
+        const int run = pre && d.pre_tc ? static_cast<int>(std::max(1LL, units * c.n_kv_heads / (kRunsPerSM * m->n_sm))) : 1;
+        for (int i = 0; i < B; ++i) {
+          const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i], rows = ql * m->G;
+          if ((rows > 16) != (pre == 1)) continue;
+          for (int r0 = 0; r0 < rows; r0 += step) {
+            const int first = local ? std::max(0, cached + r0 / m->G - c.sliding_window + 1) / kAttn8Split : 0;
+            const int end = (cached + (std::min(rows, r0 + step) - 1) / m->G) / kAttn8Split + 1;
+            units += end - first;
+            if (pass)
+              for (int sp = first; sp < end; sp += run)
+                to.insert(to.end(), {i, b->cu_q[i], ql, cached, sp, r0, std::min(end, sp + run), 0});
+          }
+        }
+      }
+    }
+  for (int k = 0; k < 4; ++k) {  // int4, then int2: first, for their alignment
+    if (blocks[k].size() / 8 * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
+    d.items[k] = take(blocks[k].size());
+    d.n_items[k] = static_cast<int>(blocks[k].size() / 8);
+  }
   d.seal = take(2 * static_cast<size_t>(n_seal));
   d.n_seal = n_seal;
   d.tokens = take(T);
   d.positions = take(T);
   d.slot_page = take(T);
   d.logit_rows = take(R);
-  d.dec_start = take(B + 1);
-  d.pre_start = take(B + 1);
   d.open_stride = open_stride;
   d.open_table = take(static_cast<size_t>(B) * open_stride);
   d.page_table = take(static_cast<size_t>(B) * stride);
@@ -269,14 +301,6 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   d.part_splits = splits;
   d.own_slots = most_q > 1 ? 2 : 1;
   d.lower8 = most_dec <= 8;
-  long long items[2] = {0, 0};
-  auto items_of = [&](int i, int rows_per_cta) {
-    const int ql = b->cu_q[i + 1] - b->cu_q[i], kv = b->cached_len[i] + ql;
-    return static_cast<long long>((ql * m->G + rows_per_cta - 1) / rows_per_cta) * c.n_kv_heads * ((kv - 1) / kAttn8Split + 1);
-  };
-  for (int i = 0; i < B; ++i) items[(b->cu_q[i + 1] - b->cu_q[i]) * m->G > 16] += items_of(i, 16);
-  if (items[0] > 0x7fffffffLL || items[1] > 0x7fffffffLL) return fail(VD_ERR_CAPACITY, "plan too large");
-
   const int slot = t->slot;
   VD_CUDA_TRY(cudaEventSynchronize(t->uploaded[slot]));  // this staging buffer's previous copy is done
   if (t->host_cap[slot] < off) {
@@ -310,22 +334,8 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       h[d.positions + q0 + k] = cached + k;
       h[d.slot_page + q0 + k] = h[d.open_table + static_cast<size_t>(i) * open_stride + (cached + k) / 16 - first];
     }
-    const bool dec = ql * m->G <= 16;  // the decode class's descriptions, then the other one's
-    int* at = h + d.cls_desc + 4 * static_cast<size_t>(dec ? d.n_dec : n_dec + d.n_pre);
-    at[0] = i;
-    at[1] = q0;
-    at[2] = ql;
-    at[3] = cached;
-    if (dec) {
-      h[d.dec_start + d.n_dec++] = d.items_dec;
-      d.items_dec += static_cast<int>(items_of(i, 16));
-    } else {
-      h[d.pre_start + d.n_pre++] = d.items_pre;
-      d.items_pre += static_cast<int>(items_of(i, 16));
-    }
   }
-  h[d.dec_start + d.n_dec] = d.items_dec;
-  h[d.pre_start + d.n_pre] = d.items_pre;
+  for (int k = 0; k < 4; ++k) std::copy(blocks[k].begin(), blocks[k].end(), h + d.items[k]);
   for (int j = 0; j < R; ++j) h[d.logit_rows + j] = b->logit_rows[j];
   d.base = t->dev;
   d.part_o = t->part;
@@ -369,27 +379,23 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
   a.open_stride = d.open_stride;
   a.Hq = c.n_heads;
   a.Hkv = c.n_kv_heads;
+  a.open = static_cast<const __nv_bfloat16*>(pool->data) +
+           static_cast<size_t>(layer) * pool->num_pages * 2 * c.n_kv_heads * 16 * c.head_dim;
   a.layer_row0 = static_cast<int>(static_cast<long long>(layer) * pool->num_pages * 2 * c.n_kv_heads * 16);
   a.window = layer_is_local(c, layer) ? c.sliding_window : 0;
   a.max_splits = d.part_splits;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(c.head_dim)));
   a.status = m->status;
   int rc;
-  if (d.n_dec) {
+  for (int cls = 0; cls < 2; ++cls) {  // decode-shaped requests, then the others
+    const int k = cls + (a.window > 0 ? 2 : 0);
+    if (d.n_items[k] == 0) continue;
     Prof p(m, K_ATTN, s);
-    a.cls_desc = reinterpret_cast<const int4*>(d.base + d.cls_desc);
-    a.cls_start = d.base + d.dec_start;
-    a.n_cls = d.n_dec;
-    a.own_slots = d.own_slots;
-    if ((rc = launch_attention8(pool->map, a, c.head_dim, d.kv8->format, d.lower8, d.items_dec, s))) return rc;
-  }
-  if (d.n_pre) {
-    Prof p(m, K_ATTN, s);
-    a.cls_desc = reinterpret_cast<const int4*>(d.base + d.cls_desc) + d.n_dec;
-    a.cls_start = d.base + d.pre_start;
-    a.n_cls = d.n_pre;
-    a.own_slots = 2;
-    if ((rc = launch_attention8(pool->map, a, c.head_dim, d.kv8->format, false, d.items_pre, s))) return rc;
+    a.items = reinterpret_cast<const int4*>(d.base + d.items[k]);
+    a.own_slots = cls ? 2 : d.own_slots;
+    if ((rc = cls && d.pre_tc ? launch_attention8_tc(a, c.head_dim, d.kv8->format, d.n_items[k], s)
+                              : launch_attention8(pool->map, a, c.head_dim, d.kv8->format, !cls && d.lower8, d.n_items[k], s)))
+      return rc;
   }
   MergeArgs g{};
   g.part_o = d.part_o;

@@ -78,25 +78,14 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  const int item = blockIdx.x;
-  int lo_i = 0, hi_i = a.n_cls - 1;
-  while (lo_i < hi_i) {  // last j with cls_start[j] <= item: 32 of them per memory round trip
-    const int step = (hi_i - lo_i) / 32 + 1, j = lo_i + lane * step;
-    const unsigned at = __ballot_sync(0xffffffffu, j <= hi_i && a.cls_start[j] <= item);  // lane 0 always
-    lo_i += (31 - __clz(at)) * step;
-    hi_i = min(hi_i, lo_i + step - 1);
-  }
-  const int4 desc = a.cls_desc[lo_i];  // request, first token, tokens, cached tokens
-  const int b = desc.x, q0 = desc.y, qlen = desc.z, cached = desc.w;
-  int local = item - a.cls_start[lo_i];
-  const int kv_len = cached + qlen;
+  // The block: its request, rows and split come from the plan in one round trip
+  // (a search over the requests took three), the KV heads of one split side by
+  // side, so that CTAs in flight together read whole pages.
+  const int kvh = blockIdx.x % a.Hkv;
+  const int4 d0 = a.items[2 * (blockIdx.x / a.Hkv)], d1 = a.items[2 * (blockIdx.x / a.Hkv) + 1];
+  const int b = d0.x, q0 = d0.y, qlen = d0.z, cached = d0.w, sidx = d1.x, r0 = d1.y;
   const int G = a.Hq / a.Hkv;
-  const int nsplit = (kv_len - 1) / kSplit8 + 1;
-  const int sidx = local % nsplit;
-  local /= nsplit;
-  const int kvh = local % a.Hkv;
   const int rows = qlen * G;
-  const int r0 = (local / a.Hkv) * 16;
   const int r_end = min(rows, r0 + 16);
   const int p_min = cached + r0 / G, p_max = cached + (r_end - 1) / G;
   const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
@@ -132,7 +121,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
     tma_load_3d(own_s + o * C::OWN + C::OWN / 2, &kvmap, &own_bar[o], 0, 0, row + a.Hkv * 16);
   }
   float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (lane < n8) sc = a.scales[static_cast<size_t>(pid) * a.Hkv + kvh];
+  if (lane < n8) sc = __ldcg(a.scales + static_cast<size_t>(pid) * a.Hkv + kvh);
 
   // ---- this lane's rows g (and g + 8), their queries as fp16 fragments
   int pos[NR], lo[NR], own[NR];
@@ -493,11 +482,11 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
 }
 
 template <int HD, int FMT, bool LOWER8>
-int launch_attn8_t(const CUtensorMap& kvmap, const Attn8Args& a, int n_items, cudaStream_t s) {
+int launch_attn8_t(const CUtensorMap& kvmap, const Attn8Args& a, int n_blocks, cudaStream_t s) {
   using C = Attn8Cfg<HD, LOWER8>;
   static_assert(C::smem(2) + 1024 <= 227 * 1024, "shared memory");
   VD_CUDA_TRY(cudaFuncSetAttribute(attn8_kernel<HD, FMT, LOWER8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2)));
-  VD_CUDA_TRY(launch_k(attn8_kernel<HD, FMT, LOWER8>, dim3(n_items), dim3(128), C::smem(a.own_slots), s, kvmap, a));
+  VD_CUDA_TRY(launch_k(attn8_kernel<HD, FMT, LOWER8>, dim3(static_cast<unsigned>(n_blocks) * a.Hkv), dim3(128), C::smem(a.own_slots), s, kvmap, a));
   return VD_OK;
 }
 
@@ -505,16 +494,16 @@ int launch_attn8_t(const CUtensorMap& kvmap, const Attn8Args& a, int n_items, cu
 
 static_assert(kAttn8Split == kSplit8, "split of the plan's items");
 
-int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int format, bool lower8, int n_items,
+int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int format, bool lower8, int n_blocks,
                       cudaStream_t s) {
-  if (n_items <= 0) return VD_OK;
+  if (n_blocks <= 0) return VD_OK;
 #define VD_ATTN8(HD_)                                                                                             \
   if (hd == HD_) {                                                                                                \
     if (format == VD_KV8_INT8)                                                                                    \
-      return lower8 ? launch_attn8_t<HD_, kKv8Int8, true>(kvmap, a, n_items, s)                                   \
-                    : launch_attn8_t<HD_, kKv8Int8, false>(kvmap, a, n_items, s);                                 \
-    return lower8 ? launch_attn8_t<HD_, kKv8E4m3, true>(kvmap, a, n_items, s)                                     \
-                  : launch_attn8_t<HD_, kKv8E4m3, false>(kvmap, a, n_items, s);                                   \
+      return lower8 ? launch_attn8_t<HD_, kKv8Int8, true>(kvmap, a, n_blocks, s)                                   \
+                    : launch_attn8_t<HD_, kKv8Int8, false>(kvmap, a, n_blocks, s);                                 \
+    return lower8 ? launch_attn8_t<HD_, kKv8E4m3, true>(kvmap, a, n_blocks, s)                                     \
+                  : launch_attn8_t<HD_, kKv8E4m3, false>(kvmap, a, n_blocks, s);                                   \
   }
   VD_ATTN8(64)
   VD_ATTN8(128)

@@ -239,11 +239,11 @@ struct Attn8Args {
   float* part_ml;           // [T][Hq][max_splits][2]
   const int* page_table;    // [B][pt_stride] pages of the cache
   const int* open_table;    // [B][open_stride] pages of the bf16 pool, from logical page cached_len / 16 on
-  const int4* cls_desc;     // [n_cls] requests of this launch class: number, first token, tokens, cached tokens
-  const int* cls_start;     // [n_cls + 1] item prefix sums
+  const int4* items;        // [blocks][2]: request, first token, tokens, cached tokens; split, first row, end of the
+                            // splits (tcgen05 kernel, whose blocks take several), 0
+  const __nv_bfloat16* open;  // the layer's first page of the bf16 pool
   const uint8_t* codes;     // the layer's first page
   const float4* scales;
-  int n_cls;
   int pt_stride, open_stride;
   int Hq, Hkv;
   int layer_row0;           // first row of this layer in the bf16 pool
@@ -254,8 +254,10 @@ struct Attn8Args {
   int* status;
 };
 // lower8: every block of the launch has at most 8 rows.
-int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int format, bool lower8, int n_items,
+int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int format, bool lower8, int n_blocks,
                       cudaStream_t s);
+// The same rows in blocks of 256 on tcgen05, head dimensions 64 and 128.
+int launch_attention8_tc(const Attn8Args& a, int hd, int format, int n_blocks, cudaStream_t s);
 // Sealing and its reverse, page copies (kv8.cu).  Pairs of page ids: `dev` on the
 // device (a plan's), or else in the launch's own arguments.
 constexpr int kPagePairs = 448;
