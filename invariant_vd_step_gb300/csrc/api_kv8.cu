@@ -254,7 +254,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     off += n;
     return static_cast<int>(o);
   };
-  // Attention blocks: 16 rows and a split for decode-shaped requests, 256 rows and
+  // Attention blocks: 16 rows and a split for decode-shaped requests, 128 rows and
   // a run of splits on tcgen05 for the others (16 rows and a split where that kernel
   // does not go); for global layers and, without the splits that the window hides,
   // for local ones.
@@ -263,7 +263,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   d.pre_tc = m->prefill_kernel == 0 && c.head_dim <= 128;
   for (int local = 0; local <= (windowed ? 1 : 0); ++local)
     for (int pre = 0; pre < 2; ++pre) {
-      const int step = pre && d.pre_tc ? 256 : 16;
+      const int step = pre && d.pre_tc ? 128 : 16;
       std::vector<int>& to = blocks[2 * local + pre];
       long long units = 0;
       for (int pass = 0; pass < 2; ++pass) {  // the (row block, split) pairs are counted, then dealt out

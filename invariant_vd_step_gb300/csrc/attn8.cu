@@ -7,23 +7,26 @@
 // 16), its bf16 version if i = own, nothing beyond.
 //
 // Per chunk and row, with codes c, K scale k, V scale v of each page and
-// everything else float32 unless stated:
+// everything else float32 unless stated; m0 is the row's maximum over the chunks
+// of the split before this one (-inf at the first):
 //   t_j = (q c_j) k scale + log2 v       (the product in fp16, exact operands)
-//   m   = max_j t_j,   p_j = 2^(t_j - m)
-//   l   = sum_j p_j / v,   O = sum_j fp16(p_j) c_j
+//   m   = max(m0, max_j t_j),   p_j = 2^(t_j - m),   alpha = 2^(m0 - m)
+//   l   = l alpha + sum_j p_j / v,   O = O alpha + sum_j fp16(p_j) c_j
 // so O / l is the softmax's mean of the values: the V scale rides in the
 // exponent and the codes enter the product as they are.  fp16(p) is off by 2^-12
-// of p or 2^-25 (the largest p of a chunk is 1), where bf16 would be off by 2^-9.
-// The row's own page takes part with a scale per token, a power of two that
-// makes its bf16 values exact in fp16 (kv8.cuh).  No state is rescaled within a
-// chunk: its 128 scores are all there before the maximum is taken.
+// of p or 2^-25 (the largest p is 1), where bf16 would be off by 2^-9.  The row's
+// own page takes part with a scale per token, a power of two that makes its bf16
+// values exact in fp16 (kv8.cuh).
 //
-// Order: the pages of a chunk ascending, the own page last; partial sums of l
-// over keys {2t, 2t+1, 8+2t, 9+2t} of each page in thread t of four, then (s_0 +
-// s_1) + (s_2 + s_3); the chunks of a split folded left to right with the merge
-// kernel's arithmetic, then the splits by the merge kernel.  A masked key has the
-// weight 0 and adds +0 to every sum.  None of it depends on the batch, the block
-// a row is in or the other rows.
+// Order: the pages of a chunk ascending, the own page last.  Keys 2t + e and 2t +
+// 8 + e of each page go to the partial sum l_(t, e) of eight, t < 4, e < 2, of
+// the chunk's first four pages or its last four; the half chunk's l is the sum
+// over t, as (0 + 1) + (2 + 3), of l_(t, 0) + l_(t, 1), and the halves are added at
+// the end of the split.  The four chunks of a split run side by side, one per
+// warp, share their maxima before they take their weights, and are folded left to
+// right (one fma per value); the merge kernel folds the splits.  A masked key has
+// the weight 0 and adds +0 to every sum.  None of it depends on the batch, the
+// block a row is in or the other rows.
 #include <math.h>
 
 #include "attn_tile.cuh"
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   uint64_t* bar = bars + warp * SL;
   uint64_t* own_bar = bars + 4 * SL;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(own_bar + 2);
-  __shared__ float fold_m[4][8 * NR], fold_l[4][8 * NR];
+  __shared__ float fold_m[4][8 * NR], fold_l[2][4][8 * NR];  // per chunk and row: its largest score, its halves' l
 
   // Up to the wait for the previous kernel the CTA reads only the status word and
   // the plan (uploaded before the step's first kernel).
@@ -318,12 +321,26 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
     mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
   }
 
-  // ---- weights, their sums and P V.  A masked score is -inf and its weight 0; a
-  // row that sees no key of the chunk (m = -inf) may get NaN here, in its own O
-  // and l only, which the fold below leaves out.
-  float l[NR], o_acc[HD / 8][4];
+  // ---- the running maximum of the split at this chunk
+  if (t4 == 0)
 #pragma unroll
-  for (int r = 0; r < NR; ++r) l[r] = 0.f;
+    for (int r = 0; r < NR; ++r) fold_m[warp][gq + 8 * r] = mx[r];
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    for (int w = 0; w < warp; ++w) mx[r] = fmaxf(mx[r], fold_m[w][gq + 8 * r]);
+    if (mx[r] == -INFINITY) mx[r] = 0.f;  // no key seen so far: every score is -inf, every weight 0
+  }
+
+  // ---- weights, their sums and P V
+  float l[NR][2][2], o_acc[HD / 8][4];  // l: [half of the chunk's pages][e]
+#pragma unroll
+  for (int r = 0; r < NR; ++r) l[r][0][0] = l[r][0][1] = l[r][1][0] = l[r][1][1] = 0.f;
+  // weights x, 1 / V scales y of keys 2t, 2t + 1, 2t + 8, 2t + 9 of a page
+  auto add_l = [&](float (&s)[2], const float (&x)[4], float y0, float y1, float y2, float y3) {
+    s[0] = __fmaf_rn(x[2], y2, __fmaf_rn(x[0], y0, s[0]));
+    s[1] = __fmaf_rn(x[3], y3, __fmaf_rn(x[1], y1, s[1]));
+  };
 #pragma unroll
   for (int n = 0; n < HD / 8; ++n) o_acc[n][0] = o_acc[n][1] = o_acc[n][2] = o_acc[n][3] = 0.f;
   auto weights = [&](int i, float (&p)[NR][4], uint32_t (&pa)[4]) {
@@ -348,10 +365,11 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
     const float iv = __shfl_sync(0xffffffffu, sc.y, i);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const float ps = __fadd_rn(__fadd_rn(p[r][0], p[r][1]), __fadd_rn(p[r][2], p[r][3]));
-      const float ln = __fmaf_rn(ps, iv, l[r]);
       // (a page that the row does not see stays out, whatever its scale)
-      if (full(a8 + i) || (a8 + i < own[r] && (a8 + i) * 16 + 15 >= lo[r])) l[r] = ln;
+      if (full(a8 + i) || (a8 + i < own[r] && (a8 + i) * 16 + 15 >= lo[r])) {
+        if (a8 + i < pg0 + kChunkPages / 2) add_l(l[r][0], p[r], iv, iv, iv, iv);
+        else add_l(l[r][1], p[r], iv, iv, iv, iv);
+      }
     }
     if (!wait(&bar[cp % SL], (cp / SL) & 1)) break;
     used = cp + 1;
@@ -388,9 +406,10 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
       uint32_t pa[4];
       weights(kChunkPages + o, p, pa);
 #pragma unroll
-      for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) l[r] = __fmaf_rn(p[r][x], up[x], l[r]);
+      for (int r = 0; r < NR; ++r) {
+        if (ao + o < pg0 + kChunkPages / 2) add_l(l[r][0], p[r], up[0], up[1], up[2], up[3]);
+        else add_l(l[r][1], p[r], up[0], up[1], up[2], up[3]);
+      }
 #pragma unroll
       for (int np = 0; np < HD / 16; ++np) {
         uint32_t w[4];
@@ -406,10 +425,14 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
     }
   }
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 1));
-    l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 2));
-  }
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float x = __fadd_rn(l[r][h][0], l[r][h][1]);
+      x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 1));
+      x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      if (t4 == 0) fold_l[h][warp][gq + 8 * r] = x;
+    }
   if (!ok) {  // gave up: every copy lands before the warp leaves
     for (int j = used; j < issued; ++j) drain_wait(&bar[j % SL], (j / SL) & 1);
     for (int o = 0; o < no; ++o) drain_wait(&own_bar[ao + o - own_lo], 0);
@@ -422,10 +445,6 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   float* fo = reinterpret_cast<float*>(ring);  // [row][HD]
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    if (t4 == 0) {
-      fold_m[warp][gq + 8 * r] = mx[r];
-      fold_l[warp][gq + 8 * r] = l[r];
-    }
 #pragma unroll
     for (int n = 0; n < HD / 8; ++n)
       *reinterpret_cast<float2*>(fo + (gq + 8 * r) * HD + ((n ^ gq) * 8) + t4 * 2) =
@@ -437,48 +456,38 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   const int frow = threadIdx.x / TPR, fd = threadIdx.x % TPR;
   const int row = r0 + frow;
   if (row >= rows) return;
-  const int p = cached + row / G, flo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  float M = 0.f, L = 0.f, O[PER];
-  bool any = false;
+  float M = -INFINITY, L[2] = {0.f, 0.f}, O[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) O[i] = 0.f;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const int k0 = sidx * kSplit8 + w * kChunk8;
-    if (max(flo, k0) > min(p, k0 + kChunk8 - 1)) continue;  // the row sees no key of the chunk
-    const float m = fold_m[w][frow], lw = fold_l[w][frow];
     const float* src = reinterpret_cast<const float*>(ring0 + w * C::RING) + frow * HD;
-    float x[PER];
+    float alpha;
+    kv8_running_max(M, fold_m[w][frow], alpha);
+    L[0] = __fmaf_rn(L[0], alpha, fold_l[0][w][frow]);
+    L[1] = __fmaf_rn(L[1], alpha, fold_l[1][w][frow]);
 #pragma unroll
     for (int i = 0; i < PER / 4; ++i) {
       const float4 v = *reinterpret_cast<const float4*>(src + (((i * TPR + fd) * 4) ^ ((frow & 7) * 8)));
-      x[4 * i] = v.x;
-      x[4 * i + 1] = v.y;
-      x[4 * i + 2] = v.z;
-      x[4 * i + 3] = v.w;
-    }
-    if (!any) {
-      M = m;
-      L = lw;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) O[i] = x[i];
-      any = true;
-    } else {
-      const float mn = fmaxf(M, m), ca = ex2(__fsub_rn(M, mn)), cb = ex2(__fsub_rn(m, mn));
-      L = __fadd_rn(__fmul_rn(L, ca), __fmul_rn(lw, cb));
-#pragma unroll
-      for (int i = 0; i < PER; ++i) O[i] = __fadd_rn(__fmul_rn(O[i], ca), __fmul_rn(x[i], cb));
-      M = mn;
+      O[4 * i] = __fmaf_rn(O[4 * i], alpha, v.x);
+      O[4 * i + 1] = __fmaf_rn(O[4 * i + 1], alpha, v.y);
+      O[4 * i + 2] = __fmaf_rn(O[4 * i + 2], alpha, v.z);
+      O[4 * i + 3] = __fmaf_rn(O[4 * i + 3], alpha, v.w);
     }
   }
-  if (!any) return;
+  // a row that sees no key of the split has no partial
+  const int p = cached + row / G, flo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+  if (max(flo, sidx * kSplit8) > min(p, sidx * kSplit8 + kSplit8 - 1)) return;
   const size_t base = (static_cast<size_t>(q0 + row / G) * a.Hq + kvh * G + row % G) * a.max_splits + sidx;
   if (fd == 0) {
     a.part_ml[base * 2] = M;
-    a.part_ml[base * 2 + 1] = L;
+    a.part_ml[base * 2 + 1] = __fadd_rn(L[0], L[1]);
   }
 #pragma unroll
   for (int i = 0; i < PER / 4; ++i)
     *reinterpret_cast<float4*>(a.part_o + base * HD + (i * TPR + fd) * 4) =
-        make_float4(O[4 * i], O[4 * i + 1], O[4 * i + 2], O[4 * i + 3]);
+        make_float4(__fadd_rn(O[4 * i], 0.f), __fadd_rn(O[4 * i + 1], 0.f), __fadd_rn(O[4 * i + 2], 0.f),
+                    __fadd_rn(O[4 * i + 3], 0.f));  // (no negative zeros, whichever kernel ran)
 }
 
 template <int HD, int FMT, bool LOWER8>

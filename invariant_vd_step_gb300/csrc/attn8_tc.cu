@@ -6,25 +6,26 @@
 // step over fp16 operands gives what an mma.sync m16n8k16 step gives, and both
 // kernels take the same steps (tests compare them).
 //
-// A CTA owns up to 256 rows of one (request, KV head), as two tiles of 128 (the
-// MMA's M), and a range of splits, whose chunks of 128 keys it takes one after
-// another.  Per chunk and tile: S = Q K^T (N = 128) into tensor memory; the
-// tile's 128 softmax threads, one row each, take the chunk's maximum, turn S into
-// fp16 weights in its place, and O = P V of the chunk goes to columns of its own,
-// which the same threads fold into the split's O in their registers.  While one
-// tile's softmax runs, the other tile's products do.  What it takes per chunk and
-// SM: the products 2048 cycles at the dense rate, 32768 exponentials and about
-// 1600 issue slots per scheduler in the softmax warps.
+// A CTA owns up to 128 rows (the MMA's M) of one (request, KV head) and a run of
+// splits, whose chunks of 128 keys it takes one after another.  Per chunk: S = Q
+// K^T (N = 128) into one of two score buffers of tensor memory; the softmax
+// threads, two per row with 64 keys each, take the row's maximum, turn S into
+// fp16 weights in its place, and O = P V of the chunk goes to one of two O
+// buffers, which the same threads (64 dims each) fold into the split's O in their
+// registers once the next chunk's weights are written.  The next chunk's scores
+// run beside the softmax.  What a chunk takes per SM: the products 1024 cycles at
+// the dense rate, 16384 exponentials (512 cycles), and about 1350 issue slots per
+// scheduler in the softmax and conversion warps.
 //
-// Four warps turn the codes into the operands: a lane's operand words (kv8.cuh)
-// are rows of 64 fp16 with the 128-byte swizzle after two 4-byte stores each, V
-// transposed ([dim][key]) so that both operands are K-major.  The pages that are
-// some row's own enter as a second K/V stage of their chunk, in bf16 scaled per
-// token to exact fp16, with scores of their own; a row takes 16 of their columns.
+// Eight warps turn the codes into the operands, a page each: a lane's operand
+// words (kv8.cuh) are rows of 64 fp16 with the 128-byte swizzle after two 4-byte
+// stores each, V transposed ([dim][key]) so that both operands are K-major.  The
+// pages that are some row's own enter as a second K/V stage of their chunk, in
+// bf16 scaled per token to exact fp16, with scores of their own (in the chunk's O
+// buffer); a row takes 16 of their columns.
 //
-// Roles (512 threads): warp 0 allocates tensor memory, its lane 0 issues the
-// MMAs; warps 4..7 convert; warps 8..11 and 12..15 are the tiles' softmax.  Every
-// wait is bounded.
+// Roles (640 threads): warp 0 allocates tensor memory, its lane 0 issues the MMAs;
+// warps 4..11 convert; warps 12..19 are the softmax.  Every wait is bounded.
 #include <math.h>
 
 #include "kv8.cuh"
@@ -38,14 +39,15 @@ constexpr int kSplit8 = 512, kChunk8 = 128, kChunkPages = 8;
 template <int HD>
 struct Tc8Cfg {
   static constexpr int ROWS = 128;
-  static constexpr int Q_BYTES = ROWS * HD * 2;     // one tile: [hd block][row][64]
+  static constexpr int Q_BYTES = ROWS * HD * 2;     // [hd block][row][64]
   static constexpr int K_BYTES = kChunk8 * HD * 2;  // [hd block][key][64]
   static constexpr int V_BYTES = kChunk8 * HD * 2;  // [key block][dim][64]
   static constexpr int STAGES = 2;
   static constexpr int SCALES = kChunk8 * 3 * 4;    // per stage: 8 pages or 128 tokens x (K scale, log2 of V's, 1 / V's)
   static constexpr int SC_RING = 4;
-  static constexpr int SMEM = 1024 + 2 * Q_BYTES + STAGES * (K_BYTES + V_BYTES) + SC_RING * SCALES + 256;
-  static constexpr int TMEM_COLS = 512;  // tile t: scores (then weights) from 128 t, O of a chunk from 256 + 128 t
+  static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + SC_RING * SCALES + 256;
+  static constexpr int TMEM_COLS = 512;  // chunk c: scores (then weights) from 128 (c % 2), O from 256 + 128 (c % 2)
+  static constexpr int THREADS = 640;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -53,35 +55,39 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {  // fp16 A and 
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// 32 columns of this thread's lane; the values may be used after wait_ld32.
-__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// Columns of this thread's lane; the values may be used after the wait_ld.
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
+      "%23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void wait_ld32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])::"memory");
-}
-__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {  // waits
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
+      : "r"(taddr));
+}
+__device__ __forceinline__ void wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+        "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+        "+r"(r[15])::"memory");
 }
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
@@ -101,30 +107,72 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Item: its request, rows [r0, r0 + n_rows) and splits [sp0, sp1).
+// Packed float32 pairs; each half rounded as the scalar operation rounds it.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ float f2_lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float f2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t f2_fma(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_sub(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+// Barrier of the softmax threads that also tells whether any of them has given up.
+__device__ __forceinline__ bool softmax_sync(bool ok) {
+  uint32_t bad;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(bad)
+      : "r"(ok ? 0u : 1u)
+      : "memory");
+  return bad == 0;
+}
+
+// Item: its request, rows [r0, r0 + 128) and splits [sp0, sp1).
 template <int HD, int FMT>
-__global__ void __launch_bounds__(512, 1) attn8_tc_kernel(Attn8Args a) {
+__global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8Args a) {
   using C = Tc8Cfg<HD>;
   constexpr int KK = HD / 16, UNITS = Kv8Cfg<HD>::UNITS, PART = Kv8Cfg<HD>::PART;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
-  uint8_t* sk = sq + 2 * C::Q_BYTES;               // K of stage s at sk + s * K_BYTES
+  uint8_t* sk = sq + C::Q_BYTES;                   // K of stage s at sk + (s % 2) * K_BYTES
   uint8_t* sv = sk + C::STAGES * C::K_BYTES;
   float* scales = reinterpret_cast<float*>(sv + C::STAGES * C::V_BYTES);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scales) + C::SC_RING * C::SCALES);
-  uint64_t* v_full = k_full + 2;
+  uint64_t* v_full = k_full + 2;     // [stage % 2] (and the two below)
   uint64_t* k_empty = v_full + 2;
   uint64_t* v_empty = k_empty + 2;
-  uint64_t* q_full = v_empty + 2;    // [tile] (and everything below)
-  uint64_t* s_full = q_full + 2;     // scores of a chunk, and O of the chunk before, are there
-  uint64_t* s16_full = s_full + 2;   // scores of the own pages
-  uint64_t* o_free = s16_full + 2;   // O of the chunk before has been folded (chunks with own pages)
-  uint64_t* p_full = o_free + 2;     // weights are there
-  uint64_t* o_full = p_full + 2;     // O of the last chunk
-  uint64_t* mma_done = o_full + 2;
+  uint64_t* s_full = v_empty + 2;    // [chunk % 2]: its scores are there, the own pages' too
+  uint64_t* p_full = s_full + 2;     // its weights are
+  uint64_t* o_full = p_full + 2;     // its O is
+  uint64_t* o_free = o_full + 2;     // its O has been folded
+  uint64_t* q_full = o_free + 2;
+  uint64_t* mma_done = q_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ float ex[2][2][128];  // [chunk % 2][half][row] largest scores
+  __shared__ float ex_l[2][128];   // l of the halves at a split's end
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ int skip;
@@ -132,8 +180,7 @@ __global__ void __launch_bounds__(512, 1) attn8_tc_kernel(Attn8Args a) {
   const int4 d0 = a.items[2 * (blockIdx.x / a.Hkv)], d1 = a.items[2 * (blockIdx.x / a.Hkv) + 1];
   const int b = d0.x, q0 = d0.y, qlen = d0.z, cached = d0.w, sp0 = d1.x, r0 = d1.y, sp1 = d1.z;
   const int G = a.Hq / a.Hkv, rows = qlen * G, kv_len = cached + qlen;
-  const int r_end = min(rows, r0 + 256);
-  const int ntile = r_end - r0 > 128 ? 2 : 1;
+  const int r_end = min(rows, r0 + C::ROWS);
   const int p_min = cached + r0 / G, p_max = cached + (r_end - 1) / G;
   const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
   const int own_lo = p_min >> 4, own_hi = p_max >> 4;
@@ -142,17 +189,16 @@ __global__ void __launch_bounds__(512, 1) attn8_tc_kernel(Attn8Args a) {
   if (threadIdx.x == 0) {
     skip = a.status ? *reinterpret_cast<volatile int*>(a.status) : 0;
     for (int k = 0; k < 2; ++k) {
-      mbar_init(&k_full[k], 128);
-      mbar_init(&v_full[k], 128);
+      mbar_init(&k_full[k], 256);
+      mbar_init(&v_full[k], 256);
       mbar_init(&k_empty[k], 1);
       mbar_init(&v_empty[k], 1);
-      mbar_init(&q_full[k], 128);
       mbar_init(&s_full[k], 1);
-      mbar_init(&s16_full[k], 1);
-      mbar_init(&o_free[k], 128);
-      mbar_init(&p_full[k], 128);
+      mbar_init(&p_full[k], 256);
       mbar_init(&o_full[k], 1);
+      mbar_init(&o_free[k], 256);
     }
+    mbar_init(q_full, 256);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -177,82 +223,81 @@ __global__ void __launch_bounds__(512, 1) attn8_tc_kernel(Attn8Args a) {
   auto hi16 = [&](int ch) { return min(kChunkPages, own_hi + 1 - ch * kChunkPages); };
 
   if (warp < 4) {
-    regs_dec<40>();
+    regs_dec<48>();
     if (warp == 0 && lane == 0) {
       const uint32_t id_s = idesc_f16(128, kChunk8), id_pv = idesc_f16(128, HD);
       const uint32_t q_lo = sw128_desc_lo(smem_u32(sq)), k_lo = sw128_desc_lo(smem_u32(sk)), v_lo = sw128_desc_lo(smem_u32(sv));
       auto wait = [&](uint64_t* f, int n) { return mbar_wait(f, n & 1, abort_flag, a.status); };
-      // scores of tile t against the K of stage st into columns `col`
-      auto scores = [&](int t, int st, uint32_t col) {
-        const uint32_t q = q_lo + t * (C::Q_BYTES >> 4), k = k_lo + (st & 1) * (C::K_BYTES >> 4);
+      // scores against the K of stage st into columns `col`
+      auto scores = [&](int st, uint32_t col) {
+        const uint32_t k = k_lo + (st & 1) * (C::K_BYTES >> 4);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
-          umma_bf16_lo(tmem + col, q + (kk >> 2) * (C::ROWS * 128 >> 4) + 2 * (kk & 3),
+          umma_bf16_lo(tmem + col, q_lo + (kk >> 2) * (C::ROWS * 128 >> 4) + 2 * (kk & 3),
                        k + (kk >> 2) * (kChunk8 * 128 >> 4) + 2 * (kk & 3), id_s, kk ? 1u : 0u);
       };
-      // O of tile t += weights of pages [x0, x1) in columns `p` times the V of stage st; first: from zero
-      auto pv = [&](int t, int st, uint32_t p, int x0, int x1, bool first) {
+      // O at columns `o` += weights of pages [x0, x1) in columns `p` times the V of stage st; first: from zero
+      auto pv = [&](int st, uint32_t o, uint32_t p, int x0, int x1, bool first) {
         const uint32_t v = v_lo + (st & 1) * (C::V_BYTES >> 4);
+#pragma unroll 1
         for (int x = x0; x < x1; ++x)
-          umma_bf16_ta(tmem + 256 + 128 * t, tmem + p + 8 * x, v + (x >> 2) * (HD * 128 >> 4) + 2 * (x & 3), id_pv,
+          umma_bf16_ta(tmem + o, tmem + p + 8 * x, v + (x >> 2) * (HD * 128 >> 4) + 2 * (x & 3), id_pv,
                        first && x == x0 ? 0u : 1u);
       };
-      int n16[2] = {0, 0};
-      bool ok = true;
-      for (int t = 0; t < ntile; ++t) ok = ok && wait(&q_full[t], 0);
-      // P V of chunk ch, whose stages are st (and st + 1), number it
-      auto chunk_pv = [&](int t, int ch, int st, int it) {
-        if (!wait(&p_full[t], it) || !wait(&v_full[st & 1], st >> 1)) return false;
-        const bool dg = diag(ch);
-        if (dg && !wait(&v_full[(st + 1) & 1], (st + 1) >> 1)) return false;
-        tc_fence_after();
-        pv(t, st, 128 * t, lo8(ch), hi8(ch), true);
-        if (dg) pv(t, st + 1, 128 * t + 64, lo16(ch), hi16(ch), lo8(ch) >= hi8(ch));
-        return true;
-      };
-      int st = 0, st_prev = 0;
-      for (int ch = ch0; ok && ch <= ch1; ++ch) {
+      // Stages are numbered along the chunks: one for a chunk's 8-bit pages, one
+      // more for its own pages.  Scores run up to two chunks ahead of P V; at
+      // chunks with own pages, whose two stages fill both slots, they wait for
+      // the P V of every chunk before.
+      int ns = ch0, st_s = 0, st_v = 0;  // next chunk to score and its stage; the stage of the chunk whose P V is next
+      bool ok = wait(q_full, 0);
+#pragma unroll 1
+      for (int ch = ch0 - 1; ok && ch <= ch1; ++ch) {  // (the first round only scores)
         const int it = ch - ch0;
-        ok = wait(&k_full[st & 1], st >> 1);
-        for (int t = 0; ok && t < ntile; ++t) {
-          if (it > 0) ok = chunk_pv(t, ch - 1, st_prev, it - 1);
+        if (ch >= ch0) {
+          const bool dg = diag(ch);
+          ok = wait(&p_full[it & 1], it >> 1) && wait(&v_full[st_v & 1], st_v >> 1) &&
+               (!dg || wait(&v_full[(st_v + 1) & 1], (st_v + 1) >> 1)) &&
+               (it < 2 || wait(&o_free[it & 1], (it >> 1) - 1));
           if (!ok) break;
           tc_fence_after();
-          scores(t, st, 128 * t);
-          umma_commit(&s_full[t]);
+          const uint32_t o = 256 + 128 * (it & 1), p = 128 * (it & 1);
+          pv(st_v, o, p, lo8(ch), hi8(ch), true);
+          if (dg) pv(st_v + 1, o, p + 64, lo16(ch), hi16(ch), lo8(ch) >= hi8(ch));
+          umma_commit(&o_full[it & 1]);
+          umma_commit(&v_empty[st_v & 1]);
+          if (dg) umma_commit(&v_empty[(st_v + 1) & 1]);
+          st_v += dg ? 2 : 1;
         }
-        if (!ok) break;
-        umma_commit(&k_empty[st & 1]);
-        if (it > 0) {
-          umma_commit(&v_empty[st_prev & 1]);
-          if (diag(ch - 1)) umma_commit(&v_empty[(st_prev + 1) & 1]);
-        }
-        st_prev = st++;
-        if (diag(ch)) {
-          ok = wait(&k_full[st & 1], st >> 1);
-          for (int t = 0; ok && t < ntile; ++t) {
-            ok = wait(&o_free[t], n16[t]++);
+#pragma unroll 1
+        while (ns <= ch1 && ns <= ch + 2) {
+          const bool dg = diag(ns);
+          if (ns > ch + 1 && (dg || (ns > ch0 && diag(ns - 1)))) break;
+          const int n = ns - ch0;
+          ok = wait(&k_full[st_s & 1], st_s >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          scores(st_s, 128 * (n & 1));
+          umma_commit(&k_empty[st_s & 1]);
+          ++st_s;
+          if (dg) {  // own pages, into the columns that the chunk's O takes later
+            ok = wait(&k_full[st_s & 1], st_s >> 1) && (n < 2 || wait(&o_free[n & 1], (n >> 1) - 1));
             if (!ok) break;
             tc_fence_after();
-            scores(t, st, 256 + 128 * t);
-            umma_commit(&s16_full[t]);
+            scores(st_s, 256 + 128 * (n & 1));
+            umma_commit(&k_empty[st_s & 1]);
+            ++st_s;
           }
-          if (!ok) break;
-          umma_commit(&k_empty[st & 1]);
-          ++st;
+          umma_commit(&s_full[n & 1]);
+          ++ns;
         }
-      }
-      for (int t = 0; ok && t < ntile; ++t) {
-        ok = chunk_pv(t, ch1, st_prev, ch1 - ch0);
-        if (ok) umma_commit(&o_full[t]);
       }
       umma_commit(mma_done);
     }
-  } else if (warp < 8) {
-    // ---- operands.  Each warp takes two pages of a stage's K, then of its V.
-    regs_dec<88>();
-    const int cw = warp - 4, g = lane >> 2, t4 = lane & 3;
-    uint4 w[2][UNITS];
+  } else if (warp < 12) {
+    // ---- operands: this warp's page of each chunk, K, then V
+    regs_dec<56>();
+    const int pg = warp - 4, g = lane >> 2, t4 = lane & 3;
+    uint4 w[UNITS];
     const int* pt = a.page_table + static_cast<size_t>(b) * a.pt_stride;
     int st = 0;
     bool ok = true;
@@ -260,343 +305,316 @@ __global__ void __launch_bounds__(512, 1) attn8_tc_kernel(Attn8Args a) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(f, n & 1, abort_flag, a.status));
       return ok;
     };
-    auto load = [&](int ch, bool v, const int (&pid)[2]) {
+    auto here = [&](int ch) { return pg >= lo8(ch) && pg < hi8(ch); };
+    auto load = [&](int ch, bool v, int pid) {
+      const uint4* src =
+          reinterpret_cast<const uint4*>(a.codes + (static_cast<size_t>(pid) * a.Hkv + kvh) * (2 * PART) + (v ? PART : 0)) + lane;
+      const bool in = here(ch);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.codes + (static_cast<size_t>(pid[x]) * a.Hkv + kvh) * (2 * PART) + (v ? PART : 0));
-        const bool in = 2 * cw + x >= lo8(ch) && 2 * cw + x < hi8(ch);
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) w[x][u] = in ? __ldcg(src + u * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
-      }
+      for (int u = 0; u < UNITS; ++u) w[u] = in ? __ldcg(src + u * 32) : make_uint4(0u, 0u, 0u, 0u);
     };
-    auto ids = [&](int ch, int (&pid)[2]) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int pg = 2 * cw + x;
-        pid[x] = ch <= ch1 && pg >= lo8(ch) && pg < hi8(ch) ? pt[ch * kChunkPages + pg] : 0;
-      }
-    };
-    // One operand word: two fp16 pairs of row `row` (row % 8 = g), at 16-byte columns c and c + 1.
-    auto put = [&](uint32_t base, int row, int c, uint32_t word) {
+    auto id_of = [&](int ch) { return ch <= ch1 && here(ch) ? pt[ch * kChunkPages + pg] : 0; };
+    // The two fp16 pairs of an operand word go to 16-byte columns c and c + 1 of
+    // row g of an 8-row group; `col`: offset of this lane's pair in column c, swizzled.
+    auto col = [&](int c) { return static_cast<uint32_t>(g * 128 + ((c ^ g) << 4) + t4 * 4); };
+    auto put = [&](uint32_t at0, uint32_t at1, uint32_t word) {
       uint32_t lo, hi;
       kv8_expand<FMT>(word, lo, hi);
-      const uint32_t at = base + row * 128 + t4 * 4;
-      sts32(at + ((c ^ g) << 4), lo);
-      sts32(at + (((c + 1) ^ g) << 4), hi);
+      sts32(at0, lo);
+      sts32(at1, hi);
     };
-    int pid[2], pid_next[2];
-    ids(ch0, pid);
+    int pid = id_of(ch0);
     load(ch0, false, pid);
+#pragma unroll 1
     for (int ch = ch0; ok && ch <= ch1; ++ch) {
-      ids(ch + 1, pid_next);
+      const int pid_next = id_of(ch + 1);
       if (st >= 2 && !warp_wait(&k_empty[st & 1], (st >> 1) - 1)) break;
-      float* sc = scales + (st & 3) * (C::SCALES / 4);
-      if (lane < 2) {
-        const int x = 2 * cw + lane;
+      if (lane == 0) {
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x >= lo8(ch) && x < hi8(ch)) f = __ldcg(a.scales + static_cast<size_t>(lane ? pid[1] : pid[0]) * a.Hkv + kvh);
-        sc[x * 4] = f.x;
-        sc[x * 4 + 1] = f.z;
-        sc[x * 4 + 2] = f.y;
+        if (here(ch)) f = __ldcg(a.scales + static_cast<size_t>(pid) * a.Hkv + kvh);
+        *reinterpret_cast<float4*>(scales + (st & 3) * (C::SCALES / 4) + pg * 4) = make_float4(f.x, f.z, f.y, 0.f);
       }
-      {
-        const uint32_t base = smem_u32(sk + (st & 1) * C::K_BYTES);
+      {  // unit u: k-steps 2 u and 2 u + 1 of key blocks 0 and 1
+        const uint32_t base = smem_u32(sk + (st & 1) * C::K_BYTES) + pg * (16 * 128);
+        uint32_t c[8];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int row = (2 * cw + x) * 16 + g;
+        for (int k = 0; k < 8; ++k) c[k] = base + col(k);
 #pragma unroll
-          for (int u = 0; u < UNITS; ++u) {  // k-steps 2 u and 2 u + 1; key blocks 0 and 1
-            const uint32_t blk = base + (u >> 1) * (kChunk8 * 128);
-            const int c = (u & 1) * 4;
-            put(blk, row, c, w[x][u].x);
-            put(blk, row + 8, c, w[x][u].y);
-            put(blk, row, c + 2, w[x][u].z);
-            put(blk, row + 8, c + 2, w[x][u].w);
-          }
+        for (int u = 0; u < UNITS; ++u) {
+          const int k = (u & 1) * 4, at = (u >> 1) * (kChunk8 * 128);
+          put(c[k] + at, c[k + 1] + at, w[u].x);
+          put(c[k] + at + 8 * 128, c[k + 1] + at + 8 * 128, w[u].y);
+          put(c[k + 2] + at, c[k + 3] + at, w[u].z);
+          put(c[k + 2] + at + 8 * 128, c[k + 3] + at + 8 * 128, w[u].w);
         }
       }
       load(ch, true, pid);
       fence_proxy_async_smem();
       mbar_arrive(&k_full[st & 1]);
       if (st >= 2 && !warp_wait(&v_empty[st & 1], (st >> 1) - 1)) break;
-      {
-        const uint32_t base = smem_u32(sv + (st & 1) * C::V_BYTES);
+      {  // unit u: dims 32 u .. + 31; this page's 16 keys are columns 2 (page % 4) and + 1 of its key block
+        const uint32_t base = smem_u32(sv + (st & 1) * C::V_BYTES) + (pg >> 2) * (HD * 128);
+        const uint32_t c0 = base + col((pg & 3) * 2), c1 = base + col((pg & 3) * 2 + 1);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int page = 2 * cw + x;
-          const uint32_t blk = base + (page >> 2) * (HD * 128);
-          const int c = (page & 3) * 2;
-#pragma unroll
-          for (int u = 0; u < UNITS; ++u) {
-            put(blk, 32 * u + g, c, w[x][u].x);
-            put(blk, 32 * u + 8 + g, c, w[x][u].y);
-            put(blk, 32 * u + 16 + g, c, w[x][u].z);
-            put(blk, 32 * u + 24 + g, c, w[x][u].w);
-          }
+        for (int u = 0; u < UNITS; ++u) {
+          const int at = 32 * u * 128;
+          put(c0 + at, c1 + at, w[u].x);
+          put(c0 + at + 8 * 128, c1 + at + 8 * 128, w[u].y);
+          put(c0 + at + 16 * 128, c1 + at + 16 * 128, w[u].z);
+          put(c0 + at + 24 * 128, c1 + at + 24 * 128, w[u].w);
         }
       }
-      pid[0] = pid_next[0];
-      pid[1] = pid_next[1];
+      pid = pid_next;
       if (ch < ch1) load(ch + 1, false, pid);
       fence_proxy_async_smem();
       mbar_arrive(&v_full[st & 1]);
       ++st;
-      if (diag(ch)) {
-        // the own pages in bf16: lane (token, half of the head dimension); the scales of a token that is not finite
-        // are NaN, and its V counts as 0 (its weight is NaN, or 0 where it is not seen)
-        if (st >= 2 && !(warp_wait(&k_empty[st & 1], (st >> 1) - 1) && warp_wait(&v_empty[st & 1], (st >> 1) - 1))) break;
-        float* so = scales + (st & 3) * (C::SCALES / 4);
-        const int token = lane >> 1, half = lane & 1;
-        for (int x = 0; x < 2; ++x) {
-          const int pg = 2 * cw + x, page = ch * kChunkPages + pg;
-          if (pg < lo16(ch) || pg >= hi16(ch)) continue;
-          const int phys = a.open_table[static_cast<size_t>(b) * a.open_stride + page - (cached >> 4)];
-          const bool have = page * 16 + token < kv_len;
-          const int key = pg * 16 + token;
-          for (int v = 0; v < 2; ++v) {
-            const uint4* src = reinterpret_cast<const uint4*>(a.open + ((static_cast<size_t>(phys) * 2 + v) * a.Hkv + kvh) * PART +
-                                                              token * HD + half * (HD / 2));
-            uint32_t mx = 0u;
-#pragma unroll
-            for (int i = 0; i < HD / 16; ++i) {
-              const uint4 y = have ? __ldcg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-              mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
-                                         __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
+      if (!diag(ch)) continue;
+      // The own pages in bf16: lane (token, half of the head dimension).  The scales
+      // of a token that is not finite are NaN, and its V counts as 0 (its weight is
+      // NaN, or 0 where it is not seen).
+      const int token = lane >> 1, half = lane & 1, page = ch * kChunkPages + pg, key = pg * 16 + token;
+      const bool in = pg >= lo16(ch) && pg < hi16(ch), have = in && page * 16 + token < kv_len;
+      const int phys = in ? a.open_table[static_cast<size_t>(b) * a.open_stride + page - (cached >> 4)] : 0;
+      float* so = scales + (st & 3) * (C::SCALES / 4);
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        if (st >= 2 && !warp_wait(v ? &v_empty[st & 1] : &k_empty[st & 1], (st >> 1) - 1)) break;
+        const uint4* src = reinterpret_cast<const uint4*>(a.open + ((static_cast<size_t>(phys) * 2 + v) * a.Hkv + kvh) * PART +
+                                                          token * HD + half * (HD / 2));
+        if (in) {
+          uint32_t mx = 0u;
+#pragma unroll 4
+          for (int i = 0; i < HD / 16; ++i) {
+            const uint4 y = have ? __ldcg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
+                                       __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
+          }
+          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          const int e = kv8_exp(kv8_max_halves(mx));
+          const float up = kv8_up(e);
+          if (half == 0) {
+            if (v == 0) {
+              so[key] = e == 255 ? kv8_nan() : kv8_down(e);
+            } else {
+              so[kChunk8 + key] = e == 255 ? kv8_nan() : kv8_log2_down(e);
+              so[2 * kChunk8 + key] = up;
             }
-            mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            const int e = kv8_exp(kv8_max_halves(mx));
-            const float up = kv8_up(e);
-            if (half == 0) {
-              if (v == 0) {
-                so[key] = e == 255 ? kv8_nan() : kv8_down(e);
-              } else {
-                so[kChunk8 + key] = e == 255 ? kv8_nan() : kv8_log2_down(e);
-                so[2 * kChunk8 + key] = up;
-              }
-            }
+          }
 #pragma unroll 2
-            for (int i = 0; i < HD / 16; ++i) {
-              uint4 y = have ? __ldcg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-              y = make_uint4(kv8_to_f16(y.x, up), kv8_to_f16(y.y, up), kv8_to_f16(y.z, up), kv8_to_f16(y.w, up));
-              const int d = half * (HD / 2) + i * 8;  // dims d .. d + 7
-              if (v == 0) {
-                *reinterpret_cast<uint4*>(sk + (st & 1) * C::K_BYTES + (d >> 6) * (kChunk8 * 128) + key * 128 +
-                                          ((((d >> 3) & 7) ^ (key & 7)) << 4)) = y;
-              } else {
-                if (e == 255) y = make_uint4(0u, 0u, 0u, 0u);
-                uint8_t* to = sv + (st & 1) * C::V_BYTES + (key >> 6) * (HD * 128) + (key & 7) * 2;
-                const uint32_t h[4] = {y.x, y.y, y.z, y.w};
+          for (int i = 0; i < HD / 16; ++i) {
+            uint4 y = have ? __ldcg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+            y = make_uint4(kv8_to_f16(y.x, up), kv8_to_f16(y.y, up), kv8_to_f16(y.z, up), kv8_to_f16(y.w, up));
+            const int d = half * (HD / 2) + i * 8;  // dims d .. d + 7
+            if (v == 0) {
+              *reinterpret_cast<uint4*>(sk + (st & 1) * C::K_BYTES + (d >> 6) * (kChunk8 * 128) + key * 128 +
+                                        ((((d >> 3) & 7) ^ (key & 7)) << 4)) = y;
+            } else {
+              if (e == 255) y = make_uint4(0u, 0u, 0u, 0u);
+              uint8_t* to = sv + (st & 1) * C::V_BYTES + (key >> 6) * (HD * 128) + (key & 7) * 2;
+              const uint32_t h[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  *reinterpret_cast<uint16_t*>(to + (d + k) * 128 + ((((key >> 3) & 7) ^ ((d + k) & 7)) << 4)) =
-                      static_cast<uint16_t>(h[k >> 1] >> (16 * (k & 1)));
-              }
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint16_t*>(to + (d + k) * 128 + ((((key >> 3) & 7) ^ ((d + k) & 7)) << 4)) =
+                    static_cast<uint16_t>(h[k >> 1] >> (16 * (k & 1)));
             }
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&k_full[st & 1]);
-        mbar_arrive(&v_full[st & 1]);
-        ++st;
+        mbar_arrive(v ? &v_full[st & 1] : &k_full[st & 1]);
       }
+      ++st;
     }
   } else {
-    // ---- softmax: one row per thread
-    regs_inc<192>();
-    const int t = (warp - 8) >> 2, lr = (warp & 3) * 32 + lane, row = r0 + t * 128 + lr;
+    // ---- softmax: two threads per row, of which thread h takes pages 4 h .. + 3 of a chunk and dims HD / 2 h .. of O
+    regs_inc<160>();
+    constexpr int HP = kChunkPages / 2, OD = HD / 2;
+    const int h = (warp - 12) >> 2, lr = (warp & 3) * 32 + lane, row = r0 + lr;
     const bool valid = row < r_end;
     const int tok = valid ? row / G : 0, hq = kvh * G + (valid ? row % G : 0);
     const int pos = valid ? cached + tok : -1, own = pos >> 4;
     const int lo = valid ? (a.window > 0 ? max(0, pos - a.window + 1) : 0) : 1;
-    if (t < ntile) {
-      float rowfac;
-      {  // the row's query -> [hd block][row][64] fp16, 128-byte swizzle
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD);
-        uint4 x[HD / 8];
-        uint32_t mx = 0u;
+    float rowfac;
+    {  // the row's query -> [hd block][row][64] fp16, 128-byte swizzle; each thread half of it
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD);
+      uint32_t mx = 0u;
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) x[i] = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i)
-          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-        const int e = kv8_exp(kv8_max_halves(mx));
-        const float up = kv8_up(e);
-        rowfac = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i)
-          *reinterpret_cast<uint4*>(sq + t * C::Q_BYTES + (i >> 3) * (C::ROWS * 128) + lr * 128 + (((i & 7) ^ (lr & 7)) << 4)) =
-              make_uint4(kv8_to_f16(x[i].x, up), kv8_to_f16(x[i].y, up), kv8_to_f16(x[i].z, up), kv8_to_f16(x[i].w, up));
-        fence_proxy_async_smem();
-        mbar_arrive(&q_full[t]);
+      for (int i = 0; i < HD / 8; ++i) {
+        const uint4 x = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
       }
-      const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const uint32_t s_at = lanes + 128 * t, o_at = lanes + 256 + 128 * t;
-      bool ok = true;
-      auto warp_wait = [&](uint64_t* f, int n) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(f, n & 1, abort_flag, a.status));
-        return ok;
-      };
-      float M = 0.f, L = 0.f, O[HD];
-      bool any = false;          // O holds chunks of the split in hand
-      float mc = 0.f, lc = 0.f;  // of the chunk whose O is still in tensor memory
-      // Folds that chunk (number ch) into the split's state, and stores the split's if it was its last
-      auto fold = [&](int ch) {
-        const bool sees = valid && max(lo, ch * kChunk8) <= min(pos, ch * kChunk8 + kChunk8 - 1);
-        const float mn = any ? fmaxf(M, mc) : mc;
-        const float ca = ex2(__fsub_rn(M, mn)), cb = ex2(__fsub_rn(mc, mn));
+      const int e = kv8_exp(kv8_max_halves(mx));
+      const float up = kv8_up(e);
+      rowfac = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
 #pragma unroll
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t x[32];
-          ld32(o_at + 32 * c, x);
-          wait_ld32(x);
-          if (sees) {
-            if (any) {
+      for (int k = 0; k < HD / 16; ++k) {
+        const int i = h * (HD / 16) + k;
+        const uint4 x = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(sq + (i >> 3) * (C::ROWS * 128) + lr * 128 + (((i & 7) ^ (lr & 7)) << 4)) =
+            make_uint4(kv8_to_f16(x.x, up), kv8_to_f16(x.y, up), kv8_to_f16(x.z, up), kv8_to_f16(x.w, up));
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+    }
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    bool ok = true;
+    auto warp_wait = [&](uint64_t* f, int n) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(f, n & 1, abort_flag, a.status));
+      return ok;
+    };
+    // The split in hand: running maximum M, this thread's l and O (pairs of dims).
+    // `alpha`, `l_ch`: of the chunk whose O is not folded yet, the factor for what
+    // is before it (0 at a split's first, as what O and L hold is then of another
+    // split, and finite or NaN for good) and its l.
+    float M = -INFINITY, M_old = 0.f, L = 0.f, alpha = 0.f, l_ch = 0.f;
+    uint64_t O[OD / 2];
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                O[32 * c + i] = __fadd_rn(__fmul_rn(O[32 * c + i], ca), __fmul_rn(__uint_as_float(x[i]), cb));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) O[32 * c + i] = __uint_as_float(x[i]);
-            }
-          }
-        }
-        if (sees) {
-          L = any ? __fadd_rn(__fmul_rn(L, ca), __fmul_rn(lc, cb)) : lc;
-          M = mn;
-          any = true;
-        }
-        if ((ch & 3) == 3 || ch == ch1) {
-          if (any) {
-            const size_t base = (static_cast<size_t>(q0 + tok) * a.Hq + hq) * a.max_splits + (ch >> 2);
-            a.part_ml[base * 2] = M;
-            a.part_ml[base * 2 + 1] = L;
-            float4* po = reinterpret_cast<float4*>(a.part_o + base * HD);
-#pragma unroll
-            for (int i = 0; i < HD / 4; ++i) po[i] = make_float4(O[4 * i], O[4 * i + 1], O[4 * i + 2], O[4 * i + 3]);
-          }
-          any = false;
-        }
-      };
-      int st = 0, n16 = 0;
-      for (int ch = ch0; ch <= ch1; ++ch) {
-        const int it = ch - ch0, pg0 = ch * kChunkPages;
-        if (!warp_wait(&s_full[t], it)) break;
+    for (int i = 0; i < OD / 2; ++i) O[i] = 0ull;
+    int st = 0;
+#pragma unroll 1
+    for (int ch = ch0; ch <= ch1 + 1; ++ch) {
+      const int it = ch - ch0, pg0 = ch * kChunkPages;
+      const float alpha_old = alpha, l_old = l_ch;
+      const bool first = (ch & 3) == 0 || it == 0;
+      if (ch <= ch1) {
+        warp_wait(&s_full[it & 1], it >> 1);
         tc_fence_after();
-        if (it > 0) fold(ch - 1);
-        const float* sc = scales + (st & 3) * (C::SCALES / 4);
-        const bool dg = diag(ch);
+        const uint32_t s_at = lanes + 128 * (it & 1);
+        const float4* sc = reinterpret_cast<const float4*>(scales + (st & 3) * (C::SCALES / 4)) + h * HP;
         const float* so = scales + ((st + 1) & 3) * (C::SCALES / 4);
-        if (dg) {
-          tc_fence_before();
-          mbar_arrive(&o_free[t]);
-          if (!warp_wait(&s16_full[t], n16++)) break;
-          tc_fence_after();
-        }
+        const bool dg = diag(ch);
+        if (dg) warp_wait(&v_full[(st + 1) & 1], (st + 1) >> 1);  // the V scales of the own pages' tokens
         st += dg ? 2 : 1;
-        // every row of the warp sees the whole chunk in 8 bits (rows that are none aside)
-        const bool full = __all_sync(0xffffffffu, !valid || (lo <= ch * kChunk8 && own >= pg0 + kChunkPages));
-        float mx = -INFINITY;
+        // every row of the warp sees this half chunk in 8 bits (rows that are none aside)
+        const bool full = __all_sync(0xffffffffu, !valid || (lo <= (pg0 + h * HP) * 16 && own >= pg0 + h * HP + HP));
+        uint64_t t[HP * 8];  // scores, as pairs of keys
+        uint32_t x[2][16];
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        ld16(s_at + 64 * h, x[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[32];
-          ld32(s_at + 32 * c, x);
-          wait_ld32(x);
+        for (int pg = 0; pg < HP; ++pg) {
+          const float4 f = sc[pg];
+          const float ks = __fmul_rn(f.x, rowfac);
+          const uint64_t k2 = f2(ks, ks), lv2 = f2(f.y, f.y);
+          wait_ld16(x[pg & 1]);
+          if (pg + 1 < HP) ld16(s_at + 64 * h + 16 * (pg + 1), x[(pg + 1) & 1]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int pg = 2 * c + h;
-            const float ks = __fmul_rn(sc[pg * 4], rowfac), lv = sc[pg * 4 + 1];
-            if (full) {
+          for (int i = 0; i < 8; ++i) t[pg * 8 + i] = f2_fma(f2(x[pg & 1][2 * i], x[pg & 1][2 * i + 1]), k2, lv2);
+          if (!full) {
+            const int page = pg0 + h * HP + pg;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) mx = fmaxf(mx, __fmaf_rn(__uint_as_float(x[16 * h + i]), ks, lv));
-            } else if (pg0 + pg < own) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if ((pg0 + pg) * 16 + i >= lo) mx = fmaxf(mx, __fmaf_rn(__uint_as_float(x[16 * h + i]), ks, lv));
+            for (int i = 0; i < 8; ++i) {
+              const int key = page * 16 + 2 * i;
+              t[pg * 8 + i] = f2(page < own && key >= lo ? f2_lo(t[pg * 8 + i]) : -INFINITY,
+                                 page < own && key + 1 >= lo ? f2_hi(t[pg * 8 + i]) : -INFINITY);
             }
-          }
-        }
-        const int x0 = lo16(ch), x1 = hi16(ch);
-        if (dg) {
-          for (int pg = x0; pg < x1; ++pg) {
-            if (!__any_sync(0xffffffffu, own == pg0 + pg)) continue;
-            uint32_t x[16];
-            ld16(o_at + 16 * pg, x);
-            if (own == pg0 + pg) {
+            if (dg && ok && page >= own_lo && page <= own_hi) {  // the rows whose own page it is
+              uint32_t y[16];
+              ld16(lanes + 256 + 128 * (it & 1) + 16 * (h * HP + pg), y);
+              wait_ld16(y);
+              if (page == own) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int key = (pg0 + pg) * 16 + i;
-                const float v = __fmaf_rn(__uint_as_float(x[i]), __fmul_rn(so[pg * 16 + i], rowfac), so[kChunk8 + pg * 16 + i]);
-                if (key >= lo && key <= pos) mx = fmaxf(mx, v);
+                for (int i = 0; i < 16; ++i) {
+                  const int n = (h * HP + pg) * 16 + i, key = page * 16 + i;
+                  const float v = __fmaf_rn(__uint_as_float(y[i]), __fmul_rn(so[n], rowfac), so[kChunk8 + n]);
+                  const float w = key >= lo && key <= pos ? v : -INFINITY;
+                  uint64_t& z = t[pg * 8 + (i >> 1)];
+                  z = (i & 1) ? f2(f2_lo(z), w) : f2(w, f2_hi(z));
+                }
               }
             }
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(f2_lo(t[pg * 8 + i]), f2_hi(t[pg * 8 + i])));
         }
-        mc = mx;
-        float l[4] = {0.f, 0.f, 0.f, 0.f};
+        ex[it & 1][h][lr] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        ok = softmax_sync(ok);  // also: every score has been read
+        if (!ok) break;
+        if (first) {
+          M_old = M;
+          M = -INFINITY;
+        }
+        kv8_running_max(M, fmaxf(ex[it & 1][0][lr], ex[it & 1][1][lr]), alpha);
+        if (first) alpha = 0.f;
+        const float u = M == -INFINITY ? 0.f : M;  // no key seen so far: every score is -inf, every weight 0
+        const uint64_t u2 = f2(u, u);
+        uint64_t l[4] = {0ull, 0ull, 0ull, 0ull};  // pair t: the partial sums (t, 0) and (t, 1)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[32];
-          ld32(s_at + 32 * c, x);
-          wait_ld32(x);
+        for (int pg = 0; pg < HP; ++pg) {
+          const float iv = sc[pg].z;
+          const uint64_t iv2 = f2(iv, iv);
+          const int page = pg0 + h * HP + pg;
+          uint32_t pk[8];
+          if (full) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int pg = 2 * c + h;
-            const float ks = __fmul_rn(sc[pg * 4], rowfac), lv = sc[pg * 4 + 1], iv = sc[pg * 4 + 2];
-            const bool mine = full || pg0 + pg < own;
-            float p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float v = __fmaf_rn(__uint_as_float(x[16 * h + i]), ks, lv);
-              if (!full && !(mine && (pg0 + pg) * 16 + i >= lo)) v = -INFINITY;
-              p[i] = ex2(__fsub_rn(v, mx));
+            for (int i = 0; i < 8; ++i) {
+              const uint64_t s2 = f2_sub(t[pg * 8 + i], u2);
+              const float p0 = ex2(f2_lo(s2)), p1 = ex2(f2_hi(s2));
+              l[i & 3] = f2_fma(f2(p0, p1), iv2, l[i & 3]);
+              pk[i] = pack_f16x2(p0, p1);
             }
-            if (full || (mine && (pg0 + pg) * 16 + 15 >= lo)) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                l[k] = __fmaf_rn(__fadd_rn(__fadd_rn(p[2 * k], p[2 * k + 1]), __fadd_rn(p[2 * k + 8], p[2 * k + 9])), iv, l[k]);
+            st8(s_at + 8 * (h * HP + pg), pk);
+            if (dg && page >= own_lo && page <= own_hi) {  // another row's own page
+              const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+              st8(s_at + 64 + 8 * (h * HP + pg), zero);
             }
-            uint32_t pk[8];
+          } else {
+            const bool mine = page == own, sees = (page < own || mine) && page * 16 + 15 >= lo;
+            const float* up = so + 2 * kChunk8 + (h * HP + pg) * 16;
+            uint32_t p8[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(p[2 * i], p[2 * i + 1]);
-            st8(s_at + 8 * pg, pk);
+            for (int i = 0; i < 8; ++i) {
+              const uint64_t s2 = f2_sub(t[pg * 8 + i], u2);
+              const float p0 = ex2(f2_lo(s2)), p1 = ex2(f2_hi(s2));
+              // (a page that the row does not see stays out, whatever its scale)
+              if (sees) l[i & 3] = f2_fma(f2(p0, p1), mine ? f2(up[2 * i], up[2 * i + 1]) : iv2, l[i & 3]);
+              pk[i] = pack_f16x2(p0, p1);
+              p8[i] = mine ? 0u : pk[i];
+              pk[i] = mine ? pk[i] : 0u;
+            }
+            st8(s_at + 8 * (h * HP + pg), p8);
+            if (dg && page >= own_lo && page <= own_hi) st8(s_at + 64 + 8 * (h * HP + pg), pk);
           }
         }
-        if (dg) {
-          for (int pg = x0; pg < x1; ++pg) {
-            uint32_t x[16], pk[8];
-            ld16(o_at + 16 * pg, x);
-            const bool mine = own == pg0 + pg;
-            float p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int key = (pg0 + pg) * 16 + i;
-              const float v = __fmaf_rn(__uint_as_float(x[i]), __fmul_rn(so[pg * 16 + i], rowfac), so[kChunk8 + pg * 16 + i]);
-              p[i] = mine && key >= lo && key <= pos ? ex2(__fsub_rn(v, mx)) : 0.f;
-            }
-            if (mine) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float* up = so + 2 * kChunk8 + pg * 16 + 2 * k;
-                l[k] = __fmaf_rn(p[2 * k], up[0], l[k]);
-                l[k] = __fmaf_rn(p[2 * k + 1], up[1], l[k]);
-                l[k] = __fmaf_rn(p[2 * k + 8], up[8], l[k]);
-                l[k] = __fmaf_rn(p[2 * k + 9], up[9], l[k]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(p[2 * i], p[2 * i + 1]);
-            st8(s_at + 64 + 8 * pg, pk);
-          }
-        }
-        lc = __fadd_rn(__fadd_rn(l[0], l[1]), __fadd_rn(l[2], l[3]));
+        l_ch = __fadd_rn(__fadd_rn(__fadd_rn(f2_lo(l[0]), f2_hi(l[0])), __fadd_rn(f2_lo(l[1]), f2_hi(l[1]))),
+                         __fadd_rn(__fadd_rn(f2_lo(l[2]), f2_hi(l[2])), __fadd_rn(f2_lo(l[3]), f2_hi(l[3]))));
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[t]);
+        mbar_arrive(&p_full[it & 1]);
       }
-      if (ok && warp_wait(&o_full[t], 0)) {
+      if (it == 0) continue;
+      // ---- O of the chunk before, and its split's partial if it was the last of it
+      const int pc = ch - 1, pit = it - 1;
+      if (warp_wait(&o_full[pit & 1], pit >> 1)) {
         tc_fence_after();
-        fold(ch1);
+        uint32_t y[OD];
+        const uint32_t o_at = lanes + 256 + 128 * (pit & 1) + OD * h;
+#pragma unroll
+        for (int c = 0; c < OD / 32; ++c) ld32(o_at + 32 * c, y + 32 * c);
+#pragma unroll
+        for (int c = 0; c < OD / 32; ++c) wait_ld32(y + 32 * c);
+        tc_fence_before();
+        mbar_arrive(&o_free[pit & 1]);
+        const uint64_t al = f2(alpha_old, alpha_old);
+#pragma unroll
+        for (int i = 0; i < OD / 2; ++i) O[i] = f2_fma(O[i], al, f2(y[2 * i], y[2 * i + 1]));
+        L = __fmaf_rn(L, alpha_old, l_old);
+      }
+      if ((pc & 3) == 3 || pc == ch1) {
+        const int sp = pc >> 2;
+        ex_l[h][lr] = L;
+        ok = softmax_sync(ok);
+        if (!ok) break;
+        if (valid && max(lo, sp * kSplit8) <= min(pos, sp * kSplit8 + kSplit8 - 1)) {
+          const size_t base = (static_cast<size_t>(q0 + tok) * a.Hq + hq) * a.max_splits + sp;
+          if (h == 0) {
+            a.part_ml[base * 2] = pc == ch1 ? M : M_old;
+            a.part_ml[base * 2 + 1] = __fadd_rn(ex_l[0][lr], ex_l[1][lr]);
+          }
+          ulonglong2* po = reinterpret_cast<ulonglong2*>(a.part_o + base * HD + OD * h);
+#pragma unroll
+          for (int i = 0; i < OD / 4; ++i) po[i] = make_ulonglong2(f2_add(O[2 * i], 0ull), f2_add(O[2 * i + 1], 0ull));
+        }
       }
     }
   }
@@ -614,7 +632,7 @@ template <int HD, int FMT>
 int launch_attn8_tc_t(const Attn8Args& a, int n_blocks, cudaStream_t s) {
   using C = Tc8Cfg<HD>;
   VD_CUDA_TRY(cudaFuncSetAttribute(attn8_tc_kernel<HD, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-  VD_CUDA_TRY(launch_k(attn8_tc_kernel<HD, FMT>, dim3(static_cast<unsigned>(n_blocks) * a.Hkv), dim3(512), C::SMEM, s, a));
+  VD_CUDA_TRY(launch_k(attn8_tc_kernel<HD, FMT>, dim3(static_cast<unsigned>(n_blocks) * a.Hkv), dim3(C::THREADS), C::SMEM, s, a));
   return VD_OK;
 }
 

@@ -61,6 +61,14 @@ __device__ __forceinline__ uint32_t kv8_to_f16(uint32_t v, float f) {
 }
 __device__ __forceinline__ uint32_t kv8_max_halves(uint32_t v) { return max(v & 0xffffu, v >> 16); }
 
+// The running maximum m of a row after a chunk whose largest score is mx, and the
+// factor for the sums before it (1 where it stays, -inf included).
+__device__ __forceinline__ void kv8_running_max(float& m, float mx, float& alpha) {
+  const float mn = fmaxf(m, mx);
+  alpha = mn == m ? 1.0f : ex2(__fsub_rn(m, mn));
+  m = mn;
+}
+
 __device__ __forceinline__ void mma_f16_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "

@@ -256,7 +256,7 @@ struct Attn8Args {
 // lower8: every block of the launch has at most 8 rows.
 int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int format, bool lower8, int n_blocks,
                       cudaStream_t s);
-// The same rows in blocks of 256 on tcgen05, head dimensions 64 and 128.
+// The same rows in blocks of 128 on tcgen05, head dimensions 64 and 128.
 int launch_attention8_tc(const Attn8Args& a, int hd, int format, int n_blocks, cudaStream_t s);
 // Sealing and its reverse, page copies (kv8.cu).  Pairs of page ids: `dev` on the
 // device (a plan's), or else in the launch's own arguments.
