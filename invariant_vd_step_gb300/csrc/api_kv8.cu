@@ -41,6 +41,8 @@ struct vd_kv8_plan {
   size_t dev_cap = 0;  // ints
   float* part = nullptr;
   size_t part_cap = 0;  // floats
+  float* tot = nullptr;
+  size_t tot_cap = 0;   // floats
   int* host[2] = {nullptr, nullptr};  // pinned staging
   size_t host_cap[2] = {0, 0};
   cudaEvent_t uploaded[2] = {nullptr, nullptr};
@@ -50,7 +52,9 @@ struct vd_kv8_plan {
 namespace {
 
 // Runs of splits per SM that the tcgen05 blocks are cut into, if they have as many.
-constexpr int kRunsPerSM = 4;
+constexpr int kRunsPerSM = 12;
+// Blocks per SM from which they are not cut.
+constexpr int kDirectPerSM = 2;
 
 int check_device(const vd_model* m) {
   int dev = -1;
@@ -261,25 +265,38 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   std::vector<int> blocks[4];
   const bool windowed = c.sliding_window > 0 && c.local_global_period > 0;
   d.pre_tc = m->prefill_kernel == 0 && c.head_dim <= 128;
+  size_t total_blocks = 0;  // most blocks of a layer that fold their splits themselves
+  bool direct[2] = {false, false};
   for (int local = 0; local <= (windowed ? 1 : 0); ++local)
     for (int pre = 0; pre < 2; ++pre) {
-      const int step = pre && d.pre_tc ? 128 : 16;
+      const bool tc = pre && d.pre_tc;
+      const int step = tc ? 128 : 16;
       std::vector<int>& to = blocks[2 * local + pre];
-      long long units = 0;
+      long long units = 0, row_blocks = 0;
       for (int pass = 0; pass < 2; ++pass) {  // the (row block, split) pairs are counted, then dealt out
-        const int run = pre && d.pre_tc ? static_cast<int>(std::max(1LL, units * c.n_kv_heads / (kRunsPerSM * m->n_sm))) : 1;
+        // Blocks that alone fill the SMs take all of their splits; fewer are cut
+        // into runs of splits.
+        direct[local] = tc && row_blocks * c.n_kv_heads >= static_cast<long long>(kDirectPerSM) * m->n_sm;
+        const int run = !tc ? 1 : direct[local] ? 1 << 30 : static_cast<int>(std::max(1LL, units * c.n_kv_heads / (kRunsPerSM * m->n_sm)));
+        int n_direct = 0;
         for (int i = 0; i < B; ++i) {
           const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i], rows = ql * m->G;
           if ((rows > 16) != (pre == 1)) continue;
           for (int r0 = 0; r0 < rows; r0 += step) {
             const int first = local ? std::max(0, cached + r0 / m->G - c.sliding_window + 1) / kAttn8Split : 0;
             const int end = (cached + (std::min(rows, r0 + step) - 1) / m->G) / kAttn8Split + 1;
-            units += end - first;
-            if (pass)
-              for (int sp = first; sp < end; sp += run)
-                to.insert(to.end(), {i, b->cu_q[i], ql, cached, sp, r0, std::min(end, sp + run), 0});
+            if (!pass) {
+              units += end - first;
+              ++row_blocks;
+              continue;
+            }
+            const int n = end - first, parts = (n - 1) / run + 1;  // runs of like lengths
+            for (int k = 0; k < parts; ++k)
+              to.insert(to.end(), {i, b->cu_q[i], ql, cached, first + n * k / parts, r0, first + n * (k + 1) / parts,
+                                   direct[local] ? n_direct++ : -1});
           }
         }
+        total_blocks = std::max(total_blocks, static_cast<size_t>(n_direct));
       }
     }
   for (int k = 0; k < 4; ++k) {  // int4, then int2: first, for their alignment
@@ -293,6 +310,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   d.positions = take(T);
   d.slot_page = take(T);
   d.logit_rows = take(R);
+  d.merge_list = take(T);
   d.open_stride = open_stride;
   d.open_table = take(static_cast<size_t>(B) * open_stride);
   d.page_table = take(static_cast<size_t>(B) * stride);
@@ -311,11 +329,14 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     t->host_cap[slot] = off * 2;
   }
   const size_t rows = static_cast<size_t>(T) * c.n_heads * splits;
+  const size_t tot = total_blocks * c.n_kv_heads * 128 * c.head_dim;  // floats
   int rc;
-  if (off > t->dev_cap || rows * (c.head_dim + 2) > t->part_cap) t->planned = false;  // the old plan's buffers go
-  if ((rc = grow(&t->dev, &t->dev_cap, off)) || (rc = grow(&t->part, &t->part_cap, rows * (c.head_dim + 2)))) return rc;
+  if (off > t->dev_cap || rows * (c.head_dim + 2) > t->part_cap || tot > t->tot_cap) t->planned = false;  // the old plan's buffers go
+  if ((rc = grow(&t->dev, &t->dev_cap, off)) || (rc = grow(&t->part, &t->part_cap, rows * (c.head_dim + 2))) ||
+      (rc = grow(&t->tot, &t->tot_cap, tot)))
+    return rc;
   int* h = t->host[slot];
-  int ns = 0;
+  int ns = 0, n_listed = 0;
   for (int i = 0; i < B; ++i) {
     const int q0 = b->cu_q[i], ql = b->cu_q[i + 1] - q0, cached = b->cached_len[i], first = cached / 16;
     const int full = (cached + ql) / 16, open = (cached + ql + 15) / 16 - first;
@@ -329,6 +350,8 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       h[d.seal + 2 * ns] = h[d.open_table + static_cast<size_t>(i) * open_stride + j - first];
       h[d.seal + 2 * ns + 1] = h[d.page_table + static_cast<size_t>(i) * stride + j];
     }
+    if (ql * m->G <= 16)  // the decode class first
+      for (int k = 0; k < ql; ++k) h[d.merge_list + n_listed++] = q0 + k;
     for (int k = 0; k < ql; ++k) {
       h[d.tokens + q0 + k] = b->token_ids ? b->token_ids[q0 + k] : 0;
       h[d.positions + q0 + k] = cached + k;
@@ -337,6 +360,11 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   }
   for (int k = 0; k < 4; ++k) std::copy(blocks[k].begin(), blocks[k].end(), h + d.items[k]);
   for (int j = 0; j < R; ++j) h[d.logit_rows + j] = b->logit_rows[j];
+  for (int local = 0; local < 2; ++local) d.n_merge_kv8[local] = direct[local] ? n_listed : T;
+  for (int i = 0; i < B; ++i)
+    if ((b->cu_q[i + 1] - b->cu_q[i]) * m->G > 16)
+      for (int k = b->cu_q[i]; k < b->cu_q[i + 1]; ++k) h[d.merge_list + n_listed++] = k;
+  d.totals = reinterpret_cast<float4*>(t->tot);
   d.base = t->dev;
   d.part_o = t->part;
   d.part_ml = t->part + rows * c.head_dim;
@@ -379,6 +407,8 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
   a.open_stride = d.open_stride;
   a.Hq = c.n_heads;
   a.Hkv = c.n_kv_heads;
+  a.totals = d.totals;
+  a.out = out;
   a.open = static_cast<const __nv_bfloat16*>(pool->data) +
            static_cast<size_t>(layer) * pool->num_pages * 2 * c.n_kv_heads * 16 * c.head_dim;
   a.layer_row0 = static_cast<int>(static_cast<long long>(layer) * pool->num_pages * 2 * c.n_kv_heads * 16);
@@ -397,12 +427,15 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
                               : launch_attention8(pool->map, a, c.head_dim, d.kv8->format, !cls && d.lower8, d.n_items[k], s)))
       return rc;
   }
+  const int n_merge = d.n_merge_kv8[a.window > 0];
+  if (n_merge == 0) return VD_OK;  // every row's splits were folded by its block
   MergeArgs g{};
+  g.tokens = n_merge < d.T ? d.base + d.merge_list : nullptr;
   g.part_o = d.part_o;
   g.part_ml = d.part_ml;
   g.out = out;
   g.positions = d.base + d.positions;
-  g.T = d.T;
+  g.T = n_merge;
   g.Hq = c.n_heads;
   g.window = a.window;
   g.split = kAttn8Split;
@@ -509,6 +542,7 @@ void vd_destroy_kv8_plan(vd_kv8_plan* t) {
   }
   if (t->dev) cudaFree(t->dev);
   if (t->part) cudaFree(t->part);
+  if (t->tot) cudaFree(t->tot);
   if (dev != t->device) cudaSetDevice(dev);
   delete t;
 }

@@ -20,7 +20,7 @@
 //
 // Order: the pages of a chunk ascending, the own page last.  Keys 2t + e and 2t +
 // 8 + e of each page go to the partial sum l_(t, e) of eight, t < 4, e < 2, of
-// the chunk's first four pages or its last four; the half chunk's l is the sum
+// the half of the chunk (four pages) that they are in; the half's l is the sum
 // over t, as (0 + 1) + (2 + 3), of l_(t, 0) + l_(t, 1), and the halves are added at
 // the end of the split.  The four chunks of a split run side by side, one per
 // warp, share their maxima before they take their weights, and are folded left to
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   uint64_t* bar = bars + warp * SL;
   uint64_t* own_bar = bars + 4 * SL;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(own_bar + 2);
-  __shared__ float fold_m[4][8 * NR], fold_l[2][4][8 * NR];  // per chunk and row: its largest score, its halves' l
+  __shared__ float fold_m[4][8 * NR], fold_l[kChunkParts][4][8 * NR];  // per chunk and row: its largest score, its parts' l
 
   // Up to the wait for the previous kernel the CTA reads only the status word and
   // the plan (uploaded before the step's first kernel).
@@ -333,13 +333,20 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   }
 
   // ---- weights, their sums and P V
-  float l[NR][2][2], o_acc[HD / 8][4];  // l: [half of the chunk's pages][e]
+  float l[NR][kChunkParts][2], o_acc[HD / 8][4];  // l: [part of the chunk's pages][e]
 #pragma unroll
-  for (int r = 0; r < NR; ++r) l[r][0][0] = l[r][0][1] = l[r][1][0] = l[r][1][1] = 0.f;
-  // weights x, 1 / V scales y of keys 2t, 2t + 1, 2t + 8, 2t + 9 of a page
-  auto add_l = [&](float (&s)[2], const float (&x)[4], float y0, float y1, float y2, float y3) {
-    s[0] = __fmaf_rn(x[2], y2, __fmaf_rn(x[0], y0, s[0]));
-    s[1] = __fmaf_rn(x[3], y3, __fmaf_rn(x[1], y1, s[1]));
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int h = 0; h < kChunkParts; ++h) l[r][h][0] = l[r][h][1] = 0.f;
+  // weights x, 1 / V scales y of keys 2t, 2t + 1, 2t + 8, 2t + 9 of page `page`
+  auto add_l = [&](float (&s)[kChunkParts][2], int page, const float (&x)[4], float y0, float y1, float y2, float y3) {
+    const int q = (page - pg0) / (kChunkPages / kChunkParts);
+#pragma unroll
+    for (int h = 0; h < kChunkParts; ++h)
+      if (h == q) {
+        s[h][0] = __fmaf_rn(x[2], y2, __fmaf_rn(x[0], y0, s[h][0]));
+        s[h][1] = __fmaf_rn(x[3], y3, __fmaf_rn(x[1], y1, s[h][1]));
+      }
   };
 #pragma unroll
   for (int n = 0; n < HD / 8; ++n) o_acc[n][0] = o_acc[n][1] = o_acc[n][2] = o_acc[n][3] = 0.f;
@@ -366,10 +373,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       // (a page that the row does not see stays out, whatever its scale)
-      if (full(a8 + i) || (a8 + i < own[r] && (a8 + i) * 16 + 15 >= lo[r])) {
-        if (a8 + i < pg0 + kChunkPages / 2) add_l(l[r][0], p[r], iv, iv, iv, iv);
-        else add_l(l[r][1], p[r], iv, iv, iv, iv);
-      }
+      if (full(a8 + i) || (a8 + i < own[r] && (a8 + i) * 16 + 15 >= lo[r])) add_l(l[r], a8 + i, p[r], iv, iv, iv, iv);
     }
     if (!wait(&bar[cp % SL], (cp / SL) & 1)) break;
     used = cp + 1;
@@ -406,10 +410,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
       uint32_t pa[4];
       weights(kChunkPages + o, p, pa);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        if (ao + o < pg0 + kChunkPages / 2) add_l(l[r][0], p[r], up[0], up[1], up[2], up[3]);
-        else add_l(l[r][1], p[r], up[0], up[1], up[2], up[3]);
-      }
+      for (int r = 0; r < NR; ++r) add_l(l[r], ao + o, p[r], up[0], up[1], up[2], up[3]);
 #pragma unroll
       for (int np = 0; np < HD / 16; ++np) {
         uint32_t w[4];
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kChunkParts; ++h) {
       float x = __fadd_rn(l[r][h][0], l[r][h][1]);
       x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 1));
       x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   const int frow = threadIdx.x / TPR, fd = threadIdx.x % TPR;
   const int row = r0 + frow;
   if (row >= rows) return;
-  float M = -INFINITY, L[2] = {0.f, 0.f}, O[PER];
+  float M = -INFINITY, L[kChunkParts] = {}, O[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) O[i] = 0.f;
 #pragma unroll
@@ -464,8 +465,8 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
     const float* src = reinterpret_cast<const float*>(ring0 + w * C::RING) + frow * HD;
     float alpha;
     kv8_running_max(M, fold_m[w][frow], alpha);
-    L[0] = __fmaf_rn(L[0], alpha, fold_l[0][w][frow]);
-    L[1] = __fmaf_rn(L[1], alpha, fold_l[1][w][frow]);
+#pragma unroll
+    for (int h = 0; h < kChunkParts; ++h) L[h] = __fmaf_rn(L[h], alpha, fold_l[h][w][frow]);
 #pragma unroll
     for (int i = 0; i < PER / 4; ++i) {
       const float4 v = *reinterpret_cast<const float4*>(src + (((i * TPR + fd) * 4) ^ ((frow & 7) * 8)));
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   const size_t base = (static_cast<size_t>(q0 + row / G) * a.Hq + kvh * G + row % G) * a.max_splits + sidx;
   if (fd == 0) {
     a.part_ml[base * 2] = M;
-    a.part_ml[base * 2 + 1] = __fadd_rn(L[0], L[1]);
+    a.part_ml[base * 2 + 1] = kv8_sum_parts(L);
   }
 #pragma unroll
   for (int i = 0; i < PER / 4; ++i)

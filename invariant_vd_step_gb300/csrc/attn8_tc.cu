@@ -11,11 +11,15 @@
 // K^T (N = 128) into one of two score buffers of tensor memory; the softmax
 // threads, two per row with 64 keys each, take the row's maximum, turn S into
 // fp16 weights in its place, and O = P V of the chunk goes to one of two O
-// buffers, which the same threads (64 dims each) fold into the split's O in their
-// registers once the next chunk's weights are written.  The next chunk's scores
-// run beside the softmax.  What a chunk takes per SM: the products 1024 cycles at
-// the dense rate, 16384 exponentials (512 cycles), and about 1350 issue slots per
-// scheduler in the softmax and conversion warps.
+// buffers, which the same threads (half of the dims each) fold into the
+// split's O in their registers two chunks later, when the scores that were issued
+// behind it are there.  A run that holds all of a block's splits folds them too, as
+// the merge kernel does (its totals wait in global memory, in L2, while a split is
+// in hand), and writes the output; shorter runs, which launches of few blocks
+// take, leave the splits' partials to that kernel.  The next chunk's scores run beside the softmax.  What a
+// chunk takes per SM: the products 1024 cycles at the dense rate, 16384
+// exponentials (512 cycles), and about 1700 issue slots per scheduler in the
+// softmax and conversion warps.
 //
 // Eight warps turn the codes into the operands, a page each: a lane's operand
 // words (kv8.cuh) are rows of 64 fp16 with the 128-byte swizzle after two 4-byte
@@ -45,9 +49,13 @@ struct Tc8Cfg {
   static constexpr int STAGES = 2;
   static constexpr int SCALES = kChunk8 * 3 * 4;    // per stage: 8 pages or 128 tokens x (K scale, log2 of V's, 1 / V's)
   static constexpr int SC_RING = 4;
-  static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + SC_RING * SCALES + 256;
+  static constexpr int NT = kChunkParts;  // softmax threads per row
+  static constexpr int NS = 128 * NT;
+  static constexpr int OUT_BYTES = 4 * NT * 32 * 128;  // per softmax warp: 32 rows x 32 dims of float32
+  static constexpr int REC_BYTES = NS * 40;  // per softmax thread: two chunks' factor, l and maximum; the totals' maximum and l
+  static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + OUT_BYTES + REC_BYTES + SC_RING * SCALES + 256;
   static constexpr int TMEM_COLS = 512;  // chunk c: scores (then weights) from 128 (c % 2), O from 256 + 128 (c % 2)
-  static constexpr int THREADS = 640;
+  static constexpr int THREADS = 384 + NS;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -88,6 +96,16 @@ __device__ __forceinline__ void wait_ld16(uint32_t* r) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
         "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
         "+r"(r[15])::"memory");
+}
+template <int N>
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
+  if constexpr (N == 32) ld32(taddr, r);
+  else ld16(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void wait_cols(uint32_t* r) {
+  if constexpr (N == 32) wait_ld32(r);
+  else wait_ld16(r);
 }
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
@@ -130,6 +148,11 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t x, uint64_t y) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
 __device__ __forceinline__ uint64_t f2_sub(uint64_t x, uint64_t y) {
   uint64_t r;
   asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
@@ -141,9 +164,9 @@ __device__ __forceinline__ bool softmax_sync(bool ok) {
   uint32_t bad;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "bar.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(bad)
-      : "r"(ok ? 0u : 1u)
+      : "r"(ok ? 0u : 1u), "n"(128 * kChunkParts)
       : "memory");
   return bad == 0;
 }
@@ -158,21 +181,24 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   uint8_t* sq = smem;
   uint8_t* sk = sq + C::Q_BYTES;                   // K of stage s at sk + (s % 2) * K_BYTES
   uint8_t* sv = sk + C::STAGES * C::K_BYTES;
-  float* scales = reinterpret_cast<float*>(sv + C::STAGES * C::V_BYTES);
+  uint8_t* so_out = sv + C::STAGES * C::V_BYTES;
+  float4* rec = reinterpret_cast<float4*>(so_out + C::OUT_BYTES);     // [2][NS]
+  float2* rec_tot = reinterpret_cast<float2*>(rec + 2 * C::NS);       // [NS]
+  float* scales = reinterpret_cast<float*>(rec_tot + C::NS);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scales) + C::SC_RING * C::SCALES);
   uint64_t* v_full = k_full + 2;     // [stage % 2] (and the two below)
   uint64_t* k_empty = v_full + 2;
   uint64_t* v_empty = k_empty + 2;
-  uint64_t* s_full = v_empty + 2;    // [chunk % 2]: its scores are there, the own pages' too
-  uint64_t* p_full = s_full + 2;     // its weights are
-  uint64_t* o_full = p_full + 2;     // its O is
-  uint64_t* o_free = o_full + 2;     // its O has been folded
-  uint64_t* q_full = o_free + 2;
-  uint64_t* mma_done = q_full + 1;
+  uint64_t* s_full = v_empty + 2;    // [chunk % 2]: its 8-bit scores are there, and O of the chunk two before it
+  uint64_t* p_full = s_full + 2;     // its weights are, and that O has been folded
+  uint64_t* q_full = p_full + 2;
+  uint64_t* s16_full = q_full + 1;   // scores of the own pages of a chunk that has some
+  uint64_t* o_free = s16_full + 1;   // the columns that they take are free
+  uint64_t* mma_done = o_free + 1;   // every MMA has completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  __shared__ float ex[2][2][128];  // [chunk % 2][half][row] largest scores
-  __shared__ float ex_l[2][128];   // l of the halves at a split's end
+  __shared__ float ex[2][C::NT][128];  // [chunk % 2][half][row] largest scores
+  __shared__ float ex_l[C::NT][128];   // l of the halves at a split's end
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ int skip;
@@ -194,11 +220,11 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       mbar_init(&k_empty[k], 1);
       mbar_init(&v_empty[k], 1);
       mbar_init(&s_full[k], 1);
-      mbar_init(&p_full[k], 256);
-      mbar_init(&o_full[k], 1);
-      mbar_init(&o_free[k], 256);
+      mbar_init(&p_full[k], C::NS);
     }
-    mbar_init(q_full, 256);
+    mbar_init(q_full, C::NS);
+    mbar_init(s16_full, 1);
+    mbar_init(o_free, C::NS);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -223,7 +249,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   auto hi16 = [&](int ch) { return min(kChunkPages, own_hi + 1 - ch * kChunkPages); };
 
   if (warp < 4) {
-    regs_dec<48>();
+    regs_dec<40>();
     if (warp == 0 && lane == 0) {
       const uint32_t id_s = idesc_f16(128, kChunk8), id_pv = idesc_f16(128, HD);
       const uint32_t q_lo = sw128_desc_lo(smem_u32(sq)), k_lo = sw128_desc_lo(smem_u32(sk)), v_lo = sw128_desc_lo(smem_u32(sv));
@@ -248,22 +274,20 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       // more for its own pages.  Scores run up to two chunks ahead of P V; at
       // chunks with own pages, whose two stages fill both slots, they wait for
       // the P V of every chunk before.
-      int ns = ch0, st_s = 0, st_v = 0;  // next chunk to score and its stage; the stage of the chunk whose P V is next
+      int ns = ch0, st_s = 0, st_v = 0, n16 = 0;  // next chunk to score, its stage; the stage of the chunk whose P V is next
       bool ok = wait(q_full, 0);
 #pragma unroll 1
       for (int ch = ch0 - 1; ok && ch <= ch1; ++ch) {  // (the first round only scores)
-        const int it = ch - ch0;
         if (ch >= ch0) {
+          const int it = ch - ch0;
           const bool dg = diag(ch);
           ok = wait(&p_full[it & 1], it >> 1) && wait(&v_full[st_v & 1], st_v >> 1) &&
-               (!dg || wait(&v_full[(st_v + 1) & 1], (st_v + 1) >> 1)) &&
-               (it < 2 || wait(&o_free[it & 1], (it >> 1) - 1));
+               (!dg || wait(&v_full[(st_v + 1) & 1], (st_v + 1) >> 1));
           if (!ok) break;
           tc_fence_after();
           const uint32_t o = 256 + 128 * (it & 1), p = 128 * (it & 1);
           pv(st_v, o, p, lo8(ch), hi8(ch), true);
           if (dg) pv(st_v + 1, o, p + 64, lo16(ch), hi16(ch), lo8(ch) >= hi8(ch));
-          umma_commit(&o_full[it & 1]);
           umma_commit(&v_empty[st_v & 1]);
           if (dg) umma_commit(&v_empty[(st_v + 1) & 1]);
           st_v += dg ? 2 : 1;
@@ -277,17 +301,18 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
           if (!ok) break;
           tc_fence_after();
           scores(st_s, 128 * (n & 1));
+          umma_commit(&s_full[n & 1]);
           umma_commit(&k_empty[st_s & 1]);
           ++st_s;
           if (dg) {  // own pages, into the columns that the chunk's O takes later
-            ok = wait(&k_full[st_s & 1], st_s >> 1) && (n < 2 || wait(&o_free[n & 1], (n >> 1) - 1));
+            ok = wait(&k_full[st_s & 1], st_s >> 1) && wait(o_free, n16++);
             if (!ok) break;
             tc_fence_after();
             scores(st_s, 256 + 128 * (n & 1));
+            umma_commit(s16_full);
             umma_commit(&k_empty[st_s & 1]);
             ++st_s;
           }
-          umma_commit(&s_full[n & 1]);
           ++ns;
         }
       }
@@ -295,7 +320,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
     }
   } else if (warp < 12) {
     // ---- operands: this warp's page of each chunk, K, then V
-    regs_dec<56>();
+    regs_dec<48>();
     const int pg = warp - 4, g = lane >> 2, t4 = lane & 3;
     uint4 w[UNITS];
     const int* pt = a.page_table + static_cast<size_t>(b) * a.pt_stride;
@@ -370,30 +395,35 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       mbar_arrive(&v_full[st & 1]);
       ++st;
       if (!diag(ch)) continue;
-      // The own pages in bf16: lane (token, half of the head dimension).  The scales
+      // The own pages in bf16, eight tokens at a time, four lanes a token.  The scales
       // of a token that is not finite are NaN, and its V counts as 0 (its weight is
       // NaN, or 0 where it is not seen).
-      const int token = lane >> 1, half = lane & 1, page = ch * kChunkPages + pg, key = pg * 16 + token;
-      const bool in = pg >= lo16(ch) && pg < hi16(ch), have = in && page * 16 + token < kv_len;
+      const int page = ch * kChunkPages + pg;
+      const bool in = pg >= lo16(ch) && pg < hi16(ch);
       const int phys = in ? a.open_table[static_cast<size_t>(b) * a.open_stride + page - (cached >> 4)] : 0;
       float* so = scales + (st & 3) * (C::SCALES / 4);
 #pragma unroll 1
       for (int v = 0; v < 2; ++v) {
         if (st >= 2 && !warp_wait(v ? &v_empty[st & 1] : &k_empty[st & 1], (st >> 1) - 1)) break;
-        const uint4* src = reinterpret_cast<const uint4*>(a.open + ((static_cast<size_t>(phys) * 2 + v) * a.Hkv + kvh) * PART +
-                                                          token * HD + half * (HD / 2));
-        if (in) {
+        const __nv_bfloat16* src = a.open + ((static_cast<size_t>(phys) * 2 + v) * a.Hkv + kvh) * PART + t4 * (HD / 4);
+#pragma unroll 1
+        for (int token = g; in && token < 16; token += 8) {
+          const int key = pg * 16 + token;
+          const bool have = page * 16 + token < kv_len;
+          uint4 y[HD / 32];
           uint32_t mx = 0u;
-#pragma unroll 4
-          for (int i = 0; i < HD / 16; ++i) {
-            const uint4 y = have ? __ldcg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
-                                       __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
-          }
+#pragma unroll
+          for (int i = 0; i < HD / 32; ++i)
+            y[i] = have ? __ldcg(reinterpret_cast<const uint4*>(src + token * HD) + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int i = 0; i < HD / 32; ++i)
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
+                                       __vmaxu2(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu)));
           mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const int e = kv8_exp(kv8_max_halves(mx));
           const float up = kv8_up(e);
-          if (half == 0) {
+          if (t4 == 0) {
             if (v == 0) {
               so[key] = e == 255 ? kv8_nan() : kv8_down(e);
             } else {
@@ -401,22 +431,19 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
               so[2 * kChunk8 + key] = up;
             }
           }
-#pragma unroll 2
-          for (int i = 0; i < HD / 16; ++i) {
-            uint4 y = have ? __ldcg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-            y = make_uint4(kv8_to_f16(y.x, up), kv8_to_f16(y.y, up), kv8_to_f16(y.z, up), kv8_to_f16(y.w, up));
-            const int d = half * (HD / 2) + i * 8;  // dims d .. d + 7
+#pragma unroll
+          for (int i = 0; i < HD / 32; ++i) {
+            const uint32_t x[4] = {kv8_to_f16(y[i].x, up), kv8_to_f16(y[i].y, up), kv8_to_f16(y[i].z, up), kv8_to_f16(y[i].w, up)};
+            const int d = t4 * (HD / 4) + i * 8;  // dims d .. d + 7
             if (v == 0) {
               *reinterpret_cast<uint4*>(sk + (st & 1) * C::K_BYTES + (d >> 6) * (kChunk8 * 128) + key * 128 +
-                                        ((((d >> 3) & 7) ^ (key & 7)) << 4)) = y;
+                                        ((((d >> 3) & 7) ^ (key & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
             } else {
-              if (e == 255) y = make_uint4(0u, 0u, 0u, 0u);
-              uint8_t* to = sv + (st & 1) * C::V_BYTES + (key >> 6) * (HD * 128) + (key & 7) * 2;
-              const uint32_t h[4] = {y.x, y.y, y.z, y.w};
+              uint8_t* to = sv + (st & 1) * C::V_BYTES + (key >> 6) * (HD * 128) + (key & 7) * 2 + d * 128;
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint16_t*>(to + (d + k) * 128 + ((((key >> 3) & 7) ^ ((d + k) & 7)) << 4)) =
-                    static_cast<uint16_t>(h[k >> 1] >> (16 * (k & 1)));
+              for (int k = 0; k < 8; ++k)  // (d % 8 = 0)
+                *reinterpret_cast<uint16_t*>(to + k * 128 + ((((key >> 3) & 7) ^ k) << 4)) =
+                    e == 255 ? static_cast<uint16_t>(0) : static_cast<uint16_t>(x[k >> 1] >> (16 * (k & 1)));
             }
           }
         }
@@ -426,9 +453,9 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       ++st;
     }
   } else {
-    // ---- softmax: two threads per row, of which thread h takes pages 4 h .. + 3 of a chunk and dims HD / 2 h .. of O
-    regs_inc<160>();
-    constexpr int HP = kChunkPages / 2, OD = HD / 2;
+    // ---- softmax: two threads per row, of which thread h takes pages 4 h .. + 3 of a chunk and half of O's dims
+    regs_inc<168>();
+    constexpr int HP = kChunkPages / C::NT, OD = HD / C::NT;
     const int h = (warp - 12) >> 2, lr = (warp & 3) * 32 + lane, row = r0 + lr;
     const bool valid = row < r_end;
     const int tok = valid ? row / G : 0, hq = kvh * G + (valid ? row % G : 0);
@@ -447,8 +474,8 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       const float up = kv8_up(e);
       rowfac = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
 #pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        const int i = h * (HD / 16) + k;
+      for (int k = 0; k < HD / 8 / C::NT; ++k) {
+        const int i = h * (HD / 8 / C::NT) + k;
         const uint4 x = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(sq + (i >> 3) * (C::ROWS * 128) + lr * 128 + (((i & 7) ^ (lr & 7)) << 4)) =
             make_uint4(kv8_to_f16(x.x, up), kv8_to_f16(x.y, up), kv8_to_f16(x.z, up), kv8_to_f16(x.w, up));
@@ -462,160 +489,245 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       ok = ok && __all_sync(0xffffffffu, mbar_wait(f, n & 1, abort_flag, a.status));
       return ok;
     };
-    // The split in hand: running maximum M, this thread's l and O (pairs of dims).
-    // `alpha`, `l_ch`: of the chunk whose O is not folded yet, the factor for what
-    // is before it (0 at a split's first, as what O and L hold is then of another
-    // split, and finite or NaN for good) and its l.
-    float M = -INFINITY, M_old = 0.f, L = 0.f, alpha = 0.f, l_ch = 0.f;
+    // The split in hand: this thread's l and O (pairs of dims); M: the running
+    // maximum at the chunk whose weights were taken last.  O of a chunk is folded
+    // two chunks later, with the factor for what is before it (0 at a split's first
+    // chunk, as what O and L hold is then of another split, and finite or NaN for
+    // good) and its l, which wait in shared memory, in a record of the thread's own.
+    float M = -INFINITY, L = 0.f;
     uint64_t O[OD / 2];
 #pragma unroll
     for (int i = 0; i < OD / 2; ++i) O[i] = 0ull;
-    int st = 0;
+    // The block's totals over the splits before (runs that hold all of them).
+    float4* totals = a.totals && d1.w >= 0 ? a.totals + (static_cast<size_t>(d1.w) * a.Hkv + kvh) * (C::ROWS * HD / 4) : nullptr;
+    const int sthread = threadIdx.x - 384;
+    bool have = false;
+    rec_tot[sthread] = make_float2(0.f, 0.f);
+    int st = 0, n16 = 0;
 #pragma unroll 1
-    for (int ch = ch0; ch <= ch1 + 1; ++ch) {
-      const int it = ch - ch0, pg0 = ch * kChunkPages;
-      const float alpha_old = alpha, l_old = l_ch;
-      const bool first = (ch & 3) == 0 || it == 0;
-      if (ch <= ch1) {
-        warp_wait(&s_full[it & 1], it >> 1);
-        tc_fence_after();
-        const uint32_t s_at = lanes + 128 * (it & 1);
-        const float4* sc = reinterpret_cast<const float4*>(scales + (st & 3) * (C::SCALES / 4)) + h * HP;
-        const float* so = scales + ((st + 1) & 3) * (C::SCALES / 4);
-        const bool dg = diag(ch);
-        if (dg) warp_wait(&v_full[(st + 1) & 1], (st + 1) >> 1);  // the V scales of the own pages' tokens
-        st += dg ? 2 : 1;
-        // every row of the warp sees this half chunk in 8 bits (rows that are none aside)
-        const bool full = __all_sync(0xffffffffu, !valid || (lo <= (pg0 + h * HP) * 16 && own >= pg0 + h * HP + HP));
-        uint64_t t[HP * 8];  // scores, as pairs of keys
-        uint32_t x[2][16];
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        ld16(s_at + 64 * h, x[0]);
+    for (int ch = ch0; ch <= ch1 + 2; ++ch) {
+      const int it = ch - ch0, pg0 = ch * kChunkPages + h * HP;  // this thread's first page
+      const uint32_t s_at = lanes + 128 * (it & 1), o_at = lanes + 256 + 128 * (it & 1);
+      const bool scored = ch <= ch1;
+      // O of chunk ch - 2 is there with the scores of ch, which were issued behind
+      // its P V; behind the last chunk there is the end of all MMAs.
+      warp_wait(scored ? &s_full[it & 1] : mma_done, scored ? it >> 1 : 0);
+      tc_fence_after();
+      if (it >= 2) {
+        constexpr int W = OD < 32 ? OD : 32;
+        const float4 r = rec[(it & 1) * C::NS + sthread];  // factor, l, maximum
+        const uint64_t al = f2(r.x, r.x);
 #pragma unroll
-        for (int pg = 0; pg < HP; ++pg) {
+        for (int c = 0; c < OD; c += W) {
+          uint32_t y[W];
+          ld_cols<W>(o_at + OD * h + c, y);
+          wait_cols<W>(y);
+#pragma unroll
+          for (int i = 0; i < W / 2; ++i) O[c / 2 + i] = f2_fma(O[c / 2 + i], al, f2(y[2 * i], y[2 * i + 1]));
+        }
+        L = __fmaf_rn(L, r.x, r.y);
+        const int pc = ch - 2, sp = pc >> 2;
+        if ((pc & 3) == 3 || pc == ch1) {  // its split's last
+          ex_l[h][lr] = L;
+          ok = softmax_sync(ok);
+          if (!ok) break;
+          float x[C::NT];
+#pragma unroll
+          for (int k = 0; k < C::NT; ++k) x[k] = ex_l[k][lr];
+          const float Ls = kv8_sum_parts(x);
+          const bool sees = valid && max(lo, sp * kSplit8) <= min(pos, sp * kSplit8 + kSplit8 - 1);
+          if (totals) {
+            // O <- the totals with this split, in the merge kernel's arithmetic
+            float4* tot = totals + sthread;  // [4 dims][thread]
+            const bool fold_in = sees && have, load = have && (sees || pc == ch1);
+            float2 ml = rec_tot[sthread];
+            const float mn = fmaxf(ml.x, r.z), ca = ex2(__fsub_rn(ml.x, mn)), cb = ex2(__fsub_rn(r.z, mn));
+            const uint64_t ca2 = f2(ca, ca), cb2 = f2(cb, cb);
+            if (load) {
+#pragma unroll
+              for (int i = 0; i < OD / 4; ++i) {
+                const float4 v = __ldcg(tot + i * C::NS);
+                const uint64_t v0 = f2(v.x, v.y), v1 = f2(v.z, v.w);
+                O[2 * i] = fold_in ? f2_add(f2_mul(v0, ca2), f2_mul(f2_add(O[2 * i], 0ull), cb2)) : v0;
+                O[2 * i + 1] = fold_in ? f2_add(f2_mul(v1, ca2), f2_mul(f2_add(O[2 * i + 1], 0ull), cb2)) : v1;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < OD / 2; ++i) O[i] = f2_add(O[i], 0ull);
+            }
+            if (sees) {
+              ml = have ? make_float2(mn, __fadd_rn(__fmul_rn(ml.y, ca), __fmul_rn(Ls, cb))) : make_float2(r.z, Ls);
+              rec_tot[sthread] = ml;
+              have = true;
+            }
+            if (pc < ch1) {
+              if (sees)
+#pragma unroll
+                for (int i = 0; i < OD / 4; ++i)
+                  __stcg(tot + i * C::NS, make_float4(f2_lo(O[2 * i]), f2_hi(O[2 * i]), f2_lo(O[2 * i + 1]), f2_hi(O[2 * i + 1])));
+            } else if (valid) {
+              uint4* to = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD + OD * h);
+#pragma unroll
+              for (int i = 0; i < OD / 8; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = pack_bf16x2(__fdiv_rn(f2_lo(O[4 * i + k]), ml.y), __fdiv_rn(f2_hi(O[4 * i + k]), ml.y));
+                to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          } else {
+            // The split's partial.  32 dims at a time go through shared memory, so
+            // that a store of the warp writes 128 bytes of each of four rows.
+            if (sees && h == 0) {
+              const size_t base = (static_cast<size_t>(q0 + tok) * a.Hq + hq) * a.max_splits + sp;
+              a.part_ml[base * 2] = r.z;
+              a.part_ml[base * 2 + 1] = Ls;
+            }
+            float4* buf = reinterpret_cast<float4*>(so_out) + (warp - 12) * 256;  // [row][8], the 16-byte words XORed with the row
+            const unsigned rows_seen = __ballot_sync(0xffffffffu, sees);
+#pragma unroll
+            for (int c = 0; c < OD; c += 32) {
+              constexpr int W = OD < 32 ? OD / 4 : 8;  // words of a row
+#pragma unroll
+              for (int i = 0; i < W; ++i) {
+                const uint64_t v0 = f2_add(O[c / 2 + 2 * i], 0ull), v1 = f2_add(O[c / 2 + 2 * i + 1], 0ull);
+                buf[lane * W + (i ^ (lane & (W - 1)))] = make_float4(f2_lo(v0), f2_hi(v0), f2_lo(v1), f2_hi(v1));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < W; ++k) {
+                const int rl = k * (32 / W) + lane / W, i = lane % W;
+                if ((rows_seen >> rl) & 1u) {
+                  const int rr = r0 + (warp & 3) * 32 + rl;
+                  const size_t base = (static_cast<size_t>(q0 + rr / G) * a.Hq + kvh * G + rr % G) * a.max_splits + sp;
+                  *reinterpret_cast<float4*>(a.part_o + base * HD + OD * h + c + i * 4) = buf[rl * W + (i ^ (rl & (W - 1)))];
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+      if (!scored) continue;
+      const float4* sc = reinterpret_cast<const float4*>(scales + (st & 3) * (C::SCALES / 4)) + h * HP;
+      const float* so = scales + ((st + 1) & 3) * (C::SCALES / 4) + h * HP * 16;
+      const bool dg = diag(ch);
+      if (dg) {
+        tc_fence_before();
+        mbar_arrive(o_free);
+        warp_wait(s16_full, n16++);
+        warp_wait(&v_full[(st + 1) & 1], (st + 1) >> 1);  // (the V scales of the own pages' tokens)
+        tc_fence_after();
+      }
+      st += dg ? 2 : 1;
+      // every row of the warp sees this half in 8 bits (rows that are none aside)
+      const bool full = __all_sync(0xffffffffu, !valid || (lo <= pg0 * 16 && own >= pg0 + HP));
+      float t[HP * 16];
+#pragma unroll
+      for (int p0 = 0; p0 < HP; p0 += 2) {
+        uint32_t x[32];
+        ld32(s_at + 16 * (HP * h + p0), x);
+        wait_ld32(x);
+#pragma unroll
+        for (int pg = p0; pg < p0 + 2; ++pg) {
           const float4 f = sc[pg];
           const float ks = __fmul_rn(f.x, rowfac);
           const uint64_t k2 = f2(ks, ks), lv2 = f2(f.y, f.y);
-          wait_ld16(x[pg & 1]);
-          if (pg + 1 < HP) ld16(s_at + 64 * h + 16 * (pg + 1), x[(pg + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) t[pg * 8 + i] = f2_fma(f2(x[pg & 1][2 * i], x[pg & 1][2 * i + 1]), k2, lv2);
-          if (!full) {
-            const int page = pg0 + h * HP + pg;
+          for (int i = pg * 16; i < pg * 16 + 16; i += 2) {
+            const uint64_t s2 = f2_fma(f2(x[i - 16 * p0], x[i - 16 * p0 + 1]), k2, lv2);
+            t[i] = f2_lo(s2);
+            t[i + 1] = f2_hi(s2);
+          }
+        }
+      }
+      if (!full) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int key = page * 16 + 2 * i;
-              t[pg * 8 + i] = f2(page < own && key >= lo ? f2_lo(t[pg * 8 + i]) : -INFINITY,
-                                 page < own && key + 1 >= lo ? f2_hi(t[pg * 8 + i]) : -INFINITY);
-            }
-            if (dg && ok && page >= own_lo && page <= own_hi) {  // the rows whose own page it is
-              uint32_t y[16];
-              ld16(lanes + 256 + 128 * (it & 1) + 16 * (h * HP + pg), y);
-              wait_ld16(y);
-              if (page == own) {
+        for (int pg = 0; pg < HP; ++pg) {
+          const int page = pg0 + pg;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const int n = (h * HP + pg) * 16 + i, key = page * 16 + i;
-                  const float v = __fmaf_rn(__uint_as_float(y[i]), __fmul_rn(so[n], rowfac), so[kChunk8 + n]);
-                  const float w = key >= lo && key <= pos ? v : -INFINITY;
-                  uint64_t& z = t[pg * 8 + (i >> 1)];
-                  z = (i & 1) ? f2(f2_lo(z), w) : f2(w, f2_hi(z));
-                }
+          for (int i = 0; i < 16; ++i)
+            if (!(page < own && page * 16 + i >= lo)) t[pg * 16 + i] = -INFINITY;
+          if (dg && page >= own_lo && page <= own_hi) {  // some rows' own page
+            uint32_t y[16];
+            ld16(o_at + 16 * (h * HP + pg), y);
+            wait_ld16(y);
+            if (page == own) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int key = page * 16 + i;
+                const float v = __fmaf_rn(__uint_as_float(y[i]), __fmul_rn(so[pg * 16 + i], rowfac), so[kChunk8 + pg * 16 + i]);
+                if (key >= lo && key <= pos) t[pg * 16 + i] = v;
               }
             }
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(f2_lo(t[pg * 8 + i]), f2_hi(t[pg * 8 + i])));
         }
-        ex[it & 1][h][lr] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        ok = softmax_sync(ok);  // also: every score has been read
-        if (!ok) break;
-        if (first) {
-          M_old = M;
-          M = -INFINITY;
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < HP * 16; i += 2) m4[(i >> 1) & 3] = fmaxf(m4[(i >> 1) & 3], fmaxf(t[i], t[i + 1]));
+      ex[it & 1][h][lr] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      ok = softmax_sync(ok);  // also: every score has been read
+      if (!ok) break;
+      const bool first = (ch & 3) == 0 || it == 0;
+      if (first) M = -INFINITY;
+      float mx = ex[it & 1][0][lr];
+#pragma unroll
+      for (int k = 1; k < C::NT; ++k) mx = fmaxf(mx, ex[it & 1][k][lr]);
+      float alpha;
+      kv8_running_max(M, mx, alpha);
+      if (first) alpha = 0.f;
+      const float u = M == -INFINITY ? 0.f : M;  // no key seen so far: every score is -inf, every weight 0
+      const uint64_t u2 = f2(u, u);
+      uint64_t l[4] = {0ull, 0ull, 0ull, 0ull};  // pair t: the partial sums (t, 0) and (t, 1)
+#pragma unroll
+      for (int pg = 0; pg < HP; ++pg) {
+        const float iv = sc[pg].z;
+        const uint64_t iv2 = f2(iv, iv);
+        const int page = pg0 + pg;
+        const uint32_t at = s_at + 8 * (h * HP + pg);
+        const bool own16 = dg && page >= own_lo && page <= own_hi;
+        uint32_t pk[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t s2 = f2_sub(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]), u2);
+          t[pg * 16 + 2 * i] = ex2(f2_lo(s2));
+          t[pg * 16 + 2 * i + 1] = ex2(f2_hi(s2));
+          pk[i] = pack_f16x2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]);
         }
-        kv8_running_max(M, fmaxf(ex[it & 1][0][lr], ex[it & 1][1][lr]), alpha);
-        if (first) alpha = 0.f;
-        const float u = M == -INFINITY ? 0.f : M;  // no key seen so far: every score is -inf, every weight 0
-        const uint64_t u2 = f2(u, u);
-        uint64_t l[4] = {0ull, 0ull, 0ull, 0ull};  // pair t: the partial sums (t, 0) and (t, 1)
+        if (full) {
 #pragma unroll
-        for (int pg = 0; pg < HP; ++pg) {
-          const float iv = sc[pg].z;
-          const uint64_t iv2 = f2(iv, iv);
-          const int page = pg0 + h * HP + pg;
-          uint32_t pk[8];
-          if (full) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint64_t s2 = f2_sub(t[pg * 8 + i], u2);
-              const float p0 = ex2(f2_lo(s2)), p1 = ex2(f2_hi(s2));
-              l[i & 3] = f2_fma(f2(p0, p1), iv2, l[i & 3]);
-              pk[i] = pack_f16x2(p0, p1);
-            }
-            st8(s_at + 8 * (h * HP + pg), pk);
-            if (dg && page >= own_lo && page <= own_hi) {  // another row's own page
-              const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-              st8(s_at + 64 + 8 * (h * HP + pg), zero);
-            }
-          } else {
-            const bool mine = page == own, sees = (page < own || mine) && page * 16 + 15 >= lo;
-            const float* up = so + 2 * kChunk8 + (h * HP + pg) * 16;
-            uint32_t p8[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint64_t s2 = f2_sub(t[pg * 8 + i], u2);
-              const float p0 = ex2(f2_lo(s2)), p1 = ex2(f2_hi(s2));
-              // (a page that the row does not see stays out, whatever its scale)
-              if (sees) l[i & 3] = f2_fma(f2(p0, p1), mine ? f2(up[2 * i], up[2 * i + 1]) : iv2, l[i & 3]);
-              pk[i] = pack_f16x2(p0, p1);
-              p8[i] = mine ? 0u : pk[i];
-              pk[i] = mine ? pk[i] : 0u;
-            }
-            st8(s_at + 8 * (h * HP + pg), p8);
-            if (dg && page >= own_lo && page <= own_hi) st8(s_at + 64 + 8 * (h * HP + pg), pk);
+          for (int i = 0; i < 8; ++i) l[i & 3] = f2_fma(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]), iv2, l[i & 3]);
+          st8(at, pk);
+          if (own16) {  // other rows' own page
+            const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            st8(at + 64, zero);
           }
-        }
-        l_ch = __fadd_rn(__fadd_rn(__fadd_rn(f2_lo(l[0]), f2_hi(l[0])), __fadd_rn(f2_lo(l[1]), f2_hi(l[1]))),
-                         __fadd_rn(__fadd_rn(f2_lo(l[2]), f2_hi(l[2])), __fadd_rn(f2_lo(l[3]), f2_hi(l[3]))));
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[it & 1]);
-      }
-      if (it == 0) continue;
-      // ---- O of the chunk before, and its split's partial if it was the last of it
-      const int pc = ch - 1, pit = it - 1;
-      if (warp_wait(&o_full[pit & 1], pit >> 1)) {
-        tc_fence_after();
-        uint32_t y[OD];
-        const uint32_t o_at = lanes + 256 + 128 * (pit & 1) + OD * h;
+        } else {
+          const bool mine = page == own;
+          if ((page < own || mine) && page * 16 + 15 >= lo) {  // (a page that the row does not see stays out, whatever its scale)
+            const float* up = so + 2 * kChunk8 + pg * 16;
 #pragma unroll
-        for (int c = 0; c < OD / 32; ++c) ld32(o_at + 32 * c, y + 32 * c);
-#pragma unroll
-        for (int c = 0; c < OD / 32; ++c) wait_ld32(y + 32 * c);
-        tc_fence_before();
-        mbar_arrive(&o_free[pit & 1]);
-        const uint64_t al = f2(alpha_old, alpha_old);
-#pragma unroll
-        for (int i = 0; i < OD / 2; ++i) O[i] = f2_fma(O[i], al, f2(y[2 * i], y[2 * i + 1]));
-        L = __fmaf_rn(L, alpha_old, l_old);
-      }
-      if ((pc & 3) == 3 || pc == ch1) {
-        const int sp = pc >> 2;
-        ex_l[h][lr] = L;
-        ok = softmax_sync(ok);
-        if (!ok) break;
-        if (valid && max(lo, sp * kSplit8) <= min(pos, sp * kSplit8 + kSplit8 - 1)) {
-          const size_t base = (static_cast<size_t>(q0 + tok) * a.Hq + hq) * a.max_splits + sp;
-          if (h == 0) {
-            a.part_ml[base * 2] = pc == ch1 ? M : M_old;
-            a.part_ml[base * 2 + 1] = __fadd_rn(ex_l[0][lr], ex_l[1][lr]);
+            for (int i = 0; i < 8; ++i)
+              l[i & 3] = f2_fma(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]), mine ? f2(up[2 * i], up[2 * i + 1]) : iv2, l[i & 3]);
           }
-          ulonglong2* po = reinterpret_cast<ulonglong2*>(a.part_o + base * HD + OD * h);
+          uint32_t p8[8];
 #pragma unroll
-          for (int i = 0; i < OD / 4; ++i) po[i] = make_ulonglong2(f2_add(O[2 * i], 0ull), f2_add(O[2 * i + 1], 0ull));
+          for (int i = 0; i < 8; ++i) {
+            p8[i] = mine ? 0u : pk[i];
+            pk[i] = mine ? pk[i] : 0u;
+          }
+          st8(at, p8);
+          if (own16) st8(at + 64, pk);
         }
       }
+      const float l_ch = __fadd_rn(__fadd_rn(__fadd_rn(f2_lo(l[0]), f2_hi(l[0])), __fadd_rn(f2_lo(l[1]), f2_hi(l[1]))),
+                                   __fadd_rn(__fadd_rn(f2_lo(l[2]), f2_hi(l[2])), __fadd_rn(f2_lo(l[3]), f2_hi(l[3]))));
+      rec[(it & 1) * C::NS + sthread] = make_float4(alpha, l_ch, M, 0.f);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[it & 1]);
     }
   }
   // Teardown: issued MMAs finish, then tensor memory is freed.

@@ -7,6 +7,7 @@
 namespace vd {
 
 constexpr int kKv8Int8 = 0, kKv8E4m3 = 1;
+constexpr int kChunkParts = 2;  // parts of a chunk's pages whose l are summed apart (threads per row of the tcgen05 kernel)
 
 // Codes of one (page, head): K part, then V part, each HD / 32 units of 512
 // bytes: 16 bytes for each lane of a warp, the operand words of mma.sync
@@ -67,6 +68,13 @@ __device__ __forceinline__ void kv8_running_max(float& m, float mx, float& alpha
   const float mn = fmaxf(m, mx);
   alpha = mn == m ? 1.0f : ex2(__fsub_rn(m, mn));
   m = mn;
+}
+
+__device__ __forceinline__ float kv8_sum_parts(const float (&x)[kChunkParts]) {
+  float s = 0.f;
+  if constexpr (kChunkParts == 2) s = __fadd_rn(x[0], x[1]);
+  if constexpr (kChunkParts == 4) s = __fadd_rn(__fadd_rn(x[0], x[1]), __fadd_rn(x[2], x[3]));
+  return s;
 }
 
 __device__ __forceinline__ void mma_f16_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {

@@ -239,8 +239,11 @@ struct Attn8Args {
   float* part_ml;           // [T][Hq][max_splits][2]
   const int* page_table;    // [B][pt_stride] pages of the cache
   const int* open_table;    // [B][open_stride] pages of the bf16 pool, from logical page cached_len / 16 on
-  const int4* items;        // [blocks][2]: request, first token, tokens, cached tokens; split, first row, end of the
-                            // splits (tcgen05 kernel, whose blocks take several), 0
+  const int4* items;        // [blocks][2]: request, first token, tokens, cached tokens; split, first row; and for
+                            // the tcgen05 kernel, whose blocks take several: end of the splits, the block's number
+                            // among those whose splits it folds itself (-1: it leaves partials)
+  float4* totals;           // [such blocks][Hkv][128 rows x hd floats]
+  __nv_bfloat16* out;       // [T][Hq][hd] (their rows)
   const __nv_bfloat16* open;  // the layer's first page of the bf16 pool
   const uint8_t* codes;     // the layer's first page
   const float4* scales;
