@@ -43,6 +43,8 @@ struct vd_kv8_plan {
   size_t part_cap = 0;  // floats
   float* tot = nullptr;
   size_t tot_cap = 0;   // floats
+  uint8_t* images = nullptr;
+  size_t images_cap = 0;
   int* host[2] = {nullptr, nullptr};  // pinned staging
   size_t host_cap[2] = {0, 0};
   cudaEvent_t uploaded[2] = {nullptr, nullptr};
@@ -265,6 +267,24 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   std::vector<int> blocks[4];
   const bool windowed = c.sliding_window > 0 && c.local_global_period > 0;
   d.pre_tc = m->prefill_kernel == 0 && c.head_dim <= 128;
+  // The tcgen05 blocks' requests have images of their chunks: of chunk 0 on, then of
+  // those that hold own pages, numbered one request after the other.
+  std::vector<int> image0(B, 0), chunks[2];
+  long long n_images = 0;
+  if (d.pre_tc)
+    for (int i = 0; i < B; ++i) {
+      const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i], kv = cached + ql, all = (kv + 127) / 128;
+      if (ql * m->G <= 16) continue;
+      image0[i] = static_cast<int>(n_images);
+      for (int local = 0; local <= (windowed ? 1 : 0); ++local) {
+        const int first = local ? std::max(0, cached - c.sliding_window + 1) / 128 : 0;
+        for (int ch = first; ch < all; ++ch) chunks[local].insert(chunks[local].end(), {i, ch, image0[i] + ch, 0, cached, kv, 0, 0});
+        for (int ch = cached / 128; ch < all; ++ch)
+          chunks[local].insert(chunks[local].end(), {i, ch, image0[i] + all + ch - cached / 128, 1, cached, kv, 0, 0});
+      }
+      n_images += 2 * all - cached / 128;
+      if (n_images * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
+    }
   size_t total_blocks = 0;  // most blocks of a layer that fold their splits themselves
   bool direct[2] = {false, false};
   for (int local = 0; local <= (windowed ? 1 : 0); ++local)
@@ -292,7 +312,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
             }
             const int n = end - first, parts = (n - 1) / run + 1;  // runs of like lengths
             for (int k = 0; k < parts; ++k)
-              to.insert(to.end(), {i, b->cu_q[i], ql, cached, first + n * k / parts, r0, first + n * (k + 1) / parts,
+              to.insert(to.end(), {tc ? image0[i] : i, b->cu_q[i], ql, cached, first + n * k / parts, r0, first + n * (k + 1) / parts,
                                    direct[local] ? n_direct++ : -1});
           }
         }
@@ -303,6 +323,10 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     if (blocks[k].size() / 8 * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
     d.items[k] = take(blocks[k].size());
     d.n_items[k] = static_cast<int>(blocks[k].size() / 8);
+  }
+  for (int k = 0; k < 2; ++k) {
+    d.chunks[k] = take(chunks[k].size());
+    d.n_chunks[k] = static_cast<int>(chunks[k].size() / 8);
   }
   d.seal = take(2 * static_cast<size_t>(n_seal));
   d.n_seal = n_seal;
@@ -329,11 +353,13 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     t->host_cap[slot] = off * 2;
   }
   const size_t rows = static_cast<size_t>(T) * c.n_heads * splits;
+  const size_t images = static_cast<size_t>(n_images) * c.n_kv_heads * attn8_image_bytes(c.head_dim);
   const size_t tot = total_blocks * c.n_kv_heads * 128 * c.head_dim;  // floats
   int rc;
-  if (off > t->dev_cap || rows * (c.head_dim + 2) > t->part_cap || tot > t->tot_cap) t->planned = false;  // the old plan's buffers go
+  if (off > t->dev_cap || rows * (c.head_dim + 2) > t->part_cap || tot > t->tot_cap || images > t->images_cap)
+    t->planned = false;  // the old plan's buffers go
   if ((rc = grow(&t->dev, &t->dev_cap, off)) || (rc = grow(&t->part, &t->part_cap, rows * (c.head_dim + 2))) ||
-      (rc = grow(&t->tot, &t->tot_cap, tot)))
+      (rc = grow(&t->tot, &t->tot_cap, tot)) || (rc = grow(&t->images, &t->images_cap, images)))
     return rc;
   int* h = t->host[slot];
   int ns = 0, n_listed = 0;
@@ -359,12 +385,14 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     }
   }
   for (int k = 0; k < 4; ++k) std::copy(blocks[k].begin(), blocks[k].end(), h + d.items[k]);
+  for (int k = 0; k < 2; ++k) std::copy(chunks[k].begin(), chunks[k].end(), h + d.chunks[k]);
   for (int j = 0; j < R; ++j) h[d.logit_rows + j] = b->logit_rows[j];
   for (int local = 0; local < 2; ++local) d.n_merge_kv8[local] = direct[local] ? n_listed : T;
   for (int i = 0; i < B; ++i)
     if ((b->cu_q[i + 1] - b->cu_q[i]) * m->G > 16)
       for (int k = b->cu_q[i]; k < b->cu_q[i + 1]; ++k) h[d.merge_list + n_listed++] = k;
   d.totals = reinterpret_cast<float4*>(t->tot);
+  d.images = t->images;
   d.base = t->dev;
   d.part_o = t->part;
   d.part_ml = t->part + rows * c.head_dim;
@@ -407,12 +435,14 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
   a.open_stride = d.open_stride;
   a.Hq = c.n_heads;
   a.Hkv = c.n_kv_heads;
+  a.images = d.images;
   a.totals = d.totals;
   a.out = out;
   a.open = static_cast<const __nv_bfloat16*>(pool->data) +
            static_cast<size_t>(layer) * pool->num_pages * 2 * c.n_kv_heads * 16 * c.head_dim;
   a.layer_row0 = static_cast<int>(static_cast<long long>(layer) * pool->num_pages * 2 * c.n_kv_heads * 16);
   a.window = layer_is_local(c, layer) ? c.sliding_window : 0;
+  a.chunks = reinterpret_cast<const int4*>(d.base + d.chunks[a.window > 0]);
   a.max_splits = d.part_splits;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(c.head_dim)));
   a.status = m->status;
@@ -423,7 +453,8 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
     Prof p(m, K_ATTN, s);
     a.items = reinterpret_cast<const int4*>(d.base + d.items[k]);
     a.own_slots = cls ? 2 : d.own_slots;
-    if ((rc = cls && d.pre_tc ? launch_attention8_tc(a, c.head_dim, d.kv8->format, d.n_items[k], s)
+    p.kernels = cls && d.pre_tc ? 2 : 1;
+    if ((rc = cls && d.pre_tc ? launch_attention8_tc(a, c.head_dim, d.kv8->format, d.n_chunks[k >> 1], d.n_items[k], s)
                               : launch_attention8(pool->map, a, c.head_dim, d.kv8->format, !cls && d.lower8, d.n_items[k], s)))
       return rc;
   }
@@ -543,6 +574,7 @@ void vd_destroy_kv8_plan(vd_kv8_plan* t) {
   if (t->dev) cudaFree(t->dev);
   if (t->part) cudaFree(t->part);
   if (t->tot) cudaFree(t->tot);
+  if (t->images) cudaFree(t->images);
   if (dev != t->device) cudaSetDevice(dev);
   delete t;
 }

@@ -21,15 +21,19 @@
 // exponentials (512 cycles), and about 1700 issue slots per scheduler in the
 // softmax and conversion warps.
 //
-// Eight warps turn the codes into the operands, a page each: a lane's operand
-// words (kv8.cuh) are rows of 64 fp16 with the 128-byte swizzle after two 4-byte
-// stores each, V transposed ([dim][key]) so that both operands are K-major.  The
-// pages that are some row's own enter as a second K/V stage of their chunk, in
-// bf16 scaled per token to exact fp16, with scores of their own (in the chunk's O
-// buffer); a row takes 16 of their columns.
+// The operands are made once per launch, not once per row block: an expanding
+// kernel turns every chunk of the launch's requests into an image of the two
+// shared-memory tiles, rows of 64 fp16 with the 128-byte swizzle, V transposed
+// ([dim][key]) so that both are K-major, and of the chunk's scales; a block then
+// fetches a tile with one bulk copy (from L2: a request's blocks run together).
+// The pages that are some row's own have a second image of their chunk, in bf16
+// scaled per token to exact fp16, and scores of their own (in the columns that the
+// chunk's O takes later); a row takes 16 of their columns.  Converting inside the
+// blocks, by eight warps beside the softmax, took a third of the issue slots and
+// made a chunk's softmax wait: 5000 cycles per chunk, XXXX now.
 //
-// Roles (640 threads): warp 0 allocates tensor memory, its lane 0 issues the MMAs;
-// warps 4..11 convert; warps 12..19 are the softmax.  Every wait is bounded.
+// Roles (384 threads): warp 0 allocates tensor memory, its lane 0 issues the MMAs;
+// warp 1's lane 0 the copies; warps 4..11 are the softmax.  Every wait is bounded.
 #include <math.h>
 
 #include "kv8.cuh"
@@ -55,7 +59,9 @@ struct Tc8Cfg {
   static constexpr int REC_BYTES = NS * 40;  // per softmax thread: two chunks' factor, l and maximum; the totals' maximum and l
   static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + OUT_BYTES + REC_BYTES + SC_RING * SCALES + 256;
   static constexpr int TMEM_COLS = 512;  // chunk c: scores (then weights) from 128 (c % 2), O from 256 + 128 (c % 2)
-  static constexpr int THREADS = 384 + NS;
+  static constexpr int THREADS = 128 + NS;
+  // A chunk's image: K tile, V tile, scales
+  static constexpr int IMAGE = K_BYTES + V_BYTES + SCALES;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -171,11 +177,135 @@ __device__ __forceinline__ bool softmax_sync(bool ok) {
   return bad == 0;
 }
 
-// Item: its request, rows [r0, r0 + 128) and splits [sp0, sp1).
+// Images of chunks: one block per (chunk, KV head), a warp per page.  A lane's
+// operand words (kv8.cuh) become two 4-byte pieces of rows of the tiles, which
+// leave shared memory in whole 16-byte words.  Bound by memory: 32 KB of codes in
+// and 64 KB of fp16 out per block at hd 128.
 template <int HD, int FMT>
+__global__ void __launch_bounds__(256) attn8_expand_kernel(Attn8Args a) {
+  using C = Tc8Cfg<HD>;
+  constexpr int UNITS = Kv8Cfg<HD>::UNITS, PART = Kv8Cfg<HD>::PART;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int pg = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int kvh = blockIdx.x % a.Hkv;
+  const int4 d = a.chunks[2 * (blockIdx.x / a.Hkv)], e = a.chunks[2 * (blockIdx.x / a.Hkv) + 1];
+  const int b = d.x, ch = d.y, image = d.z, cached = e.x, kv_len = e.y;
+  const bool own = d.w != 0;  // the image of the chunk's own pages
+  const int page = ch * kChunkPages + pg;
+  const bool in = own ? page >= cached >> 4 && page * 16 < kv_len : (page + 1) * 16 <= kv_len;
+  const int pid = !in ? 0
+                  : own ? a.open_table[static_cast<size_t>(b) * a.open_stride + page - (cached >> 4)]
+                        : a.page_table[static_cast<size_t>(b) * a.pt_stride + page];
+  pdl_wait();
+  pdl_trigger();
+  uint8_t *sk = smem, *sv = sk + C::K_BYTES;
+  float* sc = reinterpret_cast<float*>(sv + C::V_BYTES);
+  if (!own) {
+    const size_t block = static_cast<size_t>(pid) * a.Hkv + kvh;
+    const uint4* src = reinterpret_cast<const uint4*>(a.codes + block * (2 * PART)) + lane;
+    uint4 w[2][UNITS];
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) w[v][u] = in ? __ldcg(src + v * (PART / 16) + u * 32) : make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0) {
+      const float4 f = in ? __ldcg(a.scales + block) : make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(sc + pg * 4) = make_float4(f.x, f.z, f.y, 0.f);
+    }
+    // the two fp16 pairs of a word go to 16-byte columns c and c + 1 of row g of an 8-row group
+    auto col = [&](int c) { return static_cast<uint32_t>(g * 128 + ((c ^ g) << 4) + t4 * 4); };
+    auto put = [&](uint32_t at0, uint32_t at1, uint32_t word) {
+      uint32_t lo, hi;
+      kv8_expand<FMT>(word, lo, hi);
+      sts32(at0, lo);
+      sts32(at1, hi);
+    };
+    const uint32_t kb = smem_u32(sk) + pg * (16 * 128);
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {  // k-steps 2 u and 2 u + 1 of key blocks 0 and 1
+      const int k = (u & 1) * 4, at = (u >> 1) * (kChunk8 * 128);
+      put(kb + at + col(k), kb + at + col(k + 1), w[0][u].x);
+      put(kb + at + 8 * 128 + col(k), kb + at + 8 * 128 + col(k + 1), w[0][u].y);
+      put(kb + at + col(k + 2), kb + at + col(k + 3), w[0][u].z);
+      put(kb + at + 8 * 128 + col(k + 2), kb + at + 8 * 128 + col(k + 3), w[0][u].w);
+    }
+    // this page's 16 keys are columns 2 (page % 4) and + 1 of its key block
+    const uint32_t vb = smem_u32(sv) + (pg >> 2) * (HD * 128), c0 = vb + col((pg & 3) * 2), c1 = vb + col((pg & 3) * 2 + 1);
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {  // dims 32 u .. + 31
+      const int at = 32 * u * 128;
+      put(c0 + at, c1 + at, w[1][u].x);
+      put(c0 + at + 8 * 128, c1 + at + 8 * 128, w[1][u].y);
+      put(c0 + at + 16 * 128, c1 + at + 16 * 128, w[1][u].z);
+      put(c0 + at + 24 * 128, c1 + at + 24 * 128, w[1][u].w);
+    }
+  } else {
+    // The own pages in bf16, eight tokens at a time, four lanes a token; zeros behind
+    // the last token and in other pages.  The scales of a token that is not finite are
+    // NaN, and its V counts as 0 (its weight is NaN, or 0 where it is not seen).
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const __nv_bfloat16* src = a.open + ((static_cast<size_t>(pid) * 2 + v) * a.Hkv + kvh) * PART + t4 * (HD / 4);
+#pragma unroll
+      for (int token = g; token < 16; token += 8) {
+        const int key = pg * 16 + token;
+        const bool have = in && page * 16 + token < kv_len;
+        uint4 y[HD / 32];
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int i = 0; i < HD / 32; ++i)
+          y[i] = have ? __ldcg(reinterpret_cast<const uint4*>(src + token * HD) + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < HD / 32; ++i)
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
+                                     __vmaxu2(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu)));
+        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int ex = kv8_exp(kv8_max_halves(mx));
+        const float up = kv8_up(ex);
+        if (t4 == 0) {
+          if (v == 0) {
+            sc[key] = ex == 255 ? kv8_nan() : kv8_down(ex);
+          } else {
+            sc[kChunk8 + key] = ex == 255 ? kv8_nan() : kv8_log2_down(ex);
+            sc[2 * kChunk8 + key] = up;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < HD / 32; ++i) {
+          const uint32_t x[4] = {kv8_to_f16(y[i].x, up), kv8_to_f16(y[i].y, up), kv8_to_f16(y[i].z, up), kv8_to_f16(y[i].w, up)};
+          const int dim = t4 * (HD / 4) + i * 8;  // .. + 7
+          if (v == 0) {
+            *reinterpret_cast<uint4*>(sk + (dim >> 6) * (kChunk8 * 128) + key * 128 + ((((dim >> 3) & 7) ^ (key & 7)) << 4)) =
+                make_uint4(x[0], x[1], x[2], x[3]);
+          } else {
+            uint8_t* to = sv + (key >> 6) * (HD * 128) + (key & 7) * 2 + dim * 128;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)  // (dim % 8 = 0)
+              *reinterpret_cast<uint16_t*>(to + k * 128 + ((((key >> 3) & 7) ^ k) << 4)) =
+                  ex == 255 ? static_cast<uint16_t>(0) : static_cast<uint16_t>(x[k >> 1] >> (16 * (k & 1)));
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  uint4* to = reinterpret_cast<uint4*>(a.images + (static_cast<size_t>(image) * a.Hkv + kvh) * C::IMAGE);
+  const uint4* from = reinterpret_cast<const uint4*>(smem);
+  constexpr int TILES = (C::K_BYTES + C::V_BYTES) / 16;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < TILES; i += 256) to[i] = from[i];
+  for (int i = TILES + threadIdx.x; i < C::IMAGE / 16; i += 256)
+    if (own || i < TILES + kChunkPages) to[i] = from[i];  // (an 8-bit chunk's scales end there)
+}
+
+// Item: its request's first image (of chunk 0; those of the own pages' chunks
+// follow the others), rows [r0, r0 + 128) and splits [sp0, sp1).
+template <int HD>
 __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8Args a) {
   using C = Tc8Cfg<HD>;
-  constexpr int KK = HD / 16, UNITS = Kv8Cfg<HD>::UNITS, PART = Kv8Cfg<HD>::PART;
+  constexpr int KK = HD / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
@@ -204,7 +334,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   __shared__ int skip;
   const int kvh = blockIdx.x % a.Hkv;
   const int4 d0 = a.items[2 * (blockIdx.x / a.Hkv)], d1 = a.items[2 * (blockIdx.x / a.Hkv) + 1];
-  const int b = d0.x, q0 = d0.y, qlen = d0.z, cached = d0.w, sp0 = d1.x, r0 = d1.y, sp1 = d1.z;
+  const int image0 = d0.x, q0 = d0.y, qlen = d0.z, cached = d0.w, sp0 = d1.x, r0 = d1.y, sp1 = d1.z;
   const int G = a.Hq / a.Hkv, rows = qlen * G, kv_len = cached + qlen;
   const int r_end = min(rows, r0 + C::ROWS);
   const int p_min = cached + r0 / G, p_max = cached + (r_end - 1) / G;
@@ -215,8 +345,8 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   if (threadIdx.x == 0) {
     skip = a.status ? *reinterpret_cast<volatile int*>(a.status) : 0;
     for (int k = 0; k < 2; ++k) {
-      mbar_init(&k_full[k], 256);
-      mbar_init(&v_full[k], 256);
+      mbar_init(&k_full[k], 1);
+      mbar_init(&v_full[k], 1);
       mbar_init(&k_empty[k], 1);
       mbar_init(&v_empty[k], 1);
       mbar_init(&s_full[k], 1);
@@ -248,8 +378,9 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   auto lo16 = [&](int ch) { return max(0, own_lo - ch * kChunkPages); };
   auto hi16 = [&](int ch) { return min(kChunkPages, own_hi + 1 - ch * kChunkPages); };
 
+  int issued_k = 0, issued_v = 0;  // stages whose copies have been issued (the copying thread's)
   if (warp < 4) {
-    regs_dec<40>();
+    regs_dec<72>();
     if (warp == 0 && lane == 0) {
       const uint32_t id_s = idesc_f16(128, kChunk8), id_pv = idesc_f16(128, HD);
       const uint32_t q_lo = sw128_desc_lo(smem_u32(sq)), k_lo = sw128_desc_lo(smem_u32(sk)), v_lo = sw128_desc_lo(smem_u32(sv));
@@ -318,145 +449,33 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       }
       umma_commit(mma_done);
     }
-  } else if (warp < 12) {
-    // ---- operands: this warp's page of each chunk, K, then V
-    regs_dec<48>();
-    const int pg = warp - 4, g = lane >> 2, t4 = lane & 3;
-    uint4 w[UNITS];
-    const int* pt = a.page_table + static_cast<size_t>(b) * a.pt_stride;
-    int st = 0;
-    bool ok = true;
-    auto warp_wait = [&](uint64_t* f, int n) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(f, n & 1, abort_flag, a.status));
-      return ok;
-    };
-    auto here = [&](int ch) { return pg >= lo8(ch) && pg < hi8(ch); };
-    auto load = [&](int ch, bool v, int pid) {
-      const uint4* src =
-          reinterpret_cast<const uint4*>(a.codes + (static_cast<size_t>(pid) * a.Hkv + kvh) * (2 * PART) + (v ? PART : 0)) + lane;
-      const bool in = here(ch);
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) w[u] = in ? __ldcg(src + u * 32) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto id_of = [&](int ch) { return ch <= ch1 && here(ch) ? pt[ch * kChunkPages + pg] : 0; };
-    // The two fp16 pairs of an operand word go to 16-byte columns c and c + 1 of
-    // row g of an 8-row group; `col`: offset of this lane's pair in column c, swizzled.
-    auto col = [&](int c) { return static_cast<uint32_t>(g * 128 + ((c ^ g) << 4) + t4 * 4); };
-    auto put = [&](uint32_t at0, uint32_t at1, uint32_t word) {
-      uint32_t lo, hi;
-      kv8_expand<FMT>(word, lo, hi);
-      sts32(at0, lo);
-      sts32(at1, hi);
-    };
-    int pid = id_of(ch0);
-    load(ch0, false, pid);
+    if (warp == 1 && lane == 0) {  // ---- copies
+      const int own_image = image0 + (kv_len + kChunk8 - 1) / kChunk8 - cached / kChunk8;  // + chunk: that of its own pages
+      auto wait = [&](uint64_t* f, int n) { return mbar_wait(f, n & 1, abort_flag, a.status); };
+      int st = 0;
+      auto stage = [&](int image) -> bool {
+        const uint8_t* src = a.images + (static_cast<size_t>(image) * a.Hkv + kvh) * C::IMAGE;
+        const int s2 = st & 1, k = (st >> 1) - 1;
+        if (st >= 2 && !wait(&k_empty[s2], k)) return false;
+        mbar_arrive_expect_tx(&k_full[s2], C::K_BYTES + C::SCALES);
+        bulk_load(sk + s2 * C::K_BYTES, src, C::K_BYTES, &k_full[s2]);
+        bulk_load(scales + (st & 3) * (C::SCALES / 4), src + C::K_BYTES + C::V_BYTES, C::SCALES, &k_full[s2]);
+        issued_k = st + 1;
+        if (st >= 2 && !wait(&v_empty[s2], k)) return false;
+        mbar_arrive_expect_tx(&v_full[s2], C::V_BYTES);
+        bulk_load(sv + s2 * C::V_BYTES, src + C::K_BYTES, C::V_BYTES, &v_full[s2]);
+        issued_v = ++st;
+        return true;
+      };
+      bool ok = true;
 #pragma unroll 1
-    for (int ch = ch0; ok && ch <= ch1; ++ch) {
-      const int pid_next = id_of(ch + 1);
-      if (st >= 2 && !warp_wait(&k_empty[st & 1], (st >> 1) - 1)) break;
-      if (lane == 0) {
-        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (here(ch)) f = __ldcg(a.scales + static_cast<size_t>(pid) * a.Hkv + kvh);
-        *reinterpret_cast<float4*>(scales + (st & 3) * (C::SCALES / 4) + pg * 4) = make_float4(f.x, f.z, f.y, 0.f);
-      }
-      {  // unit u: k-steps 2 u and 2 u + 1 of key blocks 0 and 1
-        const uint32_t base = smem_u32(sk + (st & 1) * C::K_BYTES) + pg * (16 * 128);
-        uint32_t c[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) c[k] = base + col(k);
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const int k = (u & 1) * 4, at = (u >> 1) * (kChunk8 * 128);
-          put(c[k] + at, c[k + 1] + at, w[u].x);
-          put(c[k] + at + 8 * 128, c[k + 1] + at + 8 * 128, w[u].y);
-          put(c[k + 2] + at, c[k + 3] + at, w[u].z);
-          put(c[k + 2] + at + 8 * 128, c[k + 3] + at + 8 * 128, w[u].w);
-        }
-      }
-      load(ch, true, pid);
-      fence_proxy_async_smem();
-      mbar_arrive(&k_full[st & 1]);
-      if (st >= 2 && !warp_wait(&v_empty[st & 1], (st >> 1) - 1)) break;
-      {  // unit u: dims 32 u .. + 31; this page's 16 keys are columns 2 (page % 4) and + 1 of its key block
-        const uint32_t base = smem_u32(sv + (st & 1) * C::V_BYTES) + (pg >> 2) * (HD * 128);
-        const uint32_t c0 = base + col((pg & 3) * 2), c1 = base + col((pg & 3) * 2 + 1);
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const int at = 32 * u * 128;
-          put(c0 + at, c1 + at, w[u].x);
-          put(c0 + at + 8 * 128, c1 + at + 8 * 128, w[u].y);
-          put(c0 + at + 16 * 128, c1 + at + 16 * 128, w[u].z);
-          put(c0 + at + 24 * 128, c1 + at + 24 * 128, w[u].w);
-        }
-      }
-      pid = pid_next;
-      if (ch < ch1) load(ch + 1, false, pid);
-      fence_proxy_async_smem();
-      mbar_arrive(&v_full[st & 1]);
-      ++st;
-      if (!diag(ch)) continue;
-      // The own pages in bf16, eight tokens at a time, four lanes a token.  The scales
-      // of a token that is not finite are NaN, and its V counts as 0 (its weight is
-      // NaN, or 0 where it is not seen).
-      const int page = ch * kChunkPages + pg;
-      const bool in = pg >= lo16(ch) && pg < hi16(ch);
-      const int phys = in ? a.open_table[static_cast<size_t>(b) * a.open_stride + page - (cached >> 4)] : 0;
-      float* so = scales + (st & 3) * (C::SCALES / 4);
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        if (st >= 2 && !warp_wait(v ? &v_empty[st & 1] : &k_empty[st & 1], (st >> 1) - 1)) break;
-        const __nv_bfloat16* src = a.open + ((static_cast<size_t>(phys) * 2 + v) * a.Hkv + kvh) * PART + t4 * (HD / 4);
-#pragma unroll 1
-        for (int token = g; in && token < 16; token += 8) {
-          const int key = pg * 16 + token;
-          const bool have = page * 16 + token < kv_len;
-          uint4 y[HD / 32];
-          uint32_t mx = 0u;
-#pragma unroll
-          for (int i = 0; i < HD / 32; ++i)
-            y[i] = have ? __ldcg(reinterpret_cast<const uint4*>(src + token * HD) + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int i = 0; i < HD / 32; ++i)
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
-                                       __vmaxu2(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu)));
-          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int e = kv8_exp(kv8_max_halves(mx));
-          const float up = kv8_up(e);
-          if (t4 == 0) {
-            if (v == 0) {
-              so[key] = e == 255 ? kv8_nan() : kv8_down(e);
-            } else {
-              so[kChunk8 + key] = e == 255 ? kv8_nan() : kv8_log2_down(e);
-              so[2 * kChunk8 + key] = up;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < HD / 32; ++i) {
-            const uint32_t x[4] = {kv8_to_f16(y[i].x, up), kv8_to_f16(y[i].y, up), kv8_to_f16(y[i].z, up), kv8_to_f16(y[i].w, up)};
-            const int d = t4 * (HD / 4) + i * 8;  // dims d .. d + 7
-            if (v == 0) {
-              *reinterpret_cast<uint4*>(sk + (st & 1) * C::K_BYTES + (d >> 6) * (kChunk8 * 128) + key * 128 +
-                                        ((((d >> 3) & 7) ^ (key & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-            } else {
-              uint8_t* to = sv + (st & 1) * C::V_BYTES + (key >> 6) * (HD * 128) + (key & 7) * 2 + d * 128;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)  // (d % 8 = 0)
-                *reinterpret_cast<uint16_t*>(to + k * 128 + ((((key >> 3) & 7) ^ k) << 4)) =
-                    e == 255 ? static_cast<uint16_t>(0) : static_cast<uint16_t>(x[k >> 1] >> (16 * (k & 1)));
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(v ? &v_full[st & 1] : &k_full[st & 1]);
-      }
-      ++st;
+      for (int ch = ch0; ok && ch <= ch1; ++ch) ok = stage(image0 + ch) && (!diag(ch) || stage(own_image + ch));
     }
   } else {
     // ---- softmax: two threads per row, of which thread h takes pages 4 h .. + 3 of a chunk and half of O's dims
-    regs_inc<168>();
+    regs_inc<216>();
     constexpr int HP = kChunkPages / C::NT, OD = HD / C::NT;
-    const int h = (warp - 12) >> 2, lr = (warp & 3) * 32 + lane, row = r0 + lr;
+    const int h = (warp - 4) >> 2, lr = (warp & 3) * 32 + lane, row = r0 + lr;
     const bool valid = row < r_end;
     const int tok = valid ? row / G : 0, hq = kvh * G + (valid ? row % G : 0);
     const int pos = valid ? cached + tok : -1, own = pos >> 4;
@@ -500,7 +519,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
     for (int i = 0; i < OD / 2; ++i) O[i] = 0ull;
     // The block's totals over the splits before (runs that hold all of them).
     float4* totals = a.totals && d1.w >= 0 ? a.totals + (static_cast<size_t>(d1.w) * a.Hkv + kvh) * (C::ROWS * HD / 4) : nullptr;
-    const int sthread = threadIdx.x - 384;
+    const int sthread = threadIdx.x - 128;
     bool have = false;
     rec_tot[sthread] = make_float2(0.f, 0.f);
     int st = 0, n16 = 0;
@@ -584,7 +603,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
               a.part_ml[base * 2] = r.z;
               a.part_ml[base * 2 + 1] = Ls;
             }
-            float4* buf = reinterpret_cast<float4*>(so_out) + (warp - 12) * 256;  // [row][8], the 16-byte words XORed with the row
+            float4* buf = reinterpret_cast<float4*>(so_out) + (warp - 4) * 256;  // [row][8], the 16-byte words XORed with the row
             const unsigned rows_seen = __ballot_sync(0xffffffffu, sees);
 #pragma unroll
             for (int c = 0; c < OD; c += 32) {
@@ -617,7 +636,6 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
         tc_fence_before();
         mbar_arrive(o_free);
         warp_wait(s16_full, n16++);
-        warp_wait(&v_full[(st + 1) & 1], (st + 1) >> 1);  // (the V scales of the own pages' tokens)
         tc_fence_after();
       }
       st += dg ? 2 : 1;
@@ -730,7 +748,11 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       mbar_arrive(&p_full[it & 1]);
     }
   }
-  // Teardown: issued MMAs finish, then tensor memory is freed.
+  // Teardown: copies land and issued MMAs finish, then tensor memory is freed.
+  if (warp == 1 && lane == 0) {
+    for (int st = max(0, issued_k - 2); st < issued_k; ++st) drain_wait(&k_full[st & 1], (st >> 1) & 1);
+    for (int st = max(0, issued_v - 2); st < issued_v; ++st) drain_wait(&v_full[st & 1], (st >> 1) & 1);
+  }
   if (warp == 0 && lane == 0) drain_wait(mma_done, 0);
   tc_fence_before();
   __syncthreads();
@@ -741,21 +763,27 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
 }
 
 template <int HD, int FMT>
-int launch_attn8_tc_t(const Attn8Args& a, int n_blocks, cudaStream_t s) {
+int launch_attn8_tc_t(const Attn8Args& a, int n_chunks, int n_blocks, cudaStream_t s) {
   using C = Tc8Cfg<HD>;
-  VD_CUDA_TRY(cudaFuncSetAttribute(attn8_tc_kernel<HD, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-  VD_CUDA_TRY(launch_k(attn8_tc_kernel<HD, FMT>, dim3(static_cast<unsigned>(n_blocks) * a.Hkv), dim3(C::THREADS), C::SMEM, s, a));
+  constexpr int kExpandSmem = 1024 + C::IMAGE;
+  VD_CUDA_TRY(cudaFuncSetAttribute(attn8_expand_kernel<HD, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem));
+  VD_CUDA_TRY(launch_k(attn8_expand_kernel<HD, FMT>, dim3(static_cast<unsigned>(n_chunks) * a.Hkv), dim3(256), kExpandSmem, s, a));
+  VD_CUDA_TRY(cudaFuncSetAttribute(attn8_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+  VD_CUDA_TRY(launch_k(attn8_tc_kernel<HD>, dim3(static_cast<unsigned>(n_blocks) * a.Hkv), dim3(C::THREADS), C::SMEM, s, a));
   return VD_OK;
 }
 
 }  // namespace
 
-int launch_attention8_tc(const Attn8Args& a, int hd, int format, int n_blocks, cudaStream_t s) {
+size_t attn8_image_bytes(int hd) { return hd == 64 ? Tc8Cfg<64>::IMAGE : Tc8Cfg<128>::IMAGE; }
+
+int launch_attention8_tc(const Attn8Args& a, int hd, int format, int n_chunks, int n_blocks, cudaStream_t s) {
   if (n_blocks <= 0) return VD_OK;
+  const bool i8 = format == VD_KV8_INT8;
   if (hd == 64)
-    return format == VD_KV8_INT8 ? launch_attn8_tc_t<64, kKv8Int8>(a, n_blocks, s) : launch_attn8_tc_t<64, kKv8E4m3>(a, n_blocks, s);
+    return i8 ? launch_attn8_tc_t<64, kKv8Int8>(a, n_chunks, n_blocks, s) : launch_attn8_tc_t<64, kKv8E4m3>(a, n_chunks, n_blocks, s);
   if (hd == 128)
-    return format == VD_KV8_INT8 ? launch_attn8_tc_t<128, kKv8Int8>(a, n_blocks, s) : launch_attn8_tc_t<128, kKv8E4m3>(a, n_blocks, s);
+    return i8 ? launch_attn8_tc_t<128, kKv8Int8>(a, n_chunks, n_blocks, s) : launch_attn8_tc_t<128, kKv8E4m3>(a, n_chunks, n_blocks, s);
   return fail(VD_ERR_UNSUPPORTED, "the tcgen05 kernel of the 8-bit cache takes head_dim 64 or 128");
 }
 

@@ -239,9 +239,11 @@ struct Attn8Args {
   float* part_ml;           // [T][Hq][max_splits][2]
   const int* page_table;    // [B][pt_stride] pages of the cache
   const int* open_table;    // [B][open_stride] pages of the bf16 pool, from logical page cached_len / 16 on
-  const int4* items;        // [blocks][2]: request, first token, tokens, cached tokens; split, first row; and for
+  const int4* items;        // [blocks][2]: request (tcgen05: its first image), first token, tokens, cached tokens; split, first row; and for
                             // the tcgen05 kernel, whose blocks take several: end of the splits, the block's number
                             // among those whose splits it folds itself (-1: it leaves partials)
+  const int4* chunks;       // [chunks][2]: request, chunk, image, 1: the image of its own pages; cached, all tokens, 0, 0
+  uint8_t* images;          // [images][Hkv] attn8_image_bytes()
   float4* totals;           // [such blocks][Hkv][128 rows x hd floats]
   __nv_bfloat16* out;       // [T][Hq][hd] (their rows)
   const __nv_bfloat16* open;  // the layer's first page of the bf16 pool
@@ -260,7 +262,8 @@ struct Attn8Args {
 int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int format, bool lower8, int n_blocks,
                       cudaStream_t s);
 // The same rows in blocks of 128 on tcgen05, head dimensions 64 and 128.
-int launch_attention8_tc(const Attn8Args& a, int hd, int format, int n_blocks, cudaStream_t s);
+int launch_attention8_tc(const Attn8Args& a, int hd, int format, int n_chunks, int n_blocks, cudaStream_t s);
+size_t attn8_image_bytes(int hd);  // a chunk of 128 keys of one KV head, expanded
 // Sealing and its reverse, page copies (kv8.cu).  Pairs of page ids: `dev` on the
 // device (a plan's), or else in the launch's own arguments.
 constexpr int kPagePairs = 448;

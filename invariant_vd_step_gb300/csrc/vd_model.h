@@ -73,6 +73,8 @@ struct Desc {
   int items[4] = {}, n_items[4] = {};    // attention blocks: decode class, others; the same for local layers
   int seal = 0, n_seal = 0;              // offset of the (bf16 page, cache page) pairs that the step seals
   int open_table = 0, open_stride = 0;   // pages of the bf16 pool, per request
+  int chunks[2] = {}, n_chunks[2] = {};  // chunks that the tcgen05 blocks of global, of local layers read
+  uint8_t* images = nullptr;             // and their images
   float4* totals = nullptr;              // of the blocks that fold their splits themselves
   int merge_list = 0, n_merge_kv8[2] = {};  // tokens whose splits the merge kernel folds: on global, on local layers
   int own_slots = 1;                     // bf16 pages that a decode-class block can hold
