@@ -7,6 +7,7 @@
 #include <new>
 #include <string>
 #include <unordered_set>
+#include <utility>
 #include <vector>
 
 #include "vd_internal.h"
@@ -52,11 +53,6 @@ struct vd_kv8_plan {
 };
 
 namespace {
-
-// Runs of splits per SM that the tcgen05 blocks are cut into, if they have as many.
-constexpr int kRunsPerSM = 12;
-// Blocks per SM from which they are not cut.
-constexpr int kDirectPerSM = 2;
 
 int check_device(const vd_model* m) {
   int dev = -1;
@@ -285,40 +281,51 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       n_images += 2 * all - cached / 128;
       if (n_images * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
     }
+  // Of the tcgen05 row blocks, as many as fill the SMs in whole rounds take all of
+  // their splits and need no merge; those of the last, partial round are cut into
+  // runs of splits, so that it takes less of a round.  (A token's heads are in one
+  // block, or the cut moves back to where they are.)
   size_t total_blocks = 0;  // most blocks of a layer that fold their splits themselves
-  bool direct[2] = {false, false};
-  for (int local = 0; local <= (windowed ? 1 : 0); ++local)
-    for (int pre = 0; pre < 2; ++pre) {
-      const bool tc = pre && d.pre_tc;
-      const int step = tc ? 128 : 16;
-      std::vector<int>& to = blocks[2 * local + pre];
-      long long units = 0, row_blocks = 0;
-      for (int pass = 0; pass < 2; ++pass) {  // the (row block, split) pairs are counted, then dealt out
-        // Blocks that alone fill the SMs take all of their splits; fewer are cut
-        // into runs of splits.
-        direct[local] = tc && row_blocks * c.n_kv_heads >= static_cast<long long>(kDirectPerSM) * m->n_sm;
-        const int run = !tc ? 1 : direct[local] ? 1 << 30 : static_cast<int>(std::max(1LL, units * c.n_kv_heads / (kRunsPerSM * m->n_sm)));
-        int n_direct = 0;
-        for (int i = 0; i < B; ++i) {
-          const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i], rows = ql * m->G;
-          if ((rows > 16) != (pre == 1)) continue;
-          for (int r0 = 0; r0 < rows; r0 += step) {
-            const int first = local ? std::max(0, cached + r0 / m->G - c.sliding_window + 1) / kAttn8Split : 0;
-            const int end = (cached + (std::min(rows, r0 + step) - 1) / m->G) / kAttn8Split + 1;
-            if (!pass) {
-              units += end - first;
-              ++row_blocks;
-              continue;
-            }
-            const int n = end - first, parts = (n - 1) / run + 1;  // runs of like lengths
-            for (int k = 0; k < parts; ++k)
-              to.insert(to.end(), {tc ? image0[i] : i, b->cu_q[i], ql, cached, first + n * k / parts, r0, first + n * (k + 1) / parts,
-                                   direct[local] ? n_direct++ : -1});
-          }
-        }
-        total_blocks = std::max(total_blocks, static_cast<size_t>(n_direct));
+  std::vector<int> merge[2];  // tokens that the merge kernel folds
+  for (int local = 0; local <= (windowed ? 1 : 0); ++local) {
+    auto splits_of = [&](int i, int r0, int step, int* first) {
+      const int cached = b->cached_len[i], rows = (b->cu_q[i + 1] - b->cu_q[i]) * m->G;
+      *first = local ? std::max(0, cached + r0 / m->G - c.sliding_window + 1) / kAttn8Split : 0;
+      return (cached + (std::min(rows, r0 + step) - 1) / m->G) / kAttn8Split + 1 - *first;
+    };
+    std::vector<std::pair<int, int>> rb;  // (request, first row) of the row blocks
+    for (int i = 0; i < B; ++i) {
+      const int q0 = b->cu_q[i], ql = b->cu_q[i + 1] - q0, cached = b->cached_len[i], rows = ql * m->G;
+      if (rows > 16 && d.pre_tc) {
+        for (int r0 = 0; r0 < rows; r0 += 128) rb.emplace_back(i, r0);
+        continue;
+      }
+      for (int k = 0; k < ql; ++k) merge[local].push_back(q0 + k);
+      std::vector<int>& to = blocks[2 * local + (rows > 16)];
+      for (int r0 = 0; r0 < rows; r0 += 16) {
+        int first;
+        const int n = splits_of(i, r0, 16, &first);
+        for (int k = 0; k < n; ++k) to.insert(to.end(), {i, q0, ql, cached, first + k, r0, 0, 0});
       }
     }
+    const int n_rb = static_cast<int>(rb.size()), Hkv = c.n_kv_heads;
+    int direct = static_cast<int>(static_cast<long long>(n_rb) * Hkv / m->n_sm * m->n_sm / Hkv);
+    while (direct < n_rb && direct > 0 && rb[direct].second % m->G) --direct;
+    // runs that the others are cut into: as many as SMs
+    const int parts_of = n_rb > direct ? std::max(1, m->n_sm / ((n_rb - direct) * Hkv)) : 1;
+    for (int j = 0; j < n_rb; ++j) {
+      const int i = rb[j].first, r0 = rb[j].second, q0 = b->cu_q[i], ql = b->cu_q[i + 1] - q0, rows = ql * m->G;
+      int first;
+      const int n = splits_of(i, r0, 128, &first), parts = j < direct ? 1 : std::min(parts_of, n);
+      for (int k = 0; k < parts; ++k)
+        blocks[2 * local + 1].insert(blocks[2 * local + 1].end(),
+                                     {image0[i], q0, ql, b->cached_len[i], first + n * k / parts, r0, first + n * (k + 1) / parts,
+                                      parts == 1 && j < direct ? j : -1});
+      if (j >= direct)  // the tokens whose first head is in the block
+        for (int t0 = (r0 + m->G - 1) / m->G; t0 * m->G < std::min(rows, r0 + 128); ++t0) merge[local].push_back(q0 + t0);
+    }
+    total_blocks = std::max(total_blocks, static_cast<size_t>(direct));
+  }
   for (int k = 0; k < 4; ++k) {  // int4, then int2: first, for their alignment
     if (blocks[k].size() / 8 * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
     d.items[k] = take(blocks[k].size());
@@ -334,7 +341,10 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   d.positions = take(T);
   d.slot_page = take(T);
   d.logit_rows = take(R);
-  d.merge_list = take(T);
+  for (int k = 0; k < 2; ++k) {
+    d.merge_list[k] = take(merge[k].size());
+    d.n_merge_kv8[k] = static_cast<int>(merge[k].size());
+  }
   d.open_stride = open_stride;
   d.open_table = take(static_cast<size_t>(B) * open_stride);
   d.page_table = take(static_cast<size_t>(B) * stride);
@@ -362,7 +372,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       (rc = grow(&t->tot, &t->tot_cap, tot)) || (rc = grow(&t->images, &t->images_cap, images)))
     return rc;
   int* h = t->host[slot];
-  int ns = 0, n_listed = 0;
+  int ns = 0;
   for (int i = 0; i < B; ++i) {
     const int q0 = b->cu_q[i], ql = b->cu_q[i + 1] - q0, cached = b->cached_len[i], first = cached / 16;
     const int full = (cached + ql) / 16, open = (cached + ql + 15) / 16 - first;
@@ -376,8 +386,6 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       h[d.seal + 2 * ns] = h[d.open_table + static_cast<size_t>(i) * open_stride + j - first];
       h[d.seal + 2 * ns + 1] = h[d.page_table + static_cast<size_t>(i) * stride + j];
     }
-    if (ql * m->G <= 16)  // the decode class first
-      for (int k = 0; k < ql; ++k) h[d.merge_list + n_listed++] = q0 + k;
     for (int k = 0; k < ql; ++k) {
       h[d.tokens + q0 + k] = b->token_ids ? b->token_ids[q0 + k] : 0;
       h[d.positions + q0 + k] = cached + k;
@@ -387,10 +395,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   for (int k = 0; k < 4; ++k) std::copy(blocks[k].begin(), blocks[k].end(), h + d.items[k]);
   for (int k = 0; k < 2; ++k) std::copy(chunks[k].begin(), chunks[k].end(), h + d.chunks[k]);
   for (int j = 0; j < R; ++j) h[d.logit_rows + j] = b->logit_rows[j];
-  for (int local = 0; local < 2; ++local) d.n_merge_kv8[local] = direct[local] ? n_listed : T;
-  for (int i = 0; i < B; ++i)
-    if ((b->cu_q[i + 1] - b->cu_q[i]) * m->G > 16)
-      for (int k = b->cu_q[i]; k < b->cu_q[i + 1]; ++k) h[d.merge_list + n_listed++] = k;
+  for (int k = 0; k < 2; ++k) std::copy(merge[k].begin(), merge[k].end(), h + d.merge_list[k]);
   d.totals = reinterpret_cast<float4*>(t->tot);
   d.images = t->images;
   d.base = t->dev;
@@ -461,7 +466,7 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
   const int n_merge = d.n_merge_kv8[a.window > 0];
   if (n_merge == 0) return VD_OK;  // every row's splits were folded by its block
   MergeArgs g{};
-  g.tokens = n_merge < d.T ? d.base + d.merge_list : nullptr;
+  g.tokens = n_merge < d.T ? d.base + d.merge_list[a.window > 0] : nullptr;
   g.part_o = d.part_o;
   g.part_ml = d.part_ml;
   g.out = out;

@@ -118,6 +118,16 @@ __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -480,30 +490,34 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
     const int tok = valid ? row / G : 0, hq = kvh * G + (valid ? row % G : 0);
     const int pos = valid ? cached + tok : -1, own = pos >> 4;
     const int lo = valid ? (a.window > 0 ? max(0, pos - a.window + 1) : 0) : 1;
-    float rowfac;
-    {  // the row's query -> [hd block][row][64] fp16, 128-byte swizzle; each thread half of it
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD);
-      uint32_t mx = 0u;
+    {  // the queries -> [hd block][row][64] fp16, 128-byte swizzle: 16 bytes per lane, whole rows per instruction
+      constexpr int LPR = HD / 8, RPI = 32 / LPR;  // lanes of a row, rows of a warp's instruction
+      const int w8 = warp - 4, c = lane % LPR;
+      uint4 x[16 / RPI];
 #pragma unroll
-      for (int i = 0; i < HD / 8; ++i) {
-        const uint4 x = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+      for (int k = 0; k < 16 / RPI; ++k) {
+        const int rr = r0 + w8 * 16 + k * RPI + lane / LPR;
+        x[k] = rr < r_end ? reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(q0 + rr / G) * a.Hq + kvh * G + rr % G) * HD)[c]
+                          : make_uint4(0u, 0u, 0u, 0u);
       }
-      const int e = kv8_exp(kv8_max_halves(mx));
-      const float up = kv8_up(e);
-      rowfac = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
 #pragma unroll
-      for (int k = 0; k < HD / 8 / C::NT; ++k) {
-        const int i = h * (HD / 8 / C::NT) + k;
-        const uint4 x = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(sq + (i >> 3) * (C::ROWS * 128) + lr * 128 + (((i & 7) ^ (lr & 7)) << 4)) =
-            make_uint4(kv8_to_f16(x.x, up), kv8_to_f16(x.y, up), kv8_to_f16(x.z, up), kv8_to_f16(x.w, up));
+      for (int k = 0; k < 16 / RPI; ++k) {
+        const int rl = w8 * 16 + k * RPI + lane / LPR;
+        uint32_t mx = __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu), __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
+#pragma unroll
+        for (int d = 1; d < LPR; d *= 2) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const int e = kv8_exp(kv8_max_halves(mx));
+        const float up = kv8_up(e);
+        if (c == 0) ex_l[0][rl] = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
+        *reinterpret_cast<uint4*>(sq + (c >> 3) * (C::ROWS * 128) + rl * 128 + (((c & 7) ^ (rl & 7)) << 4)) =
+            make_uint4(kv8_to_f16(x[k].x, up), kv8_to_f16(x[k].y, up), kv8_to_f16(x[k].z, up), kv8_to_f16(x[k].w, up));
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     }
+    bool ok = softmax_sync(true);
+    const float rowfac = ex_l[0][lr];
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    bool ok = true;
     auto warp_wait = [&](uint64_t* f, int n) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(f, n & 1, abort_flag, a.status));
       return ok;
@@ -530,6 +544,8 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       const bool scored = ch <= ch1;
       // O of chunk ch - 2 is there with the scores of ch, which were issued behind
       // its P V; behind the last chunk there is the end of all MMAs.
+      const int pc = ch - 2, sp = pc >> 2;  // the chunk that is folded now
+      const bool split_end = (pc & 3) == 3 || pc == ch1;
       warp_wait(scored ? &s_full[it & 1] : mma_done, scored ? it >> 1 : 0);
       tc_fence_after();
       if (it >= 2) {
@@ -545,8 +561,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
           for (int i = 0; i < W / 2; ++i) O[c / 2 + i] = f2_fma(O[c / 2 + i], al, f2(y[2 * i], y[2 * i + 1]));
         }
         L = __fmaf_rn(L, r.x, r.y);
-        const int pc = ch - 2, sp = pc >> 2;
-        if ((pc & 3) == 3 || pc == ch1) {  // its split's last
+        if (split_end) {
           ex_l[h][lr] = L;
           ok = softmax_sync(ok);
           if (!ok) break;
@@ -642,6 +657,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       // every row of the warp sees this half in 8 bits (rows that are none aside)
       const bool full = __all_sync(0xffffffffu, !valid || (lo <= pg0 * 16 && own >= pg0 + HP));
       float t[HP * 16];
+      float iv[HP];
 #pragma unroll
       for (int p0 = 0; p0 < HP; p0 += 2) {
         uint32_t x[32];
@@ -652,6 +668,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
           const float4 f = sc[pg];
           const float ks = __fmul_rn(f.x, rowfac);
           const uint64_t k2 = f2(ks, ks), lv2 = f2(f.y, f.y);
+          iv[pg] = f.z;
 #pragma unroll
           for (int i = pg * 16; i < pg * 16 + 16; i += 2) {
             const uint64_t s2 = f2_fma(f2(x[i - 16 * p0], x[i - 16 * p0 + 1]), k2, lv2);
@@ -699,47 +716,44 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       const float u = M == -INFINITY ? 0.f : M;  // no key seen so far: every score is -inf, every weight 0
       const uint64_t u2 = f2(u, u);
       uint64_t l[4] = {0ull, 0ull, 0ull, 0ull};  // pair t: the partial sums (t, 0) and (t, 1)
+      uint32_t pk[HP * 8];
 #pragma unroll
-      for (int pg = 0; pg < HP; ++pg) {
-        const float iv = sc[pg].z;
-        const uint64_t iv2 = f2(iv, iv);
-        const int page = pg0 + pg;
-        const uint32_t at = s_at + 8 * (h * HP + pg);
-        const bool own16 = dg && page >= own_lo && page <= own_hi;
-        uint32_t pk[8];
+      for (int i = 0; i < HP * 8; ++i) {
+        const uint64_t s2 = f2_sub(f2(t[2 * i], t[2 * i + 1]), u2);
+        t[2 * i] = ex2(f2_lo(s2));
+        t[2 * i + 1] = ex2(f2_hi(s2));
+        pk[i] = pack_f16x2(t[2 * i], t[2 * i + 1]);
+        if (full) l[i & 3] = f2_fma(f2(t[2 * i], t[2 * i + 1]), f2(iv[i >> 3], iv[i >> 3]), l[i & 3]);
+      }
+      if (!full) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint64_t s2 = f2_sub(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]), u2);
-          t[pg * 16 + 2 * i] = ex2(f2_lo(s2));
-          t[pg * 16 + 2 * i + 1] = ex2(f2_hi(s2));
-          pk[i] = pack_f16x2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]);
-        }
-        if (full) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) l[i & 3] = f2_fma(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]), iv2, l[i & 3]);
-          st8(at, pk);
-          if (own16) {  // other rows' own page
-            const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            st8(at + 64, zero);
-          }
-        } else {
+        for (int pg = 0; pg < HP; ++pg) {
+          const int page = pg0 + pg;
           const bool mine = page == own;
           if ((page < own || mine) && page * 16 + 15 >= lo) {  // (a page that the row does not see stays out, whatever its scale)
             const float* up = so + 2 * kChunk8 + pg * 16;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              l[i & 3] = f2_fma(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]), mine ? f2(up[2 * i], up[2 * i + 1]) : iv2, l[i & 3]);
+              l[i & 3] = f2_fma(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]),
+                                mine ? f2(up[2 * i], up[2 * i + 1]) : f2(iv[pg], iv[pg]), l[i & 3]);
           }
-          uint32_t p8[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            p8[i] = mine ? 0u : pk[i];
-            pk[i] = mine ? pk[i] : 0u;
-          }
-          st8(at, p8);
-          if (own16) st8(at + 64, pk);
         }
       }
+      if (dg) {  // the weights of own pages, 0 for the other rows, and 0 for them among the 8-bit pages
+#pragma unroll
+        for (int pg = 0; pg < HP; ++pg) {
+          const int page = pg0 + pg;
+          if (page < own_lo || page > own_hi) continue;
+          uint32_t p16[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            p16[i] = page == own ? pk[pg * 8 + i] : 0u;
+            pk[pg * 8 + i] = page == own ? 0u : pk[pg * 8 + i];
+          }
+          st8(s_at + 64 + 8 * (h * HP + pg), p16);
+        }
+      }
+      st32(s_at + 8 * HP * h, pk);
       const float l_ch = __fadd_rn(__fadd_rn(__fadd_rn(f2_lo(l[0]), f2_hi(l[0])), __fadd_rn(f2_lo(l[1]), f2_hi(l[1]))),
                                    __fadd_rn(__fadd_rn(f2_lo(l[2]), f2_hi(l[2])), __fadd_rn(f2_lo(l[3]), f2_hi(l[3]))));
       rec[(it & 1) * C::NS + sthread] = make_float4(alpha, l_ch, M, 0.f);

@@ -76,7 +76,7 @@ struct Desc {
   int chunks[2] = {}, n_chunks[2] = {};  // chunks that the tcgen05 blocks of global, of local layers read
   uint8_t* images = nullptr;             // and their images
   float4* totals = nullptr;              // of the blocks that fold their splits themselves
-  int merge_list = 0, n_merge_kv8[2] = {};  // tokens whose splits the merge kernel folds: on global, on local layers
+  int merge_list[2] = {}, n_merge_kv8[2] = {};  // tokens whose splits the merge kernel folds: on global, on local layers
   int own_slots = 1;                     // bf16 pages that a decode-class block can hold
   bool lower8 = false;                   // every decode-class block has at most 8 rows
 };
