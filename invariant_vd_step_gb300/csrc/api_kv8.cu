@@ -33,6 +33,7 @@ struct vd_kv8 {
 struct vd_kv8_plan {
   vd_model* m = nullptr;
   int device = 0, max_tokens = 0;
+  int prefill = 0;  // vd_kv8_set_prefill
   // the plan in force
   Desc d;
   unsigned long long pool_id = 0, cache_id = 0;
@@ -256,31 +257,49 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     off += n;
     return static_cast<int>(o);
   };
-  // Attention blocks: 16 rows and a split for decode-shaped requests, 128 rows and
-  // a run of splits on tcgen05 for the others (16 rows and a split where that kernel
-  // does not go); for global layers and, without the splits that the window hides,
-  // for local ones.
-  std::vector<int> blocks[4];
+  // Attention blocks: 16 rows and a split on mma.sync for decode-shaped requests
+  // and short chunks, 128 rows and a run of splits on tcgen05 for the rest; for
+  // global layers and, without the splits that the window hides, for local ones.
+  std::vector<int> blocks[6];
   const bool windowed = c.sliding_window > 0 && c.local_global_period > 0;
-  d.pre_tc = m->prefill_kernel == 0 && c.head_dim <= 128;
+  std::vector<unsigned char> tc(B, 0);
+  if (m->prefill_kernel == 0 && t->prefill != 1 && c.head_dim <= 128) {
+    // What a chunk's (row block, KV head, 128 keys) units cost, in us at head dim 128:
+    // 0.0095 for each of 16 rows on mma.sync; on tcgen05 0.02 for each of 128 rows and
+    // as much for the keys' image, and 9 more for the launch.  (Sweep of 48 shapes, 1
+    // to 32 requests of 5 to 1024 tokens behind 0 to 8000: 1 x 64 behind 1000, 32 heads
+    // over 8, 18 against 23 us; 1 x 512 behind 0 42 against 26; 32 x 8 behind 500 to
+    // 4000 99 against 184; 9 x 77 behind up to 2500 171 against 87.)
+    double gain = 0;
+    for (int i = 0; i < B; ++i) {
+      const int ql = b->cu_q[i + 1] - b->cu_q[i], rows = ql * m->G, all = (b->cached_len[i] + ql + 127) / 128;
+      const int seen = windowed && c.local_global_period > c.n_layers ? std::min(all, (c.sliding_window + ql + 127) / 128) : all;
+      const double unit = seen * c.n_kv_heads * (c.head_dim / 128.0);
+      const double more = unit * (0.0095 * ((rows + 15) / 16) - 0.02 * ((rows + 127) / 128 + 1));
+      if (rows > 16 && (more > 0 || t->prefill == 2)) {
+        tc[i] = 1;
+        gain += more;
+      }
+    }
+    if (gain < 9 && t->prefill == 0) std::fill(tc.begin(), tc.end(), 0);
+  }
   // The tcgen05 blocks' requests have images of their chunks: of chunk 0 on, then of
   // those that hold own pages, numbered one request after the other.
   std::vector<int> image0(B, 0), chunks[2];
   long long n_images = 0;
-  if (d.pre_tc)
-    for (int i = 0; i < B; ++i) {
-      const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i], kv = cached + ql, all = (kv + 127) / 128;
-      if (ql * m->G <= 16) continue;
-      image0[i] = static_cast<int>(n_images);
-      for (int local = 0; local <= (windowed ? 1 : 0); ++local) {
-        const int first = local ? std::max(0, cached - c.sliding_window + 1) / 128 : 0;
-        for (int ch = first; ch < all; ++ch) chunks[local].insert(chunks[local].end(), {i, ch, image0[i] + ch, 0, cached, kv, 0, 0});
-        for (int ch = cached / 128; ch < all; ++ch)
-          chunks[local].insert(chunks[local].end(), {i, ch, image0[i] + all + ch - cached / 128, 1, cached, kv, 0, 0});
-      }
-      n_images += 2 * all - cached / 128;
-      if (n_images * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
+  for (int i = 0; i < B; ++i) {
+    const int ql = b->cu_q[i + 1] - b->cu_q[i], cached = b->cached_len[i], kv = cached + ql, all = (kv + 127) / 128;
+    if (!tc[i]) continue;
+    image0[i] = static_cast<int>(n_images);
+    for (int local = 0; local <= (windowed ? 1 : 0); ++local) {
+      const int first = local ? std::max(0, cached - c.sliding_window + 1) / 128 : 0;
+      for (int ch = first; ch < all; ++ch) chunks[local].insert(chunks[local].end(), {i, ch, image0[i] + ch, 0, cached, kv, 0, 0});
+      for (int ch = cached / 128; ch < all; ++ch)
+        chunks[local].insert(chunks[local].end(), {i, ch, image0[i] + all + ch - cached / 128, 1, cached, kv, 0, 0});
     }
+    n_images += 2 * all - cached / 128;
+    if (n_images * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
+  }
   // Of the tcgen05 row blocks, as many as fill the SMs in whole rounds take all of
   // their splits and need no merge; those of the last, partial round are cut into
   // runs of splits, so that it takes less of a round.  (A token's heads are in one
@@ -296,12 +315,12 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     std::vector<std::pair<int, int>> rb;  // (request, first row) of the row blocks
     for (int i = 0; i < B; ++i) {
       const int q0 = b->cu_q[i], ql = b->cu_q[i + 1] - q0, cached = b->cached_len[i], rows = ql * m->G;
-      if (rows > 16 && d.pre_tc) {
+      if (tc[i]) {
         for (int r0 = 0; r0 < rows; r0 += 128) rb.emplace_back(i, r0);
         continue;
       }
       for (int k = 0; k < ql; ++k) merge[local].push_back(q0 + k);
-      std::vector<int>& to = blocks[2 * local + (rows > 16)];
+      std::vector<int>& to = blocks[3 * local + (rows > 16)];
       for (int r0 = 0; r0 < rows; r0 += 16) {
         int first;
         const int n = splits_of(i, r0, 16, &first);
@@ -318,7 +337,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       int first;
       const int n = splits_of(i, r0, 128, &first), parts = j < direct ? 1 : std::min(parts_of, n);
       for (int k = 0; k < parts; ++k)
-        blocks[2 * local + 1].insert(blocks[2 * local + 1].end(),
+        blocks[3 * local + 2].insert(blocks[3 * local + 2].end(),
                                      {image0[i], q0, ql, b->cached_len[i], first + n * k / parts, r0, first + n * (k + 1) / parts,
                                       parts == 1 && j < direct ? j : -1});
       if (j >= direct)  // the tokens whose first head is in the block
@@ -326,7 +345,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     }
     total_blocks = std::max(total_blocks, static_cast<size_t>(direct));
   }
-  for (int k = 0; k < 4; ++k) {  // int4, then int2: first, for their alignment
+  for (int k = 0; k < 6; ++k) {  // int4, then int2: first, for their alignment
     if (blocks[k].size() / 8 * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
     d.items[k] = take(blocks[k].size());
     d.n_items[k] = static_cast<int>(blocks[k].size() / 8);
@@ -392,7 +411,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       h[d.slot_page + q0 + k] = h[d.open_table + static_cast<size_t>(i) * open_stride + (cached + k) / 16 - first];
     }
   }
-  for (int k = 0; k < 4; ++k) std::copy(blocks[k].begin(), blocks[k].end(), h + d.items[k]);
+  for (int k = 0; k < 6; ++k) std::copy(blocks[k].begin(), blocks[k].end(), h + d.items[k]);
   for (int k = 0; k < 2; ++k) std::copy(chunks[k].begin(), chunks[k].end(), h + d.chunks[k]);
   for (int j = 0; j < R; ++j) h[d.logit_rows + j] = b->logit_rows[j];
   for (int k = 0; k < 2; ++k) std::copy(merge[k].begin(), merge[k].end(), h + d.merge_list[k]);
@@ -452,15 +471,16 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
   a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(c.head_dim)));
   a.status = m->status;
   int rc;
-  for (int cls = 0; cls < 2; ++cls) {  // decode-shaped requests, then the others
-    const int k = cls + (a.window > 0 ? 2 : 0);
+  const int local = a.window > 0;
+  for (int cls = 0; cls < 3; ++cls) {
+    const int k = 3 * local + cls;
     if (d.n_items[k] == 0) continue;
     Prof p(m, K_ATTN, s);
+    p.kernels = cls == 2 ? 2 : 1;
     a.items = reinterpret_cast<const int4*>(d.base + d.items[k]);
     a.own_slots = cls ? 2 : d.own_slots;
-    p.kernels = cls && d.pre_tc ? 2 : 1;
-    if ((rc = cls && d.pre_tc ? launch_attention8_tc(a, c.head_dim, d.kv8->format, d.n_chunks[k >> 1], d.n_items[k], s)
-                              : launch_attention8(pool->map, a, c.head_dim, d.kv8->format, !cls && d.lower8, d.n_items[k], s)))
+    if ((rc = cls == 2 ? launch_attention8_tc(a, c.head_dim, d.kv8->format, d.n_chunks[local], d.n_items[k], s)
+                       : launch_attention8(pool->map, a, c.head_dim, d.kv8->format, !cls && d.lower8, d.n_items[k], s)))
       return rc;
   }
   const int n_merge = d.n_merge_kv8[a.window > 0];
@@ -588,6 +608,13 @@ int vd_kv8_plan_make(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, const vd_kv8_b
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (const int rc = check_call(p, c, pool, s)) return rc;
   return guarded([&] { return make_plan(p, c, pool, b, s); });
+}
+
+int vd_kv8_set_prefill(vd_kv8_plan* p, int32_t kernel) {
+  if (!p) return fail(VD_ERR_INVALID_ARG, "null plan");
+  if (kernel < 0 || kernel > 2) return fail(VD_ERR_INVALID_ARG, "kernel must be 0, 1 or 2");
+  p->prefill = kernel;
+  return VD_OK;
 }
 
 int vd_op_kv8_rope_kv(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, int32_t layer, const void* qkv, void* q_out,

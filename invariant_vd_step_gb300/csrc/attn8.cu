@@ -40,24 +40,32 @@ constexpr int kSplit8 = 512;   // keys of a split
 constexpr int kChunk8 = 128;   // keys of a chunk
 constexpr int kChunkPages = kChunk8 / 16;
 
-// LOWER8: the block holds at most 8 rows (a lane's second row is none).
-template <int HD, bool LOWER8>
+// NB: the block's rows in groups of 8 (1 or 2).  Keys, and for P V the dims, are
+// the M of the products and the rows their N, so that a block of few rows (4 per
+// token at four heads per KV head) leaves little of them empty.
+template <int HD, int NB>
 struct Attn8Cfg {
   static constexpr int PART = Kv8Cfg<HD>::PART;
-  static constexpr int SL = LOWER8 ? 3 : 4;         // copies in flight per warp
-  static constexpr int NR = LOWER8 ? 1 : 2;         // rows per lane
+  static constexpr int SL = NB == 1 ? 3 : 4;        // copies in flight per warp
   static constexpr int OWN = 2 * 32 * HD;           // K and V of one bf16 page
   static constexpr int RING = SL * PART;            // per warp
-  static constexpr int SC = (kChunkPages + 2) * 32 * NR * 16;  // scores per warp: [page][lane][key block][row, key pair]
-  static_assert(RING >= 8 * NR * HD * 4, "the chunk's O fits the warp's ring");
+  static_assert(RING >= 8 * NB * HD * 4, "the chunk's O, [row][HD], takes the place of the copies");
+  // per warp: the scores, [page][lane][row group]: keys g, g + 8 of rows 2t, 2t + 1
+  static constexpr int SC = (kChunkPages + 2) * 32 * NB * 16;
   static constexpr int smem(int own_slots) { return 1024 + own_slots * OWN + 4 * (RING + SC) + (4 * SL + 2) * 8 + 16; }
 };
 
-template <int HD, int FMT, bool LOWER8>
-__global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {  // an 8 x 8 fragment of fp16
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <int HD, int FMT, int NB>
+__global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
     attn8_kernel(const __grid_constant__ CUtensorMap kvmap, Attn8Args a) {
-  using C = Attn8Cfg<HD, LOWER8>;
-  constexpr int NR = C::NR, SL = C::SL, KK = HD / 16, UNITS = Kv8Cfg<HD>::UNITS;
+  using C = Attn8Cfg<HD, NB>;
+  constexpr int NR = 2 * NB, SL = C::SL, KK = HD / 16, UNITS = Kv8Cfg<HD>::UNITS;  // NR: rows per lane
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -65,12 +73,13 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   uint8_t* own_s = smem;
   uint8_t* ring0 = smem + a.own_slots * C::OWN;
   uint8_t* ring = ring0 + warp * C::RING;
-  float4* score = reinterpret_cast<float4*>(ring0 + 4 * C::RING + warp * C::SC) + lane * NR;  // page i at score[i * 32 * NR]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring0 + 4 * (C::RING + C::SC));
+  uint8_t* score_s = ring0 + 4 * C::RING;
+  float4* score = reinterpret_cast<float4*>(score_s + warp * C::SC) + lane * NB;  // page i at score[i * 32 * NB]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(score_s + 4 * C::SC);
   uint64_t* bar = bars + warp * SL;
   uint64_t* own_bar = bars + 4 * SL;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(own_bar + 2);
-  __shared__ float fold_m[4][8 * NR], fold_l[kChunkParts][4][8 * NR];  // per chunk and row: its largest score, its parts' l
+  __shared__ float fold_m[4][8 * NB], fold_l[kChunkParts][4][8 * NB];  // per chunk and row: its largest score, its parts' l
 
   // Up to the wait for the previous kernel the CTA reads only the status word and
   // the plan (uploaded before the step's first kernel).
@@ -107,7 +116,10 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   if (max(sidx * kSplit8, lo_min) > min(sidx * kSplit8 + kSplit8 - 1, p_max)) return;  // no visible key of these rows
 
   // Copies of this warp: its K pages, then its V pages, copy j into slot j % SL,
-  // issued by the lane that holds the page's id.
+  // issued by the lane that holds the page's id.  (Straight from memory into
+  // registers, which the codes' order allows, with as many bytes in flight, the
+  // kernel took 10 to 25 % longer: the loads of a whole page then have to be
+  // waited for where its first word is used.)
   const uint8_t* page = a.codes + (static_cast<size_t>(pid) * a.Hkv + kvh) * (2 * C::PART);
   auto issue = [&](int j, bool v) {
     uint64_t* f = &bar[j % SL];
@@ -126,42 +138,43 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (lane < n8) sc = __ldcg(a.scales + static_cast<size_t>(pid) * a.Hkv + kvh);
 
-  // ---- this lane's rows g (and g + 8), their queries as fp16 fragments
-  int pos[NR], lo[NR], own[NR];
-  uint32_t qf[KK][4];
+  // ---- the rows' queries as fp16 B fragments (lane: row g of each group), and
+  // what this lane needs of the rows whose scores it gets, 2t and 2t + 1 of each
+  uint32_t qf[KK][NB][2];
   float rowfac[NR];
+  int pos[NR], lo[NR], own[NR];
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int row = r0 + gq + 8 * r;
+  for (int n = 0; n < NB; ++n) {
+    const int row = r0 + 8 * n + gq;
     const bool valid = row < rows;
-    const int tok = row / G, hq = kvh * G + row % G;
-    pos[r] = valid ? cached + tok : -1;
-    own[r] = pos[r] >> 4;  // -1 for a row that is none
-    lo[r] = valid ? (a.window > 0 ? max(0, pos[r] - a.window + 1) : 0) : 1;
-    const __nv_bfloat16* qr = a.q + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD + t4 * 2;
+    const __nv_bfloat16* qr = a.q + (static_cast<size_t>(q0 + row / G) * a.Hq + kvh * G + row % G) * HD + t4 * 2;
     uint32_t mx = 0u;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
-      qf[kk][r] = valid ? *reinterpret_cast<const uint32_t*>(qr + kk * 16) : 0u;
-      qf[kk][2 + r] = valid ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8) : 0u;
+      qf[kk][n][0] = valid ? *reinterpret_cast<const uint32_t*>(qr + kk * 16) : 0u;
+      qf[kk][n][1] = valid ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8) : 0u;
     }
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk)
-      mx = __vmaxu2(mx, __vmaxu2(qf[kk][r] & 0x7fff7fffu, qf[kk][2 + r] & 0x7fff7fffu));
+      mx = __vmaxu2(mx, __vmaxu2(qf[kk][n][0] & 0x7fff7fffu, qf[kk][n][1] & 0x7fff7fffu));
     mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const int e = kv8_exp(kv8_max_halves(mx));
-    const float up = kv8_up(e);
-    rowfac[r] = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
+    const float up = kv8_up(e), fac = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
-      qf[kk][r] = kv8_to_f16(qf[kk][r], up);
-      qf[kk][2 + r] = kv8_to_f16(qf[kk][2 + r], up);
+      qf[kk][n][0] = kv8_to_f16(qf[kk][n][0], up);
+      qf[kk][n][1] = kv8_to_f16(qf[kk][n][1], up);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = 2 * n + k, rr = r0 + 8 * n + 2 * t4 + k;
+      rowfac[r] = __shfl_sync(0xffffffffu, fac, (2 * t4 + k) * 4);
+      pos[r] = rr < rows ? cached + rr / G : -1;
+      own[r] = pos[r] >> 4;  // -1 for a row that is none
+      lo[r] = rr < rows ? (a.window > 0 ? max(0, pos[r] - a.window + 1) : 0) : 1;
     }
   }
-  if (LOWER8)
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) qf[kk][1] = qf[kk][3] = 0u;
 
   bool ok = true;
   auto wait = [&](uint64_t* f, uint32_t parity) {
@@ -182,8 +195,8 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   const int full_lo = a.window > 0 ? (max(0, p_max - a.window + 1) + 15) >> 4 : 0;
   auto full = [&](int pg) { return pg >= full_lo && pg < own_lo; };
 
-  // ---- scores of the 8-bit pages, two at a time (four chains of products); the
-  // odd last one is taken twice
+  // ---- scores of the 8-bit pages, two at a time; the odd last one is taken
+  // twice.  Element e of a score fragment: key g + 8 (e / 2), row 2t + e % 2.
   float mx[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
@@ -194,31 +207,30 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
     used = i1 + 1;
     const uint4* kp0 = reinterpret_cast<const uint4*>(ring + (i % SL) * C::PART) + lane;
     const uint4* kp1 = reinterpret_cast<const uint4*>(ring + (i1 % SL) * C::PART) + lane;
-    float acc[2][2][4];
+    float acc[2][NB][4];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[x][j][0] = acc[x][j][1] = acc[x][j][2] = acc[x][j][3] = 0.f;
+      for (int n = 0; n < NB; ++n) acc[x][n][0] = acc[x][n][1] = acc[x][n][2] = acc[x][n][3] = 0.f;
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
-      const uint4 w0 = kp0[u * 32], w1 = kp1[u * 32];
-      uint32_t b0, b1;
-      kv8_expand<FMT>(w0.x, b0, b1);
-      mma_f16_16816(acc[0][0], qf[2 * u], b0, b1);
-      kv8_expand<FMT>(w0.y, b0, b1);
-      mma_f16_16816(acc[0][1], qf[2 * u], b0, b1);
-      kv8_expand<FMT>(w1.x, b0, b1);
-      mma_f16_16816(acc[1][0], qf[2 * u], b0, b1);
-      kv8_expand<FMT>(w1.y, b0, b1);
-      mma_f16_16816(acc[1][1], qf[2 * u], b0, b1);
-      kv8_expand<FMT>(w0.z, b0, b1);
-      mma_f16_16816(acc[0][0], qf[2 * u + 1], b0, b1);
-      kv8_expand<FMT>(w0.w, b0, b1);
-      mma_f16_16816(acc[0][1], qf[2 * u + 1], b0, b1);
-      kv8_expand<FMT>(w1.z, b0, b1);
-      mma_f16_16816(acc[1][0], qf[2 * u + 1], b0, b1);
-      kv8_expand<FMT>(w1.w, b0, b1);
-      mma_f16_16816(acc[1][1], qf[2 * u + 1], b0, b1);
+      const uint4 w[2] = {kp0[u * 32], kp1[u * 32]};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t f[4];
+        kv8_expand<FMT>(w[x].x, f[0], f[2]);
+        kv8_expand<FMT>(w[x].y, f[1], f[3]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) mma_f16_16816(acc[x][n], f, qf[2 * u][n][0], qf[2 * u][n][1]);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t f[4];
+        kv8_expand<FMT>(w[x].z, f[0], f[2]);
+        kv8_expand<FMT>(w[x].w, f[1], f[3]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) mma_f16_16816(acc[x][n], f, qf[2 * u + 1][n][0], qf[2 * u + 1][n][1]);
+      }
     }
     __syncwarp();
     refill(i);
@@ -227,169 +239,165 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
     for (int x = 0; x < 2; ++x) {
       const int ii = x ? i1 : i, pgi = a8 + ii;
       const float ks = __shfl_sync(0xffffffffu, sc.x, ii), lv = __shfl_sync(0xffffffffu, sc.z, ii);
-      float v[NR][4];  // [row][key block, key of the pair]
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const float c = __fmul_rn(ks, rowfac[r]);
+      for (int n = 0; n < NB; ++n) {
+        float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[r][e] = __fmaf_rn(acc[x][e >> 1][2 * r + (e & 1)], c, lv);
-      }
-      if (!full(pgi)) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
+        for (int e = 0; e < 4; ++e) v[e] = __fmaf_rn(acc[x][n][e], __fmul_rn(ks, rowfac[2 * n + (e & 1)]), lv);
+        if (!full(pgi)) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = pgi * 16 + (e >> 1) * 8 + t4 * 2 + (e & 1);
-            if (!(key >= lo[r] && pgi < own[r])) v[r][e] = -INFINITY;
+            const int r = 2 * n + (e & 1), key = pgi * 16 + gq + 8 * (e >> 1);
+            if (!(key >= lo[r] && pgi < own[r])) v[e] = -INFINITY;
           }
-      }
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        mx[r] = fmaxf(mx[r], fmaxf(fmaxf(v[r][0], v[r][1]), fmaxf(v[r][2], v[r][3])));
-        score[ii * 32 * NR + r] = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+        }
+        mx[2 * n] = fmaxf(mx[2 * n], fmaxf(v[0], v[2]));
+        mx[2 * n + 1] = fmaxf(mx[2 * n + 1], fmaxf(v[1], v[3]));
+        score[ii * 32 * NB + n] = make_float4(v[0], v[1], v[2], v[3]);
       }
     }
   }
   // ---- scores of the own pages
-  int ve[2][4];  // [own page][key]: the exponents of V tokens 2t, 2t + 1, 2t + 8, 2t + 9
+  int ve[2][4];     // [own page][key]: the exponents of V tokens 2t, 2t + 1, 2t + 8, 2t + 9
+  float vup[2][2];  // [own page]: 1 / V scale of tokens g, g + 8
   const int mi = lane >> 3, r8 = lane & 7;
 #pragma unroll 1
   for (int o = 0; o < no; ++o) {
     const int oi = ao + o - own_lo;
     if (!wait(&own_bar[oi], 0)) break;
     const uint32_t kb = smem_u32(own_s + oi * C::OWN), vb = kb + C::OWN / 2;
-    // largest magnitudes: of K tokens 8 j + g, then of V tokens 8 j + 2 t + {0, 1}
+    // largest magnitudes: of K tokens g and g + 8, then of V tokens 8 j + 2 t + {0, 1}
     uint32_t km[2] = {0u, 0u}, vm[2] = {0u, 0u};
 #pragma unroll 4
     for (int kk = 0; kk < KK; ++kk) {
       uint32_t w[4];
-      ldmatrix_x4(w, kb + kv_off<HD>((mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
-      km[0] = __vmaxu2(km[0], __vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu));
-      km[1] = __vmaxu2(km[1], __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+      ldmatrix_x4(w, kb + kv_off<HD>((mi & 1) * 8 + r8, kk * 2 + (mi >> 1)));
+      km[0] = __vmaxu2(km[0], __vmaxu2(w[0] & 0x7fff7fffu, w[2] & 0x7fff7fffu));
+      km[1] = __vmaxu2(km[1], __vmaxu2(w[1] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
       ldmatrix_x4_trans(w, vb + kv_off<HD>((mi & 1) * 8 + r8, kk * 2 + (mi >> 1)));
       vm[0] = __vmaxu2(vm[0], __vmaxu2(w[0] & 0x7fff7fffu, w[2] & 0x7fff7fffu));
       vm[1] = __vmaxu2(vm[1], __vmaxu2(w[1] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
     }
-    int ke[2], vx[4];
+    int vx[4];
+    float kup[2], kd[2], lv[2], up[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       km[j] = __vmaxu2(km[j], __shfl_xor_sync(0xffffffffu, km[j], 1));
       km[j] = __vmaxu2(km[j], __shfl_xor_sync(0xffffffffu, km[j], 2));
-      ke[j] = kv8_exp(kv8_max_halves(km[j]));
+      const int ke = kv8_exp(kv8_max_halves(km[j]));
+      kup[j] = kv8_up(ke);
+      kd[j] = ke == 255 ? kv8_nan() : kv8_down(ke);
 #pragma unroll
       for (int x = 4; x < 32; x *= 2) vm[j] = __vmaxu2(vm[j], __shfl_xor_sync(0xffffffffu, vm[j], x));
       vx[2 * j] = kv8_exp(vm[j] & 0xffffu);
       vx[2 * j + 1] = kv8_exp(vm[j] >> 16);
+      const int e0 = __shfl_sync(0xffffffffu, vx[2 * j], gq >> 1), e1 = __shfl_sync(0xffffffffu, vx[2 * j + 1], gq >> 1);
+      const int e = gq & 1 ? e1 : e0;  // of token g + 8 j
+      lv[j] = e == 255 ? kv8_nan() : kv8_log2_down(e);
+      up[j] = kv8_up(e);
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       if (o == 0) ve[0][x] = vx[x];
       else ve[1][x] = vx[x];
     }
-    const float kup[2] = {kv8_up(ke[0]), kv8_up(ke[1])};
-    float acc[2][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+    for (int x = 0; x < 2; ++x) {
+      if (o == 0) vup[0][x] = up[x];
+      else vup[1][x] = up[x];
+    }
+    float acc[NB][4];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       uint32_t w[4];
-      ldmatrix_x4(w, kb + kv_off<HD>((mi >> 1) * 8 + r8, kk * 2 + (mi & 1)));
-      mma_f16_16816(acc[0], qf[kk], kv8_to_f16(w[0], kup[0]), kv8_to_f16(w[1], kup[0]));
-      mma_f16_16816(acc[1], qf[kk], kv8_to_f16(w[2], kup[1]), kv8_to_f16(w[3], kup[1]));
+      ldmatrix_x4(w, kb + kv_off<HD>((mi & 1) * 8 + r8, kk * 2 + (mi >> 1)));
+      const uint32_t f[4] = {kv8_to_f16(w[0], kup[0]), kv8_to_f16(w[1], kup[1]), kv8_to_f16(w[2], kup[0]), kv8_to_f16(w[3], kup[1])};
+#pragma unroll
+      for (int n = 0; n < NB; ++n) mma_f16_16816(acc[n], f, qf[kk][n][0], qf[kk][n][1]);
     }
-    float v[NR][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int kx = __shfl_sync(0xffffffffu, ke[e >> 1], (2 * t4 + (e & 1)) * 4);
-      const float kd = kx == 255 ? kv8_nan() : kv8_down(kx);
-      const float lv = vx[e] == 255 ? kv8_nan() : kv8_log2_down(vx[e]);
-      const int key = (ao + o) * 16 + (e >> 1) * 8 + t4 * 2 + (e & 1);
+    for (int n = 0; n < NB; ++n) {
+      float v[4];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
+      for (int e = 0; e < 4; ++e) {
+        const int r = 2 * n + (e & 1), key = (ao + o) * 16 + gq + 8 * (e >> 1);
         const bool vis = key >= lo[r] && key <= pos[r] && ao + o == own[r];
-        v[r][e] = vis ? __fmaf_rn(acc[e >> 1][2 * r + (e & 1)], __fmul_rn(kd, rowfac[r]), lv) : -INFINITY;
-        mx[r] = fmaxf(mx[r], v[r][e]);
+        v[e] = vis ? __fmaf_rn(acc[n][e], __fmul_rn(kd[e >> 1], rowfac[r]), lv[e >> 1]) : -INFINITY;
+        mx[r] = fmaxf(mx[r], v[e]);
       }
+      score[(kChunkPages + o) * 32 * NB + n] = make_float4(v[0], v[1], v[2], v[3]);
     }
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-      score[(kChunkPages + o) * 32 * NR + r] = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
   }
+  // ---- the running maximum of the split at this chunk
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-  }
-
-  // ---- the running maximum of the split at this chunk
-  if (t4 == 0)
 #pragma unroll
-    for (int r = 0; r < NR; ++r) fold_m[warp][gq + 8 * r] = mx[r];
+    for (int x = 4; x < 32; x *= 2) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], x));
+    if (gq == 0) fold_m[warp][8 * (r >> 1) + 2 * t4 + (r & 1)] = mx[r];
+  }
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    for (int w = 0; w < warp; ++w) mx[r] = fmaxf(mx[r], fold_m[w][gq + 8 * r]);
+    for (int w = 0; w < warp; ++w) mx[r] = fmaxf(mx[r], fold_m[w][8 * (r >> 1) + 2 * t4 + (r & 1)]);
     if (mx[r] == -INFINITY) mx[r] = 0.f;  // no key seen so far: every score is -inf, every weight 0
   }
 
   // ---- weights, their sums and P V
-  float l[NR][kChunkParts][2], o_acc[HD / 8][4];  // l: [part of the chunk's pages][e]
+  float l[NR][kChunkParts], o_acc[HD / 16][NB][4];  // element e of O: dim 16 x + g + 8 (e / 2), row 2t + e % 2
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
-    for (int h = 0; h < kChunkParts; ++h) l[r][h][0] = l[r][h][1] = 0.f;
-  // weights x, 1 / V scales y of keys 2t, 2t + 1, 2t + 8, 2t + 9 of page `page`
-  auto add_l = [&](float (&s)[kChunkParts][2], int page, const float (&x)[4], float y0, float y1, float y2, float y3) {
-    const int q = (page - pg0) / (kChunkPages / kChunkParts);
+    for (int h = 0; h < kChunkParts; ++h) l[r][h] = 0.f;
 #pragma unroll
-    for (int h = 0; h < kChunkParts; ++h)
-      if (h == q) {
-        s[h][0] = __fmaf_rn(x[2], y2, __fmaf_rn(x[0], y0, s[h][0]));
-        s[h][1] = __fmaf_rn(x[3], y3, __fmaf_rn(x[1], y1, s[h][1]));
+  for (int x = 0; x < HD / 16; ++x)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) o_acc[x][n][0] = o_acc[x][n][1] = o_acc[x][n][2] = o_acc[x][n][3] = 0.f;
+  // Weights of page `pg`, at place i of the scores, as B fragments; their share of
+  // l, with the 1 / V scales y0, y1 of its tokens g, g + 8.
+  auto weights = [&](int i, int pg, float y0, float y1, bool all, uint32_t (&pb)[NB][2]) {
+    const int part = (pg - pg0) / (kChunkPages / kChunkParts);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const float4 v = score[i * 32 * NB + n];
+      const float p[4] = {ex2(__fsub_rn(v.x, mx[2 * n])), ex2(__fsub_rn(v.y, mx[2 * n + 1])),
+                          ex2(__fsub_rn(v.z, mx[2 * n])), ex2(__fsub_rn(v.w, mx[2 * n + 1]))};
+      pb[n][0] = transpose8(pack_f16x2(p[0], p[1]));
+      pb[n][1] = transpose8(pack_f16x2(p[2], p[3]));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = 2 * n + k;
+        // (a page that the row does not see stays out, whatever its scale)
+        if (all || ((i < kChunkPages ? pg < own[r] : pg == own[r]) && pg * 16 + 15 >= lo[r])) {
+#pragma unroll
+          for (int h = 0; h < kChunkParts; ++h)
+            if (h == part) l[r][h] = __fmaf_rn(p[2 + k], y1, __fmaf_rn(p[k], y0, l[r][h]));
+        }
       }
-  };
-#pragma unroll
-  for (int n = 0; n < HD / 8; ++n) o_acc[n][0] = o_acc[n][1] = o_acc[n][2] = o_acc[n][3] = 0.f;
-  auto weights = [&](int i, float (&p)[NR][4], uint32_t (&pa)[4]) {
-    if (LOWER8) pa[1] = pa[3] = 0u;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float4 v = score[i * 32 * NR + r];
-      p[r][0] = ex2(__fsub_rn(v.x, mx[r]));
-      p[r][1] = ex2(__fsub_rn(v.y, mx[r]));
-      p[r][2] = ex2(__fsub_rn(v.z, mx[r]));
-      p[r][3] = ex2(__fsub_rn(v.w, mx[r]));
-      pa[r] = pack_f16x2(p[r][0], p[r][1]);
-      pa[2 + r] = pack_f16x2(p[r][2], p[r][3]);
     }
   };
 #pragma unroll 1
   for (int i = 0; i < n8; ++i) {
     const int cp = n8 + i;  // the copy of page i's V
-    float p[NR][4];
-    uint32_t pa[4];
-    weights(i, p, pa);
+    uint32_t pb[NB][2];
     const float iv = __shfl_sync(0xffffffffu, sc.y, i);
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      // (a page that the row does not see stays out, whatever its scale)
-      if (full(a8 + i) || (a8 + i < own[r] && (a8 + i) * 16 + 15 >= lo[r])) add_l(l[r], a8 + i, p[r], iv, iv, iv, iv);
-    }
+    weights(i, a8 + i, iv, iv, full(a8 + i), pb);
     if (!wait(&bar[cp % SL], (cp / SL) & 1)) break;
     used = cp + 1;
     const uint4* vp = reinterpret_cast<const uint4*>(ring + (cp % SL) * C::PART) + lane;
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       const uint4 w = vp[u * 32];
-      uint32_t b0, b1;
-      kv8_expand<FMT>(w.x, b0, b1);
-      mma_f16_16816(o_acc[4 * u], pa, b0, b1);
-      kv8_expand<FMT>(w.y, b0, b1);
-      mma_f16_16816(o_acc[4 * u + 1], pa, b0, b1);
-      kv8_expand<FMT>(w.z, b0, b1);
-      mma_f16_16816(o_acc[4 * u + 2], pa, b0, b1);
-      kv8_expand<FMT>(w.w, b0, b1);
-      mma_f16_16816(o_acc[4 * u + 3], pa, b0, b1);
+      uint32_t f[4];
+      kv8_expand<FMT>(w.x, f[0], f[2]);
+      kv8_expand<FMT>(w.y, f[1], f[3]);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) mma_f16_16816(o_acc[2 * u][n], f, pb[n][0], pb[n][1]);
+      kv8_expand<FMT>(w.z, f[0], f[2]);
+      kv8_expand<FMT>(w.w, f[1], f[3]);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) mma_f16_16816(o_acc[2 * u + 1][n], f, pb[n][0], pb[n][1]);
     }
     __syncwarp();
     refill(cp);
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
 #pragma unroll 1
     for (int o = 0; o < no; ++o) {
       const uint32_t vb = smem_u32(own_s + (ao + o - own_lo) * C::OWN + C::OWN / 2);
-      float up[4];    // of keys 2t, 2t + 1, 2t + 8, 2t + 9
+      float up[4];                  // of keys 2t, 2t + 1, 2t + 8, 2t + 9
       uint32_t keep[2] = {0u, 0u};  // fp16 pairs: a token that is not finite counts as 0 here (its weight is NaN, or 0)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -406,22 +414,19 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
         up[x] = kv8_up(e);
         if (e != 255) keep[x >> 1] |= 0xffffu << (16 * (x & 1));
       }
-      float p[NR][4];
-      uint32_t pa[4];
-      weights(kChunkPages + o, p, pa);
+      uint32_t pb[NB][2];
+      weights(kChunkPages + o, ao + o, o == 0 ? vup[0][0] : vup[1][0], o == 0 ? vup[0][1] : vup[1][1], false, pb);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) add_l(l[r], ao + o, p[r], up[0], up[1], up[2], up[3]);
-#pragma unroll
-      for (int np = 0; np < HD / 16; ++np) {
+      for (int x = 0; x < HD / 16; ++x) {
         uint32_t w[4];
-        ldmatrix_x4_trans(w, vb + kv_off<HD>((mi & 1) * 8 + r8, np * 2 + (mi >> 1)));
+        ldmatrix_x4_trans(w, vb + kv_off<HD>((mi & 1) * 8 + r8, x * 2 + (mi >> 1)));
+        uint32_t f[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x0 = w[2 * h], x1 = w[2 * h + 1];
-          const uint32_t b0 = pack_f16x2(__fmul_rn(bf16_lo(x0), up[0]), __fmul_rn(bf16_hi(x0), up[1])) & keep[0];
-          const uint32_t b1 = pack_f16x2(__fmul_rn(bf16_lo(x1), up[2]), __fmul_rn(bf16_hi(x1), up[3])) & keep[1];
-          mma_f16_16816(o_acc[2 * np + h], pa, b0, b1);
-        }
+        for (int k = 0; k < 4; ++k)  // (dims 8 (k / 2) on, keys 8 (k % 2) on) -> fragment register k / 2 + 2 (k % 2)
+          f[(k >> 1) + 2 * (k & 1)] =
+              pack_f16x2(__fmul_rn(bf16_lo(w[k]), up[2 * (k & 1)]), __fmul_rn(bf16_hi(w[k]), up[2 * (k & 1) + 1])) & keep[k & 1];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) mma_f16_16816(o_acc[x][n], f, pb[n][0], pb[n][1]);
       }
     }
   }
@@ -429,31 +434,31 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
   for (int r = 0; r < NR; ++r)
 #pragma unroll
     for (int h = 0; h < kChunkParts; ++h) {
-      float x = __fadd_rn(l[r][h][0], l[r][h][1]);
-      x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 1));
-      x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 2));
-      if (t4 == 0) fold_l[h][warp][gq + 8 * r] = x;
+      float x = l[r][h];
+#pragma unroll
+      for (int k = 4; k < 32; k *= 2) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, k));
+      if (gq == 0) fold_l[h][warp][8 * (r >> 1) + 2 * t4 + (r & 1)] = x;
     }
   if (!ok) {  // gave up: every copy lands before the warp leaves
     for (int j = used; j < issued; ++j) drain_wait(&bar[j % SL], (j / SL) & 1);
     for (int o = 0; o < no; ++o) drain_wait(&own_bar[ao + o - own_lo], 0);
   }
 
-  // ---- the chunks of the split, left to right.  Each warp's O goes to its own
-  // ring, all of whose copies have been used; 8-float groups of a row are XORed
-  // with the row, so that the stores of a warp meet no bank twice.
+  // ---- the chunks of the split, left to right.  Each warp's O takes the place of
+  // its copies; 8-float groups of a row are XORed with the row's pair, so that the
+  // stores of a warp meet no bank twice.
   __syncwarp();
   float* fo = reinterpret_cast<float*>(ring);  // [row][HD]
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
+  for (int x = 0; x < HD / 16; ++x)
 #pragma unroll
-    for (int n = 0; n < HD / 8; ++n)
-      *reinterpret_cast<float2*>(fo + (gq + 8 * r) * HD + ((n ^ gq) * 8) + t4 * 2) =
-          make_float2(o_acc[n][2 * r], o_acc[n][2 * r + 1]);
-  }
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        fo[(8 * n + 2 * t4 + (e & 1)) * HD + ((16 * x + 8 * (e >> 1)) ^ (8 * t4)) + gq] = o_acc[x][n][e];
   __syncthreads();
   if (*abort_flag) return;
-  constexpr int TPR = 128 / (8 * NR), PER = HD / TPR;  // threads and dims per row
+  constexpr int TPR = 128 / (8 * NB), PER = HD / TPR;  // threads and dims per row
   const int frow = threadIdx.x / TPR, fd = threadIdx.x % TPR;
   const int row = r0 + frow;
   if (row >= rows) return;
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
     for (int h = 0; h < kChunkParts; ++h) L[h] = __fmaf_rn(L[h], alpha, fold_l[h][w][frow]);
 #pragma unroll
     for (int i = 0; i < PER / 4; ++i) {
-      const float4 v = *reinterpret_cast<const float4*>(src + (((i * TPR + fd) * 4) ^ ((frow & 7) * 8)));
+      const float4 v = *reinterpret_cast<const float4*>(src + (((i * TPR + fd) * 4) ^ (8 * ((frow >> 1) & 3))));
       O[4 * i] = __fmaf_rn(O[4 * i], alpha, v.x);
       O[4 * i + 1] = __fmaf_rn(O[4 * i + 1], alpha, v.y);
       O[4 * i + 2] = __fmaf_rn(O[4 * i + 2], alpha, v.z);
@@ -491,12 +496,12 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (LOWER8 ? 4 : 2) : 2)
                     __fadd_rn(O[4 * i + 3], 0.f));  // (no negative zeros, whichever kernel ran)
 }
 
-template <int HD, int FMT, bool LOWER8>
+template <int HD, int FMT, int NB>
 int launch_attn8_t(const CUtensorMap& kvmap, const Attn8Args& a, int n_blocks, cudaStream_t s) {
-  using C = Attn8Cfg<HD, LOWER8>;
+  using C = Attn8Cfg<HD, NB>;
   static_assert(C::smem(2) + 1024 <= 227 * 1024, "shared memory");
-  VD_CUDA_TRY(cudaFuncSetAttribute(attn8_kernel<HD, FMT, LOWER8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2)));
-  VD_CUDA_TRY(launch_k(attn8_kernel<HD, FMT, LOWER8>, dim3(static_cast<unsigned>(n_blocks) * a.Hkv), dim3(128), C::smem(a.own_slots), s, kvmap, a));
+  VD_CUDA_TRY(cudaFuncSetAttribute(attn8_kernel<HD, FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2)));
+  VD_CUDA_TRY(launch_k(attn8_kernel<HD, FMT, NB>, dim3(static_cast<unsigned>(n_blocks) * a.Hkv), dim3(128), C::smem(a.own_slots), s, kvmap, a));
   return VD_OK;
 }
 
@@ -510,10 +515,10 @@ int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int 
 #define VD_ATTN8(HD_)                                                                                             \
   if (hd == HD_) {                                                                                                \
     if (format == VD_KV8_INT8)                                                                                    \
-      return lower8 ? launch_attn8_t<HD_, kKv8Int8, true>(kvmap, a, n_blocks, s)                                   \
-                    : launch_attn8_t<HD_, kKv8Int8, false>(kvmap, a, n_blocks, s);                                 \
-    return lower8 ? launch_attn8_t<HD_, kKv8E4m3, true>(kvmap, a, n_blocks, s)                                     \
-                  : launch_attn8_t<HD_, kKv8E4m3, false>(kvmap, a, n_blocks, s);                                   \
+      return lower8 ? launch_attn8_t<HD_, kKv8Int8, 1>(kvmap, a, n_blocks, s)                                   \
+                    : launch_attn8_t<HD_, kKv8Int8, 2>(kvmap, a, n_blocks, s);                                 \
+    return lower8 ? launch_attn8_t<HD_, kKv8E4m3, 1>(kvmap, a, n_blocks, s)                                     \
+                  : launch_attn8_t<HD_, kKv8E4m3, 2>(kvmap, a, n_blocks, s);                                   \
   }
   VD_ATTN8(64)
   VD_ATTN8(128)

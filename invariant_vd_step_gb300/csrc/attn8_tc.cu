@@ -164,11 +164,6 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t x, uint64_t y) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
-__device__ __forceinline__ uint64_t f2_mul(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
 __device__ __forceinline__ uint64_t f2_sub(uint64_t x, uint64_t y) {
   uint64_t r;
   asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
@@ -576,14 +571,16 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
             const bool fold_in = sees && have, load = have && (sees || pc == ch1);
             float2 ml = rec_tot[sthread];
             const float mn = fmaxf(ml.x, r.z), ca = ex2(__fsub_rn(ml.x, mn)), cb = ex2(__fsub_rn(r.z, mn));
-            const uint64_t ca2 = f2(ca, ca), cb2 = f2(cb, cb);
             if (load) {
 #pragma unroll
               for (int i = 0; i < OD / 4; ++i) {
                 const float4 v = __ldcg(tot + i * C::NS);
-                const uint64_t v0 = f2(v.x, v.y), v1 = f2(v.z, v.w);
-                O[2 * i] = fold_in ? f2_add(f2_mul(v0, ca2), f2_mul(f2_add(O[2 * i], 0ull), cb2)) : v0;
-                O[2 * i + 1] = fold_in ? f2_add(f2_mul(v1, ca2), f2_mul(f2_add(O[2 * i + 1], 0ull), cb2)) : v1;
+                // (in scalars: the packed product and sum come out as one fma, which is not what the merge kernel computes)
+                auto both = [&](float tot, float o) {
+                  return fold_in ? __fadd_rn(__fmul_rn(tot, ca), __fmul_rn(__fadd_rn(o, 0.f), cb)) : tot;
+                };
+                O[2 * i] = f2(both(v.x, f2_lo(O[2 * i])), both(v.y, f2_hi(O[2 * i])));
+                O[2 * i + 1] = f2(both(v.z, f2_lo(O[2 * i + 1])), both(v.w, f2_hi(O[2 * i + 1])));
               }
             } else {
 #pragma unroll

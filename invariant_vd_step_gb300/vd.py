@@ -180,6 +180,7 @@ _SIGS = {
     "vd_kv8_plan_create": (ctypes.c_int, [_VP, ctypes.c_int32, ctypes.POINTER(_VP)]),
     "vd_destroy_kv8_plan": (None, [_VP]),
     "vd_kv8_plan_make": (ctypes.c_int, [_VP, _VP, _VP, ctypes.POINTER(KV8Batch), _VP]),
+    "vd_kv8_set_prefill": (ctypes.c_int, [_VP, ctypes.c_int32]),
     "vd_op_kv8_rope_kv": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int32, _VP, _VP, _VP]),
     "vd_op_kv8_seal": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int32, _VP]),
     "vd_op_kv8_attention": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int32, _VP, _VP, _VP]),
@@ -895,6 +896,10 @@ class KV8Plan:
         check(lib().vd_kv8_plan_make(_live(self, cache, pool), cache.h, pool.h, ctypes.byref(b),
                                      _model_stream(self.model, stream)))
         self.num_tokens, self.num_logit_rows = int(cu[-1]), len(rows)
+
+    def set_prefill(self, kernel: int):
+        """vd_kv8_set_prefill: kernel of longer chunks in later plans (0 by size, 1 mma.sync, 2 tcgen05); the same bits."""
+        check(lib().vd_kv8_set_prefill(_live(self), int(kernel)))
 
     def rope_kv(self, cache: KV8Cache, pool: KVPool, layer: int, qkv: torch.Tensor, q_out: torch.Tensor, stream=None):
         """vd_op_kv8_rope_kv: qkv bf16 [T][(Hq + 2 Hkv) hd], q_out bf16 [T][Hq][hd]."""

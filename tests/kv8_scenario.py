@@ -84,11 +84,12 @@ class KV8Scenario:
         cu = np.concatenate([[0], np.cumsum([n for _, _, n in reqs])]).astype(np.int32)
         return cu, np.array([c for _, c, _ in reqs], np.int32), t8, t16, L
 
-    def attention(self, reqs, layer=0, scatter=True, stream=None):
+    def attention(self, reqs, layer=0, scatter=True, kernel=0):
         cu, cached, t8, t16, _ = self.setup(reqs, scatter)
         q = torch.cat([self.q[rid][c:c + n] for rid, c, n in reqs])
         out = torch.full_like(q, float("nan"))
         self.plan = vd.KV8Plan(self.model, len(q))
+        self.plan.set_prefill(kernel)
         self.plan.plan(self.cache, self.pool, cu, cached, t8, t16)
         self.plan.seal(self.cache, self.pool, layer)
         self.plan.attention(self.cache, self.pool, layer, q, out)

@@ -124,13 +124,14 @@ SHAPES = [
 def test_attention_against_64_bits(Hq, Hkv, hd, window, reqs, fmt):
     ready()
     sc = KV8Scenario(kv8_spec(Hq, Hkv, hd, window), [c + n for c, n in reqs], fmt, seed=hd + window)
-    out = sc.attention([(i, c, n) for i, (c, n) in enumerate(reqs)]).double()
-    at = 0
-    for i, (c, n) in enumerate(reqs):
-        want, tol = sc.exact(i, c, n, window)
-        err = (out[at:at + n] - want).abs()
-        assert (err <= tol).all(), (i, c, n, float((err / tol).max()))
-        at += n
+    for kernel in (1, 2):
+        out = sc.attention([(i, c, n) for i, (c, n) in enumerate(reqs)], kernel=kernel).double()
+        at = 0
+        for i, (c, n) in enumerate(reqs):
+            want, tol = sc.exact(i, c, n, window)
+            err = (out[at:at + n] - want).abs()
+            assert (err <= tol).all(), (kernel, i, c, n, float((err / tol).max()))
+            at += n
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -142,10 +143,13 @@ def test_rows_do_not_depend_on_how_they_are_run(Hq, Hkv, hd, window, fmt):
     n = 661
     sc = KV8Scenario(kv8_spec(Hq, Hkv, hd, window), [n, 300, 40], fmt, seed=9, max_tokens=2048)
     whole = bits(sc.attention([(0, 0, n)]))
+    for kernel in (1, 2):
+        np.testing.assert_array_equal(bits(sc.attention([(0, 0, n)], kernel=kernel)), whole, err_msg=str(kernel))
     for cuts in ([(0, 16), (16, 17), (33, 95), (128, 400), (528, 133)], [(0, 650), (650, 11)]):
         for c, k in cuts:
-            got = bits(sc.attention([(1, 299, 1), (0, c, k), (2, 0, 40)]))
-            np.testing.assert_array_equal(got[1:1 + k], whole[c:c + k], err_msg=f"{c} {k}")
+            for kernel in (0, 2):
+                got = bits(sc.attention([(1, 299, 1), (0, c, k), (2, 0, 40)], kernel=kernel))
+                np.testing.assert_array_equal(got[1:1 + k], whole[c:c + k], err_msg=f"{c} {k} {kernel}")
     for c in (0, 1, 15, 16, 100, 127, 128, 129, 511, 512, 640, 660):
         k = min(16 // (Hq // Hkv), n - c)
         for m in {1, max(1, min(2, k)), k}:
@@ -163,11 +167,12 @@ def test_many_requests_and_odd_orders():
     for i in rng.permutation(70):
         c = int(rng.integers(0, lens[i]))
         reqs.append((int(i), c, lens[i] - c if rng.random() < 0.5 else 1))
-    out, at = sc.attention(reqs).double(), 0
-    for i, c, n in reqs:
-        want, tol = sc.exact(i, c, n)
-        assert ((out[at:at + n] - want).abs() <= tol).all(), (i, c, n)
-        at += n
+    for kernel in (0, 2):
+        out, at = sc.attention(reqs, kernel=kernel).double(), 0
+        for i, c, n in reqs:
+            want, tol = sc.exact(i, c, n)
+            assert ((out[at:at + n] - want).abs() <= tol).all(), (kernel, i, c, n)
+            at += n
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -187,13 +192,14 @@ def test_scales_that_differ_by_many_orders(fmt):
         sc.kv[2][:, 1] = 0               # and one of zeros
     sc = KV8Scenario(kv8_spec(4, 2, 128), [220, 150, 90], fmt, seed=2, edit=edit)
     reqs = [(0, 0, 220), (1, 149, 1), (2, 50, 40)]
-    out, at = sc.attention(reqs).double(), 0
-    for i, c, n in reqs:
-        want, tol = sc.exact(i, c, n)
-        err = (out[at:at + n] - want).abs()
-        assert (err <= tol).all(), (i, float((err - tol).max()))
-        at += n
-    assert (out[221:] == 0).all()
+    for kernel in (1, 2):
+        out, at = sc.attention(reqs, kernel=kernel).double(), 0
+        for i, c, n in reqs:
+            want, tol = sc.exact(i, c, n)
+            err = (out[at:at + n] - want).abs()
+            assert (err <= tol).all(), (kernel, i, float((err - tol).max()))
+            at += n
+        assert (out[221:] == 0).all()
 
 
 @pytest.mark.parametrize("q_scale", [2.0 ** -100, 30.0, 2.0 ** 60])
@@ -225,7 +231,8 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them_only(kind, whic
         sc = KV8Scenario(spec, [n], "int8", seed=6, edit=edit)
         for reqs in ([(0, 0, n)], [(0, 33, 90)], [(0, 69, 1)], [(0, 70, 2)], [(0, 126, 1)], [(0, 128, 2)]):
             c, k = reqs[0][1:]
-            out = sc.attention(reqs)
+            out = sc.attention(reqs, kernel=1)
+            np.testing.assert_array_equal(bits(sc.attention(reqs, kernel=2)), bits(out))
             for r in range(k):
                 p = c + r
                 sees = 70 <= p < 80 if p // 16 == 4 else p >= 80 and (w == 0 or p - w + 1 <= 79)
@@ -237,6 +244,22 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them_only(kind, whic
                         assert out[r].isnan().all(), (w, p)
                 else:
                     np.testing.assert_array_equal(bits(out[r]), clean[p], err_msg=f"{w} {p}")
+
+
+@pytest.mark.parametrize("Hq,Hkv,hd,window", [(32, 8, 128, 0), (12, 4, 64, 700), (24, 8, 128, 0)])
+def test_blocks_that_fold_their_splits_and_blocks_cut_into_runs(Hq, Hkv, hd, window):
+    """More row blocks than SMs, over several splits: most fold their own splits, the last ones leave them to the merge;
+    with 3 heads per KV head a token's rows may lie in two blocks.  Every row as its token alone."""
+    ready()
+    n = 1500
+    sc = KV8Scenario(kv8_spec(Hq, Hkv, hd, window), [n, 700], "int8", seed=8, max_tokens=2300)
+    reqs = [(0, 200, n - 200), (1, 0, 700)]
+    got = bits(sc.attention(reqs, kernel=2))
+    np.testing.assert_array_equal(bits(sc.attention(reqs, kernel=1)), got)
+    for c in (200, 511, 777, 1024, n - 1):
+        np.testing.assert_array_equal(bits(sc.attention([(0, c, 1)]))[0], got[c - 200], err_msg=str(c))
+    want, tol = sc.exact(1, 0, 700, window)
+    assert ((sc.attention(reqs, kernel=2)[n - 200:].double() - want).abs() <= tol).all()
 
 
 def test_streams_and_two_plans():
@@ -343,6 +366,8 @@ def test_refusals():
     refused(4, vd.KV8Cache, sc.model, 4, "int8", memory=torch.zeros(256, dtype=torch.uint8, device="cuda"))
     refused(4, vd.KV8Plan, sc.model, 65)
     refused(1, vd.KV8Plan, sc.model, 0)
+    refused(1, plan.set_prefill, 3)
+    refused(1, plan.set_prefill, -1)
     # a plan without work
     plan.plan(sc.cache, sc.pool, [0], [], np.zeros((0, 0)), np.zeros((0, 0)))
     plan.seal(sc.cache, sc.pool, 0)
