@@ -540,6 +540,7 @@ class KVPool:
         self.num_pages = num_pages
         nbytes = model.pool_bytes(num_pages)
         self.memory = memory  # keep alive when caller-owned
+        self._pages = None
         h = ctypes.c_void_p()
         ptr = _ptr(memory) if memory is not None else None
         check(lib().vd_kv_pool_alloc(model.h, num_pages, ptr, nbytes if memory is not None else 0,
@@ -562,32 +563,36 @@ class KVPool:
 
     def view(self) -> torch.Tensor:
         """The pool as a bf16 tensor [layers][pages][2][Hkv][16][hd] (requires caller memory)."""
-        s = self.model.spec
         if self.memory is None:
             raise RuntimeError("view() needs a pool created over caller memory")
-        return self.memory.view(torch.bfloat16)[: s.n_layers * self.num_pages * 2 * s.n_kv_heads * 16 * s.head_dim] \
-            .view(s.n_layers, self.num_pages, 2, s.n_kv_heads, 16, s.head_dim)
+        if self._pages is None or self._pages[0] is not self.memory:
+            s = self.model.spec
+            v = self.memory.view(torch.bfloat16)[: s.n_layers * self.num_pages * 2 * s.n_kv_heads * 16 * s.head_dim]
+            self._pages = self.memory, v.view(s.n_layers, self.num_pages, 2, s.n_kv_heads, 16, s.head_dim)
+        return self._pages[1].detach()  # a tensor of its own: three views took 7 us, a page copy's call 5
 
     def copy_pages(self, src, dst, stream=None):
         """vd_kv_copy_pages: pages src[i] to pages dst[i], in every layer."""
         n, src, dst = _page_lists(src, dst)
-        check(lib().vd_kv_copy_pages(_live(self), n, src.ctypes.data, dst.ctypes.data, _model_stream(self.model, stream)))
+        check(lib().vd_kv_copy_pages(_live(self), n, src, dst, _model_stream(self.model, stream)))
 
 
 def _ids(a):
     """Page ids as a contiguous int32 array; ids that int32 does not hold are refused."""
+    if type(a) is np.ndarray and a.dtype == np.int32 and a.ndim == 1 and a.flags.c_contiguous:
+        return a
     a = np.asarray(a)
-    if a.dtype != np.int32 or a.ndim != 1 or not a.flags.c_contiguous:
-        _need(a.size == 0 or (a.dtype.kind in "iu" and -2 ** 31 <= int(a.min()) and int(a.max()) < 2 ** 31),
-              "page ids: integers that fit in 32 bits")
-        a = np.ascontiguousarray(a.reshape(-1), dtype=np.int32)
-    return a
+    _need(a.size == 0 or (a.dtype.kind in "iu" and -2 ** 31 <= int(a.min()) and int(a.max()) < 2 ** 31),
+          "page ids: integers that fit in 32 bits")
+    return np.ascontiguousarray(a.reshape(-1), dtype=np.int32)
 
 
 def _page_lists(src, dst):
+    """(number, sources, destinations) as arguments of a library call."""
     src, dst = _ids(src), _ids(dst)
-    _need(len(src) == len(dst), "as many destinations as sources")
-    return len(src), src, dst
+    if len(src) != len(dst):
+        raise VDError(VD_ERR_INVALID_ARG, "as many destinations as sources")
+    return len(src), _rows_ptr(src), _rows_ptr(dst)
 
 
 def _live(*objects):
@@ -837,20 +842,17 @@ class KV8Cache:
     def seal(self, pool: KVPool, src, dst, layer: int = -1, stream=None):
         """vd_kv8_seal: pages src[i] of the bf16 pool into pages dst[i], in one layer or in all (-1)."""
         n, src, dst = _page_lists(src, dst)
-        check(lib().vd_kv8_seal(_live(self, pool), pool.h, layer, n, src.ctypes.data, dst.ctypes.data,
-                                _model_stream(self.model, stream)))
+        check(lib().vd_kv8_seal(_live(self, pool), pool.h, layer, n, src, dst, _model_stream(self.model, stream)))
 
     def unseal(self, pool: KVPool, src, dst, layer: int = -1, stream=None):
         """vd_kv8_unseal: the values of pages src[i], rounded to bf16, into pages dst[i] of the bf16 pool."""
         n, src, dst = _page_lists(src, dst)
-        check(lib().vd_kv8_unseal(_live(self, pool), pool.h, layer, n, src.ctypes.data, dst.ctypes.data,
-                                  _model_stream(self.model, stream)))
+        check(lib().vd_kv8_unseal(_live(self, pool), pool.h, layer, n, src, dst, _model_stream(self.model, stream)))
 
     def copy_pages(self, src, dst, stream=None):
         """vd_kv8_copy_pages: pages src[i] to pages dst[i], in every layer."""
         n, src, dst = _page_lists(src, dst)
-        check(lib().vd_kv8_copy_pages(_live(self), n, src.ctypes.data, dst.ctypes.data,
-                                      _model_stream(self.model, stream)))
+        check(lib().vd_kv8_copy_pages(_live(self), n, src, dst, _model_stream(self.model, stream)))
 
 
 class KV8Plan:
