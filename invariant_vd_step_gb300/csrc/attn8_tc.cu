@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ float ex[2][C::NT][128];  // [chunk % 2][half][row] largest scores
-  __shared__ float ex_l[C::NT][128];   // l of the halves at a split's end
+  __shared__ float ex_l[2][C::NT][128];  // [chunk % 2] l of the halves at a split's end: the last two may be neighbours
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ int skip;
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
         for (int d = 1; d < LPR; d *= 2) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, d));
         const int e = kv8_exp(kv8_max_halves(mx));
         const float up = kv8_up(e);
-        if (c == 0) ex_l[0][rl] = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
+        if (c == 0) ex_l[0][0][rl] = e == 255 ? kv8_nan() : __fmul_rn(a.scale_log2, kv8_down(e));
         *reinterpret_cast<uint4*>(sq + (c >> 3) * (C::ROWS * 128) + rl * 128 + (((c & 7) ^ (rl & 7)) << 4)) =
             make_uint4(kv8_to_f16(x[k].x, up), kv8_to_f16(x[k].y, up), kv8_to_f16(x[k].z, up), kv8_to_f16(x[k].w, up));
       }
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       mbar_arrive(q_full);
     }
     bool ok = softmax_sync(true);
-    const float rowfac = ex_l[0][lr];
+    const float rowfac = ex_l[0][0][lr];
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     auto warp_wait = [&](uint64_t* f, int n) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(f, n & 1, abort_flag, a.status));
@@ -557,12 +557,12 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
         }
         L = __fmaf_rn(L, r.x, r.y);
         if (split_end) {
-          ex_l[h][lr] = L;
+          ex_l[it & 1][h][lr] = L;
           ok = softmax_sync(ok);
           if (!ok) break;
           float x[C::NT];
 #pragma unroll
-          for (int k = 0; k < C::NT; ++k) x[k] = ex_l[k][lr];
+          for (int k = 0; k < C::NT; ++k) x[k] = ex_l[it & 1][k][lr];
           const float Ls = kv8_sum_parts(x);
           const bool sees = valid && max(lo, sp * kSplit8) <= min(pos, sp * kSplit8 + kSplit8 - 1);
           if (totals) {
