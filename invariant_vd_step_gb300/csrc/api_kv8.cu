@@ -43,8 +43,6 @@ struct vd_kv8_plan {
   size_t dev_cap = 0;  // ints
   float* part = nullptr;
   size_t part_cap = 0;  // floats
-  float* tot = nullptr;
-  size_t tot_cap = 0;   // floats
   uint8_t* images = nullptr;
   size_t images_cap = 0;
   int* host[2] = {nullptr, nullptr};  // pinned staging
@@ -304,7 +302,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   // their splits and need no merge; those of the last, partial round are cut into
   // runs of splits, so that it takes less of a round.  (A token's heads are in one
   // block, or the cut moves back to where they are.)
-  size_t total_blocks = 0;  // most blocks of a layer that fold their splits themselves
+
   std::vector<int> merge[2];  // tokens that the merge kernel folds
   for (int local = 0; local <= (windowed ? 1 : 0); ++local) {
     auto splits_of = [&](int i, int r0, int step, int* first) {
@@ -339,11 +337,10 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       for (int k = 0; k < parts; ++k)
         blocks[3 * local + 2].insert(blocks[3 * local + 2].end(),
                                      {image0[i], q0, ql, b->cached_len[i], first + n * k / parts, r0, first + n * (k + 1) / parts,
-                                      parts == 1 && j < direct ? j : -1});
+                                      j < direct});
       if (j >= direct)  // the tokens whose first head is in the block
         for (int t0 = (r0 + m->G - 1) / m->G; t0 * m->G < std::min(rows, r0 + 128); ++t0) merge[local].push_back(q0 + t0);
     }
-    total_blocks = std::max(total_blocks, static_cast<size_t>(direct));
   }
   for (int k = 0; k < 6; ++k) {  // int4, then int2: first, for their alignment
     if (blocks[k].size() / 8 * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
@@ -383,12 +380,11 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   }
   const size_t rows = static_cast<size_t>(T) * c.n_heads * splits;
   const size_t images = static_cast<size_t>(n_images) * c.n_kv_heads * attn8_image_bytes(c.head_dim);
-  const size_t tot = total_blocks * c.n_kv_heads * 128 * c.head_dim;  // floats
   int rc;
-  if (off > t->dev_cap || rows * (c.head_dim + 2) > t->part_cap || tot > t->tot_cap || images > t->images_cap)
+  if (off > t->dev_cap || rows * (c.head_dim + 2) > t->part_cap || images > t->images_cap)
     t->planned = false;  // the old plan's buffers go
   if ((rc = grow(&t->dev, &t->dev_cap, off)) || (rc = grow(&t->part, &t->part_cap, rows * (c.head_dim + 2))) ||
-      (rc = grow(&t->tot, &t->tot_cap, tot)) || (rc = grow(&t->images, &t->images_cap, images)))
+      (rc = grow(&t->images, &t->images_cap, images)))
     return rc;
   int* h = t->host[slot];
   int ns = 0;
@@ -415,7 +411,6 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   for (int k = 0; k < 2; ++k) std::copy(chunks[k].begin(), chunks[k].end(), h + d.chunks[k]);
   for (int j = 0; j < R; ++j) h[d.logit_rows + j] = b->logit_rows[j];
   for (int k = 0; k < 2; ++k) std::copy(merge[k].begin(), merge[k].end(), h + d.merge_list[k]);
-  d.totals = reinterpret_cast<float4*>(t->tot);
   d.images = t->images;
   d.base = t->dev;
   d.part_o = t->part;
@@ -460,7 +455,6 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
   a.Hq = c.n_heads;
   a.Hkv = c.n_kv_heads;
   a.images = d.images;
-  a.totals = d.totals;
   a.out = out;
   a.open = static_cast<const __nv_bfloat16*>(pool->data) +
            static_cast<size_t>(layer) * pool->num_pages * 2 * c.n_kv_heads * 16 * c.head_dim;
@@ -598,7 +592,6 @@ void vd_destroy_kv8_plan(vd_kv8_plan* t) {
   }
   if (t->dev) cudaFree(t->dev);
   if (t->part) cudaFree(t->part);
-  if (t->tot) cudaFree(t->tot);
   if (t->images) cudaFree(t->images);
   if (dev != t->device) cudaSetDevice(dev);
   delete t;

@@ -10,16 +10,21 @@
 // splits, whose chunks of 128 keys it takes one after another.  Per chunk: S = Q
 // K^T (N = 128) into one of two score buffers of tensor memory; the softmax
 // threads, two per row with 64 keys each, take the row's maximum, turn S into
-// fp16 weights in its place, and O = P V of the chunk goes to one of two O
-// buffers, which the same threads (half of the dims each) fold into the
-// split's O in their registers two chunks later, when the scores that were issued
-// behind it are there.  A run that holds all of a block's splits folds them too, as
-// the merge kernel does (its totals wait in global memory, in L2, while a split is
-// in hand), and writes the output; shorter runs, which launches of few blocks
-// take, leave the splits' partials to that kernel.  The next chunk's scores run beside the softmax.  What a
-// chunk takes per SM: the products 1024 cycles at the dense rate, 16384
-// exponentials (512 cycles), and about 1700 issue slots per scheduler in the
-// softmax and conversion warps.
+// fp16 weights in its place, and fold O = P V of the chunk before (half of the dims
+// each) into the split's O in their registers; P V and the scores of the chunk
+// after the next run meanwhile.  A run that holds all of a block's splits folds
+// them too, as the merge kernel does (its totals wait in tensor memory while a
+// split is in hand), and writes the output; shorter runs, which the last blocks of a
+// launch are cut into, leave the splits' partials to that kernel.
+//
+// What a chunk takes per SM: the products 1024 cycles at the dense rate, 16384
+// exponentials 512, 64 KB of operands from L2; about 1500 issue slots per
+// scheduler, whose two softmax warps leave more than half of its cycles idle: that
+// is what bounds it (3000 cycles per chunk).  Measured, 2048 tokens behind 6144
+// keys, 32 heads over 8 of 128: 375 us, 641 TFLOP/s.  424 us with the totals in
+// global memory, two O buffers and one barrier of all softmax threads (the two of a
+// row need only each other); 447 with the folding in four warps of its own, which
+// became what the others waited for; 414 with 216 registers (spills), 232 now.
 //
 // The operands are made once per launch, not once per row block: an expanding
 // kernel turns every chunk of the launch's requests into an image of the two
@@ -27,10 +32,10 @@
 // ([dim][key]) so that both are K-major, and of the chunk's scales; a block then
 // fetches a tile with one bulk copy (from L2: a request's blocks run together).
 // The pages that are some row's own have a second image of their chunk, in bf16
-// scaled per token to exact fp16, and scores of their own (in the columns that the
-// chunk's O takes later); a row takes 16 of their columns.  Converting inside the
-// blocks, by eight warps beside the softmax, took a third of the issue slots and
-// made a chunk's softmax wait: 5000 cycles per chunk, XXXX now.
+// scaled per token to exact fp16, and scores of their own (in the other score
+// buffer); a row takes 16 of their columns.  Converting inside the blocks, by eight
+// warps beside the softmax, took a third of the issue slots: 738 us where the images
+// came to 489.
 //
 // Roles (384 threads): warp 0 allocates tensor memory, its lane 0 issues the MMAs;
 // warp 1's lane 0 the copies; warps 4..11 are the softmax.  Every wait is bounded.
@@ -56,9 +61,8 @@ struct Tc8Cfg {
   static constexpr int NT = kChunkParts;  // softmax threads per row
   static constexpr int NS = 128 * NT;
   static constexpr int OUT_BYTES = 4 * NT * 32 * 128;  // per softmax warp: 32 rows x 32 dims of float32
-  static constexpr int REC_BYTES = NS * 40;  // per softmax thread: two chunks' factor, l and maximum; the totals' maximum and l
-  static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + OUT_BYTES + REC_BYTES + SC_RING * SCALES + 256;
-  static constexpr int TMEM_COLS = 512;  // chunk c: scores (then weights) from 128 (c % 2), O from 256 + 128 (c % 2)
+  static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + OUT_BYTES + SC_RING * SCALES + 256;
+  static constexpr int TMEM_COLS = 512;  // chunk c: scores (then weights) from 128 (c % 2), O from 256; the totals from 384
   static constexpr int THREADS = 128 + NS;
   // A chunk's image: K tile, V tile, scales
   static constexpr int IMAGE = K_BYTES + V_BYTES + SCALES;
@@ -102,16 +106,6 @@ __device__ __forceinline__ void wait_ld16(uint32_t* r) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
         "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
         "+r"(r[15])::"memory");
-}
-template <int N>
-__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
-  if constexpr (N == 32) ld32(taddr, r);
-  else ld16(taddr, r);
-}
-template <int N>
-__device__ __forceinline__ void wait_cols(uint32_t* r) {
-  if constexpr (N == 32) wait_ld32(r);
-  else wait_ld16(r);
 }
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
@@ -170,14 +164,17 @@ __device__ __forceinline__ uint64_t f2_sub(uint64_t x, uint64_t y) {
   return r;
 }
 
-// Barrier of the softmax threads that also tells whether any of them has given up.
-__device__ __forceinline__ bool softmax_sync(bool ok) {
+// Barrier id of THREADS softmax threads that also tells whether any of them has
+// given up.  The two threads of a row are in warps that share nothing with others,
+// so these meet in barriers of their own.
+template <int THREADS>
+__device__ __forceinline__ bool softmax_sync(int id, bool ok) {
   uint32_t bad;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "bar.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(bad)
-      : "r"(ok ? 0u : 1u), "n"(128 * kChunkParts)
+      : "r"(ok ? 0u : 1u), "r"(id), "n"(THREADS)
       : "memory");
   return bad == 0;
 }
@@ -317,19 +314,17 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   uint8_t* sk = sq + C::Q_BYTES;                   // K of stage s at sk + (s % 2) * K_BYTES
   uint8_t* sv = sk + C::STAGES * C::K_BYTES;
   uint8_t* so_out = sv + C::STAGES * C::V_BYTES;
-  float4* rec = reinterpret_cast<float4*>(so_out + C::OUT_BYTES);     // [2][NS]
-  float2* rec_tot = reinterpret_cast<float2*>(rec + 2 * C::NS);       // [NS]
-  float* scales = reinterpret_cast<float*>(rec_tot + C::NS);
+  float* scales = reinterpret_cast<float*>(so_out + C::OUT_BYTES);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scales) + C::SC_RING * C::SCALES);
   uint64_t* v_full = k_full + 2;     // [stage % 2] (and the two below)
   uint64_t* k_empty = v_full + 2;
   uint64_t* v_empty = k_empty + 2;
-  uint64_t* s_full = v_empty + 2;    // [chunk % 2]: its 8-bit scores are there, and O of the chunk two before it
-  uint64_t* p_full = s_full + 2;     // its weights are, and that O has been folded
+  uint64_t* s_full = v_empty + 2;    // [chunk % 2]: its 8-bit scores are there
+  uint64_t* p_full = s_full + 2;     // its weights are, and O of the chunk before has been folded
   uint64_t* q_full = p_full + 2;
   uint64_t* s16_full = q_full + 1;   // scores of the own pages of a chunk that has some
-  uint64_t* o_free = s16_full + 1;   // the columns that they take are free
-  uint64_t* mma_done = o_free + 1;   // every MMA has completed
+  uint64_t* o_full = s16_full + 1;   // O of a chunk
+  uint64_t* mma_done = o_full + 1;   // every MMA has completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ float ex[2][C::NT][128];  // [chunk % 2][half][row] largest scores
@@ -359,7 +354,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
     }
     mbar_init(q_full, C::NS);
     mbar_init(s16_full, 1);
-    mbar_init(o_free, C::NS);
+    mbar_init(o_full, 1);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -385,7 +380,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
 
   int issued_k = 0, issued_v = 0;  // stages whose copies have been issued (the copying thread's)
   if (warp < 4) {
-    regs_dec<72>();
+    regs_dec<40>();
     if (warp == 0 && lane == 0) {
       const uint32_t id_s = idesc_f16(128, kChunk8), id_pv = idesc_f16(128, HD);
       const uint32_t q_lo = sw128_desc_lo(smem_u32(sq)), k_lo = sw128_desc_lo(smem_u32(sk)), v_lo = sw128_desc_lo(smem_u32(sv));
@@ -398,19 +393,25 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
           umma_bf16_lo(tmem + col, q_lo + (kk >> 2) * (C::ROWS * 128 >> 4) + 2 * (kk & 3),
                        k + (kk >> 2) * (kChunk8 * 128 >> 4) + 2 * (kk & 3), id_s, kk ? 1u : 0u);
       };
-      // O at columns `o` += weights of pages [x0, x1) in columns `p` times the V of stage st; first: from zero
-      auto pv = [&](int st, uint32_t o, uint32_t p, int x0, int x1, bool first) {
+      // O += weights of pages [x0, x1) in columns `p` times the V of stage st; first: from zero
+      auto pv = [&](int st, uint32_t p, int x0, int x1, bool first) {
         const uint32_t v = v_lo + (st & 1) * (C::V_BYTES >> 4);
+        auto one = [&](int x, uint32_t add) {
+          umma_bf16_ta(tmem + 256, tmem + p + 8 * x, v + (x >> 2) * (HD * 128 >> 4) + 2 * (x & 3), id_pv, add);
+        };
+        if (first && x0 == 0 && x1 == kChunkPages) {
+#pragma unroll
+          for (int x = 0; x < kChunkPages; ++x) one(x, x ? 1u : 0u);
+        } else {
 #pragma unroll 1
-        for (int x = x0; x < x1; ++x)
-          umma_bf16_ta(tmem + o, tmem + p + 8 * x, v + (x >> 2) * (HD * 128 >> 4) + 2 * (x & 3), id_pv,
-                       first && x == x0 ? 0u : 1u);
+          for (int x = x0; x < x1; ++x) one(x, first && x == x0 ? 0u : 1u);
+        }
       };
       // Stages are numbered along the chunks: one for a chunk's 8-bit pages, one
       // more for its own pages.  Scores run up to two chunks ahead of P V; at
       // chunks with own pages, whose two stages fill both slots, they wait for
       // the P V of every chunk before.
-      int ns = ch0, st_s = 0, st_v = 0, n16 = 0;  // next chunk to score, its stage; the stage of the chunk whose P V is next
+      int ns = ch0, st_s = 0, st_v = 0;  // next chunk to score, its stage; the stage of the chunk whose P V is next
       bool ok = wait(q_full, 0);
 #pragma unroll 1
       for (int ch = ch0 - 1; ok && ch <= ch1; ++ch) {  // (the first round only scores)
@@ -421,9 +422,10 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
                (!dg || wait(&v_full[(st_v + 1) & 1], (st_v + 1) >> 1));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t o = 256 + 128 * (it & 1), p = 128 * (it & 1);
-          pv(st_v, o, p, lo8(ch), hi8(ch), true);
-          if (dg) pv(st_v + 1, o, p + 64, lo16(ch), hi16(ch), lo8(ch) >= hi8(ch));
+          const uint32_t p = 128 * (it & 1);
+          pv(st_v, p, lo8(ch), hi8(ch), true);
+          if (dg) pv(st_v + 1, p + 64, lo16(ch), hi16(ch), lo8(ch) >= hi8(ch));
+          umma_commit(o_full);
           umma_commit(&v_empty[st_v & 1]);
           if (dg) umma_commit(&v_empty[(st_v + 1) & 1]);
           st_v += dg ? 2 : 1;
@@ -440,11 +442,11 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
           umma_commit(&s_full[n & 1]);
           umma_commit(&k_empty[st_s & 1]);
           ++st_s;
-          if (dg) {  // own pages, into the columns that the chunk's O takes later
-            ok = wait(&k_full[st_s & 1], st_s >> 1) && wait(o_free, n16++);
+          if (dg) {  // own pages, into the other score buffer, which the next chunk takes later
+            ok = wait(&k_full[st_s & 1], st_s >> 1);
             if (!ok) break;
             tc_fence_after();
-            scores(st_s, 256 + 128 * (n & 1));
+            scores(st_s, 128 * (1 - (n & 1)));
             umma_commit(s16_full);
             umma_commit(&k_empty[st_s & 1]);
             ++st_s;
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
     }
   } else {
     // ---- softmax: two threads per row, of which thread h takes pages 4 h .. + 3 of a chunk and half of O's dims
-    regs_inc<216>();
+    regs_inc<232>();
     constexpr int HP = kChunkPages / C::NT, OD = HD / C::NT;
     const int h = (warp - 4) >> 2, lr = (warp & 3) * 32 + lane, row = r0 + lr;
     const bool valid = row < r_end;
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     }
-    bool ok = softmax_sync(true);
+    bool ok = softmax_sync<C::NS>(1, true);
     const float rowfac = ex_l[0][0][lr];
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     auto warp_wait = [&](uint64_t* f, int n) {
@@ -519,107 +521,222 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
     };
     // The split in hand: this thread's l and O (pairs of dims); M: the running
     // maximum at the chunk whose weights were taken last.  O of a chunk is folded
-    // two chunks later, with the factor for what is before it (0 at a split's first
-    // chunk, as what O and L hold is then of another split, and finite or NaN for
-    // good) and its l, which wait in shared memory, in a record of the thread's own.
+    // behind the next one's weights, with the factor for what is before it: 0 at a
+    // split's first chunk, as what O and L hold is then of another split, and finite
+    // or NaN for good.
     float M = -INFINITY, L = 0.f;
     uint64_t O[OD / 2];
 #pragma unroll
     for (int i = 0; i < OD / 2; ++i) O[i] = 0ull;
-    // The block's totals over the splits before (runs that hold all of them).
-    float4* totals = a.totals && d1.w >= 0 ? a.totals + (static_cast<size_t>(d1.w) * a.Hkv + kvh) * (C::ROWS * HD / 4) : nullptr;
-    const int sthread = threadIdx.x - 128;
+    const bool all = d1.w != 0;         // the run holds all of the block's splits: they are folded here
+    float2 ml = make_float2(0.f, 0.f);  // maximum and l of those before, whose O is the totals
     bool have = false;
-    rec_tot[sthread] = make_float2(0.f, 0.f);
     int st = 0, n16 = 0;
+    float alpha0 = 0.f, l0 = 0.f, M0 = 0.f;  // of the chunk before: factor, l, maximum
 #pragma unroll 1
-    for (int ch = ch0; ch <= ch1 + 2; ++ch) {
+    for (int ch = ch0; ch <= ch1 + 1; ++ch) {
       const int it = ch - ch0, pg0 = ch * kChunkPages + h * HP;  // this thread's first page
-      const uint32_t s_at = lanes + 128 * (it & 1), o_at = lanes + 256 + 128 * (it & 1);
-      const bool scored = ch <= ch1;
-      // O of chunk ch - 2 is there with the scores of ch, which were issued behind
-      // its P V; behind the last chunk there is the end of all MMAs.
-      const int pc = ch - 2, sp = pc >> 2;  // the chunk that is folded now
-      const bool split_end = (pc & 3) == 3 || pc == ch1;
-      warp_wait(scored ? &s_full[it & 1] : mma_done, scored ? it >> 1 : 0);
-      tc_fence_after();
-      if (it >= 2) {
-        constexpr int W = OD < 32 ? OD : 32;
-        const float4 r = rec[(it & 1) * C::NS + sthread];  // factor, l, maximum
-        const uint64_t al = f2(r.x, r.x);
-#pragma unroll
-        for (int c = 0; c < OD; c += W) {
-          uint32_t y[W];
-          ld_cols<W>(o_at + OD * h + c, y);
-          wait_cols<W>(y);
-#pragma unroll
-          for (int i = 0; i < W / 2; ++i) O[c / 2 + i] = f2_fma(O[c / 2 + i], al, f2(y[2 * i], y[2 * i + 1]));
+      const uint32_t s_at = lanes + 128 * (it & 1);
+      float alpha = 0.f, l_ch = 0.f;
+      if (ch <= ch1) {
+        warp_wait(&s_full[it & 1], it >> 1);
+        tc_fence_after();
+        const float4* sc = reinterpret_cast<const float4*>(scales + (st & 3) * (C::SCALES / 4)) + h * HP;
+        const float* so = scales + ((st + 1) & 3) * (C::SCALES / 4) + h * HP * 16;
+        const bool dg = diag(ch);
+        if (dg) {
+          warp_wait(s16_full, n16++);
+          tc_fence_after();
         }
-        L = __fmaf_rn(L, r.x, r.y);
-        if (split_end) {
+        st += dg ? 2 : 1;
+        // every row of the warp sees this half in 8 bits (rows that are none aside)
+        const bool full = __all_sync(0xffffffffu, !valid || (lo <= pg0 * 16 && own >= pg0 + HP));
+        float t[HP * 16];
+        float iv[HP];
+#pragma unroll
+        for (int p0 = 0; p0 < HP; p0 += 2) {
+          uint32_t x[32];
+          ld32(s_at + 16 * (HP * h + p0), x);
+          wait_ld32(x);
+#pragma unroll
+          for (int pg = p0; pg < p0 + 2; ++pg) {
+            const float4 f = sc[pg];
+            const float ks = __fmul_rn(f.x, rowfac);
+            const uint64_t k2 = f2(ks, ks), lv2 = f2(f.y, f.y);
+            iv[pg] = f.z;
+#pragma unroll
+            for (int i = pg * 16; i < pg * 16 + 16; i += 2) {
+              const uint64_t s2 = f2_fma(f2(x[i - 16 * p0], x[i - 16 * p0 + 1]), k2, lv2);
+              t[i] = f2_lo(s2);
+              t[i + 1] = f2_hi(s2);
+            }
+          }
+        }
+        if (!full) {
+#pragma unroll
+          for (int pg = 0; pg < HP; ++pg) {
+            const int page = pg0 + pg;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!(page < own && page * 16 + i >= lo)) t[pg * 16 + i] = -INFINITY;
+            if (dg && page >= own_lo && page <= own_hi) {  // some rows' own page
+              uint32_t y[16];
+              ld16(lanes + 128 * (1 - (it & 1)) + 16 * (h * HP + pg), y);
+              wait_ld16(y);
+              if (page == own) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const int key = page * 16 + i;
+                  const float v = __fmaf_rn(__uint_as_float(y[i]), __fmul_rn(so[pg * 16 + i], rowfac), so[kChunk8 + pg * 16 + i]);
+                  if (key >= lo && key <= pos) t[pg * 16 + i] = v;
+                }
+              }
+            }
+          }
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < HP * 16; i += 2) m4[(i >> 1) & 3] = fmaxf(m4[(i >> 1) & 3], fmaxf(t[i], t[i + 1]));
+        ex[it & 1][h][lr] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        ok = softmax_sync<32 * C::NT>(2 + (warp & 3), ok);  // also: every score has been read
+        if (!ok) break;
+        const bool first = (ch & 3) == 0 || it == 0;
+        if (first) M = -INFINITY;
+        float mx = ex[it & 1][0][lr];
+#pragma unroll
+        for (int k = 1; k < C::NT; ++k) mx = fmaxf(mx, ex[it & 1][k][lr]);
+        kv8_running_max(M, mx, alpha);
+        if (first) alpha = 0.f;
+        const float u = M == -INFINITY ? 0.f : M;  // no key seen so far: every score is -inf, every weight 0
+        const uint64_t u2 = f2(u, u);
+        uint64_t l[4] = {0ull, 0ull, 0ull, 0ull};  // pair t: the partial sums (t, 0) and (t, 1)
+        uint32_t pk[HP * 8];
+#pragma unroll
+        for (int i = 0; i < HP * 8; ++i) {
+          const uint64_t s2 = f2_sub(f2(t[2 * i], t[2 * i + 1]), u2);
+          t[2 * i] = ex2(f2_lo(s2));
+          t[2 * i + 1] = ex2(f2_hi(s2));
+          pk[i] = pack_f16x2(t[2 * i], t[2 * i + 1]);
+          if (full) l[i & 3] = f2_fma(f2(t[2 * i], t[2 * i + 1]), f2(iv[i >> 3], iv[i >> 3]), l[i & 3]);
+        }
+        if (!full) {
+#pragma unroll
+          for (int pg = 0; pg < HP; ++pg) {
+            const int page = pg0 + pg;
+            const bool mine = page == own;
+            if ((page < own || mine) && page * 16 + 15 >= lo) {  // (a page that the row does not see stays out, whatever its scale)
+              const float* up = so + 2 * kChunk8 + pg * 16;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                l[i & 3] = f2_fma(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]),
+                                  mine ? f2(up[2 * i], up[2 * i + 1]) : f2(iv[pg], iv[pg]), l[i & 3]);
+            }
+          }
+        }
+        if (dg) {  // the weights of own pages, 0 for the other rows, and 0 for them among the 8-bit pages
+#pragma unroll
+          for (int pg = 0; pg < HP; ++pg) {
+            const int page = pg0 + pg;
+            if (page < own_lo || page > own_hi) continue;
+            uint32_t p16[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              p16[i] = page == own ? pk[pg * 8 + i] : 0u;
+              pk[pg * 8 + i] = page == own ? 0u : pk[pg * 8 + i];
+            }
+            st8(s_at + 64 + 8 * (h * HP + pg), p16);
+          }
+        }
+        st32(s_at + 8 * HP * h, pk);
+        l_ch = __fadd_rn(__fadd_rn(__fadd_rn(f2_lo(l[0]), f2_hi(l[0])), __fadd_rn(f2_lo(l[1]), f2_hi(l[1]))),
+                         __fadd_rn(__fadd_rn(f2_lo(l[2]), f2_hi(l[2])), __fadd_rn(f2_lo(l[3]), f2_hi(l[3]))));
+      }
+      if (it > 0) {  // O of the chunk before
+        const int pc = ch - 1, sp = pc >> 2;
+        warp_wait(o_full, it - 1);
+        tc_fence_after();
+        const uint64_t al = f2(alpha0, alpha0);
+#pragma unroll
+        for (int c = 0; c < OD; c += 32) {
+          uint32_t y[32];
+          ld32(lanes + 256 + OD * h + c, y);
+          wait_ld32(y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) O[c / 2 + i] = f2_fma(O[c / 2 + i], al, f2(y[2 * i], y[2 * i + 1]));
+        }
+        L = __fmaf_rn(L, alpha0, l0);
+        if ((pc & 3) == 3 || pc == ch1) {  // the split's end
           ex_l[it & 1][h][lr] = L;
-          ok = softmax_sync(ok);
+          ok = softmax_sync<32 * C::NT>(2 + (warp & 3), ok);
           if (!ok) break;
           float x[C::NT];
 #pragma unroll
           for (int k = 0; k < C::NT; ++k) x[k] = ex_l[it & 1][k][lr];
           const float Ls = kv8_sum_parts(x);
           const bool sees = valid && max(lo, sp * kSplit8) <= min(pos, sp * kSplit8 + kSplit8 - 1);
-          if (totals) {
-            // O <- the totals with this split, in the merge kernel's arithmetic
-            float4* tot = totals + sthread;  // [4 dims][thread]
-            const bool fold_in = sees && have, load = have && (sees || pc == ch1);
-            float2 ml = rec_tot[sthread];
-            const float mn = fmaxf(ml.x, r.z), ca = ex2(__fsub_rn(ml.x, mn)), cb = ex2(__fsub_rn(r.z, mn));
-            if (load) {
-#pragma unroll
-              for (int i = 0; i < OD / 4; ++i) {
-                const float4 v = __ldcg(tot + i * C::NS);
-                // (in scalars: the packed product and sum come out as one fma, which is not what the merge kernel computes)
-                auto both = [&](float tot, float o) {
-                  return fold_in ? __fadd_rn(__fmul_rn(tot, ca), __fmul_rn(__fadd_rn(o, 0.f), cb)) : tot;
-                };
-                O[2 * i] = f2(both(v.x, f2_lo(O[2 * i])), both(v.y, f2_hi(O[2 * i])));
-                O[2 * i + 1] = f2(both(v.z, f2_lo(O[2 * i + 1])), both(v.w, f2_hi(O[2 * i + 1])));
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < OD / 2; ++i) O[i] = f2_add(O[i], 0ull);
-            }
+          if (all) {
+            // the totals with this split, in the merge kernel's arithmetic (what O holds is not needed after)
+            const bool fold_in = sees && have;
+            const float mn = fmaxf(ml.x, M0), ca = ex2(__fsub_rn(ml.x, mn)), cb = ex2(__fsub_rn(M0, mn));
+            // (in scalars: the packed product and sum come out as one fma, which is not what the merge kernel computes)
+            auto both = [&](uint32_t tot, float o) {
+              const float t = __uint_as_float(tot);
+              o = __fadd_rn(o, 0.f);
+              return fold_in ? __fadd_rn(__fmul_rn(t, ca), __fmul_rn(o, cb)) : have ? t : o;
+            };
+            const bool any = __any_sync(0xffffffffu, have), every = __all_sync(0xffffffffu, !valid || fold_in);
             if (sees) {
-              ml = have ? make_float2(mn, __fadd_rn(__fmul_rn(ml.y, ca), __fmul_rn(Ls, cb))) : make_float2(r.z, Ls);
-              rec_tot[sthread] = ml;
-              have = true;
+              ml = have ? make_float2(mn, __fadd_rn(__fmul_rn(ml.y, ca), __fmul_rn(Ls, cb))) : make_float2(M0, Ls);
             }
-            if (pc < ch1) {
-              if (sees)
+            uint4* to = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD + OD * h);
 #pragma unroll
-                for (int i = 0; i < OD / 4; ++i)
-                  __stcg(tot + i * C::NS, make_float4(f2_lo(O[2 * i]), f2_hi(O[2 * i]), f2_lo(O[2 * i + 1]), f2_hi(O[2 * i + 1])));
-            } else if (valid) {
-              uint4* to = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD + OD * h);
+            for (int c = 0; c < OD; c += 32) {
+              uint32_t y[32];
+              if (any) {
+                ld32(lanes + 384 + OD * h + c, y);
+                wait_ld32(y);
+              }
+              if (every) {
 #pragma unroll
-              for (int i = 0; i < OD / 8; ++i) {
-                uint32_t w[4];
+                for (int i = 0; i < 32; ++i) {
+                  const float o = __fadd_rn((i & 1) ? f2_hi(O[(c + i) / 2]) : f2_lo(O[(c + i) / 2]), 0.f);
+                  y[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(y[i]), ca), __fmul_rn(o, cb)));
+                }
+              } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  w[k] = pack_bf16x2(__fdiv_rn(f2_lo(O[4 * i + k]), ml.y), __fdiv_rn(f2_hi(O[4 * i + k]), ml.y));
-                to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 16; ++i) {
+                  y[2 * i] = __float_as_uint(both(y[2 * i], f2_lo(O[c / 2 + i])));
+                  y[2 * i + 1] = __float_as_uint(both(y[2 * i + 1], f2_hi(O[c / 2 + i])));
+                }
+              }
+              if (pc < ch1) {
+                st32(lanes + 384 + OD * h + c, y);
+              } else if (valid) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    w[k] = pack_bf16x2(__fdiv_rn(__uint_as_float(y[8 * i + 2 * k]), ml.y), __fdiv_rn(__uint_as_float(y[8 * i + 2 * k + 1]), ml.y));
+                  to[c / 8 + i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
               }
             }
+            have = have || sees;
+            tmem_wait_st();
           } else {
             // The split's partial.  32 dims at a time go through shared memory, so
             // that a store of the warp writes 128 bytes of each of four rows.
             if (sees && h == 0) {
               const size_t base = (static_cast<size_t>(q0 + tok) * a.Hq + hq) * a.max_splits + sp;
-              a.part_ml[base * 2] = r.z;
+              a.part_ml[base * 2] = M0;
               a.part_ml[base * 2 + 1] = Ls;
             }
             float4* buf = reinterpret_cast<float4*>(so_out) + (warp - 4) * 256;  // [row][8], the 16-byte words XORed with the row
             const unsigned rows_seen = __ballot_sync(0xffffffffu, sees);
 #pragma unroll
             for (int c = 0; c < OD; c += 32) {
-              constexpr int W = OD < 32 ? OD / 4 : 8;  // words of a row
+              constexpr int W = 8;  // words of a row
 #pragma unroll
               for (int i = 0; i < W; ++i) {
                 const uint64_t v0 = f2_add(O[c / 2 + 2 * i], 0ull), v1 = f2_add(O[c / 2 + 2 * i + 1], 0ull);
@@ -640,123 +757,14 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
           }
         }
       }
-      if (!scored) continue;
-      const float4* sc = reinterpret_cast<const float4*>(scales + (st & 3) * (C::SCALES / 4)) + h * HP;
-      const float* so = scales + ((st + 1) & 3) * (C::SCALES / 4) + h * HP * 16;
-      const bool dg = diag(ch);
-      if (dg) {
+      if (ch <= ch1) {
+        alpha0 = alpha;
+        l0 = l_ch;
+        M0 = M;
+        tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(o_free);
-        warp_wait(s16_full, n16++);
-        tc_fence_after();
+        mbar_arrive(&p_full[it & 1]);
       }
-      st += dg ? 2 : 1;
-      // every row of the warp sees this half in 8 bits (rows that are none aside)
-      const bool full = __all_sync(0xffffffffu, !valid || (lo <= pg0 * 16 && own >= pg0 + HP));
-      float t[HP * 16];
-      float iv[HP];
-#pragma unroll
-      for (int p0 = 0; p0 < HP; p0 += 2) {
-        uint32_t x[32];
-        ld32(s_at + 16 * (HP * h + p0), x);
-        wait_ld32(x);
-#pragma unroll
-        for (int pg = p0; pg < p0 + 2; ++pg) {
-          const float4 f = sc[pg];
-          const float ks = __fmul_rn(f.x, rowfac);
-          const uint64_t k2 = f2(ks, ks), lv2 = f2(f.y, f.y);
-          iv[pg] = f.z;
-#pragma unroll
-          for (int i = pg * 16; i < pg * 16 + 16; i += 2) {
-            const uint64_t s2 = f2_fma(f2(x[i - 16 * p0], x[i - 16 * p0 + 1]), k2, lv2);
-            t[i] = f2_lo(s2);
-            t[i + 1] = f2_hi(s2);
-          }
-        }
-      }
-      if (!full) {
-#pragma unroll
-        for (int pg = 0; pg < HP; ++pg) {
-          const int page = pg0 + pg;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (!(page < own && page * 16 + i >= lo)) t[pg * 16 + i] = -INFINITY;
-          if (dg && page >= own_lo && page <= own_hi) {  // some rows' own page
-            uint32_t y[16];
-            ld16(o_at + 16 * (h * HP + pg), y);
-            wait_ld16(y);
-            if (page == own) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int key = page * 16 + i;
-                const float v = __fmaf_rn(__uint_as_float(y[i]), __fmul_rn(so[pg * 16 + i], rowfac), so[kChunk8 + pg * 16 + i]);
-                if (key >= lo && key <= pos) t[pg * 16 + i] = v;
-              }
-            }
-          }
-        }
-      }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < HP * 16; i += 2) m4[(i >> 1) & 3] = fmaxf(m4[(i >> 1) & 3], fmaxf(t[i], t[i + 1]));
-      ex[it & 1][h][lr] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      ok = softmax_sync(ok);  // also: every score has been read
-      if (!ok) break;
-      const bool first = (ch & 3) == 0 || it == 0;
-      if (first) M = -INFINITY;
-      float mx = ex[it & 1][0][lr];
-#pragma unroll
-      for (int k = 1; k < C::NT; ++k) mx = fmaxf(mx, ex[it & 1][k][lr]);
-      float alpha;
-      kv8_running_max(M, mx, alpha);
-      if (first) alpha = 0.f;
-      const float u = M == -INFINITY ? 0.f : M;  // no key seen so far: every score is -inf, every weight 0
-      const uint64_t u2 = f2(u, u);
-      uint64_t l[4] = {0ull, 0ull, 0ull, 0ull};  // pair t: the partial sums (t, 0) and (t, 1)
-      uint32_t pk[HP * 8];
-#pragma unroll
-      for (int i = 0; i < HP * 8; ++i) {
-        const uint64_t s2 = f2_sub(f2(t[2 * i], t[2 * i + 1]), u2);
-        t[2 * i] = ex2(f2_lo(s2));
-        t[2 * i + 1] = ex2(f2_hi(s2));
-        pk[i] = pack_f16x2(t[2 * i], t[2 * i + 1]);
-        if (full) l[i & 3] = f2_fma(f2(t[2 * i], t[2 * i + 1]), f2(iv[i >> 3], iv[i >> 3]), l[i & 3]);
-      }
-      if (!full) {
-#pragma unroll
-        for (int pg = 0; pg < HP; ++pg) {
-          const int page = pg0 + pg;
-          const bool mine = page == own;
-          if ((page < own || mine) && page * 16 + 15 >= lo) {  // (a page that the row does not see stays out, whatever its scale)
-            const float* up = so + 2 * kChunk8 + pg * 16;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              l[i & 3] = f2_fma(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]),
-                                mine ? f2(up[2 * i], up[2 * i + 1]) : f2(iv[pg], iv[pg]), l[i & 3]);
-          }
-        }
-      }
-      if (dg) {  // the weights of own pages, 0 for the other rows, and 0 for them among the 8-bit pages
-#pragma unroll
-        for (int pg = 0; pg < HP; ++pg) {
-          const int page = pg0 + pg;
-          if (page < own_lo || page > own_hi) continue;
-          uint32_t p16[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            p16[i] = page == own ? pk[pg * 8 + i] : 0u;
-            pk[pg * 8 + i] = page == own ? 0u : pk[pg * 8 + i];
-          }
-          st8(s_at + 64 + 8 * (h * HP + pg), p16);
-        }
-      }
-      st32(s_at + 8 * HP * h, pk);
-      const float l_ch = __fadd_rn(__fadd_rn(__fadd_rn(f2_lo(l[0]), f2_hi(l[0])), __fadd_rn(f2_lo(l[1]), f2_hi(l[1]))),
-                                   __fadd_rn(__fadd_rn(f2_lo(l[2]), f2_hi(l[2])), __fadd_rn(f2_lo(l[3]), f2_hi(l[3]))));
-      rec[(it & 1) * C::NS + sthread] = make_float4(alpha, l_ch, M, 0.f);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[it & 1]);
     }
   }
   // Teardown: copies land and issued MMAs finish, then tensor memory is freed.

@@ -244,7 +244,6 @@ struct Attn8Args {
                             // among those whose splits it folds itself (-1: it leaves partials)
   const int4* chunks;       // [chunks][2]: request, chunk, image, 1: the image of its own pages; cached, all tokens, 0, 0
   uint8_t* images;          // [images][Hkv] attn8_image_bytes()
-  float4* totals;           // [such blocks][Hkv][128 rows x hd floats]
   __nv_bfloat16* out;       // [T][Hq][hd] (their rows)
   const __nv_bfloat16* open;  // the layer's first page of the bf16 pool
   const uint8_t* codes;     // the layer's first page
