@@ -265,9 +265,11 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     // What a chunk's (row block, KV head, 128 keys) units cost, in us at head dim 128:
     // 0.0095 for each of 16 rows on mma.sync; on tcgen05 0.02 for each of 128 rows and
     // as much for the keys' image, and 9 more for the launch.  (Sweep of 48 shapes, 1
-    // to 32 requests of 5 to 1024 tokens behind 0 to 8000: 1 x 64 behind 1000, 32 heads
-    // over 8, 18 against 23 us; 1 x 512 behind 0 42 against 26; 32 x 8 behind 500 to
-    // 4000 99 against 184; 9 x 77 behind up to 2500 171 against 87.)
+    // to 32 requests of 5 to 1024 tokens behind 0 to 8000, 32 heads over 8, mma.sync
+    // against tcgen05: 1 x 64 behind 1000 20 against 22 us; 1 x 512 behind 0 48 against
+    // 25; 32 x 8 behind 500 to 4000 115 against 182; 9 x 77 behind up to 2500 198 against
+    // 83.  The rule takes the faster one but for near ties and 1 x 256 behind 0, 26
+    // against 20.5.)
     double gain = 0;
     for (int i = 0; i < B; ++i) {
       const int ql = b->cu_q[i + 1] - b->cu_q[i], rows = ql * m->G, all = (b->cached_len[i] + ql + 127) / 128;
