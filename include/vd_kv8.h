@@ -80,7 +80,8 @@ int vd_kv8_unseal(vd_kv8* c, vd_kv_pool* pool, int32_t layer, int32_t n, const i
                   void* stream);
 
 /* ---- steps over the cache ----
-XX
+ * The requests of a step, one after the other: request b's new tokens are cu_q[b] ..
+ * cu_q[b + 1] - 1, at the positions from cached_len[b] on.
  * page_table[b * page_table_stride + i] is the page of the *cache* that holds
  * request b's logical page i, for the pages that are complete after the step,
  * i < (cached_len + q_len) / 16; of these the ones from cached_len / 16 on are
@@ -133,7 +134,7 @@ int vd_op_kv8_rope_kv(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, int32_t layer
 int vd_op_kv8_seal(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, int32_t layer, void* stream);
 /* Attention of the planned tokens: q, out dev bf16 [T][Hq][hd]; q has been
  * rotated, K/V of the new tokens are in the bf16 pool and the pages that the step
- * completes are sealed.  Slots of the bf16 pool behind a row's position are not
+ * completes are sealed.  q and out may not overlap (VD_ERR_INVALID_ARG).  Slots of the bf16 pool behind a row's position are not
  * seen, whatever they hold.  Sums, softmax statistics and outputs' partials are
  * float32; weights enter the product with V as fp16, at most 2^-11 of themselves
  * (or 2^-25 of the largest) off. */

@@ -93,10 +93,24 @@ int check_layer(const vd_model* m, int layer) {
 int check_pages(int n, const int* src, const int* dst, int src_pages, int dst_pages, bool across) {
   if (n < 0) return fail(VD_ERR_INVALID_ARG, "negative number of pages");
   if (n > 0 && (!src || !dst)) return fail(VD_ERR_INVALID_ARG, "null page list");
-  std::vector<unsigned char> seen(n > 0 ? dst_pages : 0, 0);
-  for (int i = 0; i < n; ++i) {
+  for (int i = 0; i < n; ++i)
     if (src[i] < 0 || src[i] >= src_pages || dst[i] < 0 || dst[i] >= dst_pages)
       return fail(VD_ERR_OUT_OF_RANGE, "page id out of range");
+  // A mark per page, or for few pages of many the sorted list: 3 of a million 0.04 us
+  // instead of 28, 448 of a million 10.5 instead of 27, 448 of 65536 9.6 where the
+  // marks take 1.5.
+  if (n < dst_pages / 2048) {
+    std::vector<int> sorted(dst, dst + n);
+    std::sort(sorted.begin(), sorted.end());
+    if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end())
+      return fail(VD_ERR_INVALID_ARG, "a page is written twice");
+    for (int i = 0; across && i < n; ++i)
+      if (std::binary_search(sorted.begin(), sorted.end(), src[i]))
+        return fail(VD_ERR_INVALID_ARG, "a page is both a source and a destination");
+    return VD_OK;
+  }
+  std::vector<unsigned char> seen(n > 0 ? dst_pages : 0, 0);
+  for (int i = 0; i < n; ++i) {
     if (seen[dst[i]]) return fail(VD_ERR_INVALID_ARG, "a page is written twice");
     seen[dst[i]] = 1;
   }
@@ -380,7 +394,13 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     VD_CUDA_TRY(cudaMallocHost(reinterpret_cast<void**>(&t->host[slot]), off * 2 * sizeof(int)));
     t->host_cap[slot] = off * 2;
   }
-  const size_t rows = static_cast<size_t>(T) * c.n_heads * splits;
+  // Partials, of the tokens from the first to the last that the merge kernel folds
+  // (a long prompt's blocks fold most of their own).
+  int part0 = T, part1 = 0;
+  for (const std::vector<int>& list : merge)
+    for (const int t : list) part0 = std::min(part0, t), part1 = std::max(part1, t + 1);
+  const size_t per_token = static_cast<size_t>(c.n_heads) * splits;
+  const size_t rows = part1 > part0 ? (part1 - part0) * per_token : 0, skip = part1 > part0 ? part0 * per_token : 0;
   const size_t images = static_cast<size_t>(n_images) * c.n_kv_heads * attn8_image_bytes(c.head_dim);
   int rc;
   if (off > t->dev_cap || rows * (c.head_dim + 2) > t->part_cap || images > t->images_cap)
@@ -415,8 +435,11 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   for (int k = 0; k < 2; ++k) std::copy(merge[k].begin(), merge[k].end(), h + d.merge_list[k]);
   d.images = t->images;
   d.base = t->dev;
-  d.part_o = t->part;
-  d.part_ml = t->part + rows * c.head_dim;
+  auto at_token0 = [](float* p, size_t floats) {  // (lies before the buffer; its tokens are in it)
+    return reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(p) - floats * sizeof(float));
+  };
+  d.part_o = at_token0(t->part, skip * c.head_dim);
+  d.part_ml = at_token0(t->part + rows * c.head_dim, skip * 2);
   d.kv8 = cache;
   t->planned = false;  // until the new plan is on its way
   VD_CUDA_TRY(cudaMemcpyAsync(t->dev, h, off * sizeof(int), cudaMemcpyHostToDevice, s));
@@ -638,6 +661,10 @@ int vd_op_kv8_attention(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, int32_t lay
   if (p->d.T == 0) return VD_OK;
   if (!q || !out) return fail(VD_ERR_INVALID_ARG, "null argument");
   if (!aligned16(q) || !aligned16(out)) return fail(VD_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
+  const size_t bytes = static_cast<size_t>(p->d.T) * p->m->cfg.n_heads * p->m->cfg.head_dim * 2;
+  if (qa < oa + bytes && oa < qa + bytes)  // (blocks that write their rows' outputs run beside blocks that read queries)
+    return fail(VD_ERR_INVALID_ARG, "q and out overlap");
   return run_kv8_attention(p->m, pool, layer, p->d, static_cast<const __nv_bfloat16*>(q),
                            static_cast<__nv_bfloat16*>(out), s);
 }

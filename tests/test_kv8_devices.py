@@ -1,0 +1,61 @@
+"""Calls over the 8-bit cache refuse tensors on different GPUs, and closed objects, before they reach the library
+(stand-ins for tensors: no GPU needed)."""
+
+import pytest
+import torch
+
+from invariant_vd_step_gb300 import vd
+from test_tree_devices import OnGpu
+
+
+def plan_without_library(monkeypatch):
+    class NoLibrary:
+        def __getattr__(self, name):
+            def call(*a):
+                raise AssertionError(f"{name} reached")
+            return call
+    monkeypatch.setattr(vd, "lib", NoLibrary)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(vd, "_current_raw_stream", lambda device: 0)
+    plan = object.__new__(vd.KV8Plan)
+    spec = type("Spec", (), dict(n_heads=4, head_dim=64, qkv_dim=512, vocab=100))
+    plan.h, plan.model = 1, type("M", (), dict(h=1, spec=spec))()
+    plan.num_tokens, plan.num_logit_rows = 3, 3
+    other = lambda h=1: type("P", (), dict(h=h, model=plan.model))()  # noqa: E731
+    return plan, other
+
+
+def refused(calls):
+    for i, call in enumerate(calls):
+        with pytest.raises(vd.VDError) as e:
+            call()
+            pytest.fail(f"call {i} was taken")
+        assert e.value.code == vd.VD_ERR_INVALID_ARG
+
+
+def test_tensors_on_two_gpus_are_refused(monkeypatch):
+    plan, other = plan_without_library(monkeypatch)
+    q = [OnGpu((3, 4, 64), torch.bfloat16, d) for d in (0, 1)]
+    qkv = [OnGpu((3, 512), torch.bfloat16, d) for d in (0, 1)]
+    try:
+        refused([lambda: plan.attention(other(), other(), 0, q[1], q[0]),
+                 lambda: plan.attention(other(), other(), 0, q[0], q[1]),
+                 lambda: plan.attention(other(), other(), 0, q[1], q[1]),  # not the current device
+                 lambda: plan.rope_kv(other(), other(), 0, qkv[1], q[0]),
+                 lambda: plan.rope_kv(other(), other(), 0, qkv[0], q[1]),
+                 lambda: plan.step(other(), other(), OnGpu((3, 100), torch.float32, 1))])
+    finally:
+        plan.h = None  # nothing for close() to destroy
+
+
+def test_closed_objects_are_refused(monkeypatch):
+    plan, other = plan_without_library(monkeypatch)
+    q = OnGpu((3, 4, 64), torch.bfloat16, 0)
+    try:
+        refused([lambda: plan.attention(other(None), other(), 0, q, OnGpu((3, 4, 64), torch.bfloat16, 0)),
+                 lambda: plan.attention(other(), other(None), 0, q, OnGpu((3, 4, 64), torch.bfloat16, 0)),
+                 lambda: plan.seal(other(None), other(), 0), lambda: plan.seal(other(), other(None), 0)])
+        plan.model.h = None
+        refused([lambda: plan.seal(other(), other(), 0)])
+    finally:
+        plan.h = None
