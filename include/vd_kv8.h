@@ -121,8 +121,8 @@ void vd_destroy_kv8_plan(vd_kv8_plan* p);
 int vd_kv8_plan_make(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, const vd_kv8_batch* b, void* stream);
 
 /* Kernel of the chunks of more than 16 rows (q_len * Hq / Hkv) in the plans made
- * after the call: 0 (default) chosen by their sizes, 1 mma.sync, 2 tcgen05 where the
- * head dimension is at most 128.  The same bits either way.  (A model set to
+ * after the call: 0 (default) chosen by their sizes, 1 mma.sync, 2 tcgen05.  The
+ * same bits either way.  (A model set to
  * mma.sync by vd_set_attention_prefill takes that.)  Errors: VD_ERR_INVALID_ARG. */
 int vd_kv8_set_prefill(vd_kv8_plan* p, int32_t kernel);
 

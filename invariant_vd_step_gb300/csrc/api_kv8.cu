@@ -275,15 +275,16 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   std::vector<int> blocks[6];
   const bool windowed = c.sliding_window > 0 && c.local_global_period > 0;
   std::vector<unsigned char> tc(B, 0);
-  if (m->prefill_kernel == 0 && t->prefill != 1 && c.head_dim <= 128) {
+  if (m->prefill_kernel == 0 && t->prefill != 1) {
     // What a chunk's (row block, KV head, 128 keys) units cost, in us at head dim 128:
     // 0.0095 for each of 16 rows on mma.sync; on tcgen05 0.02 for each of 128 rows and
     // as much for the keys' image, and 9 more for the launch.  (Sweep of 48 shapes, 1
     // to 32 requests of 5 to 1024 tokens behind 0 to 8000, 32 heads over 8, mma.sync
     // against tcgen05: 1 x 64 behind 1000 20 against 22 us; 1 x 512 behind 0 48 against
     // 25; 32 x 8 behind 500 to 4000 115 against 182; 9 x 77 behind up to 2500 198 against
-    // 83.  The rule takes the faster one but for near ties and 1 x 256 behind 0, 26
-    // against 20.5.)
+    // 83; 8 heads over 4 of 256: 1 x 512 behind 4000 207 against 89, 32 x 32 behind 100 to
+    // 1000 86 against 101.  The rule takes the faster one but for near ties and, 32 heads
+    // over 8, 1 x 256 behind 0, 26 against 20.5.)
     double gain = 0;
     for (int i = 0; i < B; ++i) {
       const int ql = b->cu_q[i + 1] - b->cu_q[i], rows = ql * m->G, all = (b->cached_len[i] + ql + 127) / 128;
@@ -312,7 +313,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
         chunks[local].insert(chunks[local].end(), {i, ch, image0[i] + all + ch - cached / 128, 1, cached, kv, 0, 0});
     }
     n_images += 2 * all - cached / 128;
-    if (n_images * c.n_kv_heads > 0x7fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
+    if (n_images * c.n_kv_heads > 0x3fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
   }
   // Of the tcgen05 row blocks, as many as fill the SMs in whole rounds take all of
   // their splits and need no merge; those of the last, partial round are cut into
@@ -341,11 +342,11 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
         for (int k = 0; k < n; ++k) to.insert(to.end(), {i, q0, ql, cached, first + k, r0, 0, 0});
       }
     }
-    const int n_rb = static_cast<int>(rb.size()), Hkv = c.n_kv_heads;
-    int direct = static_cast<int>(static_cast<long long>(n_rb) * Hkv / m->n_sm * m->n_sm / Hkv);
+    const int n_rb = static_cast<int>(rb.size()), ctas = c.n_kv_heads * (c.head_dim > 128 ? 2 : 1);  // CTAs of a row block
+    int direct = static_cast<int>(static_cast<long long>(n_rb) * ctas / m->n_sm * m->n_sm / ctas);
     while (direct < n_rb && direct > 0 && rb[direct].second % m->G) --direct;
     // runs that the others are cut into: as many as SMs
-    const int parts_of = n_rb > direct ? std::max(1, m->n_sm / ((n_rb - direct) * Hkv)) : 1;
+    const int parts_of = n_rb > direct ? std::max(1, m->n_sm / ((n_rb - direct) * ctas)) : 1;
     for (int j = 0; j < n_rb; ++j) {
       const int i = rb[j].first, r0 = rb[j].second, q0 = b->cu_q[i], ql = b->cu_q[i + 1] - q0, rows = ql * m->G;
       int first;

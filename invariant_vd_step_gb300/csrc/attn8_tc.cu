@@ -1,5 +1,5 @@
 // Attention over the 8-bit KV cache for long row blocks: 5th-generation tensor
-// cores (tcgen05), head dimensions 64 and 128.
+// cores (tcgen05).
 //
 // The rows, pages, chunks and splits, the arithmetic of a row and its order are
 // those of attn8.cu (its header has the formulas), bit for bit: a tcgen05 K = 16
@@ -25,6 +25,12 @@
 // global memory, two O buffers and one barrier of all softmax threads (the two of a
 // row need only each other); 447 with the folding in four warps of its own, which
 // became what the others waited for; 414 with 216 registers (spills), 232 now.
+//
+// Head dimension 256: a row block is two CTAs, each with all of the scores and half
+// of the dims of V and O, so that tensor memory and registers hold what they hold at
+// 128; K comes in two units of 128 dims.  512 tokens behind 4000, 8 heads over 4: 89 us
+// where mma.sync takes 207.  (One unit of 256 dims, without a second one in flight:
+// the same.)
 //
 // The operands are made once per launch, not once per row block: an expanding
 // kernel turns every chunk of the launch's requests into an image of the two
@@ -54,18 +60,23 @@ struct Tc8Cfg {
   static constexpr int ROWS = 128;
   static constexpr int Q_BYTES = ROWS * HD * 2;     // [hd block][row][64]
   static constexpr int K_BYTES = kChunk8 * HD * 2;  // [hd block][key][64]
-  static constexpr int V_BYTES = kChunk8 * HD * 2;  // [key block][dim][64]
-  static constexpr int STAGES = 2;
+  static constexpr int VD = HD < 128 ? HD : 128;    // dims of a block's O
+  static constexpr int HALVES = HD / VD;            // blocks that share a row block's scores, each with VD of the dims
+  static constexpr int V_BYTES = kChunk8 * VD * 2;  // [key block][dim][64]
+  static constexpr int KU = HALVES;                 // units that K is copied in: of at most 128 dims
+  static constexpr int KU_BYTES = K_BYTES / KU;
+  static constexpr int STAGES = 2;                  // of K's units, and of V
   static constexpr int SCALES = kChunk8 * 3 * 4;    // per stage: 8 pages or 128 tokens x (K scale, log2 of V's, 1 / V's)
   static constexpr int SC_RING = 4;
   static constexpr int NT = kChunkParts;  // softmax threads per row
   static constexpr int NS = 128 * NT;
-  static constexpr int OUT_BYTES = 4 * NT * 32 * 128;  // per softmax warp: 32 rows x 32 dims of float32
-  static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + OUT_BYTES + SC_RING * SCALES + 256;
+  static constexpr int OUT_DIMS = HD <= 128 ? 32 : 16;
+  static constexpr int OUT_BYTES = 4 * NT * 32 * OUT_DIMS * 4;  // per softmax warp: 32 rows x OUT_DIMS of float32
+  static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (KU_BYTES + V_BYTES) + OUT_BYTES + SC_RING * SCALES + 256;
   static constexpr int TMEM_COLS = 512;  // chunk c: scores (then weights) from 128 (c % 2), O from 256; the totals from 384
   static constexpr int THREADS = 128 + NS;
-  // A chunk's image: K tile, V tile, scales
-  static constexpr int IMAGE = K_BYTES + V_BYTES + SCALES;
+  // A chunk's image: K tile, V tiles, scales
+  static constexpr int IMAGE = K_BYTES + HALVES * V_BYTES + SCALES;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -179,19 +190,21 @@ __device__ __forceinline__ bool softmax_sync(int id, bool ok) {
   return bad == 0;
 }
 
-// Images of chunks: one block per (chunk, KV head), a warp per page.  A lane's
+// Images of chunks: one block per (chunk, KV head, K or V), a warp per page.  A lane's
 // operand words (kv8.cuh) become two 4-byte pieces of rows of the tiles, which
-// leave shared memory in whole 16-byte words.  Bound by memory: 32 KB of codes in
-// and 64 KB of fp16 out per block at hd 128.
+// leave shared memory in whole 16-byte words.  Bound by the latency of its pages: 16
+// KB of codes in and 32 KB of fp16 out per block at hd 128, 512 such blocks a request
+// of 4096 keys and 8 KV heads.
 template <int HD, int FMT>
-__global__ void __launch_bounds__(256) attn8_expand_kernel(Attn8Args a) {
+__global__ void __launch_bounds__(256, HD <= 128 ? 5 : 3) attn8_expand_kernel(Attn8Args a) {
   using C = Tc8Cfg<HD>;
   constexpr int UNITS = Kv8Cfg<HD>::UNITS, PART = Kv8Cfg<HD>::PART;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int pg = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int kvh = blockIdx.x % a.Hkv;
-  const int4 d = a.chunks[2 * (blockIdx.x / a.Hkv)], e = a.chunks[2 * (blockIdx.x / a.Hkv) + 1];
+  const int v = blockIdx.x & 1, block_of = blockIdx.x >> 1;  // K or V
+  const int kvh = block_of % a.Hkv;
+  const int4 d = a.chunks[2 * (block_of / a.Hkv)], e = a.chunks[2 * (block_of / a.Hkv) + 1];
   const int b = d.x, ch = d.y, image = d.z, cached = e.x, kv_len = e.y;
   const bool own = d.w != 0;  // the image of the chunk's own pages
   const int page = ch * kChunkPages + pg;
@@ -201,17 +214,15 @@ __global__ void __launch_bounds__(256) attn8_expand_kernel(Attn8Args a) {
                         : a.page_table[static_cast<size_t>(b) * a.pt_stride + page];
   pdl_wait();
   pdl_trigger();
-  uint8_t *sk = smem, *sv = sk + C::K_BYTES;
-  float* sc = reinterpret_cast<float*>(sv + C::V_BYTES);
+  static_assert(C::K_BYTES == C::HALVES * C::V_BYTES, "K's tile or V's");
+  float* sc = reinterpret_cast<float*>(smem + C::K_BYTES);
   if (!own) {
     const size_t block = static_cast<size_t>(pid) * a.Hkv + kvh;
     const uint4* src = reinterpret_cast<const uint4*>(a.codes + block * (2 * PART)) + lane;
-    uint4 w[2][UNITS];
+    uint4 w[UNITS];
 #pragma unroll
-    for (int v = 0; v < 2; ++v)
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) w[v][u] = in ? __ldcg(src + v * (PART / 16) + u * 32) : make_uint4(0u, 0u, 0u, 0u);
-    if (lane == 0) {
+    for (int u = 0; u < UNITS; ++u) w[u] = in ? __ldcg(src + v * (PART / 16) + u * 32) : make_uint4(0u, 0u, 0u, 0u);
+    if (v == 0 && lane == 0) {
       const float4 f = in ? __ldcg(a.scales + block) : make_float4(0.f, 0.f, 0.f, 0.f);
       *reinterpret_cast<float4*>(sc + pg * 4) = make_float4(f.x, f.z, f.y, 0.f);
     }
@@ -223,83 +234,85 @@ __global__ void __launch_bounds__(256) attn8_expand_kernel(Attn8Args a) {
       sts32(at0, lo);
       sts32(at1, hi);
     };
-    const uint32_t kb = smem_u32(sk) + pg * (16 * 128);
+    if (v == 0) {
+      const uint32_t kb = smem_u32(smem) + pg * (16 * 128);
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) {  // k-steps 2 u and 2 u + 1 of key blocks 0 and 1
-      const int k = (u & 1) * 4, at = (u >> 1) * (kChunk8 * 128);
-      put(kb + at + col(k), kb + at + col(k + 1), w[0][u].x);
-      put(kb + at + 8 * 128 + col(k), kb + at + 8 * 128 + col(k + 1), w[0][u].y);
-      put(kb + at + col(k + 2), kb + at + col(k + 3), w[0][u].z);
-      put(kb + at + 8 * 128 + col(k + 2), kb + at + 8 * 128 + col(k + 3), w[0][u].w);
-    }
-    // this page's 16 keys are columns 2 (page % 4) and + 1 of its key block
-    const uint32_t vb = smem_u32(sv) + (pg >> 2) * (HD * 128), c0 = vb + col((pg & 3) * 2), c1 = vb + col((pg & 3) * 2 + 1);
+      for (int u = 0; u < UNITS; ++u) {  // k-steps 2 u and 2 u + 1 of key blocks 0 and 1
+        const int k = (u & 1) * 4, at = (u >> 1) * (kChunk8 * 128);
+        put(kb + at + col(k), kb + at + col(k + 1), w[u].x);
+        put(kb + at + 8 * 128 + col(k), kb + at + 8 * 128 + col(k + 1), w[u].y);
+        put(kb + at + col(k + 2), kb + at + col(k + 3), w[u].z);
+        put(kb + at + 8 * 128 + col(k + 2), kb + at + 8 * 128 + col(k + 3), w[u].w);
+      }
+    } else {
+      // this page's 16 keys are columns 2 (page % 4) and + 1 of its key block
+      const uint32_t vb = smem_u32(smem) + (pg >> 2) * (C::VD * 128), c0 = vb + col((pg & 3) * 2), c1 = vb + col((pg & 3) * 2 + 1);
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) {  // dims 32 u .. + 31
-      const int at = 32 * u * 128;
-      put(c0 + at, c1 + at, w[1][u].x);
-      put(c0 + at + 8 * 128, c1 + at + 8 * 128, w[1][u].y);
-      put(c0 + at + 16 * 128, c1 + at + 16 * 128, w[1][u].z);
-      put(c0 + at + 24 * 128, c1 + at + 24 * 128, w[1][u].w);
+      for (int u = 0; u < UNITS; ++u) {  // dims 32 u .. + 31
+        const int at = 32 * u / C::VD * C::V_BYTES + 32 * u % C::VD * 128;
+        put(c0 + at, c1 + at, w[u].x);
+        put(c0 + at + 8 * 128, c1 + at + 8 * 128, w[u].y);
+        put(c0 + at + 16 * 128, c1 + at + 16 * 128, w[u].z);
+        put(c0 + at + 24 * 128, c1 + at + 24 * 128, w[u].w);
+      }
     }
   } else {
     // The own pages in bf16, eight tokens at a time, four lanes a token; zeros behind
     // the last token and in other pages.  The scales of a token that is not finite are
     // NaN, and its V counts as 0 (its weight is NaN, or 0 where it is not seen).
+    const __nv_bfloat16* src = a.open + ((static_cast<size_t>(pid) * 2 + v) * a.Hkv + kvh) * PART + t4 * (HD / 4);
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const __nv_bfloat16* src = a.open + ((static_cast<size_t>(pid) * 2 + v) * a.Hkv + kvh) * PART + t4 * (HD / 4);
+    for (int token = g; token < 16; token += 8) {
+      const int key = pg * 16 + token;
+      const bool have = in && page * 16 + token < kv_len;
+      uint4 y[HD / 32];
+      uint32_t mx = 0u;
 #pragma unroll
-      for (int token = g; token < 16; token += 8) {
-        const int key = pg * 16 + token;
-        const bool have = in && page * 16 + token < kv_len;
-        uint4 y[HD / 32];
-        uint32_t mx = 0u;
+      for (int i = 0; i < HD / 32; ++i)
+        y[i] = have ? __ldcg(reinterpret_cast<const uint4*>(src + token * HD) + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int i = 0; i < HD / 32; ++i)
-          y[i] = have ? __ldcg(reinterpret_cast<const uint4*>(src + token * HD) + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < HD / 32; ++i)
-          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
-                                     __vmaxu2(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu)));
-        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int ex = kv8_exp(kv8_max_halves(mx));
-        const float up = kv8_up(ex);
-        if (t4 == 0) {
-          if (v == 0) {
-            sc[key] = ex == 255 ? kv8_nan() : kv8_down(ex);
-          } else {
-            sc[kChunk8 + key] = ex == 255 ? kv8_nan() : kv8_log2_down(ex);
-            sc[2 * kChunk8 + key] = up;
-          }
+      for (int i = 0; i < HD / 32; ++i)
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
+                                   __vmaxu2(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu)));
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int ex = kv8_exp(kv8_max_halves(mx));
+      const float up = kv8_up(ex);
+      if (t4 == 0) {
+        if (v == 0) {
+          sc[key] = ex == 255 ? kv8_nan() : kv8_down(ex);
+        } else {
+          sc[kChunk8 + key] = ex == 255 ? kv8_nan() : kv8_log2_down(ex);
+          sc[2 * kChunk8 + key] = up;
         }
+      }
 #pragma unroll
-        for (int i = 0; i < HD / 32; ++i) {
-          const uint32_t x[4] = {kv8_to_f16(y[i].x, up), kv8_to_f16(y[i].y, up), kv8_to_f16(y[i].z, up), kv8_to_f16(y[i].w, up)};
-          const int dim = t4 * (HD / 4) + i * 8;  // .. + 7
-          if (v == 0) {
-            *reinterpret_cast<uint4*>(sk + (dim >> 6) * (kChunk8 * 128) + key * 128 + ((((dim >> 3) & 7) ^ (key & 7)) << 4)) =
-                make_uint4(x[0], x[1], x[2], x[3]);
-          } else {
-            uint8_t* to = sv + (key >> 6) * (HD * 128) + (key & 7) * 2 + dim * 128;
+      for (int i = 0; i < HD / 32; ++i) {
+        const uint32_t x[4] = {kv8_to_f16(y[i].x, up), kv8_to_f16(y[i].y, up), kv8_to_f16(y[i].z, up), kv8_to_f16(y[i].w, up)};
+        const int dim = t4 * (HD / 4) + i * 8;  // .. + 7
+        if (v == 0) {
+          *reinterpret_cast<uint4*>(smem + (dim >> 6) * (kChunk8 * 128) + key * 128 + ((((dim >> 3) & 7) ^ (key & 7)) << 4)) =
+              make_uint4(x[0], x[1], x[2], x[3]);
+        } else {
+          uint8_t* to = smem + dim / C::VD * C::V_BYTES + (key >> 6) * (C::VD * 128) + (key & 7) * 2 + dim % C::VD * 128;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)  // (dim % 8 = 0)
-              *reinterpret_cast<uint16_t*>(to + k * 128 + ((((key >> 3) & 7) ^ k) << 4)) =
-                  ex == 255 ? static_cast<uint16_t>(0) : static_cast<uint16_t>(x[k >> 1] >> (16 * (k & 1)));
-          }
+          for (int k = 0; k < 8; ++k)  // (dim % 8 = 0)
+            *reinterpret_cast<uint16_t*>(to + k * 128 + ((((key >> 3) & 7) ^ k) << 4)) =
+                ex == 255 ? static_cast<uint16_t>(0) : static_cast<uint16_t>(x[k >> 1] >> (16 * (k & 1)));
         }
       }
     }
   }
   __syncthreads();
-  uint4* to = reinterpret_cast<uint4*>(a.images + (static_cast<size_t>(image) * a.Hkv + kvh) * C::IMAGE);
+  uint8_t* image_at = a.images + (static_cast<size_t>(image) * a.Hkv + kvh) * C::IMAGE;
+  uint4* to = reinterpret_cast<uint4*>(image_at + v * C::K_BYTES);
   const uint4* from = reinterpret_cast<const uint4*>(smem);
-  constexpr int TILES = (C::K_BYTES + C::V_BYTES) / 16;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < TILES; i += 256) to[i] = from[i];
-  for (int i = TILES + threadIdx.x; i < C::IMAGE / 16; i += 256)
-    if (own || i < TILES + kChunkPages) to[i] = from[i];  // (an 8-bit chunk's scales end there)
+  for (int i = threadIdx.x; i < C::K_BYTES / 16; i += 256) to[i] = from[i];
+  // scales: of an 8-bit chunk's pages, by K's block; of own tokens K's, then V's two
+  const int s0 = own && v ? kChunk8 / 4 : 0, s1 = !own ? (v ? 0 : kChunkPages) : v ? C::SCALES / 16 : kChunk8 / 4;
+  to = reinterpret_cast<uint4*>(image_at + 2 * C::K_BYTES);
+  for (int i = s0 + threadIdx.x; i < s1; i += 256) to[i] = reinterpret_cast<const uint4*>(sc)[i];
 }
 
 // Item: its request's first image (of chunk 0; those of the own pages' chunks
@@ -311,8 +324,8 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
-  uint8_t* sk = sq + C::Q_BYTES;                   // K of stage s at sk + (s % 2) * K_BYTES
-  uint8_t* sv = sk + C::STAGES * C::K_BYTES;
+  uint8_t* sk = sq + C::Q_BYTES;                   // unit u of K (KU per stage) at sk + (u % 2) * KU_BYTES; V of stage s at sv + (s % 2) * V_BYTES
+  uint8_t* sv = sk + C::STAGES * C::KU_BYTES;
   uint8_t* so_out = sv + C::STAGES * C::V_BYTES;
   float* scales = reinterpret_cast<float*>(so_out + C::OUT_BYTES);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scales) + C::SC_RING * C::SCALES);
@@ -332,8 +345,9 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ int skip;
-  const int kvh = blockIdx.x % a.Hkv;
-  const int4 d0 = a.items[2 * (blockIdx.x / a.Hkv)], d1 = a.items[2 * (blockIdx.x / a.Hkv) + 1];
+  const int half = blockIdx.x % C::HALVES, block_of = blockIdx.x / C::HALVES;
+  const int kvh = block_of % a.Hkv;
+  const int4 d0 = a.items[2 * (block_of / a.Hkv)], d1 = a.items[2 * (block_of / a.Hkv) + 1];
   const int image0 = d0.x, q0 = d0.y, qlen = d0.z, cached = d0.w, sp0 = d1.x, r0 = d1.y, sp1 = d1.z;
   const int G = a.Hq / a.Hkv, rows = qlen * G, kv_len = cached + qlen;
   const int r_end = min(rows, r0 + C::ROWS);
@@ -378,26 +392,35 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   auto lo16 = [&](int ch) { return max(0, own_lo - ch * kChunkPages); };
   auto hi16 = [&](int ch) { return min(kChunkPages, own_hi + 1 - ch * kChunkPages); };
 
-  int issued_k = 0, issued_v = 0;  // stages whose copies have been issued (the copying thread's)
+  int issued_k = 0, issued_v = 0;  // units of K and stages of V whose copies have been issued (the copying thread's)
   if (warp < 4) {
     regs_dec<40>();
     if (warp == 0 && lane == 0) {
-      const uint32_t id_s = idesc_f16(128, kChunk8), id_pv = idesc_f16(128, HD);
+      const uint32_t id_s = idesc_f16(128, kChunk8), id_pv = idesc_f16(128, C::VD);
       const uint32_t q_lo = sw128_desc_lo(smem_u32(sq)), k_lo = sw128_desc_lo(smem_u32(sk)), v_lo = sw128_desc_lo(smem_u32(sv));
       auto wait = [&](uint64_t* f, int n) { return mbar_wait(f, n & 1, abort_flag, a.status); };
-      // scores against the K of stage st into columns `col`
-      auto scores = [&](int st, uint32_t col) {
-        const uint32_t k = k_lo + (st & 1) * (C::K_BYTES >> 4);
+      // scores against the K of stage st into columns `col`, unit by unit
+      auto scores = [&](int st, uint32_t col) -> bool {
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-          umma_bf16_lo(tmem + col, q_lo + (kk >> 2) * (C::ROWS * 128 >> 4) + 2 * (kk & 3),
-                       k + (kk >> 2) * (kChunk8 * 128 >> 4) + 2 * (kk & 3), id_s, kk ? 1u : 0u);
+        for (int part = 0; part < C::KU; ++part) {
+          const int u = st * C::KU + part;
+          if (!wait(&k_full[u & 1], u >> 1)) return false;
+          tc_fence_after();
+          const uint32_t k = k_lo + (u & 1) * (C::KU_BYTES >> 4);
+          const uint32_t q = q_lo + part * (C::Q_BYTES / C::KU >> 4);
+#pragma unroll
+          for (int kk = 0; kk < KK / C::KU; ++kk)
+            umma_bf16_lo(tmem + col, q + (kk >> 2) * (C::ROWS * 128 >> 4) + 2 * (kk & 3),
+                         k + (kk >> 2) * (kChunk8 * 128 >> 4) + 2 * (kk & 3), id_s, part || kk ? 1u : 0u);
+          umma_commit(&k_empty[u & 1]);
+        }
+        return true;
       };
       // O += weights of pages [x0, x1) in columns `p` times the V of stage st; first: from zero
       auto pv = [&](int st, uint32_t p, int x0, int x1, bool first) {
         const uint32_t v = v_lo + (st & 1) * (C::V_BYTES >> 4);
         auto one = [&](int x, uint32_t add) {
-          umma_bf16_ta(tmem + 256, tmem + p + 8 * x, v + (x >> 2) * (HD * 128 >> 4) + 2 * (x & 3), id_pv, add);
+          umma_bf16_ta(tmem + 256, tmem + p + 8 * x, v + (x >> 2) * (C::VD * 128 >> 4) + 2 * (x & 3), id_pv, add);
         };
         if (first && x0 == 0 && x1 == kChunkPages) {
 #pragma unroll
@@ -435,21 +458,13 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
           const bool dg = diag(ns);
           if (ns > ch + 1 && (dg || (ns > ch0 && diag(ns - 1)))) break;
           const int n = ns - ch0;
-          ok = wait(&k_full[st_s & 1], st_s >> 1);
+          ok = scores(st_s++, 128 * (n & 1));
           if (!ok) break;
-          tc_fence_after();
-          scores(st_s, 128 * (n & 1));
           umma_commit(&s_full[n & 1]);
-          umma_commit(&k_empty[st_s & 1]);
-          ++st_s;
           if (dg) {  // own pages, into the other score buffer, which the next chunk takes later
-            ok = wait(&k_full[st_s & 1], st_s >> 1);
+            ok = scores(st_s++, 128 * (1 - (n & 1)));
             if (!ok) break;
-            tc_fence_after();
-            scores(st_s, 128 * (1 - (n & 1)));
             umma_commit(s16_full);
-            umma_commit(&k_empty[st_s & 1]);
-            ++st_s;
           }
           ++ns;
         }
@@ -462,15 +477,19 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       int st = 0;
       auto stage = [&](int image) -> bool {
         const uint8_t* src = a.images + (static_cast<size_t>(image) * a.Hkv + kvh) * C::IMAGE;
-        const int s2 = st & 1, k = (st >> 1) - 1;
-        if (st >= 2 && !wait(&k_empty[s2], k)) return false;
-        mbar_arrive_expect_tx(&k_full[s2], C::K_BYTES + C::SCALES);
-        bulk_load(sk + s2 * C::K_BYTES, src, C::K_BYTES, &k_full[s2]);
-        bulk_load(scales + (st & 3) * (C::SCALES / 4), src + C::K_BYTES + C::V_BYTES, C::SCALES, &k_full[s2]);
-        issued_k = st + 1;
-        if (st >= 2 && !wait(&v_empty[s2], k)) return false;
+        const int s2 = st & 1;
+#pragma unroll
+        for (int part = 0; part < C::KU; ++part) {
+          const int u = st * C::KU + part;
+          if (u >= 2 && !wait(&k_empty[u & 1], (u >> 1) - 1)) return false;
+          mbar_arrive_expect_tx(&k_full[u & 1], C::KU_BYTES + (part ? 0 : C::SCALES));
+          bulk_load(sk + (u & 1) * C::KU_BYTES, src + part * C::KU_BYTES, C::KU_BYTES, &k_full[u & 1]);
+          if (part == 0) bulk_load(scales + (st & 3) * (C::SCALES / 4), src + 2 * C::K_BYTES, C::SCALES, &k_full[u & 1]);
+          issued_k = u + 1;
+        }
+        if (st >= 2 && !wait(&v_empty[s2], (st >> 1) - 1)) return false;
         mbar_arrive_expect_tx(&v_full[s2], C::V_BYTES);
-        bulk_load(sv + s2 * C::V_BYTES, src + C::K_BYTES, C::V_BYTES, &v_full[s2]);
+        bulk_load(sv + s2 * C::V_BYTES, src + C::K_BYTES + half * C::V_BYTES, C::V_BYTES, &v_full[s2]);
         issued_v = ++st;
         return true;
       };
@@ -481,7 +500,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   } else {
     // ---- softmax: two threads per row, of which thread h takes pages 4 h .. + 3 of a chunk and half of O's dims
     regs_inc<232>();
-    constexpr int HP = kChunkPages / C::NT, OD = HD / C::NT;
+    constexpr int HP = kChunkPages / C::NT, OD = C::VD / C::NT;
     const int h = (warp - 4) >> 2, lr = (warp & 3) * 32 + lane, row = r0 + lr;
     const bool valid = row < r_end;
     const int tok = valid ? row / G : 0, hq = kvh * G + (valid ? row % G : 0);
@@ -688,7 +707,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
             if (sees) {
               ml = have ? make_float2(mn, __fadd_rn(__fmul_rn(ml.y, ca), __fmul_rn(Ls, cb))) : make_float2(M0, Ls);
             }
-            uint4* to = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD + OD * h);
+            uint4* to = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD + half * C::VD + OD * h);
 #pragma unroll
             for (int c = 0; c < OD; c += 32) {
               uint32_t y[32];
@@ -725,18 +744,18 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
             have = have || sees;
             tmem_wait_st();
           } else {
-            // The split's partial.  32 dims at a time go through shared memory, so
-            // that a store of the warp writes 128 bytes of each of four rows.
-            if (sees && h == 0) {
+            // The split's partial.  OUT_DIMS at a time go through shared memory, so
+            // that a store of the warp writes as many of a few rows each.
+            if (sees && h == 0 && half == 0) {
               const size_t base = (static_cast<size_t>(q0 + tok) * a.Hq + hq) * a.max_splits + sp;
               a.part_ml[base * 2] = M0;
               a.part_ml[base * 2 + 1] = Ls;
             }
-            float4* buf = reinterpret_cast<float4*>(so_out) + (warp - 4) * 256;  // [row][8], the 16-byte words XORed with the row
+            float4* buf = reinterpret_cast<float4*>(so_out) + (warp - 4) * (8 * C::OUT_DIMS);  // [row][W], the 16-byte words XORed with the row
             const unsigned rows_seen = __ballot_sync(0xffffffffu, sees);
 #pragma unroll
-            for (int c = 0; c < OD; c += 32) {
-              constexpr int W = 8;  // words of a row
+            for (int c = 0; c < OD; c += C::OUT_DIMS) {
+              constexpr int W = C::OUT_DIMS / 4;  // words of a row
 #pragma unroll
               for (int i = 0; i < W; ++i) {
                 const uint64_t v0 = f2_add(O[c / 2 + 2 * i], 0ull), v1 = f2_add(O[c / 2 + 2 * i + 1], 0ull);
@@ -749,7 +768,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
                 if ((rows_seen >> rl) & 1u) {
                   const int rr = r0 + (warp & 3) * 32 + rl;
                   const size_t base = (static_cast<size_t>(q0 + rr / G) * a.Hq + kvh * G + rr % G) * a.max_splits + sp;
-                  *reinterpret_cast<float4*>(a.part_o + base * HD + OD * h + c + i * 4) = buf[rl * W + (i ^ (rl & (W - 1)))];
+                  *reinterpret_cast<float4*>(a.part_o + base * HD + half * C::VD + OD * h + c + i * 4) = buf[rl * W + (i ^ (rl & (W - 1)))];
                 }
               }
               __syncwarp();
@@ -769,7 +788,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   }
   // Teardown: copies land and issued MMAs finish, then tensor memory is freed.
   if (warp == 1 && lane == 0) {
-    for (int st = max(0, issued_k - 2); st < issued_k; ++st) drain_wait(&k_full[st & 1], (st >> 1) & 1);
+    for (int u = max(0, issued_k - 2); u < issued_k; ++u) drain_wait(&k_full[u & 1], (u >> 1) & 1);
     for (int st = max(0, issued_v - 2); st < issued_v; ++st) drain_wait(&v_full[st & 1], (st >> 1) & 1);
   }
   if (warp == 0 && lane == 0) drain_wait(mma_done, 0);
@@ -784,17 +803,17 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
 template <int HD, int FMT>
 int launch_attn8_tc_t(const Attn8Args& a, int n_chunks, int n_blocks, cudaStream_t s) {
   using C = Tc8Cfg<HD>;
-  constexpr int kExpandSmem = 1024 + C::IMAGE;
+  constexpr int kExpandSmem = 1024 + C::K_BYTES + C::SCALES;
   VD_CUDA_TRY(cudaFuncSetAttribute(attn8_expand_kernel<HD, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem));
-  VD_CUDA_TRY(launch_k(attn8_expand_kernel<HD, FMT>, dim3(static_cast<unsigned>(n_chunks) * a.Hkv), dim3(256), kExpandSmem, s, a));
+  VD_CUDA_TRY(launch_k(attn8_expand_kernel<HD, FMT>, dim3(static_cast<unsigned>(n_chunks) * a.Hkv * 2), dim3(256), kExpandSmem, s, a));
   VD_CUDA_TRY(cudaFuncSetAttribute(attn8_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-  VD_CUDA_TRY(launch_k(attn8_tc_kernel<HD>, dim3(static_cast<unsigned>(n_blocks) * a.Hkv), dim3(C::THREADS), C::SMEM, s, a));
+  VD_CUDA_TRY(launch_k(attn8_tc_kernel<HD>, dim3(static_cast<unsigned>(n_blocks) * a.Hkv * C::HALVES), dim3(C::THREADS), C::SMEM, s, a));
   return VD_OK;
 }
 
 }  // namespace
 
-size_t attn8_image_bytes(int hd) { return hd == 64 ? Tc8Cfg<64>::IMAGE : Tc8Cfg<128>::IMAGE; }
+size_t attn8_image_bytes(int hd) { return hd == 64 ? Tc8Cfg<64>::IMAGE : hd == 128 ? Tc8Cfg<128>::IMAGE : Tc8Cfg<256>::IMAGE; }
 
 int launch_attention8_tc(const Attn8Args& a, int hd, int format, int n_chunks, int n_blocks, cudaStream_t s) {
   if (n_blocks <= 0) return VD_OK;
@@ -803,7 +822,9 @@ int launch_attention8_tc(const Attn8Args& a, int hd, int format, int n_chunks, i
     return i8 ? launch_attn8_tc_t<64, kKv8Int8>(a, n_chunks, n_blocks, s) : launch_attn8_tc_t<64, kKv8E4m3>(a, n_chunks, n_blocks, s);
   if (hd == 128)
     return i8 ? launch_attn8_tc_t<128, kKv8Int8>(a, n_chunks, n_blocks, s) : launch_attn8_tc_t<128, kKv8E4m3>(a, n_chunks, n_blocks, s);
-  return fail(VD_ERR_UNSUPPORTED, "the tcgen05 kernel of the 8-bit cache takes head_dim 64 or 128");
+  if (hd == 256)
+    return i8 ? launch_attn8_tc_t<256, kKv8Int8>(a, n_chunks, n_blocks, s) : launch_attn8_tc_t<256, kKv8E4m3>(a, n_chunks, n_blocks, s);
+  return fail(VD_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
 }
 
 }  // namespace vd
