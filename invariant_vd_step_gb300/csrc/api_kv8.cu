@@ -53,6 +53,8 @@ struct vd_kv8_plan {
 
 namespace {
 
+constexpr int kSplitPages = kAttn8Split / 16;
+
 int check_device(const vd_model* m) {
   int dev = -1;
   VD_CUDA_TRY(cudaGetDevice(&dev));
@@ -368,6 +370,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     d.chunks[k] = take(chunks[k].size());
     d.n_chunks[k] = static_cast<int>(chunks[k].size() / 8);
   }
+  for (int k = 0; k < 2; ++k) d.split_pages[k] = take(kSplitPages * static_cast<size_t>(d.n_items[3 * k]));
   d.seal = take(2 * static_cast<size_t>(n_seal));
   d.n_seal = n_seal;
   d.tokens = take(T);
@@ -431,6 +434,14 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     }
   }
   for (int k = 0; k < 6; ++k) std::copy(blocks[k].begin(), blocks[k].end(), h + d.items[k]);
+  for (int k = 0; k < 2; ++k)
+    for (int n = 0; n < d.n_items[3 * k]; ++n) {
+      const int* item = blocks[3 * k].data() + 8 * static_cast<size_t>(n);
+      const int i = item[0], j0 = item[4] * kSplitPages;
+      for (int j = 0; j < kSplitPages; ++j)  // (a row of the image's table is zero behind the request's pages)
+        h[d.split_pages[k] + static_cast<size_t>(n) * kSplitPages + j] =
+            j0 + j < stride ? h[d.page_table + static_cast<size_t>(i) * stride + j0 + j] : 0;
+    }
   for (int k = 0; k < 2; ++k) std::copy(chunks[k].begin(), chunks[k].end(), h + d.chunks[k]);
   for (int j = 0; j < R; ++j) h[d.logit_rows + j] = b->logit_rows[j];
   for (int k = 0; k < 2; ++k) std::copy(merge[k].begin(), merge[k].end(), h + d.merge_list[k]);
@@ -499,6 +510,7 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
     p.kernels = cls == 2 ? 2 : 1;
     a.items = reinterpret_cast<const int4*>(d.base + d.items[k]);
     a.own_slots = cls ? 2 : d.own_slots;
+    a.split_pages = cls ? nullptr : d.base + d.split_pages[local];
     if ((rc = cls == 2 ? launch_attention8_tc(a, c.head_dim, d.kv8->format, d.n_chunks[local], d.n_items[k], s)
                        : launch_attention8(pool->map, a, c.head_dim, d.kv8->format, !cls && d.lower8, d.n_items[k], s)))
       return rc;

@@ -101,10 +101,14 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
     fence_barrier_init();
   }
   // The block: its request, rows and split come from the plan in one round trip
-  // (a search over the requests took three), the KV heads of one split side by
-  // side, so that CTAs in flight together read whole pages.
+  // (a search over the requests took three), and with them a decode block's pages;
+  // the KV heads of one split side by side, so that CTAs in flight together read
+  // whole pages.
   const int kvh = blockIdx.x % a.Hkv;
-  const int4 d0 = a.items[2 * (blockIdx.x / a.Hkv)], d1 = a.items[2 * (blockIdx.x / a.Hkv) + 1];
+  const int item = blockIdx.x / a.Hkv;
+  const int4 d0 = a.items[2 * item], d1 = a.items[2 * item + 1];
+  int pid = 0, opid = 0;  // lane i: the page a8 + i in 8 bits, ao + i in bf16
+  if (a.split_pages && lane < kChunkPages) pid = a.split_pages[item * (kSplit8 / 16) + warp * kChunkPages + lane];
   const int b = d0.x, q0 = d0.y, qlen = d0.z, cached = d0.w, sidx = d1.x, r0 = d1.y;
   const int G = a.Hq / a.Hkv;
   const int rows = qlen * G;
@@ -116,8 +120,8 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
   const int own_lo = p_min >> 4, own_hi = p_max >> 4;
   const int a8 = max(pg0, lo_min >> 4), n8 = max(0, min(pg0 + kChunkPages, own_hi) - a8);
   const int ao = max(pg0, own_lo), no = max(0, min(pg0 + kChunkPages - 1, own_hi) - ao + 1);
-  int pid = 0, opid = 0;
-  if (lane < n8) pid = a.page_table[static_cast<size_t>(b) * a.pt_stride + a8 + lane];
+  if (a.split_pages) pid = __shfl_sync(0xffffffffu, pid, (lane + a8 - pg0) & 31);
+  else if (lane < n8) pid = a.page_table[static_cast<size_t>(b) * a.pt_stride + a8 + lane];
   if (lane < no) opid = a.open_table[static_cast<size_t>(b) * a.open_stride + ao + lane - (cached >> 4)];
   __syncthreads();
   pdl_wait();

@@ -237,6 +237,7 @@ struct Attn8Args {
   const __nv_bfloat16* q;   // [T][Hq][hd]
   float* part_o;            // [T][Hq][max_splits][hd]
   float* part_ml;           // [T][Hq][max_splits][2]
+  const int* split_pages;   // decode blocks: [item][32] pages of the item's split (else null: from page_table)
   const int* page_table;    // [B][pt_stride] pages of the cache
   const int* open_table;    // [B][open_stride] pages of the bf16 pool, from logical page cached_len / 16 on
   const int4* items;        // [blocks][2]: request (tcgen05: its first image), first token, tokens, cached tokens; split, first row; and for

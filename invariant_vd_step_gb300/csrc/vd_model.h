@@ -71,6 +71,7 @@ struct Desc {
   // Steps over the 8-bit cache (vd_kv8_plan); part_* as above
   const vd_kv8* kv8 = nullptr;
   int items[6] = {}, n_items[6] = {};    // attention blocks: decode class, others, those on tcgen05; the same for local layers
+  int split_pages[2] = {0, 0};           // {global, local}: [decode item][32] pages of its split
   int seal = 0, n_seal = 0;              // offset of the (bf16 page, cache page) pairs that the step seals
   int open_table = 0, open_stride = 0;   // pages of the bf16 pool, per request
   int chunks[2] = {}, n_chunks[2] = {};  // chunks that the tcgen05 blocks of global, of local layers read
