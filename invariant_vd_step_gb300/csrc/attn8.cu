@@ -29,12 +29,13 @@
 // block a row is in or the other rows.
 //
 // What bounds it.  Decode reads each page once: 256 requests of 512 to 8192 tokens,
-// 32 heads over 8 of 128, take 406 us, 5.7 TB/s, 0.84 of what a copy reaches.  A chunk
+// 32 heads over 8 of 128, take 402 us, 5.7 TB/s, 0.85 of what a copy reaches.  A chunk
 // per warp is one pass: scores to shared memory, one maximum, weights, P V; four
 // CTAs per SM (127 registers), each warp with three pages in flight, cover each
 // other's latencies, and the issue slots are 48 % busy.  With the rows as M of the
 // products, 12 of 16 were empty here: 424 us.  Four pages in flight and three CTAs, or
-// two and five, are slower; pages loaded straight to registers take 467 to 528 us.
+// two and five, are slower; pages loaded straight to registers take 467 to 528 us;
+// resident CTAs that take blocks off a count, 401.
 // At head dimension 256 the registers allow two CTAs: a window of 1024 keys for 48
 // requests of 3 tokens, 8 heads over 4, 29 us, 3.6 TB/s, two rounds of latency.
 #include <math.h>
