@@ -549,6 +549,12 @@ int vd_kv8_create(vd_model* m, int32_t format, int32_t num_pages, void* dev_mem,
   const size_t need = vd_kv8_bytes(m, num_pages);
   if (dev_mem && bytes < need) return fail(VD_ERR_CAPACITY, "dev_mem smaller than vd_kv8_bytes()");
   if (reinterpret_cast<uintptr_t>(dev_mem) & 255) return fail(VD_ERR_INVALID_ARG, "dev_mem must be 256-byte aligned");
+  if (dev_mem) {
+    cudaPointerAttributes at{};
+    VD_CUDA_TRY(cudaPointerGetAttributes(&at, dev_mem));
+    if (!(at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == m->device)))
+      return fail(VD_ERR_INVALID_ARG, "dev_mem is not memory of the model's device");
+  }
   vd_kv8* c = new (std::nothrow) vd_kv8();
   if (!c) return fail(VD_ERR_CAPACITY, "out of host memory");
   static std::atomic<unsigned long long> next_id{1};

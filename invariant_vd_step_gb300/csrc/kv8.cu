@@ -92,16 +92,24 @@ __device__ __forceinline__ int seal_pair_k(int kk, int r, int t) {  // dims 16 k
   return seal_place<HD>(0, kk >> 1, r * 4 + t) * 2 + (kk & 1);
 }
 
+// Warps per block of values: two at head dimension 256, where one would hold 64
+// registers of it and 20 warps per SM could not hide the loads (NEWFIG).
+template <int HD>
+constexpr int kSealWarps = HD > 128 ? 2 : 1;
+
 template <int HD, int FMT>
 __global__ void __launch_bounds__(128) kv8_seal_kernel(SealArgs a, const __grid_constant__ PagePairs pairs) {
-  constexpr int PART = Kv8Cfg<HD>::PART, IT = HD / 64;
-  __shared__ uint4 stage[4][PART / 16];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int PART = Kv8Cfg<HD>::PART, W = kSealWarps<HD>, IT = HD / 64 / W, U = 4 / W;  // U: blocks of values per CTA
+  __shared__ uint4 stage[U][PART / 16];
+  __shared__ uint32_t largest[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % W, own = warp / W;
   pdl_wait();
   pdl_trigger();
-  const long long unit = static_cast<long long>(blockIdx.x) * 4 + warp;
-  const int kv = static_cast<int>(unit & 1), per = 2 * a.Hkv * a.layers;
-  if (unit >= static_cast<long long>(pairs.n) * per) return;
+  const int per = 2 * a.Hkv * a.layers;
+  const long long at_most = static_cast<long long>(pairs.n) * per - 1, mine = static_cast<long long>(blockIdx.x) * U + own;
+  if (W == 1 && mine > at_most) return;
+  const long long unit = min(mine, at_most);  // (where warps meet, those behind the last block do its work again)
+  const int kv = static_cast<int>(unit & 1);
   const int i = static_cast<int>(unit / per), rest = static_cast<int>(unit % per) >> 1;
   const int head = rest % a.Hkv, layer = rest / a.Hkv;
   const int2 pp = pair_of(pairs, i);
@@ -113,7 +121,7 @@ __global__ void __launch_bounds__(128) kv8_seal_kernel(SealArgs a, const __grid_
   for (int it = 0; it < IT; ++it)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const auto at = SealItem<HD>::at(kv, it * 32 + lane, v);
+      const auto at = SealItem<HD>::at(kv, (sub * IT + it) * 32 + lane, v);
       x[it][v] = *reinterpret_cast<const uint4*>(src + at.token * HD + at.chunk * 8);
     }
   uint32_t mx = 0u;
@@ -126,6 +134,12 @@ __global__ void __launch_bounds__(128) kv8_seal_kernel(SealArgs a, const __grid_
     }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  if constexpr (W > 1) {
+    if (lane == 0) largest[warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < W; ++k) mx = __vmaxu2(mx, largest[own * W + k]);
+  }
   const uint32_t mb = kv8_max_halves(mx);
   const bool finite = mb < 0x7f80u;
   const float amax = finite ? fmaxf(__uint_as_float(mb << 16), kKv8Least) : 1.0f;
@@ -138,10 +152,10 @@ __global__ void __launch_bounds__(128) kv8_seal_kernel(SealArgs a, const __grid_
   }
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
-    const int idx = it * 32 + lane;
+    const int idx = (sub * IT + it) * 32 + lane;
     const uint32_t* w[4] = {&x[it][0].x, &x[it][1].x, &x[it][2].x, &x[it][3].x};
     if (kv) {
-      uint32_t* words = reinterpret_cast<uint32_t*>(stage[warp]);
+      uint32_t* words = reinterpret_cast<uint32_t*>(stage[own]);
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         float f[4];
@@ -150,7 +164,7 @@ __global__ void __launch_bounds__(128) kv8_seal_kernel(SealArgs a, const __grid_
         words[seal_word_v<HD>(idx % (HD / 8), g, idx / (HD / 8))] = kv8_code4<FMT>(q, f[0], f[1], f[2], f[3]);
       }
     } else {
-      uint2* words = reinterpret_cast<uint2*>(stage[warp]);
+      uint2* words = reinterpret_cast<uint2*>(stage[own]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {  // dims 2 t, + 1, + 8, + 9 of both tokens
         uint32_t c[2];
@@ -163,10 +177,11 @@ __global__ void __launch_bounds__(128) kv8_seal_kernel(SealArgs a, const __grid_
       }
     }
   }
-  __syncwarp();
+  if (W > 1) __syncthreads();
+  else __syncwarp();
 #pragma unroll
-  for (int j = 0; j < PART / 512; ++j) reinterpret_cast<uint4*>(dst)[j * 32 + lane] = stage[warp][seal_place<HD>(kv, j, lane)];
-  if (lane == 0) {
+  for (int j = sub; j < PART / 512; j += W) reinterpret_cast<uint4*>(dst)[j * 32 + lane] = stage[own][seal_place<HD>(kv, j, lane)];
+  if (sub == 0 && lane == 0) {
     float* sc = reinterpret_cast<float*>(a.scales + layer * a.scales_layer + block);
     const float scale = finite ? __fdiv_rn(amax, FMT == kKv8Int8 ? 127.0f : 448.0f) : kv8_nan();
     if (!kv) {
@@ -273,7 +288,8 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(CopyArgs a, const __gri
 template <int HD>
 int launch_seal_t(const SealArgs& a, const PagePairs& p, bool unseal, cudaStream_t s) {
   const long long units = static_cast<long long>(p.n) * a.layers * a.Hkv * 2;
-  const dim3 grid(static_cast<unsigned>((units + 3) / 4));
+  const int per_cta = unseal ? 4 : 4 / kSealWarps<HD>;
+  const dim3 grid(static_cast<unsigned>((units + per_cta - 1) / per_cta));
   const bool i8 = a.format == VD_KV8_INT8;
   auto k = unseal ? (i8 ? kv8_unseal_kernel<HD, kKv8Int8> : kv8_unseal_kernel<HD, kKv8E4m3>)
                   : (i8 ? kv8_seal_kernel<HD, kKv8Int8> : kv8_seal_kernel<HD, kKv8E4m3>);

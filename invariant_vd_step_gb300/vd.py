@@ -567,8 +567,9 @@ class KVPool:
             raise RuntimeError("view() needs a pool created over caller memory")
         if self._pages is None or self._pages[0] is not self.memory:
             s = self.model.spec
-            v = self.memory.view(torch.bfloat16)[: s.n_layers * self.num_pages * 2 * s.n_kv_heads * 16 * s.head_dim]
-            self._pages = self.memory, v.view(s.n_layers, self.num_pages, 2, s.n_kv_heads, 16, s.head_dim)
+            with torch.inference_mode(False):  # (kept: later calls may need a tensor that autograd takes)
+                v = self.memory.view(torch.bfloat16)[: s.n_layers * self.num_pages * 2 * s.n_kv_heads * 16 * s.head_dim]
+                self._pages = self.memory, v.view(s.n_layers, self.num_pages, 2, s.n_kv_heads, 16, s.head_dim)
         return self._pages[1].detach()  # a tensor of its own: three views took 7 us, a page copy's call 5
 
     def copy_pages(self, src, dst, stream=None):
@@ -804,6 +805,7 @@ class KV8Cache:
         _need(format in _FORMATS, f"format {format!r}: one of {sorted(_FORMATS)}")
         self.model, self.num_pages, self.format = model, num_pages, format
         self.memory = memory  # keep alive when caller-owned
+        self._parts = None
         if memory is not None:
             _need(memory.get_device() >= 0 and memory.is_contiguous(), "memory: contiguous, on the model's GPU")
         h = ctypes.c_void_p()
@@ -822,22 +824,25 @@ class KV8Cache:
         except Exception:
             pass
 
-    def _split(self):
+    def _view(self, i: int) -> torch.Tensor:
         if self.memory is None:
             raise RuntimeError("codes() and scales() need a cache created over caller memory")
-        s, flat = self.model.spec, self.memory.view(torch.uint8).reshape(-1)
-        blocks = s.n_layers * self.num_pages * s.n_kv_heads
-        return s, flat[:blocks * 32 * s.head_dim], flat[blocks * 32 * s.head_dim:blocks * (32 * s.head_dim + 16)]
+        if self._parts is None or self._parts[0] is not self.memory:
+            with torch.inference_mode(False):  # (kept, as in KVPool.view)
+                s, flat = self.model.spec, self.memory.view(torch.uint8).reshape(-1)
+                at = (s.n_layers, self.num_pages, s.n_kv_heads)
+                n = s.n_layers * self.num_pages * s.n_kv_heads
+                codes, scales = flat[:n * 32 * s.head_dim], flat[n * 32 * s.head_dim:n * (32 * s.head_dim + 16)]
+                self._parts = self.memory, codes.view(*at, 32 * s.head_dim), scales.view(torch.float32).view(*at, 4)
+        return self._parts[i].detach()
 
     def codes(self) -> torch.Tensor:
         """The codes as bytes [layers][pages][Hkv][32 hd], in the order of vd_kv8.h (requires caller memory)."""
-        s, codes, _ = self._split()
-        return codes.view(s.n_layers, self.num_pages, s.n_kv_heads, 32 * s.head_dim)
+        return self._view(1)
 
     def scales(self) -> torch.Tensor:
         """The scales as float32 [layers][pages][Hkv][4] (requires caller memory)."""
-        s, _, scales = self._split()
-        return scales.view(torch.float32).view(s.n_layers, self.num_pages, s.n_kv_heads, 4)
+        return self._view(2)
 
     def seal(self, pool: KVPool, src, dst, layer: int = -1, stream=None):
         """vd_kv8_seal: pages src[i] of the bf16 pool into pages dst[i], in one layer or in all (-1)."""

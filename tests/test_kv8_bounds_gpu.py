@@ -174,3 +174,17 @@ def test_few_pages_of_many_are_checked():
     before[:, [n - 1, 5, 6]] = before[:, [0, 0, 1]]
     torch.cuda.synchronize()
     assert torch.equal(cache.codes(), before)
+
+
+def test_memory_that_is_not_on_the_models_device_is_refused():
+    """(host memory; another GPU's takes the same check)"""
+    import ctypes
+    ready()
+    sc = KV8Scenario(kv8_spec(2, 1, 64), [16], "int8")
+    n = sc.model.kv8_bytes(4)
+    host = torch.zeros(n + 256, dtype=torch.uint8).pin_memory()
+    h = ctypes.c_void_p()
+    at = (host.data_ptr() + 255) // 256 * 256
+    assert vd.lib().vd_kv8_create(sc.model.h, 0, 4, at, n, ctypes.byref(h)) == 1 and not h.value
+    with pytest.raises(vd.VDError):
+        vd.KV8Cache(sc.model, 4, "int8", memory=host)

@@ -1,6 +1,7 @@
 """Calls over the 8-bit cache refuse tensors on different GPUs, and closed objects, before they reach the library
 (stand-ins for tensors: no GPU needed)."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -59,3 +60,24 @@ def test_closed_objects_are_refused(monkeypatch):
         refused([lambda: plan.seal(other(), other(), 0)])
     finally:
         plan.h = None
+
+
+def test_a_pools_view_is_the_memory_whatever_mode_it_was_made_in():
+    spec = type("Spec", (), dict(n_layers=2, n_kv_heads=1, head_dim=64))
+    pool = object.__new__(vd.KVPool)
+    pool.h, pool._pages, pool.num_pages, pool.model = None, None, 3, type("M", (), dict(spec=spec))()
+    pool.memory = torch.zeros(2 * 3 * 2 * 16 * 64 * 2 + 256, dtype=torch.uint8)
+    with torch.inference_mode():
+        assert pool.view().shape == (2, 3, 2, 1, 16, 64)
+    x = torch.ones(64, requires_grad=True)
+    (pool.view() * x).sum().backward()  # (refused for tensors of inference mode)
+    a, b = pool.view(), pool.view()
+    a[1, 2, 0, 0, 5, 7] = 3.0
+    assert b[1, 2, 0, 0, 5, 7] == 3.0 and a is not b
+    np.testing.assert_array_equal(pool.memory[:-256].view(torch.bfloat16).float().numpy().nonzero()[0],
+                                  [((1 * 3 + 2) * 2 * 16 + 5) * 64 + 7])
+    pool.memory = torch.zeros_like(pool.memory)  # other memory: another view
+    assert (pool.view() == 0).all()
+    pool.memory = None
+    with pytest.raises(RuntimeError):
+        pool.view()
