@@ -122,16 +122,20 @@ int check_pages(int n, const int* src, const int* dst, int src_pages, int dst_pa
   return VD_OK;
 }
 
-template <typename F>
-int for_pairs(int n, const int* src, const int* dst, F launch) {
-  for (int i = 0; i < n; i += kPagePairs) {
-    PagePairs p;
+template <typename P, typename F>
+int for_pairs_of(int n, const int* src, const int* dst, F launch) {
+  for (int i = 0; i < n; i += P::kMost) {
+    P p;
     p.dev = nullptr;
-    p.n = std::min(kPagePairs, n - i);
+    p.n = std::min(P::kMost, n - i);
     for (int k = 0; k < p.n; ++k) p.at[k] = make_int2(src[i + k], dst[i + k]);
     if (const int rc = launch(p)) return rc;
   }
   return VD_OK;
+}
+template <typename F>
+int for_pairs(int n, const int* src, const int* dst, F launch) {
+  return n <= PagePairs::kMost ? for_pairs_of<PagePairs>(n, src, dst, launch) : for_pairs_of<ManyPagePairs>(n, src, dst, launch);
 }
 
 SealArgs seal_args(const vd_kv8* c, const vd_kv_pool* pool, int layer) {  // layer -1: all
@@ -157,7 +161,7 @@ int seal_call(vd_kv8* c, vd_kv_pool* pool, int layer, int n, const int* src, con
   const int np = pool->num_pages, nc = c->num_pages;
   if (const int rc = check_pages(n, src, dst, unseal ? nc : np, unseal ? np : nc, false)) return rc;
   const SealArgs a = seal_args(c, pool, layer);
-  return for_pairs(n, src, dst, [&](const PagePairs& p) {
+  return for_pairs(n, src, dst, [&](const auto& p) {
     return launch_kv8_seal(a, p, unseal, static_cast<cudaStream_t>(stream));
   });
 }
@@ -709,7 +713,7 @@ int vd_kv_copy_pages(vd_kv_pool* pool, int32_t n, const int32_t* src, const int3
     a.bytes = 2LL * f.n_kv_heads * 16 * f.head_dim * 2;
     a.layer = a.bytes * pool->num_pages;
     a.layers = f.n_layers;
-    return for_pairs(n, src, dst, [&](const PagePairs& p) { return launch_copy_pages(a, p, static_cast<cudaStream_t>(stream)); });
+    return for_pairs(n, src, dst, [&](const auto& p) { return launch_copy_pages(a, p, static_cast<cudaStream_t>(stream)); });
   });
 }
 
@@ -727,7 +731,7 @@ int vd_kv8_copy_pages(vd_kv8* c, int32_t n, const int32_t* src, const int32_t* d
     a.extra_layer = c->scales_layer();
     a.n_extra = f.n_kv_heads;
     a.layers = f.n_layers;
-    return for_pairs(n, src, dst, [&](const PagePairs& p) { return launch_copy_pages(a, p, static_cast<cudaStream_t>(stream)); });
+    return for_pairs(n, src, dst, [&](const auto& p) { return launch_copy_pages(a, p, static_cast<cudaStream_t>(stream)); });
   });
 }
 

@@ -241,8 +241,8 @@ struct Attn8Args {
   const int* page_table;    // [B][pt_stride] pages of the cache
   const int* open_table;    // [B][open_stride] pages of the bf16 pool, from logical page cached_len / 16 on
   const int4* items;        // [blocks][2]: request (tcgen05: its first image), first token, tokens, cached tokens; split, first row; and for
-                            // the tcgen05 kernel, whose blocks take several: end of the splits, the block's number
-                            // among those whose splits it folds itself (-1: it leaves partials)
+                            // the tcgen05 kernel, whose blocks take several: end of the splits, whether it
+                            // folds them itself (else it leaves partials)
   const int4* chunks;       // [chunks][2]: request, chunk, image, 1: the image of its own pages; cached, all tokens, 0, 0
   uint8_t* images;          // [images][Hkv] attn8_image_bytes()
   __nv_bfloat16* out;       // [T][Hq][hd] (their rows)
@@ -261,17 +261,21 @@ struct Attn8Args {
 // lower8: every block of the launch has at most 8 rows.
 int launch_attention8(const CUtensorMap& kvmap, const Attn8Args& a, int hd, int format, bool lower8, int n_blocks,
                       cudaStream_t s);
-// The same rows in blocks of 128 on tcgen05, head dimensions 64 and 128.
+// The same rows in blocks of 128 on tcgen05.
 int launch_attention8_tc(const Attn8Args& a, int hd, int format, int n_chunks, int n_blocks, cudaStream_t s);
 size_t attn8_image_bytes(int hd);  // a chunk of 128 keys of one KV head, expanded
 // Sealing and its reverse, page copies (kv8.cu).  Pairs of page ids: `dev` on the
-// device (a plan's), or else in the launch's own arguments.
-constexpr int kPagePairs = 448;
-struct PagePairs {
+// device (a plan's), or else in the launch's own arguments: 3.6 KB of them, or, for
+// more pairs, 32 KB (the most that a launch takes).
+template <int N>
+struct PagePairsN {
+  static constexpr int kMost = N;
   const int2* dev;  // [n] (source, destination) or null
   int n;
-  int2 at[kPagePairs];
+  int2 at[N];
 };
+using PagePairs = PagePairsN<448>;
+using ManyPagePairs = PagePairsN<4000>;
 struct SealArgs {
   __nv_bfloat16* pool;      // first layer
   uint8_t* codes;
@@ -280,6 +284,7 @@ struct SealArgs {
   int layers, Hkv, hd, format;
 };
 int launch_kv8_seal(const SealArgs& a, const PagePairs& pairs, bool unseal, cudaStream_t s);
+int launch_kv8_seal(const SealArgs& a, const ManyPagePairs& pairs, bool unseal, cudaStream_t s);
 struct CopyArgs {
   uint8_t* data;            // pages of `bytes` bytes, `layer` bytes from layer to layer
   long long bytes, layer;
@@ -288,6 +293,7 @@ struct CopyArgs {
   int n_extra, layers;
 };
 int launch_copy_pages(const CopyArgs& a, const PagePairs& pairs, cudaStream_t s);
+int launch_copy_pages(const CopyArgs& a, const ManyPagePairs& pairs, cudaStream_t s);
 // Fixed-size device scratch of vd_op_attention_static (bytes) and its
 // device address on the current device (looked up once per device).
 constexpr size_t kAttnStaticScratchBytes = static_cast<size_t>(16) << 20;

@@ -8,7 +8,8 @@ import torch
 
 from gpu_util import bits, ready
 from invariant_vd_step_gb300 import vd
-from kv8_scenario import KV8Scenario, kv8_spec, sealed_values
+from kv8_scenario import KV8Scenario, e4m3, kv8_spec, sealed_values
+from test_kv8_gpu import _decode
 
 pytestmark = pytest.mark.gpu
 
@@ -188,3 +189,29 @@ def test_memory_that_is_not_on_the_models_device_is_refused():
     assert vd.lib().vd_kv8_create(sc.model.h, 0, 4, at, n, ctypes.byref(h)) == 1 and not h.value
     with pytest.raises(vd.VDError):
         vd.KV8Cache(sc.model, 4, "int8", memory=host)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("exponent", [-78, -3, 0, 100, 127])
+def test_codes_of_every_pair_of_significands(fmt, exponent):
+    """Blocks whose largest magnitudes have each of bf16's 128 significands, over values that have each of them at eight
+    exponents, a / 2 among them: every tie of the codes' rounding is there, and goes to the even code."""
+    ready()
+    sc = KV8Scenario(kv8_spec(2, 1, 64), [16], fmt)
+    a = (1 + torch.arange(128, device="cuda").double() / 128)[:, None]                   # [128][1]
+    x = (1 + torch.arange(128, device="cuda").double() / 128)[:, None] * 2.0 ** -torch.arange(8, device="cuda").double()
+    x = x.reshape(1, -1).repeat(128, 1)                                                  # [128][1024]
+    x = torch.where(x > a, a / 2, x)
+    x[:, 0] = a[:, 0]
+    x[:, 1::2] *= -1
+    x = (x * 2.0 ** exponent).bfloat16().view(64, 2, 1, 16, 64)[None]                    # blocks: K and V of 64 pages
+    pool = vd.KVPool(sc.model, 64, memory=torch.empty(x.nbytes, dtype=torch.uint8, device="cuda"))
+    pool.view().copy_(x)
+    cache = vd.KV8Cache(sc.model, 64, fmt, memory=torch.empty(sc.model.kv8_bytes(64), dtype=torch.uint8, device="cuda"))
+    cache.seal(pool, np.arange(64), np.arange(64))
+    torch.cuda.synchronize()
+    codes, _ = _decode(cache, fmt)
+    y = x.double()
+    top = y.abs().amax((-2, -1), keepdim=True)
+    assert (top.flatten() == (a * 2.0 ** exponent).flatten()).all()
+    assert torch.equal(codes, torch.round(y * 127 / top) if fmt == "int8" else e4m3(y * 448 / top))
