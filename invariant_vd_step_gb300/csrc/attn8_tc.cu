@@ -21,7 +21,7 @@
 // exponentials 512, 64 KB of operands from L2; about 1500 issue slots per
 // scheduler, whose two softmax warps leave more than half of its cycles idle: that
 // is what bounds it (3000 cycles per chunk).  Measured, 2048 tokens behind 6144
-// keys, 32 heads over 8 of 128: 375 us, 641 TFLOP/s.  424 us with the totals in
+// keys, 32 heads over 8 of 128: 371 us, 648 TFLOP/s.  424 us with the totals in
 // global memory, two O buffers and one barrier of all softmax threads (the two of a
 // row need only each other); 447 with the folding in four warps of its own, which
 // became what the others waited for; 414 with 216 registers (spills), 232 now.

@@ -64,7 +64,7 @@ def test_a_long_history(fmt):
     assert ((got[0].double() - want).abs() <= tol).all()
 
 
-@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("hd", [64, 128, 256])
 @pytest.mark.parametrize("end", [513, 545, 640, 641, 1024, 1025, 1153])
 def test_ends_behind_a_split(end, hd):
     """Chunks whose last keys begin a split: two ends of splits follow each other."""
@@ -215,3 +215,43 @@ def test_codes_of_every_pair_of_significands(fmt, exponent):
     top = y.abs().amax((-2, -1), keepdim=True)
     assert (top.flatten() == (a * 2.0 ** exponent).flatten()).all()
     assert torch.equal(codes, torch.round(y * 127 / top) if fmt == "int8" else e4m3(y * 448 / top))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("window", [0, 1, 300])
+def test_long_chunks_at_head_dimension_256(window, fmt):
+    """Two CTAs share a row block there: against 64 bits, the mma.sync kernel and single tokens; with and without blocks that
+    fold their own splits."""
+    ready()
+    for Hq, Hkv in ((8, 4), (48, 24)):
+        sc = KV8Scenario(kv8_spec(Hq, Hkv, 256, window), [1100, 37], fmt, seed=6, max_tokens=900)
+        reqs = [(0, 333, 767), (1, 0, 37), (1, 36, 1)]
+        got = sc.attention(reqs, kernel=2)
+        np.testing.assert_array_equal(bits(sc.attention(reqs, kernel=1)), bits(got))
+        for c in (333, 511, 512, 800, 1099):
+            np.testing.assert_array_equal(bits(sc.attention([(0, c, 1)]))[0], bits(got)[c - 333], err_msg=str(c))
+        for rid, c, n, at in ((0, 333, 767, 0), (1, 0, 37, 767)):
+            want, tol = sc.exact(rid, c, n, window)
+            assert ((got[at:at + n].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("kind", ["inf", "nan"])
+@pytest.mark.parametrize("hd", [128, 256])
+def test_values_that_are_not_finite_in_long_chunks(kind, hd):
+    """One K value of a sealed page, then one of the chunk's own tokens: both kernels give the same bits, NaN where a row sees
+    it and what they gave without it before."""
+    ready()
+    bad = float(kind)
+    base = KV8Scenario(kv8_spec(4, 2, hd), [700], "int8", seed=9)
+    clean = bits(base.attention([(0, 300, 400)], kernel=2))
+    for page, token in ((10, 3), (20, 15)):  # sealed before; own and sealed by the step
+        def edit(s):
+            s.kv[0][page, 0, :, token, 5] = bad
+        sc = KV8Scenario(kv8_spec(4, 2, hd), [700], "int8", seed=9, edit=edit)
+        got = [sc.attention([(0, 300, 400)], kernel=k) for k in (1, 2)]
+        assert torch.equal(got[0].isnan(), got[1].isnan())
+        first = page * 16 + token  # the first position that sees it
+        seen = torch.arange(300, 700, device="cuda") >= first
+        assert got[1][seen].isnan().all()
+        for g in got:
+            np.testing.assert_array_equal(bits(g)[(~seen).cpu().numpy()], clean[(~seen).cpu().numpy()])
