@@ -582,10 +582,17 @@ def _ids(a):
     """Page ids as a contiguous int32 array; ids that int32 does not hold are refused."""
     if type(a) is np.ndarray and a.dtype == np.int32 and a.ndim == 1 and a.flags.c_contiguous:
         return a
+    a = _fits_int32(a, "page ids").reshape(-1)
+    a = np.ascontiguousarray(a, dtype=np.int32)
+    return a if a.flags.writeable else a.copy()  # (one that is a view of something passing)
+
+
+def _fits_int32(a, what: str):
     a = np.asarray(a)
-    _need(a.size == 0 or (a.dtype.kind in "iu" and -2 ** 31 <= int(a.min()) and int(a.max()) < 2 ** 31),
-          "page ids: integers that fit in 32 bits")
-    return np.ascontiguousarray(a.reshape(-1), dtype=np.int32)
+    _need(a.size == 0 or a.dtype == np.int32
+          or (a.dtype.kind in "iu" and -2 ** 31 <= int(a.min()) and int(a.max()) < 2 ** 31),
+          f"{what}: integers that fit in 32 bits")
+    return a
 
 
 def _page_lists(src, dst):
@@ -888,14 +895,14 @@ class KV8Plan:
 
     def plan(self, cache: KV8Cache, pool: KVPool, cu_q, cached_len, page_table, open_table, token_ids=None,
              logit_rows=(), stream=None):
-        cu, p_cu = _i32(cu_q)
-        c, p_c = _i32(cached_len)
+        cu, p_cu = _i32(_fits_int32(cu_q, "cu_q"))
+        c, p_c = _i32(_fits_int32(cached_len, "cached_len"))
         tables = []
         for t in (page_table, open_table):
-            t = np.ascontiguousarray(t, dtype=np.int32)
+            t = np.ascontiguousarray(_fits_int32(t, "page ids"), dtype=np.int32)
             tables.append(t.reshape(len(c), -1) if t.size else t.reshape(len(c), 0))
-        tok, p_tok = _i32(np.asarray(token_ids).reshape(-1)) if token_ids is not None else (None, None)
-        rows, p_rows = _i32(np.asarray(logit_rows).reshape(-1))
+        tok, p_tok = _i32(_fits_int32(token_ids, "token_ids").reshape(-1)) if token_ids is not None else (None, None)
+        rows, p_rows = _i32(_fits_int32(logit_rows, "logit_rows").reshape(-1))
         _need(cu.ndim == 1 and c.ndim == 1 and len(cu) == len(c) + 1 and (tok is None or len(tok) == cu[-1]),
               "cu_q [B + 1], cached_len [B], token_ids [cu_q[B]]")
         b = KV8Batch(int(cu[-1]), len(c), len(rows), tables[0].shape[1], tables[1].shape[1], 0, p_cu, p_c,

@@ -81,3 +81,30 @@ def test_a_pools_view_is_the_memory_whatever_mode_it_was_made_in():
     pool.memory = None
     with pytest.raises(RuntimeError):
         pool.view()
+
+
+def test_numbers_that_32_bits_do_not_hold_are_refused(monkeypatch):
+    plan, other = plan_without_library(monkeypatch)
+    good = dict(cu_q=[0, 1], cached_len=[3], page_table=[[0]], open_table=[[0]], token_ids=[1], logit_rows=[0])
+    try:
+        refused([lambda k=k, v=v: plan.plan(other(), other(), **{**good, k: v}) for k, v in [
+            ("cu_q", [0, 2 ** 32 + 1]), ("cached_len", [2 ** 32]), ("page_table", [[2 ** 32]]), ("open_table", [[-2 ** 32]]),
+            ("open_table", [[0.0]]), ("token_ids", [2 ** 32 + 1]), ("logit_rows", [2 ** 32])]])
+        with pytest.raises(AssertionError, match="reached"):
+            plan.plan(other(), other(), **good)
+    finally:
+        plan.h = None
+
+
+def test_page_ids_stay_alive_until_the_call():
+    class Passing:  # an array of ids that nothing else holds, and that may not be written
+        def __array__(self, dtype=None, copy=None):
+            a = np.arange(5, dtype=np.int32)
+            a.flags.writeable = False
+            return a
+    a = vd._ids(Passing())
+    assert a.flags.writeable and a.tolist() == [0, 1, 2, 3, 4]
+    n, src, dst = vd._page_lists(Passing(), [4, 3, 2, 1, 0])
+    assert n == 5
+    kept = np.frombuffer((vd.ctypes.c_int32 * 5).from_address(vd.ctypes.addressof(src)), np.int32)
+    assert kept.tolist() == [0, 1, 2, 3, 4]
