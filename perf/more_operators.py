@@ -168,8 +168,6 @@ def _prepare_attend(case, seed):
         source.close()
         st["pool"] = _pool(st["model"], st.pop("open")[None])
         st["plan"] = vd.KV8Plan(st["model"], B * n)
-        st["plan"].plan(st["cache"], st["pool"], np.arange(0, B * n + 1, n), st["cached"], st["table"],
-                        st["open_table"])
         st["out"] = torch.empty_like(st["q"])
         return st
     st["codes"], st["scale"] = _quantise(values, case["format"])
@@ -240,6 +238,10 @@ def run(st):
     op = st["case"]["op"]
     if own:
         if op == "attend":
+            # Histories grow with every step, so a program plans each step anew: the plan is part of the pass.
+            B, n = st["case"]["B"], st["case"]["n"]
+            st["plan"].plan(st["cache"], st["pool"], np.arange(0, B * n + 1, n), st["cached"], st["table"],
+                            st["open_table"])
             st["plan"].attention(st["cache"], st["pool"], 0, st["q"], st["out"])
             return st["out"]
         if op == "seal":
