@@ -7,16 +7,22 @@
 // 16), its bf16 version if i = own, nothing beyond.
 //
 // Per chunk and row, with codes c, K scale k, V scale v of each page and
-// everything else float32 unless stated; m0 is the row's maximum over the chunks
-// of the split before this one (-inf at the first):
-//   t_j = (q c_j) k scale + log2 v       (the product in fp16, exact operands)
-//   m   = max(m0, max_j t_j),   p_j = 2^(t_j - m),   alpha = 2^(m0 - m)
-//   l   = l alpha + sum_j p_j / v,   O = O alpha + sum_j fp16(p_j) c_j
-// so O / l is the softmax's mean of the values: the V scale rides in the
-// exponent and the codes enter the product as they are.  fp16(p) is off by 2^-12
-// of p or 2^-25 (the largest p is 1), where bf16 would be off by 2^-9.  The row's
-// own page takes part with a scale per token, a power of two that makes its bf16
-// values exact in fp16 (kv8.cuh).
+// everything else float32 unless stated; 0 marks what the chunks of the split before
+// this one left (S = -inf at the first):
+//   s_j = (q c_j) k scale                (the product in fp16, exact operands)
+//   S   = max(S0, max_j s_j),   r = max_j (s_j + log2 v_j) - S
+//   u   = max(log2 v - r, -90),  p_j = 2^(s_j - (S - u)),   w_j = p_j 2^-u = 2^(s_j - S)
+//   l   = l 2^(S0 - S) + sum_j w_j
+//   O   = O 2^(S0 - S + r0 - r) + sum_j fp16(p_j) c_j
+// so O 2^r / l is the softmax's mean of the values, and a split's partial is (S, l, O
+// 2^r), the last two times 2^-24.  The V scale rides in the exponent and the codes enter
+// the product as they are; r makes the largest p of the row 1, and fp16 rounds p by
+// 2^-12 of itself or 2^-25, where bf16 would be off by 2^-9.  S and l know nothing of V:
+// with p relative to the largest alone, keys whose V is 2^126 below the largest, or 0,
+// would leave the denominator.  With the bound -90 of u (below it nothing of p is left
+// in fp16) each weight of 2^-36 of the largest and more is in l whatever the V, and
+// where no V is that far apart all down to 2^-126.  The row's own page takes part with a
+// scale per token, a power of two that makes its bf16 values exact in fp16 (kv8.cuh).
 //
 // Order: the pages of a chunk ascending, the own page last.  Keys 2t + e and 2t +
 // 8 + e of each page go to the partial sum l_(t, e) of eight, t < 4, e < 2, of
@@ -90,7 +96,8 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
   uint64_t* bar = bars + warp * SL;
   uint64_t* own_bar = bars + 4 * SL;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(own_bar + 2);
-  __shared__ float fold_m[4][8 * NB], fold_l[kChunkParts][4][8 * NB];  // per chunk and row: its largest score, its parts' l
+  __shared__ float2 fold_m[4][8 * NB];
+  __shared__ float fold_l[kChunkParts][4][8 * NB];  // per chunk and row: its Kv8Max, its parts' l
 
   // Up to the wait for the previous kernel the CTA reads only the status word and
   // the plan (uploaded before the step's first kernel).
@@ -212,9 +219,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
 
   // ---- scores of the 8-bit pages, two at a time; the odd last one is taken
   // twice.  Element e of a score fragment: key g + 8 (e / 2), row 2t + e % 2.
-  float mx[NR];
-#pragma unroll
-  for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
+  Kv8Max mx[NR];
 #pragma unroll 1
   for (int i = 0; i < n8; i += 2) {
     const int i1 = min(i + 1, n8 - 1);
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
       for (int n = 0; n < NB; ++n) {
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __fmaf_rn(acc[x][n][e], __fmul_rn(ks, rowfac[2 * n + (e & 1)]), lv);
+        for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(acc[x][n][e], __fmul_rn(ks, rowfac[2 * n + (e & 1)]));
         if (!full(pgi)) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -266,15 +271,18 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
             if (!(key >= lo[r] && pgi < own[r])) v[e] = -INFINITY;
           }
         }
-        mx[2 * n] = fmaxf(mx[2 * n], fmaxf(v[0], v[2]));
-        mx[2 * n + 1] = fmaxf(mx[2 * n + 1], fmaxf(v[1], v[3]));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float s1 = fmaxf(v[k], v[2 + k]);
+          kv8_take(mx[2 * n + k], s1, __fadd_rn(s1, lv));
+        }
         score[ii * 32 * NB + n] = make_float4(v[0], v[1], v[2], v[3]);
       }
     }
   }
   // ---- scores of the own pages
   int ve[2][4];     // [own page][key]: the exponents of V tokens 2t, 2t + 1, 2t + 8, 2t + 9
-  float vup[2][2];  // [own page]: 1 / V scale of tokens g, g + 8
+  float vlv[2][2];  // [own page]: log2 of the V scales of tokens g, g + 8
   const int mi = lane >> 3, r8 = lane & 7;
 #pragma unroll 1
   for (int o = 0; o < no; ++o) {
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
       vm[1] = __vmaxu2(vm[1], __vmaxu2(w[1] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
     }
     int vx[4];
-    float kup[2], kd[2], lv[2], up[2];
+    float kup[2], kd[2], lv[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       km[j] = __vmaxu2(km[j], __shfl_xor_sync(0xffffffffu, km[j], 1));
@@ -309,7 +317,6 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
       const int e0 = __shfl_sync(0xffffffffu, vx[2 * j], gq >> 1), e1 = __shfl_sync(0xffffffffu, vx[2 * j + 1], gq >> 1);
       const int e = gq & 1 ? e1 : e0;  // of token g + 8 j
       lv[j] = e == 255 ? kv8_nan() : kv8_log2_down(e);
-      up[j] = kv8_up(e);
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -318,8 +325,8 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      if (o == 0) vup[0][x] = up[x];
-      else vup[1][x] = up[x];
+      if (o == 0) vlv[0][x] = lv[x];
+      else vlv[1][x] = lv[x];
     }
     float acc[NB][4];
 #pragma unroll
@@ -339,24 +346,29 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
       for (int e = 0; e < 4; ++e) {
         const int r = 2 * n + (e & 1), key = (ao + o) * 16 + gq + 8 * (e >> 1);
         const bool vis = key >= lo[r] && key <= pos[r] && ao + o == own[r];
-        v[e] = vis ? __fmaf_rn(acc[n][e], __fmul_rn(kd[e >> 1], rowfac[r]), lv[e >> 1]) : -INFINITY;
-        mx[r] = fmaxf(mx[r], v[e]);
+        v[e] = vis ? __fmul_rn(acc[n][e], __fmul_rn(kd[e >> 1], rowfac[r])) : -INFINITY;
+        kv8_take(mx[r], v[e], __fadd_rn(v[e], lv[e >> 1]));
       }
       score[(kChunkPages + o) * 32 * NB + n] = make_float4(v[0], v[1], v[2], v[3]);
     }
   }
-  // ---- the running maximum of the split at this chunk
+  // ---- the running maxima of the split at this chunk
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
 #pragma unroll
-    for (int x = 4; x < 32; x *= 2) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], x));
-    if (gq == 0) fold_m[warp][8 * (r >> 1) + 2 * t4 + (r & 1)] = mx[r];
+    for (int x = 4; x < 32; x *= 2)
+      kv8_take(mx[r], __shfl_xor_sync(0xffffffffu, mx[r].s, x), __shfl_xor_sync(0xffffffffu, mx[r].t, x));
+    if (gq == 0) fold_m[warp][8 * (r >> 1) + 2 * t4 + (r & 1)] = make_float2(mx[r].s, mx[r].t);
   }
   __syncthreads();
+  Kv8Base base[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    for (int w = 0; w < warp; ++w) mx[r] = fmaxf(mx[r], fold_m[w][8 * (r >> 1) + 2 * t4 + (r & 1)]);
-    if (mx[r] == -INFINITY) mx[r] = 0.f;  // no key seen so far: every score is -inf, every weight 0
+    for (int w = 0; w < warp; ++w) {
+      const float2 m = fold_m[w][8 * (r >> 1) + 2 * t4 + (r & 1)];
+      kv8_take(mx[r], m.x, m.y);
+    }
+    base[r] = Kv8Base(mx[r], kv8_exponent(mx[r]));
   }
 
   // ---- weights, their sums and P V
@@ -369,35 +381,42 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
   for (int x = 0; x < HD / 16; ++x)
 #pragma unroll
     for (int n = 0; n < NB; ++n) o_acc[x][n][0] = o_acc[x][n][1] = o_acc[x][n][2] = o_acc[x][n][3] = 0.f;
-  // Weights of page `pg`, at place i of the scores, as B fragments; their share of
-  // l, with the 1 / V scales y0, y1 of its tokens g, g + 8.
-  auto weights = [&](int i, int pg, float y0, float y1, bool all, uint32_t (&pb)[NB][2]) {
+  // Weights of page `pg`, at place i of the scores, as B fragments, and their share of l;
+  // of(r, j): row r's Kv8Weight of token g + 8 j.
+  auto weights = [&](int i, int pg, auto of, uint32_t (&pb)[NB][2]) {
     const int part = (pg - pg0) / (kChunkPages / kChunkParts);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const float4 v = score[i * 32 * NB + n];
-      const float p[4] = {ex2(__fsub_rn(v.x, mx[2 * n])), ex2(__fsub_rn(v.y, mx[2 * n + 1])),
-                          ex2(__fsub_rn(v.z, mx[2 * n])), ex2(__fsub_rn(v.w, mx[2 * n + 1]))};
+      const float s4[4] = {v.x, v.y, v.z, v.w};
+      float p[4], back[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const Kv8Weight w = of(2 * n + (e & 1), e >> 1);
+        p[e] = ex2(__fsub_rn(s4[e], w.base));
+        back[e] = w.back;
+      }
       pb[n][0] = transpose8(pack_f16x2(p[0], p[1]));
       pb[n][1] = transpose8(pack_f16x2(p[2], p[3]));
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = 2 * n + k;
-        // (a page that the row does not see stays out, whatever its scale)
-        if (all || ((i < kChunkPages ? pg < own[r] : pg == own[r]) && pg * 16 + 15 >= lo[r])) {
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int h = 0; h < kChunkParts; ++h)
-            if (h == part) l[r][h] = __fmaf_rn(p[2 + k], y1, __fmaf_rn(p[k], y0, l[r][h]));
-        }
-      }
+        for (int h = 0; h < kChunkParts; ++h)
+          if (h == part) l[2 * n + k][h] = __fmaf_rn(p[2 + k], back[2 + k], __fmaf_rn(p[k], back[k], l[2 * n + k][h]));
     }
   };
 #pragma unroll 1
   for (int i = 0; i < n8; ++i) {
     const int cp = n8 + i;  // the copy of page i's V
     uint32_t pb[NB][2];
-    const float iv = __shfl_sync(0xffffffffu, sc.y, i);
-    weights(i, a8 + i, iv, iv, full(a8 + i), pb);
+    const float lv = __shfl_sync(0xffffffffu, sc.z, i);
+    const int pg = a8 + i;
+    const bool all = full(pg);
+    Kv8Weight w[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r)  // (a page that the row does not see stays out, whatever its scale)
+      w[r] = all || (pg < own[r] && pg * 16 + 15 >= lo[r]) ? base[r](lv) : kv8_no_weight();
+    weights(i, pg, [&](int r, int) { return w[r]; }, pb);
     if (!wait(&bar[cp % SL], (cp / SL) & 1)) break;
     used = cp + 1;
     const uint4* vp = reinterpret_cast<const uint4*>(ring + (cp % SL) * C::PART) + lane;
@@ -430,7 +449,12 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
         if (e != 255) keep[x >> 1] |= 0xffffu << (16 * (x & 1));
       }
       uint32_t pb[NB][2];
-      weights(kChunkPages + o, ao + o, o == 0 ? vup[0][0] : vup[1][0], o == 0 ? vup[0][1] : vup[1][1], false, pb);
+      const int pg = ao + o;
+      const float lv[2] = {o == 0 ? vlv[0][0] : vlv[1][0], o == 0 ? vlv[0][1] : vlv[1][1]};
+      weights(kChunkPages + o, pg, [&](int r, int j) {  // (a token that the row does not see stays out)
+        const int key = pg * 16 + gq + 8 * j;
+        return pg == own[r] && key >= lo[r] && key <= pos[r] ? base[r](lv[j]) : kv8_no_weight();
+      }, pb);
 #pragma unroll
       for (int x = 0; x < HD / 16; ++x) {
         uint32_t w[4];
@@ -477,38 +501,42 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
   const int frow = threadIdx.x / TPR, fd = threadIdx.x % TPR;
   const int row = r0 + frow;
   if (row >= rows) return;
-  float M = -INFINITY, L[kChunkParts] = {}, O[PER];
+  Kv8Max M;
+  float M_ex = 0.f, L[kChunkParts] = {}, O[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) O[i] = 0.f;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const float* src = reinterpret_cast<const float*>(ring0 + w * C::RING) + frow * HD;
-    float alpha;
-    kv8_running_max(M, fold_m[w][frow], alpha);
+    float al, ao;
+    const float s0 = M.s;
+    kv8_take(M, fold_m[w][frow].x, fold_m[w][frow].y);
+    kv8_factors(M, s0, M_ex, al, ao);
 #pragma unroll
-    for (int h = 0; h < kChunkParts; ++h) L[h] = __fmaf_rn(L[h], alpha, fold_l[h][w][frow]);
+    for (int h = 0; h < kChunkParts; ++h) L[h] = __fmaf_rn(L[h], al, fold_l[h][w][frow]);
 #pragma unroll
     for (int i = 0; i < PER / 4; ++i) {
       const float4 v = *reinterpret_cast<const float4*>(src + (((i * TPR + fd) * 4) ^ (8 * ((frow >> 1) & 3))));
-      O[4 * i] = __fmaf_rn(O[4 * i], alpha, v.x);
-      O[4 * i + 1] = __fmaf_rn(O[4 * i + 1], alpha, v.y);
-      O[4 * i + 2] = __fmaf_rn(O[4 * i + 2], alpha, v.z);
-      O[4 * i + 3] = __fmaf_rn(O[4 * i + 3], alpha, v.w);
+      O[4 * i] = __fmaf_rn(O[4 * i], ao, v.x);
+      O[4 * i + 1] = __fmaf_rn(O[4 * i + 1], ao, v.y);
+      O[4 * i + 2] = __fmaf_rn(O[4 * i + 2], ao, v.z);
+      O[4 * i + 3] = __fmaf_rn(O[4 * i + 3], ao, v.w);
     }
   }
   // a row that sees no key of the split has no partial
   const int p = cached + row / G, flo = a.window > 0 ? max(0, p - a.window + 1) : 0;
   if (max(flo, sidx * kSplit8) > min(p, sidx * kSplit8 + kSplit8 - 1)) return;
-  const size_t base = (static_cast<size_t>(q0 + row / G) * a.Hq + kvh * G + row % G) * a.max_splits + sidx;
+  const size_t at = (static_cast<size_t>(q0 + row / G) * a.Hq + kvh * G + row % G) * a.max_splits + sidx;
   if (fd == 0) {
-    a.part_ml[base * 2] = M;
-    a.part_ml[base * 2 + 1] = kv8_sum_parts(L);
+    a.part_ml[at * 2] = M.s;
+    a.part_ml[at * 2 + 1] = __fmul_rn(kv8_sum_parts(L), kPart);
   }
+  const float unit = ex2(__fadd_rn(M_ex, kPartLog2));
 #pragma unroll
   for (int i = 0; i < PER / 4; ++i)
-    *reinterpret_cast<float4*>(a.part_o + base * HD + (i * TPR + fd) * 4) =
-        make_float4(__fadd_rn(O[4 * i], 0.f), __fadd_rn(O[4 * i + 1], 0.f), __fadd_rn(O[4 * i + 2], 0.f),
-                    __fadd_rn(O[4 * i + 3], 0.f));  // (no negative zeros, whichever kernel ran)
+    *reinterpret_cast<float4*>(a.part_o + at * HD + (i * TPR + fd) * 4) =
+        make_float4(kv8_part(O[4 * i], unit), kv8_part(O[4 * i + 1], unit), kv8_part(O[4 * i + 2], unit),
+                    kv8_part(O[4 * i + 3], unit));
 }
 
 template <int HD, int FMT, int NB>

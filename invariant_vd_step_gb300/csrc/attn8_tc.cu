@@ -21,10 +21,11 @@
 // exponentials 512, 64 KB of operands from L2; about 1500 issue slots per
 // scheduler, whose two softmax warps leave more than half of its cycles idle: that
 // is what bounds it (3000 cycles per chunk).  Measured, 2048 tokens behind 6144
-// keys, 32 heads over 8 of 128: 371 us, 648 TFLOP/s.  424 us with the totals in
+// keys, 32 heads over 8 of 128: 385 us, 625 TFLOP/s.  With one maximum for scores and V
+// scales together, which loses weights, 371; before that 424 with the totals in
 // global memory, two O buffers and one barrier of all softmax threads (the two of a
-// row need only each other); 447 with the folding in four warps of its own, which
-// became what the others waited for; 414 with 216 registers (spills), 232 now.
+// row need only each other), 447 with the folding in four warps of its own, which
+// became what the others waited for, and 414 with 216 registers in place of 232.
 //
 // Head dimension 256: a row block is two CTAs, each with all of the scores and half
 // of the dims of V and O, so that tensor memory and registers hold what they hold at
@@ -66,7 +67,7 @@ struct Tc8Cfg {
   static constexpr int KU = HALVES;                 // units that K is copied in: of at most 128 dims
   static constexpr int KU_BYTES = K_BYTES / KU;
   static constexpr int STAGES = 2;                  // of K's units, and of V
-  static constexpr int SCALES = kChunk8 * 3 * 4;    // per stage: 8 pages or 128 tokens x (K scale, log2 of V's, 1 / V's)
+  static constexpr int SCALES = kChunk8 * 2 * 4;    // per stage: 8 pages or 128 tokens x (K scale, log2 of V's)
   static constexpr int SC_RING = 4;
   static constexpr int NT = kChunkParts;  // softmax threads per row
   static constexpr int NS = 128 * NT;
@@ -164,11 +165,6 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t x, uint64_t y, uint64_t z) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
   return r;
 }
-__device__ __forceinline__ uint64_t f2_add(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
 __device__ __forceinline__ uint64_t f2_sub(uint64_t x, uint64_t y) {
   uint64_t r;
   asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
@@ -224,7 +220,7 @@ __global__ void __launch_bounds__(256, HD <= 128 ? 5 : 3) attn8_expand_kernel(At
     for (int u = 0; u < UNITS; ++u) w[u] = in ? __ldcg(src + v * (PART / 16) + u * 32) : make_uint4(0u, 0u, 0u, 0u);
     if (v == 0 && lane == 0) {
       const float4 f = in ? __ldcg(a.scales + block) : make_float4(0.f, 0.f, 0.f, 0.f);
-      *reinterpret_cast<float4*>(sc + pg * 4) = make_float4(f.x, f.z, f.y, 0.f);
+      *reinterpret_cast<float2*>(sc + pg * 2) = make_float2(f.x, f.z);
     }
     // the two fp16 pairs of a word go to 16-byte columns c and c + 1 of row g of an 8-row group
     auto col = [&](int c) { return static_cast<uint32_t>(g * 128 + ((c ^ g) << 4) + t4 * 4); };
@@ -283,7 +279,6 @@ __global__ void __launch_bounds__(256, HD <= 128 ? 5 : 3) attn8_expand_kernel(At
           sc[key] = ex == 255 ? kv8_nan() : kv8_down(ex);
         } else {
           sc[kChunk8 + key] = ex == 255 ? kv8_nan() : kv8_log2_down(ex);
-          sc[2 * kChunk8 + key] = up;
         }
       }
 #pragma unroll
@@ -309,8 +304,8 @@ __global__ void __launch_bounds__(256, HD <= 128 ? 5 : 3) attn8_expand_kernel(At
   const uint4* from = reinterpret_cast<const uint4*>(smem);
 #pragma unroll 4
   for (int i = threadIdx.x; i < C::K_BYTES / 16; i += 256) to[i] = from[i];
-  // scales: of an 8-bit chunk's pages, by K's block; of own tokens K's, then V's two
-  const int s0 = own && v ? kChunk8 / 4 : 0, s1 = !own ? (v ? 0 : kChunkPages) : v ? C::SCALES / 16 : kChunk8 / 4;
+  // scales: of an 8-bit chunk's pages, by K's block; of own tokens K's, then V's
+  const int s0 = own && v ? kChunk8 / 4 : 0, s1 = !own ? (v ? 0 : kChunkPages / 2) : v ? C::SCALES / 16 : kChunk8 / 4;
   to = reinterpret_cast<uint4*>(image_at + 2 * C::K_BYTES);
   for (int i = s0 + threadIdx.x; i < s1; i += 256) to[i] = reinterpret_cast<const uint4*>(sc)[i];
 }
@@ -340,7 +335,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
   uint64_t* mma_done = o_full + 1;   // every MMA has completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  __shared__ float ex[2][C::NT][128];  // [chunk % 2][half][row] largest scores
+  __shared__ float2 ex[2][C::NT][128];  // [chunk % 2][half][row] Kv8Max of the chunk
   __shared__ float ex_l[2][C::NT][128];  // [chunk % 2] l of the halves at a split's end: the last two may be neighbours
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -538,12 +533,13 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
       ok = ok && __all_sync(0xffffffffu, mbar_wait(f, n & 1, abort_flag, a.status));
       return ok;
     };
-    // The split in hand: this thread's l and O (pairs of dims); M: the running
-    // maximum at the chunk whose weights were taken last.  O of a chunk is folded
-    // behind the next one's weights, with the factor for what is before it: 0 at a
-    // split's first chunk, as what O and L hold is then of another split, and finite
-    // or NaN for good.
-    float M = -INFINITY, L = 0.f;
+    // The split in hand: this thread's l and O (pairs of dims); M, r: the running
+    // maxima at the chunk whose weights were taken last, and O's exponent.  O of a chunk
+    // is folded behind the next one's weights, with the factor for what is before it: 0
+    // at a split's first chunk, as what O and L hold is then of another split, and
+    // finite or NaN for good.
+    Kv8Max M;
+    float r = 0.f, L = 0.f;
     uint64_t O[OD / 2];
 #pragma unroll
     for (int i = 0; i < OD / 2; ++i) O[i] = 0ull;
@@ -551,16 +547,16 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
     float2 ml = make_float2(0.f, 0.f);  // maximum and l of those before, whose O is the totals
     bool have = false;
     int st = 0, n16 = 0;
-    float alpha0 = 0.f, l0 = 0.f, M0 = 0.f;  // of the chunk before: factor, l, maximum
+    float al0 = 0.f, ao0 = 0.f, l0 = 0.f, S0 = 0.f, r0e = 0.f;  // of the chunk before: factors, l, largest score, exponent
 #pragma unroll 1
     for (int ch = ch0; ch <= ch1 + 1; ++ch) {
       const int it = ch - ch0, pg0 = ch * kChunkPages + h * HP;  // this thread's first page
       const uint32_t s_at = lanes + 128 * (it & 1);
-      float alpha = 0.f, l_ch = 0.f;
+      float al = 0.f, ao = 0.f, l_ch = 0.f;
       if (ch <= ch1) {
         warp_wait(&s_full[it & 1], it >> 1);
         tc_fence_after();
-        const float4* sc = reinterpret_cast<const float4*>(scales + (st & 3) * (C::SCALES / 4)) + h * HP;
+        const float2* sc = reinterpret_cast<const float2*>(scales + (st & 3) * (C::SCALES / 4)) + h * HP;
         const float* so = scales + ((st + 1) & 3) * (C::SCALES / 4) + h * HP * 16;
         const bool dg = diag(ch);
         if (dg) {
@@ -570,8 +566,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
         st += dg ? 2 : 1;
         // every row of the warp sees this half in 8 bits (rows that are none aside)
         const bool full = __all_sync(0xffffffffu, !valid || (lo <= pg0 * 16 && own >= pg0 + HP));
-        float t[HP * 16];
-        float iv[HP];
+        float t[HP * 16], lv8[HP];
 #pragma unroll
         for (int p0 = 0; p0 < HP; p0 += 2) {
           uint32_t x[32];
@@ -579,18 +574,20 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
           wait_ld32(x);
 #pragma unroll
           for (int pg = p0; pg < p0 + 2; ++pg) {
-            const float4 f = sc[pg];
+            const float2 f = sc[pg];
             const float ks = __fmul_rn(f.x, rowfac);
-            const uint64_t k2 = f2(ks, ks), lv2 = f2(f.y, f.y);
-            iv[pg] = f.z;
+            lv8[pg] = f.y;
+            const uint64_t k2 = f2(ks, ks);
 #pragma unroll
             for (int i = pg * 16; i < pg * 16 + 16; i += 2) {
-              const uint64_t s2 = f2_fma(f2(x[i - 16 * p0], x[i - 16 * p0 + 1]), k2, lv2);
+              // (+ 0: a packed product and the difference below would come out as one fma)
+              const uint64_t s2 = f2_fma(f2(x[i - 16 * p0], x[i - 16 * p0 + 1]), k2, 0ull);
               t[i] = f2_lo(s2);
               t[i + 1] = f2_hi(s2);
             }
           }
         }
+        Kv8Max mc;  // of this half of the chunk
         if (!full) {
 #pragma unroll
           for (int pg = 0; pg < HP; ++pg) {
@@ -606,49 +603,74 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   const int key = page * 16 + i;
-                  const float v = __fmaf_rn(__uint_as_float(y[i]), __fmul_rn(so[pg * 16 + i], rowfac), so[kChunk8 + pg * 16 + i]);
+                  const float v = __fmul_rn(__uint_as_float(y[i]), __fmul_rn(so[pg * 16 + i], rowfac));
                   if (key >= lo && key <= pos) t[pg * 16 + i] = v;
+                  const float lv = so[kChunk8 + pg * 16 + i];
+                  kv8_take(mc, t[pg * 16 + i], __fadd_rn(t[pg * 16 + i], lv));
                 }
               }
             }
           }
         }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < HP * 16; i += 2) m4[(i >> 1) & 3] = fmaxf(m4[(i >> 1) & 3], fmaxf(t[i], t[i + 1]));
-        ex[it & 1][h][lr] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        for (int pg = 0; pg < HP; ++pg) {
+          float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) m2[(i >> 1) & 1] = fmaxf(m2[(i >> 1) & 1], fmaxf(t[pg * 16 + i], t[pg * 16 + i + 1]));
+          const float s1 = fmaxf(m2[0], m2[1]);
+          if (full || pg0 + pg != own) kv8_take(mc, s1, __fadd_rn(s1, lv8[pg]));
+        }
+        ex[it & 1][h][lr] = make_float2(mc.s, mc.t);
         ok = softmax_sync<32 * C::NT>(2 + (warp & 3), ok);  // also: every score has been read
         if (!ok) break;
         const bool first = (ch & 3) == 0 || it == 0;
-        if (first) M = -INFINITY;
-        float mx = ex[it & 1][0][lr];
+        if (first) {
+          M = Kv8Max();
+          r = 0.f;
+        }
+        const float s0 = M.s;
 #pragma unroll
-        for (int k = 1; k < C::NT; ++k) mx = fmaxf(mx, ex[it & 1][k][lr]);
-        kv8_running_max(M, mx, alpha);
-        if (first) alpha = 0.f;
-        const float u = M == -INFINITY ? 0.f : M;  // no key seen so far: every score is -inf, every weight 0
-        const uint64_t u2 = f2(u, u);
+        for (int k = 0; k < C::NT; ++k) kv8_take(M, ex[it & 1][k][lr].x, ex[it & 1][k][lr].y);
+        kv8_factors(M, s0, r, al, ao);
+        if (first) al = ao = 0.f;
+        const Kv8Base base(M, r);
         uint64_t l[4] = {0ull, 0ull, 0ull, 0ull};  // pair t: the partial sums (t, 0) and (t, 1)
         uint32_t pk[HP * 8];
+        auto page_weights = [&](int pg, const Kv8Weight& w) {
+          const uint64_t base2 = f2(w.base, w.base), back2 = f2(w.back, w.back);
 #pragma unroll
-        for (int i = 0; i < HP * 8; ++i) {
-          const uint64_t s2 = f2_sub(f2(t[2 * i], t[2 * i + 1]), u2);
-          t[2 * i] = ex2(f2_lo(s2));
-          t[2 * i + 1] = ex2(f2_hi(s2));
-          pk[i] = pack_f16x2(t[2 * i], t[2 * i + 1]);
-          if (full) l[i & 3] = f2_fma(f2(t[2 * i], t[2 * i + 1]), f2(iv[i >> 3], iv[i >> 3]), l[i & 3]);
-        }
-        if (!full) {
+          for (int i = pg * 8; i < pg * 8 + 8; ++i) {
+            const uint64_t s2 = f2_sub(f2(t[2 * i], t[2 * i + 1]), base2);
+            t[2 * i] = ex2(f2_lo(s2));
+            t[2 * i + 1] = ex2(f2_hi(s2));
+            pk[i] = pack_f16x2(t[2 * i], t[2 * i + 1]);
+            l[i & 3] = f2_fma(f2(t[2 * i], t[2 * i + 1]), back2, l[i & 3]);
+          }
+        };
+        if (full) {
+#pragma unroll
+          for (int pg = 0; pg < HP; ++pg) page_weights(pg, base(lv8[pg]));
+        } else {
 #pragma unroll
           for (int pg = 0; pg < HP; ++pg) {
             const int page = pg0 + pg;
-            const bool mine = page == own;
-            if ((page < own || mine) && page * 16 + 15 >= lo) {  // (a page that the row does not see stays out, whatever its scale)
-              const float* up = so + 2 * kChunk8 + pg * 16;
+            if (dg && page == own) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                l[i & 3] = f2_fma(f2(t[pg * 16 + 2 * i], t[pg * 16 + 2 * i + 1]),
-                                  mine ? f2(up[2 * i], up[2 * i + 1]) : f2(iv[pg], iv[pg]), l[i & 3]);
+              for (int i = pg * 8; i < pg * 8 + 8; ++i) {
+                float back[2];
+#pragma unroll
+                for (int k = 2 * i; k < 2 * i + 2; ++k) {
+                  // (a token that the row does not see stays out, whatever it holds)
+                  const Kv8Weight w = t[k] != -INFINITY ? base(so[kChunk8 + k]) : kv8_no_weight();
+                  t[k] = ex2(__fsub_rn(t[k], w.base));
+                  back[k & 1] = w.back;
+                }
+                pk[i] = pack_f16x2(t[2 * i], t[2 * i + 1]);
+                l[i & 3] = f2_fma(f2(t[2 * i], t[2 * i + 1]), f2(back[0], back[1]), l[i & 3]);
+              }
+            } else {  // (a page that the row does not see stays out, whatever its scale)
+              const Kv8Weight w = page < own && page * 16 + 15 >= lo ? base(lv8[pg]) : kv8_no_weight();
+              page_weights(pg, w);
             }
           }
         }
@@ -674,16 +696,16 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
         const int pc = ch - 1, sp = pc >> 2;
         warp_wait(o_full, it - 1);
         tc_fence_after();
-        const uint64_t al = f2(alpha0, alpha0);
+        const uint64_t ao2 = f2(ao0, ao0);
 #pragma unroll
         for (int c = 0; c < OD; c += 32) {
           uint32_t y[32];
           ld32(lanes + 256 + OD * h + c, y);
           wait_ld32(y);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) O[c / 2 + i] = f2_fma(O[c / 2 + i], al, f2(y[2 * i], y[2 * i + 1]));
+          for (int i = 0; i < 16; ++i) O[c / 2 + i] = f2_fma(O[c / 2 + i], ao2, f2(y[2 * i], y[2 * i + 1]));
         }
-        L = __fmaf_rn(L, alpha0, l0);
+        L = __fmaf_rn(L, al0, l0);
         if ((pc & 3) == 3 || pc == ch1) {  // the split's end
           ex_l[it & 1][h][lr] = L;
           ok = softmax_sync<32 * C::NT>(2 + (warp & 3), ok);
@@ -691,21 +713,21 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
           float x[C::NT];
 #pragma unroll
           for (int k = 0; k < C::NT; ++k) x[k] = ex_l[it & 1][k][lr];
-          const float Ls = kv8_sum_parts(x);
+          const float Ls = __fmul_rn(kv8_sum_parts(x), kPart), unit = ex2(__fadd_rn(r0e, kPartLog2));
+          const uint64_t unit2 = f2(unit, unit);
           const bool sees = valid && max(lo, sp * kSplit8) <= min(pos, sp * kSplit8 + kSplit8 - 1);
           if (all) {
             // the totals with this split, in the merge kernel's arithmetic (what O holds is not needed after)
             const bool fold_in = sees && have;
-            const float mn = fmaxf(ml.x, M0), ca = ex2(__fsub_rn(ml.x, mn)), cb = ex2(__fsub_rn(M0, mn));
+            const float mn = fmaxf(ml.x, S0), ca = ex2(__fsub_rn(ml.x, mn)), cb = ex2(__fsub_rn(S0, mn));
             // (in scalars: the packed product and sum come out as one fma, which is not what the merge kernel computes)
             auto both = [&](uint32_t tot, float o) {
               const float t = __uint_as_float(tot);
-              o = __fadd_rn(o, 0.f);
               return fold_in ? __fadd_rn(__fmul_rn(t, ca), __fmul_rn(o, cb)) : have ? t : o;
             };
             const bool any = __any_sync(0xffffffffu, have), every = __all_sync(0xffffffffu, !valid || fold_in);
             if (sees) {
-              ml = have ? make_float2(mn, __fadd_rn(__fmul_rn(ml.y, ca), __fmul_rn(Ls, cb))) : make_float2(M0, Ls);
+              ml = have ? make_float2(mn, __fadd_rn(__fmul_rn(ml.y, ca), __fmul_rn(Ls, cb))) : make_float2(S0, Ls);
             }
             uint4* to = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(q0 + tok) * a.Hq + hq) * HD + half * C::VD + OD * h);
 #pragma unroll
@@ -717,15 +739,17 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
               }
               if (every) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float o = __fadd_rn((i & 1) ? f2_hi(O[(c + i) / 2]) : f2_lo(O[(c + i) / 2]), 0.f);
-                  y[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(y[i]), ca), __fmul_rn(o, cb)));
+                for (int i = 0; i < 32; i += 2) {
+                  const uint64_t o = f2_fma(O[(c + i) / 2], unit2, 0ull);  // (kv8_part)
+                  y[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(y[i]), ca), __fmul_rn(f2_lo(o), cb)));
+                  y[i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(y[i + 1]), ca), __fmul_rn(f2_hi(o), cb)));
                 }
               } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  y[2 * i] = __float_as_uint(both(y[2 * i], f2_lo(O[c / 2 + i])));
-                  y[2 * i + 1] = __float_as_uint(both(y[2 * i + 1], f2_hi(O[c / 2 + i])));
+                  const uint64_t o = f2_fma(O[c / 2 + i], unit2, 0ull);
+                  y[2 * i] = __float_as_uint(both(y[2 * i], f2_lo(o)));
+                  y[2 * i + 1] = __float_as_uint(both(y[2 * i + 1], f2_hi(o)));
                 }
               }
               if (pc < ch1) {
@@ -748,7 +772,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
             // that a store of the warp writes as many of a few rows each.
             if (sees && h == 0 && half == 0) {
               const size_t base = (static_cast<size_t>(q0 + tok) * a.Hq + hq) * a.max_splits + sp;
-              a.part_ml[base * 2] = M0;
+              a.part_ml[base * 2] = S0;
               a.part_ml[base * 2 + 1] = Ls;
             }
             float4* buf = reinterpret_cast<float4*>(so_out) + (warp - 4) * (8 * C::OUT_DIMS);  // [row][W], the 16-byte words XORed with the row
@@ -758,7 +782,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
               constexpr int W = C::OUT_DIMS / 4;  // words of a row
 #pragma unroll
               for (int i = 0; i < W; ++i) {
-                const uint64_t v0 = f2_add(O[c / 2 + 2 * i], 0ull), v1 = f2_add(O[c / 2 + 2 * i + 1], 0ull);
+                const uint64_t v0 = f2_fma(O[c / 2 + 2 * i], unit2, 0ull), v1 = f2_fma(O[c / 2 + 2 * i + 1], unit2, 0ull);
                 buf[lane * W + (i ^ (lane & (W - 1)))] = make_float4(f2_lo(v0), f2_hi(v0), f2_lo(v1), f2_hi(v1));
               }
               __syncwarp();
@@ -777,9 +801,11 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
         }
       }
       if (ch <= ch1) {
-        alpha0 = alpha;
+        al0 = al;
+        ao0 = ao;
         l0 = l_ch;
-        M0 = M;
+        S0 = M.s;
+        r0e = r;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[it & 1]);

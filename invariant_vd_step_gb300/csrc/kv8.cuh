@@ -44,7 +44,7 @@ __device__ __forceinline__ void kv8_expand(uint32_t w, uint32_t& lo, uint32_t& h
 // the sign are `amax`, lands in [2^7, 2^8): exact for every element above 2^-24
 // of it (fp16 has 11 bits, bf16 8), off by 2^-32 of the largest below.  The range
 // is that of the codes, so that the weights of the own page's tokens and of the
-// 8-bit ones, which carry the V scales, have like sizes in fp16.  (Rows whose
+// 8-bit ones, which carry the V scales in the product, have like sizes in fp16.  (Rows whose
 // largest is below 2^-87 count from there.)
 __device__ __forceinline__ int kv8_exp(uint32_t amax) { return max(static_cast<int>(amax >> 7), 40); }  // 255: inf or NaN
 __device__ __forceinline__ float kv8_up(int e) { return __uint_as_float(static_cast<uint32_t>(261 - e) << 23); }  // 2^n
@@ -62,12 +62,57 @@ __device__ __forceinline__ uint32_t kv8_to_f16(uint32_t v, float f) {
 }
 __device__ __forceinline__ uint32_t kv8_max_halves(uint32_t v) { return max(v & 0xffffu, v >> 16); }
 
-// The running maximum m of a row after a chunk whose largest score is mx, and the
-// factor for the sums before it (1 where it stays, -inf included).
-__device__ __forceinline__ void kv8_running_max(float& m, float mx, float& alpha) {
-  const float mn = fmaxf(m, mx);
-  alpha = mn == m ? 1.0f : ex2(__fsub_rn(m, mn));
-  m = mn;
+// What a row's weights are taken relative to, over the keys seen so far: its largest
+// score s, and the largest t of t_j = s_j + log2 of j's V scale.  Maxima, so that they
+// do not depend on the order of the keys; they ignore NaN (whose weights are NaN).
+struct Kv8Max {
+  float s = -INFINITY, t = -INFINITY;
+};
+__device__ __forceinline__ void kv8_take(Kv8Max& m, float s, float t) {
+  m.s = fmaxf(m.s, s);
+  m.t = fmaxf(m.t, t);
+}
+// r, the exponent of O: O holds 2^-r of the values' sum, so that the largest of the
+// weights times V scales that enter the product in fp16 is about 1.  Where scores are so
+// large that t has lost the V scale, r is still within the scales' range.
+__device__ __forceinline__ float kv8_exponent(const Kv8Max& m) {
+  return m.s == -INFINITY ? 0.f : fminf(fmaxf(__fsub_rn(m.t, m.s), -94.f), 122.f);
+}
+// m has taken up a chunk: the factors for the l and the O before it, of base s0 and
+// exponent r, which becomes m's.
+__device__ __forceinline__ void kv8_factors(const Kv8Max& m, float s0, float& r, float& al, float& ao) {
+  const float d = m.s == s0 ? 0.f : __fsub_rn(s0, m.s), r0 = r;
+  r = kv8_exponent(m);
+  al = ex2(d);
+  ao = ex2(__fadd_rn(d, __fsub_rn(r0, r)));
+}
+// A key whose V scale has the log2 lv enters the product with 2^(s_j - base), base = s -
+// (lv - r): its weight times 2^(lv - r), in one exponential; l takes that times back,
+// 2^(r - lv).  lv - r counts as -90 below, where nothing is left in fp16 either way and
+// weights above 2^-36 still are normal numbers.  (NaN stays.)
+struct Kv8Weight {
+  float base, back;
+};
+struct Kv8Base {  // of a row at a chunk; s: any value where no key has been seen (every score is -inf then)
+  float s, r, k;
+  // k: 0 where float32 scores are 16 or more apart (2^27): there the base is s, as its
+  // rounding would move what should be about 1 out of fp16's range
+  __device__ __forceinline__ Kv8Base(const Kv8Max& m, float r_)
+      : s(m.s == -INFINITY ? 0.f : m.s), r(r_), k(fabsf(m.s) < 0x1p27f ? -1.f : 0.f) {}
+  __device__ __forceinline__ Kv8Base() : s(0.f), r(0.f), k(0.f) {}
+  __device__ __forceinline__ Kv8Weight operator()(float lv) const {
+    float up = __fsub_rn(lv, r);
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(up) : "f"(up), "f"(-90.f));
+    return {__fmaf_rn(up, k, s), ex2(-up)};
+  }
+};
+__device__ __forceinline__ Kv8Weight kv8_no_weight() { return {0.f, 0.f}; }  // of keys whose scores are -inf
+
+// A split's partial: base s, l 2^-24 and the sum of the values 2^-24, which float32 holds
+// for any bf16 values (2^24 of them at 2^128) and at any scale above 2^-94.
+constexpr float kPartLog2 = -24.f, kPart = 0x1p-24f;
+__device__ __forceinline__ float kv8_part(float o, float unit) {
+  return __fmaf_rn(o, unit, 0.f);  // (+ 0: a zero of O may have either sign, by the kernel that ran)
 }
 
 __device__ __forceinline__ float kv8_sum_parts(const float (&x)[kChunkParts]) {
