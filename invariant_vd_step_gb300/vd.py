@@ -579,12 +579,14 @@ class KVPool:
 
 
 def _ids(a):
-    """Page ids as a contiguous int32 array; ids that int32 does not hold are refused."""
-    if type(a) is np.ndarray and a.dtype == np.int32 and a.ndim == 1 and a.flags.c_contiguous:
+    """Page ids as a contiguous and writeable int32 array; ids that int32 does not hold are refused.
+
+    Writeable, as `_rows_ptr` keeps only such an array alive: of a read-only one it gives the bare address."""
+    if type(a) is np.ndarray and a.dtype == np.int32 and a.ndim == 1 and a.flags.carray:
         return a
     a = _fits_int32(a, "page ids").reshape(-1)
     a = np.ascontiguousarray(a, dtype=np.int32)
-    return a if a.flags.writeable else a.copy()  # (one that is a view of something passing)
+    return a if a.flags.carray else a.copy()
 
 
 def _fits_int32(a, what: str):

@@ -108,3 +108,42 @@ def test_page_ids_stay_alive_until_the_call():
     assert n == 5
     kept = np.frombuffer((vd.ctypes.c_int32 * 5).from_address(vd.ctypes.addressof(src)), np.int32)
     assert kept.tolist() == [0, 1, 2, 3, 4]
+
+
+def test_read_only_page_ids_are_read_while_they_live(monkeypatch):
+    """Read-only arrays that nothing else holds, passed to each call that takes page ids: what the library reads at the
+    address that it gets is those ids, with other arrays of the size made in between."""
+    import ctypes
+    junk, seen = [], []
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*a):
+                n, src, dst = a[-4:-1]
+                junk.extend(np.full(n, -1, np.int32) for _ in range(50))  # takes up memory that is free
+                at = lambda p: p if isinstance(p, int) else ctypes.addressof(p)  # noqa: E731
+                seen.append([np.frombuffer((ctypes.c_int32 * n).from_address(at(p)), np.int32).tolist()
+                             for p in (src, dst)])
+                return 0
+            return call
+    monkeypatch.setattr(vd, "lib", Library)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(vd, "_current_raw_stream", lambda device: 0)
+    model = type("M", (), dict(h=1))()
+    cache, pool = object.__new__(vd.KV8Cache), object.__new__(vd.KVPool)
+    cache.h = pool.h = 1
+    cache.model = pool.model = model
+
+    def ids(first):
+        a = np.arange(first, first + 700, dtype=np.int32)
+        a.flags.writeable = False
+        return a
+    try:
+        for call in (pool.copy_pages, cache.copy_pages, lambda s, d: cache.seal(pool, s, d),
+                     lambda s, d: cache.unseal(pool, s, d)):
+            call(ids(0), ids(1000))
+            assert seen.pop() == [list(range(700)), list(range(1000, 1700))]
+            call(np.broadcast_to(np.int32(5), 3), ids(7)[:3])  # read-only views
+            assert seen.pop() == [[5, 5, 5], [7, 8, 9]]
+    finally:
+        cache.h = pool.h = None
