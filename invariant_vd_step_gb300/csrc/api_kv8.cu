@@ -340,12 +340,13 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
         for (int r0 = 0; r0 < rows; r0 += 128) rb.emplace_back(i, r0);
         continue;
       }
+      const int part0 = static_cast<int>(merge[local].size());
       for (int k = 0; k < ql; ++k) merge[local].push_back(q0 + k);
       std::vector<int>& to = blocks[3 * local + (rows > 16)];
       for (int r0 = 0; r0 < rows; r0 += 16) {
         int first;
         const int n = splits_of(i, r0, 16, &first);
-        for (int k = 0; k < n; ++k) to.insert(to.end(), {i, q0, ql, cached, first + k, r0, 0, 0});
+        for (int k = 0; k < n; ++k) to.insert(to.end(), {i, q0, ql, cached, first + k, r0, 0, part0});
       }
     }
     const int n_rb = static_cast<int>(rb.size()), ctas = c.n_kv_heads * (c.head_dim > 128 ? 2 : 1);  // CTAs of a row block
@@ -353,14 +354,18 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     while (direct < n_rb && direct > 0 && rb[direct].second % m->G) --direct;
     // runs that the others are cut into: as many as SMs
     const int parts_of = n_rb > direct ? std::max(1, m->n_sm / ((n_rb - direct) * ctas)) : 1;
+    int part0 = 0;
     for (int j = 0; j < n_rb; ++j) {
       const int i = rb[j].first, r0 = rb[j].second, q0 = b->cu_q[i], ql = b->cu_q[i + 1] - q0, rows = ql * m->G;
       int first;
       const int n = splits_of(i, r0, 128, &first), parts = j < direct ? 1 : std::min(parts_of, n);
+      // (a request's blocks that leave partials follow each other, and so do their tokens)
+      if (j >= direct && (j == direct || rb[j - 1].first != i))
+        part0 = static_cast<int>(merge[local].size()) - (r0 + m->G - 1) / m->G;
       for (int k = 0; k < parts; ++k)
         blocks[3 * local + 2].insert(blocks[3 * local + 2].end(),
                                      {image0[i], q0, ql, b->cached_len[i], first + n * k / parts, r0, first + n * (k + 1) / parts,
-                                      j < direct});
+                                      j < direct ? kAttn8Folds : part0});
       if (j >= direct)  // the tokens whose first head is in the block
         for (int t0 = (r0 + m->G - 1) / m->G; t0 * m->G < std::min(rows, r0 + 128); ++t0) merge[local].push_back(q0 + t0);
     }
@@ -384,6 +389,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   for (int k = 0; k < 2; ++k) {
     d.merge_list[k] = take(merge[k].size());
     d.n_merge_kv8[k] = static_cast<int>(merge[k].size());
+    d.merge_all[k] = d.n_merge_kv8[k] == T && std::is_sorted(merge[k].begin(), merge[k].end());
   }
   d.open_stride = open_stride;
   d.open_table = take(static_cast<size_t>(B) * open_stride);
@@ -402,13 +408,9 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     VD_CUDA_TRY(cudaMallocHost(reinterpret_cast<void**>(&t->host[slot]), off * 2 * sizeof(int)));
     t->host_cap[slot] = off * 2;
   }
-  // Partials, of the tokens from the first to the last that the merge kernel folds
-  // (a long prompt's blocks fold most of their own).
-  int part0 = T, part1 = 0;
-  for (const std::vector<int>& list : merge)
-    for (const int t : list) part0 = std::min(part0, t), part1 = std::max(part1, t + 1);
-  const size_t per_token = static_cast<size_t>(c.n_heads) * splits;
-  const size_t rows = part1 > part0 ? (part1 - part0) * per_token : 0, skip = part1 > part0 ? part0 * per_token : 0;
+  // Partials, of the tokens that the merge kernel folds (a long prompt's blocks fold
+  // most of their own); global and local layers take turns in them.
+  const size_t rows = std::max(merge[0].size(), merge[1].size()) * c.n_heads * splits;
   const size_t images = static_cast<size_t>(n_images) * c.n_kv_heads * attn8_image_bytes(c.head_dim);
   int rc;
   if (off > t->dev_cap || rows * (c.head_dim + 2) > t->part_cap || images > t->images_cap)
@@ -451,11 +453,8 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   for (int k = 0; k < 2; ++k) std::copy(merge[k].begin(), merge[k].end(), h + d.merge_list[k]);
   d.images = t->images;
   d.base = t->dev;
-  auto at_token0 = [](float* p, size_t floats) {  // (lies before the buffer; its tokens are in it)
-    return reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(p) - floats * sizeof(float));
-  };
-  d.part_o = at_token0(t->part, skip * c.head_dim);
-  d.part_ml = at_token0(t->part + rows * c.head_dim, skip * 2);
+  d.part_o = t->part;
+  d.part_ml = t->part + rows * c.head_dim;
   d.kv8 = cache;
   t->planned = false;  // until the new plan is on its way
   VD_CUDA_TRY(cudaMemcpyAsync(t->dev, h, off * sizeof(int), cudaMemcpyHostToDevice, s));
@@ -519,10 +518,11 @@ int vd::run_kv8_attention(vd_model* m, vd_kv_pool* pool, int layer, const Desc& 
                        : launch_attention8(pool->map, a, c.head_dim, d.kv8->format, !cls && d.lower8, d.n_items[k], s)))
       return rc;
   }
-  const int n_merge = d.n_merge_kv8[a.window > 0];
+  const int n_merge = d.n_merge_kv8[local];
   if (n_merge == 0) return VD_OK;  // every row's splits were folded by its block
   MergeArgs g{};
-  g.tokens = n_merge < d.T ? d.base + d.merge_list[a.window > 0] : nullptr;
+  g.tokens = d.merge_all[local] ? nullptr : d.base + d.merge_list[local];
+  g.by_rank = true;
   g.part_o = d.part_o;
   g.part_ml = d.part_ml;
   g.out = out;

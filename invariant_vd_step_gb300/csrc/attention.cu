@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(128) merge_kernel(MergeArgs a) {
   if (!row) return;
   const int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
   const int s0 = lo / a.split, s1 = p / a.split;
-  const size_t base = (static_cast<size_t>(tok) * a.Hq + h) * a.max_splits;
+  const size_t base = (static_cast<size_t>(a.by_rank ? w / a.Hq : tok) * a.Hq + h) * a.max_splits;
   float M = a.part_ml[(base + s0) * 2], L = a.part_ml[(base + s0) * 2 + 1];
   float O[PER];
   load_part<PER>(a.part_o + (base + s0) * HD + lane * PER, O);

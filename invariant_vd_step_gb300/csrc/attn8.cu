@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
   const int4 d0 = a.items[2 * item], d1 = a.items[2 * item + 1];
   int pid = 0, opid = 0;  // lane i: the page a8 + i in 8 bits, ao + i in bf16
   if (a.split_pages && lane < kChunkPages) pid = a.split_pages[item * (kSplit8 / 16) + warp * kChunkPages + lane];
-  const int b = d0.x, q0 = d0.y, qlen = d0.z, cached = d0.w, sidx = d1.x, r0 = d1.y;
+  const int b = d0.x, q0 = d0.y, qlen = d0.z, cached = d0.w, sidx = d1.x, r0 = d1.y, part0 = d1.w;
   const int G = a.Hq / a.Hkv;
   const int rows = qlen * G;
   const int r_end = min(rows, r0 + 16);
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(128, HD <= 128 ? (NB == 1 ? 4 : 3) : 2)
   // a row that sees no key of the split has no partial
   const int p = cached + row / G, flo = a.window > 0 ? max(0, p - a.window + 1) : 0;
   if (max(flo, sidx * kSplit8) > min(p, sidx * kSplit8 + kSplit8 - 1)) return;
-  const size_t at = (static_cast<size_t>(q0 + row / G) * a.Hq + kvh * G + row % G) * a.max_splits + sidx;
+  const size_t at = (static_cast<size_t>(part0 + row / G) * a.Hq + kvh * G + row % G) * a.max_splits + sidx;
   if (fd == 0) {
     a.part_ml[at * 2] = M.s;
     a.part_ml[at * 2 + 1] = __fmul_rn(kv8_sum_parts(L), kPart);

@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
     uint64_t O[OD / 2];
 #pragma unroll
     for (int i = 0; i < OD / 2; ++i) O[i] = 0ull;
-    const bool all = d1.w != 0;         // the run holds all of the block's splits: they are folded here
+    const bool all = d1.w == kAttn8Folds;  // the run holds all of the block's splits: they are folded here
     float2 ml = make_float2(0.f, 0.f);  // maximum and l of those before, whose O is the totals
     bool have = false;
     int st = 0, n16 = 0;
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
             // The split's partial.  OUT_DIMS at a time go through shared memory, so
             // that a store of the warp writes as many of a few rows each.
             if (sees && h == 0 && half == 0) {
-              const size_t base = (static_cast<size_t>(q0 + tok) * a.Hq + hq) * a.max_splits + sp;
+              const size_t base = (static_cast<size_t>(d1.w + tok) * a.Hq + hq) * a.max_splits + sp;
               a.part_ml[base * 2] = S0;
               a.part_ml[base * 2 + 1] = Ls;
             }
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(Tc8Cfg<HD>::THREADS, 1) attn8_tc_kernel(Attn8A
                 const int rl = k * (32 / W) + lane / W, i = lane % W;
                 if ((rows_seen >> rl) & 1u) {
                   const int rr = r0 + (warp & 3) * 32 + rl;
-                  const size_t base = (static_cast<size_t>(q0 + rr / G) * a.Hq + kvh * G + rr % G) * a.max_splits + sp;
+                  const size_t base = (static_cast<size_t>(d1.w + rr / G) * a.Hq + kvh * G + rr % G) * a.max_splits + sp;
                   *reinterpret_cast<float4*>(a.part_o + base * HD + half * C::VD + OD * h + c + i * 4) = buf[rl * W + (i ^ (rl & (W - 1)))];
                 }
               }

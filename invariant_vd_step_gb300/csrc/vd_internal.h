@@ -171,6 +171,7 @@ struct MergeArgs {
   const int* positions;    // [T]
   const int* tokens;       // tokens to merge (T of them), or null for 0..T-1
   int T, Hq, window, split, max_splits;
+  bool by_rank = false;    // the partials' rows are those of the T tokens, not of all (their numbers)
 };
 int attn_key_tile(int hd);
 // Items of one sequence (both host and device use the same formula).
@@ -233,16 +234,18 @@ bool attn_tc_supported(int hd);
 int launch_attention_tc(const CUtensorMap& kvmap_tc, const AttnArgs& a, int hd, int n_items, cudaStream_t s);
 // Attention over the 8-bit cache (attn8.cu): split partials, folded by launch_merge.
 constexpr int kAttn8Split = 512;  // keys of a split
+constexpr int kAttn8Folds = -2147483647 - 1;
 struct Attn8Args {
   const __nv_bfloat16* q;   // [T][Hq][hd]
-  float* part_o;            // [T][Hq][max_splits][hd]
-  float* part_ml;           // [T][Hq][max_splits][2]
+  float* part_o;            // [merged tokens][Hq][max_splits][hd]
+  float* part_ml;           // [merged tokens][Hq][max_splits][2]
   const int* split_pages;   // decode blocks: [item][32] pages of the item's split (else null: from page_table)
   const int* page_table;    // [B][pt_stride] pages of the cache
   const int* open_table;    // [B][open_stride] pages of the bf16 pool, from logical page cached_len / 16 on
-  const int4* items;        // [blocks][2]: request (tcgen05: its first image), first token, tokens, cached tokens; split, first row; and for
-                            // the tcgen05 kernel, whose blocks take several: end of the splits, whether it
-                            // folds them itself (else it leaves partials)
+  const int4* items;        // [blocks][2]: request (tcgen05: its first image), first token, tokens, cached tokens; split, first row, end
+                            // of the splits (the tcgen05 kernel's blocks take several), row of the partials
+                            // of the request's first token (may lie before the first one), or
+                            // kAttn8Folds: the block folds its splits itself
   const int4* chunks;       // [chunks][2]: request, chunk, image, 1: the image of its own pages; cached, all tokens, 0, 0
   uint8_t* images;          // [images][Hkv] attn8_image_bytes()
   __nv_bfloat16* out;       // [T][Hq][hd] (their rows)

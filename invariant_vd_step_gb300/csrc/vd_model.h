@@ -76,7 +76,10 @@ struct Desc {
   int open_table = 0, open_stride = 0;   // pages of the bf16 pool, per request
   int chunks[2] = {}, n_chunks[2] = {};  // chunks that the tcgen05 blocks of global, of local layers read
   uint8_t* images = nullptr;             // and their images
-  int merge_list[2] = {}, n_merge_kv8[2] = {};  // tokens whose splits the merge kernel folds: on global, on local layers
+  // Tokens whose splits the merge kernel folds, on global, on local layers; the partials'
+  // rows are in their order.  merge_all: they are 0 .. T - 1.
+  int merge_list[2] = {}, n_merge_kv8[2] = {};
+  bool merge_all[2] = {};
   int own_slots = 1;                     // bf16 pages that a decode-class block can hold
   bool lower8 = false;                   // every decode-class block has at most 8 rows
 };

@@ -1,0 +1,50 @@
+"""Device memory that plans over the 8-bit cache take, and rows that do not depend on it."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import bits, ready
+from invariant_vd_step_gb300 import vd
+from kv8_scenario import KV8Scenario, kv8_spec
+
+pytestmark = pytest.mark.gpu
+
+MB = 1 << 20
+
+
+def taken(f):
+    """Device memory that f's work takes and keeps, in bytes."""
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    f()
+    torch.cuda.synchronize()
+    return before - torch.cuda.mem_get_info()[0]
+
+
+def test_partials_are_those_of_the_merged_tokens():
+    """A single token before, behind and between long chunks, whose last blocks alone leave partials: the same bits in every
+    order, and memory for few of the tokens."""
+    ready()
+    Hq, hd = 32, 64
+    sc = KV8Scenario(kv8_spec(Hq, 8, hd), [32000, 5000, 700], "int8", seed=2, max_tokens=2500)
+    long, one, mid = (0, 29952, 2048), (1, 4999, 1), (2, 300, 400)
+    want = {r: bits(sc.attention([r], kernel=1)) for r in (long, one, mid)}
+    for reqs in ([one, long, mid], [long, one], [one, long], [long, mid, one], [mid, one, long]):
+        cu, cached, t8, t16, _ = sc.setup(reqs)
+        q = torch.cat([sc.q[rid][c:c + n] for rid, c, n in reqs])
+        out = torch.full_like(q, float("nan"))
+        plan = vd.KV8Plan(sc.model, len(q))
+        plan.set_prefill(2)
+        used = taken(lambda: plan.plan(sc.cache, sc.pool, cu, cached, t8, t16))
+        plan.seal(sc.cache, sc.pool, 0)
+        plan.attention(sc.cache, sc.pool, 0, q, out)
+        torch.cuda.synchronize()
+        for i, r in enumerate(reqs):
+            np.testing.assert_array_equal(bits(out[cu[i]:cu[i + 1]]), want[r], err_msg=f"{reqs} {r}")
+        # Partials of all tokens are 2049 x 32 x 63 splits x 66 floats, 1040 MB; of the last partial round of row blocks,
+        # at most an eighth of the chunks' 76 x 8 and less than one round of SMs, a quarter of that.  Images of the
+        # histories: (32000 + 700) / 128 chunks and two more each, 8 heads, 33 KB: 69 MB.
+        assert used < 400 * MB, (reqs, used / MB)
+        plan.close()
+    assert sc.model.device_status() == 0
