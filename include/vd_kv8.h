@@ -122,8 +122,10 @@ int vd_kv8_plan_make(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, const vd_kv8_b
 
 /* Kernel of the chunks of more than 16 rows (q_len * Hq / Hkv) in the plans made
  * after the call: 0 (default) chosen by their sizes, 1 mma.sync, 2 tcgen05.  The
- * same bits either way.  (A model set to
- * mma.sync by vd_set_attention_prefill takes that.)  Errors: VD_ERR_INVALID_ARG. */
+ * same bits either way.  tcgen05 keeps fp16 images of its requests' histories in the
+ * plan's memory, twice the bytes of their codes in one layer; the default takes it for
+ * 8 GiB of them at most.  (A model set to mma.sync by vd_set_attention_prefill takes
+ * that.)  Errors: VD_ERR_INVALID_ARG. */
 int vd_kv8_set_prefill(vd_kv8_plan* p, int32_t kernel);
 
 /* vd_op_rope_kv of the planned tokens: qkv dev bf16 [T][(Hq+2Hkv) hd] -> q_out

@@ -54,6 +54,10 @@ struct vd_kv8_plan {
 namespace {
 
 constexpr int kSplitPages = kAttn8Split / 16;
+// Images that the choice of kernels may ask for: 65 KB for 128 keys of a KV head of 128
+// dims, twice the bytes of the same keys' codes in one layer, so histories of 16 M such
+// keys (2 M tokens of 8 heads).  Chunks beyond them go to mma.sync.
+constexpr size_t kMostImageBytes = static_cast<size_t>(8) << 30;
 
 int check_device(const vd_model* m) {
   int dev = -1;
@@ -281,6 +285,11 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   std::vector<int> blocks[6];
   const bool windowed = c.sliding_window > 0 && c.local_global_period > 0;
   std::vector<unsigned char> tc(B, 0);
+  // Images of request i: of all its chunks, and again of those that hold own pages.
+  auto images_of = [&](int i) {
+    const int cached = b->cached_len[i], all = (cached + b->cu_q[i + 1] - b->cu_q[i] + 127) / 128;
+    return 2 * all - cached / 128;
+  };
   if (m->prefill_kernel == 0 && t->prefill != 1) {
     // What a chunk's (row block, KV head, 128 keys) units cost, in us at head dim 128:
     // 0.0095 for each of 16 rows on mma.sync; on tcgen05 0.02 for each of 128 rows and
@@ -291,16 +300,31 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     // 83; 8 heads over 4 of 256: 1 x 512 behind 4000 207 against 89, 32 x 32 behind 100 to
     // 1000 86 against 101.  The rule takes the faster one but for near ties and, 32 heads
     // over 8, 1 x 256 behind 0, 26 against 20.5.)
-    double gain = 0;
+    struct Choice {
+      double more;    // what tcgen05 gains
+      size_t images;  // bytes that it takes
+      int i;
+    };
+    std::vector<Choice> choices;
     for (int i = 0; i < B; ++i) {
       const int ql = b->cu_q[i + 1] - b->cu_q[i], rows = ql * m->G, all = (b->cached_len[i] + ql + 127) / 128;
       const int seen = windowed && c.local_global_period > c.n_layers ? std::min(all, (c.sliding_window + ql + 127) / 128) : all;
       const double unit = seen * c.n_kv_heads * (c.head_dim / 128.0);
       const double more = unit * (0.0095 * ((rows + 15) / 16) - 0.02 * ((rows + 127) / 128 + 1));
-      if (rows > 16 && (more > 0 || t->prefill == 2)) {
-        tc[i] = 1;
-        gain += more;
-      }
+      if (rows > 16 && (more > 0 || t->prefill == 2))
+        choices.push_back({more, images_of(i) * static_cast<size_t>(c.n_kv_heads) * attn8_image_bytes(c.head_dim), i});
+    }
+    std::sort(choices.begin(), choices.end(), [](const Choice& x, const Choice& y) {  // the most gain per byte first
+      const double a = x.more * y.images, b = y.more * x.images;
+      return a != b ? a > b : x.i < y.i;
+    });
+    double gain = 0;
+    size_t bytes = 0;
+    for (const Choice& x : choices) {
+      if (t->prefill == 0 && bytes + x.images > kMostImageBytes) continue;
+      tc[x.i] = 1;
+      gain += x.more;
+      bytes += x.images;
     }
     if (gain < 9 && t->prefill == 0) std::fill(tc.begin(), tc.end(), 0);
   }
@@ -318,7 +342,7 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       for (int ch = cached / 128; ch < all; ++ch)
         chunks[local].insert(chunks[local].end(), {i, ch, image0[i] + all + ch - cached / 128, 1, cached, kv, 0, 0});
     }
-    n_images += 2 * all - cached / 128;
+    n_images += images_of(i);
     if (n_images * c.n_kv_heads > 0x3fffffff) return fail(VD_ERR_CAPACITY, "plan too large");
   }
   // Of the tcgen05 row blocks, as many as fill the SMs in whole rounds take all of

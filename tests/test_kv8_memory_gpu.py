@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_util import bits, ready
-from invariant_vd_step_gb300 import vd
+from invariant_vd_step_gb300 import synth, vd
 from kv8_scenario import KV8Scenario, kv8_spec
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +48,40 @@ def test_partials_are_those_of_the_merged_tokens():
         assert used < 400 * MB, (reqs, used / MB)
         plan.close()
     assert sc.model.device_status() == 0
+
+
+def test_images_of_long_histories_are_bounded():
+    """Chunks of 64 requests that share a history of 32768 tokens: its fp16 images for each, 275 MB, would be 17.6 GB.  The
+    plan takes 8 GiB at most, and leaves the other requests to the kernel that needs none: the same bits."""
+    ready()
+    Hq, Hkv, hd, c, n, B = 128, 16, 128, 32768, 15, 64
+    spec = kv8_spec(Hq, Hkv, hd)
+    W = {k: v.cuda() for k, v in synth.make_weights(spec, seed=0).items()}
+    model = vd.Model(spec, W, max_tokens=B * n, max_seqs=B, max_logit_rows=1, max_context=c + n)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    made = lambda pages: vd.KVPool(model, pages, memory=torch.zeros(model.pool_bytes(pages), dtype=torch.uint8,  # noqa: E731
+                                                                    device="cuda"))
+    cache, staging, pool = vd.KV8Cache(model, c // 16, "int8"), made(c // 16), made(B)
+    staging.view().normal_(generator=g)
+    order = np.random.default_rng(1).permutation(c // 16).astype(np.int32)
+    cache.seal(staging, np.arange(c // 16), order)
+    pool.view()[:] = torch.randn((1, 1, 2, Hkv, 16, hd), generator=g, device="cuda").bfloat16()
+    q1 = torch.randn((n, Hq, hd), generator=g, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+
+    def run(b, kernel):
+        plan, q = vd.KV8Plan(model, b * n), q1.repeat(b, 1, 1)
+        out = torch.full_like(q, float("nan"))
+        plan.set_prefill(kernel)
+        used = taken(lambda: plan.plan(cache, pool, np.arange(0, b * n + 1, n), np.full(b, c), np.tile(order, (b, 1)),
+                                       np.arange(b)[:, None]))
+        plan.attention(cache, pool, 0, q, out)
+        torch.cuda.synchronize()
+        plan.close()
+        return out, used
+    want, _ = run(1, 1)
+    out, used = run(B, 0)
+    np.testing.assert_array_equal(bits(out), np.tile(bits(want), (B, 1, 1)))
+    # partials of at most all tokens: 960 x 128 x 65 splits x 130 floats, 4.2 GB
+    assert 4096 * MB < used < (8192 + 4000) * MB, used / MB
+    assert model.device_status() == 0
