@@ -171,15 +171,21 @@ int seal_call(vd_kv8* c, vd_kv_pool* pool, int layer, int n, const int* src, con
 }
 
 // Grows a device buffer to at least n elements (the old one is freed once the
-// device is done with it).
+// device is done with it), by half of it for the plans to come, 64 MB at most, where
+// there is room for that.
 template <typename T>
 int grow(T** p, size_t* cap, size_t n) {
   if (n <= *cap) return VD_OK;
-  const size_t want = std::max(n, *cap + *cap / 2);
+  size_t want = std::max(n, *cap + std::min(*cap / 2, (static_cast<size_t>(64) << 20) / sizeof(T)));
   if (*p) cudaFree(*p);
   *p = nullptr;
   *cap = 0;
-  VD_CUDA_TRY(cudaMalloc(reinterpret_cast<void**>(p), want * sizeof(T)));
+  if (want > n && cudaMalloc(reinterpret_cast<void**>(p), want * sizeof(T)) != cudaSuccess) {
+    cudaGetLastError();  // (the error is this attempt's)
+    *p = nullptr;
+    want = n;
+  }
+  if (!*p) VD_CUDA_TRY(cudaMalloc(reinterpret_cast<void**>(p), want * sizeof(T)));
   *cap = want;
   return VD_OK;
 }

@@ -85,3 +85,22 @@ def test_images_of_long_histories_are_bounded():
     # partials of at most all tokens: 960 x 128 x 65 splits x 130 floats, 4.2 GB
     assert 4096 * MB < used < (8192 + 4000) * MB, used / MB
     assert model.device_status() == 0
+
+
+def test_a_little_more_takes_a_little_more():
+    """Plans that grow by a hundredth: their memory grows by that and 64 MB at most per buffer, not by half."""
+    ready()
+    sc = KV8Scenario(kv8_spec(32, 8, 64), [32000], "int8", seed=2, max_tokens=1100)
+    plan = vd.KV8Plan(sc.model, 1100)
+    plan.set_prefill(1)
+    for n, most in ((1000, 600), (1010, 80), (1011, 1)):
+        cu, cached, t8, t16, _ = sc.setup([(0, 30000, n)])
+        q = sc.q[0][30000:30000 + n]
+        used = taken(lambda: plan.plan(sc.cache, sc.pool, cu, cached, t8, t16))
+        # 1000 tokens x 32 heads x 61 splits x 66 floats: 515 MB, a hundredth of it 5
+        assert used <= most * MB, (n, used / MB)
+    plan.seal(sc.cache, sc.pool, 0)
+    out = torch.full_like(q, float("nan"))
+    plan.attention(sc.cache, sc.pool, 0, q, out)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(bits(out), bits(sc.attention([(0, 30000, 1011)])))
