@@ -305,10 +305,12 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
     // 25; 32 x 8 behind 500 to 4000 115 against 182; 9 x 77 behind up to 2500 198 against
     // 83; 8 heads over 4 of 256: 1 x 512 behind 4000 207 against 89, 32 x 32 behind 100 to
     // 1000 86 against 101.  The rule takes the faster one but for near ties and, 32 heads
-    // over 8, 1 x 256 behind 0, 26 against 20.5.)
+    // over 8, 1 x 256 behind 0, 26 against 20.5.)  Where global and local layers take
+    // turns, one choice serves both, by what the global ones cost.
     struct Choice {
       double more;    // what tcgen05 gains
       size_t images;  // bytes that it takes
+      double rate;    // the former per byte
       int i;
     };
     std::vector<Choice> choices;
@@ -317,13 +319,13 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
       const int seen = windowed && c.local_global_period > c.n_layers ? std::min(all, (c.sliding_window + ql + 127) / 128) : all;
       const double unit = seen * c.n_kv_heads * (c.head_dim / 128.0);
       const double more = unit * (0.0095 * ((rows + 15) / 16) - 0.02 * ((rows + 127) / 128 + 1));
-      if (rows > 16 && (more > 0 || t->prefill == 2))
-        choices.push_back({more, images_of(i) * static_cast<size_t>(c.n_kv_heads) * attn8_image_bytes(c.head_dim), i});
+      if (rows > 16 && (more > 0 || t->prefill == 2)) {
+        const size_t images = images_of(i) * static_cast<size_t>(c.n_kv_heads) * attn8_image_bytes(c.head_dim);
+        choices.push_back({more, images, more / images, i});
+      }
     }
-    std::sort(choices.begin(), choices.end(), [](const Choice& x, const Choice& y) {  // the most gain per byte first
-      const double a = x.more * y.images, b = y.more * x.images;
-      return a != b ? a > b : x.i < y.i;
-    });
+    std::sort(choices.begin(), choices.end(),
+              [](const Choice& x, const Choice& y) { return x.rate != y.rate ? x.rate > y.rate : x.i < y.i; });
     double gain = 0;
     size_t bytes = 0;
     for (const Choice& x : choices) {
