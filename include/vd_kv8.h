@@ -137,11 +137,12 @@ int vd_op_kv8_seal(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, int32_t layer, v
 /* Attention of the planned tokens: q, out dev bf16 [T][Hq][hd]; q has been
  * rotated, K/V of the new tokens are in the bf16 pool and the pages that the step
  * completes are sealed.  q and out may not overlap (VD_ERR_INVALID_ARG).  Slots of
- * the bf16 pool behind a row's position are not seen, whatever they hold.  Sums, softmax statistics and outputs' partials are
- * float32; weights enter the product with V as fp16, at most 2^-11 of themselves
- * (or, times their V scales, 2^-25 of the largest such) off.  V of any sizes may stand
- * beside each other: a weight below 2^-36 of the row's largest may leave the sum of
- * weights where its V is 2^90 and more below another's. */
+ * the bf16 pool behind a row's position are not seen, whatever they hold.  Sums,
+ * softmax statistics and outputs' partials are float32; weights enter the product
+ * with V as fp16, at most 2^-11 of themselves (or, times their V scales, 2^-25 of the
+ * largest such) off.  V of any sizes may stand beside each other.  Weights below 2^-126
+ * of the row's largest may count as 0, and below 2^-36 in the sum of weights where their
+ * V is 2^90 and more below another's. */
 int vd_op_kv8_attention(vd_kv8_plan* p, vd_kv8* c, vd_kv_pool* pool, int32_t layer, const void* q, void* out,
                         void* stream);
 /* The whole decoder forward of the planned tokens over the cache (vd_step with

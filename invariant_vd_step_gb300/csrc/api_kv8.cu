@@ -299,14 +299,15 @@ int make_plan(vd_kv8_plan* t, vd_kv8* cache, vd_kv_pool* pool, const vd_kv8_batc
   if (m->prefill_kernel == 0 && t->prefill != 1) {
     // What a chunk's (row block, KV head, 128 keys) units cost, in us at head dim 128:
     // 0.0095 for each of 16 rows on mma.sync; on tcgen05 0.02 for each of 128 rows and
-    // as much for the keys' image, and 9 more for the launch.  (Sweep of 48 shapes, 1
-    // to 32 requests of 5 to 1024 tokens behind 0 to 8000, 32 heads over 8, mma.sync
-    // against tcgen05: 1 x 64 behind 1000 20 against 22 us; 1 x 512 behind 0 48 against
-    // 25; 32 x 8 behind 500 to 4000 115 against 182; 9 x 77 behind up to 2500 198 against
-    // 83; 8 heads over 4 of 256: 1 x 512 behind 4000 207 against 89, 32 x 32 behind 100 to
-    // 1000 86 against 101.  The rule takes the faster one but for near ties and, 32 heads
-    // over 8, 1 x 256 behind 0, 26 against 20.5.)  Where global and local layers take
-    // turns, one choice serves both, by what the global ones cost.
+    // as much for the keys' image, and 9 more for the launch.  (From a sweep of 48 shapes,
+    // 1 to 32 requests of 5 to 1024 tokens behind 0 to 8000, 32 heads over 8.  mma.sync
+    // against tcgen05, with today's kernels: 1 x 64 behind 1000 20 against 23 us; 1 x 512
+    // behind 0 47 against 27; 32 x 8 behind 500 to 4000 106 against 192; 9 x 77 behind up
+    // to 2500 157 against 70; 2 x 128 behind 3000 136 against 54; 8 heads over 4 of 256:
+    // 1 x 512 behind 4000 204 against 94, 32 x 32 behind 100 to 1000 84 against 114.  The
+    // rule takes the faster one but for near ties and, 32 heads over 8, 1 x 256 behind 0, 25
+    // against 20.)  Where global and local layers take turns, one choice serves both, by
+    // what the global ones cost.
     struct Choice {
       double more;    // what tcgen05 gains
       size_t images;  // bytes that it takes

@@ -17,7 +17,10 @@
 // so O 2^r / l is the softmax's mean of the values, and a split's partial is (S, l, O
 // 2^r), the last two times 2^-24.  The V scale rides in the exponent and the codes enter
 // the product as they are; r makes the largest p of the row 1, and fp16 rounds p by
-// 2^-12 of itself or 2^-25, where bf16 would be off by 2^-9.  S and l know nothing of V:
+// 2^-12 of itself or 2^-25, where bf16 would be off by 2^-9.  (The kernels of the 16-bit
+// cache hold p as two bf16 terms, 2^-17, at twice the products: here the codes are 2^-8
+// of a page's largest or 2^-4 of themselves off, and the output is rounded by 2^-9, so that
+// outputs are 0.0017 off the exact ones of these codes either way.)  S and l know nothing of V:
 // with p relative to the largest alone, keys whose V is 2^126 below the largest, or 0,
 // would leave the denominator.  With the bound -90 of u (below it nothing of p is left
 // in fp16) each weight of 2^-36 of the largest and more is in l whatever the V, and
@@ -35,15 +38,17 @@
 // block a row is in or the other rows.
 //
 // What bounds it.  Decode reads each page once: 256 requests of 512 to 8192 tokens,
-// 32 heads over 8 of 128, take 402 us, 5.7 TB/s, 0.85 of what a copy reaches.  A chunk
-// per warp is one pass: scores to shared memory, one maximum, weights, P V; four
-// CTAs per SM (127 registers), each warp with three pages in flight, cover each
-// other's latencies, and the issue slots are 48 % busy.  With the rows as M of the
-// products, 12 of 16 were empty here: 424 us.  Four pages in flight and three CTAs, or
-// two and five, are slower; pages loaded straight to registers take 467 to 528 us;
-// resident CTAs that take blocks off a count, 401.
-// At head dimension 256 the registers allow two CTAs: a window of 1024 keys for 48
-// requests of 3 tokens, 8 heads over 4, 29 us, 3.6 TB/s, two rounds of latency.
+// 32 heads over 8 of 128, take 399 us, 5.8 TB/s, 0.85 of what a copy reaches.  A chunk
+// per warp is one pass: scores to shared memory, the maxima, weights, P V; blocks of at
+// most 8 rows have four CTAs per SM (128 registers), each warp with three pages in
+// flight, which cover each other's latencies, and the issue slots are 49 % busy.  With
+// the rows as M of the products, 12 of 16 were empty here: 424 us.  Four pages in flight
+// and three CTAs, or two and five, are slower; pages loaded straight to registers take
+// 467 to 528 us; resident CTAs that take blocks off a count gained 1.
+// At head dimension 256 the registers allow two CTAs of such blocks: a window of 1024
+// keys for 48 requests of 3 tokens, 8 heads over 4 (6 rows), 28 us, 3.8 TB/s, two rounds
+// of latency.  Blocks of 9 to 16 rows take 91 KB of shared memory at 128 dims and 140 at
+// 256, two CTAs per SM and one; a launch has one kind, by its largest block.
 #include <math.h>
 
 #include "attn_tile.cuh"

@@ -25,12 +25,13 @@
 // scales together, which loses weights, 371; before that 424 with the totals in
 // global memory, two O buffers and one barrier of all softmax threads (the two of a
 // row need only each other), 447 with the folding in four warps of its own, which
-// became what the others waited for, and 414 with 216 registers in place of 232.
+// became what the others waited for, and 414 with 216 registers in place of 232 (8 bytes
+// of a thread still spill at head dimension 128, 108 at 256).
 //
 // Head dimension 256: a row block is two CTAs, each with all of the scores and half
 // of the dims of V and O, so that tensor memory and registers hold what they hold at
-// 128; K comes in two units of 128 dims.  512 tokens behind 4000, 8 heads over 4: 89 us
-// where mma.sync takes 207.  (One unit of 256 dims, without a second one in flight:
+// 128; K comes in two units of 128 dims.  512 tokens behind 4000, 8 heads over 4: 94 us
+// where mma.sync takes 204.  (One unit of 256 dims, without a second one in flight:
 // the same.)
 //
 // The operands are made once per launch, not once per row block: an expanding
