@@ -902,6 +902,7 @@ class KV8Plan:
         tables = []
         for t in (page_table, open_table):
             t = np.ascontiguousarray(_fits_int32(t, "page ids"), dtype=np.int32)
+            _need(t.size == 0 or len(c) > 0 and t.size % len(c) == 0, "page tables: as many ids for each request")
             tables.append(t.reshape(len(c), -1) if t.size else t.reshape(len(c), 0))
         tok, p_tok = _i32(_fits_int32(token_ids, "token_ids").reshape(-1)) if token_ids is not None else (None, None)
         rows, p_rows = _i32(_fits_int32(logit_rows, "logit_rows").reshape(-1))

@@ -147,3 +147,18 @@ def test_read_only_page_ids_are_read_while_they_live(monkeypatch):
             assert seen.pop() == [[5, 5, 5], [7, 8, 9]]
     finally:
         cache.h = pool.h = None
+
+
+def test_page_tables_that_are_not_rows_of_the_requests_are_refused(monkeypatch):
+    plan, other = plan_without_library(monkeypatch)
+    good = dict(cu_q=[0, 1, 2], cached_len=[3, 4], page_table=[[0], [1]], open_table=[[0], [1]])
+    none = dict(cu_q=[0], cached_len=[], page_table=[], open_table=[])
+    try:
+        refused([lambda k=k, v=v, g=g: plan.plan(other(), other(), **{**g, k: v}) for g, k, v in [
+            (good, "page_table", [0, 1, 2]), (good, "open_table", np.zeros((3, 1), int)), (none, "page_table", [[1]]),
+            (none, "open_table", [0]), (good, "cu_q", [0, 1]), (none, "cu_q", [])]])
+        for g in (good, none):
+            with pytest.raises(AssertionError, match="reached"):
+                plan.plan(other(), other(), **g)
+    finally:
+        plan.h = None
